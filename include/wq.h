@@ -465,6 +465,152 @@ WQ_API int wq_linear_w8a8(const uint16_t *x, int64_t T, int64_t K, int64_t ldx, 
                           const float *sw, int64_t N, int scheme, int acc, uint16_t *out, void *ws,
                           size_t ws_bytes, int32_t *status, wq_stream_t stream);
 
+/* ===========================================================================
+ * The attention half of a serving decoder layer: the norms around a block,
+ * rotary positions, the rotated append to a paged cache, and attention for a
+ * batch that shares a prefix.  The pages of the INT8 layer have no
+ * counterpart; the formulas below are the contract.
+ *
+ * These entries take bf16, fp16 and (norms, rotary) float tensors through
+ * `dtype`.  Row, head and page pitches are in elements and may be any
+ * non-negative value; the last dimension is contiguous.  Shapes and pitches
+ * that allow 16-byte accesses (see each entry) take vector kernels, others
+ * element-wise ones with the same results.  `status` may be NULL. */
+enum { WQ_DT_BF16 = 0, WQ_DT_F16 = 1, WQ_DT_F32 = 2 };
+
+/* ---------------------------------------------------------------------------
+ * Norms after and before a block, fused with the block's gate, its residual
+ * scale and the residual sum.  Per row t, all in float32:
+ *   n = N_post(block[t]);  h = residual[t] + scale * (gate[t] * n);
+ *   x_out[t] = h;  y[t] = N_pre(h)          (each rounded once; N_pre takes
+ *                                            the unrounded h)
+ *   N_NONE(v) = v;  N_RMS(v)_j = v_j * r * w_j,  r = 1/sqrt(mean(v^2) + eps);
+ *   N_LAYER(v)_j = (v_j - m) * r * w_j + c_j,  m = mean(v),
+ *                  r = 1/sqrt(mean((v - m)^2) + eps).
+ * A NULL residual counts as 0, a NULL gate or weight as 1, a NULL bias as 0
+ * (a bias is read by N_LAYER only).  gate is [T][H] with pitch ldg, or one
+ * row for all tokens with ldg = 0.  x_out or y may be NULL (not both); either
+ * may be block or residual itself (same pitch).  Means are sums in a fixed order.
+ * Requirements: 1 <= H <= 32768, pitches ld* >= H (ldg = 0 or >= H).  The
+ * vector kernels serve H and pitches that are multiples of 16 bytes with
+ * 16-byte aligned pointers. */
+enum { WQ_NORM_NONE = 0, WQ_NORM_RMS = 1, WQ_NORM_LAYER = 2 };
+WQ_API int wq_block_norm(const void *block, int64_t ldb, const void *residual, int64_t ldr,
+                         const void *gate, int64_t ldg, float scale, int post,
+                         const void *post_weight, const void *post_bias, int pre,
+                         const void *pre_weight, const void *pre_bias, float eps, int64_t T,
+                         int64_t H, int dtype, void *x_out, int64_t ldx, void *y, int64_t ldy,
+                         wq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions.  Pair i (i < rot/2) of a head is (x_i, x_{i+rot/2}) in the
+ * half layout and (x_{2i}, x_{2i+1}) in the interleaved one:
+ *   (a, b) -> (a c - b s, b c + a s),  (c, s) = table[position][i]
+ * (s negated with inverse = 1); elements at or past rot are copied.  Float32
+ * arithmetic, one rounding to the output type.
+ *
+ * wq_rope_table writes table float [max_pos][rot/2][2] = m cos(p f_i),
+ *   m sin(p f_i), angles in float64, with f_i = base^(-2i/rot) and m = 1 for
+ *   WQ_ROPE_PLAIN, and for contexts longer than the trained one
+ *   WQ_ROPE_LINEAR: f_i / factor;
+ *   WQ_ROPE_NTK:    base * factor^(rot/(rot-2)) in place of base (rot > 2);
+ *   WQ_ROPE_YARN:   f_i (u_i + (1 - u_i) / factor), u_i = 1 - clamp((i - lo) /
+ *     (hi - lo), 0, 1), lo = max(floor(d(beta_fast)), 0), hi =
+ *     min(ceil(d(beta_slow)), rot - 1) (hi = lo + 0.001 if equal), d(n) = rot
+ *     ln(trained / (2 pi n)) / (2 ln base); m = mscale, or with mscale = 0
+ *     0.1 ln(factor) + 1 (factor > 1).
+ *   Requirements: rot even, 2 <= rot <= 1024, base > 1, factor >= 1; YARN:
+ *   trained >= 1, beta_fast >= beta_slow > 0; mscale >= 0.
+ * wq_rope: x [T][heads][D] (pitches x_token, x_head) -> out (its pitches), at
+ *   positions int32 [T].  out may be x itself with the same pitches.  A
+ *   position outside [0, max_pos) sets status = WQ_ERR_INDEX and that token is
+ *   not written.  Requirements: rot even, 2 <= rot <= D.  The vector kernel
+ *   serves D and pitches that are multiples of 8 elements (bf16, fp16), rot a
+ *   multiple of 16 (half) or 8 (interleaved), 16-byte aligned pointers. */
+enum { WQ_ROPE_PLAIN = 0, WQ_ROPE_LINEAR = 1, WQ_ROPE_NTK = 2, WQ_ROPE_YARN = 3 };
+enum { WQ_ROPE_HALF = 0, WQ_ROPE_INTERLEAVED = 1 };
+WQ_API int wq_rope_table(float *table, int64_t max_pos, int rot, double base, int scaling,
+                         double factor, double trained, double beta_fast, double beta_slow,
+                         double mscale, wq_stream_t stream);
+WQ_API int wq_rope(const void *x, int64_t x_token, int64_t x_head, const int32_t *positions,
+                   const float *table, int64_t max_pos, int64_t T, int heads, int D, int rot,
+                   int layout, int inverse, int dtype, void *out, int64_t o_token, int64_t o_head,
+                   int32_t *status, wq_stream_t stream);
+
+/* A paged key/value cache: element d of the key of head h at in-page place o
+ * of page p is k[p * k_page + h * k_head + o * k_token + d], likewise v.  The
+ * struct is host memory; k and v are device pointers of the caller. */
+typedef struct {
+  void *k, *v;
+  int64_t k_page, k_head, k_token;
+  int64_t v_page, v_head, v_token;
+  int64_t num_pages;
+  int32_t page_size, heads; /* tokens a page holds; key/value heads */
+  int32_t dk, dv;           /* elements of a key, of a value          */
+  int32_t dtype;            /* WQ_DT_BF16 or WQ_DT_F16                */
+} wq_paged_cache;
+
+/* Rotated append: for each token t with slots[t] >= 0, page p = slots[t] /
+ * page_size, place o = slots[t] % page_size:
+ *   k[p][:][o] = rope(k_new[t]),  v[p][:][o] = v_new[t],
+ * and, with q not NULL, q_out[t] = rope(q[t]) for every t (q_out may be q).
+ * k_new [T][heads][dk], v_new [T][heads][dv], q [T][q_heads][dk], all of the
+ * cache's dtype.  A negative slot skips the append of that token (padding).  A
+ * slot at or past num_pages * page_size or a position outside the table sets
+ * status = WQ_ERR_INDEX and skips what it would have written.  Slots of one
+ * call must differ.  rot = 0 appends without rotation (positions and table
+ * may be NULL).  Requirements as wq_rope, rot = 0 or 2 <= rot <= dk. */
+WQ_API int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, int q_heads,
+                                const void *k_new, int64_t kn_token, int64_t kn_head,
+                                const void *v_new, int64_t vn_token, int64_t vn_head,
+                                const int32_t *positions, const int64_t *slots,
+                                const float *table, int64_t max_pos, int64_t T, int rot,
+                                int layout, const wq_paged_cache *cache, void *q_out,
+                                int64_t qo_token, int64_t qo_head, int32_t *status,
+                                wq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over a paged cache for B sequences that share a prefix.
+ * The prefix is prefix_len keys in the pages prefix_pages int32
+ * [ceil(prefix_len / page_size)]; sequence b continues with suffix_len[b]
+ * keys in the pages page_table[b][.] (int32, pitch ld_table, place 0 of its
+ * first page follows the prefix).  Its query tokens are rows [cu_q[b],
+ * cu_q[b+1]) of q [T][q_heads][dk]; they are the last of its keys: token j of
+ * n sees the whole prefix and suffix keys 0 .. suffix_len[b] - n + j.
+ * Query head a reads key head a / (q_heads / heads).
+ *   out[t][a] = sum_i softmax_i(scale * q.k_i) v_i     (cache dtype)
+ *   lse[t][a] = ln sum_i exp(scale * q.k_i)            (float, [T][q_heads], may be NULL)
+ * A row that sees no key gets zeros and -inf.  prefix_len = 0 is ordinary
+ * paged attention, max_suffix = 0 the prefix alone.  cu_q NULL: max_q tokens
+ * each (T = B * max_q).  max_q and max_suffix are host bounds on the tokens and keys of a
+ * sequence: values above them are cut to them, with status = WQ_ERR_INDEX;
+ * a page id outside [0, num_pages) sets the same status (its keys are left
+ * out or count as zeros).  prefix_len and the bounds are host values, so a
+ * graph that records the call keeps them; lengths and pages are device data.
+ * Cache places at or past a length are never used, whatever they hold.  A
+ * non-finite value in a key or value that only later tokens of the sequence
+ * see may spread to earlier ones (a weight of zero times it is taken).
+ * Scores, softmax statistics and sums are float32; the softmax weights are
+ * rounded to the cache's 16-bit type before they multiply the values, as the
+ * tensor cores take them.  Results do not depend on the run: no sum's order
+ * is left to chance.
+ * Requirements: bf16 or fp16; dk, dv multiples of 8, at most 128; q_heads a
+ * multiple of heads, at most 128 per key head; pitches of q and the cache
+ * multiples of 8 elements, q, k and v 16-byte aligned; B, T < 2^24.
+ * Workspace: wq_attention_shared_prefix_workspace_size() with the same
+ * arguments (0 bytes when nothing is split). */
+WQ_API size_t wq_attention_shared_prefix_workspace_size(int64_t T, int B, int max_q, int q_heads,
+                                                        const wq_paged_cache *cache,
+                                                        int64_t prefix_len, int64_t max_suffix);
+WQ_API int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_head, int64_t T,
+                                      int B, const int32_t *cu_q, int max_q, int q_heads,
+                                      const wq_paged_cache *cache, const int32_t *prefix_pages,
+                                      int64_t prefix_len, const int32_t *page_table,
+                                      int64_t ld_table, const int32_t *suffix_len,
+                                      int64_t max_suffix, float scale, void *out,
+                                      int64_t o_token, int64_t o_head, float *lse, void *ws,
+                                      size_t ws_bytes, int32_t *status, wq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,12 @@ ACC = {"i32": 0, "f32": 1}
 OUT = {"bf16": 0, "i32": 1}
 
 
+DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+NORM = {"none": 0, "rms": 1, "layer": 2}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ROPE_LAYOUT = {"half": 0, "inter": 1}
+
+
 class WQError(RuntimeError):
     pass
 
@@ -31,6 +37,21 @@ _P = _c.c_void_p
 _I = _c.c_int
 _L = _c.c_int64
 _S = _c.c_size_t
+
+_F = _c.c_float
+_D = _c.c_double
+
+
+class _PagedCache(_c.Structure):
+    """wq_paged_cache of include/wq.h."""
+    _fields_ = [("k", _P), ("v", _P),
+                ("k_page", _L), ("k_head", _L), ("k_token", _L),
+                ("v_page", _L), ("v_head", _L), ("v_token", _L),
+                ("num_pages", _L), ("page_size", _c.c_int32), ("heads", _c.c_int32),
+                ("dk", _c.c_int32), ("dv", _c.c_int32), ("dtype", _c.c_int32)]
+
+
+_PC = _c.POINTER(_PagedCache)
 
 _SIGS = {
     "wq_init": (_I, [_I]),
@@ -71,6 +92,12 @@ _SIGS = {
     "wq_moe_forward_masked_workspace_size": (_S, [_I, _I, _I, _I, _I]),
     "wq_linear_w8a8_workspace_size": (_S, [_L, _L, _L, _I]),
     "wq_linear_w8a8": (_I, [_P, _L, _L, _L, _P, _P, _L, _I, _I, _P, _P, _S, _P, _P]),
+    "wq_block_norm": (_I, [_P, _L, _P, _L, _P, _L, _F, _I, _P, _P, _I, _P, _P, _F, _L, _L, _I, _P, _L, _P, _L, _P]),
+    "wq_rope_table": (_I, [_P, _L, _I, _D, _I, _D, _D, _D, _D, _D, _P]),
+    "wq_rope": (_I, [_P, _L, _L, _P, _P, _L, _L, _I, _I, _I, _I, _I, _I, _P, _L, _L, _P, _P]),
+    "wq_rope_append_paged": (_I, [_P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _L, _L, _I, _I, _PC, _P, _L, _L, _P, _P]),
+    "wq_attention_shared_prefix_workspace_size": (_S, [_L, _I, _I, _I, _PC, _L, _L]),
+    "wq_attention_shared_prefix": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _PC, _P, _L, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P, _S, _P, _P]),
     "wq_moe_forward_masked": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P, _P]),
 }
 
@@ -607,3 +634,195 @@ def linear_w8a8(x, W, sw, scheme="channel", acc="i32", out=None, ws=None, status
            "wq_linear_w8a8")
     return out
 
+
+# ---------------------------------------------------------------- the attention half of a layer
+def _view(t, dim, dtypes, name):
+    """A CUDA tensor whose last dimension is contiguous; other strides are free."""
+    if not t.is_cuda:
+        raise WQError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise WQError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != dim:
+        raise WQError(f"{name} must have {dim} dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise WQError(f"{name} must be contiguous in its last dimension")
+    return t
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise WQError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+_FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def block_norm(block, residual=None, gate=None, scale=1.0, post="none", post_weight=None,
+               post_bias=None, pre="rms", pre_weight=None, pre_bias=None, eps=1e-6, x_out=None,
+               y=None):
+    """Norm after a block, gate, residual scale and sum, norm before the next
+    block, on rows [T, H]: h = residual + scale * (gate * N_post(block));
+    returns (h rounded, N_pre(h)).  post and pre are "none", "rms" or "layer";
+    gate is [T, H] or [H]; x_out and y may be given (block or residual too)."""
+    _view(block, 2, _FLOATS, "block")
+    dt = (block.dtype,)
+    T, H = block.shape
+    if residual is not None:
+        _shape(_view(residual, 2, dt, "residual"), (T, H), "residual")
+    ldg = 0
+    if gate is not None:
+        _shape(_view(gate, gate.dim(), dt, "gate"), (H,) if gate.dim() == 1 else (T, H), "gate")
+        ldg = gate.stride(0) if gate.dim() == 2 else 0
+    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
+                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+        if t is not None:
+            _shape(_view(t, 1, dt, name), (H,), name)
+    x_out = torch.empty_like(block, memory_format=torch.contiguous_format) if x_out is None else \
+        _shape(_view(x_out, 2, dt, "x_out"), (T, H), "x_out")
+    y = torch.empty_like(block, memory_format=torch.contiguous_format) if y is None else \
+        _shape(_view(y, 2, dt, "y"), (T, H), "y")
+    _check(lib().wq_block_norm(
+        _ptr(block), block.stride(0), _ptr(residual),
+        0 if residual is None else residual.stride(0), _ptr(gate), ldg, scale, NORM[post],
+        _ptr(post_weight), _ptr(post_bias), NORM[pre], _ptr(pre_weight), _ptr(pre_bias), eps, T, H,
+        DTYPE[block.dtype], _ptr(x_out), x_out.stride(0), _ptr(y), y.stride(0), _stream()),
+        "wq_block_norm")
+    return x_out, y
+
+
+def rope_table(max_pos, rot, base=10000.0, scaling="none", factor=1.0, trained=0, beta_fast=32.0,
+               beta_slow=1.0, mscale=0.0, device=None):
+    """Rotary table float32 [max_pos, rot/2, 2] of (cos, sin), angles in
+    float64; scaling "none", "linear", "ntk" or "yarn" for contexts `factor`
+    times the `trained` one."""
+    t = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device or "cuda")
+    _check(lib().wq_rope_table(_ptr(t), max_pos, rot, base, ROPE_SCALING[scaling], factor,
+                               float(trained), beta_fast, beta_slow, mscale, _stream()),
+           "wq_rope_table")
+    return t
+
+
+def _table(table):
+    _dev(table, torch.float32, "table")
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise WQError(f"table must be [max_pos, rot/2, 2], got {list(table.shape)}")
+    return table
+
+
+def rope(x, positions, table, layout="half", inverse=False, out=None, status=None):
+    """Rotate the first rot = 2 * table.shape[1] elements of each head of x
+    [T, heads, D] to its token's position; out may be x itself."""
+    _view(x, 3, _FLOATS, "x")
+    _table(table)
+    T, n, D = x.shape
+    _shape(_dev(positions, torch.int32, "positions"), (T,), "positions")
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else \
+        _shape(_view(out, 3, (x.dtype,), "out"), x.shape, "out")
+    _check(lib().wq_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(positions), _ptr(table),
+                         table.shape[0], T, n, D, 2 * table.shape[1], ROPE_LAYOUT[layout],
+                         int(inverse), DTYPE[x.dtype], _ptr(out), out.stride(0), out.stride(1),
+                         _ptr(status), _stream()), "wq_rope")
+    return out
+
+
+def _cache(k_cache, v_cache):
+    """The wq_paged_cache of k_cache [pages, heads, page_size, dk] and v_cache
+    [pages, heads, page_size, dv], any strides over the first three."""
+    _view(k_cache, 4, _HALVES, "k_cache")
+    _view(v_cache, 4, (k_cache.dtype,), "v_cache")
+    if k_cache.shape[:3] != v_cache.shape[:3]:
+        raise WQError("k_cache and v_cache must agree in pages, heads and page size")
+    pages, heads, page, dk = k_cache.shape
+    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
+                       *v_cache.stride()[:3], pages, page, heads, dk, v_cache.shape[3],
+                       DTYPE[k_cache.dtype])
+
+
+def _strides(t):
+    return (None, 0, 0) if t is None else (_ptr(t), t.stride(0), t.stride(1))
+
+
+def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="half", q=None,
+                      q_out=None, status=None):
+    """Write rope(k) and v [T, heads, D] at places slots int64 [T] (page *
+    page_size + place; negative: skipped) of a paged cache, and with q
+    [T, q_heads, D] return rope(q).  table None appends without rotation."""
+    c = _cache(k_cache, v_cache)
+    dt = (k_cache.dtype,)
+    T = k.shape[0]
+    _shape(_view(k, 3, dt, "k"), (T, c.heads, c.dk), "k")
+    _shape(_view(v, 3, dt, "v"), (T, c.heads, c.dv), "v")
+    _shape(_dev(slots, torch.int64, "slots"), (T,), "slots")
+    rot, max_pos = 0, 0
+    if table is not None:
+        _table(table)
+        _shape(_dev(positions, torch.int32, "positions"), (T,), "positions")
+        rot, max_pos = 2 * table.shape[1], table.shape[0]
+    if q is not None:
+        _view(q, 3, dt, "q")
+        _shape(q, (T, q.shape[1], c.dk), "q")
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else \
+            _shape(_view(q_out, 3, dt, "q_out"), q.shape, "q_out")
+    _check(lib().wq_rope_append_paged(
+        *_strides(q), 0 if q is None else q.shape[1], *_strides(k), *_strides(v),
+        _ptr(positions) if rot else None, _ptr(slots), _ptr(table), max_pos, T, rot,
+        ROPE_LAYOUT[layout], c, *_strides(q_out if q is not None else None), _ptr(status),
+        _stream()), "wq_rope_append_paged")
+    return q_out
+
+
+def attention_shared_prefix_workspace(q, k_cache, v_cache, B, prefix_len, max_suffix, max_q):
+    """A workspace for attention_shared_prefix calls of these sizes."""
+    n = lib().wq_attention_shared_prefix_workspace_size(
+        q.shape[0], B, max_q, q.shape[1], _cache(k_cache, v_cache), prefix_len, max_suffix)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+
+
+def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_table, suffix_len,
+                            max_suffix, cu_q=None, max_q=None, scale=None, out=None, lse=None,
+                            ws=None, status=None):
+    """Attention of q [T, q_heads, dk] over a paged cache: every token sees the
+    prefix_len keys in prefix_pages, and its own sequence's suffix (page_table
+    int32 [B, pages], suffix_len int32 [B]) up to itself.  cu_q int32 [B + 1]
+    splits the tokens (None: T / B each); max_q and max_suffix bound a
+    sequence's tokens and keys.  Returns out [T, q_heads, dv]; lse float32
+    [T, q_heads] is filled if given."""
+    c = _cache(k_cache, v_cache)
+    dt = (k_cache.dtype,)
+    _view(q, 3, dt, "q")
+    T, Hq, dk = q.shape
+    if dk != c.dk:
+        raise WQError(f"q and k_cache must agree in head size, got {dk} and {c.dk}")
+    _dev(suffix_len, torch.int32, "suffix_len")
+    B = suffix_len.numel()
+    _view(page_table, 2, (torch.int32,), "page_table")
+    if page_table.shape[0] != B:
+        raise WQError(f"page_table must have {B} rows, got {page_table.shape[0]}")
+    if max_suffix > page_table.shape[1] * c.page_size:
+        raise WQError(f"max_suffix {max_suffix} needs more pages than page_table has columns")
+    if prefix_len:
+        _dev(prefix_pages, torch.int32, "prefix_pages")
+        if prefix_pages.numel() * c.page_size < prefix_len:
+            raise WQError(f"prefix_len {prefix_len} needs more pages than prefix_pages holds")
+    if cu_q is not None:
+        _shape(_dev(cu_q, torch.int32, "cu_q"), (B + 1,), "cu_q")
+        if max_q is None:
+            raise WQError("cu_q needs max_q, the most tokens of a sequence")
+    elif B == 0 or T % B:
+        raise WQError(f"{T} tokens do not split evenly over {B} sequences: give cu_q")
+    else:
+        max_q = T // B
+    out = torch.empty(T, Hq, c.dv, dtype=q.dtype, device=q.device) if out is None else \
+        _shape(_view(out, 3, dt, "out"), (T, Hq, c.dv), "out")
+    if lse is not None:
+        _shape(_dev(lse, torch.float32, "lse"), (T, Hq), "lse")
+    if ws is None:
+        ws = attention_shared_prefix_workspace(q, k_cache, v_cache, B, prefix_len, max_suffix, max_q)
+    _check(lib().wq_attention_shared_prefix(
+        *_strides(q), T, B, _ptr(cu_q), max_q, Hq, c, _ptr(prefix_pages), prefix_len,
+        _ptr(page_table), page_table.stride(0), _ptr(suffix_len), max_suffix,
+        dk ** -0.5 if scale is None else scale, _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
+        _ptr(ws), ws.numel(), _ptr(status), _stream()), "wq_attention_shared_prefix")
+    return out

@@ -91,6 +91,8 @@ namespace wq {
 
 std::atomic<uint64_t> g_launches{0};
 
+int device_ok() { return check_device(); }
+
 int launched(int n) {
   g_launches.fetch_add(uint64_t(n), std::memory_order_relaxed);
   return cudaPeekAtLastError() == cudaSuccess ? WQ_OK : WQ_ERR_LAUNCH;

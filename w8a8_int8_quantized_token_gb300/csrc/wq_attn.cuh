@@ -1,0 +1,43 @@
+// Pieces shared by the attention kernels: the key ranges of a work item, the
+// page lookup and the writes of a row's result.
+#pragma once
+
+#include "wq_serve.cuh"
+
+namespace wq {
+namespace attn {
+
+// The query tokens and keys of one source: the prefix (seq = -1), seen whole
+// by every token of the call, or the suffix of one sequence.
+struct Source {
+  int t0, n;             // first query token, count
+  int len;               // keys
+  const int32_t *pages;  // its pages
+  int slot0;             // first partial-result slot
+  bool causal;
+};
+
+__device__ __forceinline__ Source source_of(const AttnArgs &a, int seq) {
+  if (seq < 0) return {0, a.T, a.P, a.prefix_pages, 0, false};
+  int t0, n;
+  if (a.cu_q) {
+    const int c0 = a.cu_q[seq], c1 = a.cu_q[seq + 1];
+    t0 = min(max(c0, 0), a.T);
+    n = min(max(c1 - t0, 0), min(a.max_q, a.T - t0));
+    if (t0 != c0 || t0 + n != c1) set_status(a.status, WQ_ERR_INDEX);
+  } else {
+    n = a.T / a.B;
+    t0 = seq * n;
+  }
+  const int l = a.max_suffix > 0 ? a.suffix_len[seq] : 0, len = min(max(l, 0), a.max_suffix);
+  if (len != l) set_status(a.status, WQ_ERR_INDEX);
+  return {t0, n, len, a.page_table + seq * a.ld_table, a.sp, true};
+}
+
+// Keys that query token j of the source sees
+__device__ __forceinline__ int visible(const Source &s, int j) {
+  return s.causal ? s.len - s.n + j + 1 : s.len;
+}
+
+}  // namespace attn
+}  // namespace wq

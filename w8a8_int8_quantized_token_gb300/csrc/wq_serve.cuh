@@ -1,0 +1,133 @@
+// Element types and vectors shared by the serving kernels (norms, rotary
+// positions, paged append, attention).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "wq_common.cuh"
+
+namespace wq {
+
+struct Bf16 {
+  using Raw = uint16_t;
+  static constexpr int kVec = 8;  // elements of a 16-byte access
+  static __device__ __forceinline__ float to_f(uint16_t v) { return bf16_to_f(v); }
+  static __device__ __forceinline__ uint16_t from_f(float f) { return f_to_bf16(f); }
+};
+struct F16 {
+  using Raw = uint16_t;
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float to_f(uint16_t v) {
+    return __half2float(__ushort_as_half(v));
+  }
+  static __device__ __forceinline__ uint16_t from_f(float f) {
+    return __half_as_ushort(__float2half_rn(f));
+  }
+};
+struct F32 {
+  using Raw = float;
+  static constexpr int kVec = 4;
+  static __device__ __forceinline__ float to_f(float v) { return v; }
+  static __device__ __forceinline__ float from_f(float f) { return f; }
+};
+
+// VW consecutive elements, VW = 1 or one 16-byte access
+template <class DT, int VW>
+struct alignas(VW == 1 ? sizeof(typename DT::Raw) : 16) Vec {
+  typename DT::Raw e[VW];
+  static __device__ __forceinline__ Vec load(const typename DT::Raw *p) {
+    Vec v;
+    if constexpr (VW == 1) {
+      v.e[0] = *p;
+    } else {
+      static_assert(sizeof(v.e) == 16, "one 16-byte access");
+      *reinterpret_cast<uint4 *>(v.e) = *reinterpret_cast<const uint4 *>(p);
+    }
+    return v;
+  }
+  __device__ __forceinline__ void store(typename DT::Raw *p) const {
+    if constexpr (VW == 1)
+      *p = e[0];
+    else
+      *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(e);
+  }
+  __device__ __forceinline__ float f(int i) const { return DT::to_f(e[i]); }
+  __device__ __forceinline__ void set(int i, float x) { e[i] = DT::from_f(x); }
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ---- launchers (host) ----
+int device_ok();  // WQ_OK on an sm_103 device
+
+struct BlockNormArgs {
+  const void *block, *residual, *gate, *w_post, *b_post, *w_pre, *b_pre;
+  int64_t ldb, ldr, ldg, ldx, ldy;
+  float scale, eps;
+  int post, pre;
+  int64_t T;
+  int H;
+  void *x_out, *y;
+};
+int launch_block_norm(const BlockNormArgs &a, int dtype, bool vec, cudaStream_t st);
+
+// One tensor of heads that a rotary launch reads and writes
+struct RopeSeg {
+  const void *src = nullptr;
+  void *dst = nullptr;
+  int64_t s_token = 0, s_head = 0;
+  int64_t d_token = 0, d_head = 0, d_page = 0;  // d_page: cache segments only
+  int heads = 0, D = 0, rot = 0;
+  bool paged = false;
+};
+struct RopeArgs {
+  RopeSeg seg[3];
+  int nseg;
+  const int32_t *positions;
+  const int64_t *slots;
+  const float *table;
+  int64_t max_pos, T, num_slots;
+  int page_size, rot, layout;
+  float sign;  // -1: inverse
+  int32_t *status;
+};
+int launch_rope(const RopeArgs &a, int dtype, bool vec, cudaStream_t st);
+int launch_rope_table(float *table, int64_t max_pos, int rot, double base, int scaling,
+                      double factor, double trained, double beta_fast, double beta_slow,
+                      double mscale, cudaStream_t st);
+
+struct AttnArgs {
+  const uint16_t *q;
+  int64_t q_token, q_head;
+  int T, B, max_q, Hq, Hkv, G;
+  const int32_t *cu_q;
+  const uint16_t *k, *v;
+  int64_t k_page, k_head, k_token, v_page, v_head, v_token, num_pages;
+  int page_size, dk, dv;
+  const int32_t *prefix_pages;
+  int P;
+  const int32_t *page_table;
+  int64_t ld_table;
+  const int32_t *suffix_len;
+  int max_suffix;
+  float scale_log2;  // scale * log2(e)
+  uint16_t *out;
+  int64_t o_token, o_head;
+  float *lse;
+  int32_t *status;
+  // plan
+  int sp, p_chunk;  // prefix: splits and keys of each (0: no prefix)
+  int ss, s_chunk;  // suffixes: splits and keys of each
+  int slots;        // sp + ss partial results a row
+  float *o_part;    // [T][Hq][slots][dv], nullptr when slots == 1
+  float *lse_part;  // [T][Hq][slots]
+};
+void plan_attention(AttnArgs &a);
+size_t attention_ws_bytes(const AttnArgs &a);
+int launch_attention(const AttnArgs &a, int dtype, cudaStream_t st);
+
+}  // namespace wq
