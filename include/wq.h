@@ -580,7 +580,7 @@ WQ_API int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, 
  * Query head a reads key head a / (q_heads / heads).
  *   out[t][a] = sum_i softmax_i(scale * q.k_i) v_i     (cache dtype)
  *   lse[t][a] = ln sum_i exp(scale * q.k_i)            (float, [T][q_heads], may be NULL)
- * A row that sees no key gets zeros and -inf.  prefix_len = 0 is ordinary
+ * with scale > 0.  A row that sees no key gets zeros and -inf.  prefix_len = 0 is ordinary
  * paged attention, max_suffix = 0 the prefix alone.  cu_q NULL: max_q tokens
  * each (T = B * max_q).  max_q and max_suffix are host bounds on the tokens and keys of a
  * sequence: values above them are cut to them, with status = WQ_ERR_INDEX;

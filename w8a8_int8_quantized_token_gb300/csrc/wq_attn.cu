@@ -418,7 +418,8 @@ int launch_small(const AttnArgs &a, cudaStream_t st) {
   if (!sized) return WQ_ERR_LAUNCH;
   constexpr int R = 16 * MT;
   const int64_t pt = (int64_t(a.T) * a.G + R - 1) / R, stl = (int64_t(a.max_q) * a.G + R - 1) / R;
-  const int64_t pi = a.sp * pt * a.Hkv, si = a.ss * stl * a.Hkv * a.B;
+  const int64_t pi = a.tc_prefix ? 0 : a.sp * pt * a.Hkv;
+  const int64_t si = a.tc_suffix ? 0 : a.ss * stl * a.Hkv * a.B;
   if (pi + si == 0) return WQ_OK;
   if (pi + si >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
   k<<<unsigned(pi + si), NW * 32, P::SMEM, st>>>(a, int(pi), int(pt), int(stl));
@@ -428,7 +429,8 @@ int launch_small(const AttnArgs &a, cudaStream_t st) {
 template <class DT>
 int launch_t(const AttnArgs &a, cudaStream_t st) {
   const bool wide = a.dk > 64 || a.dv > 64, two = int64_t(a.max_q) * a.G > 16;
-  int rc;
+  int rc = launch_attention_tiles(a, std::is_same<DT, Bf16>::value ? WQ_DT_BF16 : WQ_DT_F16, st);
+  if (rc != WQ_OK) return rc;
   if (wide) rc = two ? launch_small<DT, 128, 2>(a, st) : launch_small<DT, 128, 1>(a, st);
   else rc = two ? launch_small<DT, 64, 2>(a, st) : launch_small<DT, 64, 1>(a, st);
   if (rc != WQ_OK || !a.o_part) return rc;
@@ -451,10 +453,23 @@ void plan_attention(AttnArgs &a) {
     chunk = int(((keys + n - 1) / n + 63) / 64 * 64);
     splits = int((keys + chunk - 1) / chunk);
   };
-  const int64_t R = int64_t(a.max_q) * a.G > 16 ? 32 : 16;
-  cut((int64_t(a.T) * a.G + R - 1) / R * a.Hkv, a.P, a.sp, a.p_chunk);
-  cut((int64_t(a.max_q) * a.G + R - 1) / R * a.Hkv * a.B, a.max_suffix, a.ss, a.s_chunk);
+  // The tensor-memory kernel takes 128-row tiles and loads pages by TMA in
+  // boxes of 8 rows or more with pitches that differ from zero.
+  const bool pitches = (a.k_token || a.page_size == 1) && (a.k_head || a.Hkv == 1) &&
+                       (a.k_page || a.num_pages <= 1) && (a.v_token || a.page_size == 1) &&
+                       (a.v_head || a.Hkv == 1) && (a.v_page || a.num_pages <= 1);
+  const bool tiles = a.page_size % 8 == 0 && a.num_pages > 0 && pitches;
+  const int64_t rows_p = int64_t(a.T) * a.G, rows_s = int64_t(a.max_q) * a.G;
+  a.tc_prefix = tiles && a.P > 0 && rows_p > 32;
+  a.tc_suffix = tiles && a.max_suffix > 0 && rows_s > 32;
+  const int64_t R = rows_s > 16 ? 32 : 16;
+  if (a.tc_prefix) plan_prefix_tiles(a);
+  else cut((rows_p + R - 1) / R * a.Hkv, a.P, a.sp, a.p_chunk);
+  const int64_t sr = a.tc_suffix ? 2 * (128 / a.G) * a.G : R;
+  cut((rows_s + sr - 1) / sr * a.Hkv * a.B * (a.tc_suffix ? 8 : 1), a.max_suffix, a.ss, a.s_chunk);
+  if (a.tc_suffix && a.s_chunk % 128) a.s_chunk += 64;
   if (a.sp + a.ss == 0) a.ss = 1;  // no keys at all: one empty range writes the zeros
+  if (a.ss && a.s_chunk) a.ss = (a.max_suffix + a.s_chunk - 1) / a.s_chunk;
   a.slots = a.sp + a.ss;
 }
 

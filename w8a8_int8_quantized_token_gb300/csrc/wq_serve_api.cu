@@ -1,5 +1,7 @@
 // C ABI of the serving operators around the MoE layer: host-side argument
 // checks.  Contracts are in include/wq.h.
+#include <cmath>
+
 #include "wq_serve.cuh"
 
 using namespace wq;
@@ -207,7 +209,9 @@ int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_head, i
   AttnArgs a;
   int rc = fill_attention(a, T, B, max_q, q_heads, cache, prefix_len, max_suffix);
   if (rc != WQ_OK) return rc;
-  if (q_token < 0 || q_head < 0 || o_token < 0 || o_head < 0 || ld_table < 0) return WQ_ERR_INVALID_ARG;
+  if (q_token < 0 || q_head < 0 || o_token < 0 || o_head < 0 || ld_table < 0 || !(scale > 0.0f) ||
+      !(scale < INFINITY))
+    return WQ_ERR_INVALID_ARG;
   if (T == 0) return WQ_OK;
   if (B < 1 || !q || !out || !cache->k || !cache->v || (prefix_len > 0 && !prefix_pages))
     return WQ_ERR_INVALID_ARG;

@@ -379,6 +379,11 @@ bool make_tma_2d_b16_sw128(CUtensorMap *m, const void *ptr, int64_t rows, int64_
 // 2-D 16-bit tensor [rows][cols], box box_cols x box_rows, no swizzle
 bool make_tma_2d_b16(CUtensorMap *m, const void *ptr, int64_t rows, int64_t cols, int box_cols,
                      int box_rows);
+// 16-bit tensor of `rank` dimensions (innermost first; `strides` in elements,
+// of dimensions 1 and up), box `box`, landing 128-byte swizzled, zero fill
+// outside the tensor; box[0] is 64 elements
+bool make_tma_nd_b16_sw128(CUtensorMap *m, const void *ptr, int rank, const int64_t *dims,
+                           const int64_t *strides, const int *box);
 bool tma_available();
 int num_sms();
 
