@@ -463,8 +463,8 @@ void plan_attention(AttnArgs &a) {
   a.tc_prefix = tiles && a.P > 0 && rows_p > 32;
   a.tc_suffix = tiles && a.max_suffix > 0 && rows_s > 32;
   const int64_t R = rows_s > 16 ? 32 : 16;
-  if (a.tc_prefix) plan_prefix_tiles(a);
-  else cut((rows_p + R - 1) / R * a.Hkv, a.P, a.sp, a.p_chunk);
+  a.tc_prefix = a.tc_prefix && plan_prefix_tiles(a);
+  if (!a.tc_prefix) cut((rows_p + R - 1) / R * a.Hkv, a.P, a.sp, a.p_chunk);
   const int64_t sr = a.tc_suffix ? 2 * (128 / a.G) * a.G : R;
   cut((rows_s + sr - 1) / sr * a.Hkv * a.B * (a.tc_suffix ? 8 : 1), a.max_suffix, a.ss, a.s_chunk);
   if (a.tc_suffix && a.s_chunk % 128) a.s_chunk += 64;

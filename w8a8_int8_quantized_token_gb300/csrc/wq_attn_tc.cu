@@ -9,26 +9,30 @@
 // alternate on the tensor cores: while one tile's scores are exponentiated,
 // the other's products run.
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread owns one row
-//   warp 8          tensor memory and MMA issue (one thread)
-//   warp 9          TMA: queries, and keys and values page by page
-//   warps 10, 11    none (the third warpgroup gives its registers to the others)
+//   warps 8, 9      MMA issue of row tile 0, 1; warp 8 owns the tensor memory
+//   warp 10         TMA: queries, and keys and values page by page
+//   warp 11         none (the third warpgroup gives its registers to the others)
 // Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).  P takes the
 // place of its S (64 columns, 16-bit pairs) as the A operand of the second
 // product.  O is rescaled only when a row's maximum has grown by more than
 // 2^8 over the one in use: until then the weights are at most 2^8, their sum
 // stays exact in the same sense, and the final division removes the factor.
 //
-// The range is cut two ways.  The prefix is the same for all tokens: its
-// (key head, row tile pair) items times 128-key tiles form one line of equal
-// units, which the blocks cut into equal pieces, so a piece may end inside an
-// item and begin the next; each piece leaves a partial result.  Suffixes: a
+// The range is cut two ways.  The prefix is the same for all tokens.  A gang
+// of blocks, one per row tile pair, walks the same keys at the same time, so
+// that a tile of keys comes from HBM once and from L2 for the other members
+// (blocks that walk apart read a prefix larger than L2 once each: 160 us of
+// HBM time where 24 are needed, at 256 sequences behind 32768 keys of 8
+// heads).  (key head, group of pairs) items times 128-key tiles form one line
+// of equal units that the gangs cut into equal pieces: a piece may end inside
+// an item and begin the next, and each leaves a partial result.  Suffixes: a
 // block per (range, sequence, key head, row tile pair).
 //
 // Values past the end of a range may be anything (a page is shared with
 // unwritten places), and 0 * NaN is NaN: the last tile's tail is cleared in
 // shared memory before its product.
 //
-// Every wait is bounded (1 s); on expiry the kernel records WQ_ERR_TIMEOUT,
+// Every wait is bounded (about 1 s); on expiry the kernel records WQ_ERR_TIMEOUT,
 // waits (bounded) for its own copies and MMAs, frees tensor memory and exits.
 #include <algorithm>
 #include <type_traits>
@@ -44,7 +48,9 @@ using namespace attn;
 
 constexpr int BM = 128, BN = 128;  // rows of a tile, keys of a tile
 constexpr int NTHREADS = 384;
-constexpr int WARP_MMA = 8, WARP_TMA = 9;  // of the third warpgroup; its other two warps idle
+constexpr int WARP_MMA = 8, WARP_TMA = 10, WARP_IDLE = 11;  // MMA: one warp per row tile
+
+
 // Registers a thread: 3 x 168 at launch (the most for 384 threads), shared out
 // as 2 x 216 for the softmax, which holds a row of 128 scores, and 72
 constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
@@ -62,9 +68,9 @@ struct Plan {
   static constexpr int B_FULL = 0, B_EMPTY = NS, B_Q_FULL = 2 * NS, B_Q_EMPTY = B_Q_FULL + 1,
                        B_S = B_Q_EMPTY + 1,      // [2] scores of a row tile are in
       B_P = B_S + 2,                             // [2][2] half a tile of weights is in
-      B_O = B_P + 4,                             // [2] a value product is done
+      B_O = B_P + 4,                             // [2] a piece's last value product is done
       B_TAIL = B_O + 2,                          // a last value tile's tail is cleared
-      B_DONE = B_TAIL + 1, NBAR = B_DONE + 1;
+      B_DONE = B_TAIL + 1, NBAR = B_DONE + 2;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
@@ -73,6 +79,33 @@ struct Plan {
   static_assert(2 * BN + 2 * D <= 512, "tensor memory plan");
 };
 
+// Bounded wait of one thread.  A try suspends the thread for about 4 us by
+// itself (7800 cycles measured) before it gives up, so 2^18 of them are about
+// a second, and no clock is read.  A warp waits through one lane: the products
+// read their operands from shared memory at its full rate, and 32 lanes that
+// poll a barrier take that rate from them.
+constexpr int kTries = 1 << 18;
+__device__ __forceinline__ bool wait_one(uint32_t b, uint32_t parity, volatile int *abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < kTries; ++i) {
+    if (mbar_try(b, parity)) return true;
+    if (*abort_flag) return false;
+  }
+  return false;
+}
+// One lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t b, uint32_t parity, volatile int *abort_flag) {
+  bool ok = false;
+  if ((threadIdx.x & 31) == 0) ok = wait_one(b, parity, abort_flag);
+  return __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -116,6 +149,37 @@ __device__ __forceinline__ void fma2(float &a0, float &a1, float m, float c) {
       : "+f"(a0), "+f"(a1)
       : "f"(m), "f"(c));
 }
+// the wait for a load of 32 columns, with its registers as operands: their
+// values count from here on
+__device__ __forceinline__ void wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                 "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+                 "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
+                 "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                 "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]),
+                 "+r"(v[31])
+               :
+               : "memory");
+}
+// more registers that the same wait brought in
+__device__ __forceinline__ void pin32(uint32_t (&v)[32]) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]),
+                 "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]),
+                 "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]),
+                 "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                 "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]),
+                 "+r"(v[31]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -127,9 +191,13 @@ struct Cut {
   int tpt;            // tokens of a row tile: 128 / G
   int pairs_p;        // row tile pairs of the prefix (0: no prefix here)
   int units_p;        // 128-key tiles of the prefix
-  int blocks_p;       // blocks that share the prefix's line of units
+  int gang, gangs;    // row tile pairs that walk together; gangs on the prefix's line of units
+  int groups;         // gangs' worths of pairs: ceil(pairs_p / gang)
+  int stretch;        // units of a gang (the last may have fewer)
   int pairs_s;        // row tile pairs of a suffix (0: no suffixes here)
-  int box;            // cache rows of one TMA box
+    int box;            // cache rows of one TMA box
+  int step_pages, step_place;  // 128 keys on: pages, and places beyond them
+
   bool out16;         // out rows take 16-byte stores
 };
 
@@ -141,21 +209,17 @@ struct Piece {
   int slot, last;     // partial-result slot; slots (slot, last) stay empty
 };
 
-__device__ __forceinline__ Piece prefix_piece(const AttnArgs &a, const Cut &c, int64_t u0,
-                                              int64_t u1, int block) {
-  const int64_t total = int64_t(a.Hkv) * c.pairs_p * c.units_p;
-  const int item = int(u0 / c.units_p);
-  const int64_t start = int64_t(item) * c.units_p;
+// units u0 .. u1 of one item, for member `member` of gang `gang`
+__device__ __forceinline__ Piece prefix_piece(const AttnArgs &a, const Cut &c, int u0, int u1,
+                                              int gang, int member) {
+  const int item = u0 / c.units_p, start = item * c.units_p;
   Piece p;
   p.s = source_of(a, -1);
-  p.head = item / c.pairs_p;
-  p.tok0 = (item % c.pairs_p) * 2 * c.tpt;
-  p.k0 = int(u0 - start) * BN;
-  const int64_t e = u1 - start;
-  p.k1 = e >= c.units_p ? a.P : int(e) * BN;
-  // ordinal of this block among those that share the item
-  const int first = int(((start + 1) * c.blocks_p - 1) / total);
-  p.slot = block - first;
+  p.head = item / c.groups;
+  p.tok0 = ((item - p.head * c.groups) * c.gang + member) * 2 * c.tpt;
+  p.k0 = (u0 - start) * BN;
+  p.k1 = u1 - start >= c.units_p ? a.P : (u1 - start) * BN;
+  p.slot = gang - start / c.stretch;  // ordinal of this gang among those that share the item
   p.last = p.k1 == a.P ? a.sp : p.slot + 1;
   return p;
 }
@@ -193,7 +257,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < P::NBAR; ++i) mbar_init(bar(i), i >= P::B_P && i < P::B_O ? 4 : 1);
+        for (int i = 0; i < P::NBAR; ++i)
+      mbar_init(bar(i), i == P::B_Q_EMPTY ? 8                      // softmax warps
+                                                                        : i >= P::B_P && i < P::B_O ? 4            // warps of a row tile
+                        : i >= P::B_EMPTY && i < P::B_Q_FULL ? 2   // row tiles
+                                                             : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WARP_MMA) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -202,29 +270,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  auto fail = [&]() {
-    *abort_flag = 1;
-    set_status(a.status, WQ_ERR_TIMEOUT);
-  };
+    bool ok = true;  // this role's waits all ended in time
+
 
   // ---- this block's pieces, the same list for every role
-  const bool line = int(blockIdx.x) < c.blocks_p;
-  const int64_t total = int64_t(a.Hkv) * c.pairs_p * c.units_p;
-  const int64_t u_begin = line ? int64_t(blockIdx.x) * total / c.blocks_p : 0;
-  const int64_t u_end = line ? int64_t(blockIdx.x + 1) * total / c.blocks_p : 1;
+  const int gang = int(blockIdx.x) / max(c.gang, 1), member = int(blockIdx.x) - gang * c.gang;
+  const bool line = gang < c.gangs;
+  const int u_begin = line ? gang * c.stretch : 0;
+  const int u_end = line ? min(u_begin + c.stretch, a.Hkv * c.groups * c.units_p) : 1;
   // calls f(piece, key tiles, row tiles in use); stops when f returns false
   auto pieces = [&](auto &&f) {
-    for (int64_t u = u_begin; u < u_end;) {
+    for (int u = u_begin; u < u_end;) {
       Piece p;
       if (line) {
-        const int64_t stop = min((u / c.units_p + 1) * c.units_p, u_end);
-        p = prefix_piece(a, c, u, stop, int(blockIdx.x));
+        const int stop = min((u / c.units_p + 1) * c.units_p, u_end);
+        p = prefix_piece(a, c, u, stop, gang, member);
         u = stop;
       } else {
-        p = suffix_piece(a, c, int64_t(blockIdx.x) - c.blocks_p);
+        p = suffix_piece(a, c, int64_t(blockIdx.x) - int64_t(c.gang) * c.gangs);
         u = u_end;
       }
-      if (p.tok0 >= p.s.n) return;
+      if (p.tok0 >= p.s.n) continue;  // a gang's last group, a short sequence
       const int n = p.k1 > p.k0 ? (p.k1 - p.k0 + BN - 1) / BN : 0;
       if (!f(p, n, p.tok0 + c.tpt < p.s.n ? 2 : 1)) return;
     }
@@ -234,149 +300,198 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
     if (warp == WARP_TMA) {
       // ------------------------------------------------------------ copies
-      int g = 0;       // ring stages issued
-      int q = 0;       // pieces with keys
-      int tails = 0;
-      bool ok = true;
+      int s = 0, g = 0, q = 0;  // ring stage; stages issued; pieces with keys
+      uint32_t ph = 1;          // parity of the ring's releases
+      bool bad = false;         // a page id outside the cache
       const int nbox = BN / c.box;
-      auto wait = [&](int b, uint32_t parity) {
-        if (__all_sync(0xffffffffu, mbar_wait<200>(bar(b), parity, abort_flag))) return true;
-        fail();
-        ok = false;
-        return false;
-      };
+      const bool leader = elect_one();
       pieces([&](const Piece &p, int n, int tiles) {
         if (n == 0) return true;
-        if (!wait(P::B_Q_EMPTY, (q & 1) ^ 1)) return false;
-        if (lane == 0) {
+        if (!(ok = wait_warp(bar(P::B_Q_EMPTY), (q & 1) ^ 1, abort_flag))) return false;
+        if (leader) {
           mbar_expect_tx(bar(P::B_Q_FULL), uint32_t(tiles * P::CH * c.tpt * a.G * 128));
+#pragma unroll 1
           for (int t = 0; t < tiles; ++t)
             for (int ch = 0; ch < P::CH; ++ch)
               tma_load_3d(base + P::OFF_Q + t * P::QB + ch * BM * 128, &tmQ, ch * 64, p.head * a.G,
                           p.s.t0 + p.tok0 + t * c.tpt, bar(P::B_Q_FULL));
         }
         ++q;
+        // lane b looks up box b of a tile, one tile ahead of its copies; a bad
+        // page is read outside the tensor: zeros
+        const int key0 = p.k0 + lane * c.box;
+        int pi = key0 / a.page_size, place = key0 - pi * a.page_size;
+        int left = lane < nbox ? p.k1 - key0 : 0;  // keys from this lane's box on
+        int page = left > 0 ? p.s.pages[pi] : 0;
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
-          const int kb = p.k0 + j * BN;
-          const int boxes = min(nbox, (p.k1 - kb + c.box - 1) / c.box);  // with a key in range
-          // lane b looks box b up; a bad page is read outside the tensor: zeros
-          int page = int(a.num_pages), place = 0;
-          if (lane < boxes) {
-            const int key = kb + lane * c.box, pi = key / a.page_size;
-            place = key - pi * a.page_size;
-            page = p.s.pages[pi];
-            if (page < 0 || page >= a.num_pages) {
-              set_status(a.status, WQ_ERR_INDEX);
-              page = int(a.num_pages);
-            }
+          int y = place, w = page;
+          if (left > 0 && unsigned(w) >= unsigned(a.num_pages)) {
+            w = int(a.num_pages);
+            bad = true;
           }
-          for (int kv = 0; kv < 2; ++kv, ++g) {
-            const int s = g % P::NS;
-            if (!wait(P::B_EMPTY + s, ((g / P::NS) & 1) ^ 1)) return false;
-            const uint32_t dst = base + P::OFF_KV + uint32_t(s * P::KVB);
-            if (lane == 0) mbar_expect_tx(bar(P::B_FULL + s), uint32_t(boxes * c.box * P::CH * 128));
-            __syncwarp();
-            if (lane < boxes) {
-  #pragma unroll
-              for (int ch = 0; ch < P::CH; ++ch)
-                tma_load_4d(dst + uint32_t(ch * BN + lane * c.box) * 128, kv ? &tmV : &tmK, ch * 64,
-                            place, p.head, page, bar(P::B_FULL + s));
-            }
-            __syncwarp();
-            if (kv && kb + BN > p.k1) {
-              // clear the values past the range, once the copies are in
-              if (!wait(P::B_FULL + s, (g / P::NS) & 1)) {
-                ++g;
-                return false;
+          const int boxes = __popc(__ballot_sync(0xffffffffu, left > 0));  // with a key in range
+          pi += c.step_pages;
+          place += c.step_place;
+          if (place >= a.page_size) place -= a.page_size, ++pi;
+          left -= BN;
+          if (left > 0) page = p.s.pages[pi];
+          auto stage = [&](const CUtensorMap *map) {
+            ok = wait_warp(bar(P::B_EMPTY + s), ph, abort_flag);
+            if (!ok) return false;
+            const uint32_t full = bar(P::B_FULL + s);
+            uint32_t dst = base + P::OFF_KV + uint32_t(s * P::KVB);
+            if (leader) mbar_expect_tx(full, uint32_t(boxes * c.box * P::CH * 128));
+#pragma unroll 1
+            for (int b = 0; b < boxes; ++b) {
+              const int by = __shfl_sync(0xffffffffu, y, b), bw = __shfl_sync(0xffffffffu, w, b);
+              if (leader) {
+#pragma unroll
+                for (int ch = 0; ch < P::CH; ++ch)
+                  tma_load_4d(dst + ch * BN * 128, map, ch * 64, by, p.head, bw, full);
               }
-              uint8_t *v = sm + P::OFF_KV + s * P::KVB;
-              const int r0 = p.k1 - kb;
-              for (int i = lane; i < (BN - r0) * 8 * P::CH; i += 32) {
-                const int row = i / (8 * P::CH), ch = i % (8 * P::CH);
-                *reinterpret_cast<uint4 *>(v + ((ch / 8) * BN + r0 + row) * 128 + (ch % 8) * 16) =
-                    make_uint4(0, 0, 0, 0);
-              }
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(P::B_TAIL));
-              ++tails;
+              dst += uint32_t(c.box * 128);
             }
+            if (++s == P::NS) s = 0, ph ^= 1;
+            ++g;
+            return true;
+          };
+          if (!stage(&tmK) || !stage(&tmV)) return false;
+        }
+        const int r0 = (p.k1 - p.k0) % BN;
+        if (r0) {
+          // clear the values past the range, once the last copies are in
+          const int sv = (g - 1) % P::NS;
+          if (!(ok = wait_warp(bar(P::B_FULL + sv), ((g - 1) / P::NS) & 1, abort_flag))) return false;
+          uint8_t *v = sm + P::OFF_KV + sv * P::KVB;
+#pragma unroll 1
+          for (int i = lane; i < (BN - r0) * 8 * P::CH; i += 32) {
+            const int row = i / (8 * P::CH), ch = i % (8 * P::CH);
+            *reinterpret_cast<uint4 *>(v + ((ch / 8) * BN + r0 + row) * 128 + (ch % 8) * 16) =
+                make_uint4(0, 0, 0, 0);
           }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(P::B_TAIL));
         }
         return true;
       });
+      if (bad) set_status(a.status, WQ_ERR_INDEX);
       if (!ok) {  // let copies already in flight land before the block goes away
+        *abort_flag = 1;
         if (q > 0) mbar_wait_bounded(bar(P::B_Q_FULL), (q - 1) & 1);
         for (int i = g > P::NS ? g - P::NS : 0; i < g; ++i)
           mbar_wait_bounded(bar(P::B_FULL + i % P::NS), (i / P::NS) & 1);
       }
-    } else if (warp == WARP_MMA) {
+    } else if (warp != WARP_IDLE) {
       // ------------------------------------------------------------ products
-      if (lane == 0) {
-        constexpr uint32_t id_s = idesc_f16(BM, BN) | kTypes<DT>;
-        constexpr uint32_t id_o = idesc_f16(BM, D) | kTypes<DT> | kBTransposed;
-        int g = 0, q = 0, tails = 0;
-        int done[2] = {0, 0};  // key tiles each row tile has worked on
-        auto wait = [&](int b, uint32_t parity) {
-          if (mbar_wait(bar(b), parity, abort_flag)) return true;
-          fail();
-          return false;
-        };
-        auto scores = [&](int t, int stage) {
-          const uint32_t qa = base + P::OFF_Q + t * P::QB, ka = base + P::OFF_KV + uint32_t(stage * P::KVB);
-  #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t o = uint32_t(k / 4) * (BM * 128) + uint32_t(k % 4) * 32;
-            mma_f16(tmem + t * BN, sdesc(qa + o), sdesc(ka + o), id_s, k ? 1u : 0u);
-          }
-          mma_commit(bar(P::B_S + t));
-        };
-        pieces([&](const Piece &p, int n, int tiles) {
-          if (n == 0) return true;
-          if (!wait(P::B_Q_FULL, q & 1)) return false;
+      // A warp per row tile walks, waits and (one lane) issues: PV of tile j,
+      // then QK of tile j + 1.  The two take turns, which keeps the row tiles
+      // half a step apart, and each does its waits in the other's turn: a wait
+      // takes over 100 cycles even when there is nothing to wait for.  After a
+      // wait that ran out a warp still takes its turns, so that the other ends.
+      const int t = warp - WARP_MMA;
+      const bool leader = elect_one();
+      constexpr uint32_t id_s = idesc_f16(BM, BN) | kTypes<DT>;
+      constexpr uint32_t id_o = idesc_f16(BM, D) | kTypes<DT> | kBTransposed;
+      const uint32_t ts = tmem + t * BN, to = tmem + P::T_O + t * D;
+      const uint64_t dq = sdesc(base + P::OFF_Q + t * P::QB);
+      int s = 0, q = 0, tails = 0;  // ring stage; pieces; cleared tails
+      uint32_t ph = 0, pp = 0;      // parity of the ring; of the weights
+      auto wait = [&](int b, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, wait_one(bar(b), parity, abort_flag));
+        if (!ok) *abort_flag = 1;
+      };
+      auto next = [&]() {
+        if (++s == P::NS) s = 0, ph ^= 1;
+      };
+      auto scores = [&](int stage) {
+        const uint64_t dk = sdesc(base + P::OFF_KV + uint32_t(stage * P::KVB));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = ((k / 4) * (BM * 128) + (k % 4) * 32) >> 4;
+          mma_f16(ts, dq + o, dk + o, id_s, k ? 1u : 0u);
+        }
+        mma_commit(bar(P::B_S + t));
+      };
+      // both row tiles release a stage; where there is one, it counts twice
+      auto release = [&](int stage, int tiles) {
+        mma_commit(bar(P::B_EMPTY + stage));
+        if (tiles == 1) mbar_arrive(bar(P::B_EMPTY + stage));
+      };
+      auto turn = [&](int tiles) {  // wait for it
+        if (tiles == 2) named_sync(1 + t, 64);
+      };
+      auto pass = [&](int tiles) {
+        if (tiles == 2) asm volatile("bar.arrive %0, 64;" ::"r"(2 - t) : "memory");
+      };
+      pieces([&](const Piece &p, int n, int tiles) {
+        if (n == 0) return true;
+        const bool tail = (p.k1 - p.k0) % BN != 0;
+        if (t >= tiles) {  // no rows here: step over the piece's stages
+          for (int i = 0; i < 2 * n; ++i) next();
           ++q;
-          if (!wait(P::B_FULL + g % P::NS, (g / P::NS) & 1)) return false;
-          tc_fence_after();
-          for (int t = 0; t < tiles; ++t) scores(t, g % P::NS);
-          mma_commit(bar(P::B_EMPTY + g % P::NS));
-          ++g;
-          for (int j = 0; j < n; ++j) {
-            const int sv = g % P::NS, sk = (g + 1) % P::NS;
-            if (!wait(P::B_FULL + sv, (g / P::NS) & 1)) return false;
-            if (p.k0 + (j + 1) * BN > p.k1) {
-              if (!wait(P::B_TAIL, tails & 1)) return false;
-              ++tails;
-            }
-            const uint32_t va = base + P::OFF_KV + uint32_t(sv * P::KVB);
-            for (int t = 0; t < tiles; ++t) {
-              const uint32_t ph = done[t] & 1;
-  #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (!wait(P::B_P + 2 * t + h, ph)) return false;
-                tc_fence_after();
-  #pragma unroll
-                for (int k = 4 * h; k < 4 * h + 4; ++k)
-                  mma_f16_ts(tmem + P::T_O + t * D, tmem + t * BN + 8 * k, sdesc_n(va + 2048 * k), id_o,
-                             (j | k) ? 1u : 0u);
-              }
-              mma_commit(bar(P::B_O + t));
-              ++done[t];
-              if (j + 1 < n) {
-                if (!wait(P::B_FULL + sk, ((g + 1) / P::NS) & 1)) return false;
-                tc_fence_after();
-                scores(t, sk);
-              }
-            }
-            mma_commit(bar(P::B_EMPTY + sv));
-            if (j + 1 < n) mma_commit(bar(P::B_EMPTY + sk));
-            g += j + 1 < n ? 2 : 1;
-          }
-          mma_commit(bar(P::B_Q_EMPTY));
+          tails += tail;
           return true;
-        });
-        mma_commit(bar(P::B_DONE));
-        mbar_wait_bounded(bar(P::B_DONE), 0);
-      }
+        }
+        if (t == 1) pass(tiles);  // row tile 0 begins
+        wait(P::B_Q_FULL, q & 1);
+        wait(P::B_FULL + s, ph);
+        ++q;
+        turn(tiles);
+        tc_fence_after();
+        if (leader && ok) {
+          scores(s);
+          release(s, tiles);
+        }
+        pass(tiles);
+        next();
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int sv = s;
+          const bool more = j + 1 < n;
+          wait(P::B_FULL + sv, ph);
+          next();
+          if (more) {
+            wait(P::B_FULL + s, ph);
+          } else if (tail) {
+            wait(P::B_TAIL, tails & 1);
+            ++tails;
+          }
+          const uint64_t dv = sdesc_n(base + P::OFF_KV + uint32_t(sv * P::KVB));
+          wait(P::B_P + 2 * t, pp);
+          turn(tiles);
+          tc_fence_after();
+          if (leader && ok) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ts(to, ts + 8 * k, dv + ((2048 * k) >> 4), id_o, (j | k) ? 1u : 0u);
+          }
+          wait(P::B_P + 2 * t + 1, pp);
+          pp ^= 1;
+          tc_fence_after();
+          if (leader && ok) {
+#pragma unroll
+            for (int k = 4; k < 8; ++k)
+              mma_f16_ts(to, ts + 8 * k, dv + ((2048 * k) >> 4), id_o, 1u);
+            if (more) {
+              scores(s);
+            } else {
+              mma_commit(bar(P::B_O + t));
+            }
+          }
+          // the last turn of row tile 1 is nobody's to wait for
+          if (t == 0 || more) pass(tiles);
+          if (leader && ok) {
+            release(sv, tiles);
+            if (more) release(s, tiles);
+          }
+          if (more) next();
+        }
+        return true;  // through all pieces, turns and all
+      });
+      if (leader) mma_commit(bar(P::B_DONE + t));
+      mbar_wait_bounded(bar(P::B_DONE + t), 0);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
@@ -386,68 +501,41 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t ts = tmem + lanes + t * BN, to = tmem + lanes + P::T_O + t * D;
     const float sl2 = a.scale_log2;
     int done = 0;  // key tiles so far
+        int q = 0;     // pieces with keys so far
+    int mine_pieces = 0;  // of them with this row tile
     pieces([&](const Piece &p, int n, int tiles) {
-      if (t >= tiles) return true;
+      // the queries of a piece are released by the eight softmax warps: their
+      // tiles serve as staging for the piece's results
+      auto release = [&]() {
+        if (n == 0) return;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(P::B_Q_EMPTY));
+      };
+      if (n > 0) ++q;
+      if (t >= tiles) {
+        // not before the piece's queries are in: its release must not count
+        // for the piece before
+        if (n > 0 && !(ok = wait_warp(bar(P::B_Q_FULL), (q - 1) & 1, abort_flag))) return false;
+        release();
+        return true;
+      }
       const int tok = row / a.G, j0 = p.tok0 + t * c.tpt + tok;
       const bool mine = tok < c.tpt && j0 < p.s.n;
       const int lim = mine ? min(p.k1, visible(p.s, j0)) : 0;
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j, ++done) {
         const int kb = p.k0 + j * BN;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(P::B_S + t), done & 1, abort_flag))) {
-          fail();
-          return false;
-        }
+        if (!(ok = wait_warp(bar(P::B_S + t), done & 1, abort_flag))) return false;
         tc_fence_after();
         uint32_t v[4][32];
+        
+        // 64 weights under the maximum in use, two to a word
+        uint32_t w[32];
+        float sum[4], top = -INFINITY;
+        auto weigh = [&](int h, float neg) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, v[i]);
-        tmem_wait_ld();
-        if (__any_sync(0xffffffffu, kb + BN > lim)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (kb + 32 * i + e >= lim) v[i][e] = 0xff800000u;  // -inf
-        }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = __uint_as_float(v[i][0]);
-#pragma unroll
-          for (int e = 1; e + 1 < 32; e += 2)
-            mx[i] = max3(mx[i], __uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1]));
-          mx[i] = fmaxf(mx[i], __uint_as_float(v[i][31]));
-        }
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        const bool grow = m != -INFINITY && (top - m) * sl2 > 8.0f;
-        if (__any_sync(0xffffffffu, grow)) {
-          // the product of the tile before has to be in before O is scaled
-          if (j > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(P::B_O + t), (done - 1) & 1, abort_flag))) {
-            fail();
-            return false;
-          }
-          tc_fence_after();
-          const float f = grow ? ex2((m - top) * sl2) : 1.0f;
-          l *= f;
-          if (grow) m = top;
-#pragma unroll 1
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tmem_ld32(to + 32 * i, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(to + 32 * i, o);
-          }
-          tmem_wait_st();
-        }
-        if (m == -INFINITY) m = top;
-        const float neg = m == -INFINITY ? 0.0f : -m * sl2;
-        float sum[4] = {};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+          for (int i = 0; i < 4; ++i) sum[i] = 0.0f;
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             float x = __uint_as_float(v[2 * h + e / 32][e % 32]);
@@ -455,23 +543,74 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             fma2(x, y, sl2, neg);
             x = ex2(x);
             y = ex2(y);
-            add2(sum[(e & 2)], sum[(e & 2) + 1], x, y);
+            add2(sum[e & 2], sum[(e & 2) + 1], x, y);
             w[e / 2] = pack2<DT>(x, y);
           }
+        };
+        auto top_of = [&](int i) {
+          float m0 = __uint_as_float(v[i][0]), m1 = __uint_as_float(v[i][1]);
+#pragma unroll
+          for (int e = 2; e < 30; e += 4) {
+            m0 = max3(m0, __uint_as_float(v[i][e]), __uint_as_float(v[i][e + 1]));
+            m1 = max3(m1, __uint_as_float(v[i][e + 2]), __uint_as_float(v[i][e + 3]));
+          }
+          top = max3(top, max3(m0, __uint_as_float(v[i][30]), __uint_as_float(v[i][31])), m1);
+        };
+        auto hand_over = [&](int h) {
           tmem_st32(ts + 32 * h, w);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(P::B_P + 2 * t + h));
+          l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
+        };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, v[i]);
+        wait_ld32(v[0]);
+        pin32(v[1]);
+        pin32(v[2]);
+        pin32(v[3]);
+        if (__any_sync(0xffffffffu, kb + BN > lim)) {  // keys out of this row's sight
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (kb + 32 * i + e >= lim) v[i][e] = 0xff800000u;  // -inf
         }
-        l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top_of(i);
+        const bool grow = top > m && !((top - m) * sl2 <= 8.0f);
+        if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow && m != -INFINITY ? ex2((m - top) * sl2) : 1.0f;
+          if (grow) m = top;
+          l *= f;
+          // these scores are in, so the value product of the tile before is too
+          if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tmem_ld16(to + 16 * i, o);
+              asm volatile("tcgen05.wait::ld.sync.aligned;"
+                           : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]),
+                             "+r"(o[6]), "+r"(o[7]), "+r"(o[8]), "+r"(o[9]), "+r"(o[10]), "+r"(o[11]),
+                             "+r"(o[12]), "+r"(o[13]), "+r"(o[14]), "+r"(o[15])
+                           :
+                           : "memory");
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(to + 16 * i, o);
+            }
+          }
+        }
+        const float neg = m == -INFINITY ? 0.0f : -m * sl2;
+        weigh(0, neg);
+        hand_over(0);
+        weigh(1, neg);
+        hand_over(1);
       }
       // ---- the row's result
-      if (n > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(P::B_O + t), (done - 1) & 1, abort_flag))) {
-          fail();
-          return false;
-        }
+            if (n > 0) {
+        if (!(ok = wait_warp(bar(P::B_O + t), uint32_t(mine_pieces++ & 1), abort_flag))) return false;
         tc_fence_after();
       }
       const bool none = l == 0.0f;
@@ -487,44 +626,76 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           a.lse[tg * a.Hq + qh] = lse;
         }
       }
-      float *op = a.o_part ? a.o_part + ((tg * a.Hq + qh) * a.slots + p.slot) * a.dv : nullptr;
-      uint16_t *o16 = a.out + tg * a.o_token + qh * a.o_head;
+      // Rows leave through this warp's quarter of its query tile (all products
+      // with it are done), so that a store covers whole rows: 16-byte pieces,
+      // swizzled, NC a row.  16-bit results go in one pass, float parts in two.
+      constexpr int NC = D / 8, RPI = 32 / NC;  // pieces of a staged row; rows a store covers
+      uint8_t *stage = sm + P::OFF_Q + t * P::QB + (warp & 3) * 32 * (D * 2);
+      const int64_t off = a.o_part ? ((tg * a.Hq + qh) * a.slots + p.slot) * a.dv
+                                   : tg * a.o_token + qh * a.o_head;
+      const uint32_t live = __ballot_sync(0xffffffffu, mine && !(a.o_part && none));
 #pragma unroll 1
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(to + 32 * i, o);
-          tmem_wait_ld();
-        }
+      for (int pass = 0; pass < (a.o_part ? 2 : 1); ++pass) {
+        const int cols = a.o_part ? D / 2 : D;  // columns of this pass
+#pragma unroll 1
+        for (int i = 0; i < cols / 32; ++i) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(to + pass * (D / 2) + 32 * i, o);
+            wait_ld32(o);
+          }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
-        if (!mine) continue;
+          for (int e = 0; e < 32; ++e) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+          if (a.o_part) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          if (32 * i + e >= a.dv) continue;
-          if (op) {
-            if (none) continue;  // the join skips an empty part
-            *reinterpret_cast<uint4 *>(op + 32 * i + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            *reinterpret_cast<uint4 *>(op + 32 * i + e + 4) =
-                make_uint4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4 *>(stage + (lane * NC + ((8 * i + e) ^ (lane & (NC - 1)))) * 16) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           } else {
-            uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack2<DT>(__uint_as_float(o[e + 2 * k]), __uint_as_float(o[e + 2 * k + 1]));
-            uint32_t *d = reinterpret_cast<uint32_t *>(o16 + 32 * i + e);
-            if (c.out16) {
-              *reinterpret_cast<uint4 *>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) d[k] = w[k];
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack2<DT>(__uint_as_float(o[8 * e + 2 * k]), __uint_as_float(o[8 * e + 2 * k + 1]));
+              *reinterpret_cast<uint4 *>(stage + (lane * NC + ((4 * i + e) ^ (lane & (NC - 1)))) * 16) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
+        __syncwarp();
+        const int ch = lane % NC;
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += RPI) {
+          const int r = r0 + lane / NC;
+          const int64_t at = __shfl_sync(0xffffffffu, off, r);
+          if (!((live >> r) & 1u)) continue;
+          const uint4 x = *reinterpret_cast<const uint4 *>(stage + (r * NC + (ch ^ (r & (NC - 1)))) * 16);
+          if (a.o_part) {
+            const int d = pass * (D / 2) + ch * 4;
+            if (d < a.dv) *reinterpret_cast<uint4 *>(a.o_part + at + d) = x;
+          } else if (ch * 8 < a.dv) {
+            uint32_t *d = reinterpret_cast<uint32_t *>(a.out + at + ch * 8);
+            if (c.out16) {
+              *reinterpret_cast<uint4 *>(d) = x;
+            } else {
+              d[0] = x.x;
+              d[1] = x.y;
+              d[2] = x.z;
+              d[3] = x.w;
+            }
+          }
+        }
+        __syncwarp();
       }
+      release();
       tc_fence_before();  // O is read before the next piece's first product (through B_P)
       return true;
     });
+  }
+    if (!ok) {
+    *abort_flag = 1;
+    set_status(a.status, WQ_ERR_TIMEOUT);
   }
   __syncthreads();
   if (warp == WARP_MMA) tmem_dealloc(tmem, 512);
@@ -562,13 +733,18 @@ int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st) {
   Cut c{};
   c.tpt = BM / a.G;
   c.box = gcd(a.page_size, BN);
+  c.step_pages = BN / a.page_size;
+  c.step_place = BN % a.page_size;
   c.out16 = a.o_token % 8 == 0 && a.o_head % 8 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
   int64_t blocks = 0;
   if (a.tc_prefix) {
     c.pairs_p = (a.T + 2 * c.tpt - 1) / (2 * c.tpt);
     c.units_p = (a.P + BN - 1) / BN;
-    c.blocks_p = a.p_blocks;
-    blocks = c.blocks_p;
+        c.gang = a.p_gang;
+    c.gangs = a.p_gangs;
+    c.groups = (c.pairs_p + c.gang - 1) / c.gang;
+    c.stretch = a.p_stretch;
+    blocks = int64_t(c.gang) * c.gangs;
   }
   if (a.tc_suffix) {
     c.pairs_s = (a.max_q + 2 * c.tpt - 1) / (2 * c.tpt);
@@ -582,27 +758,30 @@ int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st) {
   return wide ? launch_one<F16, 128>(a, c, blocks, st) : launch_one<F16, 64>(a, c, blocks, st);
 }
 
-// Blocks that share the prefix's units, and the most blocks that meet in one
-// item (its partial results)
-void plan_prefix_tiles(AttnArgs &a) {
+// Gangs of the prefix, and the most of them that meet in one item (its partial
+// results).  The gang size is the one that leaves the fewest of the 152 SMs
+// without rows; whole items per gang where their waves are full to nine
+// tenths, else equal pieces of at least two units.
+bool plan_prefix_tiles(AttnArgs &a) {
   const int tpt = BM / a.G;
-  const int64_t items = int64_t(a.Hkv) * ((a.T + 2 * tpt - 1) / (2 * tpt));
-  const int64_t units = (a.P + BN - 1) / BN, total = items * units;
-  const int64_t sms = 152;
-  // whole items where their waves are full to nine tenths, else equal pieces
-  // of at least two units
-  const int64_t waves = (items + sms - 1) / sms;
-  int64_t blocks = items;
-  if (items * 10 < waves * sms * 9) blocks = std::max<int64_t>(std::min(sms, total / 2), 1);
-  a.p_blocks = int(blocks);
-  a.sp = 1;
-  if (blocks != items) {
-    a.sp = 0;
-    for (int64_t i = 0; i < items; ++i) {  // fewer than 152 * waves of them
-      const int64_t f = ((i * units + 1) * blocks - 1) / total, l = ((i + 1) * units * blocks - 1) / total;
-      a.sp = std::max(a.sp, int(l - f + 1));
-    }
+  const int64_t sms = 152, pairs = (a.T + 2 * tpt - 1) / (2 * tpt), units = (a.P + BN - 1) / BN;
+  double best = 0.0;
+  for (int64_t g = std::min<int64_t>(pairs, 19); g >= 1; --g) {
+    const int64_t groups = (pairs + g - 1) / g;
+    const double use = double(sms / g * g) / double(sms) * double(pairs) / double(groups * g);
+    if (use > best + 0.02) best = use, a.p_gang = int(g);
   }
+  const int64_t items = (pairs + a.p_gang - 1) / a.p_gang * a.Hkv, total = items * units;
+  if (total >= (int64_t(1) << 31)) return false;
+  const int64_t most = sms / a.p_gang, waves = (items + most - 1) / most;
+  int64_t stretch = units;
+  if (items * 10 < waves * most * 9) stretch = std::max<int64_t>((total + most - 1) / most, 2);
+  a.p_stretch = int(stretch);
+  a.p_gangs = int((total + stretch - 1) / stretch);
+  a.sp = 1;
+  for (int64_t i = 0; stretch != units && i < items; ++i)  // fewer than 152 * waves of them
+    a.sp = std::max(a.sp, int(((i + 1) * units - 1) / stretch - i * units / stretch + 1));
+  return true;
 }
 
 }  // namespace wq

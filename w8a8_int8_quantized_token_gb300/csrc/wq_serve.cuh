@@ -123,13 +123,13 @@ struct AttnArgs {
   int sp, p_chunk;  // prefix: splits and keys of each (0: no prefix)
   int ss, s_chunk;  // suffixes: splits and keys of each
   bool tc_prefix, tc_suffix;  // taken by the tensor-memory kernel
-  int p_blocks;     // its blocks on the prefix
+  int p_gang, p_gangs, p_stretch;  // its blocks on the prefix: gangs of p_gang, units of a gang
   int slots;        // sp + ss partial results a row
   float *o_part;    // [T][Hq][slots][dv], nullptr when slots == 1
   float *lse_part;  // [T][Hq][slots]
 };
 void plan_attention(AttnArgs &a);
-void plan_prefix_tiles(AttnArgs &a);
+bool plan_prefix_tiles(AttnArgs &a);
 int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st);
 size_t attention_ws_bytes(const AttnArgs &a);
 int launch_attention(const AttnArgs &a, int dtype, cudaStream_t st);
