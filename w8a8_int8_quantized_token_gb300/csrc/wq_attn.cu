@@ -8,11 +8,13 @@
 // result and its log-sum-exp, and a last kernel joins a row's partials:
 //   m = max_s lse_s,  out = sum_s exp(lse_s - m) o_s / sum_s exp(lse_s - m).
 //
-// Few rows are bound by the reading of keys and values.  The four warps of a
-// block take 16-key pieces of the range in turn; each keeps its own running
-// maximum, sum and output (the softmax of its keys) in registers and its own
-// ring of asynchronous copies, so warps never wait for one another until the
-// range ends.  Warp matrix products (16 x 8 x 16) do the arithmetic: with 16
+// Few rows are bound by the reading of keys and values.  A warp takes 16-key
+// pieces of a range; it keeps its own running maximum, sum and output (the
+// softmax of its keys) in registers and its own ring of asynchronous copies,
+// so warps never wait for one another inside a range.  With many (sequence,
+// key head) pairs a block is one warp and nine blocks share an SM: their
+// starts and ends overlap.  With few, four warps take a range's pieces in turn
+// and add up their results at its end.  Warp matrix products (16 x 8 x 16) do the arithmetic: with 16
 // rows they need 1/5 of their rate to keep up with HBM, and unlike the tensor
 // memory path they need no 128-row tile.
 #include <algorithm>
@@ -26,7 +28,7 @@ namespace {
 using namespace attn;
 
 constexpr int KT = 16;   // keys of a piece
-constexpr int NW = 4;    // warps of a block
+
 constexpr int NST = 3;   // pieces a warp has in flight
 
 __device__ __forceinline__ float ex2(float x) {
@@ -74,23 +76,24 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // D: padded head size (64 or 128), MT: 16-row tiles
-template <class DT, int D, int MT>
+template <class DT, int D, int MT, int NW>
 struct Small {
   static constexpr int CH = D / 8;                 // 16-byte pieces of a row
   static constexpr int KB = KT * D * 2;            // bytes of 16 keys (or values)
   static constexpr int STAGE = 2 * KB;
   static constexpr int RING = NW * NST * STAGE;
-  static constexpr int JOIN = NW * MT * 16 * (D + 4) * 4;  // per-warp results, row pitch D + 4
+  static constexpr int JOIN = NW == 1 ? 0 : NW * MT * 16 * (D + 4) * 4;  // per-warp results, row pitch D + 4
   static constexpr int SMEM = RING > JOIN ? RING : JOIN;
 };
 
-template <class DT, int D, int MT>
+template <class DT, int D, int MT, int NW>
 __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, int prefix_items,
                                                              int prefix_tiles, int suffix_tiles) {
-  using P = Small<DT, D, MT>;
+  using P = Small<DT, D, MT, NW>;
   constexpr int CH = P::CH, R = 16 * MT;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = NW == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  start_next_kernel();
 
   // ---- the work item: (range, sequence, key head, row tile), row tile innermost
   int64_t it = blockIdx.x;
@@ -113,7 +116,10 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
   }
   const Source s = source_of(a, seq);
   const int rows = min(R, s.n * a.G - tile * R);  // rows of this tile
-  if (rows <= 0) return;
+  if (rows <= 0) {
+    wait_last_kernel();
+    return;
+  }
   const int row0 = tile * R;
   const int k0 = split * chunk;
   // keys that the tile's last token sees, and this range's end
@@ -306,7 +312,41 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
     __syncwarp();  // all lanes have read the slot before it is refilled
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();  // the ring becomes the exchange of the four warps' results
+  if constexpr (NW == 1) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = m * 16 + h * 8 + lane / 4;
+        float l = l_[m][h];  // this thread's keys only, so far
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (r >= rows) continue;
+        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
+        const int j = (row0 + r) / a.G, g = (row0 + r) - j * a.G;
+        const int64_t t = s.t0 + j, qh = head * a.G + g;
+        if ((lane & 3) == 0) {
+          const float lse = l == 0.0f ? -INFINITY : (m_[m][h] + log2f(l)) * 0.6931471805599453f;
+          if (a.o_part) a.lse_part[(t * a.Hq + qh) * a.slots + slot] = lse;
+          else if (a.lse) a.lse[t * a.Hq + qh] = lse;
+        }
+        if (a.o_part && l == 0.0f) continue;  // the join skips an empty part
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          const int d = n * 8 + (lane & 3) * 2;
+          if (d >= a.dv) continue;
+          const float x = o[m][n][h * 2] * inv, y = o[m][n][h * 2 + 1] * inv;
+          if (a.o_part)
+            *reinterpret_cast<float2 *>(a.o_part + ((t * a.Hq + qh) * a.slots + slot) * a.dv + d) =
+                make_float2(x, y);
+          else
+            *reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head + d) = pack2<DT>(x, y);
+        }
+      }
+    wait_last_kernel();  // the join waits for this kernel alone
+    return;
+  }
+  __syncthreads();  // the ring becomes the exchange of the warps' results
 
   constexpr int PITCH = D + 4;
   float *xo = reinterpret_cast<float *>(smem);
@@ -369,50 +409,63 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
       else if (a.lse) a.lse[t * a.Hq + qh] = lse;
     }
   }
+  wait_last_kernel();
 }
 
-// A warp joins one row's partial results
+// A warp joins one row's partial results, 32 at a time: a lane finds one
+// part's weight, and four parts' rows are in flight together.
 template <class DT>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  wait_last_kernel();
   if (row >= int64_t(a.T) * a.Hq) return;
   const float *lp = a.lse_part + row * a.slots;
+  const int d = min(lane * 4, a.dv - 4);
+  const float *op = a.o_part + row * a.slots * a.dv + d;
   float mx = -INFINITY;
   for (int s = lane; s < a.slots; s += 32) mx = fmaxf(mx, lp[s]);
   mx = warp_max(mx);
   const int64_t t = row / a.Hq, qh = row - t * a.Hq;
   const float base = mx == -INFINITY ? 0.0f : mx;
   float sum = 0.0f, x[4] = {};
-  const int d = lane * 4;
-  for (int s = 0; s < a.slots; ++s) {
-    const float w = __expf(lp[s] - base);
-    if (w == 0.0f) continue;  // an empty part holds nothing
-    sum += w;
-    if (d < a.dv) {
-      const float4 v = *reinterpret_cast<const float4 *>(a.o_part + (row * a.slots + s) * a.dv + d);
-      x[0] = __fmaf_rn(v.x, w, x[0]);
-      x[1] = __fmaf_rn(v.y, w, x[1]);
-      x[2] = __fmaf_rn(v.z, w, x[2]);
-      x[3] = __fmaf_rn(v.w, w, x[3]);
+  for (int s0 = 0; s0 < a.slots; s0 += 32) {
+    const float mine = s0 + lane < a.slots ? __expf(lp[s0 + lane] - base) : 0.0f;
+    sum += warp_sum(mine);
+    const int n = min(32, a.slots - s0);
+    for (int i = 0; i < n; i += 4) {
+      float w[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w[k] = __shfl_sync(0xffffffffu, mine, (i + k) & 31);
+        if (i + k >= n) w[k] = 0.0f;
+        // an empty part (weight zero) holds nothing that may be read
+        v[k] = w[k] != 0.0f ? *reinterpret_cast<const float4 *>(op + int64_t(s0 + i + k) * a.dv)
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[0] = __fmaf_rn(v[k].x, w[k], x[0]);
+        x[1] = __fmaf_rn(v[k].y, w[k], x[1]);
+        x[2] = __fmaf_rn(v[k].z, w[k], x[2]);
+        x[3] = __fmaf_rn(v[k].w, w[k], x[3]);
+      }
     }
   }
   const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
-  if (d < a.dv) {
-    uint2 p;
-    p.x = pack2<DT>(x[0] * inv, x[1] * inv);
-    p.y = pack2<DT>(x[2] * inv, x[3] * inv);
+  if (lane * 4 < a.dv) {
     uint32_t *o = reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head + d);
-    o[0] = p.x;
-    o[1] = p.y;
+    o[0] = pack2<DT>(x[0] * inv, x[1] * inv);
+    o[1] = pack2<DT>(x[2] * inv, x[3] * inv);
   }
   if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : base + logf(sum);
 }
 
-template <class DT, int D, int MT>
+template <class DT, int D, int MT, int NW>
 int launch_small(const AttnArgs &a, cudaStream_t st) {
-  using P = Small<DT, D, MT>;
-  auto *k = attn_small_kernel<DT, D, MT>;
+  using P = Small<DT, D, MT, NW>;
+  auto *k = attn_small_kernel<DT, D, MT, NW>;
   static bool sized = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            P::SMEM) == cudaSuccess;
   if (!sized) return WQ_ERR_LAUNCH;
@@ -422,8 +475,13 @@ int launch_small(const AttnArgs &a, cudaStream_t st) {
   const int64_t si = a.tc_suffix ? 0 : a.ss * stl * a.Hkv * a.B;
   if (pi + si == 0) return WQ_OK;
   if (pi + si >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
-  k<<<unsigned(pi + si), NW * 32, P::SMEM, st>>>(a, int(pi), int(pt), int(stl));
-  return launched(1);
+  return launch_chained(k, unsigned(pi + si), NW * 32, P::SMEM, a.tc_prefix || a.tc_suffix, st, a,
+                        int(pi), int(pt), int(stl));
+}
+
+template <class DT, int D, int MT>
+int launch_warps(const AttnArgs &a, cudaStream_t st) {
+  return a.one_warp ? launch_small<DT, D, MT, 1>(a, st) : launch_small<DT, D, MT, 4>(a, st);
 }
 
 template <class DT>
@@ -431,28 +489,17 @@ int launch_t(const AttnArgs &a, cudaStream_t st) {
   const bool wide = a.dk > 64 || a.dv > 64, two = int64_t(a.max_q) * a.G > 16;
   int rc = launch_attention_tiles(a, std::is_same<DT, Bf16>::value ? WQ_DT_BF16 : WQ_DT_F16, st);
   if (rc != WQ_OK) return rc;
-  if (wide) rc = two ? launch_small<DT, 128, 2>(a, st) : launch_small<DT, 128, 1>(a, st);
-  else rc = two ? launch_small<DT, 64, 2>(a, st) : launch_small<DT, 64, 1>(a, st);
+  if (wide) rc = two ? launch_warps<DT, 128, 2>(a, st) : launch_warps<DT, 128, 1>(a, st);
+  else rc = two ? launch_warps<DT, 64, 2>(a, st) : launch_warps<DT, 64, 1>(a, st);
   if (rc != WQ_OK || !a.o_part) return rc;
   const int64_t rows = int64_t(a.T) * a.Hq;
-  attn_join_kernel<DT><<<unsigned((rows + 3) / 4), 128, 0, st>>>(a);
-  return launched(1);
+  return launch_chained(attn_join_kernel<DT>, unsigned((rows + 3) / 4), 128, 0, true, st, a);
 }
 
 }  // namespace
 
-// Cuts the key ranges: enough items to fill the 2 x 152 resident blocks a few
-// times, ranges of at least 256 keys, whole 64-key rounds of the four warps.
+// Which kernel takes which part, and the cuts of the key ranges.
 void plan_attention(AttnArgs &a) {
-  auto cut = [](int64_t items, int64_t keys, int &splits, int &chunk) {
-    splits = chunk = 0;
-    if (keys <= 0 || items <= 0) return;
-    int64_t n = (4 * 304 + items - 1) / items;
-    n = std::min(n, (keys + 255) / 256);
-    n = std::max<int64_t>(std::min<int64_t>(n, 64), 1);
-    chunk = int(((keys + n - 1) / n + 63) / 64 * 64);
-    splits = int((keys + chunk - 1) / chunk);
-  };
   // The tensor-memory kernel takes 128-row tiles and loads pages by TMA in
   // boxes of 8 rows or more with pitches that differ from zero.
   const bool pitches = (a.k_token || a.page_size == 1) && (a.k_head || a.Hkv == 1) &&
@@ -460,16 +507,30 @@ void plan_attention(AttnArgs &a) {
                        (a.v_head || a.Hkv == 1) && (a.v_page || a.num_pages <= 1);
   const bool tiles = a.page_size % 8 == 0 && a.num_pages > 0 && pitches;
   const int64_t rows_p = int64_t(a.T) * a.G, rows_s = int64_t(a.max_q) * a.G;
-  a.tc_prefix = tiles && a.P > 0 && rows_p > 32;
+  a.tc_prefix = tiles && a.P > 0 && rows_p > 32 && plan_prefix_tiles(a);
   a.tc_suffix = tiles && a.max_suffix > 0 && rows_s > 32;
   const int64_t R = rows_s > 16 ? 32 : 16;
-  a.tc_prefix = a.tc_prefix && plan_prefix_tiles(a);
-  if (!a.tc_prefix) cut((rows_p + R - 1) / R * a.Hkv, a.P, a.sp, a.p_chunk);
-  const int64_t sr = a.tc_suffix ? 2 * (128 / a.G) * a.G : R;
-  cut((rows_s + sr - 1) / sr * a.Hkv * a.B * (a.tc_suffix ? 8 : 1), a.max_suffix, a.ss, a.s_chunk);
-  if (a.tc_suffix && a.s_chunk % 128) a.s_chunk += 64;
+  const int64_t items_s = (rows_s + R - 1) / R * a.Hkv * a.B;
+  a.one_warp = items_s >= 4 * 152;
+  // ranges of `grain` keys or multiples, at least `least`, about `want` items
+  auto cut = [](int64_t items, int64_t keys, int64_t want, int64_t least, int64_t grain, int &splits,
+                int &chunk) {
+    if (keys <= 0 || items <= 0) return;
+    const int64_t n = std::max<int64_t>(
+        std::min({(want + items - 1) / items, (keys + least - 1) / least, int64_t(64)}), 1);
+    chunk = int(((keys + n - 1) / n + grain - 1) / grain * grain);
+    splits = int((keys + chunk - 1) / chunk);
+  };
+  const int64_t want = a.one_warp ? 2 * 9 * 152 : 4 * 2 * 152, least = a.one_warp ? 128 : 256;
+  const int64_t grain = a.one_warp ? 16 : 64;
+  if (!a.tc_prefix) cut((rows_p + R - 1) / R * a.Hkv, a.P, want, least, grain, a.sp, a.p_chunk);
+  if (a.tc_suffix) {
+    const int64_t pair = 2 * (128 / a.G);
+    cut((a.max_q + pair - 1) / pair * a.Hkv * a.B, a.max_suffix, 152, 256, 128, a.ss, a.s_chunk);
+  } else {
+    cut(items_s, a.max_suffix, want, least, grain, a.ss, a.s_chunk);
+  }
   if (a.sp + a.ss == 0) a.ss = 1;  // no keys at all: one empty range writes the zeros
-  if (a.ss && a.s_chunk) a.ss = (a.max_suffix + a.s_chunk - 1) / a.s_chunk;
   a.slots = a.sp + a.ss;
 }
 

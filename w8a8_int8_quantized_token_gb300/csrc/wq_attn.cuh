@@ -39,5 +39,34 @@ __device__ __forceinline__ int visible(const Source &s, int j) {
   return s.causal ? s.len - s.n + j + 1 : s.len;
 }
 
+// The kernels of one call follow each other closely: each lets the next one's
+// blocks take the room that its own leave (start_next_kernel, in every block),
+// and none ends before the one before it has (wait_last_kernel), so that the
+// last one may read what all of them wrote.  The first is launched in plain
+// stream order, after everything that came before the call.
+__device__ __forceinline__ void start_next_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_last_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <class... Args>
+int launch_chained(void (*k)(Args...), unsigned grid, int threads, int smem, bool chained,
+                   cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, k, args...) != cudaSuccess) return WQ_ERR_LAUNCH;
+  return launched(1);
+}
+
 }  // namespace attn
 }  // namespace wq

@@ -111,6 +111,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                             int z, uint32_t bar) {
   asm volatile(
@@ -255,7 +258,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   auto bar = [&](int i) { return base + P::OFF_BAR + 8u * uint32_t(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  attn::start_next_kernel();
   if (threadIdx.x == 0) {
+    prefetch_map(&tmQ);
+    prefetch_map(&tmK);
+    prefetch_map(&tmV);
     *abort_flag = 0;
         for (int i = 0; i < P::NBAR; ++i)
       mbar_init(bar(i), i == P::B_Q_EMPTY ? 8                      // softmax warps
@@ -665,7 +672,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         __syncwarp();
         const int ch = lane % NC;
-#pragma unroll 4
+#pragma unroll
         for (int r0 = 0; r0 < 32; r0 += RPI) {
           const int r = r0 + lane / NC;
           const int64_t at = __shfl_sync(0xffffffffu, off, r);
