@@ -86,7 +86,7 @@ struct Small {
   static constexpr int SMEM = RING > JOIN ? RING : JOIN;
 };
 
-template <class DT, int D, int MT, int NW>
+template <class DT, int D, int MT, int NW, bool PAGED>
 __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, int prefix_items,
                                                              int prefix_tiles, int suffix_tiles) {
   using P = Small<DT, D, MT, NW>;
@@ -163,41 +163,63 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
                         uint32_t(warp * NST * P::STAGE);
   const int pieces = k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0;
   const int mine = pieces > warp ? (pieces - warp + NW - 1) / NW : 0;
-  const uint16_t *kh = a.k + int64_t(head) * a.k_head;
-  const uint16_t *vh = a.v + int64_t(head) * a.v_head;
 
-  // page and place of the key that lane (mod 16) looks up for piece i; a key
-  // past the range or on a bad page has page -1
-  auto look = [&](int i, int &page, int &place) {
-    const int key = k0 + (warp + i * NW) * KT + (lane & 15);
-    page = -1;
-    place = 0;
-    if (i < mine && key < k1) {
-      const int pi = key / a.page_size;
-      place = key - pi * a.page_size;
-      page = s.pages[pi];
-      if (page < 0 || page >= a.num_pages) {
-        set_status(a.status, WQ_ERR_INDEX);
-        page = -1;
-      }
-    }
-  };
-  // bit r of `on`: key r of the piece is there
-  auto issue = [&](int i, int page, int place) -> uint32_t {
-    const uint32_t on = __ballot_sync(0xffffffffu, page >= 0) & 0xffffu;
+  // The piece that is asked for next: its page is looked up one piece ahead of
+  // its copies.  PAGED: pages hold whole pieces, so that a piece has one page
+  // and its keys one pitch; else lane (mod 16) r looks up key r.
+  const int own = PAGED ? 0 : lane & 15;
+  int key = k0 + warp * KT + own;
+  int pi = key / a.page_size, place = key - pi * a.page_size;
+  int page = mine > 0 && key < k1 ? s.pages[pi] : 0;
+  bool bad = false;
+  const int lr = lane / CH, lc = lane % CH;  // this lane's row and 16-byte column of a copy
+  const uint16_t *kh = a.k + int64_t(head) * a.k_head + (lc * 8 < a.dk ? lc * 8 : 0);
+  const uint16_t *vh = a.v + int64_t(head) * a.v_head + (lc * 8 < a.dv ? lc * 8 : 0);
+  if constexpr (PAGED) {
+    kh += lr * a.k_token;
+    vh += lr * a.v_token;
+  }
+  const uint32_t ldst = ring + uint32_t(lr * CH + (lc ^ lr)) * 16;
+  // starts the copies of piece i; returns bit r for key r that is there
+  auto issue = [&](int i) -> uint32_t {
+    uint32_t on = 0;
     if (i < mine) {
-      const uint32_t st = ring + uint32_t((i % NST) * P::STAGE);
-#pragma unroll
-      for (int j = 0; j < KT * CH / 32; ++j) {
-        const int c = j * 32 + lane, r = c / CH, ch = c % CH;
-        const int pg = __shfl_sync(0xffffffffu, page, r), pl = __shfl_sync(0xffffffffu, place, r);
-        const bool ok = pg >= 0;
-        const uint32_t d = st + uint32_t(r * CH + (ch ^ (r & 7))) * 16;
-        const int64_t p64 = ok ? pg : 0;
-        const bool kk = ok && ch * 8 < a.dk, vv = ok && ch * 8 < a.dv;
-        cp16(d, kh + p64 * a.k_page + int64_t(pl) * a.k_token + (kk ? ch * 8 : 0), kk);
-        cp16(d + P::KB, vh + p64 * a.v_page + int64_t(pl) * a.v_token + (vv ? ch * 8 : 0), vv);
+      constexpr int RPC = 32 / CH;  // rows of a copy
+      bool there = key < k1;
+      if (there && unsigned(page) >= unsigned(a.num_pages)) {
+        there = false;
+        bad = true;
       }
+      const int64_t pg = there ? page : 0;
+      const uint32_t d = ldst + uint32_t((i % NST) * P::STAGE);
+      if constexpr (PAGED) {
+        const int n = there ? min(KT, k1 - key) : 0;
+        on = (1u << n) - 1;
+        const uint16_t *kp = kh + pg * a.k_page + int64_t(place) * a.k_token;
+        const uint16_t *vp = vh + pg * a.v_page + int64_t(place) * a.v_token;
+#pragma unroll
+        for (int j = 0; j < KT / RPC; ++j) {
+          const uint32_t dj = (d ^ uint32_t((j * RPC & 7) << 4)) + uint32_t(j * RPC * CH * 16);
+          cp16(dj, kp + int64_t(j * RPC) * a.k_token, j * RPC + lr < n && lc * 8 < a.dk);
+          cp16(dj + P::KB, vp + int64_t(j * RPC) * a.v_token, j * RPC + lr < n && lc * 8 < a.dv);
+        }
+      } else {
+        on = __ballot_sync(0xffffffffu, there) & 0xffffu;
+        const int64_t ko = pg * a.k_page + int64_t(place) * a.k_token;
+        const int64_t vo = pg * a.v_page + int64_t(place) * a.v_token;
+#pragma unroll
+        for (int j = 0; j < KT / RPC; ++j) {
+          const int r = j * RPC + lr;
+          const uint32_t dj = (d ^ uint32_t((j * RPC & 7) << 4)) + uint32_t(j * RPC * CH * 16);
+          cp16(dj, kh + __shfl_sync(0xffffffffu, ko, r), (on >> r & 1u) && lc * 8 < a.dk);
+          cp16(dj + P::KB, vh + __shfl_sync(0xffffffffu, vo, r), (on >> r & 1u) && lc * 8 < a.dv);
+        }
+      }
+      key += NW * KT;
+      pi += a.step_pages;
+      place += a.step_place;
+      if (place >= a.page_size) place -= a.page_size, ++pi;
+      if (key < k1) page = s.pages[pi];
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     return on;
@@ -213,104 +235,117 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[m][n][e] = 0.0f;
   }
-
-  uint32_t on[NST];
-  int page, place;
-  look(0, page, place);
+  int least = lim[0][0];  // every row of the warp sees the keys below
 #pragma unroll
-  for (int i = 0; i < NST - 1; ++i) {
-    on[i] = issue(i, page, place);
-    look(i + 1, page, place);
-  }
+  for (int m = 0; m < MT; ++m) least = min(least, min(lim[m][0], lim[m][1]));
+  least = __reduce_min_sync(0xffffffffu, least);
+
+  // ldmatrix addresses within a stage: keys for the scores, values transposed
+  const int rk = (lane & 7) + ((lane >> 4) & 1) * 8, rv = (lane & 7) + ((lane >> 3) & 1) * 8;
+  const uint32_t ak = uint32_t(rk * CH * 16 + ((((lane >> 3) & 1) ^ (rk & 7)) << 4));
+  const uint32_t av = uint32_t(P::KB + rv * CH * 16 + (((lane >> 4) ^ (rv & 7)) << 4));
+
+  uint32_t on[NST - 1];
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i) on[i] = issue(i);
   for (int i = 0; i < mine; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
     __syncwarp();  // every lane's copies of this piece are in; the slot of piece i - 1 is free
-    const uint32_t next_on = issue(i + NST - 1, page, place);
-    look(i + NST, page, place);
-    const uint32_t st = ring + uint32_t((i % NST) * P::STAGE);
     const uint32_t have = on[0];
 #pragma unroll
-    for (int k = 0; k + 1 < NST - 1; ++k) on[k] = on[k + 1];
-    on[NST - 2] = next_on;
+    for (int k = 0; k + 2 < NST; ++k) on[k] = on[k + 1];
+    on[NST - 2] = issue(i + NST - 1);
+    const uint32_t st = ring + uint32_t((i % NST) * P::STAGE);
 
     // scores: 16 keys as two 8-key columns
     float sc[MT][2][4] = {};
-    {
-      const int r = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int ch = k * 2 + ((lane >> 3) & 1);
-        uint32_t b[4];
-        ldsm4(b, st + uint32_t(r * CH + (ch ^ (r & 7))) * 16);
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t b[4];
+      ldsm4(b, (st + ak) ^ uint32_t(k << 5));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma<DT>(sc[m][0], qf[m][k], b[0], b[1]);
-          mma<DT>(sc[m][1], qf[m][k], b[2], b[3]);
-        }
+      for (int m = 0; m < MT; ++m) {
+        mma<DT>(sc[m][0], qf[m][k], b[0], b[1]);
+        mma<DT>(sc[m][1], qf[m][k], b[2], b[3]);
       }
     }
     const int key0 = k0 + (warp + i * NW) * KT;
+    if (key0 + KT > least || have != 0xffffu) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int c = n * 8 + (lane & 3) * 2 + (e & 1);
+            if (key0 + c >= lim[m][e >> 1] || !((have >> c) & 1u)) sc[m][n][e] = -INFINITY;
+          }
+    }
+    // The weights stay under the maximum in use until a row outgrows it by
+    // 2^8; then its sums are scaled and the new one is used.
+    float mx[MT][2];
+    bool grow = false;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = fmaxf(fmaxf(sc[m][0][h * 2], sc[m][0][h * 2 + 1]),
+                        fmaxf(sc[m][1][h * 2], sc[m][1][h * 2 + 1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        mx[m][h] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        grow = grow || (mx[m][h] > m_[m][h] && !((mx[m][h] - m_[m][h]) * a.scale_log2 <= 8.0f));
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float mn = fmaxf(m_[m][h], mx[m][h]);
+          const float f = m_[m][h] == -INFINITY ? 1.0f : ex2((m_[m][h] - mn) * a.scale_log2);
+          m_[m][h] = mn;
+          l_[m][h] *= f;
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n) {
+            o[m][n][h * 2] *= f;
+            o[m][n][h * 2 + 1] *= f;
+          }
+        }
+    }
     uint32_t pf[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int c = n * 8 + (lane & 3) * 2 + e;
-            float &x = sc[m][n][h * 2 + e];
-            x = (key0 + c < lim[m][h] && ((have >> c) & 1u)) ? __fmul_rn(x, a.scale_log2)
-                                                              : -INFINITY;
-            mx = fmaxf(mx, x);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m_[m][h], mx);
-        const float base = mn == -INFINITY ? 0.0f : mn;  // nothing seen yet: all weights 0
-        const float corr = ex2(m_[m][h] - base);
-        m_[m][h] = mn;
+        const float neg = m_[m][h] == -INFINITY ? 0.0f : -m_[m][h] * a.scale_log2;
         float sum = 0.0f;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float &x = sc[m][n][h * 2 + e];
-            x = ex2(x - base);
+            x = ex2(__fmaf_rn(x, a.scale_log2, neg));
             sum += x;
           }
-        l_[m][h] = __fmaf_rn(l_[m][h], corr, sum);
-        if (corr != 1.0f) {
-#pragma unroll
-          for (int n = 0; n < D / 8; ++n) {
-            o[m][n][h * 2] *= corr;
-            o[m][n][h * 2 + 1] *= corr;
-          }
-        }
+        l_[m][h] += sum;
       }
       pf[m][0] = pack2<DT>(sc[m][0][0], sc[m][0][1]);
       pf[m][1] = pack2<DT>(sc[m][0][2], sc[m][0][3]);
       pf[m][2] = pack2<DT>(sc[m][1][0], sc[m][1][1]);
       pf[m][3] = pack2<DT>(sc[m][1][2], sc[m][1][3]);
     }
-    {
-      const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
-        const int ch = n * 2 + (lane >> 4);
-        uint32_t b[4];
-        ldsm4t(b, st + P::KB + uint32_t(r * CH + (ch ^ (r & 7))) * 16);
+    for (int n = 0; n < D / 16; ++n) {
+      uint32_t b[4];
+      ldsm4t(b, (st + av) ^ uint32_t(n << 5));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma<DT>(o[m][2 * n], pf[m], b[0], b[1]);
-          mma<DT>(o[m][2 * n + 1], pf[m], b[2], b[3]);
-        }
+      for (int m = 0; m < MT; ++m) {
+        mma<DT>(o[m][2 * n], pf[m], b[0], b[1]);
+        mma<DT>(o[m][2 * n + 1], pf[m], b[2], b[3]);
       }
     }
     __syncwarp();  // all lanes have read the slot before it is refilled
   }
+  if (bad) set_status(a.status, WQ_ERR_INDEX);
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if constexpr (NW == 1) {
 #pragma unroll
@@ -326,7 +361,8 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
         const int j = (row0 + r) / a.G, g = (row0 + r) - j * a.G;
         const int64_t t = s.t0 + j, qh = head * a.G + g;
         if ((lane & 3) == 0) {
-          const float lse = l == 0.0f ? -INFINITY : (m_[m][h] + log2f(l)) * 0.6931471805599453f;
+          const float lse =
+              l == 0.0f ? -INFINITY : (m_[m][h] * a.scale_log2 + log2f(l)) * 0.6931471805599453f;
           if (a.o_part) a.lse_part[(t * a.Hq + qh) * a.slots + slot] = lse;
           else if (a.lse) a.lse[t * a.Hq + qh] = lse;
         }
@@ -360,7 +396,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if ((lane & 3) == 0) {
-        xm[warp][r] = m_[m][h];
+        xm[warp][r] = m_[m][h] == -INFINITY ? -INFINITY : m_[m][h] * a.scale_log2;
         xl[warp][r] = l;
       }
       float *w = xo + (warp * R + r) * PITCH + (lane & 3) * 2;
@@ -462,10 +498,10 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
   if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : base + logf(sum);
 }
 
-template <class DT, int D, int MT, int NW>
+template <class DT, int D, int MT, int NW, bool PAGED>
 int launch_small(const AttnArgs &a, cudaStream_t st) {
   using P = Small<DT, D, MT, NW>;
-  auto *k = attn_small_kernel<DT, D, MT, NW>;
+  auto *k = attn_small_kernel<DT, D, MT, NW, PAGED>;
   static bool sized = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            P::SMEM) == cudaSuccess;
   if (!sized) return WQ_ERR_LAUNCH;
@@ -481,7 +517,8 @@ int launch_small(const AttnArgs &a, cudaStream_t st) {
 
 template <class DT, int D, int MT>
 int launch_warps(const AttnArgs &a, cudaStream_t st) {
-  return a.one_warp ? launch_small<DT, D, MT, 1>(a, st) : launch_small<DT, D, MT, 4>(a, st);
+  if (a.page_size % KT) return launch_small<DT, D, MT, 4, false>(a, st);
+  return a.one_warp ? launch_small<DT, D, MT, 1, true>(a, st) : launch_small<DT, D, MT, 4, true>(a, st);
 }
 
 template <class DT>
@@ -511,7 +548,10 @@ void plan_attention(AttnArgs &a) {
   a.tc_suffix = tiles && a.max_suffix > 0 && rows_s > 32;
   const int64_t R = rows_s > 16 ? 32 : 16;
   const int64_t items_s = (rows_s + R - 1) / R * a.Hkv * a.B;
-  a.one_warp = items_s >= 4 * 152;
+  a.one_warp = a.page_size % KT == 0 && items_s >= 64 && a.max_suffix <= 4096;
+  const int step = KT * (a.one_warp ? 1 : 4);
+  a.step_pages = step / a.page_size;
+  a.step_place = step % a.page_size;
   // ranges of `grain` keys or multiples, at least `least`, about `want` items
   auto cut = [](int64_t items, int64_t keys, int64_t want, int64_t least, int64_t grain, int &splits,
                 int &chunk) {
@@ -521,7 +561,7 @@ void plan_attention(AttnArgs &a) {
     chunk = int(((keys + n - 1) / n + grain - 1) / grain * grain);
     splits = int((keys + chunk - 1) / chunk);
   };
-  const int64_t want = a.one_warp ? 2 * 9 * 152 : 4 * 2 * 152, least = a.one_warp ? 128 : 256;
+  const int64_t want = 1216, least = a.one_warp ? 128 : 256;
   const int64_t grain = a.one_warp ? 16 : 64;
   if (!a.tc_prefix) cut((rows_p + R - 1) / R * a.Hkv, a.P, want, least, grain, a.sp, a.p_chunk);
   if (a.tc_suffix) {
