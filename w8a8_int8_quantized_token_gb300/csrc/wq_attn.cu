@@ -548,7 +548,9 @@ void plan_attention(AttnArgs &a) {
   a.tc_suffix = tiles && a.max_suffix > 0 && rows_s > 32;
   const int64_t R = rows_s > 16 ? 32 : 16;
   const int64_t items_s = (rows_s + R - 1) / R * a.Hkv * a.B;
-  a.one_warp = a.page_size % KT == 0 && items_s >= 64 && a.max_suffix <= 4096;
+  // one warp a block where starts and ends weigh more than an even spread: many
+  // pairs, ranges that are not long, pieces of 8 KB (heads over 64)
+  a.one_warp = a.page_size % KT == 0 && items_s >= 64 && a.max_suffix <= 4096 && (a.dk > 64 || a.dv > 64);
   const int step = KT * (a.one_warp ? 1 : 4);
   a.step_pages = step / a.page_size;
   a.step_place = step % a.page_size;
@@ -561,7 +563,7 @@ void plan_attention(AttnArgs &a) {
     chunk = int(((keys + n - 1) / n + grain - 1) / grain * grain);
     splits = int((keys + chunk - 1) / chunk);
   };
-  const int64_t want = 1216, least = a.one_warp ? 128 : 256;
+  const int64_t want = a.max_suffix > 4096 ? 1824 : 1216, least = a.one_warp ? 128 : 256;
   const int64_t grain = a.one_warp ? 16 : 64;
   if (!a.tc_prefix) cut((rows_p + R - 1) / R * a.Hkv, a.P, want, least, grain, a.sp, a.p_chunk);
   if (a.tc_suffix) {

@@ -5,7 +5,11 @@
 // A row stays in registers from its one load to its stores: block, residual
 // and gate are read once, both outputs written once, and the two norms (the
 // second needs the whole of h) cost two or four block reductions in between.
-// Bound by HBM: 4 T H elements, 5 with a gate per token.
+// Bound by HBM: 4 T H elements, 5 with a gate per token.  Arithmetic goes in
+// packed float32 pairs: in single operations on 16-bit elements the kernel
+// was bound by its instructions (53 an element).
+#include <algorithm>
+
 #include "wq_serve.cuh"
 
 namespace wq {
@@ -23,171 +27,382 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
   return warp_sum(l < nw ? red[l] : 0.0f);
 }
 
-template <class DT, int VW, int NV, bool WARP>
+// The elements of a row that a thread holds: NV pieces of VW.  Where H and the
+// pitches are whole pieces, piece k begins at i0 + k * step.  Else (SHIFT) a
+// row begins some elements after a 16-byte boundary, the pieces are the
+// aligned ones around it, and the row's first and last piece are taken
+// element by element.
+template <class DT, int VW, int NV, bool WARP, bool SHIFT>
 struct Row {
+  using Raw = typename DT::Raw;
+  using V = Vec<DT, VW>;
+  using F = float[VW];
+  static constexpr int kPieces = NV;
   float v[NV][VW];
-  int i0, step, H;  // this thread's elements: i0 + k * step + [0, VW)
+  int i0, step, H;
 
-  __device__ __forceinline__ bool in(int k) const { return i0 + k * step < H; }
+  __device__ __forceinline__ int at(int k) const { return i0 + k * step; }
+  __device__ __forceinline__ bool in(int k) const {  // some of piece k
+    return SHIFT ? at(k) < H && at(k) + VW > 0 : at(k) < H;
+  }
+  __device__ __forceinline__ bool whole(int k) const { return at(k) >= 0 && at(k) + VW <= H; }
+  __device__ __forceinline__ bool has(int k, int e) const {
+    return SHIFT ? unsigned(at(k) + e) < unsigned(H) : in(k);
+  }
+  __device__ __forceinline__ V each(const Raw *p, int k) const {
+    if constexpr (VW == 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 2)
+        w[e / 2] = (has(k, e) ? uint32_t(p[at(k) + e]) : 0u) |
+                   (has(k, e + 1) ? uint32_t(p[at(k) + e + 1]) << 16 : 0u);
+      return {make_uint4(w[0], w[1], w[2], w[3])};
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = has(k, e) ? __float_as_uint(p[at(k) + e]) : 0u;
+      return {make_uint4(w[0], w[1], w[2], w[3])};
+    }
+  }
+  __device__ __forceinline__ V load(const Raw *p, int k) const {
+    if constexpr (!SHIFT) return V::load(p + at(k));
+    else return whole(k) ? V::load(p + at(k)) : each(p, k);
+  }
+  // a weight, a bias or a shared gate: its pieces lie shifted against the row's
+  __device__ __forceinline__ V load_weight(const Raw *p, int k) const {
+    if constexpr (!SHIFT) return V::load(p + at(k));
+    else return each(p, k);
+  }
+  __device__ __forceinline__ void store(Raw *p, int k) const {
+    if constexpr (!SHIFT) {
+      V x;
+      x.set(v[k]);
+      x.store(p + at(k));
+    } else if (whole(k)) {
+      V x;
+      x.set(v[k]);
+      x.store(p + at(k));
+    } else {
+#pragma unroll
+      for (int e = 0; e < VW; ++e)
+        if (has(k, e)) p[at(k) + e] = DT::from_f(v[k][e]);
+    }
+  }
+  __device__ __forceinline__ void clear_past(int k) {  // 0 outside the row
+#pragma unroll
+    for (int e = 0; e < VW; ++e)
+      if (!has(k, e)) v[k][e] = 0.0f;
+  }
+
+  // v = residual + scale * (gate * v) for piece k
+  __device__ __forceinline__ void add(int k, const V *gate, float scale, const V *residual) {
+    F r = {};
+    if (residual) residual->get(r);
+    if (gate) {
+      F g;
+      gate->get(g);
+      if constexpr (VW > 1) {
+#pragma unroll
+        for (int e = 0; e < VW; e += 2) mul2(v[k][e], v[k][e + 1], g[e], g[e + 1]);
+      } else {
+        v[k][0] *= g[0];
+      }
+    }
+    if constexpr (VW > 1) {
+#pragma unroll
+      for (int e = 0; e < VW; e += 2) fma2(v[k][e], v[k][e + 1], scale, scale, r[e], r[e + 1]);
+    } else {
+      v[k][0] = __fmaf_rn(v[k][0], scale, r[0]);
+    }
+  }
 
   // v = N(v)
   __device__ __forceinline__ void norm(int kind, const void *weight, const void *bias, float eps,
                                        float (*red)[32]) {
-    using V = Vec<DT, VW>;
-    const auto *w = static_cast<const typename DT::Raw *>(weight);
-    const auto *c = static_cast<const typename DT::Raw *>(bias);
     if (kind == WQ_NORM_NONE) return;
-    if (kind == WQ_NORM_LAYER) {
-      float s = 0.0f;
+    const bool layer = kind == WQ_NORM_LAYER;
+    const auto *w = static_cast<const Raw *>(weight);
+    const auto *c = static_cast<const Raw *>(layer ? bias : nullptr);
+    // weights are asked for ahead of the reductions where registers allow
+    constexpr bool kAhead = NV <= 4 && !SHIFT;
+    V wv[NV];
+    if (kAhead && w) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) s = __fadd_rn(s, v[k][e]);  // 0 past the row
-      const float m = __fdiv_rn(row_sum<WARP>(s, red[0]), float(H));
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < VW; ++e) v[k][e] = in(k) ? __fsub_rn(v[k][e], m) : 0.0f;
+        if (in(k)) wv[k] = load_weight(w, k);
     }
-    float s = 0.0f;
+    if (layer) {
+      float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+      for (int k = 0; k < NV; ++k) {  // 0 past the row
+        if constexpr (VW > 1) {
 #pragma unroll
-      for (int e = 0; e < VW; ++e) s = __fadd_rn(s, __fmul_rn(v[k][e], v[k][e]));
+          for (int e = 0; e < VW; e += 2) add2(s0, s1, v[k][e], v[k][e + 1]);
+        } else {
+          s0 += v[k][0];
+        }
+      }
+      const float m = -__fdiv_rn(row_sum<WARP>(s0 + s1, red[0]), float(H));
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if constexpr (VW > 1) {
+#pragma unroll
+          for (int e = 0; e < VW; e += 2) add2(v[k][e], v[k][e + 1], m, m);
+        } else {
+          v[k][0] += m;
+        }
+        clear_past(k);
+      }
+    }
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (VW > 1) {
+#pragma unroll
+        for (int e = 0; e < VW; e += 2) {
+          float x = v[k][e], y = v[k][e + 1];
+          fma2(x, y, x, y, s0, s1);
+          s0 = x;
+          s1 = y;
+        }
+      } else {
+        s0 = __fmaf_rn(v[k][0], v[k][0], s0);
+      }
+    }
     const float r = __fdiv_rn(
-        1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(row_sum<WARP>(s, red[1]), float(H)), eps)));
+        1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(row_sum<WARP>(s0 + s1, red[1]), float(H)), eps)));
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!in(k)) continue;
-      V wv, cv;
-      if (w) wv = V::load(w + i0 + k * step);
-      if (kind == WQ_NORM_LAYER && c) cv = V::load(c + i0 + k * step);
+      F wf, cf = {};
 #pragma unroll
-      for (int e = 0; e < VW; ++e) {
-        float x = __fmul_rn(v[k][e], r);
-        if (w) x = __fmul_rn(x, wv.f(e));
-        if (kind == WQ_NORM_LAYER && c) x = __fadd_rn(x, cv.f(e));
-        v[k][e] = x;
+      for (int e = 0; e < VW; ++e) wf[e] = 1.0f;
+      if (w) {
+        if (!kAhead) wv[k] = load_weight(w, k);
+        wv[k].get(wf);
       }
+      if (c) load_weight(c, k).get(cf);
+      if constexpr (VW > 1) {
+#pragma unroll
+        for (int e = 0; e < VW; e += 2) {
+          mul2(v[k][e], v[k][e + 1], r, r);
+          if (c) fma2(v[k][e], v[k][e + 1], wf[e], wf[e + 1], cf[e], cf[e + 1]);
+          else if (w) mul2(v[k][e], v[k][e + 1], wf[e], wf[e + 1]);
+        }
+      } else {
+        v[k][0] = __fmaf_rn(v[k][0] * r, wf[0], cf[0]);
+      }
+      if (SHIFT && c) clear_past(k);
     }
   }
 };
 
-// Threads of a block at most: with more than one piece a thread, half of what
-// a block may have, so that a thread may hold its pieces in 128 registers
-template <int NV, bool WARP>
-constexpr int max_threads() { return WARP ? 128 : (NV == 1 ? 1024 : 512); }
+// h is in the registers: x_out, N_pre and y
+template <class R>
+__device__ __forceinline__ void finish(const BlockNormArgs &a, int64_t t, R &row, float (*red)[32]) {
+  using Raw = typename R::Raw;
+  if (a.x_out) {
+#pragma unroll
+    for (int k = 0; k < R::kPieces; ++k)
+      if (row.in(k)) row.store(static_cast<Raw *>(a.x_out) + t * a.ldx, k);
+  }
+  if (!a.y) return;
+  row.norm(a.pre, a.w_pre, a.b_pre, a.eps, red);
+#pragma unroll
+  for (int k = 0; k < R::kPieces; ++k)
+    if (row.in(k)) row.store(static_cast<Raw *>(a.y) + t * a.ldy, k);
+}
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
 
-template <class DT, int VW, int NV, bool WARP>
-__global__ void __launch_bounds__(max_threads<NV, WARP>()) block_norm_kernel(const BlockNormArgs a) {
+// Threads of a block at most, and blocks that share an SM at least: the rows
+// in flight hide the reductions of each.
+template <int NV, bool WARP>
+constexpr int max_threads() { return WARP ? 128 : (NV == 1 ? 1024 : (NV <= 4 ? 256 : 544)); }
+template <int NV, bool WARP>
+constexpr int min_blocks() { return WARP ? 6 : (NV == 1 ? 1 : (NV <= 4 ? 3 : 1)); }
+
+template <class DT, int VW, int NV, bool WARP, bool SHIFT, bool GATE>
+__global__ void __launch_bounds__(max_threads<NV, WARP>(), min_blocks<NV, WARP>())
+    block_norm_kernel(const BlockNormArgs a) {
   using Raw = typename DT::Raw;
   using V = Vec<DT, VW>;
   __shared__ float red[4][32];
   const int64_t t = WARP ? int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   if (t >= a.T) return;  // a whole warp: no block barrier in the warp form
-  Row<DT, VW, NV, WARP> row;
+  const Raw *bp = static_cast<const Raw *>(a.block) + t * a.ldb;
+  const Raw *rp = static_cast<const Raw *>(a.residual) + t * a.ldr;
+  const Raw *gp = static_cast<const Raw *>(a.gate) + t * a.ldg;
+  Row<DT, VW, NV, WARP, SHIFT> row;
   row.H = a.H;
   row.i0 = (WARP ? threadIdx.x & 31 : threadIdx.x) * VW;
   row.step = (WARP ? 32 : blockDim.x) * VW;
-  const Raw *bp = static_cast<const Raw *>(a.block) + t * a.ldb + row.i0;
-  const Raw *rp = static_cast<const Raw *>(a.residual) + t * a.ldr + row.i0;
-  const Raw *gp = static_cast<const Raw *>(a.gate) + t * a.ldg + row.i0;
+  if (SHIFT) row.i0 -= int(reinterpret_cast<uintptr_t>(bp) / sizeof(Raw) % VW);
   // The residual and the gate are asked for together with the block, ahead of
   // the first norm, unless the row is too wide to keep them beside it.
   constexpr bool kEarly = NV * VW * sizeof(Raw) <= 64;
   V b[NV], r[NV], g[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k)
-    if (row.in(k)) b[k] = V::load(bp + k * row.step);
+    if (row.in(k)) b[k] = row.load(bp, k);
   if (kEarly && a.residual) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (row.in(k)) r[k] = V::load(rp + k * row.step);
+      if (row.in(k)) r[k] = row.load(rp, k);
   }
-  if (kEarly && a.gate) {
+  if (GATE && kEarly) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (row.in(k)) g[k] = V::load(gp + k * row.step);
+      if (row.in(k)) g[k] = SHIFT && a.ldg == 0 ? row.load_weight(gp, k) : row.load(gp, k);
   }
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
+  for (int k = 0; k < NV; ++k) {
 #pragma unroll
-    for (int e = 0; e < VW; ++e) row.v[k][e] = row.in(k) ? b[k].f(e) : 0.0f;
+    for (int e = 0; e < VW; ++e) row.v[k][e] = 0.0f;
+    if (row.in(k)) b[k].get(row.v[k]);
+  }
   row.norm(a.post, a.w_post, a.b_post, a.eps, red);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     if (!row.in(k)) continue;
     if (!kEarly) {
-      if (a.residual) r[k] = V::load(rp + k * row.step);
-      if (a.gate) g[k] = V::load(gp + k * row.step);
+      if (a.residual) r[k] = row.load(rp, k);
+      if (GATE) g[k] = SHIFT && a.ldg == 0 ? row.load_weight(gp, k) : row.load(gp, k);
     }
-#pragma unroll
-    for (int e = 0; e < VW; ++e) {
-      float x = row.v[k][e];
-      if (a.gate) x = __fmul_rn(g[k].f(e), x);
-      x = __fmul_rn(a.scale, x);
-      if (a.residual) x = __fadd_rn(r[k].f(e), x);
-      row.v[k][e] = x;
-    }
+    row.add(k, GATE ? &g[k] : nullptr, a.scale, a.residual ? &r[k] : nullptr);
   }
-  if (a.x_out) {
-    Raw *xp = static_cast<Raw *>(a.x_out) + t * a.ldx + row.i0;
+  finish(a, t, row, red + 2);
+}
+
+// Many rows: a block walks rows t, t + grid, ... and each thread copies its own
+// pieces of the row after the one at hand into shared memory while it works
+// on that, so that loads are always in flight and no thread waits for another
+// outside the reductions (a thread reads back only what it copied itself).
+template <class DT, int NV, bool GATE>
+__global__ void __launch_bounds__(256, 3) block_norm_stream_kernel(const BlockNormArgs a) {
+  using Raw = typename DT::Raw;
+  constexpr int VW = DT::kVec;
+  using V = Vec<DT, VW>;
+  __shared__ float red[2][4][32];  // by parity of the row
+  extern __shared__ __align__(16) uint8_t smem[];
+  Row<DT, VW, NV, false, false> row;
+  row.H = a.H;
+  row.i0 = threadIdx.x * VW;
+  row.step = blockDim.x * VW;
+  const int pitch = row.step * NV;  // staged elements of one array
+  constexpr int ARR = GATE ? 3 : 2;
+  auto piece = [&](int buf, int arr, int k) {
+    return reinterpret_cast<Raw *>(smem) + (buf * ARR + arr) * pitch + row.at(k);
+  };
+  auto fetch = [&](int64_t t, int buf) {
+    if (t < a.T) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (!row.in(k)) continue;
+        copy16(piece(buf, 0, k), static_cast<const Raw *>(a.block) + t * a.ldb + row.at(k));
+        if (a.residual)
+          copy16(piece(buf, 1, k), static_cast<const Raw *>(a.residual) + t * a.ldr + row.at(k));
+        if (GATE) copy16(piece(buf, ARR - 1, k), static_cast<const Raw *>(a.gate) + t * a.ldg + row.at(k));
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  fetch(blockIdx.x, 0);
+  int buf = 0;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
+    fetch(t + gridDim.x, buf ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (int e = 0; e < VW; ++e) row.v[k][e] = 0.0f;
+      if (row.in(k)) V::load(piece(buf, 0, k)).get(row.v[k]);
+    }
+    row.norm(a.post, a.w_post, a.b_post, a.eps, red[buf]);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if (!row.in(k)) continue;
-      V o;
-#pragma unroll
-      for (int e = 0; e < VW; ++e) o.set(e, row.v[k][e]);
-      o.store(xp + k * row.step);
+      V r, g;
+      if (a.residual) r = V::load(piece(buf, 1, k));
+      if (GATE) g = V::load(piece(buf, ARR - 1, k));
+      row.add(k, GATE ? &g : nullptr, a.scale, a.residual ? &r : nullptr);
     }
-  }
-  if (!a.y) return;
-  row.norm(a.pre, a.w_pre, a.b_pre, a.eps, red + 2);
-  Raw *yp = static_cast<Raw *>(a.y) + t * a.ldy + row.i0;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if (!row.in(k)) continue;
-    V o;
-#pragma unroll
-    for (int e = 0; e < VW; ++e) o.set(e, row.v[k][e]);
-    o.store(yp + k * row.step);
+    finish(a, t, row, red[buf] + 2);
   }
 }
 
-template <class DT, int VW, int NV, bool WARP>
+template <class DT, int VW, int NV, bool WARP, bool SHIFT>
 int launch_one(const BlockNormArgs &a, int threads, cudaStream_t st) {
   const int64_t blocks = WARP ? (a.T + threads / 32 - 1) / (threads / 32) : a.T;
-  block_norm_kernel<DT, VW, NV, WARP><<<unsigned(blocks), threads, 0, st>>>(a);
+  if (a.gate) block_norm_kernel<DT, VW, NV, WARP, SHIFT, true><<<unsigned(blocks), threads, 0, st>>>(a);
+  else block_norm_kernel<DT, VW, NV, WARP, SHIFT, false><<<unsigned(blocks), threads, 0, st>>>(a);
   return launched(1);
 }
 
 inline int threads_for(int pieces, int nv) { return ((pieces + nv - 1) / nv + 31) / 32 * 32; }
 
-template <class DT, int VW>
+template <class DT, int NV, bool GATE>
+int launch_stream_g(const BlockNormArgs &a, int pieces, cudaStream_t st) {
+  auto *k = block_norm_stream_kernel<DT, NV, GATE>;
+  static bool sized = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           2 * (GATE ? 3 : 2) * 256 * NV * 16) == cudaSuccess;
+  if (!sized) return WQ_ERR_LAUNCH;
+  const int threads = threads_for(pieces, NV), smem = 2 * (GATE ? 3 : 2) * threads * NV * 16;
+  // as many blocks as fit: three of 256 threads by registers, fewer by shared memory
+  const int per_sm = std::max(1, std::min(768 / threads, std::min(233472 / (smem + 2048), 8)));
+  k<<<unsigned(std::min<int64_t>(a.T, 152 * per_sm)), threads, smem, st>>>(a);
+  return launched(1);
+}
+template <class DT, int NV>
+int launch_stream(const BlockNormArgs &a, int pieces, cudaStream_t st) {
+  return a.gate ? launch_stream_g<DT, NV, true>(a, pieces, st) : launch_stream_g<DT, NV, false>(a, pieces, st);
+}
+
+template <class DT, int VW, bool SHIFT>
 int launch_t(const BlockNormArgs &a, cudaStream_t st) {
-  const int pieces = (a.H + VW - 1) / VW;
-  if (pieces <= 32) return launch_one<DT, VW, 1, true>(a, 128, st);
-  if (pieces <= 64) return launch_one<DT, VW, 2, true>(a, 128, st);
-  if (pieces <= 128) return launch_one<DT, VW, 4, true>(a, 128, st);
-  // Few rows: a thread per piece, for the shortest chain of loads.  Many: four
-  // or more pieces a thread, so that a row's loads are in flight together.
-  if (a.T <= 2 * 152 && pieces <= 1024) return launch_one<DT, VW, 1, false>(a, threads_for(pieces, 1), st);
-  if (pieces <= 4 * 512) return launch_one<DT, VW, 4, false>(a, threads_for(pieces, 4), st);
-  if (pieces <= 8 * 512) return launch_one<DT, VW, 8, false>(a, threads_for(pieces, 8), st);
-  if constexpr (VW < 8) {
-    if (pieces <= 16 * 512) return launch_one<DT, VW, 16, false>(a, threads_for(pieces, 16), st);
+  const int pieces = (a.H + VW - 1) / VW + (SHIFT ? 1 : 0);
+  if (pieces <= 32) return launch_one<DT, VW, 1, true, SHIFT>(a, 128, st);
+  if (pieces <= 64) return launch_one<DT, VW, 2, true, SHIFT>(a, 128, st);
+  // Few rows: a thread per piece, for the shortest chain of loads.  Many: some
+  // pieces a thread, and where rows are whole pieces the next row under way.
+  if (a.T <= 2 * 152 && pieces <= 1024)
+    return launch_one<DT, VW, 1, false, SHIFT>(a, threads_for(pieces, 1), st);
+  if constexpr (!SHIFT && VW > 1) {
+    if (a.T > 6 * 152 && pieces <= 4 * 256)
+      return pieces <= 2 * 256 ? launch_stream<DT, 2>(a, pieces, st) : launch_stream<DT, 4>(a, pieces, st);
   }
-  if constexpr (VW == 1) return launch_one<DT, VW, 64, false>(a, threads_for(pieces, 64), st);
+  if (pieces <= 2 * 256) return launch_one<DT, VW, 2, false, SHIFT>(a, threads_for(pieces, 2), st);
+  if (pieces <= 4 * 256) return launch_one<DT, VW, 4, false, SHIFT>(a, threads_for(pieces, 4), st);
+  if (pieces <= 8 * 512) return launch_one<DT, VW, 8, false, SHIFT>(a, threads_for(pieces, 8), st);
+  if constexpr (SHIFT || VW < 8) {
+    if (pieces <= 16 * 544) return launch_one<DT, VW, 16, false, SHIFT>(a, threads_for(pieces, 16), st);
+  }
+  if constexpr (VW == 1) return launch_one<DT, VW, 64, false, SHIFT>(a, threads_for(pieces, 64), st);
   return WQ_ERR_UNSUPPORTED;
+}
+
+// How a row is reached: pieces of 16 bytes; such pieces with every row's start
+// shifted alike; single elements
+template <class DT>
+int launch_dt(const BlockNormArgs &a, cudaStream_t st) {
+  switch (a.reach) {
+    case 0: return launch_t<DT, DT::kVec, false>(a, st);
+    case 1: return launch_t<DT, DT::kVec, true>(a, st);
+    default: return launch_t<DT, 1, false>(a, st);
+  }
 }
 
 }  // namespace
 
-int launch_block_norm(const BlockNormArgs &a, int dtype, bool vec, cudaStream_t st) {
+int launch_block_norm(const BlockNormArgs &a, int dtype, cudaStream_t st) {
   switch (dtype) {
-    case WQ_DT_BF16: return vec ? launch_t<Bf16, 8>(a, st) : launch_t<Bf16, 1>(a, st);
-    case WQ_DT_F16: return vec ? launch_t<F16, 8>(a, st) : launch_t<F16, 1>(a, st);
-    default: return vec ? launch_t<F32, 4>(a, st) : launch_t<F32, 1>(a, st);
+    case WQ_DT_BF16: return launch_dt<Bf16>(a, st);
+    case WQ_DT_F16: return launch_dt<F16>(a, st);
+    default: return launch_dt<F32>(a, st);
   }
 }
 

@@ -69,13 +69,13 @@ __global__ void rope_vec_kernel(const RopeArgs a, int per_token) {
     if (piece < nrot && a.layout == WQ_ROPE_HALF) {
       const int o0 = piece * 8, o1 = o0 + s.rot / 2;
       V p = V::load(x + o0), q = V::load(x + o1);
+      float f[8], g[8];
+      p.get(f);
+      q.get(g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float f = p.f(e), g = q.f(e);
-        turn(f, g, row[o0 + e], a.sign);
-        p.set(e, f);
-        q.set(e, g);
-      }
+      for (int e = 0; e < 8; ++e) turn(f[e], g[e], row[o0 + e], a.sign);
+      p.set(f);
+      q.set(g);
       p.store(d + o0);
       q.store(d + o1);
       continue;
@@ -87,13 +87,11 @@ __global__ void rope_vec_kernel(const RopeArgs a, int per_token) {
       if (o >= s.D) break;
       V p = V::load(x + o);
       if (a.layout == WQ_ROPE_INTERLEAVED && o < s.rot) {
+        float f[8];
+        p.get(f);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          float f = p.f(e), g = p.f(e + 1);
-          turn(f, g, row[(o + e) / 2], a.sign);
-          p.set(e, f);
-          p.set(e + 1, g);
-        }
+        for (int e = 0; e < 8; e += 2) turn(f[e], f[e + 1], row[(o + e) / 2], a.sign);
+        p.set(f);
       }
       p.store(d + o);
     }

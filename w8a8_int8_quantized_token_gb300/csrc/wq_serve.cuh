@@ -13,6 +13,15 @@ struct Bf16 {
   static constexpr int kVec = 8;  // elements of a 16-byte access
   static __device__ __forceinline__ float to_f(uint16_t v) { return bf16_to_f(v); }
   static __device__ __forceinline__ uint16_t from_f(float f) { return f_to_bf16(f); }
+  static __device__ __forceinline__ void unpack2(uint32_t w, float &lo, float &hi) {
+    lo = bf16_lo(w);
+    hi = bf16_hi(w);
+  }
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
 };
 struct F16 {
   using Raw = uint16_t;
@@ -23,6 +32,12 @@ struct F16 {
   static __device__ __forceinline__ uint16_t from_f(float f) {
     return __half_as_ushort(__float2half_rn(f));
   }
+  static __device__ __forceinline__ void unpack2(uint32_t w, float &lo, float &hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    lo = f.x;
+    hi = f.y;
+  }
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) { return f16x2_rn(lo, hi); }
 };
 struct F32 {
   using Raw = float;
@@ -31,29 +46,53 @@ struct F32 {
   static __device__ __forceinline__ float from_f(float f) { return f; }
 };
 
-// VW consecutive elements, VW = 1 or one 16-byte access
+// VW consecutive elements as they lie in memory: one, or one 16-byte access
 template <class DT, int VW>
-struct alignas(VW == 1 ? sizeof(typename DT::Raw) : 16) Vec {
-  typename DT::Raw e[VW];
+struct Vec {
+  static_assert(VW == DT::kVec, "one 16-byte access");
+  uint4 w;
   static __device__ __forceinline__ Vec load(const typename DT::Raw *p) {
-    Vec v;
-    if constexpr (VW == 1) {
-      v.e[0] = *p;
+    return {*reinterpret_cast<const uint4 *>(p)};
+  }
+  __device__ __forceinline__ void store(typename DT::Raw *p) const { *reinterpret_cast<uint4 *>(p) = w; }
+  __device__ __forceinline__ void get(float (&f)[VW]) const {
+    if constexpr (VW == 8) {
+      DT::unpack2(w.x, f[0], f[1]);
+      DT::unpack2(w.y, f[2], f[3]);
+      DT::unpack2(w.z, f[4], f[5]);
+      DT::unpack2(w.w, f[6], f[7]);
     } else {
-      static_assert(sizeof(v.e) == 16, "one 16-byte access");
-      *reinterpret_cast<uint4 *>(v.e) = *reinterpret_cast<const uint4 *>(p);
+      f[0] = __uint_as_float(w.x);
+      f[1] = __uint_as_float(w.y);
+      f[2] = __uint_as_float(w.z);
+      f[3] = __uint_as_float(w.w);
     }
-    return v;
   }
-  __device__ __forceinline__ void store(typename DT::Raw *p) const {
-    if constexpr (VW == 1)
-      *p = e[0];
+  __device__ __forceinline__ void set(const float (&f)[VW]) {
+    if constexpr (VW == 8)
+      w = make_uint4(DT::pack2(f[0], f[1]), DT::pack2(f[2], f[3]), DT::pack2(f[4], f[5]),
+                     DT::pack2(f[6], f[7]));
     else
-      *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(e);
+      w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                     __float_as_uint(f[3]));
   }
-  __device__ __forceinline__ float f(int i) const { return DT::to_f(e[i]); }
-  __device__ __forceinline__ void set(int i, float x) { e[i] = DT::from_f(x); }
 };
+template <class DT>
+struct Vec<DT, 1> {
+  typename DT::Raw w;
+  static __device__ __forceinline__ Vec load(const typename DT::Raw *p) { return {*p}; }
+  __device__ __forceinline__ void store(typename DT::Raw *p) const { *p = w; }
+  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = DT::to_f(w); }
+  __device__ __forceinline__ void set(const float (&f)[1]) { w = DT::from_f(f[0]); }
+};
+
+// x = x * y + c on pairs, one rounding each
+__device__ __forceinline__ void fma2(float &x0, float &x1, float y0, float y1, float c0, float c1) {
+  asm("{\n .reg .b64 x, y, c;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 c, {%4, %5};\n"
+      " fma.rn.f32x2 x, x, y, c;\n mov.b64 {%0, %1}, x;\n}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1), "f"(c0), "f"(c1));
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -72,8 +111,9 @@ struct BlockNormArgs {
   int64_t T;
   int H;
   void *x_out, *y;
+  int reach;  // 0: 16-byte pieces, 1: such pieces with rows shifted alike, 2: single elements
 };
-int launch_block_norm(const BlockNormArgs &a, int dtype, bool vec, cudaStream_t st);
+int launch_block_norm(const BlockNormArgs &a, int dtype, cudaStream_t st);
 
 // One tensor of heads that a rotary launch reads and writes
 struct RopeSeg {

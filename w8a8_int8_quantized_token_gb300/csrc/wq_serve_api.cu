@@ -87,18 +87,25 @@ int wq_block_norm(const void *block, int64_t ldb, const void *residual, int64_t 
   if (H > 32768 || T >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
   const unsigned esz = dtype == WQ_DT_F32 ? 4 : 2, n = 16 / esz;
   const void *ptrs[] = {block, residual, gate, post_weight, post_bias, pre_weight, pre_bias, x_out, y};
-  bool vec = H % n == 0 && ldb % n == 0 && (!residual || ldr % n == 0) && (!gate || ldg % n == 0) &&
-             (!x_out || ldx % n == 0) && (!y || ldy % n == 0);
-  for (const void *p : ptrs) {
-    if (!al(p, esz)) return WQ_ERR_UNSUPPORTED;
-    vec = vec && al(p, 16);
+  const int64_t pitch[] = {ldb, ldr, ldg, 0, 0, 0, 0, ldx, ldy};
+  bool vec = H % n == 0, shift = true;
+  for (int i = 0; i < 9; ++i) {
+    if (!ptrs[i]) continue;
+    if (!al(ptrs[i], esz)) return WQ_ERR_UNSUPPORTED;
+    vec = vec && al(ptrs[i], 16) && pitch[i] % n == 0;
+    // rows that start alike against 16-byte boundaries (one row for all, and
+    // weights, are read element by element there)
+    const bool rows = i < 3 ? !(i == 2 && ldg == 0) : i > 6;
+    if (rows)
+      shift = shift && reinterpret_cast<uintptr_t>(ptrs[i]) % 16 == reinterpret_cast<uintptr_t>(block) % 16 &&
+              pitch[i] % n == ldb % n;
   }
   const int rc = device_ok();
   if (rc != WQ_OK) return rc;
   const BlockNormArgs a{block, residual, gate, post_weight, post_bias, pre_weight, pre_bias,
                         ldb,   ldr,      ldg,  ldx,         ldy,       scale,      eps,
-                        post,  pre,      T,    int(H),      x_out,     y};
-  return launch_block_norm(a, dtype, vec, stream);
+                        post,  pre,      T,    int(H),      x_out,     y,          vec ? 0 : shift ? 1 : 2};
+  return launch_block_norm(a, dtype, stream);
 }
 
 int wq_rope_table(float *table, int64_t max_pos, int rot, double base, int scaling, double factor,
