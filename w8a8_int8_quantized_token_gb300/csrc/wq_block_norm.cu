@@ -32,37 +32,56 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 // row begins some elements after a 16-byte boundary, the pieces are the
 // aligned ones around it, and the row's first and last piece are taken
 // element by element.
-template <class DT, int VW, int NV, bool WARP, bool SHIFT>
+//
+// FULL: every thread holds NV pieces (no bounds to ask for).
+template <class DT, int VW, int NV, bool WARP, bool SHIFT, bool FULL = false>
 struct Row {
   using Raw = typename DT::Raw;
   using V = Vec<DT, VW>;
-  using F = float[VW];
   static constexpr int kPieces = NV;
-  float v[NV][VW];
+  static constexpr int NP = VW > 1 ? VW / 2 : 1;  // pairs of a piece (a single element: with a 0)
+  Pair v[NV][NP];
   int i0, step, H;
 
   __device__ __forceinline__ int at(int k) const { return i0 + k * step; }
   __device__ __forceinline__ bool in(int k) const {  // some of piece k
-    return SHIFT ? at(k) < H && at(k) + VW > 0 : at(k) < H;
+    return FULL ? true : SHIFT ? at(k) < H && at(k) + VW > 0 : at(k) < H;
   }
   __device__ __forceinline__ bool whole(int k) const { return at(k) >= 0 && at(k) + VW <= H; }
   __device__ __forceinline__ bool has(int k, int e) const {
-    return SHIFT ? unsigned(at(k) + e) < unsigned(H) : in(k);
+    return SHIFT ? unsigned(at(k) + e) < unsigned(H) : e < VW && in(k);
+  }
+  static __device__ __forceinline__ void pairs(const V &x, Pair (&p)[NP]) {
+    float f[VW];
+    x.get(f);
+    if constexpr (VW > 1) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
+    } else {
+      p[0] = pair(f[0], 0.0f);
+    }
   }
   __device__ __forceinline__ V each(const Raw *p, int k) const {
-    if constexpr (VW == 8) {
-      uint32_t w[4];
+    uint32_t w[4];
+    if (whole(k)) {  // no bounds to ask for
+      const Raw *x = p + at(k);
+      if constexpr (VW == 8) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) w[e / 2] = __byte_perm(x[e], x[e + 1], 0x5410);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(x[e]);
+      }
+    } else if constexpr (VW == 8) {
 #pragma unroll
       for (int e = 0; e < 8; e += 2)
         w[e / 2] = (has(k, e) ? uint32_t(p[at(k) + e]) : 0u) |
                    (has(k, e + 1) ? uint32_t(p[at(k) + e + 1]) << 16 : 0u);
-      return {make_uint4(w[0], w[1], w[2], w[3])};
     } else {
-      uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = has(k, e) ? __float_as_uint(p[at(k) + e]) : 0u;
-      return {make_uint4(w[0], w[1], w[2], w[3])};
     }
+    return {make_uint4(w[0], w[1], w[2], w[3])};
   }
   __device__ __forceinline__ V load(const Raw *p, int k) const {
     if constexpr (!SHIFT) return V::load(p + at(k));
@@ -74,46 +93,47 @@ struct Row {
     else return each(p, k);
   }
   __device__ __forceinline__ void store(Raw *p, int k) const {
-    if constexpr (!SHIFT) {
-      V x;
-      x.set(v[k]);
-      x.store(p + at(k));
-    } else if (whole(k)) {
-      V x;
-      x.set(v[k]);
-      x.store(p + at(k));
-    } else {
+    float f[VW > 1 ? VW : 2];
 #pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (has(k, e)) p[at(k) + e] = DT::from_f(v[k][e]);
+    for (int i = 0; i < NP; ++i) split(v[k][i], f[2 * i], f[2 * i + 1]);
+    if constexpr (VW == 1) {
+      p[at(k)] = DT::from_f(f[0]);
+    } else {
+      if (!SHIFT || whole(k)) {
+        V x;
+        x.set(f);
+        x.store(p + at(k));
+      } else if constexpr (SHIFT) {
+#pragma unroll
+        for (int e = 0; e < VW; ++e)
+          if (has(k, e)) p[at(k) + e] = DT::from_f(f[e]);
+      }
     }
   }
   __device__ __forceinline__ void clear_past(int k) {  // 0 outside the row
+    if (VW > 1 && (SHIFT ? whole(k) : in(k))) return;
 #pragma unroll
-    for (int e = 0; e < VW; ++e)
-      if (!has(k, e)) v[k][e] = 0.0f;
+    for (int i = 0; i < NP; ++i) {
+      if (!has(k, 2 * i) || !has(k, 2 * i + 1)) {
+        float x, y;
+        split(v[k][i], x, y);
+        v[k][i] = pair(has(k, 2 * i) ? x : 0.0f, has(k, 2 * i + 1) ? y : 0.0f);
+      }
+    }
   }
 
   // v = residual + scale * (gate * v) for piece k
   __device__ __forceinline__ void add(int k, const V *gate, float scale, const V *residual) {
-    F r = {};
-    if (residual) residual->get(r);
+    Pair r[NP] = {};
+    if (residual) pairs(*residual, r);
     if (gate) {
-      F g;
-      gate->get(g);
-      if constexpr (VW > 1) {
+      Pair g[NP];
+      pairs(*gate, g);
 #pragma unroll
-        for (int e = 0; e < VW; e += 2) mul2(v[k][e], v[k][e + 1], g[e], g[e + 1]);
-      } else {
-        v[k][0] *= g[0];
-      }
+      for (int i = 0; i < NP; ++i) v[k][i] = mul_p(v[k][i], g[i]);
     }
-    if constexpr (VW > 1) {
 #pragma unroll
-      for (int e = 0; e < VW; e += 2) fma2(v[k][e], v[k][e + 1], scale, scale, r[e], r[e + 1]);
-    } else {
-      v[k][0] = __fmaf_rn(v[k][0], scale, r[0]);
-    }
+    for (int i = 0; i < NP; ++i) v[k][i] = fma_p(v[k][i], pair(scale, scale), r[i]);
   }
 
   // v = N(v)
@@ -124,75 +144,69 @@ struct Row {
     const auto *w = static_cast<const Raw *>(weight);
     const auto *c = static_cast<const Raw *>(layer ? bias : nullptr);
     // weights are asked for ahead of the reductions where registers allow
-    constexpr bool kAhead = NV <= 4 && !SHIFT;
-    V wv[NV];
+    constexpr bool kAhead = NV <= 2 || (NV <= 4 && !SHIFT), kBiasAhead = NV <= 2;
+    V wv[NV], cv[NV];
     if (kAhead && w) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
         if (in(k)) wv[k] = load_weight(w, k);
     }
+    if (kBiasAhead && c) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (in(k)) cv[k] = load_weight(c, k);
+    }
+    const float over_h = __frcp_rn(float(H));
+    float x, y;
     if (layer) {
-      float s0 = 0.0f, s1 = 0.0f;
+      Pair s = 0;
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {  // 0 past the row
-        if constexpr (VW > 1) {
+      for (int k = 0; k < NV; ++k)  // 0 past the row
 #pragma unroll
-          for (int e = 0; e < VW; e += 2) add2(s0, s1, v[k][e], v[k][e + 1]);
-        } else {
-          s0 += v[k][0];
-        }
-      }
-      const float m = -__fdiv_rn(row_sum<WARP>(s0 + s1, red[0]), float(H));
+        for (int i = 0; i < NP; ++i) s = add_p(s, v[k][i]);
+      split(s, x, y);
+      const float m = -row_sum<WARP>(x + y, red[0]) * over_h;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if constexpr (VW > 1) {
 #pragma unroll
-          for (int e = 0; e < VW; e += 2) add2(v[k][e], v[k][e + 1], m, m);
-        } else {
-          v[k][0] += m;
-        }
+        for (int i = 0; i < NP; ++i) v[k][i] = add_p(v[k][i], pair(m, m));
         clear_past(k);
       }
     }
-    float s0 = 0.0f, s1 = 0.0f;
+    Pair s = 0;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if constexpr (VW > 1) {
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < VW; e += 2) {
-          float x = v[k][e], y = v[k][e + 1];
-          fma2(x, y, x, y, s0, s1);
-          s0 = x;
-          s1 = y;
-        }
-      } else {
-        s0 = __fmaf_rn(v[k][0], v[k][0], s0);
-      }
-    }
-    const float r = __fdiv_rn(
-        1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(row_sum<WARP>(s0 + s1, red[1]), float(H)), eps)));
+      for (int i = 0; i < NP; ++i) s = fma_p(v[k][i], v[k][i], s);
+    split(s, x, y);
+    const float r = rsqrtf(__fmaf_rn(row_sum<WARP>(x + y, red[1]), over_h, eps));
+    if (w) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (!in(k)) continue;
-      F wf, cf = {};
-#pragma unroll
-      for (int e = 0; e < VW; ++e) wf[e] = 1.0f;
-      if (w) {
+      for (int k = 0; k < NV; ++k) {
+        if (!in(k)) continue;
         if (!kAhead) wv[k] = load_weight(w, k);
-        wv[k].get(wf);
-      }
-      if (c) load_weight(c, k).get(cf);
-      if constexpr (VW > 1) {
+        Pair f[NP];
+        pairs(wv[k], f);
 #pragma unroll
-        for (int e = 0; e < VW; e += 2) {
-          mul2(v[k][e], v[k][e + 1], r, r);
-          if (c) fma2(v[k][e], v[k][e + 1], wf[e], wf[e + 1], cf[e], cf[e + 1]);
-          else if (w) mul2(v[k][e], v[k][e + 1], wf[e], wf[e + 1]);
-        }
-      } else {
-        v[k][0] = __fmaf_rn(v[k][0] * r, wf[0], cf[0]);
+        for (int i = 0; i < NP; ++i) v[k][i] = mul_p(mul_p(v[k][i], pair(r, r)), f[i]);
       }
-      if (SHIFT && c) clear_past(k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[k][i] = mul_p(v[k][i], pair(r, r));
+    }
+    if (c) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (!in(k)) continue;
+        Pair f[NP];
+        if (!kBiasAhead) cv[k] = load_weight(c, k);
+        pairs(cv[k], f);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) v[k][i] = add_p(v[k][i], f[i]);
+        if (SHIFT) clear_past(k);
+      }
     }
   }
 };
@@ -222,7 +236,7 @@ __device__ __forceinline__ void copy16(void *dst, const void *src) {
 // Threads of a block at most, and blocks that share an SM at least: the rows
 // in flight hide the reductions of each.
 template <int NV, bool WARP>
-constexpr int max_threads() { return WARP ? 128 : (NV == 1 ? 1024 : (NV <= 4 ? 256 : 544)); }
+constexpr int max_threads() { return WARP ? 128 : (NV == 1 ? 1024 : (NV <= 4 ? 288 : 544)); }
 template <int NV, bool WARP>
 constexpr int min_blocks() { return WARP ? 6 : (NV == 1 ? 1 : (NV <= 4 ? 3 : 1)); }
 
@@ -261,9 +275,12 @@ __global__ void __launch_bounds__(max_threads<NV, WARP>(), min_blocks<NV, WARP>(
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
+    if (row.in(k)) {
+      row.pairs(b[k], row.v[k]);
+    } else {
 #pragma unroll
-    for (int e = 0; e < VW; ++e) row.v[k][e] = 0.0f;
-    if (row.in(k)) b[k].get(row.v[k]);
+      for (int i = 0; i < row.NP; ++i) row.v[k][i] = 0;
+    }
   }
   row.norm(a.post, a.w_post, a.b_post, a.eps, red);
 #pragma unroll
@@ -282,14 +299,14 @@ __global__ void __launch_bounds__(max_threads<NV, WARP>(), min_blocks<NV, WARP>(
 // pieces of the row after the one at hand into shared memory while it works
 // on that, so that loads are always in flight and no thread waits for another
 // outside the reductions (a thread reads back only what it copied itself).
-template <class DT, int NV, bool GATE>
+template <class DT, int NV, bool GATE, bool FULL>
 __global__ void __launch_bounds__(256, 3) block_norm_stream_kernel(const BlockNormArgs a) {
   using Raw = typename DT::Raw;
   constexpr int VW = DT::kVec;
   using V = Vec<DT, VW>;
   __shared__ float red[2][4][32];  // by parity of the row
   extern __shared__ __align__(16) uint8_t smem[];
-  Row<DT, VW, NV, false, false> row;
+  Row<DT, VW, NV, false, false, FULL> row;
   row.H = a.H;
   row.i0 = threadIdx.x * VW;
   row.step = blockDim.x * VW;
@@ -318,9 +335,12 @@ __global__ void __launch_bounds__(256, 3) block_norm_stream_kernel(const BlockNo
     asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+      if (row.in(k)) {
+        row.pairs(V::load(piece(buf, 0, k)), row.v[k]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < VW; ++e) row.v[k][e] = 0.0f;
-      if (row.in(k)) V::load(piece(buf, 0, k)).get(row.v[k]);
+        for (int i = 0; i < row.NP; ++i) row.v[k][i] = 0;
+      }
     }
     row.norm(a.post, a.w_post, a.b_post, a.eps, red[buf]);
 #pragma unroll
@@ -345,9 +365,9 @@ int launch_one(const BlockNormArgs &a, int threads, cudaStream_t st) {
 
 inline int threads_for(int pieces, int nv) { return ((pieces + nv - 1) / nv + 31) / 32 * 32; }
 
-template <class DT, int NV, bool GATE>
+template <class DT, int NV, bool GATE, bool FULL>
 int launch_stream_g(const BlockNormArgs &a, int pieces, cudaStream_t st) {
-  auto *k = block_norm_stream_kernel<DT, NV, GATE>;
+  auto *k = block_norm_stream_kernel<DT, NV, GATE, FULL>;
   static bool sized = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            2 * (GATE ? 3 : 2) * 256 * NV * 16) == cudaSuccess;
   if (!sized) return WQ_ERR_LAUNCH;
@@ -359,7 +379,11 @@ int launch_stream_g(const BlockNormArgs &a, int pieces, cudaStream_t st) {
 }
 template <class DT, int NV>
 int launch_stream(const BlockNormArgs &a, int pieces, cudaStream_t st) {
-  return a.gate ? launch_stream_g<DT, NV, true>(a, pieces, st) : launch_stream_g<DT, NV, false>(a, pieces, st);
+  if (pieces % (32 * NV) == 0)
+    return a.gate ? launch_stream_g<DT, NV, true, true>(a, pieces, st)
+                  : launch_stream_g<DT, NV, false, true>(a, pieces, st);
+  return a.gate ? launch_stream_g<DT, NV, true, false>(a, pieces, st)
+                : launch_stream_g<DT, NV, false, false>(a, pieces, st);
 }
 
 template <class DT, int VW, bool SHIFT>
@@ -375,8 +399,8 @@ int launch_t(const BlockNormArgs &a, cudaStream_t st) {
     if (a.T > 6 * 152 && pieces <= 4 * 256)
       return pieces <= 2 * 256 ? launch_stream<DT, 2>(a, pieces, st) : launch_stream<DT, 4>(a, pieces, st);
   }
-  if (pieces <= 2 * 256) return launch_one<DT, VW, 2, false, SHIFT>(a, threads_for(pieces, 2), st);
-  if (pieces <= 4 * 256) return launch_one<DT, VW, 4, false, SHIFT>(a, threads_for(pieces, 4), st);
+  if (pieces <= 2 * 288) return launch_one<DT, VW, 2, false, SHIFT>(a, threads_for(pieces, 2), st);
+  if (pieces <= 4 * 288) return launch_one<DT, VW, 4, false, SHIFT>(a, threads_for(pieces, 4), st);
   if (pieces <= 8 * 512) return launch_one<DT, VW, 8, false, SHIFT>(a, threads_for(pieces, 8), st);
   if constexpr (SHIFT || VW < 8) {
     if (pieces <= 16 * 544) return launch_one<DT, VW, 16, false, SHIFT>(a, threads_for(pieces, 16), st);

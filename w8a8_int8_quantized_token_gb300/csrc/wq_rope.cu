@@ -1,10 +1,12 @@
 // Rotary positions and the rotated append to a paged cache.
 //
 // One launch walks up to three tensors of heads (queries, keys, values).  The
-// unit of a thread is 16 elements of one head: 8 pairs (two 16-byte vectors
-// half a rotation apart in the half layout, 16 consecutive elements in the
-// interleaved one), or 16 elements to copy.  Bound by HBM: every element read
-// once and written once; the table rows come from L2.
+// unit of a thread is 16 elements of a head: 8 pairs (two 16-byte vectors half
+// a rotation apart in the half layout, 16 consecutive elements in the
+// interleaved one), or 16 elements to copy; with many tokens a thread takes
+// the same unit of up to four heads, whose loads are in flight together and
+// which share the unit's part of the table row.  Bound by HBM: every element
+// read once and written once; the table rows come from L2.
 #include "wq_serve.cuh"
 
 namespace wq {
@@ -35,10 +37,9 @@ __device__ __forceinline__ const float2 *row_of(const RopeArgs &a, int64_t t, bo
   return reinterpret_cast<const float2 *>(a.table) + int64_t(p) * (a.rot / 2);
 }
 
-__device__ __forceinline__ void turn(float &x, float &y, float2 cs, float sign) {
-  const float s = __fmul_rn(cs.y, sign);
-  const float u = __fsub_rn(__fmul_rn(x, cs.x), __fmul_rn(y, s));
-  y = __fadd_rn(__fmul_rn(y, cs.x), __fmul_rn(x, s));
+__device__ __forceinline__ void turn(float &x, float &y, float c, float s) {
+  const float u = __fmaf_rn(x, c, -__fmul_rn(y, s));
+  y = __fmaf_rn(y, c, __fmul_rn(x, s));
   x = u;
 }
 
@@ -47,54 +48,91 @@ __host__ __device__ inline int units_of(const RopeSeg &s) {
   return s.rot / 16 + (s.D - s.rot / 16 * 16 + 15) / 16;
 }
 
-template <class DT>
-__global__ void rope_vec_kernel(const RopeArgs a, int per_token) {
+// Threads that share a segment's token: a unit of KH heads each
+template <int KH>
+__host__ __device__ inline int threads_of(const RopeSeg &s) {
+  return (s.heads + KH - 1) / KH * units_of(s);
+}
+
+template <class DT, int KH>
+__global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int per_token) {
   using Raw = typename DT::Raw;
   using V = Vec<DT, 8>;
-  const int64_t n = a.T * per_token;
-  for (int64_t u = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; u < n;
-       u += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t t = u / per_token;
-    int rest = int(u - t * per_token), i = 0;
-    while (rest >= a.seg[i].heads * units_of(a.seg[i])) rest -= a.seg[i].heads * units_of(a.seg[i]), ++i;
-    const RopeSeg &s = a.seg[i];
-    const int units = units_of(s), head = rest / units, piece = rest - head * units;
-    Raw *d = dst_of<Raw>(a, s, t, rest == 0);
-    if (!d) continue;
-    const float2 *row = nullptr;
-    if ((s.rot || (s.paged && a.rot)) && !(row = row_of(a, t, rest == 0))) continue;
-    d += head * s.d_head;
-    const Raw *x = static_cast<const Raw *>(s.src) + t * s.s_token + head * s.s_head;
-    const int nrot = s.rot / 16;
-    if (piece < nrot && a.layout == WQ_ROPE_HALF) {
-      const int o0 = piece * 8, o1 = o0 + s.rot / 2;
-      V p = V::load(x + o0), q = V::load(x + o1);
-      float f[8], g[8];
-      p.get(f);
-      q.get(g);
+  // blocks of whole tokens, or (y) a token's threads in blocks of 256
+  int64_t t;
+  int rest;
+  if (per_token >= 256) {
+    t = blockIdx.x;
+    rest = int(blockIdx.y * 256 + threadIdx.x);
+    if (rest >= per_token) return;
+  } else {
+    const int tokens = 256 / per_token, own = int(threadIdx.x) / per_token;
+    t = int64_t(blockIdx.x) * tokens + own;
+    rest = int(threadIdx.x) - own * per_token;
+    if (own >= tokens || t >= a.T) return;
+  }
+  int i = 0;
+  while (rest >= threads_of<KH>(a.seg[i])) rest -= threads_of<KH>(a.seg[i]), ++i;
+  const RopeSeg &s = a.seg[i];
+  const int units = units_of(s), groups = (s.heads + KH - 1) / KH;
+  const int head0 = rest / units, piece = rest - head0 * units;  // heads head0 + k * groups
+  Raw *d = dst_of<Raw>(a, s, t, rest == 0);
+  if (!d) return;
+  const float2 *row = nullptr;
+  if ((s.rot || (s.paged && a.rot)) && !(row = row_of(a, t, rest == 0))) return;
+  const Raw *x = static_cast<const Raw *>(s.src) + t * s.s_token;
+  const bool half = piece < s.rot / 16 && a.layout == WQ_ROPE_HALF;
+  const int o0 = half ? piece * 8 : piece * 16, o1 = half ? o0 + s.rot / 2 : o0 + 8;
+  const bool two = o1 < s.D;
+  // pairs of the first and of the second vector that turn
+  const int first = half ? 8 : (a.layout == WQ_ROPE_INTERLEAVED && o0 < s.rot ? 4 : 0);
+  const int second = !half && a.layout == WQ_ROPE_INTERLEAVED && o1 < s.rot ? 4 : 0;
+  V p[KH], q[KH];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) turn(f[e], g[e], row[o0 + e], a.sign);
-      p.set(f);
-      q.set(g);
-      p.store(d + o0);
-      q.store(d + o1);
-      continue;
-    }
-    const int o0 = piece * 16;  // 16 consecutive elements, rotated below rot
+  for (int k = 0; k < KH; ++k) {
+    const int head = head0 + k * groups;
+    if (head >= s.heads) break;
+    p[k] = V::load(x + head * s.s_head + o0);
+    if (two) q[k] = V::load(x + head * s.s_head + o1);
+  }
+  float c[8], n[8];  // cos and sin of the unit's pairs
+  if (first) {
+    const float2 *r = row + (half ? o0 : o0 / 2);
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int o = o0 + 8 * v;
-      if (o >= s.D) break;
-      V p = V::load(x + o);
-      if (a.layout == WQ_ROPE_INTERLEAVED && o < s.rot) {
-        float f[8];
-        p.get(f);
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) turn(f[e], f[e + 1], row[(o + e) / 2], a.sign);
-        p.set(f);
+    for (int e = 0; e < 8; e += 2) {
+      if (e < 4 || half || second) {
+        const float4 w = *reinterpret_cast<const float4 *>(r + e);
+        c[e] = w.x;
+        n[e] = w.y * a.sign;
+        c[e + 1] = w.z;
+        n[e + 1] = w.w * a.sign;
       }
-      p.store(d + o);
     }
+  }
+#pragma unroll
+  for (int k = 0; k < KH; ++k) {
+    const int head = head0 + k * groups;
+    if (head >= s.heads) break;
+    if (first) {
+      float f[8], g[8];
+      p[k].get(f);
+      q[k].get(g);
+      if (half) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) turn(f[e], g[e], c[e], n[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) turn(f[2 * e], f[2 * e + 1], c[e], n[e]);
+        if (second) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) turn(g[2 * e], g[2 * e + 1], c[4 + e], n[4 + e]);
+        }
+      }
+      p[k].set(f);
+      if (half || second) q[k].set(g);
+    }
+    p[k].store(d + head * s.d_head + o0);
+    if (two) q[k].store(d + head * s.d_head + o1);
   }
 }
 
@@ -124,7 +162,7 @@ __global__ void rope_any_kernel(const RopeArgs a, int per_token) {
     const int o0 = a.layout == WQ_ROPE_HALF ? piece : 2 * piece;
     const int o1 = a.layout == WQ_ROPE_HALF ? piece + s.rot / 2 : o0 + 1;
     float f = DT::to_f(x[o0]), g = DT::to_f(x[o1]);
-    turn(f, g, row[piece], a.sign);
+    turn(f, g, row[piece].x, row[piece].y * a.sign);
     d[o0] = DT::from_f(f);
     d[o1] = DT::from_f(g);
   }
@@ -151,19 +189,31 @@ __global__ void rope_table_kernel(float2 *table, int64_t n, int half, double log
   }
 }
 
+template <class DT, int KH>
+int launch_vec(const RopeArgs &a, cudaStream_t st) {
+  int per_token = 0;
+  for (int i = 0; i < a.nseg; ++i) per_token += threads_of<KH>(a.seg[i]);
+  if (per_token == 0) return WQ_OK;
+  const int tokens = per_token >= 256 ? 1 : 256 / per_token;
+  const dim3 grid(unsigned((a.T + tokens - 1) / tokens), unsigned(per_token >= 256 ? (per_token + 255) / 256 : 1));
+  if (grid.y > 65535) return WQ_ERR_UNSUPPORTED;
+  rope_vec_kernel<DT, KH><<<grid, 256, 0, st>>>(a, per_token);
+  return launched(1);
+}
+
 template <class DT>
 int launch_t(const RopeArgs &a, bool vec, cudaStream_t st) {
+  if constexpr (DT::kVec == 8) {
+    // four heads a thread once that leaves each SM a few blocks
+    int64_t units = 0;
+    for (int i = 0; i < a.nseg; ++i) units += a.T * a.seg[i].heads * units_of(a.seg[i]);
+    if (vec) return units > 4 * 256 * 152 * 4 ? launch_vec<DT, 4>(a, st) : launch_vec<DT, 1>(a, st);
+  }
   int per_token = 0;
-  for (int i = 0; i < a.nseg; ++i)
-    per_token += a.seg[i].heads * (vec ? units_of(a.seg[i]) : a.seg[i].D - a.seg[i].rot / 2);
+  for (int i = 0; i < a.nseg; ++i) per_token += a.seg[i].heads * (a.seg[i].D - a.seg[i].rot / 2);
   if (per_token == 0) return WQ_OK;
   const int64_t blocks = (a.T * per_token + 255) / 256;
-  const unsigned grid = unsigned(blocks < (1 << 20) ? blocks : (1 << 20));
-  if (vec) {
-    if constexpr (DT::kVec == 8) rope_vec_kernel<DT><<<grid, 256, 0, st>>>(a, per_token);
-  } else {
-    rope_any_kernel<DT><<<grid, 256, 0, st>>>(a, per_token);
-  }
+  rope_any_kernel<DT><<<unsigned(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, st>>>(a, per_token);
   return launched(1);
 }
 

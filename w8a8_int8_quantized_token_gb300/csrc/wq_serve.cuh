@@ -86,12 +86,32 @@ struct Vec<DT, 1> {
   __device__ __forceinline__ void set(const float (&f)[1]) { w = DT::from_f(f[0]); }
 };
 
-// x = x * y + c on pairs, one rounding each
-__device__ __forceinline__ void fma2(float &x0, float &x1, float y0, float y1, float c0, float c1) {
-  asm("{\n .reg .b64 x, y, c;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n mov.b64 c, {%4, %5};\n"
-      " fma.rn.f32x2 x, x, y, c;\n mov.b64 {%0, %1}, x;\n}"
-      : "+f"(x0), "+f"(x1)
-      : "f"(y0), "f"(y1), "f"(c0), "f"(c1));
+// Two floats in a register pair, for the packed float32 instructions (each
+// lane rounds once).  Kept as one 64-bit value: split into single floats
+// between operations, every one of them cost up to four moves.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void split(Pair p, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair fma_p(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair mul_p(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair add_p(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

@@ -20,7 +20,7 @@ bool cache_ok(const wq_paged_cache *c) {
 // Rotary segments that the vector kernel may take
 bool rope_vec_ok(const RopeArgs &a, int dtype) {
   if (dtype == WQ_DT_F32) return false;
-  if (a.rot % (a.layout == WQ_ROPE_HALF ? 16 : 8)) return false;
+  if (a.rot % (a.layout == WQ_ROPE_HALF ? 16 : 8) || !al(a.table, 16)) return false;
   for (int i = 0; i < a.nseg; ++i) {
     const RopeSeg &s = a.seg[i];
     if (s.D % 8 || s.s_token % 8 || s.s_head % 8 || s.d_token % 8 || s.d_head % 8 || s.d_page % 8 ||
