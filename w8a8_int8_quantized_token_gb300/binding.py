@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -50,8 +51,6 @@ class _PagedCache(_c.Structure):
                 ("num_pages", _L), ("page_size", _c.c_int32), ("heads", _c.c_int32),
                 ("dk", _c.c_int32), ("dv", _c.c_int32), ("dtype", _c.c_int32)]
 
-
-_PC = _c.POINTER(_PagedCache)
 
 _SIGS = {
     "wq_init": (_I, [_I]),
@@ -95,9 +94,9 @@ _SIGS = {
     "wq_block_norm": (_I, [_P, _L, _P, _L, _P, _L, _F, _I, _P, _P, _I, _P, _P, _F, _L, _L, _I, _P, _L, _P, _L, _P]),
     "wq_rope_table": (_I, [_P, _L, _I, _D, _I, _D, _D, _D, _D, _D, _P]),
     "wq_rope": (_I, [_P, _L, _L, _P, _P, _L, _L, _I, _I, _I, _I, _I, _I, _P, _L, _L, _P, _P]),
-    "wq_rope_append_paged": (_I, [_P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _L, _L, _I, _I, _PC, _P, _L, _L, _P, _P]),
-    "wq_attention_shared_prefix_workspace_size": (_S, [_L, _I, _I, _I, _PC, _L, _L]),
-    "wq_attention_shared_prefix": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _PC, _P, _L, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P, _S, _P, _P]),
+    "wq_rope_append_paged": (_I, [_P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _L, _L, _I, _I, _P, _P, _L, _L, _P, _P]),
+    "wq_attention_shared_prefix_workspace_size": (_S, [_L, _I, _I, _I, _P, _L, _L]),
+    "wq_attention_shared_prefix": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P, _S, _P, _P]),
     "wq_moe_forward_masked": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P, _P]),
 }
 
@@ -636,23 +635,57 @@ def linear_w8a8(x, W, sw, scheme="channel", acc="i32", out=None, ws=None, status
 
 
 # ---------------------------------------------------------------- the attention half of a layer
-def _view(t, dim, dtypes, name):
-    """A CUDA tensor whose last dimension is contiguous; other strides are free."""
+# A decode step makes these calls once per layer with little work behind each,
+# so the checks below ask a tensor for each property once.
+def _raw_stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _view(t, shape, dtype, name):
+    """Checks a CUDA tensor of this shape and type whose last dimension is
+    contiguous (other strides are free) and returns its strides."""
+    if not t.is_cuda:
+        raise WQError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise WQError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise WQError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise WQError(f"{name} must be contiguous in its last dimension")
+    return st
+
+
+def _dense(t, dtype, name):
+    """Checks a contiguous CUDA tensor and returns its shape."""
+    if not t.is_cuda:
+        raise WQError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise WQError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise WQError(f"{name} must be contiguous")
+    return t.shape
+
+
+def _dense_as(t, shape, dtype, name):
+    if _dense(t, dtype, name) != shape:
+        raise WQError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _code(t, dtypes, dim, name):
+    """The library's type code of a CUDA tensor with `dim` dimensions."""
     if not t.is_cuda:
         raise WQError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise WQError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() != dim:
         raise WQError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise WQError(f"{name} must be contiguous in its last dimension")
-    return t
+    return DTYPE[t.dtype]
 
 
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
-        raise WQError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
@@ -666,29 +699,30 @@ def block_norm(block, residual=None, gate=None, scale=1.0, post="none", post_wei
     block, on rows [T, H]: h = residual + scale * (gate * N_post(block));
     returns (h rounded, N_pre(h)).  post and pre are "none", "rms" or "layer";
     gate is [T, H] or [H]; x_out and y may be given (block or residual too)."""
-    _view(block, 2, _FLOATS, "block")
-    dt = (block.dtype,)
-    T, H = block.shape
-    if residual is not None:
-        _shape(_view(residual, 2, dt, "residual"), (T, H), "residual")
+    code = _code(block, _FLOATS, 2, "block")
+    dt, shape = block.dtype, block.shape
+    T, H = shape
+    ldb = _view(block, shape, dt, "block")[0]
+    ldr = 0 if residual is None else _view(residual, shape, dt, "residual")[0]
     ldg = 0
     if gate is not None:
-        _shape(_view(gate, gate.dim(), dt, "gate"), (H,) if gate.dim() == 1 else (T, H), "gate")
-        ldg = gate.stride(0) if gate.dim() == 2 else 0
+        if gate.dim() == 1:
+            _view(gate, (H,), dt, "gate")
+        else:
+            ldg = _view(gate, shape, dt, "gate")[0]
     for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
                     (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
         if t is not None:
-            _shape(_view(t, 1, dt, name), (H,), name)
-    x_out = torch.empty_like(block, memory_format=torch.contiguous_format) if x_out is None else \
-        _shape(_view(x_out, 2, dt, "x_out"), (T, H), "x_out")
-    y = torch.empty_like(block, memory_format=torch.contiguous_format) if y is None else \
-        _shape(_view(y, 2, dt, "y"), (T, H), "y")
+            _view(t, (H,), dt, name)
+    if x_out is None:
+        x_out = torch.empty(shape, dtype=dt, device=block.device)
+    if y is None:
+        y = torch.empty(shape, dtype=dt, device=block.device)
+    ldx, ldy = _view(x_out, shape, dt, "x_out")[0], _view(y, shape, dt, "y")[0]
     _check(lib().wq_block_norm(
-        _ptr(block), block.stride(0), _ptr(residual),
-        0 if residual is None else residual.stride(0), _ptr(gate), ldg, scale, NORM[post],
-        _ptr(post_weight), _ptr(post_bias), NORM[pre], _ptr(pre_weight), _ptr(pre_bias), eps, T, H,
-        DTYPE[block.dtype], _ptr(x_out), x_out.stride(0), _ptr(y), y.stride(0), _stream()),
-        "wq_block_norm")
+        block.data_ptr(), ldb, _at(residual), ldr, _at(gate), ldg, scale, NORM[post],
+        _at(post_weight), _at(post_bias), NORM[pre], _at(pre_weight), _at(pre_bias), eps, T, H, code,
+        x_out.data_ptr(), ldx, y.data_ptr(), ldy, _raw_stream(block)), "wq_block_norm")
     return x_out, y
 
 
@@ -698,50 +732,54 @@ def rope_table(max_pos, rot, base=10000.0, scaling="none", factor=1.0, trained=0
     float64; scaling "none", "linear", "ntk" or "yarn" for contexts `factor`
     times the `trained` one."""
     t = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device or "cuda")
-    _check(lib().wq_rope_table(_ptr(t), max_pos, rot, base, ROPE_SCALING[scaling], factor,
-                               float(trained), beta_fast, beta_slow, mscale, _stream()),
+    _check(lib().wq_rope_table(t.data_ptr(), max_pos, rot, base, ROPE_SCALING[scaling], factor,
+                               float(trained), beta_fast, beta_slow, mscale, _raw_stream(t)),
            "wq_rope_table")
     return t
 
 
 def _table(table):
-    _dev(table, torch.float32, "table")
-    if table.dim() != 3 or table.shape[2] != 2:
-        raise WQError(f"table must be [max_pos, rot/2, 2], got {list(table.shape)}")
-    return table
+    shape = _dense(table, torch.float32, "table")
+    if len(shape) != 3 or shape[2] != 2:
+        raise WQError(f"table must be [max_pos, rot/2, 2], got {list(shape)}")
+    return shape[0], 2 * shape[1]
 
 
 def rope(x, positions, table, layout="half", inverse=False, out=None, status=None):
     """Rotate the first rot = 2 * table.shape[1] elements of each head of x
     [T, heads, D] to its token's position; out may be x itself."""
-    _view(x, 3, _FLOATS, "x")
-    _table(table)
-    T, n, D = x.shape
-    _shape(_dev(positions, torch.int32, "positions"), (T,), "positions")
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else \
-        _shape(_view(out, 3, (x.dtype,), "out"), x.shape, "out")
-    _check(lib().wq_rope(_ptr(x), x.stride(0), x.stride(1), _ptr(positions), _ptr(table),
-                         table.shape[0], T, n, D, 2 * table.shape[1], ROPE_LAYOUT[layout],
-                         int(inverse), DTYPE[x.dtype], _ptr(out), out.stride(0), out.stride(1),
-                         _ptr(status), _stream()), "wq_rope")
+    code = _code(x, _FLOATS, 3, "x")
+    dt, shape = x.dtype, x.shape
+    T, n, D = shape
+    max_pos, rot = _table(table)
+    sx = _view(x, shape, dt, "x")
+    pos = _dense_as(positions, (T,), torch.int32, "positions")
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    so = _view(out, shape, dt, "out")
+    _check(lib().wq_rope(x.data_ptr(), sx[0], sx[1], pos, table.data_ptr(), max_pos, T, n, D, rot,
+                         ROPE_LAYOUT[layout], 1 if inverse else 0, code, out.data_ptr(), so[0], so[1],
+                         _at(status), _raw_stream(x)), "wq_rope")
     return out
+
+
+_CACHE = struct.Struct("@PPqqqqqqqiiiii0q")  # wq_paged_cache
 
 
 def _cache(k_cache, v_cache):
     """The wq_paged_cache of k_cache [pages, heads, page_size, dk] and v_cache
-    [pages, heads, page_size, dv], any strides over the first three."""
-    _view(k_cache, 4, _HALVES, "k_cache")
-    _view(v_cache, 4, (k_cache.dtype,), "v_cache")
-    if k_cache.shape[:3] != v_cache.shape[:3]:
+    [pages, heads, page_size, dv], any strides over the first three: its bytes,
+    heads, page size, dk and dv."""
+    code = _code(k_cache, _HALVES, 4, "k_cache")
+    dt, shape = k_cache.dtype, k_cache.shape
+    pages, heads, page, dk = shape
+    sk = _view(k_cache, shape, dt, "k_cache")
+    if v_cache.shape[:3] != shape[:3]:
         raise WQError("k_cache and v_cache must agree in pages, heads and page size")
-    pages, heads, page, dk = k_cache.shape
-    return _PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), *k_cache.stride()[:3],
-                       *v_cache.stride()[:3], pages, page, heads, dk, v_cache.shape[3],
-                       DTYPE[k_cache.dtype])
-
-
-def _strides(t):
-    return (None, 0, 0) if t is None else (_ptr(t), t.stride(0), t.stride(1))
+    sv = _view(v_cache, v_cache.shape, dt, "v_cache")
+    dv = v_cache.shape[3]
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1],
+                       sv[2], pages, page, heads, dk, dv, code), heads, page, dk, dv
 
 
 def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="half", q=None,
@@ -749,34 +787,35 @@ def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="h
     """Write rope(k) and v [T, heads, D] at places slots int64 [T] (page *
     page_size + place; negative: skipped) of a paged cache, and with q
     [T, q_heads, D] return rope(q).  table None appends without rotation."""
-    c = _cache(k_cache, v_cache)
-    dt = (k_cache.dtype,)
+    c, heads, _, dk, dv = _cache(k_cache, v_cache)
+    dt = k_cache.dtype
     T = k.shape[0]
-    _shape(_view(k, 3, dt, "k"), (T, c.heads, c.dk), "k")
-    _shape(_view(v, 3, dt, "v"), (T, c.heads, c.dv), "v")
-    _shape(_dev(slots, torch.int64, "slots"), (T,), "slots")
-    rot, max_pos = 0, 0
+    sk, sv = _view(k, (T, heads, dk), dt, "k"), _view(v, (T, heads, dv), dt, "v")
+    to = _dense_as(slots, (T,), torch.int64, "slots")
+    rot, max_pos, pos = 0, 0, None
     if table is not None:
-        _table(table)
-        _shape(_dev(positions, torch.int32, "positions"), (T,), "positions")
-        rot, max_pos = 2 * table.shape[1], table.shape[0]
+        max_pos, rot = _table(table)
+        pos = _dense_as(positions, (T,), torch.int32, "positions")
+    nq, sq, so = 0, (0, 0), (0, 0)
     if q is not None:
-        _view(q, 3, dt, "q")
-        _shape(q, (T, q.shape[1], c.dk), "q")
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else \
-            _shape(_view(q_out, 3, dt, "q_out"), q.shape, "q_out")
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != dk:
+            raise WQError(f"q must be [{T}, heads, {dk}], got {list(shape)}")
+        nq, sq = shape[1], _view(q, shape, dt, "q")
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dt, device=q.device)
+        so = _view(q_out, shape, dt, "q_out")
     _check(lib().wq_rope_append_paged(
-        *_strides(q), 0 if q is None else q.shape[1], *_strides(k), *_strides(v),
-        _ptr(positions) if rot else None, _ptr(slots), _ptr(table), max_pos, T, rot,
-        ROPE_LAYOUT[layout], c, *_strides(q_out if q is not None else None), _ptr(status),
-        _stream()), "wq_rope_append_paged")
+        _at(q), sq[0], sq[1], nq, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], pos, to,
+        _at(table), max_pos, T, rot, ROPE_LAYOUT[layout], c, _at(q_out) if nq else None, so[0], so[1],
+        _at(status), _raw_stream(k)), "wq_rope_append_paged")
     return q_out
 
 
 def attention_shared_prefix_workspace(q, k_cache, v_cache, B, prefix_len, max_suffix, max_q):
     """A workspace for attention_shared_prefix calls of these sizes."""
     n = lib().wq_attention_shared_prefix_workspace_size(
-        q.shape[0], B, max_q, q.shape[1], _cache(k_cache, v_cache), prefix_len, max_suffix)
+        q.shape[0], B, max_q, q.shape[1], _cache(k_cache, v_cache)[0], prefix_len, max_suffix)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
 
 
@@ -789,40 +828,39 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
     splits the tokens (None: T / B each); max_q and max_suffix bound a
     sequence's tokens and keys.  Returns out [T, q_heads, dv]; lse float32
     [T, q_heads] is filled if given."""
-    c = _cache(k_cache, v_cache)
-    dt = (k_cache.dtype,)
-    _view(q, 3, dt, "q")
-    T, Hq, dk = q.shape
-    if dk != c.dk:
-        raise WQError(f"q and k_cache must agree in head size, got {dk} and {c.dk}")
-    _dev(suffix_len, torch.int32, "suffix_len")
-    B = suffix_len.numel()
-    _view(page_table, 2, (torch.int32,), "page_table")
-    if page_table.shape[0] != B:
-        raise WQError(f"page_table must have {B} rows, got {page_table.shape[0]}")
-    if max_suffix > page_table.shape[1] * c.page_size:
+    c, _, page, dk, dv = _cache(k_cache, v_cache)
+    dt, shape = k_cache.dtype, q.shape
+    if len(shape) != 3 or shape[2] != dk:
+        raise WQError(f"q must be [tokens, heads, {dk}] as k_cache has, got {list(shape)}")
+    T, Hq = shape[0], shape[1]
+    sq = _view(q, shape, dt, "q")
+    B = _dense(suffix_len, torch.int32, "suffix_len").numel()
+    pages = page_table.shape[-1] if page_table.dim() == 2 else 0
+    ld = _view(page_table, (B, pages), torch.int32, "page_table")[0]
+    if max_suffix > pages * page:
         raise WQError(f"max_suffix {max_suffix} needs more pages than page_table has columns")
     if prefix_len:
-        _dev(prefix_pages, torch.int32, "prefix_pages")
-        if prefix_pages.numel() * c.page_size < prefix_len:
+        _dense(prefix_pages, torch.int32, "prefix_pages")
+        if prefix_pages.numel() * page < prefix_len:
             raise WQError(f"prefix_len {prefix_len} needs more pages than prefix_pages holds")
     if cu_q is not None:
-        _shape(_dev(cu_q, torch.int32, "cu_q"), (B + 1,), "cu_q")
+        _dense_as(cu_q, (B + 1,), torch.int32, "cu_q")
         if max_q is None:
             raise WQError("cu_q needs max_q, the most tokens of a sequence")
     elif B == 0 or T % B:
         raise WQError(f"{T} tokens do not split evenly over {B} sequences: give cu_q")
     else:
         max_q = T // B
-    out = torch.empty(T, Hq, c.dv, dtype=q.dtype, device=q.device) if out is None else \
-        _shape(_view(out, 3, dt, "out"), (T, Hq, c.dv), "out")
+    if out is None:
+        out = torch.empty(T, Hq, dv, dtype=dt, device=q.device)
+    so = _view(out, (T, Hq, dv), dt, "out")
     if lse is not None:
-        _shape(_dev(lse, torch.float32, "lse"), (T, Hq), "lse")
+        _dense_as(lse, (T, Hq), torch.float32, "lse")
     if ws is None:
         ws = attention_shared_prefix_workspace(q, k_cache, v_cache, B, prefix_len, max_suffix, max_q)
     _check(lib().wq_attention_shared_prefix(
-        *_strides(q), T, B, _ptr(cu_q), max_q, Hq, c, _ptr(prefix_pages), prefix_len,
-        _ptr(page_table), page_table.stride(0), _ptr(suffix_len), max_suffix,
-        dk ** -0.5 if scale is None else scale, _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
-        _ptr(ws), ws.numel(), _ptr(status), _stream()), "wq_attention_shared_prefix")
+        q.data_ptr(), sq[0], sq[1], T, B, _at(cu_q), max_q, Hq, c, _at(prefix_pages), prefix_len,
+        page_table.data_ptr(), ld, suffix_len.data_ptr(), max_suffix,
+        dk ** -0.5 if scale is None else scale, out.data_ptr(), so[0], so[1], _at(lse), ws.data_ptr(),
+        ws.numel(), _at(status), _raw_stream(q)), "wq_attention_shared_prefix")
     return out
