@@ -81,6 +81,14 @@ def test_block_norm_pitches_and_missing_parts(H):
     norm_check(got, keep, BF, 1.0, "rms", "rms")
 
 
+@pytest.mark.parametrize("T,H,dtype", [(5, 99, BF), (7, 4099, FP), (3, 1001, F32)])
+def test_block_norm_rows_that_start_apart(T, H, dtype):
+    """Tensors whose rows lie differently against 16-byte boundaries."""
+    i = norm_inputs(T, H, dtype, "layer", "rms", "token")
+    i["residual"] = randn(T, H + 3, dtype=dtype, seed=8)[:, 1:1 + H]
+    norm_check(wq.block_norm(post="layer", pre="rms", eps=EPS, **i), i, dtype, 1.0, "layer", "rms")
+
+
 def test_block_norm_zero_and_nonfinite_rows_stay_apart():
     i = norm_inputs(4, 512, BF, "rms", "rms", "none")
     i["block"][1] = 0

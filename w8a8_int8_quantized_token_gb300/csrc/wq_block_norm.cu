@@ -39,7 +39,7 @@ struct Row {
   using Raw = typename DT::Raw;
   using V = Vec<DT, VW>;
   static constexpr int kPieces = NV;
-  static constexpr int NP = VW > 1 ? VW / 2 : 1;  // pairs of a piece (a single element: with a 0)
+  static constexpr int NP = VW / 2;  // pairs of a piece
   Pair v[NV][NP];
   int i0, step, H;
 
@@ -49,17 +49,13 @@ struct Row {
   }
   __device__ __forceinline__ bool whole(int k) const { return at(k) >= 0 && at(k) + VW <= H; }
   __device__ __forceinline__ bool has(int k, int e) const {
-    return SHIFT ? unsigned(at(k) + e) < unsigned(H) : e < VW && in(k);
+    return SHIFT ? unsigned(at(k) + e) < unsigned(H) : in(k);
   }
   static __device__ __forceinline__ void pairs(const V &x, Pair (&p)[NP]) {
     float f[VW];
     x.get(f);
-    if constexpr (VW > 1) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
-    } else {
-      p[0] = pair(f[0], 0.0f);
-    }
+    for (int i = 0; i < NP; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
   }
   __device__ __forceinline__ V each(const Raw *p, int k) const {
     uint32_t w[4];
@@ -93,25 +89,21 @@ struct Row {
     else return each(p, k);
   }
   __device__ __forceinline__ void store(Raw *p, int k) const {
-    float f[VW > 1 ? VW : 2];
+    float f[VW];
 #pragma unroll
     for (int i = 0; i < NP; ++i) split(v[k][i], f[2 * i], f[2 * i + 1]);
-    if constexpr (VW == 1) {
-      p[at(k)] = DT::from_f(f[0]);
-    } else {
-      if (!SHIFT || whole(k)) {
-        V x;
-        x.set(f);
-        x.store(p + at(k));
-      } else if constexpr (SHIFT) {
+    if (!SHIFT || whole(k)) {
+      V x;
+      x.set(f);
+      x.store(p + at(k));
+    } else if constexpr (SHIFT) {
 #pragma unroll
-        for (int e = 0; e < VW; ++e)
-          if (has(k, e)) p[at(k) + e] = DT::from_f(f[e]);
-      }
+      for (int e = 0; e < VW; ++e)
+        if (has(k, e)) p[at(k) + e] = DT::from_f(f[e]);
     }
   }
   __device__ __forceinline__ void clear_past(int k) {  // 0 outside the row
-    if (VW > 1 && (SHIFT ? whole(k) : in(k))) return;
+    if (SHIFT ? whole(k) : in(k)) return;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       if (!has(k, 2 * i) || !has(k, 2 * i + 1)) {
@@ -236,7 +228,7 @@ __device__ __forceinline__ void copy16(void *dst, const void *src) {
 // Threads of a block at most, and blocks that share an SM at least: the rows
 // in flight hide the reductions of each.
 template <int NV, bool WARP>
-constexpr int max_threads() { return WARP ? 128 : (NV == 1 ? 1024 : (NV <= 4 ? 288 : 544)); }
+constexpr int max_threads() { return WARP ? 128 : (NV == 1 ? 1024 : (NV <= 4 ? 288 : 512)); }
 template <int NV, bool WARP>
 constexpr int min_blocks() { return WARP ? 6 : (NV == 1 ? 1 : (NV <= 4 ? 3 : 1)); }
 
@@ -355,6 +347,75 @@ __global__ void __launch_bounds__(256, 3) block_norm_stream_kernel(const BlockNo
   }
 }
 
+// Any width and alignment: the row as floats in shared memory, an element at a
+// time.  Very wide rows, and tensors whose rows do not start alike against
+// 16-byte boundaries.
+template <class DT>
+struct AnyRow {
+  using Raw = typename DT::Raw;
+  float *v;
+  int H;
+
+  __device__ __forceinline__ void norm(int kind, const void *weight, const void *bias, float eps,
+                                       float (*red)[32]) {
+    if (kind == WQ_NORM_NONE) return;
+    const bool layer = kind == WQ_NORM_LAYER;
+    const auto *w = static_cast<const Raw *>(weight);
+    const auto *c = static_cast<const Raw *>(layer ? bias : nullptr);
+    const float over_h = __frcp_rn(float(H));
+    float m = 0.0f, s = 0.0f;
+    if (layer) {
+      for (int i = threadIdx.x; i < H; i += blockDim.x) s += v[i];
+      m = row_sum<false>(s, red[0]) * over_h;
+      s = 0.0f;
+    }
+    for (int i = threadIdx.x; i < H; i += blockDim.x) {
+      v[i] -= m;
+      s = __fmaf_rn(v[i], v[i], s);
+    }
+    const float r = rsqrtf(__fmaf_rn(row_sum<false>(s, red[1]), over_h, eps));
+    for (int i = threadIdx.x; i < H; i += blockDim.x)
+      v[i] = __fmaf_rn(v[i] * r, w ? DT::to_f(w[i]) : 1.0f, c ? DT::to_f(c[i]) : 0.0f);
+  }
+  __device__ __forceinline__ void store(Raw *p) const {
+    for (int i = threadIdx.x; i < H; i += blockDim.x) p[i] = DT::from_f(v[i]);
+  }
+};
+template <class DT>
+__global__ void __launch_bounds__(512) block_norm_any_kernel(const BlockNormArgs a) {
+  using Raw = typename DT::Raw;
+  __shared__ float red[4][32];
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int64_t t = blockIdx.x;
+  const Raw *bp = static_cast<const Raw *>(a.block) + t * a.ldb;
+  const Raw *rp = static_cast<const Raw *>(a.residual) + t * a.ldr;
+  const Raw *gp = static_cast<const Raw *>(a.gate) + t * a.ldg;
+  // a thread works on its own elements of the row throughout
+  AnyRow<DT> row{reinterpret_cast<float *>(smem), a.H};
+  for (int i = threadIdx.x; i < a.H; i += blockDim.x) row.v[i] = DT::to_f(bp[i]);
+  row.norm(a.post, a.w_post, a.b_post, a.eps, red);
+  for (int i = threadIdx.x; i < a.H; i += blockDim.x) {
+    float x = row.v[i];
+    if (a.gate) x *= DT::to_f(gp[i]);
+    row.v[i] = __fmaf_rn(x, a.scale, a.residual ? DT::to_f(rp[i]) : 0.0f);
+  }
+  if (a.x_out) row.store(static_cast<Raw *>(a.x_out) + t * a.ldx);
+  if (!a.y) return;
+  row.norm(a.pre, a.w_pre, a.b_pre, a.eps, red + 2);
+  row.store(static_cast<Raw *>(a.y) + t * a.ldy);
+}
+
+template <class DT>
+int launch_any(const BlockNormArgs &a, cudaStream_t st) {
+  auto *k = block_norm_any_kernel<DT>;
+  static bool sized =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 * 4) == cudaSuccess;
+  if (!sized) return WQ_ERR_LAUNCH;
+  const int threads = std::min(512, (a.H + 31) / 32 * 32);
+  k<<<unsigned(a.T), threads, a.H * 4, st>>>(a);
+  return launched(1);
+}
+
 template <class DT, int VW, int NV, bool WARP, bool SHIFT>
 int launch_one(const BlockNormArgs &a, int threads, cudaStream_t st) {
   const int64_t blocks = WARP ? (a.T + threads / 32 - 1) / (threads / 32) : a.T;
@@ -386,8 +447,9 @@ int launch_stream(const BlockNormArgs &a, int pieces, cudaStream_t st) {
                 : launch_stream_g<DT, NV, false, false>(a, pieces, st);
 }
 
-template <class DT, int VW, bool SHIFT>
+template <class DT, bool SHIFT>
 int launch_t(const BlockNormArgs &a, cudaStream_t st) {
+  constexpr int VW = DT::kVec;
   const int pieces = (a.H + VW - 1) / VW + (SHIFT ? 1 : 0);
   if (pieces <= 32) return launch_one<DT, VW, 1, true, SHIFT>(a, 128, st);
   if (pieces <= 64) return launch_one<DT, VW, 2, true, SHIFT>(a, 128, st);
@@ -395,18 +457,16 @@ int launch_t(const BlockNormArgs &a, cudaStream_t st) {
   // pieces a thread, and where rows are whole pieces the next row under way.
   if (a.T <= 2 * 152 && pieces <= 1024)
     return launch_one<DT, VW, 1, false, SHIFT>(a, threads_for(pieces, 1), st);
-  if constexpr (!SHIFT && VW > 1) {
+  if constexpr (!SHIFT) {
     if (a.T > 6 * 152 && pieces <= 4 * 256)
       return pieces <= 2 * 256 ? launch_stream<DT, 2>(a, pieces, st) : launch_stream<DT, 4>(a, pieces, st);
   }
   if (pieces <= 2 * 288) return launch_one<DT, VW, 2, false, SHIFT>(a, threads_for(pieces, 2), st);
   if (pieces <= 4 * 288) return launch_one<DT, VW, 4, false, SHIFT>(a, threads_for(pieces, 4), st);
-  if (pieces <= 8 * 512) return launch_one<DT, VW, 8, false, SHIFT>(a, threads_for(pieces, 8), st);
-  if constexpr (SHIFT || VW < 8) {
-    if (pieces <= 16 * 544) return launch_one<DT, VW, 16, false, SHIFT>(a, threads_for(pieces, 16), st);
+  if constexpr (!SHIFT) {
+    if (pieces <= 8 * 512) return launch_one<DT, VW, 8, false, SHIFT>(a, threads_for(pieces, 8), st);
   }
-  if constexpr (VW == 1) return launch_one<DT, VW, 64, false, SHIFT>(a, threads_for(pieces, 64), st);
-  return WQ_ERR_UNSUPPORTED;
+  return launch_any<DT>(a, st);
 }
 
 // How a row is reached: pieces of 16 bytes; such pieces with every row's start
@@ -414,9 +474,9 @@ int launch_t(const BlockNormArgs &a, cudaStream_t st) {
 template <class DT>
 int launch_dt(const BlockNormArgs &a, cudaStream_t st) {
   switch (a.reach) {
-    case 0: return launch_t<DT, DT::kVec, false>(a, st);
-    case 1: return launch_t<DT, DT::kVec, true>(a, st);
-    default: return launch_t<DT, 1, false>(a, st);
+    case 0: return launch_t<DT, false>(a, st);
+    case 1: return launch_t<DT, true>(a, st);
+    default: return launch_any<DT>(a, st);
   }
 }
 
