@@ -137,21 +137,25 @@ def attention(q, k_cache, v_cache, prefix_pages, P, page_table, suffix_len, cu_q
         for b in range(len(sl)):
             n = cu[b + 1] - cu[b]
             ks, vs = keys_of(kc, pt[b], sl[b], h), keys_of(vc, pt[b], sl[b], h)
-            for j in range(n):
-                seen = max(0, sl[b] - n + j + 1)
-                k, v = torch.cat([kp, ks[:seen]]), torch.cat([vp, vs[:seen]])
-                t = cu[b] + j
-                if not len(k):
-                    continue
-                for a in range(h * G, (h + 1) * G):
-                    x = k @ f64(q[t, a]) * scale
-                    mag = float((k.abs() @ f64(q[t, a]).abs()).max()) * scale
-                    p = torch.softmax(x, 0)
-                    e = dk * E * mag + 2.0 ** -22 + 4 * E * float(x.abs().max()) + len(k) * E
-                    out[t, a] = p @ v
-                    lse[t, a] = torch.logsumexp(x, 0)
-                    spread = p @ v.abs()
-                    under = len(k) * TINY[dtype] * v.abs().amax(0)  # weights below dtype's normal range
-                    tol[t, a] = u * (out[t, a].abs() + spread) + 4 * e * spread + under + TINY[dtype]
-                    ltol[t, a] = 2 * e + 4 * E * (1 + lse[t, a].abs())
+            k, v = torch.cat([kp, ks]), torch.cat([vp, vs])
+            if n == 0 or not len(k):
+                continue
+            rows, heads = slice(cu[b], cu[b] + n), slice(h * G, (h + 1) * G)
+            qf = f64(q[rows, heads])  # [n, G, dk]
+            last = P - 1 + (sl[b] - n + 1 + torch.arange(n)).clamp(min=0)
+            seen = (torch.arange(len(k)) <= last[:, None])[:, None, :]  # [n, 1, keys]
+            count = seen.sum(-1).double()  # [n, 1]
+            x = (qf @ k.T * scale).masked_fill(~seen, -math.inf)
+            mag = (qf.abs() @ k.abs().T * scale).masked_fill(~seen, 0).amax(-1)  # [n, G]
+            some = (count > 0).expand(n, G)
+            p = torch.where(some[..., None], torch.softmax(x, -1), torch.zeros_like(x))
+            e = dk * E * mag + 2.0 ** -22 + 4 * E * x.masked_fill(~seen, 0).abs().amax(-1) + count * E
+            o, spread = p @ v, p @ v.abs()
+            under = count[..., None] * TINY[dtype] * v.abs().amax(0)  # weights below dtype's normal range
+            out[rows, heads] = o
+            tol[rows, heads] = torch.where(some[..., None], u * (o.abs() + spread) + 4 * e[..., None] * spread +
+                                           under + TINY[dtype], torch.zeros_like(o))
+            z = torch.logsumexp(x, -1)
+            lse[rows, heads] = z
+            ltol[rows, heads] = torch.where(some, 2 * e + 4 * E * (1 + z.abs()), torch.zeros_like(z))
     return out, lse, tol, ltol

@@ -298,6 +298,28 @@ def test_attention(ql, sl, P, Hkv, G, dk, dv, page, dtype, token_major):
     assert torch.equal(attn_call(i, P, max(sl), max(ql)), out)
 
 
+# enough row tiles for every SM: prefix and suffix in one walk, with tails at
+# the end of either, of both and of none, and sequences that see the prefix alone
+WALKS = [([200, 250, 170], [200, 300, 171], 333, 4, 16, 128, 16, BF), ([90, 1, 400], [90, 7, 650], 130, 8, 8, 64, 32, FP),
+         ([300, 300], [384, 512], 256, 4, 16, 64, 16, BF), ([310, 300], [310, 0], 100, 4, 16, 128, 64, FP)]
+
+
+@pytest.mark.parametrize("ql,sl,P,Hkv,G,D,page,dtype", WALKS)
+def test_attention_walks_prefix_and_suffix(ql, sl, P, Hkv, G, D, page, dtype):
+    i = attn_inputs(ql, sl, P, Hkv, G, D, D, page, dtype, False)
+    lse = torch.full((sum(ql), Hkv * G), 7.0, device="cuda")
+    st = wq.new_status()
+    out = attn_call(i, P, max(sl), max(ql), lse=lse, status=st)
+    want, wl, tol, ltol = R.attention(i["q"], i["k_cache"], i["v_cache"], i["prefix_pages"], P, i["page_table"],
+                                      i["suffix_len"], i["cu_q"], D ** -0.5, dtype)
+    R.check(out, want, tol, "out")
+    R.check(lse, wl, ltol, "lse")
+    for _ in range(100):  # the same bits whatever the timing, and no wait that ran out
+        again = attn_call(i, P, max(sl), max(ql), status=st)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out) and int(st) == 0
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("ql,sl,P", [([1, 1], [50, 90], 130), ([100, 60], [100, 90], 130)])
 def test_attention_extreme_scores(dtype, ql, sl, P):

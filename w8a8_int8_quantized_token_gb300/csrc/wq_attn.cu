@@ -448,54 +448,48 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
   wait_last_kernel();
 }
 
-// A warp joins one row's partial results, 32 at a time: a lane finds one
-// part's weight, and four parts' rows are in flight together.
-template <class DT>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+// Joins the partial results of a row: LANES threads, four columns each, walk
+// its parts, four parts' columns in flight together.  Every thread finds the
+// parts' weights itself (the statistics of a row are a few words of one line).
+template <class DT, int LANES>
+__global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
+  const int64_t row = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
+  const int d = int(threadIdx.x) % LANES * 4;
   wait_last_kernel();
-  if (row >= int64_t(a.T) * a.Hq) return;
+  if (row >= int64_t(a.T) * a.Hq || d >= a.dv) return;
   const float *lp = a.lse_part + row * a.slots;
-  const int d = min(lane * 4, a.dv - 4);
   const float *op = a.o_part + row * a.slots * a.dv + d;
   float mx = -INFINITY;
-  for (int s = lane; s < a.slots; s += 32) mx = fmaxf(mx, lp[s]);
-  mx = warp_max(mx);
-  const int64_t t = row / a.Hq, qh = row - t * a.Hq;
+#pragma unroll 4
+  for (int s = 0; s < a.slots; ++s) mx = fmaxf(mx, lp[s]);
   const float base = mx == -INFINITY ? 0.0f : mx;
   float sum = 0.0f, x[4] = {};
-  for (int s0 = 0; s0 < a.slots; s0 += 32) {
-    const float mine = s0 + lane < a.slots ? __expf(lp[s0 + lane] - base) : 0.0f;
-    sum += warp_sum(mine);
-    const int n = min(32, a.slots - s0);
-    for (int i = 0; i < n; i += 4) {
-      float w[4];
-      float4 v[4];
+  for (int s0 = 0; s0 < a.slots; s0 += 4) {
+    float w[4];
+    float4 v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        w[k] = __shfl_sync(0xffffffffu, mine, (i + k) & 31);
-        if (i + k >= n) w[k] = 0.0f;
-        // an empty part (weight zero) holds nothing that may be read
-        v[k] = w[k] != 0.0f ? *reinterpret_cast<const float4 *>(op + int64_t(s0 + i + k) * a.dv)
-                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int s = s0 + k;
+      w[k] = s < a.slots ? __expf(lp[s] - base) : 0.0f;
+      // an empty part (weight zero) holds nothing that may be read
+      v[k] = w[k] != 0.0f ? *reinterpret_cast<const float4 *>(op + int64_t(s) * a.dv)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[0] = __fmaf_rn(v[k].x, w[k], x[0]);
-        x[1] = __fmaf_rn(v[k].y, w[k], x[1]);
-        x[2] = __fmaf_rn(v[k].z, w[k], x[2]);
-        x[3] = __fmaf_rn(v[k].w, w[k], x[3]);
-      }
+    for (int k = 0; k < 4; ++k) {
+      sum += w[k];
+      x[0] = __fmaf_rn(v[k].x, w[k], x[0]);
+      x[1] = __fmaf_rn(v[k].y, w[k], x[1]);
+      x[2] = __fmaf_rn(v[k].z, w[k], x[2]);
+      x[3] = __fmaf_rn(v[k].w, w[k], x[3]);
     }
   }
   const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
-  if (lane * 4 < a.dv) {
-    uint32_t *o = reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head + d);
-    o[0] = pack2<DT>(x[0] * inv, x[1] * inv);
-    o[1] = pack2<DT>(x[2] * inv, x[3] * inv);
-  }
-  if (lane == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : base + logf(sum);
+  const int64_t t = row / a.Hq, qh = row - t * a.Hq;
+  uint32_t *o = reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head + d);
+  o[0] = pack2<DT>(x[0] * inv, x[1] * inv);
+  o[1] = pack2<DT>(x[2] * inv, x[3] * inv);
+  if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : base + logf(sum);
 }
 
 template <class DT, int D, int MT, int NW, bool PAGED>
@@ -507,7 +501,7 @@ int launch_small(const AttnArgs &a, cudaStream_t st) {
   if (!sized) return WQ_ERR_LAUNCH;
   constexpr int R = 16 * MT;
   const int64_t pt = (int64_t(a.T) * a.G + R - 1) / R, stl = (int64_t(a.max_q) * a.G + R - 1) / R;
-  const int64_t pi = a.tc_prefix ? 0 : a.sp * pt * a.Hkv;
+  const int64_t pi = a.tc_prefix || a.whole ? 0 : a.sp * pt * a.Hkv;
   const int64_t si = a.tc_suffix ? 0 : a.ss * stl * a.Hkv * a.B;
   if (pi + si == 0) return WQ_OK;
   if (pi + si >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
@@ -530,7 +524,8 @@ int launch_t(const AttnArgs &a, cudaStream_t st) {
   else rc = two ? launch_warps<DT, 64, 2>(a, st) : launch_warps<DT, 64, 1>(a, st);
   if (rc != WQ_OK || !a.o_part) return rc;
   const int64_t rows = int64_t(a.T) * a.Hq;
-  return launch_chained(attn_join_kernel<DT>, unsigned((rows + 3) / 4), 128, 0, true, st, a);
+  return a.dv <= 64 ? launch_chained(attn_join_kernel<DT, 16>, unsigned((rows + 15) / 16), 256, 0, true, st, a)
+                    : launch_chained(attn_join_kernel<DT, 32>, unsigned((rows + 7) / 8), 256, 0, true, st, a);
 }
 
 }  // namespace
@@ -571,6 +566,14 @@ void plan_attention(AttnArgs &a) {
     cut((a.max_q + pair - 1) / pair * a.Hkv * a.B, a.max_suffix, 152, 256, 128, a.ss, a.s_chunk);
   } else {
     cut(items_s, a.max_suffix, want, least, grain, a.ss, a.s_chunk);
+  }
+  // Enough row tiles for every SM: one walk over the prefix and the suffix of
+  // a sequence's rows, with no partial results to join.
+  const int64_t flat = (a.T + 2 * (128 / a.G) - 1) / (2 * (128 / a.G)) * a.Hkv;
+  a.whole = a.tc_prefix && a.tc_suffix && a.ss == 1 && flat >= 152;
+  if (a.whole) {
+    a.tc_prefix = false;
+    a.sp = 0;
   }
   if (a.sp + a.ss == 0) a.ss = 1;  // no keys at all: one empty range writes the zeros
   a.slots = a.sp + a.ss;

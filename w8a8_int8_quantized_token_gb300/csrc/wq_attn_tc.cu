@@ -32,7 +32,7 @@
 // unwritten places), and 0 * NaN is NaN: the last tile's tail is cleared in
 // shared memory before its product.
 //
-// Every wait is bounded (about 1 s); on expiry the kernel records WQ_ERR_TIMEOUT,
+// Every wait is bounded (1 s); on expiry the kernel records WQ_ERR_TIMEOUT,
 // waits (bounded) for its own copies and MMAs, frees tensor memory and exits.
 #include <algorithm>
 #include <type_traits>
@@ -69,8 +69,8 @@ struct Plan {
                        B_S = B_Q_EMPTY + 1,      // [2] scores of a row tile are in
       B_P = B_S + 2,                             // [2][2] half a tile of weights is in
       B_O = B_P + 4,                             // [2] a piece's last value product is done
-      B_TAIL = B_O + 2,                          // a last value tile's tail is cleared
-      B_DONE = B_TAIL + 1, NBAR = B_DONE + 2;
+      B_TAIL = B_O + 2,                          // [2] in turn: a last value tile's tail is cleared
+      B_DONE = B_TAIL + 2, NBAR = B_DONE + 2;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
@@ -79,19 +79,21 @@ struct Plan {
   static_assert(2 * BN + 2 * D <= 512, "tensor memory plan");
 };
 
-// Bounded wait of one thread.  A try suspends the thread for about 4 us by
-// itself (7800 cycles measured) before it gives up, so 2^18 of them are about
-// a second, and no clock is read.  A warp waits through one lane: the products
-// read their operands from shared memory at its full rate, and 32 lanes that
-// poll a barrier take that rate from them.
-constexpr int kTries = 1 << 18;
+// Bounded wait of one thread (1 s).  A try may suspend the thread by itself, so
+// the clock and the abort flag are looked at every 1024 tries only.  A warp of
+// the softmax waits through one lane: the products read their operands from
+// shared memory at its full rate, and 32 lanes that poll a barrier take that
+// rate from them.
 __device__ __forceinline__ bool wait_one(uint32_t b, uint32_t parity, volatile int *abort_flag) {
+  uint64_t t0 = 0;
+  while (true) {
 #pragma unroll 1
-  for (int i = 0; i < kTries; ++i) {
-    if (mbar_try(b, parity)) return true;
-    if (*abort_flag) return false;
+    for (int i = 0; i < 1024; ++i)
+      if (mbar_try(b, parity)) return true;
+    const uint64_t now = gtime();
+    if (t0 == 0) t0 = now;
+    if (*abort_flag || now - t0 > kTimeoutNs) return false;
   }
-  return false;
 }
 // One lane of the (converged) warp
 __device__ __forceinline__ bool elect_one() {
@@ -209,7 +211,8 @@ struct Piece {
   Source s;
   int head, tok0;     // key head; first token (of the source) of row tile 0
   int k0, k1;         // keys
-  int slot, last;     // partial-result slot; slots (slot, last) stay empty
+    int slot, last;     // partial-result slot; slots (slot, last) stay empty
+  bool open, close;   // the rows' sums begin, end with this piece
 };
 
 // units u0 .. u1 of one item, for member `member` of gang `gang`
@@ -223,7 +226,8 @@ __device__ __forceinline__ Piece prefix_piece(const AttnArgs &a, const Cut &c, i
   p.k0 = (u0 - start) * BN;
   p.k1 = u1 - start >= c.units_p ? a.P : (u1 - start) * BN;
   p.slot = gang - start / c.stretch;  // ordinal of this gang among those that share the item
-  p.last = p.k1 == a.P ? a.sp : p.slot + 1;
+    p.last = p.k1 == a.P ? a.sp : p.slot + 1;
+  p.open = p.close = true;
   return p;
 }
 
@@ -240,7 +244,8 @@ __device__ __forceinline__ Piece suffix_piece(const AttnArgs &a, const Cut &c, i
   const int lastj = min(p.s.n, p.tok0 + 2 * c.tpt) - 1;
   p.k1 = min(min(p.s.len, visible(p.s, lastj)), p.k0 + a.s_chunk);
   p.slot = p.s.slot0 + split;
-  p.last = p.slot + 1;
+    p.last = p.slot + 1;
+  p.open = p.close = true;
   return p;
 }
 
@@ -287,7 +292,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int u_end = line ? min(u_begin + c.stretch, a.Hkv * c.groups * c.units_p) : 1;
   // calls f(piece, key tiles, row tiles in use); stops when f returns false
   auto pieces = [&](auto &&f) {
-    for (int u = u_begin; u < u_end;) {
+    auto take = [&](const Piece &p) {
+      const int n = p.k1 > p.k0 ? (p.k1 - p.k0 + BN - 1) / BN : 0;
+      return f(p, n, p.tok0 + c.tpt < p.s.n ? 2 : 1);
+    };
+    for (int u = u_begin, part = 0; u < u_end;) {
       Piece p;
       if (line) {
         const int stop = min((u / c.units_p + 1) * c.units_p, u_end);
@@ -295,11 +304,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         u = stop;
       } else {
         p = suffix_piece(a, c, int64_t(blockIdx.x) - int64_t(c.gang) * c.gangs);
-        u = u_end;
+        if (a.whole && a.P > 0) {  // the prefix, then the suffix, under the same sums
+          p.open = part == 0;
+          if (part == 0) {
+            part = p.k1 > p.k0 ? 1 : 2;
+            p.close = part == 2;
+            p.s.pages = a.prefix_pages;
+            p.s.len = p.k1 = a.P;
+            p.s.causal = false;
+          } else {
+            part = 2;
+          }
+        }
+        if (!a.whole || a.P == 0 || part == 2) u = u_end;
       }
       if (p.tok0 >= p.s.n) continue;  // a gang's last group, a short sequence
-      const int n = p.k1 > p.k0 ? (p.k1 - p.k0 + BN - 1) / BN : 0;
-      if (!f(p, n, p.tok0 + c.tpt < p.s.n ? 2 : 1)) return;
+      if (!take(p)) return;
     }
   };
 
@@ -309,13 +329,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // ------------------------------------------------------------ copies
       int s = 0, g = 0, q = 0;  // ring stage; stages issued; pieces with keys
       uint32_t ph = 1;          // parity of the ring's releases
+            int tails = 0;            // cleared tails
       bool bad = false;         // a page id outside the cache
       const int nbox = BN / c.box;
       const bool leader = elect_one();
       pieces([&](const Piece &p, int n, int tiles) {
         if (n == 0) return true;
-        if (!(ok = wait_warp(bar(P::B_Q_EMPTY), (q & 1) ^ 1, abort_flag))) return false;
-        if (leader) {
+                if (p.open && !(ok = wait_warp(bar(P::B_Q_EMPTY), (q & 1) ^ 1, abort_flag))) return false;
+        if (leader && p.open) {
           mbar_expect_tx(bar(P::B_Q_FULL), uint32_t(tiles * P::CH * c.tpt * a.G * 128));
 #pragma unroll 1
           for (int t = 0; t < tiles; ++t)
@@ -323,7 +344,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               tma_load_3d(base + P::OFF_Q + t * P::QB + ch * BM * 128, &tmQ, ch * 64, p.head * a.G,
                           p.s.t0 + p.tok0 + t * c.tpt, bar(P::B_Q_FULL));
         }
-        ++q;
+                q += p.open;
         // lane b looks up box b of a tile, one tile ahead of its copies; a bad
         // page is read outside the tensor: zeros
         const int key0 = p.k0 + lane * c.box;
@@ -379,7 +400,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(P::B_TAIL));
+          // Two barriers in turn: the prefix's tail and the suffix's may both be
+          // ahead of the products, and a barrier holds one phase
+          if (lane == 0) mbar_arrive(bar(P::B_TAIL + (tails & 1)));
+          ++tails;
         }
         return true;
       });
@@ -436,15 +460,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (n == 0) return true;
         const bool tail = (p.k1 - p.k0) % BN != 0;
         if (t >= tiles) {  // no rows here: step over the piece's stages
-          for (int i = 0; i < 2 * n; ++i) next();
-          ++q;
+                    for (int i = 0; i < 2 * n; ++i) next();
+          q += p.open;
           tails += tail;
           return true;
         }
         if (t == 1) pass(tiles);  // row tile 0 begins
-        wait(P::B_Q_FULL, q & 1);
+                if (p.open) {
+          wait(P::B_Q_FULL, q & 1);
+          ++q;
+        }
         wait(P::B_FULL + s, ph);
-        ++q;
         turn(tiles);
         tc_fence_after();
         if (leader && ok) {
@@ -462,7 +488,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (more) {
             wait(P::B_FULL + s, ph);
           } else if (tail) {
-            wait(P::B_TAIL, tails & 1);
+            wait(P::B_TAIL + (tails & 1), (tails >> 1) & 1);
             ++tails;
           }
           const uint64_t dv = sdesc_n(base + P::OFF_KV + uint32_t(sv * P::KVB));
@@ -472,7 +498,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (leader && ok) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_f16_ts(to, ts + 8 * k, dv + ((2048 * k) >> 4), id_o, (j | k) ? 1u : 0u);
+              mma_f16_ts(to, ts + 8 * k, dv + ((2048 * k) >> 4), id_o, j | k || !p.open ? 1u : 0u);
           }
           wait(P::B_P + 2 * t + 1, pp);
           pp ^= 1;
@@ -481,11 +507,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int k = 4; k < 8; ++k)
               mma_f16_ts(to, ts + 8 * k, dv + ((2048 * k) >> 4), id_o, 1u);
-            if (more) {
-              scores(s);
-            } else {
-              mma_commit(bar(P::B_O + t));
-            }
+                        if (more) scores(s);
+            else if (p.close) mma_commit(bar(P::B_O + t));
           }
           // the last turn of row tile 1 is nobody's to wait for
           if (t == 0 || more) pass(tiles);
@@ -509,7 +532,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float sl2 = a.scale_log2;
     int done = 0;  // key tiles so far
         int q = 0;     // pieces with keys so far
-    int mine_pieces = 0;  // of them with this row tile
+        int ends = 0;  // results of this row tile so far
+    float m = -INFINITY, l = 0.0f;
     pieces([&](const Piece &p, int n, int tiles) {
       // the queries of a piece are released by the eight softmax warps: their
       // tiles serve as staging for the piece's results
@@ -519,8 +543,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P::B_Q_EMPTY));
       };
-      if (n > 0) ++q;
+            if (n > 0) q += p.open;
       if (t >= tiles) {
+        if (!p.close) return true;
         // not before the piece's queries are in: its release must not count
         // for the piece before
         if (n > 0 && !(ok = wait_warp(bar(P::B_Q_FULL), (q - 1) & 1, abort_flag))) return false;
@@ -530,7 +555,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int tok = row / a.G, j0 = p.tok0 + t * c.tpt + tok;
       const bool mine = tok < c.tpt && j0 < p.s.n;
       const int lim = mine ? min(p.k1, visible(p.s, j0)) : 0;
-      float m = -INFINITY, l = 0.0f;
+            if (p.open) {
+        m = -INFINITY;
+        l = 0.0f;
+      }
       for (int j = 0; j < n; ++j, ++done) {
         const int kb = p.k0 + j * BN;
         if (!(ok = wait_warp(bar(P::B_S + t), done & 1, abort_flag))) return false;
@@ -592,7 +620,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (grow) m = top;
           l *= f;
           // these scores are in, so the value product of the tile before is too
-          if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+          if ((j > 0 || !p.open) && __any_sync(0xffffffffu, f != 1.0f)) {
 #pragma unroll 1
             for (int i = 0; i < D / 16; ++i) {
               uint32_t o[16];
@@ -615,9 +643,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         weigh(1, neg);
         hand_over(1);
       }
+            if (!p.close) return true;
       // ---- the row's result
-            if (n > 0) {
-        if (!(ok = wait_warp(bar(P::B_O + t), uint32_t(mine_pieces++ & 1), abort_flag))) return false;
+      if (n > 0) {
+        if (!(ok = wait_warp(bar(P::B_O + t), uint32_t(ends++ & 1), abort_flag))) return false;
         tc_fence_after();
       }
       const bool none = l == 0.0f;
