@@ -116,8 +116,9 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
   }
   const Source s = source_of(a, seq);
   const int rows = min(R, s.n * a.G - tile * R);  // rows of this tile
+  const bool last_block = blockIdx.x == gridDim.x - 1;
   if (rows <= 0) {
-    wait_last_kernel();
+    if (last_block) wait_last_kernel();
     return;
   }
   const int row0 = tile * R;
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
             *reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head + d) = pack2<DT>(x, y);
         }
       }
-    wait_last_kernel();  // the join waits for this kernel alone
+    if (last_block) wait_last_kernel();
     return;
   }
   __syncthreads();  // the ring becomes the exchange of the warps' results
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
       else if (a.lse) a.lse[t * a.Hq + qh] = lse;
     }
   }
-  wait_last_kernel();
+  if (last_block) wait_last_kernel();
 }
 
 // Joins the partial results of a row: LANES threads, four columns each, walk
@@ -539,8 +540,24 @@ void plan_attention(AttnArgs &a) {
                        (a.v_head || a.Hkv == 1) && (a.v_page || a.num_pages <= 1);
   const bool tiles = a.page_size % 8 == 0 && a.num_pages > 0 && pitches;
   const int64_t rows_p = int64_t(a.T) * a.G, rows_s = int64_t(a.max_q) * a.G;
-  a.tc_prefix = tiles && a.P > 0 && rows_p > 32 && plan_prefix_tiles(a);
   a.tc_suffix = tiles && a.max_suffix > 0 && rows_s > 32;
+  // The prefix's products and the reading of short suffixes bind different
+  // parts of the machine but do not fit one SM together.  So the prefix gets
+  // only as many SMs as let the suffixes be read beside it: about 8 us and
+  // 1.6 us a unit on each; suffixes (half their bound) at 6 TB/s, which takes
+  // about 60 SMs.
+  int sms = 152;
+  if (a.max_suffix > 0 && !a.tc_suffix) {
+    const int64_t pair = 2 * (128 / a.G), units = (a.T + pair - 1) / pair * a.Hkv * ((a.P + 127) / 128);
+    const double read = 3.0 + double(a.B) * a.Hkv * a.max_suffix * (a.dk + a.dv) / 6e6;
+    double best = 1e30;
+    for (int k = 152; k >= 32; k -= 8) {
+      const double products = 8.0 + 1.6 * double((units + k - 1) / k);
+      const double all = products + std::max(0.0, read - products * std::min(1.0, (152 - k) / 60.0));
+      if (all < best * 0.97) best = all, sms = k;
+    }
+  }
+  a.tc_prefix = tiles && a.P > 0 && rows_p > 32 && plan_prefix_tiles(a, sms);
   const int64_t R = rows_s > 16 ? 32 : 16;
   const int64_t items_s = (rows_s + R - 1) / R * a.Hkv * a.B;
   // one warp a block where starts and ends weigh more than an even spread: many

@@ -41,8 +41,9 @@ __device__ __forceinline__ int visible(const Source &s, int j) {
 
 // The kernels of one call follow each other closely: each lets the next one's
 // blocks take the room that its own leave (start_next_kernel, in every block),
-// and none ends before the one before it has (wait_last_kernel), so that the
-// last one may read what all of them wrote.  The first is launched in plain
+// and none ends before the one before it has (its last block waits in
+// wait_last_kernel; were all to wait, those that are done would keep others
+// from starting), so that the join may read what all of them wrote.  The first is launched in plain
 // stream order, after everything that came before the call.
 __device__ __forceinline__ void start_next_kernel() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -795,16 +795,16 @@ int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st) {
 }
 
 // Gangs of the prefix, and the most of them that meet in one item (its partial
-// results).  The gang size is the one that leaves the fewest of the 152 SMs
+// results), on `sms` SMs.  The gang size is the one that leaves the fewest of them
 // without rows; whole items per gang where their waves are full to nine
 // tenths, else equal pieces of at least two units.
-bool plan_prefix_tiles(AttnArgs &a) {
+bool plan_prefix_tiles(AttnArgs &a, int sms) {
   const int tpt = BM / a.G;
-  const int64_t sms = 152, pairs = (a.T + 2 * tpt - 1) / (2 * tpt), units = (a.P + BN - 1) / BN;
+  const int64_t pairs = (a.T + 2 * tpt - 1) / (2 * tpt), units = (a.P + BN - 1) / BN;
   double best = 0.0;
-  for (int64_t g = std::min<int64_t>(pairs, 19); g >= 1; --g) {
+  for (int64_t g = std::min<int64_t>({pairs, 19, sms}); g >= 1; --g) {
     const int64_t groups = (pairs + g - 1) / g;
-    const double use = double(sms / g * g) / double(sms) * double(pairs) / double(groups * g);
+    const double use = double(sms / g * g) / sms * double(pairs) / double(groups * g);
     if (use > best + 0.02) best = use, a.p_gang = int(g);
   }
   const int64_t items = (pairs + a.p_gang - 1) / a.p_gang * a.Hkv, total = items * units;
@@ -815,7 +815,7 @@ bool plan_prefix_tiles(AttnArgs &a) {
   a.p_stretch = int(stretch);
   a.p_gangs = int((total + stretch - 1) / stretch);
   a.sp = 1;
-  for (int64_t i = 0; stretch != units && i < items; ++i)  // fewer than 152 * waves of them
+  for (int64_t i = 0; stretch != units && i < items; ++i)  // fewer than sms * waves of them
     a.sp = std::max(a.sp, int(((i + 1) * units - 1) / stretch - i * units / stretch + 1));
   return true;
 }

@@ -192,7 +192,7 @@ struct AttnArgs {
   float *lse_part;  // [T][Hq][slots]
 };
 void plan_attention(AttnArgs &a);
-bool plan_prefix_tiles(AttnArgs &a);
+bool plan_prefix_tiles(AttnArgs &a, int sms);
 int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st);
 size_t attention_ws_bytes(const AttnArgs &a);
 int launch_attention(const AttnArgs &a, int dtype, cudaStream_t st);
