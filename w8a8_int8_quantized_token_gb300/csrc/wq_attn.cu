@@ -543,17 +543,18 @@ void plan_attention(AttnArgs &a) {
   a.tc_suffix = tiles && a.max_suffix > 0 && rows_s > 32;
   // The prefix's products and the reading of short suffixes bind different
   // parts of the machine but do not fit one SM together.  So the prefix gets
-  // only as many SMs as let the suffixes be read beside it: about 8 us and
-  // 1.6 us a unit on each; suffixes (half their bound) at 6 TB/s, which takes
-  // about 60 SMs.
+  // only as many SMs as let the suffixes be read beside it: about 10 us and
+  // 1.65 us a unit on each; suffixes (half their bound) at up to 6 TB/s, which
+  // takes about 120 SMs.  Measured with 152 and with the chosen SMs: 64
+  // sequences behind 8192 keys 68 and 56 us, 200 behind 30000 157 and 144 us.
   int sms = 152;
   if (a.max_suffix > 0 && !a.tc_suffix) {
     const int64_t pair = 2 * (128 / a.G), units = (a.T + pair - 1) / pair * a.Hkv * ((a.P + 127) / 128);
     const double read = 3.0 + double(a.B) * a.Hkv * a.max_suffix * (a.dk + a.dv) / 6e6;
     double best = 1e30;
     for (int k = 152; k >= 32; k -= 8) {
-      const double products = 8.0 + 1.6 * double((units + k - 1) / k);
-      const double all = products + std::max(0.0, read - products * std::min(1.0, (152 - k) / 60.0));
+      const double products = 10.0 + 1.65 * double((units + k - 1) / k);
+      const double all = products + std::max(0.0, read - products * std::min(1.0, (152 - k) / 120.0));
       if (all < best * 0.97) best = all, sms = k;
     }
   }

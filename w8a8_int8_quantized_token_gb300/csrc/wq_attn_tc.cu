@@ -665,6 +665,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // Rows leave through this warp's quarter of its query tile (all products
       // with it are done), so that a store covers whole rows: 16-byte pieces,
       // swizzled, NC a row.  16-bit results go in one pass, float parts in two.
+      // Loops, not unrolled: this runs once, and code that is fetched for the
+      // first time costs more than what it does (3.7 us unrolled).
       constexpr int NC = D / 8, RPI = 32 / NC;  // pieces of a staged row; rows a store covers
       uint8_t *stage = sm + P::OFF_Q + t * P::QB + (warp & 3) * 32 * (D * 2);
       const int64_t off = a.o_part ? ((tg * a.Hq + qh) * a.slots + p.slot) * a.dv
@@ -701,7 +703,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         __syncwarp();
         const int ch = lane % NC;
-#pragma unroll
+#pragma unroll 2
         for (int r0 = 0; r0 < 32; r0 += RPI) {
           const int r = r0 + lane / NC;
           const int64_t at = __shfl_sync(0xffffffffu, off, r);
