@@ -475,7 +475,10 @@ WQ_API int wq_linear_w8a8(const uint16_t *x, int64_t T, int64_t K, int64_t ldx, 
  * `dtype`.  Row, head and page pitches are in elements and may be any
  * non-negative value; the last dimension is contiguous.  Shapes and pitches
  * that allow 16-byte accesses (see each entry) take vector kernels, others
- * element-wise ones with the same results.  `status` may be NULL. */
+ * element-wise ones.  `status` may be NULL.  All arithmetic is float32 (the
+ * table's angles float64); unlike in the entries above, a product and the sum
+ * it enters may be rounded once, and sums are taken in an order that depends
+ * on the shape alone, so results are the same from run to run. */
 enum { WQ_DT_BF16 = 0, WQ_DT_F16 = 1, WQ_DT_F32 = 2 };
 
 /* ---------------------------------------------------------------------------
@@ -490,10 +493,11 @@ enum { WQ_DT_BF16 = 0, WQ_DT_F16 = 1, WQ_DT_F32 = 2 };
  * A NULL residual counts as 0, a NULL gate or weight as 1, a NULL bias as 0
  * (a bias is read by N_LAYER only).  gate is [T][H] with pitch ldg, or one
  * row for all tokens with ldg = 0.  x_out or y may be NULL (not both); either
- * may be block or residual itself (same pitch).  Means are sums in a fixed order.
- * Requirements: 1 <= H <= 32768, pitches ld* >= H (ldg = 0 or >= H).  The
- * vector kernels serve H and pitches that are multiples of 16 bytes with
- * 16-byte aligned pointers. */
+ * may be block or residual itself (same pitch).
+ * Requirements: 1 <= H <= 32768, pitches ld* >= H (ldg = 0 or >= H).  16-byte
+ * accesses serve tensors whose rows start alike against 16-byte boundaries
+ * (equal addresses and pitches modulo 16 bytes; contiguous tensors of any H
+ * do), best with H and pitches in multiples of 16 bytes. */
 enum { WQ_NORM_NONE = 0, WQ_NORM_RMS = 1, WQ_NORM_LAYER = 2 };
 WQ_API int wq_block_norm(const void *block, int64_t ldb, const void *residual, int64_t ldr,
                          const void *gate, int64_t ldg, float scale, int post,

@@ -250,6 +250,9 @@ ATTN = [  # q tokens of each sequence, suffix lengths, P, Hkv, G, dk, dv, page, 
     ([1] * 40, list(range(40, 0, -1)), 700, 1, 128, 64, 64, 128, FP, False),
     ([300], [900], 513, 1, 3, 128, 128, 256, BF, False),
     ([150, 7, 90], [150, 300, 91], 259, 2, 1, 96, 128, 24, FP, True),
+    ([1] * 72, [2] * 72, 1500, 5, 8, 64, 64, 16, BF, False),   # pairs of row tiles, the last with one
+    ([1] * 72, [2] * 72, 1500, 5, 8, 128, 128, 16, BF, False),
+    ([1] * 290, [1] * 290, 700, 3, 8, 64, 64, 16, FP, False),  # ten pairs in gangs of eight or so
 ]
 
 
@@ -336,6 +339,25 @@ def test_attention_extreme_scores(dtype, ql, sl, P):
     lse = torch.empty(sum(ql), 4, device="cuda")
     R.check(attn_call(i, P, max(sl), max(ql), lse=lse, scale=0.5), want, tol, "out")
     R.check(lse, wl, ltol, "lse")
+
+
+@pytest.mark.parametrize("B,D", [(10, 64), (10, 128), (40, 64), (40, 128)])
+@pytest.mark.parametrize("up", [True, False])
+def test_attention_scores_that_keep_growing(B, D, up):
+    """Each key outweighs those before it (or after it), by 2^8 every few
+    tiles: the sums are scaled again and again, one row tile or two."""
+    P, G = 2100, 8
+    i = attn_inputs([1] * B, [3] * B, P, 1, G, D, D, 16, BF, False)
+    ramp = torch.arange(P, dtype=F32, device="cuda") / P * 4
+    pages, place = i["prefix_pages"].long()[torch.arange(P) // 16], torch.arange(P) % 16
+    i["k_cache"][pages, 0, place] = (ramp if up else ramp.flip(0))[:, None].expand(P, D).to(BF)
+    i["q"].copy_((i["q"].abs() + 0.5).to(BF))
+    want, wl, tol, ltol = R.attention(i["q"], i["k_cache"], i["v_cache"], i["prefix_pages"], P, i["page_table"],
+                                      i["suffix_len"], i["cu_q"], 0.4, BF)
+    for _ in range(20):
+        lse = torch.empty(B, G, device="cuda")
+        R.check(attn_call(i, P, 3, 1, lse=lse, scale=0.4), want, tol, "out")
+        R.check(lse, wl, ltol, "lse")
 
 
 @pytest.mark.parametrize("ql", [[1, 1], [64, 80]])

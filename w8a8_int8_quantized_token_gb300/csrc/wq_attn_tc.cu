@@ -5,15 +5,16 @@
 //   O += P V,  l += row sums of P,  at the end O / l and its log-sum-exp.
 //
 // Rows are (token, query head of the group) pairs, so that every query head
-// of a group uses the keys that are loaded once.  Tiles of the two row tiles
-// alternate on the tensor cores: while one tile's scores are exponentiated,
-// the other's products run.
+// of a group uses the keys that are loaded once.  Two row tiles alternate on
+// the tensor cores: while one tile's scores are exponentiated, the other's
+// products run.  With heads of up to 64 a third score buffer lets the next
+// scores be ready when a softmax ends.
 //   warps 0-3, 4-7  softmax of row tile 0, 1: a thread owns one row
-//   warps 8, 9      MMA issue of row tile 0, 1; warp 8 owns the tensor memory
+//   warps 8, 9      MMA issue, in turns; warp 8 owns the tensor memory
 //   warp 10         TMA: queries, and keys and values page by page
 //   warp 11         none (the third warpgroup gives its registers to the others)
-// Tensor memory: S0, S1 (128 columns each), O0, O1 (D each).  P takes the
-// place of its S (64 columns, 16-bit pairs) as the A operand of the second
+// Tensor memory: two score buffers of 128 columns (three for D = 64), O0, O1
+// (D each).  P takes the place of its S (64 columns, 16-bit pairs) as the A operand of the second
 // product.  O is rescaled only when a row's maximum has grown by more than
 // 2^8 over the one in use: until then the weights are at most 2^8, their sum
 // stays exact in the same sense, and the final division removes the factor.
@@ -48,7 +49,7 @@ using namespace attn;
 
 constexpr int BM = 128, BN = 128;  // rows of a tile, keys of a tile
 constexpr int NTHREADS = 384;
-constexpr int WARP_MMA = 8, WARP_TMA = 10, WARP_IDLE = 11;  // MMA: one warp per row tile
+constexpr int WARP_MMA = 8, WARP_TMA = 10, WARP_IDLE = 11;  // MMA: two warps
 
 
 // Registers a thread: 3 x 168 at launch (the most for 384 threads), shared out
@@ -61,22 +62,29 @@ struct Plan {
   static constexpr int CH = D / 64;              // 128-byte column chunks
   static constexpr int QB = BM * D * 2;          // bytes of one query tile
   static constexpr int KVB = BN * D * 2;         // bytes of a key or value tile
-  static constexpr int NS = D == 128 ? 5 : 8;    // ring depth: keys and values in turn
+    static constexpr int NS = D == 128 ? 5 : 8;    // ring depth: keys and values in turn
+  static constexpr int NB = D == 128 ? 2 : 3;    // score buffers in tensor memory
+  // Barriers of the steps, used in turn.  Each is waited on by one row tile's
+  // warps alone, which have seen every phase before: a wait by parity cannot
+  // tell a phase from the one two before it.
+  static constexpr int NSB = NB % 2 ? 2 * NB : NB;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * QB;
   static constexpr int OFF_BAR = OFF_KV + NS * KVB;
   static constexpr int B_FULL = 0, B_EMPTY = NS, B_Q_FULL = 2 * NS, B_Q_EMPTY = B_Q_FULL + 1,
-                       B_S = B_Q_EMPTY + 1,      // [2] scores of a row tile are in
-      B_P = B_S + 2,                             // [2][2] half a tile of weights is in
-      B_O = B_P + 4,                             // [2] a piece's last value product is done
-      B_TAIL = B_O + 2,                          // [2] in turn: a last value tile's tail is cleared
+                       B_S = B_Q_EMPTY + 1,      // [NSB] a step's scores are in
+      B_P = B_S + NSB,                           // [NSB][2] half of its weights are in
+      B_O = B_P + 2 * NSB,                        // [2][2] a value product of a row tile is done, in turn
+      B_TAIL = B_O + 4,                          // [2] in turn: a last value tile's tail is cleared
       B_DONE = B_TAIL + 2, NBAR = B_DONE + 2;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
   static_assert(SMEM <= 232448, "shared memory plan too large");
-  static constexpr uint32_t T_O = 2 * BN;        // tensor-memory column of O0
-  static_assert(2 * BN + 2 * D <= 512, "tensor memory plan");
+    static constexpr uint32_t T_O = NB * BN;       // tensor-memory column of O0
+  static_assert(NB * BN + 2 * D <= 512, "tensor memory plan");
+  // keys NB tiles ahead of the values at hand, and those between
+  static_assert(NS >= 2 * NB, "ring too shallow");
 };
 
 // Bounded wait of one thread (1 s).  A try may suspend the thread by itself, so
@@ -205,6 +213,14 @@ struct Cut {
 
   bool out16;         // out rows take 16-byte stores
 };
+
+// Whether every value product signals its end.  With as many score buffers as
+// row tiles a tile's next scores are issued after it by the same thread and
+// say so themselves; then only a result's last product signals.
+template <int NB>
+__device__ __forceinline__ bool signal_each(int tiles) {
+  return NB > tiles;
+}
 
 // One piece of work: row tiles of a source against a key range
 struct Piece {
@@ -416,108 +432,106 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     } else if (warp != WARP_IDLE) {
       // ------------------------------------------------------------ products
-      // A warp per row tile walks, waits and (one lane) issues: PV of tile j,
-      // then QK of tile j + 1.  The two take turns, which keeps the row tiles
-      // half a step apart, and each does its waits in the other's turn: a wait
-      // takes over 100 cycles even when there is nothing to wait for.  After a
-      // wait that ran out a warp still takes its turns, so that the other ends.
+      // A piece's steps k = (key tile, row tile) use the score buffers in turn:
+      // QK(k) fills one, its weights take its place, PV(k) empties it, and
+      // QK(k + NB) fills it again.  A step here is PV(k), then QK(k + NB), from
+      // k = -NB on.  With two row tiles two warps take alternate steps (a wait
+      // takes over 100 cycles even when there is nothing to wait for, and one
+      // warp's waits pass in the other's step); with one, one warp takes all.
+      // With two buffers the two warps take turns, which keeps the row tiles
+      // half a step apart: warp 0 begins a piece and warp 1 ends it, so that a
+      // turn is never given twice, and after a wait that ran out a warp still
+      // takes its turns, so that the other ends.
       const int t = warp - WARP_MMA;
       const bool leader = elect_one();
       constexpr uint32_t id_s = idesc_f16(BM, BN) | kTypes<DT>;
       constexpr uint32_t id_o = idesc_f16(BM, D) | kTypes<DT> | kBTransposed;
-      const uint32_t ts = tmem + t * BN, to = tmem + P::T_O + t * D;
-      const uint64_t dq = sdesc(base + P::OFF_Q + t * P::QB);
-      int s = 0, q = 0, tails = 0;  // ring stage; pieces; cleared tails
-      uint32_t ph = 0, pp = 0;      // parity of the ring; of the weights
+      constexpr int NB = P::NB;
+      uint32_t g = 0, kk = 0;    // ring stages and steps of the pieces before
+      int q = 0, tails = 0;      // pieces; cleared tails
+      uint32_t ends0 = 0, ends1 = 0;  // signals on each row tile's products so far
       auto wait = [&](int b, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, wait_one(bar(b), parity, abort_flag));
         if (!ok) *abort_flag = 1;
       };
-      auto next = [&]() {
-        if (++s == P::NS) s = 0, ph ^= 1;
-      };
-      auto scores = [&](int stage) {
-        const uint64_t dk = sdesc(base + P::OFF_KV + uint32_t(stage * P::KVB));
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = ((k / 4) * (BM * 128) + (k % 4) * 32) >> 4;
-          mma_f16(ts, dq + o, dk + o, id_s, k ? 1u : 0u);
-        }
-        mma_commit(bar(P::B_S + t));
-      };
       // both row tiles release a stage; where there is one, it counts twice
-      auto release = [&](int stage, int tiles) {
+      auto release = [&](uint32_t stage, int tiles) {
         mma_commit(bar(P::B_EMPTY + stage));
         if (tiles == 1) mbar_arrive(bar(P::B_EMPTY + stage));
       };
-      auto turn = [&](int tiles) {  // wait for it
-        if (tiles == 2) named_sync(1 + t, 64);
-      };
-      auto pass = [&](int tiles) {
-        if (tiles == 2) asm volatile("bar.arrive %0, 64;" ::"r"(2 - t) : "memory");
-      };
       pieces([&](const Piece &p, int n, int tiles) {
         if (n == 0) return true;
-        const bool tail = (p.k1 - p.k0) % BN != 0;
-        if (t >= tiles) {  // no rows here: step over the piece's stages
-                    for (int i = 0; i < 2 * n; ++i) next();
-          q += p.open;
-          tails += tail;
-          return true;
-        }
-        if (t == 1) pass(tiles);  // row tile 0 begins
-                if (p.open) {
-          wait(P::B_Q_FULL, q & 1);
-          ++q;
-        }
-        wait(P::B_FULL + s, ph);
-        turn(tiles);
-        tc_fence_after();
-        if (leader && ok) {
-          scores(s);
-          release(s, tiles);
-        }
-        pass(tiles);
-        next();
+        const bool tail = (p.k1 - p.k0) % BN != 0, two = tiles == 2;
+        const int steps = n * tiles;
+        const bool each = signal_each<NB>(tiles);
+        const bool turns = NB == 2 && two;
+        auto pass = [&]() { asm volatile("bar.arrive %0, 64;" ::"r"(2 - t) : "memory"); };
+        if (turns && t == 1) pass();
+        // by both warps, even where one has no rows: it must not run ahead of
+        // the pieces, whose phases of the ring it could not tell apart then
+        if (p.open) wait(P::B_Q_FULL, q & 1);
+        q += p.open;
+        int k = two ? -NB + ((t - NB) & 1) : t == 0 ? -NB : steps;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-          const int sv = s;
-          const bool more = j + 1 < n;
-          wait(P::B_FULL + sv, ph);
-          next();
-          if (more) {
-            wait(P::B_FULL + s, ph);
-          } else if (tail) {
-            wait(P::B_TAIL + (tails & 1), (tails >> 1) & 1);
-            ++tails;
+        for (; k < steps; k += tiles) {
+          const int j = two ? k >> 1 : k;                      // PV(k): key tile, on row tile o
+          const int o = two ? k & 1 : 0;
+          const int kn = k + NB, jn = two ? kn >> 1 : kn, on = two ? kn & 1 : 0;  // QK(k + NB)
+          const uint32_t vi = g + 2 * uint32_t(j) + 1, ki = g + 2 * uint32_t(jn);
+          const uint32_t sv = vi % P::NS, sk = ki % P::NS;
+          const bool more = kn < steps;
+          const uint32_t buf = (kk + uint32_t(kn)) % NB;       // of both
+          const uint32_t pb = (kk + uint32_t(k)) % P::NSB, sb = (kk + uint32_t(kn)) % P::NSB;  // barriers
+          if (k >= 0) {
+            wait(P::B_FULL + sv, (vi / P::NS) & 1);
+            if (tail && j + 1 == n) wait(P::B_TAIL + (tails & 1), (tails >> 1) & 1);
           }
-          const uint64_t dv = sdesc_n(base + P::OFF_KV + uint32_t(sv * P::KVB));
-          wait(P::B_P + 2 * t, pp);
-          turn(tiles);
+          if (more) wait(P::B_FULL + sk, (ki / P::NS) & 1);
+          const uint32_t pp = ((kk + uint32_t(k)) / P::NSB) & 1;
+          if (k >= 0) wait(P::B_P + 2 * pb, pp);
+          if (turns) named_sync(1 + t, 64);
           tc_fence_after();
-          if (leader && ok) {
+          const uint32_t ts = tmem + buf * BN, to = tmem + P::T_O + o * D;
+          if (k >= 0) {
+            const uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB);
+            if (leader && ok) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_ts(to, ts + 8 * k, dv + ((2048 * k) >> 4), id_o, j | k || !p.open ? 1u : 0u);
-          }
-          wait(P::B_P + 2 * t + 1, pp);
-          pp ^= 1;
-          tc_fence_after();
-          if (leader && ok) {
+              for (int i = 0; i < 4; ++i)
+                mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, j | i || !p.open ? 1u : 0u);
+            }
+            wait(P::B_P + 2 * pb + 1, pp);
+            tc_fence_after();
+            if (leader && ok) {
 #pragma unroll
-            for (int k = 4; k < 8; ++k)
-              mma_f16_ts(to, ts + 8 * k, dv + ((2048 * k) >> 4), id_o, 1u);
-                        if (more) scores(s);
-            else if (p.close) mma_commit(bar(P::B_O + t));
+              for (int i = 4; i < 8; ++i) mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, 1u);
+              const uint32_t end = o ? ends1 : ends0;
+              if (each) mma_commit(bar(P::B_O + 2 * o + ((end + uint32_t(j)) & 1)));
+              else if (j + 1 == n && p.close) mma_commit(bar(P::B_O + 2 * o + (end & 1)));
+            }
           }
-          // the last turn of row tile 1 is nobody's to wait for
-          if (t == 0 || more) pass(tiles);
+          if (more && leader && ok) {
+            const uint64_t dk = sdesc(base + P::OFF_KV + sk * P::KVB);
+            const uint64_t dq = sdesc(base + P::OFF_Q + on * P::QB);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t at = ((i / 4) * (BM * 128) + (i % 4) * 32) >> 4;
+              mma_f16(ts, dq + at, dk + at, id_s, i ? 1u : 0u);
+            }
+            mma_commit(bar(P::B_S + sb));
+          }
+          // the last turn is nobody's to wait for
+          if (turns && k + 1 < steps) pass();
           if (leader && ok) {
-            release(sv, tiles);
-            if (more) release(s, tiles);
+            if (k >= 0) release(sv, tiles);
+            if (more) release(sk, tiles);
           }
-          if (more) next();
         }
+        g += 2 * uint32_t(n);
+        kk += uint32_t(steps);
+        const uint32_t signals = each ? uint32_t(n) : uint32_t(p.close);
+        ends0 += signals;
+        if (two) ends1 += signals;
+        tails += tail;
         return true;  // through all pieces, turns and all
       });
       if (leader) mma_commit(bar(P::B_DONE + t));
@@ -528,12 +542,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + t * BN, to = tmem + lanes + P::T_O + t * D;
+        const uint32_t to = tmem + lanes + P::T_O + t * D;
     const float sl2 = a.scale_log2;
-    int done = 0;  // key tiles so far
+        uint32_t kk = 0;    // steps of the pieces before (both row tiles)
+    uint32_t ends = 0;  // signals on this row tile's products so far
         int q = 0;     // pieces with keys so far
-        int ends = 0;  // results of this row tile so far
-    float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f;
     pieces([&](const Piece &p, int n, int tiles) {
       // the queries of a piece are released by the eight softmax warps: their
       // tiles serve as staging for the piece's results
@@ -543,7 +557,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P::B_Q_EMPTY));
       };
-            if (n > 0) q += p.open;
+                  if (n > 0) q += p.open;
+      const bool each = signal_each<P::NB>(tiles);
+      uint32_t k = kk + uint32_t(t);
+      kk += uint32_t(n * tiles);
       if (t >= tiles) {
         if (!p.close) return true;
         // not before the piece's queries are in: its release must not count
@@ -559,9 +576,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         m = -INFINITY;
         l = 0.0f;
       }
-      for (int j = 0; j < n; ++j, ++done) {
+            for (int j = 0; j < n; ++j, k += uint32_t(tiles)) {
         const int kb = p.k0 + j * BN;
-        if (!(ok = wait_warp(bar(P::B_S + t), done & 1, abort_flag))) return false;
+        const uint32_t buf = k % P::NB, ts = tmem + lanes + buf * BN;
+        const uint32_t step = k % P::NSB;
+        if (!(ok = wait_warp(bar(P::B_S + step), (k / P::NSB) & 1, abort_flag))) return false;
         tc_fence_after();
         uint32_t v[4][32];
         
@@ -596,7 +615,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(P::B_P + 2 * t + h));
+          if (lane == 0) mbar_arrive(bar(P::B_P + 2 * step + h));
           l += (sum[0] + sum[2]) + (sum[1] + sum[3]);
         };
 #pragma unroll
@@ -619,8 +638,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const float f = grow && m != -INFINITY ? ex2((m - top) * sl2) : 1.0f;
           if (grow) m = top;
           l *= f;
-          // these scores are in, so the value product of the tile before is too
           if ((j > 0 || !p.open) && __any_sync(0xffffffffu, f != 1.0f)) {
+            // the value product of the tile before has to be in
+            if (each) {
+              const uint32_t end = ends + uint32_t(j) - 1;
+              if (!(ok = wait_warp(bar(P::B_O + 2 * t + (end & 1)), (end >> 1) & 1, abort_flag))) return false;
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int i = 0; i < D / 16; ++i) {
               uint32_t o[16];
@@ -643,10 +667,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         weigh(1, neg);
         hand_over(1);
       }
-            if (!p.close) return true;
+      if (!p.close) {
+        if (each) ends += uint32_t(n);
+        return true;
+      }
       // ---- the row's result
       if (n > 0) {
-        if (!(ok = wait_warp(bar(P::B_O + t), uint32_t(ends++ & 1), abort_flag))) return false;
+        const uint32_t end = each ? ends + uint32_t(n) - 1 : ends;
+        ends = end + 1;
+        if (!(ok = wait_warp(bar(P::B_O + 2 * t + (end & 1)), (end >> 1) & 1, abort_flag))) return false;
         tc_fence_after();
       }
       const bool none = l == 0.0f;
