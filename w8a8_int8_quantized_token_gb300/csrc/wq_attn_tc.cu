@@ -472,52 +472,64 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (p.open) wait(P::B_Q_FULL, q & 1);
         q += p.open;
         int k = two ? -NB + ((t - NB) & 1) : t == 0 ? -NB : steps;
+        // Where step k is: ring stage and parity of PV(k)'s values and of
+        // QK(k + NB)'s keys (two stages on from step to step), barrier and
+        // parity of its weights, barrier of those scores, and their buffer.
+        // Counted on, since the divisions stand in the way of the issue.
+        const int j0 = two ? k >> 1 : k, jn0 = two ? (k + NB) >> 1 : k + NB;
+        const uint32_t v0 = g + uint32_t(2 * j0 + 1 + 2 * P::NS), c0 = g + uint32_t(2 * jn0);
+        const uint32_t p0 = kk + uint32_t(k + 2 * P::NSB), s0 = kk + uint32_t(k + NB);
+        uint32_t sv = v0 % P::NS, pv = (v0 / P::NS) & 1, sk = c0 % P::NS, pk = (c0 / P::NS) & 1;
+        uint32_t pb = p0 % P::NSB, pp = (p0 / P::NSB) & 1, sb = s0 % P::NSB, buf = s0 % NB;
+        const int o = two ? t : 0, on = two ? (t + NB) & 1 : 0;  // row tiles of PV(k), of QK(k + NB)
+        const uint32_t to = tmem + P::T_O + o * D;
+        const uint64_t dq = sdesc(base + P::OFF_Q + on * P::QB);
+        auto on_by = [](uint32_t &x, uint32_t by, uint32_t of) {
+          x += by;
+          const bool wrap = x >= of;
+          x -= wrap ? of : 0;
+          return uint32_t(wrap);
+        };
 #pragma unroll 1
-        for (; k < steps; k += tiles) {
-          const int j = two ? k >> 1 : k;                      // PV(k): key tile, on row tile o
-          const int o = two ? k & 1 : 0;
-          const int kn = k + NB, jn = two ? kn >> 1 : kn, on = two ? kn & 1 : 0;  // QK(k + NB)
-          const uint32_t vi = g + 2 * uint32_t(j) + 1, ki = g + 2 * uint32_t(jn);
-          const uint32_t sv = vi % P::NS, sk = ki % P::NS;
-          const bool more = kn < steps;
-          const uint32_t buf = (kk + uint32_t(kn)) % NB;       // of both
-          const uint32_t pb = (kk + uint32_t(k)) % P::NSB, sb = (kk + uint32_t(kn)) % P::NSB;  // barriers
+        for (int j = j0; k < steps; k += tiles, ++j) {
+                    const bool more = k + NB < steps;
+          // operands and barriers, ready before the turn comes
+          uint32_t ts = tmem + buf * BN, acc = j > 0 || !p.open;
+          uint32_t bar_o = bar(P::B_O + 2 * o) + 8 * (((o ? ends1 : ends0) + (each ? uint32_t(j) : 0u)) & 1u);
+          uint32_t bar_s = bar(P::B_S + sb);
+          uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB), dk = sdesc(base + P::OFF_KV + sk * P::KVB);
+          asm volatile("" : "+r"(ts), "+r"(acc), "+r"(bar_o), "+r"(bar_s), "+l"(dv), "+l"(dk));
           if (k >= 0) {
-            wait(P::B_FULL + sv, (vi / P::NS) & 1);
+            wait(P::B_FULL + sv, pv);
             if (tail && j + 1 == n) wait(P::B_TAIL + (tails & 1), (tails >> 1) & 1);
           }
-          if (more) wait(P::B_FULL + sk, (ki / P::NS) & 1);
-          const uint32_t pp = ((kk + uint32_t(k)) / P::NSB) & 1;
+          if (more) wait(P::B_FULL + sk, pk);
           if (k >= 0) wait(P::B_P + 2 * pb, pp);
           if (turns) named_sync(1 + t, 64);
           tc_fence_after();
-          const uint32_t ts = tmem + buf * BN, to = tmem + P::T_O + o * D;
+          
           if (k >= 0) {
-            const uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB);
             if (leader && ok) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, j | i || !p.open ? 1u : 0u);
+                mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, i ? 1u : acc);
             }
             wait(P::B_P + 2 * pb + 1, pp);
             tc_fence_after();
             if (leader && ok) {
 #pragma unroll
               for (int i = 4; i < 8; ++i) mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, 1u);
-              const uint32_t end = o ? ends1 : ends0;
-              if (each) mma_commit(bar(P::B_O + 2 * o + ((end + uint32_t(j)) & 1)));
-              else if (j + 1 == n && p.close) mma_commit(bar(P::B_O + 2 * o + (end & 1)));
+              if (each || (j + 1 == n && p.close)) mma_commit(bar_o);
             }
           }
           if (more && leader && ok) {
-            const uint64_t dk = sdesc(base + P::OFF_KV + sk * P::KVB);
-            const uint64_t dq = sdesc(base + P::OFF_Q + on * P::QB);
+            
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               const uint32_t at = ((i / 4) * (BM * 128) + (i % 4) * 32) >> 4;
               mma_f16(ts, dq + at, dk + at, id_s, i ? 1u : 0u);
             }
-            mma_commit(bar(P::B_S + sb));
+            mma_commit(bar_s);
           }
           // the last turn is nobody's to wait for
           if (turns && k + 1 < steps) pass();
@@ -525,6 +537,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (k >= 0) release(sv, tiles);
             if (more) release(sk, tiles);
           }
+          pv ^= on_by(sv, 2, P::NS);
+          pk ^= on_by(sk, 2, P::NS);
+          pp ^= on_by(pb, uint32_t(tiles), P::NSB);
+          on_by(sb, uint32_t(tiles), P::NSB);
+          on_by(buf, uint32_t(tiles), NB);
         }
         g += 2 * uint32_t(n);
         kk += uint32_t(steps);
