@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           uint32_t ts = tmem + buf * BN, acc = j > 0 || !p.open;
           uint32_t bar_o = bar(P::B_O + 2 * o) + 8 * (((o ? ends1 : ends0) + (each ? uint32_t(j) : 0u)) & 1u);
           uint32_t bar_s = bar(P::B_S + sb);
+          const bool signal = each || (j + 1 == n && p.close);
           uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB), dk = sdesc(base + P::OFF_KV + sk * P::KVB);
           asm volatile("" : "+r"(ts), "+r"(acc), "+r"(bar_o), "+r"(bar_s), "+l"(dv), "+l"(dk));
           if (k >= 0) {
@@ -508,6 +509,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (turns) named_sync(1 + t, 64);
           tc_fence_after();
           
+          auto scores = [&]() {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t at = ((i / 4) * (BM * 128) + (i % 4) * 32) >> 4;
+              mma_f16(ts, dq + at, dk + at, id_s, i ? 1u : 0u);
+            }
+            mma_commit(bar_s);
+          };
           if (k >= 0) {
             if (leader && ok) {
 #pragma unroll
@@ -519,17 +528,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (leader && ok) {
 #pragma unroll
               for (int i = 4; i < 8; ++i) mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, 1u);
-              if (each || (j + 1 == n && p.close)) mma_commit(bar_o);
+              if (signal) mma_commit(bar_o);
+              if (more) scores();
             }
-          }
-          if (more && leader && ok) {
-            
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              const uint32_t at = ((i / 4) * (BM * 128) + (i % 4) * 32) >> 4;
-              mma_f16(ts, dq + at, dk + at, id_s, i ? 1u : 0u);
-            }
-            mma_commit(bar_s);
+          } else if (more && leader && ok) {
+            scores();
           }
           // the last turn is nobody's to wait for
           if (turns && k + 1 < steps) pass();
