@@ -600,7 +600,9 @@ WQ_API int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, 
  * is left to chance.
  * Requirements: bf16 or fp16; dk, dv multiples of 8, at most 128; q_heads a
  * multiple of heads, at most 128 per key head; pitches of q and the cache
- * multiples of 8 elements, q, k and v 16-byte aligned; B, T < 2^24.
+ * multiples of 8 elements, those of q and out not 0 where there is more than
+ * one token or head, pitches below 2^39; q, k and v 16-byte aligned, out
+ * 4-byte (its pitches even); B, T < 2^24.
  * Workspace: wq_attention_shared_prefix_workspace_size() with the same
  * arguments (0 bytes when nothing is split). */
 WQ_API size_t wq_attention_shared_prefix_workspace_size(int64_t T, int B, int max_q, int q_heads,

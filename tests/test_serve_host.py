@@ -85,7 +85,7 @@ def test_attention_refusals(lib):
                dict(cu=None, max_q=1), dict(B=0), dict(qt=-8), dict(ot=-2), dict(ldt=-1), dict(cache=cache(v=None))):
         assert call(**kw) == INVALID, kw
     for kw in (dict(nq=258, cache=cache()), dict(cache=cache(dk=136)), dict(cache=cache(dv=60)), dict(cache=cache(k_token=65)),
-               dict(qt=510), dict(oh=63), dict(q=FAKE + 8), dict(cache=cache(k=FAKE + 8)), dict(out=FAKE + 2),
+               dict(qt=510), dict(oh=63), dict(q=FAKE + 8), dict(cache=cache(k=FAKE + 8)), dict(out=FAKE + 2), dict(qh=0), dict(ot=0),
                dict(T=1 << 24), dict(P=1 << 30)):
         assert call(**kw) == UNSUPPORTED, kw
     size = lambda **kw: lib.wq_attention_shared_prefix_workspace_size(

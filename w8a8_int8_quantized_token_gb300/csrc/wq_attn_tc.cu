@@ -14,8 +14,8 @@
 //   warp 10         TMA: queries, and keys and values page by page
 //   warp 11         none (the third warpgroup gives its registers to the others)
 // Tensor memory: two score buffers of 128 columns (three for D = 64), O0, O1
-// (D each).  P takes the place of its S (64 columns, 16-bit pairs) as the A operand of the second
-// product.  O is rescaled only when a row's maximum has grown by more than
+// (D each).  P takes the place of its S (64 columns, 16-bit pairs) as the A
+// operand of the second product.  O is rescaled only when a row's maximum has grown by more than
 // 2^8 over the one in use: until then the weights are at most 2^8, their sum
 // stays exact in the same sense, and the final division removes the factor.
 //
@@ -28,6 +28,13 @@
 // of equal units that the gangs cut into equal pieces: a piece may end inside
 // an item and begin the next, and each leaves a partial result.  Suffixes: a
 // block per (range, sequence, key head, row tile pair).
+//
+// Measured (bf16): a step of 256 rows x 128 keys takes 1.71 us at D = 128,
+// 1.49 PFLOP/s over 152 SMs (0.77 of the measured cuBLAS burst), bound by the
+// products and the hand-overs between the roles: without the exponentials it
+// takes as long.  At D = 64 it takes 1.18 us (0.55 of burst at half the
+// products), bound by the softmax; with two score buffers it took 1.45 us.  An
+// end of a range costs about 8 us (first loads 3, last product and results 4).
 //
 // Values past the end of a range may be anything (a page is shared with
 // unwritten places), and 0 * NaN is NaN: the last tile's tail is cleared in
@@ -50,8 +57,6 @@ using namespace attn;
 constexpr int BM = 128, BN = 128;  // rows of a tile, keys of a tile
 constexpr int NTHREADS = 384;
 constexpr int WARP_MMA = 8, WARP_TMA = 10, WARP_IDLE = 11;  // MMA: two warps
-
-
 // Registers a thread: 3 x 168 at launch (the most for 384 threads), shared out
 // as 2 x 216 for the softmax, which holds a row of 128 scores, and 72
 constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
@@ -62,7 +67,7 @@ struct Plan {
   static constexpr int CH = D / 64;              // 128-byte column chunks
   static constexpr int QB = BM * D * 2;          // bytes of one query tile
   static constexpr int KVB = BN * D * 2;         // bytes of a key or value tile
-    static constexpr int NS = D == 128 ? 5 : 8;    // ring depth: keys and values in turn
+  static constexpr int NS = D == 128 ? 5 : 8;    // ring depth: keys and values in turn
   static constexpr int NB = D == 128 ? 2 : 3;    // score buffers in tensor memory
   // Barriers of the steps, used in turn.  Each is waited on by one row tile's
   // warps alone, which have seen every phase before: a wait by parity cannot
@@ -81,7 +86,7 @@ struct Plan {
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
   static_assert(SMEM <= 232448, "shared memory plan too large");
-    static constexpr uint32_t T_O = NB * BN;       // tensor-memory column of O0
+  static constexpr uint32_t T_O = NB * BN;       // tensor-memory column of O0
   static_assert(NB * BN + 2 * D <= 512, "tensor memory plan");
   // keys NB tiles ahead of the values at hand, and those between
   static_assert(NS >= 2 * NB, "ring too shallow");
@@ -285,11 +290,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     prefetch_map(&tmK);
     prefetch_map(&tmV);
     *abort_flag = 0;
-        for (int i = 0; i < P::NBAR; ++i)
-      mbar_init(bar(i), i == P::B_Q_EMPTY ? 8                      // softmax warps
-                                                                        : i >= P::B_P && i < P::B_O ? 4            // warps of a row tile
-                        : i >= P::B_EMPTY && i < P::B_Q_FULL ? 2   // row tiles
-                                                             : 1);
+    for (int i = 0; i < P::NBAR; ++i)
+      mbar_init(bar(i), i == P::B_Q_EMPTY                      ? 8   // softmax warps
+                        : i >= P::B_P && i < P::B_O            ? 4   // warps of a row tile
+                        : i >= P::B_EMPTY && i < P::B_Q_FULL   ? 2   // row tiles
+                                                               : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WARP_MMA) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -298,8 +303,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-    bool ok = true;  // this role's waits all ended in time
-
+  bool ok = true;  // this role's waits all ended in time
 
   // ---- this block's pieces, the same list for every role
   const int gang = int(blockIdx.x) / max(c.gang, 1), member = int(blockIdx.x) - gang * c.gang;
@@ -345,13 +349,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // ------------------------------------------------------------ copies
       int s = 0, g = 0, q = 0;  // ring stage; stages issued; pieces with keys
       uint32_t ph = 1;          // parity of the ring's releases
-            int tails = 0;            // cleared tails
+      int tails = 0;            // cleared tails
       bool bad = false;         // a page id outside the cache
       const int nbox = BN / c.box;
       const bool leader = elect_one();
       pieces([&](const Piece &p, int n, int tiles) {
         if (n == 0) return true;
-                if (p.open && !(ok = wait_warp(bar(P::B_Q_EMPTY), (q & 1) ^ 1, abort_flag))) return false;
+        if (p.open && !(ok = wait_warp(bar(P::B_Q_EMPTY), (q & 1) ^ 1, abort_flag))) return false;
         if (leader && p.open) {
           mbar_expect_tx(bar(P::B_Q_FULL), uint32_t(tiles * P::CH * c.tpt * a.G * 128));
 #pragma unroll 1
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               tma_load_3d(base + P::OFF_Q + t * P::QB + ch * BM * 128, &tmQ, ch * 64, p.head * a.G,
                           p.s.t0 + p.tok0 + t * c.tpt, bar(P::B_Q_FULL));
         }
-                q += p.open;
+        q += p.open;
         // lane b looks up box b of a tile, one tile ahead of its copies; a bad
         // page is read outside the tensor: zeros
         const int key0 = p.k0 + lane * c.box;
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         };
 #pragma unroll 1
         for (int j = j0; k < steps; k += tiles, ++j) {
-                    const bool more = k + NB < steps;
+          const bool more = k + NB < steps;
           // operands and barriers, ready before the turn comes
           uint32_t ts = tmem + buf * BN, acc = j > 0 || !p.open;
           uint32_t bar_o = bar(P::B_O + 2 * o) + 8 * (((o ? ends1 : ends0) + (each ? uint32_t(j) : 0u)) & 1u);
@@ -508,7 +512,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (k >= 0) wait(P::B_P + 2 * pb, pp);
           if (turns) named_sync(1 + t, 64);
           tc_fence_after();
-          
           auto scores = [&]() {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -562,12 +565,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // ------------------------------------------------------------ softmax
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t to = tmem + lanes + P::T_O + t * D;
+    const uint32_t to = tmem + lanes + P::T_O + t * D;
     const float sl2 = a.scale_log2;
-        uint32_t kk = 0;    // steps of the pieces before (both row tiles)
+    uint32_t kk = 0;    // steps of the pieces before (both row tiles)
     uint32_t ends = 0;  // signals on this row tile's products so far
-        int q = 0;     // pieces with keys so far
-        float m = -INFINITY, l = 0.0f;
+    int q = 0;          // pieces with keys so far
+    float m = -INFINITY, l = 0.0f;
     pieces([&](const Piece &p, int n, int tiles) {
       // the queries of a piece are released by the eight softmax warps: their
       // tiles serve as staging for the piece's results
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P::B_Q_EMPTY));
       };
-                  if (n > 0) q += p.open;
+      if (n > 0) q += p.open;
       const bool each = signal_each<P::NB>(tiles);
       uint32_t k = kk + uint32_t(t);
       kk += uint32_t(n * tiles);
@@ -592,18 +595,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int tok = row / a.G, j0 = p.tok0 + t * c.tpt + tok;
       const bool mine = tok < c.tpt && j0 < p.s.n;
       const int lim = mine ? min(p.k1, visible(p.s, j0)) : 0;
-            if (p.open) {
+      if (p.open) {
         m = -INFINITY;
         l = 0.0f;
       }
-            for (int j = 0; j < n; ++j, k += uint32_t(tiles)) {
+      for (int j = 0; j < n; ++j, k += uint32_t(tiles)) {
         const int kb = p.k0 + j * BN;
         const uint32_t buf = k % P::NB, ts = tmem + lanes + buf * BN;
         const uint32_t step = k % P::NSB;
         if (!(ok = wait_warp(bar(P::B_S + step), (k / P::NSB) & 1, abort_flag))) return false;
         tc_fence_after();
         uint32_t v[4][32];
-        
         // 64 weights under the maximum in use, two to a word
         uint32_t w[32];
         float sum[4], top = -INFINITY;
@@ -714,8 +716,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // Rows leave through this warp's quarter of its query tile (all products
       // with it are done), so that a store covers whole rows: 16-byte pieces,
       // swizzled, NC a row.  16-bit results go in one pass, float parts in two.
-      // Loops, not unrolled: this runs once, and code that is fetched for the
-      // first time costs more than what it does (3.7 us unrolled).
+      // With 152 blocks the float parts (128 KB each) take about 3.7 us to L2,
+      // all at the same time; 16-bit results a quarter of that.
       constexpr int NC = D / 8, RPI = 32 / NC;  // pieces of a staged row; rows a store covers
       uint8_t *stage = sm + P::OFF_Q + t * P::QB + (warp & 3) * 32 * (D * 2);
       const int64_t off = a.o_part ? ((tg * a.Hq + qh) * a.slots + p.slot) * a.dv
@@ -780,7 +782,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       return true;
     });
   }
-    if (!ok) {
+  if (!ok) {
     *abort_flag = 1;
     set_status(a.status, WQ_ERR_TIMEOUT);
   }
@@ -827,7 +829,7 @@ int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st) {
   if (a.tc_prefix) {
     c.pairs_p = (a.T + 2 * c.tpt - 1) / (2 * c.tpt);
     c.units_p = (a.P + BN - 1) / BN;
-        c.gang = a.p_gang;
+    c.gang = a.p_gang;
     c.gangs = a.p_gangs;
     c.groups = (c.pairs_p + c.gang - 1) / c.gang;
     c.stretch = a.p_stretch;

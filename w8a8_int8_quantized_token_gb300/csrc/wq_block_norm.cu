@@ -5,7 +5,10 @@
 // A row stays in registers from its one load to its stores: block, residual
 // and gate are read once, both outputs written once, and the two norms (the
 // second needs the whole of h) cost two or four block reductions in between.
-// Bound by HBM: 4 T H elements, 5 with a gate per token.  Arithmetic goes in
+// Bound by HBM: 4 T H elements, 5 with a gate per token; 8192 x 7168 bf16 take
+// 89 us, 5.3 TB/s.  Rows that are not whole 16-byte pieces are bound by their
+// instructions (weights are read element by element there): 1021 x 4099 fp16
+// with a gate take 26 us, 1.6 TB/s.  Arithmetic goes in
 // packed float32 pairs: in single operations on 16-bit elements the kernel
 // was bound by its instructions (53 an element).
 #include <algorithm>

@@ -225,6 +225,7 @@ int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_head, i
   if (max_suffix > 0 && (!page_table || !suffix_len || max_suffix > ld_table * cache->page_size))
     return WQ_ERR_INVALID_ARG;
   if (cu_q ? max_q < 1 : int64_t(max_q) * B != T) return WQ_ERR_INVALID_ARG;
+  if ((T > 1 && (!q_token || !o_token)) || (q_heads > 1 && (!q_head || !o_head))) return WQ_ERR_UNSUPPORTED;
   if (q_token % 8 || q_head % 8 || o_token % 2 || o_head % 2 || !al(q, 16) || !al(cache->k, 16) ||
       !al(cache->v, 16) || !al(out, 4) || !al(lse, 4))
     return WQ_ERR_UNSUPPORTED;
