@@ -29,11 +29,10 @@
 // an item and begin the next, and each leaves a partial result.  Suffixes: a
 // block per (range, sequence, key head, row tile pair).
 //
-// Measured (bf16): a step of 256 rows x 128 keys takes 1.71 us at D = 128,
-// 1.49 PFLOP/s over 152 SMs (0.77 of the measured cuBLAS burst), bound by the
+// Measured (bf16): a step of 256 rows x 128 keys takes 1.67 us at D = 128,
+// 1.53 PFLOP/s over 152 SMs (0.79 of the measured cuBLAS burst), bound by the
 // products and the hand-overs between the roles: without the exponentials it
-// takes as long.  At D = 64 it takes 1.18 us (0.55 of burst at half the
-// products), bound by the softmax; with two score buffers it took 1.45 us.  An
+// takes as long.  At D = 64 it takes 1.16 us (0.57 of burst), bound by the softmax; with two score buffers it took 1.45 us.  An
 // end of a range costs about 8 us (first loads 3, last product and results 4).
 //
 // Values past the end of a range may be anything (a page is shared with
@@ -58,8 +57,8 @@ constexpr int BM = 128, BN = 128;  // rows of a tile, keys of a tile
 constexpr int NTHREADS = 384;
 constexpr int WARP_MMA = 8, WARP_TMA = 10, WARP_IDLE = 11;  // MMA: two warps
 // Registers a thread: 3 x 168 at launch (the most for 384 threads), shared out
-// as 2 x 216 for the softmax, which holds a row of 128 scores, and 72
-constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
+// as 2 x 208 for the softmax, which holds a row of 128 scores, and 88
+constexpr int REGS_SOFTMAX = 208, REGS_OTHER = 88;
 static_assert(2 * REGS_SOFTMAX + REGS_OTHER <= 3 * 168, "a larger sum would wait forever");
 
 template <int D>
@@ -475,79 +474,140 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // the pieces, whose phases of the ring it could not tell apart then
         if (p.open) wait(P::B_Q_FULL, q & 1);
         q += p.open;
-        int k = two ? -NB + ((t - NB) & 1) : t == 0 ? -NB : steps;
-        // Where step k is: ring stage and parity of PV(k)'s values and of
-        // QK(k + NB)'s keys (two stages on from step to step), barrier and
-        // parity of its weights, barrier of those scores, and their buffer.
-        // Counted on, since the divisions stand in the way of the issue.
-        const int j0 = two ? k >> 1 : k, jn0 = two ? (k + NB) >> 1 : k + NB;
-        const uint32_t v0 = g + uint32_t(2 * j0 + 1 + 2 * P::NS), c0 = g + uint32_t(2 * jn0);
-        const uint32_t p0 = kk + uint32_t(k + 2 * P::NSB), s0 = kk + uint32_t(k + NB);
-        uint32_t sv = v0 % P::NS, pv = (v0 / P::NS) & 1, sk = c0 % P::NS, pk = (c0 / P::NS) & 1;
-        uint32_t pb = p0 % P::NSB, pp = (p0 / P::NSB) & 1, sb = s0 % P::NSB, buf = s0 % NB;
-        const int o = two ? t : 0, on = two ? (t + NB) & 1 : 0;  // row tiles of PV(k), of QK(k + NB)
-        const uint32_t to = tmem + P::T_O + o * D;
-        const uint64_t dq = sdesc(base + P::OFF_Q + on * P::QB);
-        auto on_by = [](uint32_t &x, uint32_t by, uint32_t of) {
-          x += by;
-          const bool wrap = x >= of;
-          x -= wrap ? of : 0;
-          return uint32_t(wrap);
-        };
-#pragma unroll 1
-        for (int j = j0; k < steps; k += tiles, ++j) {
-          const bool more = k + NB < steps;
-          // operands and barriers, ready before the turn comes
-          uint32_t ts = tmem + buf * BN, acc = j > 0 || !p.open;
-          uint32_t bar_o = bar(P::B_O + 2 * o) + 8 * (((o ? ends1 : ends0) + (each ? uint32_t(j) : 0u)) & 1u);
-          uint32_t bar_s = bar(P::B_S + sb);
-          const bool signal = each || (j + 1 == n && p.close);
-          uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB), dk = sdesc(base + P::OFF_KV + sk * P::KVB);
-          asm volatile("" : "+r"(ts), "+r"(acc), "+r"(bar_o), "+r"(bar_s), "+l"(dv), "+l"(dk));
-          if (k >= 0) {
-            wait(P::B_FULL + sv, pv);
-            if (tail && j + 1 == n) wait(P::B_TAIL + (tails & 1), (tails >> 1) & 1);
-          }
-          if (more) wait(P::B_FULL + sk, pk);
-          if (k >= 0) wait(P::B_P + 2 * pb, pp);
-          if (turns) named_sync(1 + t, 64);
-          tc_fence_after();
-          auto scores = [&]() {
+        if (turns) {
+          // The common case written out: warp t keeps to row tile t and one
+          // buffer, and what a step needs is counted on by one.  (Through the
+          // general loop below a step of 256 rows x 128 keys takes 1.71 us
+          // instead of 1.67: these warps are bound by what they issue.)
+          const uint32_t buf = (kk + uint32_t(t)) & 1, ts = tmem + buf * BN, to = tmem + P::T_O + t * D;
+          const uint64_t dq = sdesc(base + P::OFF_Q + t * P::QB);
+          uint32_t s = g % P::NS, ph = (g / P::NS) & 1, pp = ((kk + uint32_t(t)) >> 1) & 1;
+          auto next = [&]() {
+            if (++s == P::NS) s = 0, ph ^= 1;
+          };
+          auto scores = [&](uint32_t stage) {
+            const uint64_t dk = sdesc(base + P::OFF_KV + stage * P::KVB);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               const uint32_t at = ((i / 4) * (BM * 128) + (i % 4) * 32) >> 4;
               mma_f16(ts, dq + at, dk + at, id_s, i ? 1u : 0u);
             }
-            mma_commit(bar_s);
+            mma_commit(bar(P::B_S + buf));
           };
-          if (k >= 0) {
+          wait(P::B_FULL + s, ph);
+          named_sync(1 + t, 64);
+          tc_fence_after();
+          if (leader && ok) {
+            scores(s);
+            release(s, 2);
+          }
+          pass();
+          next();
+#pragma unroll 1
+          for (int j = 0; j < n; ++j) {
+            const uint32_t sv = s;
+            const bool more = j + 1 < n;
+            wait(P::B_FULL + sv, ph);
+            next();
+            if (more) wait(P::B_FULL + s, ph);
+            else if (tail) wait(P::B_TAIL + (tails & 1), (tails >> 1) & 1);
+            const uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB);
+            wait(P::B_P + 2 * buf, pp);
+            named_sync(1 + t, 64);
+            tc_fence_after();
             if (leader && ok) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, i ? 1u : acc);
+                mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, j | i || !p.open ? 1u : 0u);
             }
-            wait(P::B_P + 2 * pb + 1, pp);
+            wait(P::B_P + 2 * buf + 1, pp);
+            pp ^= 1;
             tc_fence_after();
             if (leader && ok) {
 #pragma unroll
               for (int i = 4; i < 8; ++i) mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, 1u);
-              if (signal) mma_commit(bar_o);
-              if (more) scores();
+              if (more) scores(s);
+              else if (p.close) mma_commit(bar(P::B_O + 2 * t + ((t ? ends1 : ends0) & 1)));
             }
-          } else if (more && leader && ok) {
-            scores();
+            if (t == 0 || more) pass();  // the last turn is nobody's to wait for
+            if (leader && ok) {
+              release(sv, 2);
+              if (more) release(s, 2);
+            }
+            if (more) next();
           }
-          // the last turn is nobody's to wait for
-          if (turns && k + 1 < steps) pass();
-          if (leader && ok) {
-            if (k >= 0) release(sv, tiles);
-            if (more) release(sk, tiles);
+        } else {
+          int k = two ? -NB + ((t - NB) & 1) : t == 0 ? -NB : steps;
+          // Where step k is: ring stage and parity of PV(k)'s values and of
+          // QK(k + NB)'s keys (two stages on from step to step), barrier and
+          // parity of its weights, barrier of those scores, and their buffer.
+          // Counted on, since the divisions stand in the way of the issue.
+          const int j0 = two ? k >> 1 : k, jn0 = two ? (k + NB) >> 1 : k + NB;
+          const uint32_t v0 = g + uint32_t(2 * j0 + 1 + 2 * P::NS), c0 = g + uint32_t(2 * jn0);
+          const uint32_t p0 = kk + uint32_t(k + 2 * P::NSB), s0 = kk + uint32_t(k + NB);
+          uint32_t sv = v0 % P::NS, pv = (v0 / P::NS) & 1, sk = c0 % P::NS, pk = (c0 / P::NS) & 1;
+          uint32_t pb = p0 % P::NSB, pp = (p0 / P::NSB) & 1, sb = s0 % P::NSB, buf = s0 % NB;
+          const int o = two ? t : 0, on = two ? (t + NB) & 1 : 0;  // row tiles of PV(k), of QK(k + NB)
+          const uint32_t to = tmem + P::T_O + o * D;
+          const uint64_t dq = sdesc(base + P::OFF_Q + on * P::QB);
+          auto on_by = [](uint32_t &x, uint32_t by, uint32_t of) {
+            x += by;
+            const bool wrap = x >= of;
+            x -= wrap ? of : 0;
+            return uint32_t(wrap);
+          };
+#pragma unroll 1
+          for (int j = j0; k < steps; k += tiles, ++j) {
+            const bool more = k + NB < steps;
+            // operands and barriers, ready ahead of the waits
+            uint32_t ts = tmem + buf * BN, acc = j > 0 || !p.open;
+            uint32_t bar_o = bar(P::B_O + 2 * o) + 8 * (((o ? ends1 : ends0) + (each ? uint32_t(j) : 0u)) & 1u);
+            uint32_t bar_s = bar(P::B_S + sb);
+            const bool signal = each || (j + 1 == n && p.close);
+            uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB), dk = sdesc(base + P::OFF_KV + sk * P::KVB);
+            asm volatile("" : "+r"(ts), "+r"(acc), "+r"(bar_o), "+r"(bar_s), "+l"(dv), "+l"(dk));
+            if (k >= 0) {
+              wait(P::B_FULL + sv, pv);
+              if (tail && j + 1 == n) wait(P::B_TAIL + (tails & 1), (tails >> 1) & 1);
+            }
+            if (more) wait(P::B_FULL + sk, pk);
+            if (k >= 0) wait(P::B_P + 2 * pb, pp);
+            tc_fence_after();
+            auto scores = [&]() {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint32_t at = ((i / 4) * (BM * 128) + (i % 4) * 32) >> 4;
+                mma_f16(ts, dq + at, dk + at, id_s, i ? 1u : 0u);
+              }
+              mma_commit(bar_s);
+            };
+            if (k >= 0) {
+              if (leader && ok) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, i ? 1u : acc);
+              }
+              wait(P::B_P + 2 * pb + 1, pp);
+              tc_fence_after();
+              if (leader && ok) {
+#pragma unroll
+                for (int i = 4; i < 8; ++i) mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, 1u);
+                if (signal) mma_commit(bar_o);
+                if (more) scores();
+              }
+            } else if (more && leader && ok) {
+              scores();
+            }
+            if (leader && ok) {
+              if (k >= 0) release(sv, tiles);
+              if (more) release(sk, tiles);
+            }
+            pv ^= on_by(sv, 2, P::NS);
+            pk ^= on_by(sk, 2, P::NS);
+            pp ^= on_by(pb, uint32_t(tiles), P::NSB);
+            on_by(sb, uint32_t(tiles), P::NSB);
+            on_by(buf, uint32_t(tiles), NB);
           }
-          pv ^= on_by(sv, 2, P::NS);
-          pk ^= on_by(sk, 2, P::NS);
-          pp ^= on_by(pb, uint32_t(tiles), P::NSB);
-          on_by(sb, uint32_t(tiles), P::NSB);
-          on_by(buf, uint32_t(tiles), NB);
         }
         g += 2 * uint32_t(n);
         kk += uint32_t(steps);
