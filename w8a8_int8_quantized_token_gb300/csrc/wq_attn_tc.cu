@@ -32,8 +32,9 @@
 // Measured (bf16): a step of 256 rows x 128 keys takes 1.67 us at D = 128,
 // 1.53 PFLOP/s over 152 SMs (0.79 of the measured cuBLAS burst), bound by the
 // products and the hand-overs between the roles: without the exponentials it
-// takes as long.  At D = 64 it takes 1.16 us (0.57 of burst), bound by the softmax; with two score buffers it took 1.45 us.  An
-// end of a range costs about 8 us (first loads 3, last product and results 4).
+// takes as long.  At D = 64 it takes 1.16 us (0.57 of burst), bound by the
+// softmax; with two score buffers it took 1.45 us.  An end of a range costs
+// about 8 us (first loads 3, last product and results 4).
 //
 // Values past the end of a range may be anything (a page is shared with
 // unwritten places), and 0 * NaN is NaN: the last tile's tail is cleared in
