@@ -55,23 +55,31 @@ __host__ __device__ inline int threads_of(const RopeSeg &s) {
   return (s.heads + KH - 1) / KH * units_of(s);
 }
 
+// A thread's token and its place among the token's threads: blocks of whole
+// tokens, or (y) a token's threads in blocks of 256
+__device__ __forceinline__ bool place_of(const RopeArgs &a, int per_token, int64_t &t, int &rest) {
+  if (per_token >= 256) {
+    t = blockIdx.x;
+    rest = int(blockIdx.y * 256 + threadIdx.x);
+    return rest < per_token;
+  }
+  const int tokens = 256 / per_token, own = int(threadIdx.x) / per_token;
+  t = int64_t(blockIdx.x) * tokens + own;
+  rest = int(threadIdx.x) - own * per_token;
+  return own < tokens && t < a.T;
+}
+inline dim3 grid_of(const RopeArgs &a, int per_token) {
+  const int tokens = per_token >= 256 ? 1 : 256 / per_token;
+  return dim3(unsigned((a.T + tokens - 1) / tokens), unsigned(per_token >= 256 ? (per_token + 255) / 256 : 1));
+}
+
 template <class DT, int KH>
 __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int per_token) {
   using Raw = typename DT::Raw;
   using V = Vec<DT, 8>;
-  // blocks of whole tokens, or (y) a token's threads in blocks of 256
   int64_t t;
   int rest;
-  if (per_token >= 256) {
-    t = blockIdx.x;
-    rest = int(blockIdx.y * 256 + threadIdx.x);
-    if (rest >= per_token) return;
-  } else {
-    const int tokens = 256 / per_token, own = int(threadIdx.x) / per_token;
-    t = int64_t(blockIdx.x) * tokens + own;
-    rest = int(threadIdx.x) - own * per_token;
-    if (own >= tokens || t >= a.T) return;
-  }
+  if (!place_of(a, per_token, t, rest)) return;
   int i = 0;
   while (rest >= threads_of<KH>(a.seg[i])) rest -= threads_of<KH>(a.seg[i]), ++i;
   const RopeSeg &s = a.seg[i];
@@ -139,34 +147,32 @@ __global__ void __launch_bounds__(256) rope_vec_kernel(const RopeArgs a, int per
 
 // Any size, pitch and alignment: a thread per pair or copied element
 template <class DT>
-__global__ void rope_any_kernel(const RopeArgs a, int per_token) {
+__global__ void __launch_bounds__(256) rope_any_kernel(const RopeArgs a, int per_token) {
   using Raw = typename DT::Raw;
-  const int64_t n = a.T * per_token;
-  for (int64_t u = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; u < n;
-       u += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t t = u / per_token;
-    int rest = int(u - t * per_token), i = 0;
-    while (rest >= a.seg[i].heads * (a.seg[i].D - a.seg[i].rot / 2))
-      rest -= a.seg[i].heads * (a.seg[i].D - a.seg[i].rot / 2), ++i;
-    const RopeSeg &s = a.seg[i];
-    const int units = s.D - s.rot / 2, head = rest / units, piece = rest - head * units;
-    Raw *d = dst_of<Raw>(a, s, t, rest == 0);
-    if (!d) continue;
-    const float2 *row = nullptr;
-    if ((s.rot || (s.paged && a.rot)) && !(row = row_of(a, t, rest == 0))) continue;
-    d += head * s.d_head;
-    const Raw *x = static_cast<const Raw *>(s.src) + t * s.s_token + head * s.s_head;
-    if (piece >= s.rot / 2) {
-      d[piece + s.rot / 2] = x[piece + s.rot / 2];
-      continue;
-    }
-    const int o0 = a.layout == WQ_ROPE_HALF ? piece : 2 * piece;
-    const int o1 = a.layout == WQ_ROPE_HALF ? piece + s.rot / 2 : o0 + 1;
-    float f = DT::to_f(x[o0]), g = DT::to_f(x[o1]);
-    turn(f, g, row[piece].x, row[piece].y * a.sign);
-    d[o0] = DT::from_f(f);
-    d[o1] = DT::from_f(g);
+  int64_t t;
+  int rest;
+  if (!place_of(a, per_token, t, rest)) return;
+  int i = 0;
+  while (rest >= a.seg[i].heads * (a.seg[i].D - a.seg[i].rot / 2))
+    rest -= a.seg[i].heads * (a.seg[i].D - a.seg[i].rot / 2), ++i;
+  const RopeSeg &s = a.seg[i];
+  const int units = s.D - s.rot / 2, head = rest / units, piece = rest - head * units;
+  Raw *d = dst_of<Raw>(a, s, t, rest == 0);
+  if (!d) return;
+  const float2 *row = nullptr;
+  if ((s.rot || (s.paged && a.rot)) && !(row = row_of(a, t, rest == 0))) return;
+  d += head * s.d_head;
+  const Raw *x = static_cast<const Raw *>(s.src) + t * s.s_token + head * s.s_head;
+  if (piece >= s.rot / 2) {
+    d[piece + s.rot / 2] = x[piece + s.rot / 2];
+    return;
   }
+  const int o0 = a.layout == WQ_ROPE_HALF ? piece : 2 * piece;
+  const int o1 = a.layout == WQ_ROPE_HALF ? piece + s.rot / 2 : o0 + 1;
+  float f = DT::to_f(x[o0]), g = DT::to_f(x[o1]);
+  turn(f, g, row[piece].x, row[piece].y * a.sign);
+  d[o0] = DT::from_f(f);
+  d[o1] = DT::from_f(g);
 }
 
 // Angles in float64: a float32 angle is off by 2^-8 at position 65536.
@@ -195,8 +201,7 @@ int launch_vec(const RopeArgs &a, cudaStream_t st) {
   int per_token = 0;
   for (int i = 0; i < a.nseg; ++i) per_token += threads_of<KH>(a.seg[i]);
   if (per_token == 0) return WQ_OK;
-  const int tokens = per_token >= 256 ? 1 : 256 / per_token;
-  const dim3 grid(unsigned((a.T + tokens - 1) / tokens), unsigned(per_token >= 256 ? (per_token + 255) / 256 : 1));
+  const dim3 grid = grid_of(a, per_token);
   if (grid.y > 65535) return WQ_ERR_UNSUPPORTED;
   rope_vec_kernel<DT, KH><<<grid, 256, 0, st>>>(a, per_token);
   return launched(1);
@@ -213,8 +218,9 @@ int launch_t(const RopeArgs &a, bool vec, cudaStream_t st) {
   int per_token = 0;
   for (int i = 0; i < a.nseg; ++i) per_token += a.seg[i].heads * (a.seg[i].D - a.seg[i].rot / 2);
   if (per_token == 0) return WQ_OK;
-  const int64_t blocks = (a.T * per_token + 255) / 256;
-  rope_any_kernel<DT><<<unsigned(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, st>>>(a, per_token);
+  const dim3 grid = grid_of(a, per_token);
+  if (grid.y > 65535) return WQ_ERR_UNSUPPORTED;
+  rope_any_kernel<DT><<<grid, 256, 0, st>>>(a, per_token);
   return launched(1);
 }
 
