@@ -586,11 +586,14 @@ WQ_API int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, 
  *   lse[t][a] = ln sum_i exp(scale * q.k_i)            (float, [T][q_heads], may be NULL)
  * with scale > 0.  A row that sees no key gets zeros and -inf.  prefix_len = 0 is ordinary
  * paged attention, max_suffix = 0 the prefix alone.  cu_q NULL: max_q tokens
- * each (T = B * max_q).  max_q and max_suffix are host bounds on the tokens and keys of a
- * sequence: values above them are cut to them, with status = WQ_ERR_INDEX;
- * a page id outside [0, num_pages) sets the same status (its keys are left
- * out or count as zeros).  prefix_len and the bounds are host values, so a
- * graph that records the call keeps them; lengths and pages are device data.
+ * each (T = B * max_q).  Rows of q before cu_q[0] and at or past cu_q[B] (a
+ * batch padded to the size of a recorded graph) are tokens of no sequence and
+ * see no key, not the prefix either.  max_q and max_suffix are host bounds on
+ * the tokens and keys of a sequence: values above them are cut to them, with
+ * status = WQ_ERR_INDEX (the tokens cut off see no key); a page id outside
+ * [0, num_pages) sets the same status (its keys are left out or count as
+ * zeros).  prefix_len and the bounds are host values, so a graph that records
+ * the call keeps them; lengths and pages are device data.
  * Cache places at or past a length are never used, whatever they hold.  A
  * non-finite value in a key or value that only later tokens of the sequence
  * see may spread to earlier ones (a weight of zero times it is taken).

@@ -1,0 +1,95 @@
+"""Attention: what every row of the output holds and how its weights round,
+at the places where sequences, bounds and types end."""
+import pytest
+import torch
+
+import serve_ref as R
+import test_gpu_serve as S
+from w8a8_int8_quantized_token_gb300 import binding as wq
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+def padded_inputs(lead, ql, trail, sl, P, Hkv, G, D, page, dtype):
+    """Inputs whose q has `lead` rows before the first sequence and `trail`
+    after the last, as a batch has that was padded for a recorded graph."""
+    i = S.attn_inputs(ql, sl, P, Hkv, G, D, D, page, dtype, False)
+    i["q"] = S.randn(lead + sum(ql) + trail, Hkv * G, D, dtype=dtype, seed=11, scale=2.0)
+    i["cu_q"] += lead
+    return i
+
+
+def poisoned(i, P, max_suffix, max_q, fill, **kw):
+    """The call with workspace, out and lse full of `fill`."""
+    T, Hq = i["q"].shape[:2]
+    ws = wq.attention_shared_prefix_workspace(i["q"], i["k_cache"], i["v_cache"], len(i["suffix_len"]), P, max_suffix, max_q)
+    ws[:ws.numel() // 4 * 4].view(torch.float32).fill_(fill)
+    out = torch.full((T, Hq, i["v_cache"].shape[-1]), fill, dtype=i["q"].dtype, device="cuda")
+    lse = torch.full((T, Hq), fill, device="cuda")
+    S.attn_call(i, P, max_suffix, max_q, ws=ws, out=out, lse=lse, **kw)
+    return out, lse
+
+
+NO_SEQUENCE = [  # lead, tokens, trail, suffix lengths, P, Hkv, G, D, page, dtype
+    (2, [1, 1], 3, [5, 20], 100, 2, 4, 64, 16, BF),              # few rows: prefix and suffix joined
+    (1, [2, 0, 3], 2, [9, 0, 300], 40, 1, 3, 128, 5, FP),        # ... pages off 16
+    (0, [1] * 40, 8, [30] * 40, 300, 2, 8, 128, 16, BF),         # prefix by row tiles, suffixes by warps
+    (3, [1] * 70, 1, [2] * 70, 700, 4, 8, 64, 16, BF),           # ... blocks of one warp and of four
+    (5, [70, 129], 31, [200, 129], 150, 2, 2, 64, 16, BF),       # both by row tiles, joined
+    (7, [200, 250, 170], 33, [200, 300, 171], 333, 4, 16, 128, 16, FP),  # both in one walk
+    (1, [1, 1], 2, [17, 60], 0, 2, 4, 128, 16, BF),              # suffixes alone, nothing to join
+    (4, [70, 90], 40, [100, 120], 0, 2, 2, 64, 16, FP),          # ... by row tiles
+    (1, [2, 1], 1, [0, 0], 90, 2, 4, 64, 16, BF),                # the prefix alone, nothing to join
+    (2, [30, 0, 30], 9, [0, 0, 0], 100, 2, 4, 128, 16, BF),      # ... by row tiles
+    (2, [30, 30], 9, [0, 0], 30000, 1, 4, 128, 16, BF),          # ... joined
+    (2, [3, 1], 3, [0, 0], 0, 2, 4, 64, 16, BF),                 # no keys at all
+    (0, [0, 0], 4, [8, 9], 50, 1, 2, 64, 16, BF),                # no sequence has a token
+]
+
+
+@pytest.mark.parametrize("lead,ql,trail,sl,P,Hkv,G,D,page,dtype", NO_SEQUENCE)
+@pytest.mark.parametrize("fill", [float("nan"), 50.0])
+def test_rows_of_no_sequence_are_zero(lead, ql, trail, sl, P, Hkv, G, D, page, dtype, fill):
+    """Whatever the buffers held: zeros and -inf there, and the sequences'
+    rows as the definition has them."""
+    i = padded_inputs(lead, ql, trail, sl, P, Hkv, G, D, page, dtype)
+    st = wq.new_status()
+    out, lse = poisoned(i, P, max(sl), max(max(ql), 1), fill, status=st)
+    want, wl, tol, ltol = R.attention(i["q"], i["k_cache"], i["v_cache"], i["prefix_pages"], P, i["page_table"],
+                                      i["suffix_len"], i["cu_q"], D ** -0.5, dtype)
+    own = torch.zeros(len(out), dtype=torch.bool)
+    own[lead:lead + sum(ql)] = True
+    assert (out.cpu()[~own] == 0).all() and (lse.cpu()[~own] == -float("inf")).all()
+    R.check(out, want, tol, "out")
+    R.check(lse, wl, ltol, "lse")
+    assert int(st) == 0
+
+
+CUT = [  # tokens, the bound given, suffix lengths, P, Hkv, G, D, page
+    ([1, 4, 2], 2, [9, 30, 8], 100, 2, 4, 64, 16),       # few rows, joined
+    ([1, 4, 2], 2, [9, 30, 8], 0, 2, 4, 128, 16),        # ... nothing to join
+    ([60, 150, 50], 70, [90, 200, 60], 130, 2, 4, 64, 16),     # row tiles, joined
+    ([200, 330, 170], 210, [200, 400, 171], 333, 4, 16, 64, 16),  # one walk
+    ([1, 4, 2], 2, [0, 0, 0], 100, 2, 4, 64, 16),        # the prefix alone
+    ([40, 90, 30], 40, [0, 0, 0], 100, 2, 4, 64, 16),    # ... by row tiles
+]
+
+
+@pytest.mark.parametrize("ql,most,sl,P,Hkv,G,D,page", CUT)
+@pytest.mark.parametrize("fill", [float("nan"), 50.0])
+def test_tokens_past_the_bound_are_zero_and_reported(ql, most, sl, P, Hkv, G, D, page, fill):
+    i = S.attn_inputs(ql, sl, P, Hkv, G, D, D, page, BF, False)
+    good = S.attn_call(i, P, max(sl), max(ql))
+    st = wq.new_status()
+    out, lse = poisoned(i, P, max(sl), most, fill, status=st)
+    assert int(st) == -6
+    t0 = 0
+    for n in ql:
+        cut = slice(t0 + most, t0 + n)
+        assert (out[cut] == 0).all() and (lse[cut] == -float("inf")).all()
+        assert torch.isfinite(out[t0:t0 + n]).all()
+        if n <= most:  # another split of the same keys: within two roundings of weights and result
+            d = (out[t0:t0 + n].float() - good[t0:t0 + n].float()).abs().max()
+            assert float(d) <= 4 * R.U[BF] * float(i["v_cache"].float().nan_to_num().abs().max())
+        t0 += n

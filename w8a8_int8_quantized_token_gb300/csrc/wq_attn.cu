@@ -77,6 +77,40 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   else return f16x2_rn(lo, hi);
 }
 
+// Rows before cu_q[0], at or past cu_q[B] (a batch padded for a recorded
+// graph) and past max_q in their sequence are tokens of no sequence and see no
+// key: zeros and -inf.  The work on the suffixes writes that or, where there
+// are parts to join, marks the rows for the join by a log-sum-exp that no part
+// has, since the work on the prefix covers all rows.  (Looking each row's
+// sequence up there instead cost the tile kernel 2.5 us a piece.)
+constexpr float kNoSequence = INFINITY;
+
+// For one head: rows r0, r0 + by, ... below r1
+__device__ __forceinline__ void clear_rows(const AttnArgs &a, int head, int r0, int r1, int by) {
+  for (int t = r0; t < r1; t += by) {
+    const int64_t row = int64_t(t) * a.Hq + head * a.G;
+    if (a.o_part && a.max_suffix > 0) {
+      for (int g = threadIdx.x; g < a.G; g += blockDim.x)
+        a.lse_part[(row + g + 1) * a.slots - 1] = kNoSequence;
+    } else {
+      for (int i = threadIdx.x; i < a.G * a.dv / 2; i += blockDim.x) {
+        const int g = 2 * i / a.dv, d = 2 * i - g * a.dv;
+        *reinterpret_cast<uint32_t *>(a.out + t * a.o_token + (head * a.G + g) * a.o_head + d) = 0u;
+      }
+      if (a.lse)
+        for (int g = threadIdx.x; g < a.G; g += blockDim.x) a.lse[row + g] = -INFINITY;
+    }
+  }
+}
+// One block of each (sequence, head) takes the rows past max_q in the sequence
+// and a B-th of those outside [cu_q[0], cu_q[B]).
+__device__ __forceinline__ void clear_rest(const AttnArgs &a, int seq, const Source &s, int head) {
+  const int begin = a.cu_q[0], end = max(a.cu_q[a.B], 0), next = a.cu_q[seq + 1];
+  clear_rows(a, head, s.t0 + s.n, min(next, a.T), 1);
+  if (begin > 0) clear_rows(a, head, seq, min(begin, a.T), a.B);
+  if (end < a.T) clear_rows(a, head, end + seq, a.T, a.B);
+}
+
 // D: padded head size (64 or 128), MT: 16-row tiles
 template <class DT, int D, int MT, int NW>
 struct Small {
@@ -117,9 +151,11 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
     chunk = a.s_chunk;
   }
   const Source s = source_of(a, seq);
+  const bool rest = seq >= 0 && a.cu_q && tile == 0 && split == 0;
   const int rows = min(R, s.n * a.G - tile * R);  // rows of this tile
   const bool last_block = blockIdx.x == gridDim.x - 1;
   if (rows <= 0) {
+    if (rest) clear_rest(a, seq, s, head);
     if (last_block) wait_last_kernel();
     return;
   }
@@ -251,6 +287,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
   uint32_t on[NST - 1];
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) on[i] = issue(i);
+  if (rest) clear_rest(a, seq, s, head);
   for (int i = 0; i < mine; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
     __syncwarp();  // every lane's copies of this piece are in; the slot of piece i - 1 is free
@@ -454,6 +491,8 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
 // Joins the partial results of a row: LANES threads, four columns each, walk
 // its parts, four parts' columns in flight together.  Every thread finds the
 // parts' weights itself (the statistics of a row are a few words of one line).
+// A row of no sequence has its mark in the last slot, and others may hold
+// anything.
 template <class DT, int LANES>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   const int64_t row = int64_t(blockIdx.x) * (256 / LANES) + threadIdx.x / LANES;
@@ -487,12 +526,32 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
       x[3] = __fmaf_rn(v[k].w, w[k], x[3]);
     }
   }
+  if (base == kNoSequence) sum = x[0] = x[1] = x[2] = x[3] = 0.0f;
   const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
   const int64_t t = row / a.Hq, qh = row - t * a.Hq;
   uint32_t *o = reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head + d);
   o[0] = pack2<DT>(x[0] * inv, x[1] * inv);
   o[1] = pack2<DT>(x[2] * inv, x[3] * inv);
   if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : base + logf(sum);
+}
+
+// The rows of no sequence, for calls whose suffixes the tile kernel takes, and
+// (LAST: after all other work) for calls without suffixes: a block per sequence
+// and head.
+template <bool LAST>
+__global__ void __launch_bounds__(128) attn_rest_kernel(const AttnArgs a) {
+  start_next_kernel();
+  const int seq = int(blockIdx.x / unsigned(a.Hkv)), head = int(blockIdx.x % unsigned(a.Hkv));
+  if (LAST) wait_last_kernel();
+  clear_rest(a, seq, source_of(a, seq), head);
+  if (!LAST && blockIdx.x == gridDim.x - 1) wait_last_kernel();
+}
+
+template <bool LAST>
+int launch_rest(const AttnArgs &a, cudaStream_t st) {
+  const int64_t blocks = int64_t(a.B) * a.Hkv;
+  if (blocks >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
+  return launch_chained(attn_rest_kernel<LAST>, unsigned(blocks), 128, 0, true, st, a);
 }
 
 template <class DT, int D, int MT, int NW, bool PAGED>
@@ -525,10 +584,13 @@ int launch_t(const AttnArgs &a, cudaStream_t st) {
   if (rc != WQ_OK) return rc;
   if (wide) rc = two ? launch_warps<DT, 128, 2>(a, st) : launch_warps<DT, 128, 1>(a, st);
   else rc = two ? launch_warps<DT, 64, 2>(a, st) : launch_warps<DT, 64, 1>(a, st);
-  if (rc != WQ_OK || !a.o_part) return rc;
+  if (rc == WQ_OK && a.cu_q && a.tc_suffix) rc = launch_rest<false>(a, st);
   const int64_t rows = int64_t(a.T) * a.Hq;
-  return a.dv <= 64 ? launch_chained(attn_join_kernel<DT, 16>, unsigned((rows + 15) / 16), 256, 0, true, st, a)
+  if (rc == WQ_OK && a.o_part)
+    rc = a.dv <= 64 ? launch_chained(attn_join_kernel<DT, 16>, unsigned((rows + 15) / 16), 256, 0, true, st, a)
                     : launch_chained(attn_join_kernel<DT, 32>, unsigned((rows + 7) / 8), 256, 0, true, st, a);
+  if (rc == WQ_OK && a.cu_q && a.ss == 0) rc = launch_rest<true>(a, st);
+  return rc;
 }
 
 }  // namespace
