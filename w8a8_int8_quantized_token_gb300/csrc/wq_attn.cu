@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
       x[3] = __fmaf_rn(v[k].w, w[k], x[3]);
     }
   }
-  if (base == kNoSequence) sum = x[0] = x[1] = x[2] = x[3] = 0.0f;
+  if (mx == kNoSequence) sum = x[0] = x[1] = x[2] = x[3] = 0.0f;
   const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : (sum == 0.0f ? 0.0f : sum);
   const int64_t t = row / a.Hq, qh = row - t * a.Hq;
   uint32_t *o = reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head + d);
