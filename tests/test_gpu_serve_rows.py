@@ -93,3 +93,39 @@ def test_tokens_past_the_bound_are_zero_and_reported(ql, most, sl, P, Hkv, G, D,
             d = (out[t0:t0 + n].float() - good[t0:t0 + n].float()).abs().max()
             assert float(d) <= 4 * R.U[BF] * float(i["v_cache"].float().nan_to_num().abs().max())
         t0 += n
+
+
+KERNELS = [  # tokens of each sequence, suffix keys, Hkv, G, D, page: which kernel the keys take
+    ([1, 1], 3, 1, 4, 64, 16),            # few rows, blocks of four warps
+    ([1] * 3, 40, 2, 8, 128, 5),          # ... pages off 16
+    ([4] * 16, 200, 4, 8, 128, 16),       # suffixes by blocks of one warp, prefix by row tiles
+    ([1] * 9, 3, 1, 8, 64, 16),           # prefix by row tiles (one), heads of 64
+    ([1] * 40, 3, 1, 8, 128, 16),         # ... two row tiles, heads of 128
+    ([70, 90], 150, 2, 4, 64, 16),        # suffixes by row tiles
+    ([70, 90], 150, 2, 4, 128, 32),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("ql,L,Hkv,G,D,page", KERNELS)
+def test_scores_too_large_for_one_octave(ql, L, Hkv, G, D, page, dtype):
+    """Scores around 2^32, where neighbouring float32 numbers are 512 apart:
+    the one key that is ahead of all others (by an eighth) has weight one,
+    the others none, so the result is its value to the bit (a 16-bit weight
+    times a 16-bit value is exact in float32)."""
+    P, B = 150, len(ql)
+    i = S.attn_inputs(ql, [L] * B, P, Hkv, G, D, D, page, dtype, False, hole=0.0)
+    keys = i["k_cache"]
+    keys.fill_(2.0 ** 14)
+    top = 77
+    keys[int(i["prefix_pages"][top // page]), :, top % page] = 1.125 * 2.0 ** 14
+    # heads and tokens with other significands: the offset's rounding errs either way
+    s = 1 + torch.arange(i["q"].shape[0] * Hkv * G, device="cuda").remainder(113).float() / 128
+    i["q"].copy_((s.view(-1, Hkv * G, 1) * 2.0 ** 14).expand_as(i["q"]))
+    lse = torch.empty(i["q"].shape[:2], device="cuda")
+    out = S.attn_call(i, P, L, max(ql), scale=0.125, lse=lse)
+    v = i["v_cache"][int(i["prefix_pages"][top // page]), :, top % page]
+    assert torch.equal(out, v.repeat_interleave(G, 0).expand_as(out))
+    want = s.double().view(-1, Hkv * G) * 1.125 * 2.0 ** 28 * D * 0.125
+    # a product rounded to float32, times the scale (rounded twice), times ln 2 (rounded twice)
+    R.check(lse, want.cpu(), (6 * R.E * want).cpu(), "lse")

@@ -356,14 +356,16 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float neg = m_[m][h] == -INFINITY ? 0.0f : -m_[m][h] * a.scale_log2;
+        // subtracted before it is scaled: m * c is rounded, by 2^-8 at 2^16 and by
+        // any power of two far past it
+        const float at = m_[m][h] == -INFINITY ? 0.0f : m_[m][h];
         float sum = 0.0f;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float &x = sc[m][n][h * 2 + e];
-            x = ex2(__fmaf_rn(x, a.scale_log2, neg));
+            x = ex2((x - at) * a.scale_log2);
             sum += x;
           }
         l_[m][h] += sum;
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if ((lane & 3) == 0) {
-        xm[warp][r] = m_[m][h] == -INFINITY ? -INFINITY : m_[m][h] * a.scale_log2;
+        xm[warp][r] = m_[m][h];
         xl[warp][r] = l;
       }
       float *w = xo + (warp * R + r) * PITCH + (lane & 3) * 2;
@@ -454,13 +456,13 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
     float f[NW], l = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      f[w] = ex2(xm[w][r] - base);
+      f[w] = ex2((xm[w][r] - base) * a.scale_log2);
       l = __fmaf_rn(xl[w][r], f[w], l);
     }
     const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
     const int j = (row0 + r) / a.G, g = (row0 + r) - j * a.G;
     const int64_t t = s.t0 + j, qh = head * a.G + g;
-    const float lse = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+    const float lse = l == 0.0f ? -INFINITY : (mx * a.scale_log2 + log2f(l)) * 0.6931471805599453f;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int d = c * 64 + lane * 2;

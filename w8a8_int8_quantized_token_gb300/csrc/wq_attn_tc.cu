@@ -632,6 +632,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     uint32_t ends = 0;  // signals on this row tile's products so far
     int q = 0;          // pieces with keys so far
     float m = -INFINITY, l = 0.0f;
+    // A weight is exp2(s * c - m * c) in one fused operation whose second term is
+    // rounded first.  Where that would show (m * c past 2^16: 2^-8 there, and far
+    // past it the largest weight would be any power of two), the warp subtracts
+    // m from the scores before it scales them.
+    constexpr float kFar = 65536.0f;
+    bool far = false;
     pieces([&](const Piece &p, int n, int tiles) {
       // the queries of a piece are released by the eight softmax warps: their
       // tiles serve as staging for the piece's results
@@ -659,6 +665,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (p.open) {
         m = -INFINITY;
         l = 0.0f;
+        far = false;
       }
       for (int j = 0; j < n; ++j, k += uint32_t(tiles)) {
         const int kb = p.k0 + j * BN;
@@ -717,7 +724,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top_of(i);
         const bool grow = top > m && !((top - m) * sl2 <= 8.0f);
-        if (__any_sync(0xffffffffu, grow)) {
+        if (__any_sync(0xffffffffu, grow || far)) {
           const float f = grow && m != -INFINITY ? ex2((m - top) * sl2) : 1.0f;
           if (grow) m = top;
           l *= f;
@@ -743,8 +750,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               tmem_st16(to + 16 * i, o);
             }
           }
+          const float at = m == -INFINITY ? 0.0f : m;
+          far = __any_sync(0xffffffffu, fabsf(at) * sl2 > kFar);
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[i][e] = __float_as_uint(__uint_as_float(v[i][e]) - at);
+          }
         }
-        const float neg = m == -INFINITY ? 0.0f : -m * sl2;
+        const float neg = far || m == -INFINITY ? 0.0f : -m * sl2;
         weigh(0, neg);
         hand_over(0);
         weigh(1, neg);
