@@ -129,3 +129,34 @@ def test_scores_too_large_for_one_octave(ql, L, Hkv, G, D, page, dtype):
     want = s.double().view(-1, Hkv * G) * 1.125 * 2.0 ** 28 * D * 0.125
     # a product rounded to float32, times the scale (rounded twice), times ln 2 (rounded twice)
     R.check(lse, want.cpu(), (6 * R.E * want).cpu(), "lse")
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("ql,L,Hkv,G,D,page", [k for k in KERNELS if k[-1] >= 16])
+def test_fp16_keeps_weights_far_below_the_largest(ql, L, Hkv, G, D, page, first):
+    """One key far ahead of 2^14 others that weigh about 2^-26 of it each: in all
+    they have 2^-12 of the result, and all of it where the key's value is 0."""
+    P, B, q0 = 16384, len(ql), 16.0
+    i = S.attn_inputs(ql, [L] * B, P, Hkv, G, D, D, page, FP, False, hole=0.0)
+    i["k_cache"].zero_()
+    i["v_cache"].fill_(1.0)
+    i["v_cache"][..., 1::2] = 4096.0
+    top = 5 if first else P - 5
+    page_of = int(i["prefix_pages"][top // page])
+    # score of the key: log2 e * 16 * k0 = 26 with q = (16, 0, ...), scale 1
+    k0 = torch.tensor(26 / 1.4426950408889634 / q0).half()
+    i["k_cache"][page_of, :, top % page, 0] = k0
+    i["v_cache"][page_of, :, top % page] = 0.0
+    i["q"].zero_()
+    i["q"][..., 0] = q0
+    out = S.attn_call(i, P, L, max(ql), scale=1.0)
+    want, _, _, _ = R.attention(i["q"], i["k_cache"], i["v_cache"], i["prefix_pages"], P, i["page_table"],
+                                i["suffix_len"], i["cu_q"], 1.0, FP)
+    # A weight is off by half a subnormal step of fp16, 2^-25, where the
+    # largest is at least 2^7; the exponential by 2^-22 and its argument's
+    # rounding, 26 * 2^-24 octaves; a sum of n weights by n * 2^-24; the result
+    # by its own rounding.
+    n = P + L
+    vmax = torch.tensor([1.0, 4096.0] * (D // 2), dtype=torch.float64)
+    tol = R.U[FP] * want.abs() + n * 2.0 ** -32 * vmax + want.abs() * (n * R.E + 64 * R.E)
+    R.check(out, want, tol, "out")

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float &x = sc[m][n][h * 2 + e];
-            x = ex2((x - at) * a.scale_log2);
+            x = ex2(__fmaf_rn(x - at, a.scale_log2, kWeightUp<DT>));
             sum += x;
           }
         l_[m][h] += sum;
@@ -403,8 +403,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
         const int j = (row0 + r) / a.G, g = (row0 + r) - j * a.G;
         const int64_t t = s.t0 + j, qh = head * a.G + g;
         if ((lane & 3) == 0) {
-          const float lse =
-              l == 0.0f ? -INFINITY : (m_[m][h] * a.scale_log2 + log2f(l)) * 0.6931471805599453f;
+          const float lse = lse_of<DT>(m_[m][h], a.scale_log2, l);
           if (a.o_part) a.lse_part[(t * a.Hq + qh) * a.slots + slot] = lse;
           else if (a.lse) a.lse[t * a.Hq + qh] = lse;
         }
@@ -462,7 +461,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
     const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (l == 0.0f ? 0.0f : l);
     const int j = (row0 + r) / a.G, g = (row0 + r) - j * a.G;
     const int64_t t = s.t0 + j, qh = head * a.G + g;
-    const float lse = l == 0.0f ? -INFINITY : (mx * a.scale_log2 + log2f(l)) * 0.6931471805599453f;
+    const float lse = lse_of<DT>(mx, a.scale_log2, l);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int d = c * 64 + lane * 2;

@@ -2,6 +2,8 @@
 // page lookup and the writes of a row's result.
 #pragma once
 
+#include <type_traits>
+
 #include "wq_serve.cuh"
 
 namespace wq {
@@ -32,6 +34,17 @@ __device__ __forceinline__ Source source_of(const AttnArgs &a, int seq) {
   const int l = a.max_suffix > 0 ? a.suffix_len[seq] : 0, len = min(max(l, 0), a.max_suffix);
   if (len != l) set_status(a.status, WQ_ERR_INDEX);
   return {t0, n, len, a.page_table + seq * a.ld_table, a.sp, true};
+}
+
+// Weights are taken 2^7 times their size in fp16 (at most 2^15 with 2^8 for a
+// maximum that is behind), where they would be subnormal below 2^-14 and vanish
+// below 2^-25: now below 2^-21 and 2^-32 of the largest.  The sums carry the
+// same factor, the log-sum-exp takes it off.
+template <class DT>
+constexpr float kWeightUp = std::is_same<DT, F16>::value ? 7.0f : 0.0f;
+template <class DT>
+__device__ __forceinline__ float lse_of(float max, float scale_log2, float sum) {
+  return sum == 0.0f ? -INFINITY : (max * scale_log2 + (log2f(sum) - kWeightUp<DT>)) * 0.6931471805599453f;
 }
 
 // Keys that query token j of the source sees

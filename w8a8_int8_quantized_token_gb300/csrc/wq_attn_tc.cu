@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               for (int e = 0; e < 32; ++e) v[i][e] = __float_as_uint(__uint_as_float(v[i][e]) - at);
           }
         }
-        const float neg = far || m == -INFINITY ? 0.0f : -m * sl2;
+        const float neg = far || m == -INFINITY ? kWeightUp<DT> : __fmaf_rn(-m, sl2, kWeightUp<DT>);
         weigh(0, neg);
         hand_over(0);
         weigh(1, neg);
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       const bool none = l == 0.0f;
       const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : (none ? 0.0f : l);
-      const float lse = none ? -INFINITY : (m * sl2 + log2f(l)) * 0.6931471805599453f;
+      const float lse = lse_of<DT>(m, sl2, l);
       const int64_t tg = p.s.t0 + j0, qh = int64_t(p.head) * a.G + (row - tok * a.G);
       if (mine) {
         if (a.o_part) {
