@@ -160,3 +160,26 @@ def test_fp16_keeps_weights_far_below_the_largest(ql, L, Hkv, G, D, page, first)
     vmax = torch.tensor([1.0, 4096.0] * (D // 2), dtype=torch.float64)
     tol = R.U[FP] * want.abs() + n * 2.0 ** -32 * vmax + want.abs() * (n * R.E + 64 * R.E)
     R.check(out, want, tol, "out")
+
+
+FEW_ROWS = [  # tokens of each sequence, suffix keys, P, Hkv, G, D, page: every part by the kernel for few rows
+    ([1] * 3, 40, 150, 2, 8, 128, 5),        # pages off 16
+    ([1, 1], 90, 200, 4, 16, 64, 16),        # blocks of four warps
+    ([4] * 16, 300, 0, 4, 8, 128, 16),       # blocks of one warp, two row tiles
+    ([1] * 64, 320, 0, 4, 8, 128, 32),       # ... one row tile
+    ([2] * 4, 320, 0, 1, 16, 64, 16),        # two row tiles, heads of 64
+]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("ql,L,P,Hkv,G,D,page", FEW_ROWS)
+def test_average_of_equal_values_is_the_value(ql, L, P, Hkv, G, D, page, dtype):
+    """With the same value at every key the result is that value, however the
+    weights round: they are divided by the sum of what multiplied.  Float32
+    sums of n weights are off by n * 2^-24 (n <= 320: 2^-15.6), under half a
+    step of either type (2^-9, 2^-12), so it is equal to the bit."""
+    i = S.attn_inputs(ql, [L] * len(ql), P, Hkv, G, D, D, page, dtype, False, hole=0.0)
+    v = S.randn(Hkv, 1, D, dtype=dtype, seed=21)
+    i["v_cache"].copy_(v[None].expand_as(i["v_cache"]))
+    out = S.attn_call(i, P, L, max(ql))
+    assert torch.equal(out, v.view(Hkv, D).repeat_interleave(G, 0).expand_as(out))

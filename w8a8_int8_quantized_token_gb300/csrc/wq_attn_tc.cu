@@ -16,8 +16,11 @@
 // Tensor memory: two score buffers of 128 columns (three for D = 64), O0, O1
 // (D each).  P takes the place of its S (64 columns, 16-bit pairs) as the A
 // operand of the second product.  O is rescaled only when a row's maximum has grown by more than
-// 2^8 over the one in use: until then the weights are at most 2^8, their sum
-// stays exact in the same sense, and the final division removes the factor.
+// 2^8 over the one in use: until then the weights are at most 2^8, and the final
+// division removes the factor.  P is rounded to 16 bits as the operand that it is;
+// l sums the weights as they were.  A second sum, of the rounded ones, would
+// divide the result better (error against 64 bits 0.0021 -> 0.0020 in bf16) but
+// takes the softmax 17% longer at D = 64 and 5% at D = 128.
 //
 // The range is cut two ways.  The prefix is the same for all tokens.  A gang
 // of blocks, one per row tile pair, walks the same keys at the same time, so
