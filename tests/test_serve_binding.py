@@ -1,0 +1,100 @@
+"""What the torch binding of the serving operators refuses and passes on, with
+stand-ins for CUDA tensors and for the library: no GPU is touched."""
+import pytest
+import torch
+
+from w8a8_int8_quantized_token_gb300 import binding as wq
+
+BF, I32, I64, F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+
+
+class Cuda:
+    """As much of a CUDA tensor as the binding asks for."""
+
+    def __init__(self, *shape, dtype=BF, stride=None, device=0):
+        self.shape, self.dtype, self._device = torch.Size(shape), dtype, device
+        self._stride = torch.empty(shape, device="meta").stride() if stride is None else stride
+
+    is_cuda = property(lambda self: self._device >= 0)
+    device = property(lambda self: torch.device("cuda", self._device) if self._device >= 0 else torch.device("cpu"))
+    get_device = lambda self: self._device
+    stride = lambda self, dim=None: self._stride if dim is None else self._stride[dim]
+    dim = lambda self: len(self.shape)
+    numel = lambda self: self.shape.numel()
+    data_ptr = lambda self: 4096
+    is_contiguous = lambda self: torch.empty_strided(self.shape, self._stride, device="meta").is_contiguous()
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library calls made: (name, arguments)."""
+    made = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: made.append((name, args)) or 0
+
+    monkeypatch.setattr(wq, "lib", Library)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 77, raising=False)
+    return made
+
+
+def norm_args(**kw):
+    a = dict(block=Cuda(4, 64), residual=Cuda(4, 64), gate=Cuda(64), post="layer", post_weight=Cuda(64),
+             post_bias=Cuda(64), pre="layer", pre_weight=Cuda(64), pre_bias=Cuda(64), x_out=Cuda(4, 64), y=Cuda(4, 64))
+    return {**a, **kw}
+
+
+def rope_args(**kw):
+    a = dict(x=Cuda(4, 2, 64), positions=Cuda(4, dtype=I32), table=Cuda(9, 32, 2, dtype=F32), out=Cuda(4, 2, 64),
+             status=Cuda(1, dtype=I32))
+    return {**a, **kw}
+
+
+def append_args(**kw):
+    a = dict(k=Cuda(4, 2, 64), v=Cuda(4, 2, 32), positions=Cuda(4, dtype=I32), slots=Cuda(4, dtype=I64),
+             table=Cuda(9, 32, 2, dtype=F32), k_cache=Cuda(8, 2, 16, 64), v_cache=Cuda(8, 2, 16, 32), q=Cuda(4, 6, 64),
+             q_out=Cuda(4, 6, 64), status=Cuda(1, dtype=I32))
+    return {**a, **kw}
+
+
+def attention_args(**kw):
+    a = dict(q=Cuda(4, 6, 64), k_cache=Cuda(8, 2, 16, 64), v_cache=Cuda(8, 2, 16, 32), prefix_pages=Cuda(2, dtype=I32),
+             prefix_len=20, page_table=Cuda(3, 2, dtype=I32), suffix_len=Cuda(3, dtype=I32), max_suffix=30,
+             cu_q=Cuda(4, dtype=I32), max_q=2, out=Cuda(4, 6, 32), lse=Cuda(4, 6, dtype=F32),
+             ws=Cuda(1 << 20, dtype=torch.uint8), status=Cuda(1, dtype=I32))
+    return {**a, **kw}
+
+
+ENTRIES = [(wq.block_norm, norm_args), (wq.rope, rope_args), (wq.rope_append_paged, append_args),
+           (wq.attention_shared_prefix, attention_args)]
+TENSORS = [(f, args, name) for f, args in ENTRIES for name, v in args().items()
+           if isinstance(v, Cuda) and name not in ("status", "ws")]
+
+
+@pytest.mark.parametrize("f,args", ENTRIES)
+def test_good_arguments_reach_the_library(calls, f, args):
+    f(**args())
+    assert [name for name, _ in calls] == ["wq_" + f.__name__] and 77 in calls[0][1]
+
+
+@pytest.mark.parametrize("f,args,name", TENSORS)
+@pytest.mark.parametrize("device", [-1, 1])
+def test_every_tensor_has_to_be_on_the_current_device(calls, f, args, name, device):
+    a = args()
+    t = a[name]
+    a[name] = Cuda(*t.shape, dtype=t.dtype, device=device)
+    with pytest.raises(wq.WQError, match="CUDA|cuda"):
+        f(**a)
+    assert not calls
+
+
+@pytest.mark.parametrize("f,args", ENTRIES)
+def test_another_current_device_is_refused(calls, monkeypatch, f, args):
+    """The library launches on the current device: tensors that agree with one
+    another but not with it would be read from the wrong one."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(wq.WQError, match="current device"):
+        f(**args())
+    assert not calls

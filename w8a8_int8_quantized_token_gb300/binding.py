@@ -637,15 +637,30 @@ def linear_w8a8(x, W, sw, scheme="channel", acc="i32", out=None, ws=None, status
 # ---------------------------------------------------------------- the attention half of a layer
 # A decode step makes these calls once per layer with little work behind each,
 # so the checks below ask a tensor for each property once.
-def _raw_stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _device(t, name):
+    """The device of a CUDA tensor; the library launches on the current one, so
+    it has to be that."""
+    dev = t.get_device()
+    if dev < 0:
+        raise WQError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise WQError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _view(t, shape, dtype, name):
+def _same(t, dev, name):
+    if t.get_device() != dev:
+        raise WQError(f"{name} must be a CUDA tensor on cuda:{dev}")
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _view(t, shape, dtype, name, dev):
     """Checks a CUDA tensor of this shape and type whose last dimension is
     contiguous (other strides are free) and returns its strides."""
-    if not t.is_cuda:
-        raise WQError(f"{name} must be a CUDA tensor")
+    _same(t, dev, name)
     if t.dtype is not dtype:
         raise WQError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -656,10 +671,9 @@ def _view(t, shape, dtype, name):
     return st
 
 
-def _dense(t, dtype, name):
+def _dense(t, dtype, name, dev):
     """Checks a contiguous CUDA tensor and returns its shape."""
-    if not t.is_cuda:
-        raise WQError(f"{name} must be a CUDA tensor")
+    _same(t, dev, name)
     if t.dtype is not dtype:
         raise WQError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -667,21 +681,20 @@ def _dense(t, dtype, name):
     return t.shape
 
 
-def _dense_as(t, shape, dtype, name):
-    if _dense(t, dtype, name) != shape:
+def _dense_as(t, shape, dtype, name, dev):
+    if _dense(t, dtype, name, dev) != shape:
         raise WQError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
 
 
 def _code(t, dtypes, dim, name):
-    """The library's type code of a CUDA tensor with `dim` dimensions."""
-    if not t.is_cuda:
-        raise WQError(f"{name} must be a CUDA tensor")
+    """The library's type code of a CUDA tensor with `dim` dimensions, and its device."""
+    dev = _device(t, name)
     if t.dtype not in dtypes:
         raise WQError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if t.dim() != dim:
         raise WQError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    return DTYPE[t.dtype]
+    return DTYPE[t.dtype], dev
 
 
 def _at(t):
@@ -699,30 +712,30 @@ def block_norm(block, residual=None, gate=None, scale=1.0, post="none", post_wei
     block, on rows [T, H]: h = residual + scale * (gate * N_post(block));
     returns (h rounded, N_pre(h)).  post and pre are "none", "rms" or "layer";
     gate is [T, H] or [H]; x_out and y may be given (block or residual too)."""
-    code = _code(block, _FLOATS, 2, "block")
+    code, dev = _code(block, _FLOATS, 2, "block")
     dt, shape = block.dtype, block.shape
     T, H = shape
-    ldb = _view(block, shape, dt, "block")[0]
-    ldr = 0 if residual is None else _view(residual, shape, dt, "residual")[0]
+    ldb = _view(block, shape, dt, "block", dev)[0]
+    ldr = 0 if residual is None else _view(residual, shape, dt, "residual", dev)[0]
     ldg = 0
     if gate is not None:
         if gate.dim() == 1:
-            _view(gate, (H,), dt, "gate")
+            _view(gate, (H,), dt, "gate", dev)
         else:
-            ldg = _view(gate, shape, dt, "gate")[0]
+            ldg = _view(gate, shape, dt, "gate", dev)[0]
     for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
                     (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
         if t is not None:
-            _view(t, (H,), dt, name)
+            _view(t, (H,), dt, name, dev)
     if x_out is None:
         x_out = torch.empty(shape, dtype=dt, device=block.device)
     if y is None:
         y = torch.empty(shape, dtype=dt, device=block.device)
-    ldx, ldy = _view(x_out, shape, dt, "x_out")[0], _view(y, shape, dt, "y")[0]
+    ldx, ldy = _view(x_out, shape, dt, "x_out", dev)[0], _view(y, shape, dt, "y", dev)[0]
     _check(lib().wq_block_norm(
         block.data_ptr(), ldb, _at(residual), ldr, _at(gate), ldg, scale, NORM[post],
         _at(post_weight), _at(post_bias), NORM[pre], _at(pre_weight), _at(pre_bias), eps, T, H, code,
-        x_out.data_ptr(), ldx, y.data_ptr(), ldy, _raw_stream(block)), "wq_block_norm")
+        x_out.data_ptr(), ldx, y.data_ptr(), ldy, _raw_stream(dev)), "wq_block_norm")
     return x_out, y
 
 
@@ -732,14 +745,15 @@ def rope_table(max_pos, rot, base=10000.0, scaling="none", factor=1.0, trained=0
     float64; scaling "none", "linear", "ntk" or "yarn" for contexts `factor`
     times the `trained` one."""
     t = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device or "cuda")
+    dev = _device(t, "table")
     _check(lib().wq_rope_table(t.data_ptr(), max_pos, rot, base, ROPE_SCALING[scaling], factor,
-                               float(trained), beta_fast, beta_slow, mscale, _raw_stream(t)),
+                               float(trained), beta_fast, beta_slow, mscale, _raw_stream(dev)),
            "wq_rope_table")
     return t
 
 
-def _table(table):
-    shape = _dense(table, torch.float32, "table")
+def _table(table, dev):
+    shape = _dense(table, torch.float32, "table", dev)
     if len(shape) != 3 or shape[2] != 2:
         raise WQError(f"table must be [max_pos, rot/2, 2], got {list(shape)}")
     return shape[0], 2 * shape[1]
@@ -748,18 +762,18 @@ def _table(table):
 def rope(x, positions, table, layout="half", inverse=False, out=None, status=None):
     """Rotate the first rot = 2 * table.shape[1] elements of each head of x
     [T, heads, D] to its token's position; out may be x itself."""
-    code = _code(x, _FLOATS, 3, "x")
+    code, dev = _code(x, _FLOATS, 3, "x")
     dt, shape = x.dtype, x.shape
     T, n, D = shape
-    max_pos, rot = _table(table)
-    sx = _view(x, shape, dt, "x")
-    pos = _dense_as(positions, (T,), torch.int32, "positions")
+    max_pos, rot = _table(table, dev)
+    sx = _view(x, shape, dt, "x", dev)
+    pos = _dense_as(positions, (T,), torch.int32, "positions", dev)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=x.device)
-    so = _view(out, shape, dt, "out")
+    so = _view(out, shape, dt, "out", dev)
     _check(lib().wq_rope(x.data_ptr(), sx[0], sx[1], pos, table.data_ptr(), max_pos, T, n, D, rot,
                          ROPE_LAYOUT[layout], 1 if inverse else 0, code, out.data_ptr(), so[0], so[1],
-                         _at(status), _raw_stream(x)), "wq_rope")
+                         _at(status), _raw_stream(dev)), "wq_rope")
     return out
 
 
@@ -769,17 +783,17 @@ _CACHE = struct.Struct("@PPqqqqqqqiiiii0q")  # wq_paged_cache
 def _cache(k_cache, v_cache):
     """The wq_paged_cache of k_cache [pages, heads, page_size, dk] and v_cache
     [pages, heads, page_size, dv], any strides over the first three: its bytes,
-    heads, page size, dk and dv."""
-    code = _code(k_cache, _HALVES, 4, "k_cache")
+    heads, page size, dk, dv and device."""
+    code, dev = _code(k_cache, _HALVES, 4, "k_cache")
     dt, shape = k_cache.dtype, k_cache.shape
     pages, heads, page, dk = shape
-    sk = _view(k_cache, shape, dt, "k_cache")
+    sk = _view(k_cache, shape, dt, "k_cache", dev)
     if v_cache.shape[:3] != shape[:3]:
         raise WQError("k_cache and v_cache must agree in pages, heads and page size")
-    sv = _view(v_cache, v_cache.shape, dt, "v_cache")
+    sv = _view(v_cache, v_cache.shape, dt, "v_cache", dev)
     dv = v_cache.shape[3]
     return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1],
-                       sv[2], pages, page, heads, dk, dv, code), heads, page, dk, dv
+                       sv[2], pages, page, heads, dk, dv, code), heads, page, dk, dv, dev
 
 
 def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="half", q=None,
@@ -787,28 +801,28 @@ def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="h
     """Write rope(k) and v [T, heads, D] at places slots int64 [T] (page *
     page_size + place; negative: skipped) of a paged cache, and with q
     [T, q_heads, D] return rope(q).  table None appends without rotation."""
-    c, heads, _, dk, dv = _cache(k_cache, v_cache)
+    c, heads, _, dk, dv, dev = _cache(k_cache, v_cache)
     dt = k_cache.dtype
     T = k.shape[0]
-    sk, sv = _view(k, (T, heads, dk), dt, "k"), _view(v, (T, heads, dv), dt, "v")
-    to = _dense_as(slots, (T,), torch.int64, "slots")
+    sk, sv = _view(k, (T, heads, dk), dt, "k", dev), _view(v, (T, heads, dv), dt, "v", dev)
+    to = _dense_as(slots, (T,), torch.int64, "slots", dev)
     rot, max_pos, pos = 0, 0, None
     if table is not None:
-        max_pos, rot = _table(table)
-        pos = _dense_as(positions, (T,), torch.int32, "positions")
+        max_pos, rot = _table(table, dev)
+        pos = _dense_as(positions, (T,), torch.int32, "positions", dev)
     nq, sq, so = 0, (0, 0), (0, 0)
     if q is not None:
         shape = q.shape
         if len(shape) != 3 or shape[0] != T or shape[2] != dk:
             raise WQError(f"q must be [{T}, heads, {dk}], got {list(shape)}")
-        nq, sq = shape[1], _view(q, shape, dt, "q")
+        nq, sq = shape[1], _view(q, shape, dt, "q", dev)
         if q_out is None:
             q_out = torch.empty(shape, dtype=dt, device=q.device)
-        so = _view(q_out, shape, dt, "q_out")
+        so = _view(q_out, shape, dt, "q_out", dev)
     _check(lib().wq_rope_append_paged(
         _at(q), sq[0], sq[1], nq, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], pos, to,
         _at(table), max_pos, T, rot, ROPE_LAYOUT[layout], c, _at(q_out) if nq else None, so[0], so[1],
-        _at(status), _raw_stream(k)), "wq_rope_append_paged")
+        _at(status), _raw_stream(dev)), "wq_rope_append_paged")
     return q_out
 
 
@@ -828,23 +842,23 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
     splits the tokens (None: T / B each); max_q and max_suffix bound a
     sequence's tokens and keys.  Returns out [T, q_heads, dv]; lse float32
     [T, q_heads] is filled if given."""
-    c, _, page, dk, dv = _cache(k_cache, v_cache)
+    c, _, page, dk, dv, dev = _cache(k_cache, v_cache)
     dt, shape = k_cache.dtype, q.shape
     if len(shape) != 3 or shape[2] != dk:
         raise WQError(f"q must be [tokens, heads, {dk}] as k_cache has, got {list(shape)}")
     T, Hq = shape[0], shape[1]
-    sq = _view(q, shape, dt, "q")
-    B = _dense(suffix_len, torch.int32, "suffix_len").numel()
+    sq = _view(q, shape, dt, "q", dev)
+    B = _dense(suffix_len, torch.int32, "suffix_len", dev).numel()
     pages = page_table.shape[-1] if page_table.dim() == 2 else 0
-    ld = _view(page_table, (B, pages), torch.int32, "page_table")[0]
+    ld = _view(page_table, (B, pages), torch.int32, "page_table", dev)[0]
     if max_suffix > pages * page:
         raise WQError(f"max_suffix {max_suffix} needs more pages than page_table has columns")
     if prefix_len:
-        _dense(prefix_pages, torch.int32, "prefix_pages")
+        _dense(prefix_pages, torch.int32, "prefix_pages", dev)
         if prefix_pages.numel() * page < prefix_len:
             raise WQError(f"prefix_len {prefix_len} needs more pages than prefix_pages holds")
     if cu_q is not None:
-        _dense_as(cu_q, (B + 1,), torch.int32, "cu_q")
+        _dense_as(cu_q, (B + 1,), torch.int32, "cu_q", dev)
         if max_q is None:
             raise WQError("cu_q needs max_q, the most tokens of a sequence")
     elif B == 0 or T % B:
@@ -853,14 +867,14 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
         max_q = T // B
     if out is None:
         out = torch.empty(T, Hq, dv, dtype=dt, device=q.device)
-    so = _view(out, (T, Hq, dv), dt, "out")
+    so = _view(out, (T, Hq, dv), dt, "out", dev)
     if lse is not None:
-        _dense_as(lse, (T, Hq), torch.float32, "lse")
+        _dense_as(lse, (T, Hq), torch.float32, "lse", dev)
     if ws is None:
         ws = attention_shared_prefix_workspace(q, k_cache, v_cache, B, prefix_len, max_suffix, max_q)
     _check(lib().wq_attention_shared_prefix(
         q.data_ptr(), sq[0], sq[1], T, B, _at(cu_q), max_q, Hq, c, _at(prefix_pages), prefix_len,
         page_table.data_ptr(), ld, suffix_len.data_ptr(), max_suffix,
         dk ** -0.5 if scale is None else scale, out.data_ptr(), so[0], so[1], _at(lse), ws.data_ptr(),
-        ws.numel(), _at(status), _raw_stream(q)), "wq_attention_shared_prefix")
+        ws.numel(), _at(status), _raw_stream(dev)), "wq_attention_shared_prefix")
     return out
