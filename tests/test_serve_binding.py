@@ -21,6 +21,7 @@ class Cuda:
     stride = lambda self, dim=None: self._stride if dim is None else self._stride[dim]
     dim = lambda self: len(self.shape)
     numel = lambda self: self.shape.numel()
+    element_size = lambda self: torch.empty((), dtype=self.dtype).element_size()
     data_ptr = lambda self: 4096
     is_contiguous = lambda self: torch.empty_strided(self.shape, self._stride, device="meta").is_contiguous()
 
@@ -88,6 +89,28 @@ def test_every_tensor_has_to_be_on_the_current_device(calls, f, args, name, devi
     with pytest.raises(wq.WQError, match="CUDA|cuda"):
         f(**a)
     assert not calls
+
+
+BAD_BUFFERS = [(f, args, name, bad) for f, args in ENTRIES for name in ("status", "ws") if name in args()
+               for bad in [dict(device=-1), dict(device=1), dict(stride=(0,))] +
+               ([dict(dtype=F32), dict(shape=(0,))] if name == "status" else [])]
+
+
+@pytest.mark.parametrize("f,args,name,bad", BAD_BUFFERS)
+def test_buffers_that_kernels_write_are_checked(calls, f, args, name, bad):
+    """A status in host memory or a workspace that repeats one byte would be
+    written at an address, or to a length, that is not there."""
+    a = args()
+    kw = {**dict(shape=(4096,), dtype=a[name].dtype), **bad}
+    a[name] = Cuda(*kw.pop("shape"), **kw)
+    with pytest.raises(wq.WQError, match=name):
+        f(**a)
+    assert not calls
+
+
+def test_a_workspace_counts_in_bytes(calls):
+    wq.attention_shared_prefix(**attention_args(ws=Cuda(1234, dtype=F32)))
+    assert calls[0][1][-3] == 4 * 1234
 
 
 @pytest.mark.parametrize("f,args", ENTRIES)

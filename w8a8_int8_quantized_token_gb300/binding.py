@@ -701,6 +701,16 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _status(t, dev):
+    """The address of a status word (new_status), which kernels write."""
+    if t is None:
+        return None
+    _dense(t, torch.int32, "status", dev)
+    if t.numel() < 1:
+        raise WQError("status must hold one int32")
+    return t.data_ptr()
+
+
 _FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 _HALVES = (torch.bfloat16, torch.float16)
 
@@ -773,7 +783,7 @@ def rope(x, positions, table, layout="half", inverse=False, out=None, status=Non
     so = _view(out, shape, dt, "out", dev)
     _check(lib().wq_rope(x.data_ptr(), sx[0], sx[1], pos, table.data_ptr(), max_pos, T, n, D, rot,
                          ROPE_LAYOUT[layout], 1 if inverse else 0, code, out.data_ptr(), so[0], so[1],
-                         _at(status), _raw_stream(dev)), "wq_rope")
+                         _status(status, dev), _raw_stream(dev)), "wq_rope")
     return out
 
 
@@ -822,7 +832,7 @@ def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="h
     _check(lib().wq_rope_append_paged(
         _at(q), sq[0], sq[1], nq, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], pos, to,
         _at(table), max_pos, T, rot, ROPE_LAYOUT[layout], c, _at(q_out) if nq else None, so[0], so[1],
-        _at(status), _raw_stream(dev)), "wq_rope_append_paged")
+        _status(status, dev), _raw_stream(dev)), "wq_rope_append_paged")
     return q_out
 
 
@@ -872,9 +882,11 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
         _dense_as(lse, (T, Hq), torch.float32, "lse", dev)
     if ws is None:
         ws = attention_shared_prefix_workspace(q, k_cache, v_cache, B, prefix_len, max_suffix, max_q)
+    else:
+        _dense(ws, ws.dtype, "ws", dev)
     _check(lib().wq_attention_shared_prefix(
         q.data_ptr(), sq[0], sq[1], T, B, _at(cu_q), max_q, Hq, c, _at(prefix_pages), prefix_len,
         page_table.data_ptr(), ld, suffix_len.data_ptr(), max_suffix,
         dk ** -0.5 if scale is None else scale, out.data_ptr(), so[0], so[1], _at(lse), ws.data_ptr(),
-        ws.numel(), _at(status), _raw_stream(dev)), "wq_attention_shared_prefix")
+        ws.numel() * ws.element_size(), _status(status, dev), _raw_stream(dev)), "wq_attention_shared_prefix")
     return out
