@@ -121,3 +121,12 @@ def test_another_current_device_is_refused(calls, monkeypatch, f, args):
     with pytest.raises(wq.WQError, match="current device"):
         f(**args())
     assert not calls
+
+
+@pytest.mark.parametrize("f,args", ENTRIES[2:])
+@pytest.mark.parametrize("shape", [(8, 2, 16, 32, 2), (8, 2, 16), (8, 2, 15, 32), (7, 2, 16, 32), (8, 3, 16, 32)])
+def test_v_cache_has_the_pages_of_k_cache(calls, f, args, shape):
+    """A fifth dimension would make the fourth one's elements lie apart."""
+    with pytest.raises(wq.WQError, match="v_cache"):
+        f(**args(v_cache=Cuda(*shape)))
+    assert not calls

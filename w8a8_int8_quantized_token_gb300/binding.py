@@ -798,8 +798,9 @@ def _cache(k_cache, v_cache):
     dt, shape = k_cache.dtype, k_cache.shape
     pages, heads, page, dk = shape
     sk = _view(k_cache, shape, dt, "k_cache", dev)
-    if v_cache.shape[:3] != shape[:3]:
-        raise WQError("k_cache and v_cache must agree in pages, heads and page size")
+    if v_cache.dim() != 4 or v_cache.shape[:3] != shape[:3]:
+        raise WQError(f"v_cache must be {list(shape[:3])} and the elements of a value, as k_cache has, "
+                      f"got {list(v_cache.shape)}")
     sv = _view(v_cache, v_cache.shape, dt, "v_cache", dev)
     dv = v_cache.shape[3]
     return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1],
