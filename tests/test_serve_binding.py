@@ -130,3 +130,36 @@ def test_v_cache_has_the_pages_of_k_cache(calls, f, args, shape):
     with pytest.raises(wq.WQError, match="v_cache"):
         f(**args(v_cache=Cuda(*shape)))
     assert not calls
+
+
+def passed(calls, f, **kw):
+    del calls[:]
+    f(**kw)
+    return [a for a in calls[0][1] if isinstance(a, int)]
+
+
+def test_dimensions_of_one_element_may_have_any_stride(calls):
+    """As torch.empty(64, 1).t() has: the call is that with a contiguous tensor."""
+    one = lambda **kw: norm_args(block=Cuda(1, 64), residual=Cuda(1, 64), x_out=Cuda(1, 64), y=Cuda(1, 64), **kw)
+    want = passed(calls, wq.block_norm, **one())
+    for name in ("block", "residual", "x_out", "y"):
+        assert passed(calls, wq.block_norm, **{**one(), name: Cuda(1, 64, stride=(1, 1))}) == want
+        assert passed(calls, wq.block_norm, **{**one(), name: Cuda(1, 64, stride=(0, 1))}) == want
+    single = lambda **kw: attention_args(q=Cuda(1, 1, 64), k_cache=Cuda(8, 1, 16, 64), v_cache=Cuda(8, 1, 16, 32),
+                                         page_table=Cuda(1, 2, dtype=I32), suffix_len=Cuda(1, dtype=I32),
+                                         cu_q=Cuda(2, dtype=I32), out=Cuda(1, 1, 32), lse=None, **kw)
+    want = passed(calls, wq.attention_shared_prefix, **single())
+    for kw in (dict(page_table=Cuda(1, 2, dtype=I32, stride=(1, 1))), dict(q=Cuda(1, 1, 64, stride=(3, 5, 1))),
+               dict(out=Cuda(1, 1, 32, stride=(0, 7, 1)))):
+        assert passed(calls, wq.attention_shared_prefix, **{**single(), **kw}) == want
+
+
+def test_other_strides_go_as_they_are(calls):
+    wq.block_norm(**norm_args(block=Cuda(4, 64, stride=(80, 1))))
+    assert calls[0][1][1] == 80
+    del calls[:]
+    wq.rope(**rope_args(x=Cuda(4, 2, 64, stride=(900, 200, 1))))
+    assert calls[0][1][1:3] == (900, 200)
+    del calls[:]
+    wq.rope(**rope_args(x=Cuda(4, 1, 64, stride=(900, 7, 1)), out=Cuda(4, 1, 64)))
+    assert calls[0][1][1:3] == (900, 64)

@@ -659,7 +659,9 @@ def _raw_stream(dev):
 
 def _view(t, shape, dtype, name, dev):
     """Checks a CUDA tensor of this shape and type whose last dimension is
-    contiguous (other strides are free) and returns its strides."""
+    contiguous (other strides are free) and returns its strides.  A dimension
+    of one element has any stride in torch: here the one that a contiguous
+    tensor would have, which every entry takes."""
     _same(t, dev, name)
     if t.dtype is not dtype:
         raise WQError(f"{name} must be {dtype}, got {t.dtype}")
@@ -668,6 +670,12 @@ def _view(t, shape, dtype, name, dev):
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise WQError(f"{name} must be contiguous in its last dimension")
+    if 1 in shape:
+        st = list(st)
+        st[-1] = 1
+        for i in range(len(st) - 2, -1, -1):
+            if shape[i] == 1:
+                st[i] = shape[i + 1] * st[i + 1]
     return st
 
 
