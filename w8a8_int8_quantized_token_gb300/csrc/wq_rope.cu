@@ -215,11 +215,9 @@ int launch_t(const RopeArgs &a, bool vec, cudaStream_t st) {
     for (int i = 0; i < a.nseg; ++i) units += a.T * a.seg[i].heads * units_of(a.seg[i]);
     if (vec) return units > 4 * 256 * 152 * 4 ? launch_vec<DT, 4>(a, st) : launch_vec<DT, 1>(a, st);
   }
-  int per_token = 0;
-  for (int i = 0; i < a.nseg; ++i) per_token += a.seg[i].heads * (a.seg[i].D - a.seg[i].rot / 2);
+  const int per_token = int(rope_pair_threads(a));  // at most kRopeMostThreads
   if (per_token == 0) return WQ_OK;
   const dim3 grid = grid_of(a, per_token);
-  if (grid.y > 65535) return WQ_ERR_UNSUPPORTED;
   rope_any_kernel<DT><<<grid, 256, 0, st>>>(a, per_token);
   return launched(1);
 }

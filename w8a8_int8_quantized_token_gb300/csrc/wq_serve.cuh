@@ -155,6 +155,13 @@ struct RopeArgs {
   float sign;  // -1: inverse
   int32_t *status;
 };
+// Threads that a token takes pair by pair, and the most that a launch has room for
+inline int64_t rope_pair_threads(const RopeArgs &a) {
+  int64_t n = 0;
+  for (int i = 0; i < a.nseg; ++i) n += int64_t(a.seg[i].heads) * (a.seg[i].D - a.seg[i].rot / 2);
+  return n;
+}
+constexpr int64_t kRopeMostThreads = 65535 * 256;
 int launch_rope(const RopeArgs &a, int dtype, bool vec, cudaStream_t st);
 int launch_rope_table(float *table, int64_t max_pos, int rot, double base, int scaling,
                       double factor, double trained, double beta_fast, double beta_slow,

@@ -150,9 +150,11 @@ int wq_rope(const void *x, int64_t x_token, int64_t x_head, const int32_t *posit
   a.layout = layout;
   a.sign = inverse ? -1.0f : 1.0f;
   a.status = status;
+  const bool vec = rope_vec_ok(a, dtype);
+  if (!vec && rope_pair_threads(a) > kRopeMostThreads) return WQ_ERR_UNSUPPORTED;
   const int rc = device_ok();
   if (rc != WQ_OK) return rc;
-  return launch_rope(a, dtype, rope_vec_ok(a, dtype), stream);
+  return launch_rope(a, dtype, vec, stream);
 }
 
 int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, int q_heads,
@@ -193,9 +195,11 @@ int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, int q_h
   a.layout = layout;
   a.sign = 1.0f;
   a.status = status;
+  const bool vec = rope_vec_ok(a, cache->dtype);
+  if (!vec && rope_pair_threads(a) > kRopeMostThreads) return WQ_ERR_UNSUPPORTED;
   const int rc = device_ok();
   if (rc != WQ_OK) return rc;
-  return launch_rope(a, cache->dtype, rope_vec_ok(a, cache->dtype), stream);
+  return launch_rope(a, cache->dtype, vec, stream);
 }
 
 size_t wq_attention_shared_prefix_workspace_size(int64_t T, int B, int max_q, int q_heads,
