@@ -1,5 +1,8 @@
 """Sizes at the ends of their ranges, on the host: no GPU is touched."""
 import ctypes
+import os
+import re
+import subprocess
 
 import pytest
 
@@ -34,3 +37,36 @@ def test_append_refuses_more_elements_than_a_launch_has_threads_for(lib):
 def test_rope_refuses_more_pairs_than_a_launch_has_threads_for(lib):
     call = lambda heads, D: lib.wq_rope(FAKE, 1, 1, FAKE, FAKE, 9, 4, heads, D, 2, 0, 0, 2, FAKE, 1, 1, None, None)
     assert call(65536, 16384) == UNSUPPORTED and call(65536, 257) == UNSUPPORTED  # the pair counts as one
+
+
+ONCE = r"""
+#include <cstdio>
+#include "wq_once.h"
+int main() {
+  wq::OncePerDevice once;
+  int calls = 0;
+  bool works = false;
+  auto set = [&] { ++calls; return works; };
+  auto step = [&](int device) { const bool ok = once(device, set); printf("%d%d ", ok, calls); };
+  step(0); step(0);              // a failure is not kept
+  works = true;
+  step(0); step(0);              // a success is
+  step(63); step(63); step(0);   // for its device alone
+  works = false;
+  step(5); step(63);
+}
+"""
+
+
+def test_kernels_are_set_up_on_every_device_and_after_a_failure(tmp_path):
+    src = tmp_path / "once.cpp"
+    src.write_text(ONCE)
+    subprocess.run(["g++", "-std=c++17", "-I", build_lib.CSRC, str(src), "-o", str(tmp_path / "once")], check=True)
+    out = subprocess.run([str(tmp_path / "once")], capture_output=True, text=True, check=True).stdout
+    assert out.split() == ["01", "02", "13", "13", "14", "14", "14", "05", "15"]
+
+
+@pytest.mark.parametrize("name", ["wq_attn.cu", "wq_attn_tc.cu", "wq_block_norm.cu"])
+def test_no_kernel_keeps_its_set_up_for_the_process(name):
+    text = open(os.path.join(build_lib.CSRC, name)).read()
+    assert "allow_smem(sized" in text and not re.search(r"static bool|cudaFuncSetAttribute", text)

@@ -574,9 +574,8 @@ template <class DT, int D, int MT, int NW, bool PAGED>
 int launch_small(const AttnArgs &a, cudaStream_t st) {
   using P = Small<DT, D, MT, NW>;
   auto *k = attn_small_kernel<DT, D, MT, NW, PAGED>;
-  static bool sized = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           P::SMEM) == cudaSuccess;
-  if (!sized) return WQ_ERR_LAUNCH;
+  static OncePerDevice sized;
+  if (!allow_smem(sized, k, P::SMEM)) return WQ_ERR_LAUNCH;
   constexpr int R = 16 * MT;
   const int64_t pt = (int64_t(a.T) * a.G + R - 1) / R, stl = (int64_t(a.max_q) * a.G + R - 1) / R;
   const int64_t pi = a.tc_prefix || a.whole ? 0 : a.sp * pt * a.Hkv;

@@ -874,9 +874,8 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 template <class DT, int D>
 int launch_one(const AttnArgs &a, Cut c, int64_t blocks, cudaStream_t st) {
   auto *k = attn_tile_kernel<DT, D>;
-  static bool sized = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           Plan<D>::SMEM) == cudaSuccess;
-  if (!sized) return WQ_ERR_LAUNCH;
+  static OncePerDevice sized;
+  if (!allow_smem(sized, k, Plan<D>::SMEM)) return WQ_ERR_LAUNCH;
   CUtensorMap mq, mk, mv;
   auto pitch = [](int64_t extent, int64_t stride) { return extent == 1 && stride == 0 ? 8 : stride; };
   const int64_t qd[3] = {a.dk, a.Hq, a.T};

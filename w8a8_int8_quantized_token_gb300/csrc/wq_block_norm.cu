@@ -411,9 +411,8 @@ __global__ void __launch_bounds__(512) block_norm_any_kernel(const BlockNormArgs
 template <class DT>
 int launch_any(const BlockNormArgs &a, cudaStream_t st) {
   auto *k = block_norm_any_kernel<DT>;
-  static bool sized =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 32768 * 4) == cudaSuccess;
-  if (!sized) return WQ_ERR_LAUNCH;
+  static OncePerDevice sized;
+  if (!allow_smem(sized, k, 32768 * 4)) return WQ_ERR_LAUNCH;
   const int threads = std::min(512, (a.H + 31) / 32 * 32);
   k<<<unsigned(a.T), threads, a.H * 4, st>>>(a);
   return launched(1);
@@ -432,9 +431,8 @@ inline int threads_for(int pieces, int nv) { return ((pieces + nv - 1) / nv + 31
 template <class DT, int NV, bool GATE, bool FULL>
 int launch_stream_g(const BlockNormArgs &a, int pieces, cudaStream_t st) {
   auto *k = block_norm_stream_kernel<DT, NV, GATE, FULL>;
-  static bool sized = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           2 * (GATE ? 3 : 2) * 256 * NV * 16) == cudaSuccess;
-  if (!sized) return WQ_ERR_LAUNCH;
+  static OncePerDevice sized;
+  if (!allow_smem(sized, k, 2 * (GATE ? 3 : 2) * 256 * NV * 16)) return WQ_ERR_LAUNCH;
   const int threads = threads_for(pieces, NV), smem = 2 * (GATE ? 3 : 2) * threads * NV * 16;
   // as many blocks as fit: three of 256 threads by registers, fewer by shared memory
   const int per_sm = std::max(1, std::min(768 / threads, std::min(233472 / (smem + 2048), 8)));

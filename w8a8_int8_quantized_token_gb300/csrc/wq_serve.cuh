@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "wq_common.cuh"
+#include "wq_once.h"
 
 namespace wq {
 
@@ -122,6 +123,18 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // ---- launchers (host) ----
 int device_ok();  // WQ_OK on an sm_103 device
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device
+template <class Kernel>
+bool allow_smem(OncePerDevice &once, Kernel *k, int bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  return once(dev, [&] {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) return true;
+    cudaGetLastError();  // told by the return value: no later launch is to report it
+    return false;
+  });
+}
 
 struct BlockNormArgs {
   const void *block, *residual, *gate, *w_post, *b_post, *w_pre, *b_pre;
