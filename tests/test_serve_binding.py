@@ -36,7 +36,7 @@ def calls(monkeypatch):
             return lambda *args: made.append((name, args)) or 0
 
     monkeypatch.setattr(wq, "lib", Library)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 77, raising=False)
     return made
 
@@ -117,7 +117,7 @@ def test_a_workspace_counts_in_bytes(calls):
 def test_another_current_device_is_refused(calls, monkeypatch, f, args):
     """The library launches on the current device: tensors that agree with one
     another but not with it would be read from the wrong one."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
     with pytest.raises(wq.WQError, match="current device"):
         f(**args())
     assert not calls

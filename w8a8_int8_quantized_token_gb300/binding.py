@@ -637,53 +637,89 @@ def linear_w8a8(x, W, sw, scheme="channel", acc="i32", out=None, ws=None, status
 # ---------------------------------------------------------------- the attention half of a layer
 # A decode step makes these calls once per layer with little work behind each,
 # so the checks below ask a tensor for each property once.
-def _device(t, name):
-    """The device of a CUDA tensor; the library launches on the current one, so
-    it has to be that."""
+_TC = torch._C
+
+
+def _main(t, dtypes, dim, name):
+    """Type code, device, type and shape of a call's main tensor: a CUDA tensor
+    with `dim` dimensions on the current device, where the library launches."""
     dev = t.get_device()
     if dev < 0:
         raise WQError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise WQError(f"{name} is on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev
+    if dev != _TC._cuda_getDevice():
+        raise WQError(f"{name} is on cuda:{dev}, but the current device is cuda:{_TC._cuda_getDevice()}")
+    dt, shape = t.dtype, t.shape
+    if dt not in dtypes:
+        raise WQError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {dt}")
+    if len(shape) != dim:
+        raise WQError(f"{name} must have {dim} dimensions, got {len(shape)}")
+    return DTYPE[dt], dev, dt, shape
 
 
-def _same(t, dev, name):
+def _of(t, dtype, name, dev):
+    """Checks type and device of another tensor of the call."""
     if t.get_device() != dev:
         raise WQError(f"{name} must be a CUDA tensor on cuda:{dev}")
-
-
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-def _view(t, shape, dtype, name, dev):
-    """Checks a CUDA tensor of this shape and type whose last dimension is
-    contiguous (other strides are free) and returns its strides.  A dimension
-    of one element has any stride in torch: here the one that a contiguous
-    tensor would have, which every entry takes."""
-    _same(t, dev, name)
     if t.dtype is not dtype:
         raise WQError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _as(t, shape, dtype, name, dev):
+    """Checks type, device and shape of another tensor of the call."""
+    if t.get_device() != dev or t.dtype is not dtype:
+        _of(t, dtype, name, dev)
     if t.shape != shape:
         raise WQError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
+
+
+# Pitches of a tensor whose last dimension is contiguous; other strides are
+# free.  A dimension of one element has any stride in torch: here the one that a
+# contiguous tensor would have, which every entry takes.
+def _rows(t, shape, name):
+    n0, n1 = shape
+    s0, s1 = t.stride()
+    if s1 != 1 and n1 > 1:
         raise WQError(f"{name} must be contiguous in its last dimension")
-    if 1 in shape:
-        st = list(st)
-        st[-1] = 1
-        for i in range(len(st) - 2, -1, -1):
-            if shape[i] == 1:
-                st[i] = shape[i + 1] * st[i + 1]
-    return st
+    return s0 if n0 != 1 else n1
+
+
+def _heads(t, shape, name):
+    n0, n1, n2 = shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and n2 > 1:
+        raise WQError(f"{name} must be contiguous in its last dimension")
+    if n1 == 1:
+        s1 = n2
+    return (s0 if n0 != 1 else n1 * s1), s1
+
+
+def _pages(t, shape, name):
+    n0, n1, n2, n3 = shape
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1 and n3 > 1:
+        raise WQError(f"{name} must be contiguous in its last dimension")
+    if n2 == 1:
+        s2 = n3
+    if n1 == 1:
+        s1 = n2 * s2
+    return (s0 if n0 != 1 else n1 * s1), s1, s2
+
+
+def _rows_as(t, shape, dtype, name, dev):
+    _as(t, shape, dtype, name, dev)
+    return _rows(t, shape, name)
+
+
+def _row_as(t, shape, dtype, name, dev):
+    _as(t, shape, dtype, name, dev)
+    if t.stride(0) != 1 and shape[0] > 1:
+        raise WQError(f"{name} must be contiguous")
 
 
 def _dense(t, dtype, name, dev):
     """Checks a contiguous CUDA tensor and returns its shape."""
-    _same(t, dev, name)
-    if t.dtype is not dtype:
-        raise WQError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev or t.dtype is not dtype:
+        _of(t, dtype, name, dev)
     if not t.is_contiguous():
         raise WQError(f"{name} must be contiguous")
     return t.shape
@@ -693,16 +729,6 @@ def _dense_as(t, shape, dtype, name, dev):
     if _dense(t, dtype, name, dev) != shape:
         raise WQError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     return t.data_ptr()
-
-
-def _code(t, dtypes, dim, name):
-    """The library's type code of a CUDA tensor with `dim` dimensions, and its device."""
-    dev = _device(t, name)
-    if t.dtype not in dtypes:
-        raise WQError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != dim:
-        raise WQError(f"{name} must have {dim} dimensions, got {t.dim()}")
-    return DTYPE[t.dtype], dev
 
 
 def _at(t):
@@ -730,30 +756,33 @@ def block_norm(block, residual=None, gate=None, scale=1.0, post="none", post_wei
     block, on rows [T, H]: h = residual + scale * (gate * N_post(block));
     returns (h rounded, N_pre(h)).  post and pre are "none", "rms" or "layer";
     gate is [T, H] or [H]; x_out and y may be given (block or residual too)."""
-    code, dev = _code(block, _FLOATS, 2, "block")
-    dt, shape = block.dtype, block.shape
+    code, dev, dt, shape = _main(block, _FLOATS, 2, "block")
     T, H = shape
-    ldb = _view(block, shape, dt, "block", dev)[0]
-    ldr = 0 if residual is None else _view(residual, shape, dt, "residual", dev)[0]
+    ldb = _rows(block, shape, "block")
+    ldr = 0 if residual is None else _rows_as(residual, shape, dt, "residual", dev)
     ldg = 0
     if gate is not None:
         if gate.dim() == 1:
-            _view(gate, (H,), dt, "gate", dev)
+            _row_as(gate, (H,), dt, "gate", dev)
         else:
-            ldg = _view(gate, shape, dt, "gate", dev)[0]
-    for t, name in ((post_weight, "post_weight"), (post_bias, "post_bias"),
-                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
-        if t is not None:
-            _view(t, (H,), dt, name, dev)
+            ldg = _rows_as(gate, shape, dt, "gate", dev)
+    if post_weight is not None:
+        _row_as(post_weight, (H,), dt, "post_weight", dev)
+    if post_bias is not None:
+        _row_as(post_bias, (H,), dt, "post_bias", dev)
+    if pre_weight is not None:
+        _row_as(pre_weight, (H,), dt, "pre_weight", dev)
+    if pre_bias is not None:
+        _row_as(pre_bias, (H,), dt, "pre_bias", dev)
     if x_out is None:
         x_out = torch.empty(shape, dtype=dt, device=block.device)
     if y is None:
         y = torch.empty(shape, dtype=dt, device=block.device)
-    ldx, ldy = _view(x_out, shape, dt, "x_out", dev)[0], _view(y, shape, dt, "y", dev)[0]
+    ldx, ldy = _rows_as(x_out, shape, dt, "x_out", dev), _rows_as(y, shape, dt, "y", dev)
     _check(lib().wq_block_norm(
         block.data_ptr(), ldb, _at(residual), ldr, _at(gate), ldg, scale, NORM[post],
         _at(post_weight), _at(post_bias), NORM[pre], _at(pre_weight), _at(pre_bias), eps, T, H, code,
-        x_out.data_ptr(), ldx, y.data_ptr(), ldy, _raw_stream(dev)), "wq_block_norm")
+        x_out.data_ptr(), ldx, y.data_ptr(), ldy, _TC._cuda_getCurrentRawStream(dev)), "wq_block_norm")
     return x_out, y
 
 
@@ -763,9 +792,9 @@ def rope_table(max_pos, rot, base=10000.0, scaling="none", factor=1.0, trained=0
     float64; scaling "none", "linear", "ntk" or "yarn" for contexts `factor`
     times the `trained` one."""
     t = torch.empty(max_pos, rot // 2, 2, dtype=torch.float32, device=device or "cuda")
-    dev = _device(t, "table")
+    dev = _main(t, (torch.float32,), 3, "table")[1]
     _check(lib().wq_rope_table(t.data_ptr(), max_pos, rot, base, ROPE_SCALING[scaling], factor,
-                               float(trained), beta_fast, beta_slow, mscale, _raw_stream(dev)),
+                               float(trained), beta_fast, beta_slow, mscale, _TC._cuda_getCurrentRawStream(dev)),
            "wq_rope_table")
     return t
 
@@ -780,18 +809,18 @@ def _table(table, dev):
 def rope(x, positions, table, layout="half", inverse=False, out=None, status=None):
     """Rotate the first rot = 2 * table.shape[1] elements of each head of x
     [T, heads, D] to its token's position; out may be x itself."""
-    code, dev = _code(x, _FLOATS, 3, "x")
-    dt, shape = x.dtype, x.shape
+    code, dev, dt, shape = _main(x, _FLOATS, 3, "x")
     T, n, D = shape
     max_pos, rot = _table(table, dev)
-    sx = _view(x, shape, dt, "x", dev)
+    sx = _heads(x, shape, "x")
     pos = _dense_as(positions, (T,), torch.int32, "positions", dev)
     if out is None:
         out = torch.empty(shape, dtype=dt, device=x.device)
-    so = _view(out, shape, dt, "out", dev)
+    _as(out, shape, dt, "out", dev)
+    so = _heads(out, shape, "out")
     _check(lib().wq_rope(x.data_ptr(), sx[0], sx[1], pos, table.data_ptr(), max_pos, T, n, D, rot,
                          ROPE_LAYOUT[layout], 1 if inverse else 0, code, out.data_ptr(), so[0], so[1],
-                         _status(status, dev), _raw_stream(dev)), "wq_rope")
+                         _status(status, dev), _TC._cuda_getCurrentRawStream(dev)), "wq_rope")
     return out
 
 
@@ -801,18 +830,16 @@ _CACHE = struct.Struct("@PPqqqqqqqiiiii0q")  # wq_paged_cache
 def _cache(k_cache, v_cache):
     """The wq_paged_cache of k_cache [pages, heads, page_size, dk] and v_cache
     [pages, heads, page_size, dv], any strides over the first three: its bytes,
-    heads, page size, dk, dv and device."""
-    code, dev = _code(k_cache, _HALVES, 4, "k_cache")
-    dt, shape = k_cache.dtype, k_cache.shape
+    heads, page size, dk, dv, device and type."""
+    code, dev, dt, shape = _main(k_cache, _HALVES, 4, "k_cache")
     pages, heads, page, dk = shape
-    sk = _view(k_cache, shape, dt, "k_cache", dev)
-    if v_cache.dim() != 4 or v_cache.shape[:3] != shape[:3]:
-        raise WQError(f"v_cache must be {list(shape[:3])} and the elements of a value, as k_cache has, "
-                      f"got {list(v_cache.shape)}")
-    sv = _view(v_cache, v_cache.shape, dt, "v_cache", dev)
-    dv = v_cache.shape[3]
-    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1],
-                       sv[2], pages, page, heads, dk, dv, code), heads, page, dk, dv, dev
+    sk, vs = _pages(k_cache, shape, "k_cache"), v_cache.shape
+    if len(vs) != 4 or vs[0] != pages or vs[1] != heads or vs[2] != page:
+        raise WQError(f"v_cache must be {list(shape[:3])} and the elements of a value, as k_cache has, got {list(vs)}")
+    _of(v_cache, dt, "v_cache", dev)
+    sv, dv = _pages(v_cache, vs, "v_cache"), vs[3]
+    return _CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], pages, page,
+                       heads, dk, dv, code), heads, page, dk, dv, dev, dt
 
 
 def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="half", q=None,
@@ -820,10 +847,12 @@ def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="h
     """Write rope(k) and v [T, heads, D] at places slots int64 [T] (page *
     page_size + place; negative: skipped) of a paged cache, and with q
     [T, q_heads, D] return rope(q).  table None appends without rotation."""
-    c, heads, _, dk, dv, dev = _cache(k_cache, v_cache)
-    dt = k_cache.dtype
+    c, heads, _, dk, dv, dev, dt = _cache(k_cache, v_cache)
     T = k.shape[0]
-    sk, sv = _view(k, (T, heads, dk), dt, "k", dev), _view(v, (T, heads, dv), dt, "v", dev)
+    ks, vs = (T, heads, dk), (T, heads, dv)
+    _as(k, ks, dt, "k", dev)
+    _as(v, vs, dt, "v", dev)
+    sk, sv = _heads(k, ks, "k"), _heads(v, vs, "v")
     to = _dense_as(slots, (T,), torch.int64, "slots", dev)
     rot, max_pos, pos = 0, 0, None
     if table is not None:
@@ -834,14 +863,16 @@ def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="h
         shape = q.shape
         if len(shape) != 3 or shape[0] != T or shape[2] != dk:
             raise WQError(f"q must be [{T}, heads, {dk}], got {list(shape)}")
-        nq, sq = shape[1], _view(q, shape, dt, "q", dev)
+        _of(q, dt, "q", dev)
+        nq, sq = shape[1], _heads(q, shape, "q")
         if q_out is None:
             q_out = torch.empty(shape, dtype=dt, device=q.device)
-        so = _view(q_out, shape, dt, "q_out", dev)
+        _as(q_out, shape, dt, "q_out", dev)
+        so = _heads(q_out, shape, "q_out")
     _check(lib().wq_rope_append_paged(
         _at(q), sq[0], sq[1], nq, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], pos, to,
         _at(table), max_pos, T, rot, ROPE_LAYOUT[layout], c, _at(q_out) if nq else None, so[0], so[1],
-        _status(status, dev), _raw_stream(dev)), "wq_rope_append_paged")
+        _status(status, dev), _TC._cuda_getCurrentRawStream(dev)), "wq_rope_append_paged")
     return q_out
 
 
@@ -861,15 +892,17 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
     splits the tokens (None: T / B each); max_q and max_suffix bound a
     sequence's tokens and keys.  Returns out [T, q_heads, dv]; lse float32
     [T, q_heads] is filled if given."""
-    c, _, page, dk, dv, dev = _cache(k_cache, v_cache)
-    dt, shape = k_cache.dtype, q.shape
+    c, _, page, dk, dv, dev, dt = _cache(k_cache, v_cache)
+    shape = q.shape
     if len(shape) != 3 or shape[2] != dk:
         raise WQError(f"q must be [tokens, heads, {dk}] as k_cache has, got {list(shape)}")
-    T, Hq = shape[0], shape[1]
-    sq = _view(q, shape, dt, "q", dev)
+    T, Hq, _ = shape
+    _of(q, dt, "q", dev)
+    sq = _heads(q, shape, "q")
     B = _dense(suffix_len, torch.int32, "suffix_len", dev).numel()
-    pages = page_table.shape[-1] if page_table.dim() == 2 else 0
-    ld = _view(page_table, (B, pages), torch.int32, "page_table", dev)[0]
+    ps = page_table.shape
+    pages = ps[-1] if len(ps) == 2 else 0
+    ld = _rows_as(page_table, (B, pages), torch.int32, "page_table", dev)
     if max_suffix > pages * page:
         raise WQError(f"max_suffix {max_suffix} needs more pages than page_table has columns")
     if prefix_len:
@@ -886,16 +919,19 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
         max_q = T // B
     if out is None:
         out = torch.empty(T, Hq, dv, dtype=dt, device=q.device)
-    so = _view(out, (T, Hq, dv), dt, "out", dev)
+    shape = (T, Hq, dv)
+    _as(out, shape, dt, "out", dev)
+    so = _heads(out, shape, "out")
     if lse is not None:
         _dense_as(lse, (T, Hq), torch.float32, "lse", dev)
     if ws is None:
         ws = attention_shared_prefix_workspace(q, k_cache, v_cache, B, prefix_len, max_suffix, max_q)
-    else:
-        _dense(ws, ws.dtype, "ws", dev)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise WQError(f"ws must be a contiguous CUDA tensor on cuda:{dev}")
     _check(lib().wq_attention_shared_prefix(
         q.data_ptr(), sq[0], sq[1], T, B, _at(cu_q), max_q, Hq, c, _at(prefix_pages), prefix_len,
         page_table.data_ptr(), ld, suffix_len.data_ptr(), max_suffix,
         dk ** -0.5 if scale is None else scale, out.data_ptr(), so[0], so[1], _at(lse), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _status(status, dev), _raw_stream(dev)), "wq_attention_shared_prefix")
+        ws.numel() * ws.element_size(), _status(status, dev), _TC._cuda_getCurrentRawStream(dev)),
+        "wq_attention_shared_prefix")
     return out
