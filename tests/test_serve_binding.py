@@ -163,3 +163,11 @@ def test_other_strides_go_as_they_are(calls):
     del calls[:]
     wq.rope(**rope_args(x=Cuda(4, 1, 64, stride=(900, 7, 1)), out=Cuda(4, 1, 64)))
     assert calls[0][1][1:3] == (900, 64)
+
+
+@pytest.mark.parametrize("f,args,name", [(wq.rope_append_paged, append_args, "positions"),
+                                         (wq.attention_shared_prefix, attention_args, "prefix_pages")])
+def test_a_missing_tensor_is_named(calls, f, args, name):
+    with pytest.raises(wq.WQError, match=name):
+        f(**args(**{name: None}))
+    assert not calls

@@ -856,6 +856,8 @@ def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="h
     to = _dense_as(slots, (T,), torch.int64, "slots", dev)
     rot, max_pos, pos = 0, 0, None
     if table is not None:
+        if positions is None:
+            raise WQError("a table needs positions")
         max_pos, rot = _table(table, dev)
         pos = _dense_as(positions, (T,), torch.int32, "positions", dev)
     nq, sq, so = 0, (0, 0), (0, 0)
@@ -906,6 +908,8 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
     if max_suffix > pages * page:
         raise WQError(f"max_suffix {max_suffix} needs more pages than page_table has columns")
     if prefix_len:
+        if prefix_pages is None:
+            raise WQError(f"prefix_len {prefix_len} needs prefix_pages")
         _dense(prefix_pages, torch.int32, "prefix_pages", dev)
         if prefix_pages.numel() * page < prefix_len:
             raise WQError(f"prefix_len {prefix_len} needs more pages than prefix_pages holds")
