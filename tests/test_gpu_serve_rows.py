@@ -43,6 +43,8 @@ NO_SEQUENCE = [  # lead, tokens, trail, suffix lengths, P, Hkv, G, D, page, dtyp
     (1, [2, 1], 1, [0, 0], 90, 2, 4, 64, 16, BF),                # the prefix alone, nothing to join
     (2, [30, 0, 30], 9, [0, 0, 0], 100, 2, 4, 128, 16, BF),      # ... by row tiles
     (2, [30, 30], 9, [0, 0], 30000, 1, 4, 128, 16, BF),          # ... joined
+    (300, [70], 500, [90], 100, 2, 2, 64, 16, BF),               # more padding than tokens
+    (100, [40], 300, [0], 100, 2, 4, 64, 16, BF),                # ... and the prefix alone
     (2, [3, 1], 3, [0, 0], 0, 2, 4, 64, 16, BF),                 # no keys at all
     (0, [0, 0], 4, [8, 9], 50, 1, 2, 64, 16, BF),                # no sequence has a token
 ]

@@ -90,30 +90,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // sequence up there instead cost the tile kernel 2.5 us a piece.)
 constexpr float kNoSequence = INFINITY;
 
-// For one head: rows r0, r0 + by, ... below r1
+// For one head: rows r0, r0 + by, ... below r1, a warp for each row's query heads in turn
 __device__ __forceinline__ void clear_rows(const AttnArgs &a, int head, int r0, int r1, int by) {
-  for (int t = r0; t < r1; t += by) {
-    const int64_t row = int64_t(t) * a.Hq + head * a.G;
+  if (r0 >= r1) return;
+  const int lane = threadIdx.x & 31, n = ((r1 - r0 - 1) / by + 1) * a.G;
+  for (int i = threadIdx.x >> 5; i < n; i += blockDim.x >> 5) {
+    const int j = i / a.G, qh = head * a.G + i - j * a.G;
+    const int64_t t = r0 + int64_t(j) * by, row = t * a.Hq + qh;
     if (a.o_part && a.max_suffix > 0) {
-      for (int g = threadIdx.x; g < a.G; g += blockDim.x)
-        a.lse_part[(row + g + 1) * a.slots - 1] = kNoSequence;
+      if (lane == 0) a.lse_part[(row + 1) * a.slots - 1] = kNoSequence;
     } else {
-      for (int i = threadIdx.x; i < a.G * a.dv / 2; i += blockDim.x) {
-        const int g = 2 * i / a.dv, d = 2 * i - g * a.dv;
-        *reinterpret_cast<uint32_t *>(a.out + t * a.o_token + (head * a.G + g) * a.o_head + d) = 0u;
-      }
-      if (a.lse)
-        for (int g = threadIdx.x; g < a.G; g += blockDim.x) a.lse[row + g] = -INFINITY;
+      uint32_t *o = reinterpret_cast<uint32_t *>(a.out + t * a.o_token + qh * a.o_head);
+      for (int d = lane; d < a.dv / 2; d += 32) o[d] = 0u;
+      if (lane == 0 && a.lse) a.lse[row] = -INFINITY;
     }
   }
 }
-// One block of each (sequence, head) takes the rows past max_q in the sequence
-// and a B-th of those outside [cu_q[0], cu_q[B]).
-__device__ __forceinline__ void clear_rest(const AttnArgs &a, int seq, const Source &s, int head) {
+// `parts` blocks of each (sequence, head) share the rows past max_q in the
+// sequence and a B-th of those outside [cu_q[0], cu_q[B]).
+__device__ __forceinline__ void clear_rest(const AttnArgs &a, int seq, const Source &s, int head,
+                                           int part, int parts) {
   const int begin = a.cu_q[0], end = max(a.cu_q[a.B], 0), next = a.cu_q[seq + 1];
-  clear_rows(a, head, s.t0 + s.n, min(next, a.T), 1);
-  if (begin > 0) clear_rows(a, head, seq, min(begin, a.T), a.B);
-  if (end < a.T) clear_rows(a, head, end + seq, a.T, a.B);
+  const int own = seq * parts + part, all = a.B * parts;
+  clear_rows(a, head, s.t0 + s.n + part, min(next, a.T), parts);
+  if (begin > 0) clear_rows(a, head, own, min(begin, a.T), all);
+  if (end < a.T) clear_rows(a, head, end + own, a.T, all);
 }
 
 // D: padded head size (64 or 128), MT: 16-row tiles
@@ -156,11 +157,11 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
     chunk = a.s_chunk;
   }
   const Source s = source_of(a, seq);
-  const bool rest = seq >= 0 && a.cu_q && tile == 0 && split == 0;
+  const bool rest = seq >= 0 && a.cu_q && !a.rest_apart && tile == 0 && split == 0;
   const int rows = min(R, s.n * a.G - tile * R);  // rows of this tile
   const bool last_block = blockIdx.x == gridDim.x - 1;
   if (rows <= 0) {
-    if (rest) clear_rest(a, seq, s, head);
+    if (rest) clear_rest(a, seq, s, head, 0, 1);
     if (last_block) wait_last_kernel();
     return;
   }
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(NW * 32) attn_small_kernel(const AttnArgs a, i
   uint32_t on[NST - 1];
 #pragma unroll
   for (int i = 0; i < NST - 1; ++i) on[i] = issue(i);
-  if (rest) clear_rest(a, seq, s, head);
+  if (rest) clear_rest(a, seq, s, head, 0, 1);
   for (int i = 0; i < mine; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
     __syncwarp();  // every lane's copies of this piece are in; the slot of piece i - 1 is free
@@ -551,23 +552,25 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AttnArgs a) {
   if (d == 0 && a.lse) a.lse[row] = sum == 0.0f ? -INFINITY : base + logf(sum);
 }
 
-// The rows of no sequence, for calls whose suffixes the tile kernel takes, and
-// (LAST: after all other work) for calls without suffixes: a block per sequence
-// and head.
+// The rows of no sequence, for calls whose suffixes the tile kernel takes or
+// that have more rows than their sequences may have tokens, and (LAST: after all
+// other work) for calls without suffixes.
 template <bool LAST>
-__global__ void __launch_bounds__(128) attn_rest_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(128) attn_rest_kernel(const AttnArgs a, int parts) {
   start_next_kernel();
-  const int seq = int(blockIdx.x / unsigned(a.Hkv)), head = int(blockIdx.x % unsigned(a.Hkv));
+  const int it = int(blockIdx.x / unsigned(parts)), part = int(blockIdx.x % unsigned(parts));
+  const int seq = it / a.Hkv, head = it - seq * a.Hkv;
   if (LAST) wait_last_kernel();
-  clear_rest(a, seq, source_of(a, seq), head);
+  clear_rest(a, seq, source_of(a, seq), head, part, parts);
   if (!LAST && blockIdx.x == gridDim.x - 1) wait_last_kernel();
 }
 
 template <bool LAST>
 int launch_rest(const AttnArgs &a, cudaStream_t st) {
-  const int64_t blocks = int64_t(a.B) * a.Hkv;
+  const int parts = std::max(1, a.T / 16 / a.B);  // so that none has many more than 16 rows
+  const int64_t blocks = int64_t(a.B) * a.Hkv * parts;
   if (blocks >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
-  return launch_chained(attn_rest_kernel<LAST>, unsigned(blocks), 128, 0, true, st, a);
+  return launch_chained(attn_rest_kernel<LAST>, unsigned(blocks), 128, 0, true, st, a, parts);
 }
 
 template <class DT, int D, int MT, int NW, bool PAGED>
@@ -599,7 +602,7 @@ int launch_t(const AttnArgs &a, cudaStream_t st) {
   if (rc != WQ_OK) return rc;
   if (wide) rc = two ? launch_warps<DT, 128, 2>(a, st) : launch_warps<DT, 128, 1>(a, st);
   else rc = two ? launch_warps<DT, 64, 2>(a, st) : launch_warps<DT, 64, 1>(a, st);
-  if (rc == WQ_OK && a.cu_q && a.tc_suffix) rc = launch_rest<false>(a, st);
+  if (rc == WQ_OK && a.cu_q && a.ss > 0 && a.rest_apart) rc = launch_rest<false>(a, st);
   const int64_t rows = int64_t(a.T) * a.Hq;
   if (rc == WQ_OK && a.o_part)
     rc = a.dv <= 64 ? launch_chained(attn_join_kernel<DT, 16>, unsigned((rows + 15) / 16), 256, 0, true, st, a)
@@ -676,6 +679,7 @@ void plan_attention(AttnArgs &a) {
   }
   if (a.sp + a.ss == 0) a.ss = 1;  // no keys at all: one empty range writes the zeros
   a.slots = a.sp + a.ss;
+  a.rest_apart = a.tc_suffix || a.T > int64_t(a.B) * a.max_q;
 }
 
 size_t attention_ws_bytes(const AttnArgs &a) {

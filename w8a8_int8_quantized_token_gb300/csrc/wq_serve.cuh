@@ -204,6 +204,7 @@ struct AttnArgs {
   int ss, s_chunk;  // suffixes: splits and keys of each
   bool tc_prefix, tc_suffix;  // taken by the tensor-memory kernel
   bool whole;       // it takes prefix and suffix of a sequence's rows in one walk
+  bool rest_apart;  // rows of no sequence have a kernel of their own
   bool one_warp;    // blocks of one warp in the kernel for few rows
   int step_pages, step_place;  // from a warp's piece to its next: pages, and places beyond them
   int p_gang, p_gangs, p_stretch;  // its blocks on the prefix: gangs of p_gang, units of a gang
