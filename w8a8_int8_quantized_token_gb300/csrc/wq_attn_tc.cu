@@ -72,19 +72,27 @@ struct Plan {
   static constexpr int KVB = BN * D * 2;         // bytes of a key or value tile
   static constexpr int NS = D == 128 ? 5 : 8;    // ring depth: keys and values in turn
   static constexpr int NB = D == 128 ? 2 : 3;    // score buffers in tensor memory
-  // Barriers of the steps, used in turn.  Each is waited on by one row tile's
-  // warps alone, which have seen every phase before: a wait by parity cannot
-  // tell a phase from the one two before it.
+  // A wait by parity cannot tell a phase from the one two before it: whoever
+  // waits has to know that all phases before are over.  Within a piece each
+  // step's barrier (used in turn) is waited on by one row tile's warps alone,
+  // which have seen every phase.  Between pieces, one of which may leave row
+  // tile 1 without work, every softmax and product warp waits for the queries,
+  // which come after all of the piece before, and takes part in their release.
   static constexpr int NSB = NB % 2 ? 2 * NB : NB;
+  // Signals of a row tile's value products, used in turn.  Not all are waited
+  // on: when the scores of key tile j are in, the products up to j - NB are over
+  // (j - 3 at most), so that a wait for one of four is never met by an older one.
+  static constexpr int NO = 4;
+  static constexpr int Q_EMPTY_COUNT = 8 + 2;  // softmax and product warps
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * QB;
   static constexpr int OFF_BAR = OFF_KV + NS * KVB;
   static constexpr int B_FULL = 0, B_EMPTY = NS, B_Q_FULL = 2 * NS, B_Q_EMPTY = B_Q_FULL + 1,
                        B_S = B_Q_EMPTY + 1,      // [NSB] a step's scores are in
-      B_P = B_S + NSB,                           // [NSB][2] half of its weights are in
-      B_O = B_P + 2 * NSB,                        // [2][2] a value product of a row tile is done, in turn
-      B_TAIL = B_O + 4,                          // [2] in turn: a last value tile's tail is cleared
-      B_DONE = B_TAIL + 2, NBAR = B_DONE + 2;
+                       B_P = B_S + NSB,          // [NSB][2] half of its weights are in
+                       B_O = B_P + 2 * NSB,      // [2][NO] a value product of a row tile is done
+                       B_TAIL = B_O + 2 * NO,    // [2] in turn: a last value tile's tail is cleared
+                       B_DONE = B_TAIL + 2, NBAR = B_DONE + 2;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int SMEM = OFF_ABORT + 4 + 1024;
@@ -294,7 +302,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     prefetch_map(&tmV);
     *abort_flag = 0;
     for (int i = 0; i < P::NBAR; ++i)
-      mbar_init(bar(i), i == P::B_Q_EMPTY                      ? 8   // softmax warps
+      mbar_init(bar(i), i == P::B_Q_EMPTY                      ? P::Q_EMPTY_COUNT
                         : i >= P::B_P && i < P::B_O            ? 4   // warps of a row tile
                         : i >= P::B_EMPTY && i < P::B_Q_FULL   ? 2   // row tiles
                                                                : 1);
@@ -474,9 +482,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const bool turns = NB == 2 && two;
         auto pass = [&]() { asm volatile("bar.arrive %0, 64;" ::"r"(2 - t) : "memory"); };
         if (turns && t == 1) pass();
-        // by both warps, even where one has no rows: it must not run ahead of
-        // the pieces, whose phases of the ring it could not tell apart then
-        if (p.open) wait(P::B_Q_FULL, q & 1);
+        if (p.open) {  // by both warps, even where one has no rows
+          wait(P::B_Q_FULL, q & 1);
+          if (ok && lane == 0) mbar_arrive(bar(P::B_Q_EMPTY));
+        }
         q += p.open;
         if (turns) {
           // The common case written out: warp t keeps to row tile t and one
@@ -531,7 +540,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
               for (int i = 4; i < 8; ++i) mma_f16_ts(to, ts + 8 * i, dv + ((2048 * i) >> 4), id_o, 1u);
               if (more) scores(s);
-              else if (p.close) mma_commit(bar(P::B_O + 2 * t + ((t ? ends1 : ends0) & 1)));
+              else if (p.close) mma_commit(bar(P::B_O + P::NO * t + ((t ? ends1 : ends0) % P::NO)));
             }
             if (t == 0 || more) pass();  // the last turn is nobody's to wait for
             if (leader && ok) {
@@ -565,7 +574,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const bool more = k + NB < steps;
             // operands and barriers, ready ahead of the waits
             uint32_t ts = tmem + buf * BN, acc = j > 0 || !p.open;
-            uint32_t bar_o = bar(P::B_O + 2 * o) + 8 * (((o ? ends1 : ends0) + (each ? uint32_t(j) : 0u)) & 1u);
+            uint32_t bar_o = bar(P::B_O + P::NO * o) + 8 * (((o ? ends1 : ends0) + (each ? uint32_t(j) : 0u)) % P::NO);
             uint32_t bar_s = bar(P::B_S + sb);
             const bool signal = each || (j + 1 == n && p.close);
             uint64_t dv = sdesc_n(base + P::OFF_KV + sv * P::KVB), dk = sdesc(base + P::OFF_KV + sk * P::KVB);
@@ -642,24 +651,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     constexpr float kFar = 65536.0f;
     bool far = false;
     pieces([&](const Piece &p, int n, int tiles) {
-      // the queries of a piece are released by the eight softmax warps: their
-      // tiles serve as staging for the piece's results
+      // the queries of a piece are released at its end: their tiles serve as
+      // staging for its results
       auto release = [&]() {
         if (n == 0) return;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(P::B_Q_EMPTY));
       };
-      if (n > 0) q += p.open;
+      if (n > 0 && p.open) {
+        if (!(ok = wait_warp(bar(P::B_Q_FULL), q & 1, abort_flag))) return false;
+        ++q;
+      }
       const bool each = signal_each<P::NB>(tiles);
       uint32_t k = kk + uint32_t(t);
       kk += uint32_t(n * tiles);
       if (t >= tiles) {
-        if (!p.close) return true;
-        // not before the piece's queries are in: its release must not count
-        // for the piece before
-        if (n > 0 && !(ok = wait_warp(bar(P::B_Q_FULL), (q - 1) & 1, abort_flag))) return false;
-        release();
+        if (p.close) release();
         return true;
       }
       const int tok = row / a.G, j0 = p.tok0 + t * c.tpt + tok;
@@ -735,7 +743,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             // the value product of the tile before has to be in
             if (each) {
               const uint32_t end = ends + uint32_t(j) - 1;
-              if (!(ok = wait_warp(bar(P::B_O + 2 * t + (end & 1)), (end >> 1) & 1, abort_flag))) return false;
+              if (!(ok = wait_warp(bar(P::B_O + P::NO * t + end % P::NO), (end / P::NO) & 1, abort_flag))) return false;
               tc_fence_after();
             }
 #pragma unroll 1
@@ -776,7 +784,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (n > 0) {
         const uint32_t end = each ? ends + uint32_t(n) - 1 : ends;
         ends = end + 1;
-        if (!(ok = wait_warp(bar(P::B_O + 2 * t + (end & 1)), (end >> 1) & 1, abort_flag))) return false;
+        if (!(ok = wait_warp(bar(P::B_O + P::NO * t + end % P::NO), (end / P::NO) & 1, abort_flag))) return false;
         tc_fence_after();
       }
       const bool none = l == 0.0f;
