@@ -60,11 +60,12 @@ def need(cond, what):
         raise Fault(what)
 
 
-def run(D, pieces, seed, NS, NB, NO, release, softmax_waits=True):
+def run(D, pieces, seed, NS, NB, NO, release, softmax_waits=True, last_two=True):
     """Runs a block over `pieces` = [(n, tiles, tail, open, close)].  With
     `release` 10 the product warps take part in the release of the queries;
     without `softmax_waits` idle softmax warps wait for them only where they
-    release them."""
+    release them; without `last_two` a piece's end is waited for by its last
+    product's signal alone."""
     R = random.Random(seed)
     NSB = 2 * NB if NB % 2 else NB
     full = [Barrier(f"full {i}", 1) for i in range(NS)]
@@ -213,11 +214,12 @@ def run(D, pieces, seed, NS, NB, NO, release, softmax_waits=True):
                 need(sbuf[k % NB] == (pi, j, t), f"softmax of {(pi, j, t)} reads {sbuf[k % NB]}")
                 for _ in range(R.randint(0, 3)):
                     yield
-                if j and R.random() < 0.3:  # a maximum grew: the sums are scaled
+                if (j or not opens) and R.random() < 0.3:  # a maximum grew: the sums are scaled
                     if each:
                         e = ends + j - 1
                         yield from wait(done[t][e % NO], e // NO)
-                    need(acc[t] == (pi, j - 1), f"sums of {(pi, j - 1, t)} are {acc[t]}")
+                    before = (pi, j - 1) if j else (pi - 1, pieces[pi - 1][0] - 1)
+                    need(acc[t] == before, f"sums of {before} of {t} are {acc[t]}")
                 for h in range(2):
                     given[pi, j, t, h] = given.get((pi, j, t, h), 0) + 1
                     if given[pi, j, t, h] == 4:
@@ -227,6 +229,8 @@ def run(D, pieces, seed, NS, NB, NO, release, softmax_waits=True):
                 k += tiles
             if closes:
                 e = ends + n - 1 if each else ends
+                if each and (n > 1 or not opens) and last_two:
+                    yield from wait(done[t][(e - 1) % NO], (e - 1) // NO)
                 yield from wait(done[t][e % NO], e // NO)
                 need(acc[t] == (pi, n - 1), f"result of {(pi, n - 1, t)} is {acc[t]}")
                 for _ in range(R.randint(0, 6)):

@@ -35,8 +35,8 @@ def test_no_order_of_events_breaks_the_pipeline(D):
 def test_the_model_sees_what_each_rule_prevents():
     """Without the softmax warps' wait for the queries, idle warps run ahead of
     a piece with one row tile; without the product warps' part in their release,
-    one that has no work falls behind; with two product signals, heads of 64
-    take the end of one product for that of a later one."""
+    one that has no work falls behind; with the last product's signal alone, heads
+    of 64 take the end of the last but two for it."""
     assert faults(128, MIXED[:1], range(40), softmax_waits=False) > 20
     assert faults(128, [[(1, 1, False, 1, 1)] * 6], range(400), release=8) > 0
-    assert faults(64, [[(16, 1, True, 1, 1)]], range(40), NO=2) > 10
+    assert faults(64, [[(16, 1, True, 1, 1)]], range(40), last_two=False) > 10

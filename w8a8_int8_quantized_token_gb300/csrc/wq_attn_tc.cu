@@ -15,12 +15,12 @@
 //   warp 11         none (the third warpgroup gives its registers to the others)
 // Tensor memory: two score buffers of 128 columns (three for D = 64), O0, O1
 // (D each).  P takes the place of its S (64 columns, 16-bit pairs) as the A
-// operand of the second product.  O is rescaled only when a row's maximum has grown by more than
-// 2^8 over the one in use: until then the weights are at most 2^8, and the final
+// operand of the second product.  O is rescaled only when a row's maximum has
+// grown by more than 2^8 over the one in use: until then the weights are at most 2^8, and the final
 // division removes the factor.  P is rounded to 16 bits as the operand that it is;
 // l sums the weights as they were.  A second sum, of the rounded ones, would
 // divide the result better (error against 64 bits 0.0021 -> 0.0020 in bf16) but
-// takes the softmax 17% longer at D = 64 and 5% at D = 128.
+// makes a call 17% longer at D = 64 (142 -> 166 us) and 5% at D = 128 (244 -> 257).
 //
 // The range is cut two ways.  The prefix is the same for all tokens.  A gang
 // of blocks, one per row tile pair, walks the same keys at the same time, so
@@ -79,10 +79,12 @@ struct Plan {
   // tile 1 without work, every softmax and product warp waits for the queries,
   // which come after all of the piece before, and takes part in their release.
   static constexpr int NSB = NB % 2 ? 2 * NB : NB;
-  // Signals of a row tile's value products, used in turn.  Not all are waited
-  // on: when the scores of key tile j are in, the products up to j - NB are over
-  // (j - 3 at most), so that a wait for one of four is never met by an older one.
-  static constexpr int NO = 4;
+  // Signals of a row tile's value products, two in turn.  Not all are waited on.
+  // When the scores of key tile j are in, the products up to j - NB are over, so
+  // the one of j - 1 may be waited for, and the one of j only after that.  (With
+  // four in turn a piece's end needs one wait, but a step of heads of 64 takes
+  // 1.22 us instead of 1.14.)
+  static constexpr int NO = 2;
   static constexpr int Q_EMPTY_COUNT = 8 + 2;  // softmax and product warps
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = 2 * QB;
@@ -224,9 +226,8 @@ struct Cut {
   int groups;         // gangs' worths of pairs: ceil(pairs_p / gang)
   int stretch;        // units of a gang (the last may have fewer)
   int pairs_s;        // row tile pairs of a suffix (0: no suffixes here)
-    int box;            // cache rows of one TMA box
+  int box;            // cache rows of one TMA box
   int step_pages, step_place;  // 128 keys on: pages, and places beyond them
-
   bool out16;         // out rows take 16-byte stores
 };
 
@@ -243,7 +244,7 @@ struct Piece {
   Source s;
   int head, tok0;     // key head; first token (of the source) of row tile 0
   int k0, k1;         // keys
-    int slot, last;     // partial-result slot; slots (slot, last) stay empty
+  int slot, last;     // partial-result slot; slots (slot, last) stay empty
   bool open, close;   // the rows' sums begin, end with this piece
 };
 
@@ -258,7 +259,7 @@ __device__ __forceinline__ Piece prefix_piece(const AttnArgs &a, const Cut &c, i
   p.k0 = (u0 - start) * BN;
   p.k1 = u1 - start >= c.units_p ? a.P : (u1 - start) * BN;
   p.slot = gang - start / c.stretch;  // ordinal of this gang among those that share the item
-    p.last = p.k1 == a.P ? a.sp : p.slot + 1;
+  p.last = p.k1 == a.P ? a.sp : p.slot + 1;
   p.open = p.close = true;
   return p;
 }
@@ -276,7 +277,7 @@ __device__ __forceinline__ Piece suffix_piece(const AttnArgs &a, const Cut &c, i
   const int lastj = min(p.s.n, p.tok0 + 2 * c.tpt) - 1;
   p.k1 = min(min(p.s.len, visible(p.s, lastj)), p.k0 + a.s_chunk);
   p.slot = p.s.slot0 + split;
-    p.last = p.slot + 1;
+  p.last = p.slot + 1;
   p.open = p.close = true;
   return p;
 }
@@ -784,6 +785,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (n > 0) {
         const uint32_t end = each ? ends + uint32_t(n) - 1 : ends;
         ends = end + 1;
+        if (each && (n > 1 || !p.open) &&
+            !(ok = wait_warp(bar(P::B_O + P::NO * t + (end - 1) % P::NO), ((end - 1) / P::NO) & 1, abort_flag)))
+          return false;
         if (!(ok = wait_warp(bar(P::B_O + P::NO * t + end % P::NO), (end / P::NO) & 1, abort_flag))) return false;
         tc_fence_after();
       }
