@@ -631,6 +631,7 @@ void plan_attention(AttnArgs &a) {
   // 1.65 us a unit on each; suffixes (half their bound) at up to 6 TB/s, which
   // takes about 120 SMs.  Measured with 152 and with the chosen SMs: 64
   // sequences behind 8192 keys 68 and 56 us, 200 behind 30000 157 and 144 us.
+  // (Heads of 64, whose units take 1.16 us, get more SMs than they need.)
   int sms = 152;
   if (a.max_suffix > 0 && !a.tc_suffix) {
     const int64_t pair = 2 * (128 / a.G), units = (a.T + pair - 1) / pair * a.Hkv * ((a.P + 127) / 128);
@@ -660,6 +661,9 @@ void plan_attention(AttnArgs &a) {
     chunk = int(((keys + n - 1) / n + grain - 1) / grain * grain);
     splits = int((keys + chunk - 1) / chunk);
   };
+  // About eight items an SM; twelve where ranges are long, whose ends then weigh
+  // less than the unevenness of fewer (64 sequences of up to 8192 keys: 198 us
+  // with 1216 items, 194 with 1824).
   const int64_t want = a.max_suffix > 4096 ? 1824 : 1216, least = a.one_warp ? 128 : 256;
   const int64_t grain = a.one_warp ? 16 : 64;
   if (!a.tc_prefix) cut((rows_p + R - 1) / R * a.Hkv, a.P, want, least, grain, a.sp, a.p_chunk);

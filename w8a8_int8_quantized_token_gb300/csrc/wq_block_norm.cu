@@ -8,9 +8,9 @@
 // Bound by HBM: 4 T H elements, 5 with a gate per token; 8192 x 7168 bf16 take
 // 89 us, 5.3 TB/s.  Rows that are not whole 16-byte pieces are bound by their
 // instructions (weights are read element by element there): 1021 x 4099 fp16
-// with a gate take 26 us, 1.6 TB/s.  Arithmetic goes in
-// packed float32 pairs: in single operations on 16-bit elements the kernel
-// was bound by its instructions (53 an element).
+// with a gate take 28.7 us, 1.46 TB/s.  Arithmetic goes in packed float32
+// pairs: in single operations on 16-bit elements the kernel was bound by its
+// instructions (53 an element).
 #include <algorithm>
 
 #include "wq_serve.cuh"

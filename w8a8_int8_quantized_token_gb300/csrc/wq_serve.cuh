@@ -47,7 +47,7 @@ struct F32 {
   static __device__ __forceinline__ float from_f(float f) { return f; }
 };
 
-// VW consecutive elements as they lie in memory: one, or one 16-byte access
+// VW consecutive elements as they lie in memory: one 16-byte access
 template <class DT, int VW>
 struct Vec {
   static_assert(VW == DT::kVec, "one 16-byte access");
@@ -77,14 +77,6 @@ struct Vec {
       w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                      __float_as_uint(f[3]));
   }
-};
-template <class DT>
-struct Vec<DT, 1> {
-  typename DT::Raw w;
-  static __device__ __forceinline__ Vec load(const typename DT::Raw *p) { return {*p}; }
-  __device__ __forceinline__ void store(typename DT::Raw *p) const { *p = w; }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = DT::to_f(w); }
-  __device__ __forceinline__ void set(const float (&f)[1]) { w = DT::from_f(f[0]); }
 };
 
 // Two floats in a register pair, for the packed float32 instructions (each
