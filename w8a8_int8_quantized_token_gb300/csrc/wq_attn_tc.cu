@@ -16,9 +16,9 @@
 // Tensor memory: two score buffers of 128 columns (three for D = 64), O0, O1
 // (D each).  P takes the place of its S (64 columns, 16-bit pairs) as the A
 // operand of the second product.  O is rescaled only when a row's maximum has
-// grown by more than 2^8 over the one in use: until then the weights are at most 2^8, and the final
-// division removes the factor.  P is rounded to 16 bits as the operand that it is;
-// l sums the weights as they were.  A second sum, of the rounded ones, would
+// grown by more than 2^8 over the one in use: until then the weights are at most
+// 2^8, and the final division removes the factor.  P is rounded to 16 bits as the
+// operand that it is; l sums the weights as they were.  A second sum, of the rounded ones, would
 // divide the result better (error against 64 bits 0.0021 -> 0.0020 in bf16) but
 // makes a call 17% longer at D = 64 (142 -> 166 us) and 5% at D = 128 (244 -> 257).
 //
@@ -32,12 +32,13 @@
 // an item and begin the next, and each leaves a partial result.  Suffixes: a
 // block per (range, sequence, key head, row tile pair).
 //
-// Measured (bf16): a step of 256 rows x 128 keys takes 1.67 us at D = 128,
-// 1.53 PFLOP/s over 152 SMs (0.79 of the measured cuBLAS burst), bound by the
+// Measured (bf16): a step of 256 rows x 128 keys takes 1.66 us at D = 128,
+// 1.54 PFLOP/s over 152 SMs (0.79 of the measured cuBLAS burst), bound by the
 // products and the hand-overs between the roles: without the exponentials it
-// takes as long.  At D = 64 it takes 1.16 us (0.57 of burst), bound by the
-// softmax; with two score buffers it took 1.45 us.  An end of a range costs
-// about 8 us (first loads 3, last product and results 4).
+// takes as long.  At D = 64 it takes 1.14 us (0.58 of burst), bound by the chain
+// of loads, maximum, weights and stores of each softmax warp (without the
+// exponentials 0.2 us less); with two score buffers it took 1.45 us.  An end of a
+// range costs about 8 us (first loads 3, last product and results 4).
 //
 // Values past the end of a range may be anything (a page is shared with
 // unwritten places), and 0 * NaN is NaN: the last tile's tail is cleared in
