@@ -574,6 +574,36 @@ WQ_API int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, 
                                 wq_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The norm of each head and its rotary position in one pass:
+ *   y = rope(x r w),  r = 1 / sqrt(mean(x^2) + eps) over the head's D elements,
+ * for models that normalise queries and keys head by head.  One weight [D] for
+ * all heads, of the tensor's dtype (NULL: ones).  Float32 arithmetic, one
+ * rounding to the output type.
+ *
+ * wq_head_norm_rope: as wq_rope without its inverse; rot = 0 is the norm alone
+ *   (positions and table may be NULL).
+ * wq_head_norm_rope_append_paged: as wq_rope_append_paged, with q_weight and
+ *   k_weight; values are copied as they are.
+ * Requirements as theirs, eps >= 0.  The vector kernel serves D, rot and pitches
+ * in whole 16-byte vectors (rot in the half layout: two of them), 16-byte
+ * aligned pointers and heads of at most 64 vectors. */
+WQ_API int wq_head_norm_rope(const void *x, int64_t x_token, int64_t x_head, const void *weight,
+                             float eps, const int32_t *positions, const float *table,
+                             int64_t max_pos, int64_t T, int heads, int D, int rot, int layout,
+                             int dtype, void *out, int64_t o_token, int64_t o_head,
+                             int32_t *status, wq_stream_t stream);
+WQ_API int wq_head_norm_rope_append_paged(const void *q, int64_t q_token, int64_t q_head,
+                                          int q_heads, const void *q_weight, const void *k_new,
+                                          int64_t kn_token, int64_t kn_head, const void *k_weight,
+                                          const void *v_new, int64_t vn_token, int64_t vn_head,
+                                          float eps, const int32_t *positions,
+                                          const int64_t *slots, const float *table,
+                                          int64_t max_pos, int64_t T, int rot, int layout,
+                                          const wq_paged_cache *cache, void *q_out,
+                                          int64_t qo_token, int64_t qo_head, int32_t *status,
+                                          wq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Attention over a paged cache for B sequences that share a prefix.
  * The prefix is prefix_len keys in the pages prefix_pages int32
  * [ceil(prefix_len / page_size)]; sequence b continues with suffix_len[b]

@@ -159,3 +159,23 @@ def attention(q, k_cache, v_cache, prefix_pages, P, page_table, suffix_len, cu_q
             lse[rows, heads] = z
             ltol[rows, heads] = torch.where(some, 2 * e + 4 * E * (1 + z.abs()), torch.zeros_like(z))
     return out, lse, tol, ltol
+
+
+def head_norm_rotate(x, w, pos, tab, layout, eps):
+    """rope(RMS(x) w) of x [T, heads, D] in float64, and its magnitudes as rotate gives them; tab None: the norm alone."""
+    x = f64(x)
+    y = x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps) * (1.0 if w is None else f64(w))
+    if tab is None:
+        return y, y.abs()
+    z, mag = rotate(y, pos, tab, layout)
+    rot = 2 * tab.shape[1]
+    mag[..., rot:] = y[..., rot:].abs()
+    return z, mag
+
+
+def head_norm_tol(y, mag, dtype, D):
+    """The sum of squares: chains of at most max(16, D / 32) fused steps in a
+    lane, five levels of a tree, the mean's product: relative to itself, halved
+    by the root; the root's reciprocal (2 ulp, 4 E), two products: 16 + D / 32 +
+    8 units at most.  The rotation 4 E, one rounding to dtype."""
+    return U[dtype] * y.abs() + (28 + D / 32) * E * mag + TINY[dtype]

@@ -95,6 +95,8 @@ _SIGS = {
     "wq_rope_table": (_I, [_P, _L, _I, _D, _I, _D, _D, _D, _D, _D, _P]),
     "wq_rope": (_I, [_P, _L, _L, _P, _P, _L, _L, _I, _I, _I, _I, _I, _I, _P, _L, _L, _P, _P]),
     "wq_rope_append_paged": (_I, [_P, _L, _L, _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _L, _L, _I, _I, _P, _P, _L, _L, _P, _P]),
+    "wq_head_norm_rope": (_I, [_P, _L, _L, _P, _F, _P, _P, _L, _L, _I, _I, _I, _I, _I, _P, _L, _L, _P, _P]),
+    "wq_head_norm_rope_append_paged": (_I, [_P, _L, _L, _I, _P, _P, _L, _L, _P, _P, _L, _L, _F, _P, _P, _P, _L, _L, _I, _I, _P, _P, _L, _L, _P, _P]),
     "wq_attention_shared_prefix_workspace_size": (_S, [_L, _I, _I, _I, _P, _L, _L]),
     "wq_attention_shared_prefix": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P, _S, _P, _P]),
     "wq_moe_forward_masked": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P, _P]),
@@ -875,6 +877,75 @@ def rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, layout="h
         _at(q), sq[0], sq[1], nq, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], pos, to,
         _at(table), max_pos, T, rot, ROPE_LAYOUT[layout], c, _at(q_out) if nq else None, so[0], so[1],
         _status(status, dev), _TC._cuda_getCurrentRawStream(dev)), "wq_rope_append_paged")
+    return q_out
+
+
+def _turned(positions, T, table, dev):
+    """Address of the positions, table rows and rotated elements of a call; a
+    table of None turns nothing."""
+    if table is None:
+        return None, 0, 0
+    if positions is None:
+        raise WQError("a table needs positions")
+    max_pos, rot = _table(table, dev)
+    return _dense_as(positions, (T,), torch.int32, "positions", dev), max_pos, rot
+
+
+def head_norm_rope(x, weight, positions, table, eps=1e-6, layout="half", out=None, status=None):
+    """RMS norm of each head of x [T, heads, D] with one weight [D] (None:
+    ones), its first rot = 2 * table.shape[1] elements then rotated to its
+    token's position (table None: the norm alone); out may be x itself."""
+    code, dev, dt, shape = _main(x, _FLOATS, 3, "x")
+    T, n, D = shape
+    pos, max_pos, rot = _turned(positions, T, table, dev)
+    sx = _heads(x, shape, "x")
+    if weight is not None:
+        _row_as(weight, (D,), dt, "weight", dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=x.device)
+    _as(out, shape, dt, "out", dev)
+    so = _heads(out, shape, "out")
+    _check(lib().wq_head_norm_rope(
+        x.data_ptr(), sx[0], sx[1], _at(weight), eps, pos, _at(table), max_pos, T, n, D, rot,
+        ROPE_LAYOUT[layout], code, out.data_ptr(), so[0], so[1], _status(status, dev),
+        _TC._cuda_getCurrentRawStream(dev)), "wq_head_norm_rope")
+    return out
+
+
+def head_norm_rope_append_paged(k, v, positions, slots, table, k_cache, v_cache, k_weight=None,
+                                q=None, q_weight=None, eps=1e-6, layout="half", q_out=None,
+                                status=None):
+    """rope_append_paged of keys, and with q of queries, whose heads are
+    normalised first: head_norm_rope(k, k_weight) goes to the cache beside v,
+    head_norm_rope(q, q_weight) is returned."""
+    c, heads, _, dk, dv, dev, dt = _cache(k_cache, v_cache)
+    T = k.shape[0]
+    ks, vs = (T, heads, dk), (T, heads, dv)
+    _as(k, ks, dt, "k", dev)
+    _as(v, vs, dt, "v", dev)
+    sk, sv = _heads(k, ks, "k"), _heads(v, vs, "v")
+    to = _dense_as(slots, (T,), torch.int64, "slots", dev)
+    pos, max_pos, rot = _turned(positions, T, table, dev)
+    if k_weight is not None:
+        _row_as(k_weight, (dk,), dt, "k_weight", dev)
+    nq, sq, so = 0, (0, 0), (0, 0)
+    if q is not None:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != dk:
+            raise WQError(f"q must be [{T}, heads, {dk}], got {list(shape)}")
+        _of(q, dt, "q", dev)
+        nq, sq = shape[1], _heads(q, shape, "q")
+        if q_weight is not None:
+            _row_as(q_weight, (dk,), dt, "q_weight", dev)
+        if q_out is None:
+            q_out = torch.empty(shape, dtype=dt, device=q.device)
+        _as(q_out, shape, dt, "q_out", dev)
+        so = _heads(q_out, shape, "q_out")
+    _check(lib().wq_head_norm_rope_append_paged(
+        _at(q), sq[0], sq[1], nq, _at(q_weight), k.data_ptr(), sk[0], sk[1], _at(k_weight),
+        v.data_ptr(), sv[0], sv[1], eps, pos, to, _at(table), max_pos, T, rot, ROPE_LAYOUT[layout], c,
+        _at(q_out) if nq else None, so[0], so[1], _status(status, dev),
+        _TC._cuda_getCurrentRawStream(dev)), "wq_head_norm_rope_append_paged")
     return q_out
 
 

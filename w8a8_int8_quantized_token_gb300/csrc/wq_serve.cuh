@@ -168,6 +168,15 @@ inline int64_t rope_pair_threads(const RopeArgs &a) {
 }
 constexpr int64_t kRopeMostThreads = 65535 * 256;
 int launch_rope(const RopeArgs &a, int dtype, bool vec, cudaStream_t st);
+// Norms of heads in the same pass: norm[i] says whether segment i has one
+struct HeadNormArgs {
+  RopeArgs r;
+  const void *weight[3];  // [D], nullptr: ones
+  bool norm[3];
+  float inv_d[3];  // 1 / D
+  float eps;
+};
+int launch_head_norm(const HeadNormArgs &h, int dtype, bool vec, cudaStream_t st);
 int launch_rope_table(float *table, int64_t max_pos, int rot, double base, int scaling,
                       double factor, double trained, double beta_fast, double beta_slow,
                       double mscale, cudaStream_t st);

@@ -30,6 +30,21 @@ bool rope_vec_ok(const RopeArgs &a, int dtype) {
   return true;
 }
 
+// Head norms that the vector kernel may take: float tensors too, and weights
+// that start on 16 bytes
+bool head_norm_vec_ok(const HeadNormArgs &h, int dtype) {
+  const RopeArgs &a = h.r;
+  const int n = dtype == WQ_DT_F32 ? 4 : 8;
+  if (a.rot % (a.layout == WQ_ROPE_HALF ? 2 * n : n) || !al(a.table, 16)) return false;
+  for (int i = 0; i < a.nseg; ++i) {
+    const RopeSeg &s = a.seg[i];
+    if (s.D % n || s.s_token % n || s.s_head % n || s.d_token % n || s.d_head % n || s.d_page % n ||
+        !al(s.src, 16) || !al(s.dst, 16) || !al(h.weight[i], 16))
+      return false;
+  }
+  return true;
+}
+
 int fill_attention(AttnArgs &a, int64_t T, int B, int max_q, int q_heads, const wq_paged_cache *c,
                    int64_t prefix_len, int64_t max_suffix) {
   if (T < 0 || B < 0 || max_q < 0 || q_heads < 1 || prefix_len < 0 || max_suffix < 0 || !cache_ok(c))
@@ -200,6 +215,95 @@ int wq_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, int q_h
   const int rc = device_ok();
   if (rc != WQ_OK) return rc;
   return launch_rope(a, cache->dtype, vec, stream);
+}
+
+int wq_head_norm_rope(const void *x, int64_t x_token, int64_t x_head, const void *weight, float eps,
+                      const int32_t *positions, const float *table, int64_t max_pos, int64_t T,
+                      int heads, int D, int rot, int layout, int dtype, void *out, int64_t o_token,
+                      int64_t o_head, int32_t *status, wq_stream_t stream) {
+  if (T < 0 || heads < 0 || D < 0 || max_pos < 0 || dtype < WQ_DT_BF16 || dtype > WQ_DT_F32 ||
+      layout < WQ_ROPE_HALF || layout > WQ_ROPE_INTERLEAVED || x_token < 0 || x_head < 0 ||
+      o_token < 0 || o_head < 0 || !(eps >= 0.0f))
+    return WQ_ERR_INVALID_ARG;
+  if (T == 0 || heads == 0) return WQ_OK;
+  if (D < 1 || rot < 0 || rot % 2 || rot > D || !x || !out || (rot && (!positions || !table)))
+    return WQ_ERR_INVALID_ARG;
+  const unsigned esz = dtype == WQ_DT_F32 ? 4 : 2;
+  if (T >= (int64_t(1) << 31) || heads > (1 << 16) || D > (1 << 14) || !al(table, 8) || !al(x, esz) ||
+      !al(out, esz) || !al(weight, esz))
+    return WQ_ERR_UNSUPPORTED;
+  HeadNormArgs h{};
+  RopeArgs &a = h.r;
+  a.seg[0] = {x, out, x_token, x_head, o_token, o_head, 0, heads, D, rot, false};
+  a.nseg = 1;
+  a.positions = positions;
+  a.table = table;
+  a.max_pos = max_pos;
+  a.T = T;
+  a.rot = rot;
+  a.layout = layout;
+  a.status = status;
+  h.weight[0] = weight;
+  h.norm[0] = true;
+  h.inv_d[0] = 1.0f / float(D);
+  h.eps = eps;
+  const bool vec = head_norm_vec_ok(h, dtype);
+  const int rc = device_ok();
+  if (rc != WQ_OK) return rc;
+  return launch_head_norm(h, dtype, vec, stream);
+}
+
+int wq_head_norm_rope_append_paged(const void *q, int64_t q_token, int64_t q_head, int q_heads,
+                                   const void *q_weight, const void *k_new, int64_t kn_token,
+                                   int64_t kn_head, const void *k_weight, const void *v_new,
+                                   int64_t vn_token, int64_t vn_head, float eps,
+                                   const int32_t *positions, const int64_t *slots,
+                                   const float *table, int64_t max_pos, int64_t T, int rot,
+                                   int layout, const wq_paged_cache *cache, void *q_out,
+                                   int64_t qo_token, int64_t qo_head, int32_t *status,
+                                   wq_stream_t stream) {
+  if (T < 0 || q_heads < 0 || rot < 0 || rot % 2 || max_pos < 0 || layout < WQ_ROPE_HALF ||
+      layout > WQ_ROPE_INTERLEAVED || !cache_ok(cache) || q_token < 0 || q_head < 0 || kn_token < 0 ||
+      kn_head < 0 || vn_token < 0 || vn_head < 0 || qo_token < 0 || qo_head < 0 || rot > cache->dk ||
+      !(eps >= 0.0f))
+    return WQ_ERR_INVALID_ARG;
+  if (T == 0) return WQ_OK;
+  if (!k_new || !v_new || !slots || !cache->k || !cache->v || (rot && (!positions || !table)) ||
+      (q && (!q_out || q_heads < 1)))
+    return WQ_ERR_INVALID_ARG;
+  if (T >= (int64_t(1) << 31) || cache->heads > (1 << 16) || q_heads > (1 << 16) ||
+      cache->dk > (1 << 14) || cache->dv > (1 << 14) || !al(table, 8))
+    return WQ_ERR_UNSUPPORTED;
+  for (const void *p : {q, static_cast<const void *>(q_out), k_new, v_new, q_weight, k_weight,
+                        static_cast<const void *>(cache->k), static_cast<const void *>(cache->v)})
+    if (!al(p, 2)) return WQ_ERR_UNSUPPORTED;
+  HeadNormArgs h{};
+  RopeArgs &a = h.r;
+  a.seg[0] = {k_new, cache->k, kn_token, kn_head, cache->k_token, cache->k_head, cache->k_page,
+              cache->heads, cache->dk, rot, true};
+  a.seg[1] = {v_new, cache->v, vn_token, vn_head, cache->v_token, cache->v_head, cache->v_page,
+              cache->heads, cache->dv, 0, true};
+  if (q) a.seg[2] = {q, q_out, q_token, q_head, qo_token, qo_head, 0, q_heads, cache->dk, rot, false};
+  a.nseg = q ? 3 : 2;
+  a.positions = positions;
+  a.slots = slots;
+  a.table = table;
+  a.max_pos = max_pos;
+  a.T = T;
+  a.num_slots = cache->num_pages * cache->page_size;
+  a.page_size = cache->page_size;
+  a.rot = rot;
+  a.layout = layout;
+  a.status = status;
+  h.weight[0] = k_weight;
+  h.weight[2] = q ? q_weight : nullptr;
+  h.norm[0] = h.norm[2] = true;
+  h.inv_d[0] = h.inv_d[2] = 1.0f / float(cache->dk);
+  h.eps = eps;
+  const bool vec = head_norm_vec_ok(h, cache->dtype);
+  const int rc = device_ok();
+  if (rc != WQ_OK) return rc;
+  return launch_head_norm(h, cache->dtype, vec, stream);
 }
 
 size_t wq_attention_shared_prefix_workspace_size(int64_t T, int B, int max_q, int q_heads,
