@@ -650,6 +650,42 @@ WQ_API int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_
                                       int64_t o_token, int64_t o_head, float *lse, void *ws,
                                       size_t ws_bytes, int32_t *status, wq_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Accumulated attention weight of cached keys: what each key of a sequence has
+ * been worth to the tokens so far.
+ * Sequences, tokens, keys and pages are those of wq_attention_shared_prefix
+ * (key_len its suffix_len), whose lse of the same call is taken: with a shared
+ * prefix the weights are those of the whole softmax.  For sequence b with n new
+ * tokens, key head h and key i < key_len[b]:
+ *   weights[b][h][i] = decay * w + sum_{j < n, i <= key_len[b] - n + j} sum_{a
+ *                      of the q_heads / heads query heads of h}
+ *                      exp(scale * q[j][a].k_i - lse[j][a]),
+ * w = weights[b][h][i] where i < key_len[b] - n, and 0 for the tokens' own
+ * keys, whose places need not be written before.  weights float, pitches w_seq
+ * and w_head, last dimension contiguous; places at or past key_len[b] are
+ * neither read nor written.  A sequence without new tokens only decays.  A row
+ * with lse = -inf (a token that saw no key) gives no weight.  Call it once a
+ * step, after the attention.
+ * max_q, max_len: host bounds, values above them are cut with status =
+ * WQ_ERR_INDEX, as in the attention.  A page id outside [0, num_pages) sets the
+ * same status; the weights of its keys stay as they were.  The cache's values
+ * (v) are not read.  Scores, weights and sums are float32 and do not depend on
+ * the run.
+ * Requirements: those of wq_attention_shared_prefix on q and the keys; rows of
+ * weights that share no place; decay >= 0.
+ * Workspace: wq_attention_weights_paged_workspace_size() with the same
+ * arguments (0 bytes where a sequence's tokens are few, as in decoding). */
+WQ_API size_t wq_attention_weights_paged_workspace_size(int64_t T, int B, int max_q, int q_heads,
+                                                        const wq_paged_cache *cache,
+                                                        int64_t max_len);
+WQ_API int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_head, int64_t T,
+                                      int B, const int32_t *cu_q, int max_q, int q_heads,
+                                      const wq_paged_cache *cache, const int32_t *page_table,
+                                      int64_t ld_table, const int32_t *key_len, int64_t max_len,
+                                      float scale, const float *lse, float decay, float *weights,
+                                      int64_t w_seq, int64_t w_head, void *ws, size_t ws_bytes,
+                                      int32_t *status, wq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -179,3 +179,41 @@ def head_norm_tol(y, mag, dtype, D):
     by the root; the root's reciprocal (2 ulp, 4 E), two products: 16 + D / 32 +
     8 units at most.  The rotation 4 E, one rounding to dtype."""
     return U[dtype] * y.abs() + (28 + D / 32) * E * mag + TINY[dtype]
+
+
+def attention_weights(q, k_cache, page_table, key_len, cu_q, lse, weights, scale, decay):
+    """The new weights in float64 and their tolerance.
+
+    A score takes dk products in float32, off by at most dk E times the sum of
+    |q k| scale; the factor scale log2(e), the product with it and the sum with
+    the log-sum-exp (itself times log2(e)) round at most four times, each E times
+    |score| + |lse|; the exponential is off by 2^-22 and its argument's base
+    change by as much.  Rows are added in chains of at most 64 within a tile (any
+    page size: all rows over 8 warps), tile by tile and part by part."""
+    pt, kl, cu = page_table.cpu().long(), key_len.cpu().tolist(), cu_q.cpu().tolist()
+    B, Hkv = weights.shape[:2]
+    G = q.shape[1] // Hkv
+    q, kc, lse, w = f64(q), k_cache.cpu(), f64(lse), f64(weights)
+    tol = torch.zeros_like(w)
+    for b in range(B):
+        n, m = cu[b + 1] - cu[b], kl[b]
+        old = max(0, m - n)
+        w[b, :, :old] *= decay
+        w[b, :, old:m] = 0
+        tol[b, :, :m] = 2 * E * w[b, :, :m].abs()
+        if n == 0 or m == 0:
+            continue
+        seen = torch.arange(m) <= (m - n + torch.arange(n))[:, None]
+        for h in range(Hkv):
+            k = keys_of(kc, pt[b], m, h)
+            rows, heads = slice(cu[b], cu[b] + n), slice(h * G, (h + 1) * G)
+            x = (q[rows, heads] @ k.T) * scale  # [n, G, m]
+            mag = (q[rows, heads].abs() @ k.abs().T) * scale
+            z = lse[rows, heads][..., None]
+            p = torch.where(seen[:, None] & (z > -math.inf), torch.exp(x - z), torch.zeros(()).double())
+            e = q.shape[2] * E * mag + 2.0 ** -21 + 4 * E * (x.abs() + z.abs().nan_to_num(posinf=0.0))
+            chain = 64 + n * G / 8 + 2 * 152
+            add = p.sum((0, 1))
+            w[b, h, :m] += add
+            tol[b, h, :m] += (p * e * 1.01).sum((0, 1)) + chain * E * add + E * w[b, h, :m].abs() + TINY[torch.float32]
+    return w, tol

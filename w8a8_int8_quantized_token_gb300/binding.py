@@ -99,6 +99,8 @@ _SIGS = {
     "wq_head_norm_rope_append_paged": (_I, [_P, _L, _L, _I, _P, _P, _L, _L, _P, _P, _L, _L, _F, _P, _P, _P, _L, _L, _I, _I, _P, _P, _L, _L, _P, _P]),
     "wq_attention_shared_prefix_workspace_size": (_S, [_L, _I, _I, _I, _P, _L, _L]),
     "wq_attention_shared_prefix": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P, _S, _P, _P]),
+    "wq_attention_weights_paged_workspace_size": (_S, [_L, _I, _I, _I, _P, _L]),
+    "wq_attention_weights_paged": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _F, _P, _F, _P, _L, _L, _P, _S, _P, _P]),
     "wq_moe_forward_masked": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P, _P]),
 }
 
@@ -1010,3 +1012,78 @@ def attention_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, page_
         ws.numel() * ws.element_size(), _status(status, dev), _TC._cuda_getCurrentRawStream(dev)),
         "wq_attention_shared_prefix")
     return out
+
+
+# ---------------------------------------------------------------- what cached keys are worth, and which stay
+def _keys(k_cache):
+    """The wq_paged_cache of k_cache [pages, heads, page_size, dk] alone, as _cache gives it."""
+    code, dev, dt, shape = _main(k_cache, _HALVES, 4, "k_cache")
+    pages, heads, page, dk = shape
+    sk = _pages(k_cache, shape, "k_cache")
+    return _CACHE.pack(k_cache.data_ptr(), 0, sk[0], sk[1], sk[2], 0, 0, 0, pages, page, heads, dk, 1,
+                       code), heads, page, dk, dev, dt
+
+
+def _per_key(t, B, heads, least, dtype, name, dev):
+    """Pitches of a tensor [B, heads, at least `least`] that has a value for each key."""
+    _of(t, dtype, name, dev)
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != heads or shape[2] < least:
+        raise WQError(f"{name} must be [{B}, {heads}, {least} or more], got {list(shape)}")
+    return _heads(t, shape, name)
+
+
+def _workspace(ws, size, dev):
+    """Address and bytes of a workspace, which is made where there is none."""
+    if ws is None:
+        ws = torch.empty(max(size(), 1), dtype=torch.uint8, device=torch.device("cuda", dev))
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise WQError(f"ws must be a contiguous CUDA tensor on cuda:{dev}")
+    return ws, ws.numel() * ws.element_size()
+
+
+def attention_weights_paged_workspace(q, k_cache, B, max_len, max_q):
+    """A workspace for attention_weights_paged calls of these sizes."""
+    n = lib().wq_attention_weights_paged_workspace_size(q.shape[0], B, max_q, q.shape[1], _keys(k_cache)[0], max_len)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+
+
+def attention_weights_paged(q, k_cache, page_table, key_len, max_len, lse, weights, cu_q=None,
+                            max_q=None, scale=None, decay=1.0, ws=None, status=None):
+    """Add to weights float32 [B, heads, max_len or more] what each key of the
+    sequences (page_table int32 [B, pages], key_len int32 [B]) weighed in the
+    attention of their new tokens q [T, q_heads, dk], whose lse [T, q_heads]
+    attention_shared_prefix has filled; older weights are taken decay times,
+    the new tokens' own keys start at zero.  cu_q, max_q and scale as there.
+    Returns weights."""
+    c, heads, page, dk, dev, dt = _keys(k_cache)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != dk:
+        raise WQError(f"q must be [tokens, heads, {dk}] as k_cache has, got {list(shape)}")
+    T, Hq, _ = shape
+    _of(q, dt, "q", dev)
+    sq = _heads(q, shape, "q")
+    B = _dense(key_len, torch.int32, "key_len", dev).numel()
+    ps = page_table.shape
+    pages = ps[-1] if len(ps) == 2 else 0
+    ld = _rows_as(page_table, (B, pages), torch.int32, "page_table", dev)
+    if max_len > pages * page:
+        raise WQError(f"max_len {max_len} needs more pages than page_table has columns")
+    if cu_q is not None:
+        _dense_as(cu_q, (B + 1,), torch.int32, "cu_q", dev)
+        if max_q is None:
+            raise WQError("cu_q needs max_q, the most tokens of a sequence")
+    elif T and (B == 0 or T % B):
+        raise WQError(f"{T} tokens do not split evenly over {B} sequences: give cu_q")
+    else:
+        max_q = T // B if B else 0
+    _dense_as(lse, (T, Hq), torch.float32, "lse", dev)
+    sw = _per_key(weights, B, heads, max_len, torch.float32, "weights", dev)
+    ws, size = _workspace(
+        ws, lambda: lib().wq_attention_weights_paged_workspace_size(T, B, max_q, Hq, c, max_len), dev)
+    _check(lib().wq_attention_weights_paged(
+        q.data_ptr(), sq[0], sq[1], T, B, _at(cu_q), max_q, Hq, c, page_table.data_ptr(), ld,
+        key_len.data_ptr(), max_len, dk ** -0.5 if scale is None else scale, lse.data_ptr(), decay,
+        weights.data_ptr(), sw[0], sw[1], ws.data_ptr(), size, _status(status, dev),
+        _TC._cuda_getCurrentRawStream(dev)), "wq_attention_weights_paged")
+    return weights

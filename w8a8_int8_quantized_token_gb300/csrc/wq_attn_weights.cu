@@ -1,0 +1,630 @@
+// Accumulated attention weight of the keys of a paged cache (tcgen05, sm_103a).
+//
+//   w[b][h][i] = decay w[b][h][i] + sum_{rows r that see key i} exp(c q_r.k_i - lse_r)
+//
+// over the new tokens' rows r = (token, query head of group h) of sequence b,
+// whose log-sum-exp the attention over the same keys has left.
+//
+// The scores are taken as S^T = K Q^T: 128 keys are the rows of a tensor-memory
+// tile and up to 128 query rows its columns.  So a thread owns a key and sums
+// along its columns: no sum crosses threads, a masked or unwritten key spoils
+// nothing but its own row, and nothing has to be cleared.  Two key tiles share
+// every query tile that is loaded.
+//   warps 0-3, 4-7  weights of key tile 0, 1 of a pair: a thread owns a key
+//   warp 8          TMA: key tiles page by page, query tiles
+//   warp 9          MMA issue; owns the tensor memory
+// Tensor memory: two score buffers of 128 columns for each key tile.
+//
+// A unit is a (sequence, key head, pair of key tiles, query tile); those in
+// which no token sees a key are left out.  All units lie on one line, which the
+// blocks cut into equal pieces, so that ragged lengths and the triangle of a
+// prompt cost no idle SMs.  Where the cut falls between the query tiles of a
+// pair, the parts of its sums go to the workspace and a second kernel adds them
+// in the order of the line.  One query tile a sequence (decode) is never cut.
+//
+// Few rows: bound by HBM, every key read once.  Many rows: bound by the
+// exponentials (16 a clock on an SM), which take twice as long as the products.
+//
+// Every wait is bounded (1 s); on expiry the kernel records WQ_ERR_TIMEOUT,
+// waits (bounded) for its own copies and MMAs, frees tensor memory and exits.
+#include <algorithm>
+#include <type_traits>
+
+#include "wq_attn.cuh"
+#include "wq_tc.cuh"
+
+namespace wq {
+namespace {
+
+using namespace tc;
+using attn::start_next_kernel;
+using attn::wait_last_kernel;
+
+constexpr int BK = 128, BR = 128;  // keys, query rows of a tile
+constexpr int PAIR = 2 * BK;       // keys of a pair of tiles
+constexpr int NTHREADS = 320;
+constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr int MAX_BLOCKS = 152;    // one block an SM
+
+template <int D>
+struct Plan {
+  static constexpr int CH = D / 64;            // 128-byte column chunks
+  static constexpr int KB = BK * D * 2;        // bytes of a key tile
+  static constexpr int QB = BR * D * 2;        // bytes of a query tile
+  static constexpr int NK = D == 128 ? 4 : 8;  // key tiles in flight
+  static constexpr int NQ = 2;                 // query tiles in flight
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = NQ * QB;
+  static constexpr int OFF_LSE = OFF_K + NK * KB;  // [2 key tiles][2][BR] float
+  static constexpr int OFF_BAR = OFF_LSE + 2 * 2 * BR * 4;
+  static constexpr int B_K_FULL = 0, B_K_EMPTY = NK, B_Q_FULL = 2 * NK, B_Q_EMPTY = B_Q_FULL + NQ,
+                       B_S_FULL = B_Q_EMPTY + NQ,  // [key tile][buffer]
+                       B_S_EMPTY = B_S_FULL + 4, B_DONE = B_S_EMPTY + 4, NBAR = B_DONE + 1;
+  static constexpr int OFF_START = OFF_BAR + NBAR * 8;  // sequence and offset of the block's first unit, total
+  static constexpr int OFF_SCAN = OFF_START + 32;       // sums of the warps
+  static constexpr int OFF_TMEM = OFF_SCAN + (NTHREADS / 32) * 8;
+  static constexpr int OFF_ABORT = OFF_TMEM + 4;
+  static constexpr int SMEM = OFF_ABORT + 4 + 1024;
+  static_assert(OFF_START % 8 == 0 && SMEM <= 232448, "shared memory plan");
+};
+
+// A sequence: its tokens, keys, and the cost of its units
+struct Seq {
+  int t0, n, len;
+  int old;       // keys that were there before the tokens' own (negative: tokens with no key)
+  int pairs, tiles;
+  int p1, d1;    // first pair whose keys not all tokens see, and how far it starts past `old`
+
+  // query tiles that see nothing of pair p, at the front of the sequence's
+  __device__ __forceinline__ int first_tile(int p, int shift) const {
+    return max(0, (p * PAIR - old) >> shift);
+  }
+  // units of the pairs before p, of one key head
+  __device__ __forceinline__ int64_t before(int p, int shift) const {
+    if (n == 0) return p;
+    const int64_t m = max(0, p - p1);
+    return int64_t(p) * tiles - (m * (d1 >> shift) + int64_t(PAIR >> shift) * (m * (m - 1) / 2));
+  }
+};
+
+__device__ __forceinline__ Seq seq_of(const WeightArgs &a, int c0, int c1, int l) {
+  Seq s;
+  s.t0 = min(max(c0, 0), a.T);
+  s.n = min(max(c1 - s.t0, 0), min(a.max_q, a.T - s.t0));
+  s.len = min(max(l, 0), a.max_len);
+  s.old = s.len - s.n;
+  s.pairs = (s.len + PAIR - 1) / PAIR;
+  s.tiles = (s.n + (1 << a.shift) - 1) >> a.shift;
+  s.p1 = s.old <= 0 ? 0 : (s.old + PAIR - 1) / PAIR;
+  s.d1 = s.p1 * PAIR - s.old;
+  return s;
+}
+__device__ __forceinline__ bool in_range(const WeightArgs &a, const Seq &s, int c0, int c1, int l) {
+  return s.t0 == c0 && s.t0 + s.n == c1 && s.len == l;
+}
+__device__ __forceinline__ int first_of(const WeightArgs &a, int b) {
+  return a.cu_q ? a.cu_q[b] : b * a.max_q;
+}
+
+// Sequence and offset in it of place `at` of the line, by the whole block; the
+// line's length if `at` is computed from it by the caller's f(total).
+struct Place {
+  int b;
+  int64_t off, total, at;
+};
+template <class F>
+__device__ __forceinline__ Place locate(const WeightArgs &a, int64_t *scan, int64_t *out, bool tell,
+                                        F &&f) {
+  const int per = (a.B + NTHREADS - 1) / NTHREADS, b0 = threadIdx.x * per;
+  auto cost = [&](int b, bool say) {
+    const int c0 = first_of(a, b), c1 = first_of(a, b + 1), l = a.key_len[b];
+    const Seq s = seq_of(a, c0, c1, l);
+    if (say && !in_range(a, s, c0, c1, l)) set_status(a.status, WQ_ERR_INDEX);
+    return s.before(s.pairs, a.shift) * a.heads;
+  };
+  int64_t own = 0;
+  for (int b = b0; b < min(b0 + per, a.B); ++b) own += cost(b, tell);
+  int64_t sum = own;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) scan[warp] = sum;
+  __syncthreads();
+  int64_t total = 0, base = 0;
+#pragma unroll
+  for (int w = 0; w < NTHREADS / 32; ++w) {
+    if (w < warp) base += scan[w];
+    total += scan[w];
+  }
+  const int64_t at = f(total);
+  sum += base;
+  if (at >= sum - own && at < sum) {
+    int64_t left = at - (sum - own);
+    int b = b0;
+    for (int64_t c; left >= (c = cost(b, false)); ++b) left -= c;
+    out[0] = b;
+    out[1] = left;
+  }
+  __syncthreads();
+  Place p{int(out[0]), out[1], total, at};
+  return p;
+}
+
+// Query tiles [qa, qb) of one sequence against one pair of key tiles
+struct Piece {
+  int b, h, k0, qa, qb;
+  Seq s;
+  bool whole;  // all query tiles of the pair
+  int slot;    // else: where its sums go
+};
+
+// The pieces of a block, one after the other
+struct Walk {
+  int b, h, p;
+  int64_t u, left;  // units of the pair that are done; units of the block to come
+  int n0, n1, nl;   // the next sequence, read ahead
+  Seq s;
+
+  __device__ __forceinline__ void ahead(const WeightArgs &a) {
+    const bool some = b + 1 < a.B;
+    n0 = some ? first_of(a, b + 1) : 0;
+    n1 = some ? first_of(a, b + 2) : 0;
+    nl = some ? a.key_len[b + 1] : 0;
+  }
+  __device__ __forceinline__ void begin(const WeightArgs &a, const Place &at, int64_t units) {
+    b = at.b;
+    left = units;
+    u = 0;
+    h = p = 0;
+    if (units <= 0) return;
+    s = seq_of(a, first_of(a, b), first_of(a, b + 1), a.key_len[b]);
+    ahead(a);
+    const int64_t head = s.before(s.pairs, a.shift);
+    h = int(at.off / head);
+    const int64_t rest = at.off - h * head;
+    int lo = 0, hi = s.pairs - 1;  // the last pair that starts at or before `rest`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (s.before(mid, a.shift) <= rest) lo = mid;
+      else hi = mid - 1;
+    }
+    p = lo;
+    u = rest - s.before(p, a.shift);
+  }
+  __device__ __forceinline__ bool next(const WeightArgs &a, Piece &o) {
+    if (left <= 0) return false;
+    while (p >= s.pairs) {  // the next head, or sequence with keys
+      p = 0;
+      if (s.pairs > 0 && ++h < a.heads) break;
+      h = 0;
+      ++b;
+      s = seq_of(a, n0, n1, nl);
+      ahead(a);
+    }
+    o.b = b;
+    o.h = h;
+    o.k0 = p * PAIR;
+    o.s = s;
+    const int first = s.n ? s.first_tile(p, a.shift) : 0, all = s.n ? s.tiles - first : 1;
+    const int take = int(min(int64_t(all) - u, left));
+    o.qa = s.n ? first + int(u) : 0;
+    o.qb = s.n ? o.qa + take : 0;
+    o.whole = take == all;
+    o.slot = u == 0 ? 1 : 0;
+    left -= take;
+    u += take;
+    if (u == all) u = 0, ++p;
+    return true;
+  }
+};
+
+template <class DT>
+constexpr uint32_t kTypes = std::is_same<DT, Bf16>::value ? (1u << 7) | (1u << 10) : 0u;
+
+// -lse in base 2, to be added to scores in base 2.  A row that saw no key
+// (lse = -inf) gives no weight, as one of lse = inf does.
+__device__ __forceinline__ float neg_lse2(float l) {
+  constexpr float hi = 1.44269502162933349609375f, lo = 1.92596299112661746887e-8f;  // log2(e) in two parts
+  if (fabsf(l) == INFINITY) return -INFINITY;
+  return __fmaf_rn(-l, hi, __fmul_rn(-l, lo));
+}
+
+// The new value of key i (of piece or item s, b, h), given the sum over the rows
+__device__ __forceinline__ float *weight_at(const WeightArgs &a, int b, int h, int i) {
+  return a.w + b * a.w_seq + h * a.w_head + i;
+}
+__device__ __forceinline__ bool page_ok(const WeightArgs &a, int b, int i) {
+  const int page = a.page_table[b * a.ld_table + i / a.page_size];
+  return unsigned(page) < unsigned(a.num_pages);
+}
+
+template <class DT, int D>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmK, const WeightArgs a) {
+  using P = Plan<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::OFF_ABORT);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + P::OFF_TMEM);
+  auto bar = [&](int i) { return base + P::OFF_BAR + 8u * uint32_t(i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  start_next_kernel();
+  if (threadIdx.x == 0) {
+    prefetch_map(&tmQ);
+    prefetch_map(&tmK);
+    *abort_flag = 0;
+    for (int i = 0; i < P::NBAR; ++i) mbar_init(bar(i), i >= P::B_S_EMPTY && i < P::B_DONE ? 4 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == WARP_MMA) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  const Place at = locate(a, reinterpret_cast<int64_t *>(sm + P::OFF_SCAN),
+                          reinterpret_cast<int64_t *>(sm + P::OFF_START), blockIdx.x == 0,
+                          [](int64_t total) { return total * blockIdx.x / gridDim.x; });
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk;
+  walk.begin(a, at, at.total * (blockIdx.x + 1) / gridDim.x - at.at);
+  const int tpt = 1 << a.shift;  // tokens of a query tile
+  bool ok = true;                // this role's waits all ended in time
+
+  if (warp == WARP_TMA) {
+    // -------------------------------------------------------------- copies
+    const bool leader = elect_one();
+    uint32_t kt = 0, qt = 0;  // key and query tiles so far
+    const int nbox = BK / a.box;
+    Piece p, nx;
+    // lane L looks up box L of a pair, one piece ahead
+    auto look = [&](const Piece &q) {
+      const int key = q.k0 + lane * a.box;
+      if (lane >= 2 * nbox || key >= q.s.len) return -1;
+      const int page = a.page_table[q.b * a.ld_table + key / a.page_size];
+      return unsigned(page) < unsigned(a.num_pages) ? page : int(a.num_pages);  // a bad page reads as zeros
+    };
+    bool more = walk.next(a, p);
+    int page = more ? look(p) : 0;
+    while (more && ok) {
+      const bool again = walk.next(a, nx);
+      const int page_next = again ? look(nx) : 0;
+      const int place = (p.k0 + lane * a.box) % a.page_size;
+      if (p.qb > p.qa) {
+#pragma unroll 1
+        for (int g = 0; g < 2 && ok; ++g) {
+          const int boxes = min(nbox, (p.s.len - p.k0 - g * BK + a.box - 1) / a.box);
+          if (boxes <= 0) break;
+          const int s = kt % P::NK;
+          if (!(ok = wait_warp(bar(P::B_K_EMPTY + s), ((kt / P::NK) & 1) ^ 1, abort_flag))) break;
+          const uint32_t full = bar(P::B_K_FULL + s);
+          uint32_t dst = base + P::OFF_K + uint32_t(s * P::KB);
+          if (leader) mbar_expect_tx(full, uint32_t(boxes * a.box * P::CH * 128));
+#pragma unroll 1
+          for (int b = 0; b < boxes; ++b) {
+            const int by = __shfl_sync(0xffffffffu, place, g * nbox + b);
+            const int bw = __shfl_sync(0xffffffffu, page, g * nbox + b);
+            if (leader) {
+#pragma unroll
+              for (int ch = 0; ch < P::CH; ++ch) tma_load_4d(dst + ch * BK * 128, &tmK, ch * 64, by, p.h, bw, full);
+            }
+            dst += uint32_t(a.box * 128);
+          }
+          ++kt;
+        }
+#pragma unroll 1
+        for (int q = p.qa; q < p.qb && ok; ++q) {
+          const int s = qt % P::NQ;
+          if (!(ok = wait_warp(bar(P::B_Q_EMPTY + s), ((qt / P::NQ) & 1) ^ 1, abort_flag))) break;
+          if (leader) {
+            mbar_expect_tx(bar(P::B_Q_FULL + s), uint32_t(P::CH * tpt * a.G * 128));
+#pragma unroll
+            for (int ch = 0; ch < P::CH; ++ch)
+              tma_load_3d(base + P::OFF_Q + s * P::QB + ch * BR * 128, &tmQ, ch * 64, p.h * a.G,
+                          p.s.t0 + q * tpt, bar(P::B_Q_FULL + s));
+          }
+          ++qt;
+        }
+      }
+      p = nx;
+      page = page_next;
+      more = again;
+    }
+    if (!ok) {  // let copies already in flight land before the block goes away
+      *abort_flag = 1;
+      for (uint32_t i = kt > P::NK ? kt - P::NK : 0; i < kt; ++i)
+        mbar_wait_bounded(bar(P::B_K_FULL + i % P::NK), (i / P::NK) & 1);
+      for (uint32_t i = qt > P::NQ ? qt - P::NQ : 0; i < qt; ++i)
+        mbar_wait_bounded(bar(P::B_Q_FULL + i % P::NQ), (i / P::NQ) & 1);
+    }
+  } else if (warp == WARP_MMA) {
+    // -------------------------------------------------------------- products
+    const bool leader = elect_one();
+    const uint32_t idesc = idesc_f16(BK, a.cols) | kTypes<DT>;
+    const int steps = (a.dk + 15) / 16;
+    uint32_t kt = 0, qt = 0, st[2] = {0, 0};
+    auto wait = [&](int b, uint32_t parity) {
+      if (ok) ok = wait_warp(bar(b), parity, abort_flag);
+    };
+    Piece p;
+    while (ok && walk.next(a, p)) {
+      if (p.qb == p.qa) continue;
+      const int tiles = p.k0 + BK < p.s.len ? 2 : 1;
+      for (int g = 0; g < tiles; ++g) wait(P::B_K_FULL + int((kt + g) % P::NK), ((kt + g) / P::NK) & 1);
+#pragma unroll 1
+      for (int q = p.qa; q < p.qb; ++q) {
+        const int sq = qt % P::NQ;
+        wait(P::B_Q_FULL + sq, (qt / P::NQ) & 1);
+        const uint64_t dq = sdesc(base + P::OFF_Q + sq * P::QB);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (g >= tiles) break;
+          const uint32_t buf = st[g] & 1;
+          wait(P::B_S_EMPTY + 2 * g + int(buf), ((st[g] >> 1) & 1) ^ 1);
+          tc_fence_after();
+          if (leader && ok) {
+            const uint64_t dk = sdesc(base + P::OFF_K + ((kt + g) % P::NK) * P::KB);
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i) {
+              const uint32_t off = ((i / 4) * (BK * 128) + (i % 4) * 32) >> 4;
+              mma_f16(tmem + g * 256 + buf * 128, dk + off, dq + off, idesc, i ? 1u : 0u);
+            }
+            if (q + 1 == p.qb) mma_commit(bar(P::B_K_EMPTY + (kt + g) % P::NK));
+            if (g + 1 == tiles) mma_commit(bar(P::B_Q_EMPTY + sq));
+            mma_commit(bar(P::B_S_FULL + 2 * g + buf));
+          }
+          ++st[g];
+        }
+        ++qt;
+      }
+      kt += uint32_t(tiles);
+    }
+    if (!ok) *abort_flag = 1;
+    if (leader) mma_commit(bar(P::B_DONE));
+    mbar_wait_bounded(bar(P::B_DONE), 0);
+  } else {
+    // -------------------------------------------------------------- weights
+    const int g = warp >> 2, tid = threadIdx.x & 127;
+    const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + g * 256;
+    float *ls = reinterpret_cast<float *>(sm + P::OFF_LSE) + g * 2 * BR;
+    const int tok = tid / a.G, hd = tid - tok * a.G;  // the column whose lse this thread brings
+    const float c = a.scale_log2;
+    uint32_t st = 0;
+    auto lse_of = [&](const Piece &q, int tile) {
+      const int j = tile * tpt + tok;
+      return tok < tpt && j < q.s.n ? a.lse[int64_t(q.s.t0 + j) * a.Hq + q.h * a.G + hd] : INFINITY;
+    };
+    // what a key had before, and whether its page is one
+    auto look = [&](const Piece &q, float &old, bool &good) {
+      const int i = q.k0 + g * BK + tid;
+      old = 0.0f;
+      good = false;
+      if (i < q.s.len) {
+        good = page_ok(a, q.b, i);
+        if (q.whole && i < q.s.old) old = *weight_at(a, q.b, q.h, i);
+      }
+    };
+    Piece p, nx;
+    float old = 0.0f, old_next = 0.0f, l = 0.0f;
+    bool good = false, good_next = false;
+    bool more = walk.next(a, p);
+    if (more) {
+      look(p, old, good);
+      l = lse_of(p, p.qa);
+    }
+    while (more && ok) {
+      const bool again = walk.next(a, nx);
+      if (again) look(nx, old_next, good_next);
+      const int i = p.k0 + g * BK + tid;
+      const bool tile = p.k0 + g * BK < p.s.len;
+      float sum = 0.0f;
+#pragma unroll 1
+      for (int q = p.qa; q < p.qb; ++q) {
+        const float mine = l;
+        if (q + 1 < p.qb) l = lse_of(p, q + 1);
+        else if (again) l = lse_of(nx, nx.qa);
+        if (!tile) continue;
+        const uint32_t buf = st & 1;
+        float *lb = ls + buf * BR;
+        lb[tid] = neg_lse2(mine);
+        named_sync(1 + g, 128);  // two steps on, all have read what was here
+        if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g + int(buf)), (st >> 1) & 1, abort_flag))) break;
+        tc_fence_after();
+        const int cols = min(tpt, p.s.n - q * tpt) * a.G;
+        // the first column whose token sees this key
+        const int c0 = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 1
+        for (int e0 = 0; e0 < cols; e0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(ts + buf * 128 + e0, v);
+          wait_ld32(v);
+          const bool all = __all_sync(0xffffffffu, c0 <= e0) && e0 + 32 <= cols;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 n = *reinterpret_cast<const float4 *>(lb + e0 + e);
+            float x[4] = {ex2(__fmaf_rn(__uint_as_float(v[e]), c, n.x)),
+                          ex2(__fmaf_rn(__uint_as_float(v[e + 1]), c, n.y)),
+                          ex2(__fmaf_rn(__uint_as_float(v[e + 2]), c, n.z)),
+                          ex2(__fmaf_rn(__uint_as_float(v[e + 3]), c, n.w))};
+            if (!all) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (e0 + e + k < c0 || e0 + e + k >= cols) x[k] = 0.0f;
+            }
+            s0 += x[0] + x[2];
+            s1 += x[1] + x[3];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(P::B_S_EMPTY + 2 * g + int(buf)));
+        ++st;
+        sum += s0 + s1;
+      }
+      if (!ok) break;
+      if (p.qa == p.qb && again) l = lse_of(nx, nx.qa);  // a sequence with no token here
+      if (tile && i < p.s.len) {
+        if (!good) set_status(a.status, WQ_ERR_INDEX);
+        if (!p.whole) a.part[(int64_t(blockIdx.x) * 2 + p.slot) * PAIR + g * BK + tid] = sum;
+        else if (good) *weight_at(a, p.b, p.h, i) = __fmaf_rn(a.decay, old, sum);
+      }
+      p = nx;
+      old = old_next;
+      good = good_next;
+      more = again;
+    }
+  }
+  if (!ok) {
+    *abort_flag = 1;
+    set_status(a.status, WQ_ERR_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == WARP_MMA) tmem_dealloc(tmem, 512);
+}
+
+// Adds the parts of the pair that block c of the first kernel began and left
+// to the blocks after it, in their order.
+__global__ void __launch_bounds__(NTHREADS) attn_weights_join_kernel(const WeightArgs a) {
+  __shared__ int64_t scan[NTHREADS / 32], out[2];
+  const int64_t blocks = gridDim.x + 1, c = blockIdx.x;
+  const Place at = locate(a, scan, out, false, [&](int64_t total) { return total * (c + 1) / blocks; });
+  wait_last_kernel();  // in every block: what follows the join may then rely on both
+  if (at.at >= at.total) return;
+  Walk w;
+  w.begin(a, at, 1);
+  const int64_t start = at.at - w.u;
+  if (w.u == 0 || start < at.total * c / blocks) return;
+  const int64_t end = start + (w.s.before(w.p + 1, a.shift) - w.s.before(w.p, a.shift));
+  const int i = w.p * PAIR + threadIdx.x;
+  if (threadIdx.x >= PAIR || i >= w.s.len || !page_ok(a, w.b, i)) return;
+  float sum = a.part[(c * 2 + 1) * PAIR + threadIdx.x];
+  int64_t lo = at.at;  // where block k begins
+  for (int64_t k = c + 1; k < blocks && lo < end; ++k) {
+    const int64_t hi = at.total * (k + 1) / blocks;
+    if (lo < hi) sum += a.part[k * 2 * PAIR + threadIdx.x];  // not of a block without units
+    lo = hi;
+  }
+  float *to = weight_at(a, w.b, w.h, i);
+  *to = __fmaf_rn(a.decay, i < w.s.old ? *to : 0.0f, sum);
+}
+
+// Any page size and pitch: a block takes 32 keys of one head, a lane a key; the
+// warps share the rows, and add their sums in the order of the warps.
+template <class DT>
+__global__ void __launch_bounds__(256) attn_weights_any_kernel(const WeightArgs a) {
+  constexpr int KT = 32, NW = 8;
+  __shared__ float ks[KT][129];
+  __shared__ float qs[NW][128];
+  __shared__ float part[NW][KT];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = (a.max_len + KT - 1) / KT;
+  const int tile = int(blockIdx.x % unsigned(tiles)), bh = int(blockIdx.x / unsigned(tiles));
+  const int b = bh / a.heads, h = bh - b * a.heads;
+  const int c0 = first_of(a, b), c1 = first_of(a, b + 1), l = a.key_len[b];
+  const Seq s = seq_of(a, c0, c1, l);
+  if (tile == 0 && h == 0 && threadIdx.x == 0 && !in_range(a, s, c0, c1, l)) set_status(a.status, WQ_ERR_INDEX);
+  const int k0 = tile * KT, i = k0 + lane;
+  if (k0 >= s.len) return;
+  for (int r = warp; r < KT; r += NW) {
+    const int key = k0 + r;
+    const bool good = key < s.len && page_ok(a, b, key);
+    const int page = good ? a.page_table[b * a.ld_table + key / a.page_size] : 0;
+    const uint16_t *k = a.k + page * a.k_page + h * a.k_head + key % a.page_size * a.k_token;
+    for (int d = lane; d < a.dk; d += 32) ks[r][d] = good ? DT::to_f(k[d]) : 0.0f;
+  }
+  __syncthreads();
+  float sum = 0.0f;
+  const int64_t rows = int64_t(s.n) * a.G;
+  for (int64_t r = warp; r < rows; r += NW) {
+    const int j = int(r / a.G), hd = h * a.G + int(r - int64_t(j) * a.G);
+    if (s.old + j < k0) continue;  // sees none of these keys
+    const uint16_t *q = a.q + (s.t0 + j) * a.q_token + hd * a.q_head;
+    __syncwarp();
+    for (int d = lane; d < a.dk; d += 32) qs[warp][d] = DT::to_f(q[d]);
+    __syncwarp();
+    float x = 0.0f;
+    for (int d = 0; d < a.dk; ++d) x = __fmaf_rn(qs[warp][d], ks[lane][d], x);
+    x = ex2(__fmaf_rn(x, a.scale_log2, neg_lse2(a.lse[int64_t(s.t0 + j) * a.Hq + hd])));
+    if (i <= s.old + j) sum += x;
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && i < s.len) {
+    if (!page_ok(a, b, i)) {
+      set_status(a.status, WQ_ERR_INDEX);
+      return;
+    }
+    sum = 0.0f;
+    for (int w = 0; w < NW; ++w) sum += part[w][lane];
+    float *to = weight_at(a, b, h, i);
+    *to = __fmaf_rn(a.decay, i < s.old ? *to : 0.0f, sum);
+  }
+}
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+template <class DT, int D>
+int launch_tiles(const WeightArgs &a, cudaStream_t st) {
+  auto *k = attn_weights_kernel<DT, D>;
+  static OncePerDevice sized;
+  if (!allow_smem(sized, k, Plan<D>::SMEM)) return WQ_ERR_LAUNCH;
+  CUtensorMap mq, mk;
+  auto pitch = [](int64_t extent, int64_t stride) { return extent == 1 && stride == 0 ? 8 : stride; };
+  const int64_t qd[3] = {a.dk, a.Hq, a.T};
+  const int64_t qs[2] = {pitch(a.Hq, a.q_head), pitch(a.T, a.q_token)};
+  const int qb[3] = {64, a.G, 1 << a.shift};
+  const int box[4] = {64, a.box, 1, 1};
+  const int64_t kd[4] = {a.dk, a.page_size, a.heads, a.num_pages};
+  const int64_t ks[3] = {pitch(a.page_size, a.k_token), pitch(a.heads, a.k_head), pitch(a.num_pages, a.k_page)};
+  if (!make_tma_nd_b16_sw128(&mq, a.q, 3, qd, qs, qb) || !make_tma_nd_b16_sw128(&mk, a.k, 4, kd, ks, box))
+    return WQ_ERR_UNSUPPORTED;
+  k<<<unsigned(a.blocks), NTHREADS, Plan<D>::SMEM, st>>>(mq, mk, a);
+  int rc = launched(1);
+  if (rc == WQ_OK && a.part && a.blocks > 1)
+    rc = attn::launch_chained(attn_weights_join_kernel, unsigned(a.blocks - 1), NTHREADS, 0, true, st, a);
+  return rc;
+}
+
+template <class DT>
+int launch_t(const WeightArgs &a, cudaStream_t st) {
+  if (a.tiles) return a.dk > 64 ? launch_tiles<DT, 128>(a, st) : launch_tiles<DT, 64>(a, st);
+  const int64_t blocks = int64_t(a.B) * a.heads * ((a.max_len + 31) / 32);
+  if (blocks >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
+  attn_weights_any_kernel<DT><<<unsigned(blocks), 256, 0, st>>>(a);
+  return launched(1);
+}
+
+}  // namespace
+
+// Query tiles of a power of two of tokens: as many as fill 128 rows, no more
+// than a sequence may have (a decode step's tile is 16 columns wide, not 128).
+void plan_weights(WeightArgs &a) {
+  a.shift = 0;
+  while ((2 << a.shift) * a.G <= BR && (1 << a.shift) < a.max_q) ++a.shift;
+  a.cols = (((1 << a.shift) * a.G) + 15) / 16 * 16;
+  a.box = gcd(a.page_size, BK);
+  const bool pitches = (a.k_token || a.page_size == 1) && (a.k_head || a.heads == 1) &&
+                       (a.k_page || a.num_pages <= 1);
+  // TMA boxes of 8 keys or more, a lane for each box of a pair; pitches other
+  // than zero; waits that end after 1 s, which 2^25 keys do not reach
+  a.tiles = a.T > 0 && a.page_size % 8 == 0 && a.num_pages > 0 && pitches && a.max_len <= (1 << 25);
+  const int64_t most = int64_t(a.B) * a.heads * ((a.max_len + PAIR - 1) / PAIR) *
+                       std::max(1, (a.max_q + (1 << a.shift) - 1) >> a.shift);
+  a.blocks = int(std::max<int64_t>(1, std::min<int64_t>(MAX_BLOCKS, most)));
+  a.split = a.tiles && a.max_q > (1 << a.shift);
+}
+
+size_t weights_ws_bytes(const WeightArgs &a) {
+  return a.split ? size_t(a.blocks) * 2 * PAIR * sizeof(float) : 0;
+}
+
+int launch_weights(const WeightArgs &a, int dtype, cudaStream_t st) {
+  return dtype == WQ_DT_BF16 ? launch_t<Bf16>(a, st) : launch_t<F16>(a, st);
+}
+
+}  // namespace wq

@@ -219,4 +219,34 @@ int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st);
 size_t attention_ws_bytes(const AttnArgs &a);
 int launch_attention(const AttnArgs &a, int dtype, cudaStream_t st);
 
+struct WeightArgs {
+  const uint16_t *q;
+  int64_t q_token, q_head;
+  int T, B, max_q, Hq, heads, G;
+  const int32_t *cu_q;
+  const uint16_t *k;
+  int64_t k_page, k_head, k_token, num_pages;
+  int page_size, dk;
+  const int32_t *page_table;
+  int64_t ld_table;
+  const int32_t *key_len;
+  int max_len;
+  float scale_log2, decay;
+  const float *lse;  // [T][Hq]
+  float *w;
+  int64_t w_seq, w_head;
+  int32_t *status;
+  // plan
+  int shift;    // log2 of the tokens of a query tile
+  int cols;     // its rows, in whole 16s
+  int box;      // cache rows of one TMA box
+  int blocks;   // that share the line of units
+  bool tiles;   // the tensor-memory kernel takes it
+  bool split;   // a pair of key tiles may be cut between blocks
+  float *part;  // [blocks][2][256], nullptr unless split
+};
+void plan_weights(WeightArgs &a);
+size_t weights_ws_bytes(const WeightArgs &a);
+int launch_weights(const WeightArgs &a, int dtype, cudaStream_t st);
+
 }  // namespace wq

@@ -82,6 +82,40 @@ int fill_attention(AttnArgs &a, int64_t T, int B, int max_q, int q_heads, const 
   return WQ_OK;
 }
 
+// Whether rows of n elements at b * seq + h * head, b < B and h < heads, share none
+bool rows_apart(int64_t B, int64_t seq, int64_t heads, int64_t head, int64_t n) {
+  if (heads == 1) return B == 1 || seq >= n;
+  if (B == 1) return head >= n;
+  return head <= seq ? head >= n && seq >= (heads - 1) * head + n : seq >= n && head >= (B - 1) * seq + n;
+}
+
+int fill_weights(WeightArgs &a, int64_t T, int B, int max_q, int q_heads, const wq_paged_cache *c,
+                 int64_t max_len) {
+  if (T < 0 || B < 0 || max_q < 0 || q_heads < 1 || max_len < 0 || !cache_ok(c) || q_heads % c->heads)
+    return WQ_ERR_INVALID_ARG;
+  if (T >= (1 << 24) || B >= (1 << 24) || max_len >= (int64_t(1) << 30) || q_heads > (1 << 16) ||
+      q_heads / c->heads > 128 || c->dk % 8 || c->dk > 128 || c->k_page % 8 || c->k_head % 8 ||
+      c->k_token % 8)
+    return WQ_ERR_UNSUPPORTED;
+  a = WeightArgs{};
+  a.T = int(T);
+  a.B = B;
+  a.max_q = int(max_q < T ? max_q : T);
+  a.Hq = q_heads;
+  a.heads = c->heads;
+  a.G = q_heads / c->heads;
+  a.k = static_cast<const uint16_t *>(c->k);
+  a.k_page = c->k_page;
+  a.k_head = c->k_head;
+  a.k_token = c->k_token;
+  a.num_pages = c->num_pages;
+  a.page_size = c->page_size;
+  a.dk = c->dk;
+  a.max_len = int(max_len);
+  plan_weights(a);
+  return WQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -362,6 +396,57 @@ int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_head, i
                                            ((rows * a.dv * 4 + 255) & ~size_t(255)));
   }
   return launch_attention(a, cache->dtype, stream);
+}
+
+size_t wq_attention_weights_paged_workspace_size(int64_t T, int B, int max_q, int q_heads,
+                                                 const wq_paged_cache *cache, int64_t max_len) {
+  WeightArgs a;
+  if (fill_weights(a, T, B, max_q, q_heads, cache, max_len) != WQ_OK) return 0;
+  return weights_ws_bytes(a);
+}
+
+int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_head, int64_t T, int B,
+                               const int32_t *cu_q, int max_q, int q_heads,
+                               const wq_paged_cache *cache, const int32_t *page_table,
+                               int64_t ld_table, const int32_t *key_len, int64_t max_len, float scale,
+                               const float *lse, float decay, float *weights, int64_t w_seq,
+                               int64_t w_head, void *ws, size_t ws_bytes, int32_t *status,
+                               wq_stream_t stream) {
+  WeightArgs a;
+  int rc = fill_weights(a, T, B, max_q, q_heads, cache, max_len);
+  if (rc != WQ_OK) return rc;
+  if (q_token < 0 || q_head < 0 || ld_table < 0 || w_seq < 0 || w_head < 0 || !(scale > 0.0f) ||
+      !(scale < INFINITY) || !(decay >= 0.0f) || !(decay < INFINITY))
+    return WQ_ERR_INVALID_ARG;
+  if (B == 0 || max_len == 0) return WQ_OK;
+  if (!cache->k || !page_table || !key_len || !weights || max_len > ld_table * cache->page_size ||
+      (T > 0 && (!q || !lse)))
+    return WQ_ERR_INVALID_ARG;
+  if (cu_q ? T > 0 && max_q < 1 : int64_t(max_q) * B != T) return WQ_ERR_INVALID_ARG;
+  if (!rows_apart(B, w_seq, a.heads, w_head, max_len)) return WQ_ERR_INVALID_ARG;
+  if ((T > 1 && !q_token) || (q_heads > 1 && !q_head)) return WQ_ERR_UNSUPPORTED;
+  if (q_token % 8 || q_head % 8 || !al(q, 16) || !al(cache->k, 16) || !al(lse, 4) || !al(weights, 4))
+    return WQ_ERR_UNSUPPORTED;
+  if (weights_ws_bytes(a) > 0 && (!ws || !al(ws, 16) || ws_bytes < weights_ws_bytes(a)))
+    return WQ_ERR_WORKSPACE;
+  rc = device_ok();
+  if (rc != WQ_OK) return rc;
+  a.q = static_cast<const uint16_t *>(q);
+  a.q_token = q_token;
+  a.q_head = q_head;
+  a.cu_q = cu_q;
+  a.page_table = page_table;
+  a.ld_table = ld_table;
+  a.key_len = key_len;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.decay = decay;
+  a.lse = lse;
+  a.w = weights;
+  a.w_seq = w_seq;
+  a.w_head = w_head;
+  a.status = status;
+  a.part = a.split ? static_cast<float *>(ws) : nullptr;
+  return launch_weights(a, cache->dtype, stream);
 }
 
 }  // extern "C"
