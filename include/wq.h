@@ -652,7 +652,7 @@ WQ_API int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_
 
 /* ---------------------------------------------------------------------------
  * Accumulated attention weight of cached keys: what each key of a sequence has
- * been worth to the tokens so far.
+ * been worth to the tokens so far, the measure that wq_evict_paged goes by.
  * Sequences, tokens, keys and pages are those of wq_attention_shared_prefix
  * (key_len its suffix_len), whose lse of the same call is taken: with a shared
  * prefix the weights are those of the whole softmax.  For sequence b with n new
@@ -685,6 +685,39 @@ WQ_API int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_
                                       float scale, const float *lse, float decay, float *weights,
                                       int64_t w_seq, int64_t w_head, void *ws, size_t ws_bytes,
                                       int32_t *status, wq_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Eviction: of each sequence's keys at most `budget` stay, head by head, and
+ * move together.  Of n = key_len[b] > budget keys of head h there stay the
+ * `first` ones, the `recent` last ones, and of those between the budget - first
+ * - recent with the largest weights[b][h][.] (as wq_attention_weights_paged has
+ * summed them; of equal ones the earlier, -0 and 0 are equal, a NaN is less than
+ * all others).  They keep their order: kept[b][h][j] (int32 [B][heads][budget],
+ * contiguous) is the place of the j-th before, its key and value go to place j
+ * of the sequence and its weight to weights_out[b][h][j].  new_len[b] = min(n,
+ * budget); kept is -1 from there on.  With n <= budget all stay (kept[j] = j).
+ * out_table NULL (or page_table itself): in place, the pages past the new length
+ * are the caller's to give back; a page may then be in no two sequences.  Else
+ * the rows go to the pages out_table[b][.], pages of their own that no sequence
+ * of the call reads, and the old ones stay as they are (a prompt that others
+ * still use).  weights_out may be weights itself (same pitches) or apart from
+ * it.  Places at or past a length are neither read nor written.  Keys need not
+ * be turned to other positions: they carry the ones that they were appended
+ * with.
+ * max_len: host bound on the lengths; longer ones are cut with status =
+ * WQ_ERR_INDEX.  A page id outside [0, num_pages) sets the same status and its
+ * rows are not moved.  key_len and new_len must not overlap.
+ * Requirements: budget >= 1, first + recent <= budget, bf16 or fp16, dk and dv
+ * at most 16384.  16-byte accesses serve keys, values and pitches in multiples
+ * of 8 elements.  Workspace: 8 bytes a kept key of every head. */
+WQ_API size_t wq_evict_paged_workspace_size(int B, int heads, int64_t budget);
+WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
+                          const wq_paged_cache *cache, int B, const int32_t *page_table,
+                          int64_t ld_table, const int32_t *key_len, int64_t max_len,
+                          int64_t budget, int64_t recent, int64_t first, const int32_t *out_table,
+                          int64_t ld_out, float *weights_out, int64_t o_seq, int64_t o_head,
+                          int32_t *new_len, int32_t *kept, void *ws, size_t ws_bytes,
+                          int32_t *status, wq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -101,6 +101,8 @@ _SIGS = {
     "wq_attention_shared_prefix": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P, _S, _P, _P]),
     "wq_attention_weights_paged_workspace_size": (_S, [_L, _I, _I, _I, _P, _L]),
     "wq_attention_weights_paged": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _F, _P, _F, _P, _L, _L, _P, _S, _P, _P]),
+    "wq_evict_paged_workspace_size": (_S, [_I, _I, _L]),
+    "wq_evict_paged": (_I, [_P, _L, _L, _P, _I, _P, _L, _P, _L, _L, _L, _L, _P, _L, _P, _L, _L, _P, _P, _P, _S, _P, _P]),
     "wq_moe_forward_masked": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P, _P]),
 }
 
@@ -1087,3 +1089,49 @@ def attention_weights_paged(q, k_cache, page_table, key_len, max_len, lse, weigh
         weights.data_ptr(), sw[0], sw[1], ws.data_ptr(), size, _status(status, dev),
         _TC._cuda_getCurrentRawStream(dev)), "wq_attention_weights_paged")
     return weights
+
+
+def evict_paged_workspace(weights, max_len, budget):
+    """A workspace for evict_paged calls of these sizes."""
+    n = lib().wq_evict_paged_workspace_size(weights.shape[0], weights.shape[1], budget)
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=weights.device)
+
+
+def evict_paged(weights, k_cache, v_cache, page_table, key_len, max_len, budget, recent=0, first=0,
+                out_table=None, weights_out=None, new_len=None, kept=None, ws=None, status=None):
+    """Keep at most `budget` keys of each sequence (page_table int32 [B, pages],
+    key_len int32 [B]), head by head: the `first` and the `recent` ones and the
+    heaviest others by weights float32 [B, heads, max_len or more].  Keys, values
+    and weights move together, in their order: in place, or with out_table int32
+    [B, pages] into other pages; weights go to weights_out [B, heads, budget or
+    more] (default: weights itself).  Returns (new_len [B], kept int32 [B, heads,
+    budget]: the places kept, -1 past new_len)."""
+    c, heads, page, _, _, dev, _ = _cache(k_cache, v_cache)
+    B = _dense(key_len, torch.int32, "key_len", dev).numel()
+    rows = min(budget, max_len)
+    tables = []
+    for t, name, keys in ((page_table, "page_table", max_len), (out_table, "out_table", rows)):
+        if t is None and name == "out_table":
+            break
+        ps = t.shape
+        pages = ps[-1] if len(ps) == 2 else 0
+        tables += [t.data_ptr(), _rows_as(t, (B, pages), torch.int32, name, dev)]
+        if keys > pages * page:
+            raise WQError(f"{name} has too few columns for {keys} keys")
+    sw = _per_key(weights, B, heads, max_len, torch.float32, "weights", dev)
+    if weights_out is None:
+        weights_out = weights
+    so = _per_key(weights_out, B, heads, rows, torch.float32, "weights_out", dev)
+    if new_len is None:
+        new_len = torch.empty_like(key_len)
+    _dense_as(new_len, (B,), torch.int32, "new_len", dev)
+    if kept is None:
+        kept = torch.empty(B, heads, budget, dtype=torch.int32, device=key_len.device)
+    _dense_as(kept, (B, heads, budget), torch.int32, "kept", dev)
+    ws, size = _workspace(ws, lambda: lib().wq_evict_paged_workspace_size(B, heads, budget), dev)
+    out = tables[2:] or (None, 0)
+    _check(lib().wq_evict_paged(
+        weights.data_ptr(), sw[0], sw[1], c, B, tables[0], tables[1], key_len.data_ptr(), max_len, budget, recent, first,
+        out[0], out[1], weights_out.data_ptr(), so[0], so[1], new_len.data_ptr(), kept.data_ptr(), ws.data_ptr(), size,
+        _status(status, dev), _TC._cuda_getCurrentRawStream(dev)), "wq_evict_paged")
+    return new_len, kept

@@ -249,4 +249,25 @@ void plan_weights(WeightArgs &a);
 size_t weights_ws_bytes(const WeightArgs &a);
 int launch_weights(const WeightArgs &a, int dtype, cudaStream_t st);
 
+struct EvictArgs {
+  const float *w;
+  int64_t w_seq, w_head;
+  uint16_t *k, *v;
+  int64_t k_page, k_head, k_token, v_page, v_head, v_token, num_pages;
+  int page_size, heads, dk, dv, B;
+  const int32_t *page_table, *out_table;
+  int64_t ld_table, ld_out;
+  const int32_t *key_len;
+  int max_len, budget, recent, first;
+  bool in_place;
+  float *w_out;
+  int64_t o_seq, o_head;
+  int32_t *new_len, *kept;
+  int32_t *status;
+  int2 *map;  // [B][heads][budget]: page and place of the keys that stay
+  // of the moving kernel: blocks of columns of keys and of values, of rows
+  int k_parts, v_parts, row_blocks;
+};
+int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st);
+
 }  // namespace wq

@@ -449,4 +449,75 @@ int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_head, i
   return launch_weights(a, cache->dtype, stream);
 }
 
+size_t wq_evict_paged_workspace_size(int B, int heads, int64_t budget) {
+  if (B < 1 || heads < 1 || budget < 1) return 0;
+  return size_t(B) * size_t(heads) * size_t(budget) * sizeof(int2);
+}
+
+int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq_paged_cache *cache,
+                   int B, const int32_t *page_table, int64_t ld_table, const int32_t *key_len,
+                   int64_t max_len, int64_t budget, int64_t recent, int64_t first,
+                   const int32_t *out_table, int64_t ld_out, float *weights_out, int64_t o_seq,
+                   int64_t o_head, int32_t *new_len, int32_t *kept, void *ws, size_t ws_bytes,
+                   int32_t *status, wq_stream_t stream) {
+  if (B < 0 || max_len < 0 || budget < 1 || recent < 0 || first < 0 || recent + first > budget || !cache_ok(cache) ||
+      ld_table < 0 || ld_out < 0 || w_seq < 0 || w_head < 0 || o_seq < 0 || o_head < 0)
+    return WQ_ERR_INVALID_ARG;
+  if (B == 0) return WQ_OK;
+  const int64_t rows = budget < max_len ? budget : max_len;  // that a sequence has at the end, at most
+  if (!key_len || !new_len || !kept || (max_len > 0 && (!weights || !weights_out || !page_table || !cache->k || !cache->v)))
+    return WQ_ERR_INVALID_ARG;
+  if (max_len > ld_table * cache->page_size || (out_table && rows > ld_out * cache->page_size)) return WQ_ERR_INVALID_ARG;
+  if (!rows_apart(B, w_seq, cache->heads, w_head, max_len) || !rows_apart(B, o_seq, cache->heads, o_head, rows))
+    return WQ_ERR_INVALID_ARG;
+  if (weights_out == weights && (w_seq != o_seq || w_head != o_head)) return WQ_ERR_INVALID_ARG;
+  // the lengths are read while the new ones are written
+  if (new_len < key_len + B && key_len < new_len + B) return WQ_ERR_INVALID_ARG;
+  if (B >= (1 << 24) || max_len >= (int64_t(1) << 30) || budget >= (int64_t(1) << 30) || cache->heads > (1 << 16) ||
+      cache->dk > (1 << 14) || cache->dv > (1 << 14) || !al(cache->k, 2) || !al(cache->v, 2) || !al(weights, 4) ||
+      !al(weights_out, 4))
+    return WQ_ERR_UNSUPPORTED;
+  if (!ws || !al(ws, 16) || ws_bytes < wq_evict_paged_workspace_size(B, cache->heads, budget)) return WQ_ERR_WORKSPACE;
+  const int rc = device_ok();
+  if (rc != WQ_OK) return rc;
+  EvictArgs a{};
+  a.w = weights;
+  a.w_seq = w_seq;
+  a.w_head = w_head;
+  a.k = static_cast<uint16_t *>(cache->k);
+  a.v = static_cast<uint16_t *>(cache->v);
+  a.k_page = cache->k_page;
+  a.k_head = cache->k_head;
+  a.k_token = cache->k_token;
+  a.v_page = cache->v_page;
+  a.v_head = cache->v_head;
+  a.v_token = cache->v_token;
+  a.num_pages = cache->num_pages;
+  a.page_size = cache->page_size;
+  a.heads = cache->heads;
+  a.dk = cache->dk;
+  a.dv = cache->dv;
+  a.B = B;
+  a.page_table = page_table;
+  a.ld_table = ld_table;
+  a.in_place = out_table == nullptr || out_table == page_table;
+  a.out_table = a.in_place ? page_table : out_table;
+  a.ld_out = a.in_place ? ld_table : ld_out;
+  a.key_len = key_len;
+  a.max_len = int(max_len);
+  a.budget = int(budget);
+  a.recent = int(recent);
+  a.first = int(first);
+  a.w_out = weights_out;
+  a.o_seq = o_seq;
+  a.o_head = o_head;
+  a.new_len = new_len;
+  a.kept = kept;
+  a.status = status;
+  a.map = static_cast<int2 *>(ws);
+  bool vec = al(cache->k, 16) && al(cache->v, 16) && cache->dk % 8 == 0 && cache->dv % 8 == 0;
+  for (int64_t p : {a.k_page, a.k_head, a.k_token, a.v_page, a.v_head, a.v_token}) vec = vec && p % 8 == 0;
+  return launch_evict(a, vec, stream);
+}
+
 }  // extern "C"
