@@ -719,6 +719,29 @@ WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
                           int32_t *new_len, int32_t *kept, void *ws, size_t ws_bytes,
                           int32_t *status, wq_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection: y, which holds
+ * the projection of x (wq_linear_w8a8's out, say), gets each token's adapter
+ * added in place:
+ *   y[t] += scales[a] * (x[t] A[a]^T) B[a]^T,  a = adapters[t],
+ * A [n][r][H], B [n][N][r], x [T][H] (pitch ldx), y [T][N] (pitch ldy), all of
+ * `dtype`, scales float [n] (NULL: ones), adapters int32 [T].  A token with a
+ * negative adapter has none: its row of y is neither read nor written.  An
+ * adapter at or past n counts as none and sets status = WQ_ERR_INDEX.  Tokens
+ * of one adapter may stand anywhere.  Adapters of smaller rank are padded with
+ * zeros.  Products and sums are float32; x A^T enters the second product with
+ * twice the bits of dtype's significand, and y is rounded once.  A row's result
+ * depends on its token and T alone, not on the tokens beside it.  y must not
+ * overlap the other arguments.
+ * Requirements: bf16 or fp16; H, N, r and pitches multiples of 8, r at most 128,
+ * n at most 8192, 16-byte aligned tensors.  Workspace:
+ * wq_lora_add_workspace_size(T, n) (0 bytes up to 256 tokens). */
+WQ_API size_t wq_lora_add_workspace_size(int64_t T, int n);
+WQ_API int wq_lora_add(const void *x, int64_t ldx, int64_t T, int64_t H, const void *A,
+                       const void *B, const float *scales, int n, int r, const int32_t *adapters,
+                       int64_t N, int dtype, void *y, int64_t ldy, void *ws, size_t ws_bytes,
+                       int32_t *status, wq_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

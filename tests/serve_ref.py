@@ -217,3 +217,23 @@ def attention_weights(q, k_cache, page_table, key_len, cu_q, lse, weights, scale
             w[b, h, :m] += add
             tol[b, h, :m] += (p * e * 1.01).sum((0, 1)) + chain * E * add + E * w[b, h, :m].abs() + TINY[torch.float32]
     return w, tol
+
+
+def lora(y, x, A, B, ids, scales, dtype):
+    """y plus each token's adapter in float64, and the tolerance: H products and
+    at most 16 sums more in float32 for a sum of the first product, two 16-bit
+    operands that leave 2 U^2 of it (fp16: relative to the row's largest), r
+    products of both operands for a sum of the second, the scale, y's rounding."""
+    y, x, A, B, s = map(f64, (y, x, A, B, scales))
+    out, tol = y.clone(), torch.zeros_like(y)
+    for t, a in enumerate(ids.tolist()):
+        if 0 <= a < A.shape[0]:
+            h, hm = A[a] @ x[t], A[a].abs() @ x[t].abs()
+            f = 1.0 if s is None else float(s[a])
+            d = f * (B[a] @ h)
+            top = h.abs().max() if dtype == torch.float16 else 0.0
+            eh = (A.shape[2] + 16) * E * hm + 2 * U[dtype] ** 2 * (h.abs() + top) + TINY[torch.float32]
+            out[t] += d
+            tol[t] = abs(f) * (B[a].abs() @ (eh + (2 * A.shape[1] + 4) * E * h.abs())) + 4 * E * (d.abs() + y[t].abs()) + \
+                U[dtype] * out[t].abs() + TINY[dtype]
+    return out, tol

@@ -103,6 +103,8 @@ _SIGS = {
     "wq_attention_weights_paged": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _F, _P, _F, _P, _L, _L, _P, _S, _P, _P]),
     "wq_evict_paged_workspace_size": (_S, [_I, _I, _L]),
     "wq_evict_paged": (_I, [_P, _L, _L, _P, _I, _P, _L, _P, _L, _L, _L, _L, _P, _L, _P, _L, _L, _P, _P, _P, _S, _P, _P]),
+    "wq_lora_add_workspace_size": (_S, [_L, _I]),
+    "wq_lora_add": (_I, [_P, _L, _L, _L, _P, _P, _P, _I, _I, _P, _L, _I, _P, _L, _P, _S, _P, _P]),
     "wq_moe_forward_masked": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P, _P]),
 }
 
@@ -1135,3 +1137,37 @@ def evict_paged(weights, k_cache, v_cache, page_table, key_len, max_len, budget,
         out[0], out[1], weights_out.data_ptr(), so[0], so[1], new_len.data_ptr(), kept.data_ptr(), ws.data_ptr(), size,
         _status(status, dev), _TC._cuda_getCurrentRawStream(dev)), "wq_evict_paged")
     return new_len, kept
+
+
+# ---------------------------------------------------------------- adapters beside a projection
+def lora_add_workspace(y, x, A):
+    """A workspace for lora_add calls of these sizes."""
+    n = lib().wq_lora_add_workspace_size(x.shape[0], A.shape[0])
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
+
+
+def lora_add(y, x, A, B, adapters, scales=None, ws=None, status=None):
+    """Add each token's low-rank adapter to y [T, N], the projection of x
+    [T, H], in place: y[t] += scales[a] * (x[t] A[a]^T) B[a]^T for a =
+    adapters[t] (int32 [T], negative: none), A [n, r, H], B [n, N, r], scales
+    float32 [n].  Returns y."""
+    code, dev, dt, shape = _main(x, _HALVES, 2, "x")
+    T, H = shape
+    ldx = _rows(x, shape, "x")
+    As = _dense(A, dt, "A", dev)
+    if len(As) != 3 or As[2] != H:
+        raise WQError(f"A must be [adapters, rank, {H}], got {list(As)}")
+    n, r, _ = As
+    Bs = _dense(B, dt, "B", dev)
+    if len(Bs) != 3 or Bs[0] != n or Bs[2] != r:
+        raise WQError(f"B must be [{n}, outputs, {r}], got {list(Bs)}")
+    N = Bs[1]
+    ldy = _rows_as(y, (T, N), dt, "y", dev)
+    ids = _dense_as(adapters, (T,), torch.int32, "adapters", dev)
+    if scales is not None:
+        _dense_as(scales, (n,), torch.float32, "scales", dev)
+    ws, size = _workspace(ws, lambda: lib().wq_lora_add_workspace_size(T, n), dev)
+    _check(lib().wq_lora_add(x.data_ptr(), ldx, T, H, A.data_ptr(), B.data_ptr(), _at(scales), n, r, ids, N, code,
+                             y.data_ptr(), ldy, ws.data_ptr(), size, _status(status, dev),
+                             _TC._cuda_getCurrentRawStream(dev)), "wq_lora_add")
+    return y

@@ -270,4 +270,22 @@ struct EvictArgs {
 };
 int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st);
 
+struct LoraArgs {
+  const uint16_t *x;
+  int64_t ldx;
+  uint16_t *y;
+  int64_t ldy;
+  const uint16_t *A, *B;  // [n][r][H], [n][N][r]
+  const float *scales;    // [n], nullptr: ones
+  const int32_t *ids;     // [T]
+  int T, H, N, r, n;
+  int32_t *status;
+  // tokens in the order of their adapters and the tiles (adapter, first place,
+  // tokens), nullptr where each cluster looks for its own
+  int *order, *ntiles;
+  int4 *tiles;
+};
+size_t lora_ws_bytes(int64_t T, int64_t n);
+int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st);
+
 }  // namespace wq

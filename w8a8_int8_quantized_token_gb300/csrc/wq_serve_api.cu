@@ -520,4 +520,39 @@ int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq
   return launch_evict(a, vec, stream);
 }
 
+size_t wq_lora_add_workspace_size(int64_t T, int n) { return T < 1 || n < 1 ? 0 : lora_ws_bytes(T, n); }
+
+int wq_lora_add(const void *x, int64_t ldx, int64_t T, int64_t H, const void *A, const void *B,
+                const float *scales, int n, int r, const int32_t *adapters, int64_t N, int dtype,
+                void *y, int64_t ldy, void *ws, size_t ws_bytes, int32_t *status,
+                wq_stream_t stream) {
+  if (T < 0 || H < 0 || N < 0 || n < 0 || r < 1 || (dtype != WQ_DT_BF16 && dtype != WQ_DT_F16))
+    return WQ_ERR_INVALID_ARG;
+  if (T == 0 || N == 0 || n == 0 || H == 0) return WQ_OK;
+  if (!x || !A || !B || !adapters || !y || ldx < H || ldy < N) return WQ_ERR_INVALID_ARG;
+  if (H % 8 || N % 8 || r % 8 || r > 128 || ldx % 8 || ldy % 8 || n > 8192 || T >= (1 << 24) ||
+      H > (1 << 20) || N > (1 << 20) || !al(x, 16) || !al(A, 16) || !al(B, 16) || !al(y, 16) || !al(scales, 4))
+    return WQ_ERR_UNSUPPORTED;
+  const size_t need = lora_ws_bytes(T, n);
+  if (need > 0 && (!ws || !al(ws, 16) || ws_bytes < need)) return WQ_ERR_WORKSPACE;
+  const int rc = device_ok();
+  if (rc != WQ_OK) return rc;
+  LoraArgs a{};
+  a.x = static_cast<const uint16_t *>(x);
+  a.ldx = ldx;
+  a.y = static_cast<uint16_t *>(y);
+  a.ldy = ldy;
+  a.A = static_cast<const uint16_t *>(A);
+  a.B = static_cast<const uint16_t *>(B);
+  a.scales = scales;
+  a.ids = adapters;
+  a.T = int(T);
+  a.H = int(H);
+  a.N = int(N);
+  a.r = r;
+  a.n = n;
+  a.status = status;
+  return launch_lora(a, dtype, ws, stream);
+}
+
 }  // extern "C"
