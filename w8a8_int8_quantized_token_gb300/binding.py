@@ -1028,6 +1028,14 @@ def _keys(k_cache):
                        code), heads, page, dk, dev, dt
 
 
+def _sequences(key_len, dev):
+    """Sequences of a call, one length each."""
+    shape = _dense(key_len, torch.int32, "key_len", dev)
+    if len(shape) != 1:
+        raise WQError(f"key_len must have 1 dimension, got {len(shape)}")
+    return shape[0]
+
+
 def _per_key(t, B, heads, least, dtype, name, dev):
     """Pitches of a tensor [B, heads, at least `least`] that has a value for each key."""
     _of(t, dtype, name, dev)
@@ -1067,7 +1075,7 @@ def attention_weights_paged(q, k_cache, page_table, key_len, max_len, lse, weigh
     T, Hq, _ = shape
     _of(q, dt, "q", dev)
     sq = _heads(q, shape, "q")
-    B = _dense(key_len, torch.int32, "key_len", dev).numel()
+    B = _sequences(key_len, dev)
     ps = page_table.shape
     pages = ps[-1] if len(ps) == 2 else 0
     ld = _rows_as(page_table, (B, pages), torch.int32, "page_table", dev)
@@ -1109,7 +1117,7 @@ def evict_paged(weights, k_cache, v_cache, page_table, key_len, max_len, budget,
     more] (default: weights itself).  Returns (new_len [B], kept int32 [B, heads,
     budget]: the places kept, -1 past new_len)."""
     c, heads, page, _, _, dev, _ = _cache(k_cache, v_cache)
-    B = _dense(key_len, torch.int32, "key_len", dev).numel()
+    B = _sequences(key_len, dev)
     rows = min(budget, max_len)
     tables = []
     for t, name, keys in ((page_table, "page_table", max_len), (out_table, "out_table", rows)):
