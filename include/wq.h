@@ -668,8 +668,7 @@ WQ_API int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_
  * step, after the attention.
  * max_q, max_len: host bounds, values above them are cut with status =
  * WQ_ERR_INDEX, as in the attention.  A page id outside [0, num_pages) sets the
- * same status; the weights of its keys stay as they were.  The cache's values
- * (v) are not read.  Scores, weights and sums are float32 and do not depend on
+ * same status; its keys count as zeros.  The cache's values (v) are not read.  Scores, weights and sums are float32 and do not depend on
  * the run.
  * Requirements: those of wq_attention_shared_prefix on q and the keys; rows of
  * weights that share no place; decay >= 0.

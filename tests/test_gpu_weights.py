@@ -134,20 +134,18 @@ def test_weights_of_one_softmax_add_up():
 
 
 def test_bad_pages_lengths_and_tokens_are_reported():
-    a = problem([1, 1], [100, 100], 2, 4, 64, 16, BF)
-    keep = a["weights"].clone()
-    a["page_table"][0, 2], a["page_table"][1, 0] = -1, 10 ** 6
-    want = {**a, "page_table": a["page_table"].clone(), "weights": keep.clone()}
-    want["page_table"][0, 2] = want["page_table"][1, 0] = 0  # any page: these keys are not looked at
-    st = wq.new_status()
-    wq.attention_weights_paged(**a, status=st)
-    assert int(st) == -6
-    wq.attention_weights_paged(**want)
-    same = torch.ones(100, dtype=torch.bool)
-    same[32:48] = False
-    assert torch.equal(a["weights"][0, :, :100][:, same], want["weights"][0, :, :100][:, same])
-    assert torch.equal(a["weights"][0, :, 32:48], keep[0, :, 32:48])
-    assert torch.equal(a["weights"][1, :, :16], keep[1, :, :16])
+    for page, dk in ((16, 64), (5, 64)):
+        a = problem([1, 1], [100, 100], 2, 4, dk, page, BF)
+        want = {**a, "page_table": a["page_table"].clone(), "weights": a["weights"].clone()}
+        a["page_table"][0, 2], a["page_table"][1, 0] = -1, 10 ** 6
+        kc = a["k_cache"]
+        for b, p in ((0, 2), (1, 0)):  # keys of a page that is none count as zeros
+            kc[want["page_table"][b, p].long()] = 0
+        st = wq.new_status()
+        wq.attention_weights_paged(**a, status=st)
+        assert int(st) == -6
+        check(want)
+        assert torch.equal(a["weights"].nan_to_num(), want["weights"].nan_to_num())
     for kw in (dict(key_len=i32([100, 101])), dict(key_len=i32([-1, 50])), dict(cu_q=i32([0, 1, 3]))):
         b, st = {**problem([1, 1], [100, 100], 2, 4, 64, 16, BF), **kw}, wq.new_status()
         wq.attention_weights_paged(**b, status=st)

@@ -161,6 +161,11 @@ struct Piece {
   int slot;    // else: where its sums go
 };
 
+// Whether the first step of piece o takes the query tile of the last one of p
+__device__ __forceinline__ bool same_queries(const Piece &p, const Piece &o) {
+  return p.b == o.b && p.h == o.h && p.qb > p.qa && o.qa == p.qb - 1;
+}
+
 // The pieces of a block, one after the other
 struct Walk {
   int b, h, p;
@@ -236,10 +241,6 @@ __device__ __forceinline__ float neg_lse2(float l) {
 __device__ __forceinline__ float *weight_at(const WeightArgs &a, int b, int h, int i) {
   return a.w + b * a.w_seq + h * a.w_head + i;
 }
-__device__ __forceinline__ bool page_ok(const WeightArgs &a, int b, int i) {
-  const int page = a.page_table[b * a.ld_table + i / a.page_size];
-  return unsigned(page) < unsigned(a.num_pages);
-}
 
 template <class DT, int D>
 __global__ void __launch_bounds__(NTHREADS, 1)
@@ -284,16 +285,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // lane L looks up box L of a pair, one piece ahead
     auto look = [&](const Piece &q) {
       const int key = q.k0 + lane * a.box;
-      if (lane >= 2 * nbox || key >= q.s.len) return -1;
-      const int page = a.page_table[q.b * a.ld_table + key / a.page_size];
-      return unsigned(page) < unsigned(a.num_pages) ? page : int(a.num_pages);  // a bad page reads as zeros
+      if (lane >= 2 * nbox || key >= q.s.len) return 0;
+      return a.page_table[q.b * a.ld_table + key / a.page_size];
     };
-    bool more = walk.next(a, p);
+    bool more = walk.next(a, p), fresh = true;
     int page = more ? look(p) : 0;
     while (more && ok) {
       const bool again = walk.next(a, nx);
       const int page_next = again ? look(nx) : 0;
       const int place = (p.k0 + lane * a.box) % a.page_size;
+      if (unsigned(page) >= unsigned(a.num_pages)) {  // read outside the tensor: zeros
+        page = int(a.num_pages);
+        set_status(a.status, WQ_ERR_INDEX);
+      }
       if (p.qb > p.qa) {
 #pragma unroll 1
         for (int g = 0; g < 2 && ok; ++g) {
@@ -318,6 +322,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
 #pragma unroll 1
         for (int q = p.qa; q < p.qb && ok; ++q) {
+          if (!fresh) {  // the tile is there
+            fresh = true;
+            continue;
+          }
           const int s = qt % P::NQ;
           if (!(ok = wait_warp(bar(P::B_Q_EMPTY + s), ((qt / P::NQ) & 1) ^ 1, abort_flag))) break;
           if (leader) {
@@ -329,6 +337,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           ++qt;
         }
+        fresh = !(again && same_queries(p, nx));
       }
       p = nx;
       page = page_next;
@@ -350,38 +359,47 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto wait = [&](int b, uint32_t parity) {
       if (ok) ok = wait_warp(bar(b), parity, abort_flag);
     };
-    Piece p;
-    while (ok && walk.next(a, p)) {
-      if (p.qb == p.qa) continue;
+    Piece p, nx;
+    bool more = walk.next(a, p), fresh = true;
+    while (ok && more) {
+      const bool again = walk.next(a, nx);
       const int tiles = p.k0 + BK < p.s.len ? 2 : 1;
-      for (int g = 0; g < tiles; ++g) wait(P::B_K_FULL + int((kt + g) % P::NK), ((kt + g) / P::NK) & 1);
+      if (p.qb > p.qa) {
+        const bool keep = again && same_queries(p, nx);  // the last query tile stays for the next piece
+        for (int g = 0; g < tiles; ++g) wait(P::B_K_FULL + int((kt + g) % P::NK), ((kt + g) / P::NK) & 1);
 #pragma unroll 1
-      for (int q = p.qa; q < p.qb; ++q) {
-        const int sq = qt % P::NQ;
-        wait(P::B_Q_FULL + sq, (qt / P::NQ) & 1);
-        const uint64_t dq = sdesc(base + P::OFF_Q + sq * P::QB);
+        for (int q = p.qa; q < p.qb; ++q) {
+          const int sq = qt % P::NQ;
+          if (fresh) wait(P::B_Q_FULL + sq, (qt / P::NQ) & 1);
+          const bool last = q + 1 == p.qb;
+          fresh = !(last && keep);
+          const uint64_t dq = sdesc(base + P::OFF_Q + sq * P::QB);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (g >= tiles) break;
-          const uint32_t buf = st[g] & 1;
-          wait(P::B_S_EMPTY + 2 * g + int(buf), ((st[g] >> 1) & 1) ^ 1);
-          tc_fence_after();
-          if (leader && ok) {
-            const uint64_t dk = sdesc(base + P::OFF_K + ((kt + g) % P::NK) * P::KB);
-#pragma unroll 1
-            for (int i = 0; i < steps; ++i) {
-              const uint32_t off = ((i / 4) * (BK * 128) + (i % 4) * 32) >> 4;
-              mma_f16(tmem + g * 256 + buf * 128, dk + off, dq + off, idesc, i ? 1u : 0u);
+          for (int g = 0; g < 2; ++g) {
+            if (g >= tiles) break;
+            const uint32_t buf = st[g] & 1;
+            wait(P::B_S_EMPTY + 2 * g + int(buf), ((st[g] >> 1) & 1) ^ 1);
+            tc_fence_after();
+            if (leader && ok) {
+              const uint64_t dk = sdesc(base + P::OFF_K + ((kt + g) % P::NK) * P::KB);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                if (i >= steps) break;
+                const uint32_t off = ((i / 4) * (BK * 128) + (i % 4) * 32) >> 4;
+                mma_f16(tmem + g * 256 + buf * 128, dk + off, dq + off, idesc, i ? 1u : 0u);
+              }
+              if (last) mma_commit(bar(P::B_K_EMPTY + (kt + g) % P::NK));
+              if (fresh && g + 1 == tiles) mma_commit(bar(P::B_Q_EMPTY + sq));
+              mma_commit(bar(P::B_S_FULL + 2 * g + buf));
             }
-            if (q + 1 == p.qb) mma_commit(bar(P::B_K_EMPTY + (kt + g) % P::NK));
-            if (g + 1 == tiles) mma_commit(bar(P::B_Q_EMPTY + sq));
-            mma_commit(bar(P::B_S_FULL + 2 * g + buf));
+            ++st[g];
           }
-          ++st[g];
+          if (fresh) ++qt;
         }
-        ++qt;
+        kt += uint32_t(tiles);
       }
-      kt += uint32_t(tiles);
+      p = nx;
+      more = again;
     }
     if (!ok) *abort_flag = 1;
     if (leader) mma_commit(bar(P::B_DONE));
@@ -398,66 +416,86 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int j = tile * tpt + tok;
       return tok < tpt && j < q.s.n ? a.lse[int64_t(q.s.t0 + j) * a.Hq + q.h * a.G + hd] : INFINITY;
     };
-    // what a key had before, and whether its page is one
-    auto look = [&](const Piece &q, float &old, bool &good) {
+    // what a key had before
+    auto look = [&](const Piece &q) {
       const int i = q.k0 + g * BK + tid;
-      old = 0.0f;
-      good = false;
-      if (i < q.s.len) {
-        good = page_ok(a, q.b, i);
-        if (q.whole && i < q.s.old) old = *weight_at(a, q.b, q.h, i);
+      return q.whole && i < q.s.old ? *weight_at(a, q.b, q.h, i) : 0.0f;
+    };
+    // columns e0 .. of a score tile, NC of them in v
+    float s0 = 0.0f, s1 = 0.0f;
+    auto weigh = [&](auto &v, const float *lb, int e0, int c0, int cols) {
+      constexpr int NC = sizeof(v) / 4;
+      const bool all = __all_sync(0xffffffffu, c0 <= e0) && e0 + NC <= cols;
+      if (all) {
+        const Pair cc = pair(c, c);
+        Pair s = pair(s0, s1);
+#pragma unroll
+        for (int e = 0; e < NC; e += 4) {
+          const float4 n = *reinterpret_cast<const float4 *>(lb + e0 + e);
+          float x, y;
+          split(fma_p(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, pair(n.x, n.y)), x, y);
+          s = add_p(s, pair(ex2(x), ex2(y)));
+          split(fma_p(pair(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), cc, pair(n.z, n.w)), x, y);
+          s = add_p(s, pair(ex2(x), ex2(y)));
+        }
+        split(s, s0, s1);
+      } else {
+#pragma unroll
+        for (int e = 0; e < NC; ++e) {
+          const float x = ex2(__fmaf_rn(__uint_as_float(v[e]), c, lb[e0 + e]));
+          if (e0 + e >= c0 && e0 + e < cols) (e & 1 ? s1 : s0) += x;
+        }
       }
     };
     Piece p, nx;
-    float old = 0.0f, old_next = 0.0f, l = 0.0f;
-    bool good = false, good_next = false;
-    bool more = walk.next(a, p);
+    float old = 0.0f, l = 0.0f;
+    uint32_t nq = 0;  // log-sum-exps staged so far
+    bool more = walk.next(a, p), fresh = true;
     if (more) {
-      look(p, old, good);
+      old = look(p);
       l = lse_of(p, p.qa);
     }
     while (more && ok) {
       const bool again = walk.next(a, nx);
-      if (again) look(nx, old_next, good_next);
+      const float old_next = again ? look(nx) : 0.0f;
       const int i = p.k0 + g * BK + tid;
       const bool tile = p.k0 + g * BK < p.s.len;
       float sum = 0.0f;
 #pragma unroll 1
       for (int q = p.qa; q < p.qb; ++q) {
+        const bool now = fresh;
         const float mine = l;
+        fresh = q + 1 < p.qb || !(again && same_queries(p, nx));
         if (q + 1 < p.qb) l = lse_of(p, q + 1);
-        else if (again) l = lse_of(nx, nx.qa);
+        else if (again && fresh) l = lse_of(nx, nx.qa);
         if (!tile) continue;
-        const uint32_t buf = st & 1;
-        float *lb = ls + buf * BR;
-        lb[tid] = neg_lse2(mine);
-        named_sync(1 + g, 128);  // two steps on, all have read what was here
+        if (now) {
+          ls[(++nq & 1) * BR + tid] = neg_lse2(mine);
+          named_sync(1 + g, 128);  // two tiles on, all have read what was here
+        }
+        const float *lb = ls + (nq & 1) * BR;
+        const uint32_t buf = st & 1, at = ts + buf * 128;
         if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g + int(buf)), (st >> 1) & 1, abort_flag))) break;
         tc_fence_after();
         const int cols = min(tpt, p.s.n - q * tpt) * a.G;
         // the first column whose token sees this key
         const int c0 = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
-        float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 1
-        for (int e0 = 0; e0 < cols; e0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(ts + buf * 128 + e0, v);
-          wait_ld32(v);
-          const bool all = __all_sync(0xffffffffu, c0 <= e0) && e0 + 32 <= cols;
+        s0 = s1 = 0.0f;
+        if (cols <= 8) {
+          uint32_t v[8];
+          tmem_ld8(at, v);
+          tmem_wait_ld(v);
+          weigh(v, lb, 0, c0, cols);
+        } else {
+          // the next 32 columns come while these are weighed
+          uint32_t v[2][32];
+          tmem_ld32(at, v[0]);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 n = *reinterpret_cast<const float4 *>(lb + e0 + e);
-            float x[4] = {ex2(__fmaf_rn(__uint_as_float(v[e]), c, n.x)),
-                          ex2(__fmaf_rn(__uint_as_float(v[e + 1]), c, n.y)),
-                          ex2(__fmaf_rn(__uint_as_float(v[e + 2]), c, n.z)),
-                          ex2(__fmaf_rn(__uint_as_float(v[e + 3]), c, n.w))};
-            if (!all) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (e0 + e + k < c0 || e0 + e + k >= cols) x[k] = 0.0f;
-            }
-            s0 += x[0] + x[2];
-            s1 += x[1] + x[3];
+          for (int k = 0; k < 4; ++k) {
+            if (32 * k >= cols) break;
+            wait_ld32(v[k & 1]);
+            if (32 * (k + 1) < cols) tmem_ld32(at + 32 * (k + 1), v[(k + 1) & 1]);
+            weigh(v[k & 1], lb, 32 * k, c0, cols);
           }
         }
         tc_fence_before();
@@ -467,15 +505,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         sum += s0 + s1;
       }
       if (!ok) break;
-      if (p.qa == p.qb && again) l = lse_of(nx, nx.qa);  // a sequence with no token here
-      if (tile && i < p.s.len) {
-        if (!good) set_status(a.status, WQ_ERR_INDEX);
+      if (p.qa == p.qb) {  // a sequence with no token here
+        fresh = true;
+        if (again) l = lse_of(nx, nx.qa);
+      }
+      if (i < p.s.len) {
         if (!p.whole) a.part[(int64_t(blockIdx.x) * 2 + p.slot) * PAIR + g * BK + tid] = sum;
-        else if (good) *weight_at(a, p.b, p.h, i) = __fmaf_rn(a.decay, old, sum);
+        else *weight_at(a, p.b, p.h, i) = __fmaf_rn(a.decay, old, sum);
       }
       p = nx;
       old = old_next;
-      good = good_next;
       more = again;
     }
   }
@@ -501,7 +540,7 @@ __global__ void __launch_bounds__(NTHREADS) attn_weights_join_kernel(const Weigh
   if (w.u == 0 || start < at.total * c / blocks) return;
   const int64_t end = start + (w.s.before(w.p + 1, a.shift) - w.s.before(w.p, a.shift));
   const int i = w.p * PAIR + threadIdx.x;
-  if (threadIdx.x >= PAIR || i >= w.s.len || !page_ok(a, w.b, i)) return;
+  if (threadIdx.x >= PAIR || i >= w.s.len) return;
   float sum = a.part[(c * 2 + 1) * PAIR + threadIdx.x];
   int64_t lo = at.at;  // where block k begins
   for (int64_t k = c + 1; k < blocks && lo < end; ++k) {
@@ -532,8 +571,12 @@ __global__ void __launch_bounds__(256) attn_weights_any_kernel(const WeightArgs 
   if (k0 >= s.len) return;
   for (int r = warp; r < KT; r += NW) {
     const int key = k0 + r;
-    const bool good = key < s.len && page_ok(a, b, key);
-    const int page = good ? a.page_table[b * a.ld_table + key / a.page_size] : 0;
+    int page = key < s.len ? a.page_table[b * a.ld_table + key / a.page_size] : 0;
+    const bool good = key < s.len && unsigned(page) < unsigned(a.num_pages);
+    if (key < s.len && !good) {
+      set_status(a.status, WQ_ERR_INDEX);
+      page = 0;
+    }
     const uint16_t *k = a.k + page * a.k_page + h * a.k_head + key % a.page_size * a.k_token;
     for (int d = lane; d < a.dk; d += 32) ks[r][d] = good ? DT::to_f(k[d]) : 0.0f;
   }
@@ -555,10 +598,6 @@ __global__ void __launch_bounds__(256) attn_weights_any_kernel(const WeightArgs 
   part[warp][lane] = sum;
   __syncthreads();
   if (warp == 0 && i < s.len) {
-    if (!page_ok(a, b, i)) {
-      set_status(a.status, WQ_ERR_INDEX);
-      return;
-    }
     sum = 0.0f;
     for (int w = 0; w < NW; ++w) sum += part[w][lane];
     float *to = weight_at(a, b, h, i);
