@@ -46,26 +46,32 @@ constexpr int NTHREADS = 320;
 constexpr int WARP_TMA = 8, WARP_MMA = 9;
 constexpr int MAX_BLOCKS = 152;    // one block an SM
 
+// Shared memory: two query tiles of as many rows as they have (a decode step's
+// have 16), and as many key tiles as fit beside them.
 template <int D>
 struct Plan {
-  static constexpr int CH = D / 64;            // 128-byte column chunks
-  static constexpr int KB = BK * D * 2;        // bytes of a key tile
-  static constexpr int QB = BR * D * 2;        // bytes of a query tile
-  static constexpr int NK = D == 128 ? 4 : 8;  // key tiles in flight
-  static constexpr int NQ = 2;                 // query tiles in flight
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = NQ * QB;
-  static constexpr int OFF_LSE = OFF_K + NK * KB;  // [2 key tiles][2][BR] float
-  static constexpr int OFF_BAR = OFF_LSE + 2 * 2 * BR * 4;
+  static constexpr int CH = D / 64;              // 128-byte column chunks
+  static constexpr int KB = BK * D * 2;          // bytes of a key tile
+  static constexpr int NK = 8;                   // key tiles in flight, at most
+  static constexpr int NQ = 2;                   // query tiles in flight
   static constexpr int B_K_FULL = 0, B_K_EMPTY = NK, B_Q_FULL = 2 * NK, B_Q_EMPTY = B_Q_FULL + NQ,
                        B_S_FULL = B_Q_EMPTY + NQ,  // [key tile][buffer]
                        B_S_EMPTY = B_S_FULL + 4, B_DONE = B_S_EMPTY + 4, NBAR = B_DONE + 1;
-  static constexpr int OFF_START = OFF_BAR + NBAR * 8;  // sequence and offset of the block's first unit, total
-  static constexpr int OFF_SCAN = OFF_START + 32;       // sums of the warps
+  static constexpr int OFF_LSE = 0;              // [2 key tiles][2][BR] float
+  static constexpr int OFF_BAR = OFF_LSE + 2 * 2 * BR * 4;
+  static constexpr int OFF_START = OFF_BAR + (NBAR + 1) / 2 * 16;  // sequence and offset of the block's first unit
+  static constexpr int OFF_SCAN = OFF_START + 16;                  // sums of the warps
   static constexpr int OFF_TMEM = OFF_SCAN + (NTHREADS / 32) * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int SMEM = OFF_ABORT + 4 + 1024;
-  static_assert(OFF_START % 8 == 0 && SMEM <= 232448, "shared memory plan");
+  static constexpr int OFF_Q = 4096;
+  static_assert(OFF_ABORT + 4 <= OFF_Q && OFF_Q % 1024 == 0, "shared memory plan");
+  static constexpr int MOST = 232448 - 1024;     // the rest aligns the tiles
+  static __host__ __device__ constexpr int query_bytes(int cols) { return cols * D * 2; }
+  static __host__ __device__ int key_tiles(int cols) {
+    const int n = (MOST - OFF_Q - NQ * query_bytes(cols)) / KB;
+    return n < NK ? n : NK;
+  }
+  static int smem(int cols) { return OFF_Q + NQ * query_bytes(cols) + key_tiles(cols) * KB + 1024; }
 };
 
 // A sequence: its tokens, keys, and the cost of its units
@@ -153,18 +159,14 @@ __device__ __forceinline__ Place locate(const WeightArgs &a, int64_t *scan, int6
   return p;
 }
 
-// Query tiles [qa, qb) of one sequence against one pair of key tiles
+// Query tiles [qa, qb) of a sequence against a pair of key tiles; with one
+// query tile in all, against `pairs` pairs one after the other
 struct Piece {
-  int b, h, k0, qa, qb;
+  int b, h, k0, pairs, qa, qb;
   Seq s;
   bool whole;  // all query tiles of the pair
   int slot;    // else: where its sums go
 };
-
-// Whether the first step of piece o takes the query tile of the last one of p
-__device__ __forceinline__ bool same_queries(const Piece &p, const Piece &o) {
-  return p.b == o.b && p.h == o.h && p.qb > p.qa && o.qa == p.qb - 1;
-}
 
 // The pieces of a block, one after the other
 struct Walk {
@@ -213,10 +215,22 @@ struct Walk {
     o.h = h;
     o.k0 = p * PAIR;
     o.s = s;
-    const int first = s.n ? s.first_tile(p, a.shift) : 0, all = s.n ? s.tiles - first : 1;
+    if (s.tiles <= 1) {  // a unit a pair
+      const int take = int(min(int64_t(s.pairs - p), left));
+      o.pairs = take;
+      o.qa = 0;
+      o.qb = s.tiles;
+      o.whole = true;
+      o.slot = 0;
+      left -= take;
+      p += take;
+      return true;
+    }
+    const int first = s.first_tile(p, a.shift), all = s.tiles - first;
     const int take = int(min(int64_t(all) - u, left));
-    o.qa = s.n ? first + int(u) : 0;
-    o.qb = s.n ? o.qa + take : 0;
+    o.pairs = 1;
+    o.qa = first + int(u);
+    o.qb = o.qa + take;
     o.whole = take == all;
     o.slot = u == 0 ? 1 : 0;
     left -= take;
@@ -274,79 +288,91 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   Walk walk;
   walk.begin(a, at, at.total * (blockIdx.x + 1) / gridDim.x - at.at);
   const int tpt = 1 << a.shift;  // tokens of a query tile
+  const uint32_t nk = uint32_t(P::key_tiles(a.cols)), qbytes = uint32_t(P::query_bytes(a.cols));
+  const uint32_t off_k = P::OFF_Q + P::NQ * qbytes;
   bool ok = true;                // this role's waits all ended in time
 
   if (warp == WARP_TMA) {
     // -------------------------------------------------------------- copies
     const bool leader = elect_one();
     uint32_t kt = 0, qt = 0;  // key and query tiles so far
+    uint32_t ks = 0, kp = 1, qs = 0, qp = 1;  // their slots and the parities of the slots' releases
     const int nbox = BK / a.box;
+    bool bad = false;  // a page id outside the cache
+    // Lane L looks up box L of a pair, one pair ahead of its copies, and starts
+    // them
+    const int mine = lane < nbox ? 0 : 1;  // its key tile
+    const uint32_t box_at = uint32_t((lane - mine * nbox) * a.box * 128);
     Piece p, nx;
-    // lane L looks up box L of a pair, one piece ahead
-    auto look = [&](const Piece &q) {
+    bool more = walk.next(a, p);
+    int pi = 0, place = 0;  // of this lane's box
+    auto begin = [&](const Piece &q) {
       const int key = q.k0 + lane * a.box;
-      if (lane >= 2 * nbox || key >= q.s.len) return 0;
-      return a.page_table[q.b * a.ld_table + key / a.page_size];
+      pi = key / a.page_size;
+      place = key - pi * a.page_size;
+      return lane < 2 * nbox && key < q.s.len ? a.page_table[q.b * a.ld_table + pi] : 0;
     };
-    bool more = walk.next(a, p), fresh = true;
-    int page = more ? look(p) : 0;
+    int page = more ? begin(p) : 0;
     while (more && ok) {
       const bool again = walk.next(a, nx);
-      const int page_next = again ? look(nx) : 0;
-      const int place = (p.k0 + lane * a.box) % a.page_size;
-      if (unsigned(page) >= unsigned(a.num_pages)) {  // read outside the tensor: zeros
-        page = int(a.num_pages);
-        set_status(a.status, WQ_ERR_INDEX);
-      }
-      if (p.qb > p.qa) {
+      const int32_t *pages = a.page_table + p.b * a.ld_table;
 #pragma unroll 1
-        for (int g = 0; g < 2 && ok; ++g) {
-          const int boxes = min(nbox, (p.s.len - p.k0 - g * BK + a.box - 1) / a.box);
+      for (int k = 0; k < p.pairs && ok; ++k) {
+        const int k0 = p.k0 + k * PAIR, y = place;
+        int w = page;
+        if (unsigned(w) >= unsigned(a.num_pages)) {  // read outside the tensor: zeros
+          w = int(a.num_pages);
+          bad = true;
+        }
+        if (k + 1 < p.pairs) {
+          pi += a.step_pages;
+          place += a.step_place;
+          if (place >= a.page_size) place -= a.page_size, ++pi;
+          page = lane < 2 * nbox && k0 + PAIR + lane * a.box < p.s.len ? pages[pi] : 0;
+        } else if (again) {
+          page = begin(nx);
+        }
+        if (p.qb == p.qa) continue;  // no token: nothing to multiply
+        const bool on = lane < 2 * nbox && k0 + lane * a.box < p.s.len;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          const int boxes = min(nbox, (p.s.len - k0 - g * BK + a.box - 1) / a.box);
           if (boxes <= 0) break;
-          const int s = kt % P::NK;
-          if (!(ok = wait_warp(bar(P::B_K_EMPTY + s), ((kt / P::NK) & 1) ^ 1, abort_flag))) break;
-          const uint32_t full = bar(P::B_K_FULL + s);
-          uint32_t dst = base + P::OFF_K + uint32_t(s * P::KB);
+          if (!(ok = wait_warp(bar(P::B_K_EMPTY) + 8 * ks, kp, abort_flag))) break;
+          const uint32_t full = bar(P::B_K_FULL) + 8 * ks, dst = base + off_k + ks * P::KB + box_at;
           if (leader) mbar_expect_tx(full, uint32_t(boxes * a.box * P::CH * 128));
-#pragma unroll 1
-          for (int b = 0; b < boxes; ++b) {
-            const int by = __shfl_sync(0xffffffffu, place, g * nbox + b);
-            const int bw = __shfl_sync(0xffffffffu, page, g * nbox + b);
-            if (leader) {
+          __syncwarp();
+          if (on && mine == g) {
 #pragma unroll
-              for (int ch = 0; ch < P::CH; ++ch) tma_load_4d(dst + ch * BK * 128, &tmK, ch * 64, by, p.h, bw, full);
-            }
-            dst += uint32_t(a.box * 128);
+            for (int ch = 0; ch < P::CH; ++ch) tma_load_4d(dst + ch * BK * 128, &tmK, ch * 64, y, p.h, w, full);
           }
+          if (++ks == nk) ks = 0, kp ^= 1;
           ++kt;
         }
+        if (k > 0) continue;  // the query tile is there
 #pragma unroll 1
         for (int q = p.qa; q < p.qb && ok; ++q) {
-          if (!fresh) {  // the tile is there
-            fresh = true;
-            continue;
-          }
-          const int s = qt % P::NQ;
-          if (!(ok = wait_warp(bar(P::B_Q_EMPTY + s), ((qt / P::NQ) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = wait_warp(bar(P::B_Q_EMPTY) + 8 * qs, qp, abort_flag))) break;
           if (leader) {
-            mbar_expect_tx(bar(P::B_Q_FULL + s), uint32_t(P::CH * tpt * a.G * 128));
+            const uint32_t full = bar(P::B_Q_FULL) + 8 * qs;
+            mbar_expect_tx(full, uint32_t(P::CH * tpt * a.G * 128));
 #pragma unroll
             for (int ch = 0; ch < P::CH; ++ch)
-              tma_load_3d(base + P::OFF_Q + s * P::QB + ch * BR * 128, &tmQ, ch * 64, p.h * a.G,
-                          p.s.t0 + q * tpt, bar(P::B_Q_FULL + s));
+              tma_load_3d(base + P::OFF_Q + qs * qbytes + ch * a.cols * 128, &tmQ, ch * 64, p.h * a.G,
+                          p.s.t0 + q * tpt, full);
           }
+          if (++qs == P::NQ) qs = 0, qp ^= 1;
           ++qt;
         }
-        fresh = !(again && same_queries(p, nx));
       }
       p = nx;
-      page = page_next;
       more = again;
     }
+    if (bad) set_status(a.status, WQ_ERR_INDEX);
     if (!ok) {  // let copies already in flight land before the block goes away
       *abort_flag = 1;
-      for (uint32_t i = kt > P::NK ? kt - P::NK : 0; i < kt; ++i)
-        mbar_wait_bounded(bar(P::B_K_FULL + i % P::NK), (i / P::NK) & 1);
+      for (uint32_t i = kt > nk ? kt - nk : 0; i < kt; ++i)
+        mbar_wait_bounded(bar(P::B_K_FULL + int(i % nk)), (i / nk) & 1);
       for (uint32_t i = qt > P::NQ ? qt - P::NQ : 0; i < qt; ++i)
         mbar_wait_bounded(bar(P::B_Q_FULL + i % P::NQ), (i / P::NQ) & 1);
     }
@@ -355,71 +381,68 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const bool leader = elect_one();
     const uint32_t idesc = idesc_f16(BK, a.cols) | kTypes<DT>;
     const int steps = (a.dk + 15) / 16;
-    uint32_t kt = 0, qt = 0, st[2] = {0, 0};
-    auto wait = [&](int b, uint32_t parity) {
-      if (ok) ok = wait_warp(bar(b), parity, abort_flag);
+    uint32_t ks = 0, kp = 0, qs = 0, qp = 0, st[2] = {0, 0};
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      if (ok) ok = wait_warp(b, parity, abort_flag);
     };
-    Piece p, nx;
-    bool more = walk.next(a, p), fresh = true;
-    while (ok && more) {
-      const bool again = walk.next(a, nx);
-      const int tiles = p.k0 + BK < p.s.len ? 2 : 1;
-      if (p.qb > p.qa) {
-        const bool keep = again && same_queries(p, nx);  // the last query tile stays for the next piece
-        for (int g = 0; g < tiles; ++g) wait(P::B_K_FULL + int((kt + g) % P::NK), ((kt + g) / P::NK) & 1);
+    Piece p;
+    while (ok && walk.next(a, p)) {
+      if (p.qb == p.qa) continue;
+#pragma unroll 1
+      for (int k = 0; k < p.pairs && ok; ++k) {
+        const int tiles = p.k0 + k * PAIR + BK < p.s.len ? 2 : 1;
+        const uint32_t k1 = ks + 1 == nk ? 0 : ks + 1, kp1 = kp ^ uint32_t(k1 == 0);
 #pragma unroll 1
         for (int q = p.qa; q < p.qb; ++q) {
-          const int sq = qt % P::NQ;
-          if (fresh) wait(P::B_Q_FULL + sq, (qt / P::NQ) & 1);
+          if (k == 0) wait(bar(P::B_Q_FULL) + 8 * qs, qp);
+          const uint64_t dq = sdesc(base + P::OFF_Q + qs * qbytes), dq1 = dq + uint64_t(a.cols * 128 >> 4);
           const bool last = q + 1 == p.qb;
-          fresh = !(last && keep);
-          const uint64_t dq = sdesc(base + P::OFF_Q + sq * P::QB);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (g >= tiles) break;
-            const uint32_t buf = st[g] & 1;
-            wait(P::B_S_EMPTY + 2 * g + int(buf), ((st[g] >> 1) & 1) ^ 1);
+            const uint32_t buf = st[g] & 1, kg = g ? k1 : ks;
+            if (q == p.qa) wait(bar(P::B_K_FULL) + 8 * kg, g ? kp1 : kp);
+            wait(bar(P::B_S_EMPTY + 2 * g) + 8 * buf, ((st[g] >> 1) & 1) ^ 1);
             tc_fence_after();
             if (leader && ok) {
-              const uint64_t dk = sdesc(base + P::OFF_K + ((kt + g) % P::NK) * P::KB);
+              const uint64_t dk = sdesc(base + off_k + kg * P::KB);
+              const uint32_t to = tmem + g * 256 + buf * 128;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 if (i >= steps) break;
-                const uint32_t off = ((i / 4) * (BK * 128) + (i % 4) * 32) >> 4;
-                mma_f16(tmem + g * 256 + buf * 128, dk + off, dq + off, idesc, i ? 1u : 0u);
+                mma_f16(to, dk + (((i / 4) * (BK * 128) + (i % 4) * 32) >> 4), (i < 4 ? dq : dq1) + ((i % 4) * 32 >> 4),
+                        idesc, i ? 1u : 0u);
               }
-              if (last) mma_commit(bar(P::B_K_EMPTY + (kt + g) % P::NK));
-              if (fresh && g + 1 == tiles) mma_commit(bar(P::B_Q_EMPTY + sq));
-              mma_commit(bar(P::B_S_FULL + 2 * g + buf));
+              if (last) mma_commit(bar(P::B_K_EMPTY) + 8 * kg);
+              if (k + 1 == p.pairs && g + 1 == tiles) mma_commit(bar(P::B_Q_EMPTY) + 8 * qs);
+              mma_commit(bar(P::B_S_FULL + 2 * g) + 8 * buf);
             }
             ++st[g];
           }
-          if (fresh) ++qt;
+          if (k + 1 == p.pairs && ++qs == P::NQ) qs = 0, qp ^= 1;
         }
-        kt += uint32_t(tiles);
+        for (int g = 0; g < tiles; ++g)
+          if (++ks == nk) ks = 0, kp ^= 1;
       }
-      p = nx;
-      more = again;
     }
     if (!ok) *abort_flag = 1;
     if (leader) mma_commit(bar(P::B_DONE));
     mbar_wait_bounded(bar(P::B_DONE), 0);
   } else {
     // -------------------------------------------------------------- weights
-    const int g = warp >> 2, tid = threadIdx.x & 127;
+    const int g = warp >> 2, tid = threadIdx.x & 127, col = g * BK + tid;
     const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + g * 256;
     float *ls = reinterpret_cast<float *>(sm + P::OFF_LSE) + g * 2 * BR;
     const int tok = tid / a.G, hd = tid - tok * a.G;  // the column whose lse this thread brings
     const float c = a.scale_log2;
-    uint32_t st = 0;
+    uint32_t st = 0, nq = 0;  // score tiles, and query tiles' log-sum-exps so far
     auto lse_of = [&](const Piece &q, int tile) {
       const int j = tile * tpt + tok;
       return tok < tpt && j < q.s.n ? a.lse[int64_t(q.s.t0 + j) * a.Hq + q.h * a.G + hd] : INFINITY;
     };
     // what a key had before
-    auto look = [&](const Piece &q) {
-      const int i = q.k0 + g * BK + tid;
-      return q.whole && i < q.s.old ? *weight_at(a, q.b, q.h, i) : 0.0f;
+    auto look = [&](const Piece &q, int k0) {
+      return q.whole && k0 + col < q.s.old ? *weight_at(a, q.b, q.h, k0 + col) : 0.0f;
     };
     // columns e0 .. of a score tile, NC of them in v
     float s0 = 0.0f, s1 = 0.0f;
@@ -448,73 +471,67 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     };
     Piece p, nx;
-    float old = 0.0f, l = 0.0f;
-    uint32_t nq = 0;  // log-sum-exps staged so far
-    bool more = walk.next(a, p), fresh = true;
-    if (more) {
-      old = look(p);
-      l = lse_of(p, p.qa);
-    }
+    bool more = walk.next(a, p);
+    float old = more ? look(p, p.k0) : 0.0f, l = more ? lse_of(p, p.qa) : 0.0f;
     while (more && ok) {
       const bool again = walk.next(a, nx);
-      const float old_next = again ? look(nx) : 0.0f;
-      const int i = p.k0 + g * BK + tid;
-      const bool tile = p.k0 + g * BK < p.s.len;
-      float sum = 0.0f;
+      float *to = weight_at(a, p.b, p.h, p.k0 + col);
 #pragma unroll 1
-      for (int q = p.qa; q < p.qb; ++q) {
-        const bool now = fresh;
-        const float mine = l;
-        fresh = q + 1 < p.qb || !(again && same_queries(p, nx));
-        if (q + 1 < p.qb) l = lse_of(p, q + 1);
-        else if (again && fresh) l = lse_of(nx, nx.qa);
-        if (!tile) continue;
-        if (now) {
-          ls[(++nq & 1) * BR + tid] = neg_lse2(mine);
-          named_sync(1 + g, 128);  // two tiles on, all have read what was here
-        }
-        const float *lb = ls + (nq & 1) * BR;
-        const uint32_t buf = st & 1, at = ts + buf * 128;
-        if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g + int(buf)), (st >> 1) & 1, abort_flag))) break;
-        tc_fence_after();
-        const int cols = min(tpt, p.s.n - q * tpt) * a.G;
-        // the first column whose token sees this key
-        const int c0 = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
-        s0 = s1 = 0.0f;
-        if (cols <= 8) {
-          uint32_t v[8];
-          tmem_ld8(at, v);
-          tmem_wait_ld(v);
-          weigh(v, lb, 0, c0, cols);
-        } else {
-          // the next 32 columns come while these are weighed
-          uint32_t v[2][32];
-          tmem_ld32(at, v[0]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (32 * k >= cols) break;
-            wait_ld32(v[k & 1]);
-            if (32 * (k + 1) < cols) tmem_ld32(at + 32 * (k + 1), v[(k + 1) & 1]);
-            weigh(v[k & 1], lb, 32 * k, c0, cols);
+      for (int k = 0; k < p.pairs && ok; ++k) {
+        const int k0 = p.k0 + k * PAIR, i = k0 + col;
+        const float was = old;
+        if (k + 1 < p.pairs) old = look(p, k0 + PAIR);
+        else if (again) old = look(nx, nx.k0);
+        const bool tile = k0 + g * BK < p.s.len;
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int q = p.qa; q < p.qb; ++q) {
+          if (k == 0) {  // the rows' log-sum-exps, the next tile's ahead
+            ls[(++nq & 1) * BR + tid] = neg_lse2(l);
+            if (q + 1 < p.qb) l = lse_of(p, q + 1);
+            else if (again) l = lse_of(nx, nx.qa);
+            named_sync(1 + g, 128);  // two tiles on, all have read what was here
           }
+          if (!tile) continue;
+          const float *lb = ls + (nq & 1) * BR;
+          const uint32_t buf = st & 1, at = ts + buf * 128;
+          if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g) + 8 * buf, (st >> 1) & 1, abort_flag))) break;
+          tc_fence_after();
+          const int cols = min(tpt, p.s.n - q * tpt) * a.G;
+          // the first column whose token sees this key
+          const int c0 = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
+          s0 = s1 = 0.0f;
+          if (cols <= 8) {
+            uint32_t v[8];
+            tmem_ld8(at, v);
+            tmem_wait_ld(v);
+            weigh(v, lb, 0, c0, cols);
+          } else {
+            // the next 32 columns come while these are weighed
+            uint32_t v[2][32];
+            tmem_ld32(at, v[0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (32 * e >= cols) break;
+              wait_ld32(v[e & 1]);
+              if (32 * (e + 1) < cols) tmem_ld32(at + 32 * (e + 1), v[(e + 1) & 1]);
+              weigh(v[e & 1], lb, 32 * e, c0, cols);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(P::B_S_EMPTY + 2 * g) + 8 * buf);
+          ++st;
+          sum += s0 + s1;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(P::B_S_EMPTY + 2 * g + int(buf)));
-        ++st;
-        sum += s0 + s1;
+        if (!ok) break;
+        if (i < p.s.len) {
+          if (!p.whole) a.part[(int64_t(blockIdx.x) * 2 + p.slot) * PAIR + col] = sum;
+          else to[k * PAIR] = __fmaf_rn(a.decay, was, sum);
+        }
       }
-      if (!ok) break;
-      if (p.qa == p.qb) {  // a sequence with no token here
-        fresh = true;
-        if (again) l = lse_of(nx, nx.qa);
-      }
-      if (i < p.s.len) {
-        if (!p.whole) a.part[(int64_t(blockIdx.x) * 2 + p.slot) * PAIR + g * BK + tid] = sum;
-        else *weight_at(a, p.b, p.h, i) = __fmaf_rn(a.decay, old, sum);
-      }
+      if (p.qa == p.qb && again) l = lse_of(nx, nx.qa);  // no token here
       p = nx;
-      old = old_next;
       more = again;
     }
   }
@@ -611,7 +628,7 @@ template <class DT, int D>
 int launch_tiles(const WeightArgs &a, cudaStream_t st) {
   auto *k = attn_weights_kernel<DT, D>;
   static OncePerDevice sized;
-  if (!allow_smem(sized, k, Plan<D>::SMEM)) return WQ_ERR_LAUNCH;
+  if (!allow_smem(sized, k, Plan<D>::MOST + 1024)) return WQ_ERR_LAUNCH;
   CUtensorMap mq, mk;
   auto pitch = [](int64_t extent, int64_t stride) { return extent == 1 && stride == 0 ? 8 : stride; };
   const int64_t qd[3] = {a.dk, a.Hq, a.T};
@@ -622,7 +639,7 @@ int launch_tiles(const WeightArgs &a, cudaStream_t st) {
   const int64_t ks[3] = {pitch(a.page_size, a.k_token), pitch(a.heads, a.k_head), pitch(a.num_pages, a.k_page)};
   if (!make_tma_nd_b16_sw128(&mq, a.q, 3, qd, qs, qb) || !make_tma_nd_b16_sw128(&mk, a.k, 4, kd, ks, box))
     return WQ_ERR_UNSUPPORTED;
-  k<<<unsigned(a.blocks), NTHREADS, Plan<D>::SMEM, st>>>(mq, mk, a);
+  k<<<unsigned(a.blocks), NTHREADS, Plan<D>::smem(a.cols), st>>>(mq, mk, a);
   int rc = launched(1);
   if (rc == WQ_OK && a.part && a.blocks > 1)
     rc = attn::launch_chained(attn_weights_join_kernel, unsigned(a.blocks - 1), NTHREADS, 0, true, st, a);
@@ -647,6 +664,8 @@ void plan_weights(WeightArgs &a) {
   while ((2 << a.shift) * a.G <= BR && (1 << a.shift) < a.max_q) ++a.shift;
   a.cols = (((1 << a.shift) * a.G) + 15) / 16 * 16;
   a.box = gcd(a.page_size, BK);
+  a.step_pages = PAIR / a.page_size;
+  a.step_place = PAIR % a.page_size;
   const bool pitches = (a.k_token || a.page_size == 1) && (a.k_head || a.heads == 1) &&
                        (a.k_page || a.num_pages <= 1);
   // TMA boxes of 8 keys or more, a lane for each box of a pair; pitches other

@@ -240,6 +240,7 @@ struct WeightArgs {
   int shift;    // log2 of the tokens of a query tile
   int cols;     // its rows, in whole 16s
   int box;      // cache rows of one TMA box
+  int step_pages, step_place;  // a pair of key tiles on: pages, and places beyond them
   int blocks;   // that share the line of units
   bool tiles;   // the tensor-memory kernel takes it
   bool split;   // a pair of key tiles may be cut between blocks
