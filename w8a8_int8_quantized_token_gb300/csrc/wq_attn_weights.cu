@@ -12,7 +12,9 @@
 // every query tile that is loaded.
 //   warps 0-3, 4-7  weights of key tile 0, 1 of a pair: a thread owns a key
 //   warp 8          TMA: key tiles page by page, query tiles
-//   warp 9          MMA issue; owns the tensor memory
+//   warps 9, 10     MMA issue for key tile 0, 1: a thread each, whose waits (over
+//                   100 cycles, even for nothing) then pass in the other's
+//                   products; warp 9 owns the tensor memory
 // Tensor memory: two score buffers of 128 columns for each key tile.
 //
 // A unit is a (sequence, key head, pair of key tiles, query tile); those in
@@ -42,21 +44,23 @@ using attn::wait_last_kernel;
 
 constexpr int BK = 128, BR = 128;  // keys, query rows of a tile
 constexpr int PAIR = 2 * BK;       // keys of a pair of tiles
-constexpr int NTHREADS = 320;
-constexpr int WARP_TMA = 8, WARP_MMA = 9;
+constexpr int NTHREADS = 352;
+constexpr int WARP_TMA = 8, WARP_MMA = 9;  // MMA: two warps
 constexpr int MAX_BLOCKS = 152;    // one block an SM
 
-// Shared memory: two query tiles of as many rows as they have (a decode step's
-// have 16), and as many key tiles as fit beside them.
+// Shared memory: a sequence of one query tile takes two of as many rows as they
+// have (a decode step's have 16), and as many key tiles as fit beside them; one
+// of many takes the keys of one pair and as many query tiles as fit, since they
+// come one a step and from L2 (two of them: 1.42 us a step without a
+// single exponential).
 template <int D>
 struct Plan {
   static constexpr int CH = D / 64;              // 128-byte column chunks
   static constexpr int KB = BK * D * 2;          // bytes of a key tile
-  static constexpr int NK = 8;                   // key tiles in flight, at most
-  static constexpr int NQ = 2;                   // query tiles in flight
+  static constexpr int NK = 8, NQ = 8;           // key and query tiles in flight, at most
   static constexpr int B_K_FULL = 0, B_K_EMPTY = NK, B_Q_FULL = 2 * NK, B_Q_EMPTY = B_Q_FULL + NQ,
                        B_S_FULL = B_Q_EMPTY + NQ,  // [key tile][buffer]
-                       B_S_EMPTY = B_S_FULL + 4, B_DONE = B_S_EMPTY + 4, NBAR = B_DONE + 1;
+                       B_S_EMPTY = B_S_FULL + 4, B_DONE = B_S_EMPTY + 4, NBAR = B_DONE + 2;
   static constexpr int OFF_LSE = 0;              // [2 key tiles][2][BR] float
   static constexpr int OFF_BAR = OFF_LSE + 2 * 2 * BR * 4;
   static constexpr int OFF_START = OFF_BAR + (NBAR + 1) / 2 * 16;  // sequence and offset of the block's first unit
@@ -67,11 +71,17 @@ struct Plan {
   static_assert(OFF_ABORT + 4 <= OFF_Q && OFF_Q % 1024 == 0, "shared memory plan");
   static constexpr int MOST = 232448 - 1024;     // the rest aligns the tiles
   static __host__ __device__ constexpr int query_bytes(int cols) { return cols * D * 2; }
-  static __host__ __device__ int key_tiles(int cols) {
-    const int n = (MOST - OFF_Q - NQ * query_bytes(cols)) / KB;
+  static __host__ __device__ int query_tiles(int cols, bool many) {
+    const int n = (MOST - OFF_Q - 2 * KB) / query_bytes(cols);
+    return many ? (n < NQ ? n : NQ) : 2;
+  }
+  static __host__ __device__ int key_tiles(int cols, bool many) {
+    const int n = (MOST - OFF_Q - query_tiles(cols, many) * query_bytes(cols)) / KB;
     return n < NK ? n : NK;
   }
-  static int smem(int cols) { return OFF_Q + NQ * query_bytes(cols) + key_tiles(cols) * KB + 1024; }
+  static int smem(int cols, bool many) {
+    return OFF_Q + query_tiles(cols, many) * query_bytes(cols) + key_tiles(cols, many) * KB + 1024;
+  }
 };
 
 // A sequence: its tokens, keys, and the cost of its units
@@ -275,7 +285,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     prefetch_map(&tmQ);
     prefetch_map(&tmK);
     *abort_flag = 0;
-    for (int i = 0; i < P::NBAR; ++i) mbar_init(bar(i), i >= P::B_S_EMPTY && i < P::B_DONE ? 4 : 1);
+    for (int i = 0; i < P::NBAR; ++i) mbar_init(bar(i), i >= P::B_S_EMPTY && i < P::B_DONE   ? 4   // warps of a key tile
+                        : (i >= P::B_K_EMPTY && i < P::B_Q_FULL) || (i >= P::B_Q_EMPTY && i < P::B_S_FULL) ? 2  // MMA warps
+                                                               : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WARP_MMA) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -288,8 +300,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   Walk walk;
   walk.begin(a, at, at.total * (blockIdx.x + 1) / gridDim.x - at.at);
   const int tpt = 1 << a.shift;  // tokens of a query tile
-  const uint32_t nk = uint32_t(P::key_tiles(a.cols)), qbytes = uint32_t(P::query_bytes(a.cols));
-  const uint32_t off_k = P::OFF_Q + P::NQ * qbytes;
+  const uint32_t nk = uint32_t(P::key_tiles(a.cols, a.split)), nq = uint32_t(P::query_tiles(a.cols, a.split));
+  const uint32_t qbytes = uint32_t(P::query_bytes(a.cols)), off_k = P::OFF_Q + nq * qbytes;
   bool ok = true;                // this role's waits all ended in time
 
   if (warp == WARP_TMA) {
@@ -361,7 +373,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               tma_load_3d(base + P::OFF_Q + qs * qbytes + ch * a.cols * 128, &tmQ, ch * 64, p.h * a.G,
                           p.s.t0 + q * tpt, full);
           }
-          if (++qs == P::NQ) qs = 0, qp ^= 1;
+          if (++qs == nq) qs = 0, qp ^= 1;
           ++qt;
         }
       }
@@ -373,61 +385,74 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       *abort_flag = 1;
       for (uint32_t i = kt > nk ? kt - nk : 0; i < kt; ++i)
         mbar_wait_bounded(bar(P::B_K_FULL + int(i % nk)), (i / nk) & 1);
-      for (uint32_t i = qt > P::NQ ? qt - P::NQ : 0; i < qt; ++i)
-        mbar_wait_bounded(bar(P::B_Q_FULL + i % P::NQ), (i / P::NQ) & 1);
+      for (uint32_t i = qt > nq ? qt - nq : 0; i < qt; ++i)
+        mbar_wait_bounded(bar(P::B_Q_FULL + int(i % nq)), (i / nq) & 1);
     }
-  } else if (warp == WARP_MMA) {
+  } else if (warp >= WARP_MMA) {
     // -------------------------------------------------------------- products
-    const bool leader = elect_one();
-    const uint32_t idesc = idesc_f16(BK, a.cols) | kTypes<DT>;
-    const int steps = (a.dk + 15) / 16;
-    uint32_t ks = 0, kp = 0, qs = 0, qp = 0, st[2] = {0, 0};
-    auto wait = [&](uint32_t b, uint32_t parity) {
-      if (ok) ok = wait_warp(b, parity, abort_flag);
-    };
-    Piece p;
-    while (ok && walk.next(a, p)) {
-      if (p.qb == p.qa) continue;
+    const int g = warp - WARP_MMA;  // key tile
+    if (elect_one()) {
+      const uint32_t idesc = idesc_f16(BK, a.cols) | kTypes<DT>;
+      const int steps = (a.dk + 15) / 16;
+      const uint64_t dq0 = sdesc(base + P::OFF_Q), dk0 = sdesc(base + off_k);
+      const uint32_t dq1 = uint32_t(a.cols * 128) >> 4;  // to a query tile's next 64 columns
+      uint32_t ks = 0, kp = 0, qs = 0, qp = 0, st = 0;
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        if (ok) ok = wait_one(b, parity, abort_flag);
+      };
+      Piece p;
+      while (ok && walk.next(a, p)) {
+        if (p.qb == p.qa) continue;
 #pragma unroll 1
-      for (int k = 0; k < p.pairs && ok; ++k) {
-        const int tiles = p.k0 + k * PAIR + BK < p.s.len ? 2 : 1;
-        const uint32_t k1 = ks + 1 == nk ? 0 : ks + 1, kp1 = kp ^ uint32_t(k1 == 0);
+        for (int k = 0; k < p.pairs && ok; ++k) {
+          const bool two = p.k0 + k * PAIR + BK < p.s.len, tile = g == 0 || two;
+          // Both warps wait for both key tiles and for every query tile, and
+          // both release them, with work for them or without: a wait by parity
+          // cannot tell a phase from the one two before it, so none may be
+          // passed over, and no slot may be filled again before both have seen it.
+          const uint32_t k1 = ks + 1 == nk ? 0 : ks + 1, kp1 = k1 == 0 ? kp ^ 1 : kp;
+          wait(bar(P::B_K_FULL) + 8 * ks, kp);
+          if (two) wait(bar(P::B_K_FULL) + 8 * k1, kp1);
+          const uint32_t kg = g ? k1 : ks, other = g ? ks : k1;
+          if (ok && (g || two)) mbar_arrive(bar(P::B_K_EMPTY) + 8 * other);
+          const uint64_t dk = dk0 + kg * uint32_t(P::KB >> 4);
 #pragma unroll 1
-        for (int q = p.qa; q < p.qb; ++q) {
-          if (k == 0) wait(bar(P::B_Q_FULL) + 8 * qs, qp);
-          const uint64_t dq = sdesc(base + P::OFF_Q + qs * qbytes), dq1 = dq + uint64_t(a.cols * 128 >> 4);
-          const bool last = q + 1 == p.qb;
+          for (int q = p.qa; q < p.qb; ++q) {
+            const bool done = k + 1 == p.pairs;  // with the query tile
+            if (k == 0) wait(bar(P::B_Q_FULL) + 8 * qs, qp);
+            if (tile) {
+              const uint32_t buf = st & 1;
+              wait(bar(P::B_S_EMPTY + 2 * g) + 8 * buf, ((st >> 1) & 1) ^ 1);
+              tc_fence_after();
+              if (ok) {
+                const uint64_t dq = dq0 + qs * (qbytes >> 4);
+                const uint32_t to = tmem + g * 256 + buf * 128;
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (g >= tiles) break;
-            const uint32_t buf = st[g] & 1, kg = g ? k1 : ks;
-            if (q == p.qa) wait(bar(P::B_K_FULL) + 8 * kg, g ? kp1 : kp);
-            wait(bar(P::B_S_EMPTY + 2 * g) + 8 * buf, ((st[g] >> 1) & 1) ^ 1);
-            tc_fence_after();
-            if (leader && ok) {
-              const uint64_t dk = sdesc(base + off_k + kg * P::KB);
-              const uint32_t to = tmem + g * 256 + buf * 128;
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                if (i >= steps) break;
-                mma_f16(to, dk + (((i / 4) * (BK * 128) + (i % 4) * 32) >> 4), (i < 4 ? dq : dq1) + ((i % 4) * 32 >> 4),
-                        idesc, i ? 1u : 0u);
+                for (int i = 0; i < D / 16; ++i) {
+                  if (i >= steps) break;
+                  mma_f16(to, dk + (((i / 4) * (BK * 128) + (i % 4) * 32) >> 4),
+                          dq + (i / 4) * dq1 + ((i % 4) * 32 >> 4), idesc, i ? 1u : 0u);
+                }
+                if (q + 1 == p.qb) mma_commit(bar(P::B_K_EMPTY) + 8 * kg);
+                if (done) mma_commit(bar(P::B_Q_EMPTY) + 8 * qs);
+                mma_commit(bar(P::B_S_FULL + 2 * g) + 8 * buf);
               }
-              if (last) mma_commit(bar(P::B_K_EMPTY) + 8 * kg);
-              if (k + 1 == p.pairs && g + 1 == tiles) mma_commit(bar(P::B_Q_EMPTY) + 8 * qs);
-              mma_commit(bar(P::B_S_FULL + 2 * g) + 8 * buf);
+              ++st;
+            } else if (done && ok) {
+              mma_commit(bar(P::B_Q_EMPTY) + 8 * qs);  // products of the pairs before may still read it
             }
-            ++st[g];
+            if (done && ++qs == nq) qs = 0, qp ^= 1;
           }
-          if (k + 1 == p.pairs && ++qs == P::NQ) qs = 0, qp ^= 1;
-        }
-        for (int g = 0; g < tiles; ++g)
+          ks = two ? k1 : ks;
+          kp = two ? kp1 : kp;
           if (++ks == nk) ks = 0, kp ^= 1;
+        }
       }
+      if (!ok) *abort_flag = 1;
+      mma_commit(bar(P::B_DONE + g));
+      mbar_wait_bounded(bar(P::B_DONE + g), 0);
     }
-    if (!ok) *abort_flag = 1;
-    if (leader) mma_commit(bar(P::B_DONE));
-    mbar_wait_bounded(bar(P::B_DONE), 0);
+    __syncwarp();
   } else {
     // -------------------------------------------------------------- weights
     const int g = warp >> 2, tid = threadIdx.x & 127, col = g * BK + tid;
@@ -435,7 +460,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     float *ls = reinterpret_cast<float *>(sm + P::OFF_LSE) + g * 2 * BR;
     const int tok = tid / a.G, hd = tid - tok * a.G;  // the column whose lse this thread brings
     const float c = a.scale_log2;
-    uint32_t st = 0, nq = 0;  // score tiles, and query tiles' log-sum-exps so far
+    uint32_t st = 0, ql = 0;  // score tiles, and query tiles' log-sum-exps so far
     auto lse_of = [&](const Piece &q, int tile) {
       const int j = tile * tpt + tok;
       return tok < tpt && j < q.s.n ? a.lse[int64_t(q.s.t0 + j) * a.Hq + q.h * a.G + hd] : INFINITY;
@@ -487,13 +512,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
         for (int q = p.qa; q < p.qb; ++q) {
           if (k == 0) {  // the rows' log-sum-exps, the next tile's ahead
-            ls[(++nq & 1) * BR + tid] = neg_lse2(l);
+            ls[(++ql & 1) * BR + tid] = neg_lse2(l);
             if (q + 1 < p.qb) l = lse_of(p, q + 1);
             else if (again) l = lse_of(nx, nx.qa);
             named_sync(1 + g, 128);  // two tiles on, all have read what was here
           }
           if (!tile) continue;
-          const float *lb = ls + (nq & 1) * BR;
+          const float *lb = ls + (ql & 1) * BR;
           const uint32_t buf = st & 1, at = ts + buf * 128;
           if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g) + 8 * buf, (st >> 1) & 1, abort_flag))) break;
           tc_fence_after();
@@ -539,7 +564,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     *abort_flag = 1;
     set_status(a.status, WQ_ERR_TIMEOUT);
   }
-  __syncthreads();
+  __syncthreads();  // the products are over
   if (warp == WARP_MMA) tmem_dealloc(tmem, 512);
 }
 
@@ -639,7 +664,7 @@ int launch_tiles(const WeightArgs &a, cudaStream_t st) {
   const int64_t ks[3] = {pitch(a.page_size, a.k_token), pitch(a.heads, a.k_head), pitch(a.num_pages, a.k_page)};
   if (!make_tma_nd_b16_sw128(&mq, a.q, 3, qd, qs, qb) || !make_tma_nd_b16_sw128(&mk, a.k, 4, kd, ks, box))
     return WQ_ERR_UNSUPPORTED;
-  k<<<unsigned(a.blocks), NTHREADS, Plan<D>::smem(a.cols), st>>>(mq, mk, a);
+  k<<<unsigned(a.blocks), NTHREADS, Plan<D>::smem(a.cols, a.split), st>>>(mq, mk, a);
   int rc = launched(1);
   if (rc == WQ_OK && a.part && a.blocks > 1)
     rc = attn::launch_chained(attn_weights_join_kernel, unsigned(a.blocks - 1), NTHREADS, 0, true, st, a);
