@@ -189,7 +189,8 @@ def attention_weights(q, k_cache, page_table, key_len, cu_q, lse, weights, scale
     the log-sum-exp (itself times log2(e)) round at most four times, each E times
     |score| + |lse|; the exponential is off by 2^-22 and its argument's base
     change by as much.  Rows are added in chains of at most 64 within a tile (any
-    page size: all rows over 8 warps), tile by tile and part by part."""
+    page size: all rows over 8 warps), tile by tile and part by part.  A weight
+    below float32's normal range, 2^-126, may count as zero."""
     pt, kl, cu = page_table.cpu().long(), key_len.cpu().tolist(), cu_q.cpu().tolist()
     B, Hkv = weights.shape[:2]
     G = q.shape[1] // Hkv
@@ -215,7 +216,7 @@ def attention_weights(q, k_cache, page_table, key_len, cu_q, lse, weights, scale
             chain = 64 + n * G / 8 + 2 * 152
             add = p.sum((0, 1))
             w[b, h, :m] += add
-            tol[b, h, :m] += (p * e * 1.01).sum((0, 1)) + chain * E * add + E * w[b, h, :m].abs() + TINY[torch.float32]
+            tol[b, h, :m] += (p * e * 1.01).sum((0, 1)) + chain * E * add + E * w[b, h, :m].abs() + n * G * 2.0 ** -126
     return w, tol
 
 

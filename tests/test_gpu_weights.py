@@ -95,6 +95,36 @@ def test_even_tokens_without_cu_q(B, q, L):
     assert torch.equal(a["weights"].nan_to_num(), b["weights"].nan_to_num())
 
 
+@pytest.mark.parametrize("lse", [-80.0, -60.0, 60.0, 95.0, math.inf])
+@pytest.mark.parametrize("ql,kl,G", [([1, 1], [200, 31], 4), ([200, 31], [300, 40], 4), ([90], [90], 5)])
+def test_weights_far_from_one(lse, ql, kl, G):
+    """Log-sum-exps that are not the scores' own: weights up to 2^120 and down
+    to nothing, in some rows only."""
+    a = problem(ql, kl, 2, G, 64, 16, BF)
+    a["lse"][::3] = lse
+    a["lse"][1::7] = lse / 2
+    check(a)
+
+
+@pytest.mark.parametrize("ql,kl", [([1, 1], [200, 31]), ([200, 31], [300, 40])])
+def test_nonfinite_queries_and_sums_reach_the_keys_they_see(ql, kl):
+    a = problem(ql, kl, 2, 4, 64, 16, BF)
+    a["weights"] = a["weights"].nan_to_num()
+    b = {**a, "q": a["q"].clone(), "lse": a["lse"].clone(), "weights": a["weights"].clone()}
+    wq.attention_weights_paged(**a)
+    row = ql[0] - 1  # the last token of the first sequence sees all its keys
+    for name, value in (("q", math.nan), ("lse", math.nan), ("q", math.inf)):
+        c = {k: v.clone() if k in ("q", "lse", "weights") else v for k, v in b.items()}
+        c[name][row, 5] = value  # a query head of key head 1
+        wq.attention_weights_paged(**c)
+        n = kl[0]
+        assert not c["weights"][0, 1, :n].isfinite().all() and (name == "q" and value == math.inf or
+                                                                c["weights"][0, 1, :n].isnan().all())
+        c["weights"][0, 1, :n], mine = 0, a["weights"].clone()
+        mine[0, 1, :n] = 0
+        assert torch.equal(c["weights"], mine)
+
+
 def test_weights_in_other_strides_and_repeated_calls():
     a = problem([2, 7], [100, 300], 3, 2, 64, 16, BF)
     b = problem([2, 7], [100, 300], 3, 2, 64, 16, BF)

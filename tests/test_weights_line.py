@@ -9,22 +9,24 @@ PAIR = 256
 
 
 class Seq:
-    def __init__(self, n, length, shift):
-        self.n, self.len, self.shift = n, length, shift
+    def __init__(self, n, length, tpt):
+        self.n, self.len, self.tpt = n, length, tpt
+        self.shift = tpt.bit_length() - 1
         self.old = length - n
         self.pairs = -(-length // PAIR)
-        self.tiles = -(-n // (1 << shift))
+        self.tiles = -(-n // tpt)
+        self.costs = -(-n // (1 << self.shift))
         self.p1 = 0 if self.old <= 0 else -(-self.old // PAIR)
         self.d1 = self.p1 * PAIR - self.old
 
-    def first_tile(self, p):
-        return max(0, (p * PAIR - self.old) >> self.shift)
+    def cost(self, p):
+        return 1 if self.tiles <= 1 else self.costs - max(0, (p * PAIR - self.old) >> self.shift)
 
     def before(self, p):
-        if self.n == 0:
+        if self.tiles <= 1:
             return p
         m = max(0, p - self.p1)
-        return p * self.tiles - (m * (self.d1 >> self.shift) + (PAIR >> self.shift) * (m * (m - 1) // 2))
+        return p * self.costs - (m * (self.d1 >> self.shift) + (PAIR >> self.shift) * (m * (m - 1) // 2))
 
 
 def place(seqs, heads, at):
@@ -59,26 +61,32 @@ def pieces(seqs, heads, at, left):
                     break
             h, b = 0, b + 1
         s = seqs[b]
-        first = s.first_tile(p) if s.n else 0
-        every = s.tiles - first if s.n else 1
-        assert every >= 1
-        take = min(every - u, left)
-        yield b, h, p, (first + u if s.n else 0), (first + u + take if s.n else 0), take == every, 1 if u == 0 else 0
+        if s.tiles <= 1:
+            take = min(s.pairs - p, left)
+            for k in range(take):
+                yield b, h, p + k, 0, s.tiles, True, 0
+            left -= take
+            p += take
+            continue
+        first, cost = max(0, (p * PAIR - s.old) // s.tpt), s.cost(p)
+        tiles, take = s.tiles - first, min(cost - u, left)
+        assert cost >= 1 and tiles >= 1
+        yield b, h, p, first + u * tiles // cost, first + (u + take) * tiles // cost, take == cost, 1 if u == 0 else 0
         left -= take
         u += take
-        if u == every:
+        if u == cost:
             u, p = 0, p + 1
 
 
-@pytest.mark.parametrize("seed", range(60))
+@pytest.mark.parametrize("seed", range(200))
 def test_every_unit_is_taken_once_and_every_part_joined(seed):
     r = random.Random(seed)
-    shift, heads = r.randint(0, 7), r.randint(1, 4)
+    tpt, heads = r.choice([1, 2, 3, 16, 18, 25, 42, 64, 100, 128]), r.randint(1, 4)
     most = r.choice([1, 3, 40, 700, 3000])
     seqs = []
     for _ in range(r.randint(1, 9)):
         n = r.choice([0, 1, r.randint(1, most)])
-        seqs.append(Seq(n, r.choice([0, n, max(0, n - r.randint(0, 9)), n + r.randint(0, 2000)]), shift))
+        seqs.append(Seq(n, r.choice([0, n, max(0, n - r.randint(0, 9)), n + r.randint(0, 2000)]), tpt))
     total = sum(s.before(s.pairs) * heads for s in seqs)
     blocks = r.choice([1, 2, 7, 152])
     cut = [total * c // blocks for c in range(blocks + 1)]
@@ -92,7 +100,7 @@ def test_every_unit_is_taken_once_and_every_part_joined(seed):
                 assert (c, slot) not in parts
                 parts[c, slot] = (b, h, p)
     want = {(b, h, p, q) for b, s in enumerate(seqs) for h in range(heads) for p in range(s.pairs)
-            for q in range(s.tiles) if p * PAIR <= s.old + min(s.n, (q + 1) << shift) - 1}
+            for q in range(s.tiles) if s.tiles == 1 or p * PAIR <= s.old + min(s.n, (q + 1) * s.tpt) - 1}
     assert set(taken) == want
     joined = set()
     for c in range(blocks - 1):
@@ -103,7 +111,8 @@ def test_every_unit_is_taken_once_and_every_part_joined(seed):
         start = at - u
         if u == 0 or start < cut[c]:
             continue
-        end = start + seqs[b].before(p + 1) - seqs[b].before(p)
+        end = start + seqs[b].cost(p)
+        assert seqs[b].cost(p) == seqs[b].before(p + 1) - seqs[b].before(p)
         # a block without units, where there are fewer than blocks, leaves no part
         for k in [(c, 1)] + [(k, 0) for k in range(c + 1, blocks) if cut[k] < min(end, cut[k + 1])]:
             assert parts[k] == (b, h, p) and k not in joined

@@ -47,6 +47,7 @@ constexpr int PAIR = 2 * BK;       // keys of a pair of tiles
 constexpr int NTHREADS = 352;
 constexpr int WARP_TMA = 8, WARP_MMA = 9;  // MMA: two warps
 constexpr int MAX_BLOCKS = 152;    // one block an SM
+constexpr int BATCH = 4;           // query tiles whose log-sum-exps are staged together
 
 // Shared memory: a sequence of one query tile takes two of as many rows as they
 // have (a decode step's have 16), and as many key tiles as fit beside them; one
@@ -61,13 +62,13 @@ struct Plan {
   static constexpr int B_K_FULL = 0, B_K_EMPTY = NK, B_Q_FULL = 2 * NK, B_Q_EMPTY = B_Q_FULL + NQ,
                        B_S_FULL = B_Q_EMPTY + NQ,  // [key tile][buffer]
                        B_S_EMPTY = B_S_FULL + 4, B_DONE = B_S_EMPTY + 4, NBAR = B_DONE + 2;
-  static constexpr int OFF_LSE = 0;              // [2 key tiles][2][BR] float
-  static constexpr int OFF_BAR = OFF_LSE + 2 * 2 * BR * 4;
+  static constexpr int OFF_LSE = 0;              // [2 key tiles][2][BATCH][BR] float
+  static constexpr int OFF_BAR = OFF_LSE + 2 * 2 * BATCH * BR * 4;
   static constexpr int OFF_START = OFF_BAR + (NBAR + 1) / 2 * 16;  // sequence and offset of the block's first unit
   static constexpr int OFF_SCAN = OFF_START + 16;                  // sums of the warps
   static constexpr int OFF_TMEM = OFF_SCAN + (NTHREADS / 32) * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int OFF_Q = 4096;
+  static constexpr int OFF_Q = 9216;
   static_assert(OFF_ABORT + 4 <= OFF_Q && OFF_Q % 1024 == 0, "shared memory plan");
   static constexpr int MOST = 232448 - 1024;     // the rest aligns the tiles
   static __host__ __device__ constexpr int query_bytes(int cols) { return cols * D * 2; }
@@ -84,22 +85,25 @@ struct Plan {
   }
 };
 
-// A sequence: its tokens, keys, and the cost of its units
+// A sequence: its tokens, keys, and the cost of its pairs of key tiles.  A pair
+// costs 1 where all tokens are one query tile.  Else it costs its query tiles,
+// as many as there would be of 2^shift tokens each, which add up without a
+// loop; the tiles themselves have tpt >= 2^shift tokens, and a part of a pair's
+// cost is that part of them.
 struct Seq {
   int t0, n, len;
   int old;       // keys that were there before the tokens' own (negative: tokens with no key)
-  int pairs, tiles;
+  int pairs, tiles, costs;
   int p1, d1;    // first pair whose keys not all tokens see, and how far it starts past `old`
 
-  // query tiles that see nothing of pair p, at the front of the sequence's
-  __device__ __forceinline__ int first_tile(int p, int shift) const {
-    return max(0, (p * PAIR - old) >> shift);
-  }
-  // units of the pairs before p, of one key head
+  // query tiles of 2^shift tokens that see nothing of pair p, at the front of the sequence's
+  __device__ __forceinline__ int unseen(int p, int shift) const { return max(0, (p * PAIR - old) >> shift); }
+  __device__ __forceinline__ int cost(int p, int shift) const { return tiles <= 1 ? 1 : costs - unseen(p, shift); }
+  // cost of the pairs before p, of one key head
   __device__ __forceinline__ int64_t before(int p, int shift) const {
-    if (n == 0) return p;
+    if (tiles <= 1) return p;
     const int64_t m = max(0, p - p1);
-    return int64_t(p) * tiles - (m * (d1 >> shift) + int64_t(PAIR >> shift) * (m * (m - 1) / 2));
+    return int64_t(p) * costs - (m * (d1 >> shift) + int64_t(PAIR >> shift) * (m * (m - 1) / 2));
   }
 };
 
@@ -110,7 +114,8 @@ __device__ __forceinline__ Seq seq_of(const WeightArgs &a, int c0, int c1, int l
   s.len = min(max(l, 0), a.max_len);
   s.old = s.len - s.n;
   s.pairs = (s.len + PAIR - 1) / PAIR;
-  s.tiles = (s.n + (1 << a.shift) - 1) >> a.shift;
+  s.tiles = (s.n + a.tpt - 1) / a.tpt;
+  s.costs = (s.n + (1 << a.shift) - 1) >> a.shift;
   s.p1 = s.old <= 0 ? 0 : (s.old + PAIR - 1) / PAIR;
   s.d1 = s.p1 * PAIR - s.old;
   return s;
@@ -236,16 +241,16 @@ struct Walk {
       p += take;
       return true;
     }
-    const int first = s.first_tile(p, a.shift), all = s.tiles - first;
-    const int take = int(min(int64_t(all) - u, left));
+    const int first = max(0, (p * PAIR - s.old) / a.tpt), cost = s.cost(p, a.shift);
+    const int64_t tiles = s.tiles - first, take = min(int64_t(cost) - u, left);
     o.pairs = 1;
-    o.qa = first + int(u);
-    o.qb = o.qa + take;
-    o.whole = take == all;
+    o.qa = first + int(u * tiles / cost);
+    o.qb = first + int((u + take) * tiles / cost);
+    o.whole = take == cost;
     o.slot = u == 0 ? 1 : 0;
     left -= take;
     u += take;
-    if (u == all) u = 0, ++p;
+    if (u == cost) u = 0, ++p;
     return true;
   }
 };
@@ -266,7 +271,7 @@ __device__ __forceinline__ float *weight_at(const WeightArgs &a, int b, int h, i
   return a.w + b * a.w_seq + h * a.w_head + i;
 }
 
-template <class DT, int D>
+template <class DT, int D, bool MANY>
 __global__ void __launch_bounds__(NTHREADS, 1)
     attn_weights_kernel(const __grid_constant__ CUtensorMap tmQ,
                         const __grid_constant__ CUtensorMap tmK, const WeightArgs a) {
@@ -291,6 +296,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WARP_MMA) tmem_alloc(smem_u32(tmem_slot), 512);
+  if constexpr (MANY) {  // rows of the query tiles that no copy fills: their scores are 0, and count nothing
+    const int rows = a.tpt * a.G, rest = (a.cols - rows) * 8, n = P::query_tiles(a.cols, MANY) * P::CH * rest;
+    for (int i = threadIdx.x; i < n; i += NTHREADS) {
+      const int chunk = i / rest;
+      *reinterpret_cast<uint4 *>(sm + P::OFF_Q + (chunk * a.cols + rows) * 128 + (i - chunk * rest) * 16) =
+          make_uint4(0, 0, 0, 0);
+    }
+    fence_async_smem();
+  }
   tc_fence_before();
   const Place at = locate(a, reinterpret_cast<int64_t *>(sm + P::OFF_SCAN),
                           reinterpret_cast<int64_t *>(sm + P::OFF_START), blockIdx.x == 0,
@@ -299,8 +313,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *tmem_slot;
   Walk walk;
   walk.begin(a, at, at.total * (blockIdx.x + 1) / gridDim.x - at.at);
-  const int tpt = 1 << a.shift;  // tokens of a query tile
-  const uint32_t nk = uint32_t(P::key_tiles(a.cols, a.split)), nq = uint32_t(P::query_tiles(a.cols, a.split));
+  const int tpt = a.tpt;
+  const uint32_t nk = uint32_t(P::key_tiles(a.cols, MANY)), nq = uint32_t(P::query_tiles(a.cols, MANY));
   const uint32_t qbytes = uint32_t(P::query_bytes(a.cols)), off_k = P::OFF_Q + nq * qbytes;
   bool ok = true;                // this role's waits all ended in time
 
@@ -457,47 +471,54 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // -------------------------------------------------------------- weights
     const int g = warp >> 2, tid = threadIdx.x & 127, col = g * BK + tid;
     const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + g * 256;
-    float *ls = reinterpret_cast<float *>(sm + P::OFF_LSE) + g * 2 * BR;
+    float *ls = reinterpret_cast<float *>(sm + P::OFF_LSE) + g * 2 * BATCH * BR;
     const int tok = tid / a.G, hd = tid - tok * a.G;  // the column whose lse this thread brings
     const float c = a.scale_log2;
-    uint32_t st = 0, ql = 0;  // score tiles, and query tiles' log-sum-exps so far
+    constexpr int LB = MANY ? BATCH : 1;
+    uint32_t st = 0, ql = 0;  // score tiles, and batches of query tiles' log-sum-exps so far
+    float l[LB];
     auto lse_of = [&](const Piece &q, int tile) {
-      const int j = tile * tpt + tok;
-      return tok < tpt && j < q.s.n ? a.lse[int64_t(q.s.t0 + j) * a.Hq + q.h * a.G + hd] : INFINITY;
+#pragma unroll
+      for (int e = 0; e < LB; ++e) {
+        const int j = (tile + e) * tpt + tok;
+        l[e] = tok < tpt && j < q.s.n ? a.lse[int64_t(q.s.t0 + j) * a.Hq + q.h * a.G + hd] : INFINITY;
+      }
     };
     // what a key had before
     auto look = [&](const Piece &q, int k0) {
       return q.whole && k0 + col < q.s.old ? *weight_at(a, q.b, q.h, k0 + col) : 0.0f;
     };
-    // columns e0 .. of a score tile, NC of them in v
-    float s0 = 0.0f, s1 = 0.0f;
-    auto weigh = [&](auto &v, const float *lb, int e0, int c0, int cols) {
+    // The sum over the NC columns of a score tile in v, of which those in [lo,
+    // hi) count; lb: their rows' log-sum-exps
+    auto weigh = [&](auto &v, const float *lb, int lo, int hi) {
       constexpr int NC = sizeof(v) / 4;
-      const bool all = __all_sync(0xffffffffu, c0 <= e0) && e0 + NC <= cols;
-      if (all) {
+      Pair s = pair(0.0f, 0.0f), t = s;
+      float x, y;
+      if (__all_sync(0xffffffffu, lo <= 0 && hi >= NC)) {
         const Pair cc = pair(c, c);
-        Pair s = pair(s0, s1);
 #pragma unroll
         for (int e = 0; e < NC; e += 4) {
-          const float4 n = *reinterpret_cast<const float4 *>(lb + e0 + e);
-          float x, y;
+          const float4 n = *reinterpret_cast<const float4 *>(lb + e);
           split(fma_p(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, pair(n.x, n.y)), x, y);
           s = add_p(s, pair(ex2(x), ex2(y)));
           split(fma_p(pair(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), cc, pair(n.z, n.w)), x, y);
-          s = add_p(s, pair(ex2(x), ex2(y)));
+          t = add_p(t, pair(ex2(x), ex2(y)));
         }
-        split(s, s0, s1);
       } else {
 #pragma unroll
-        for (int e = 0; e < NC; ++e) {
-          const float x = ex2(__fmaf_rn(__uint_as_float(v[e]), c, lb[e0 + e]));
-          if (e0 + e >= c0 && e0 + e < cols) (e & 1 ? s1 : s0) += x;
+        for (int e = 0; e < NC; e += 2) {
+          x = ex2(__fmaf_rn(__uint_as_float(v[e]), c, lb[e]));
+          y = ex2(__fmaf_rn(__uint_as_float(v[e + 1]), c, lb[e + 1]));
+          s = add_p(s, pair(e >= lo && e < hi ? x : 0.0f, e + 1 >= lo && e + 1 < hi ? y : 0.0f));
         }
       }
+      split(add_p(s, t), x, y);
+      return x + y;
     };
     Piece p, nx;
     bool more = walk.next(a, p);
-    float old = more ? look(p, p.k0) : 0.0f, l = more ? lse_of(p, p.qa) : 0.0f;
+    float old = more ? look(p, p.k0) : 0.0f;
+    if (more) lse_of(p, p.qa);
     while (more && ok) {
       const bool again = walk.next(a, nx);
       float *to = weight_at(a, p.b, p.h, p.k0 + col);
@@ -511,43 +532,43 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         float sum = 0.0f;
 #pragma unroll 1
         for (int q = p.qa; q < p.qb; ++q) {
-          if (k == 0) {  // the rows' log-sum-exps, the next tile's ahead
-            ls[(++ql & 1) * BR + tid] = neg_lse2(l);
-            if (q + 1 < p.qb) l = lse_of(p, q + 1);
-            else if (again) l = lse_of(nx, nx.qa);
-            named_sync(1 + g, 128);  // two tiles on, all have read what was here
+          const int batch = LB > 1 ? (q - p.qa) % LB : 0;
+          if (k == 0 && batch == 0) {  // the rows' log-sum-exps, the next batch's ahead
+            ++ql;
+#pragma unroll
+            for (int e = 0; e < LB; ++e) ls[((ql & 1) * LB + e) * BR + tid] = neg_lse2(l[e]);
+            if (q + LB < p.qb) lse_of(p, q + LB);
+            else if (again) lse_of(nx, nx.qa);
+            named_sync(1 + g, 128);  // two batches on, all have read what was here
           }
           if (!tile) continue;
-          const float *lb = ls + (ql & 1) * BR;
+          const float *lb = ls + ((ql & 1) * LB + batch) * BR;
           const uint32_t buf = st & 1, at = ts + buf * 128;
           if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g) + 8 * buf, (st >> 1) & 1, abort_flag))) break;
           tc_fence_after();
-          const int cols = min(tpt, p.s.n - q * tpt) * a.G;
-          // the first column whose token sees this key
-          const int c0 = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
-          s0 = s1 = 0.0f;
-          if (cols <= 8) {
+          // columns of the tile that count: its tokens' (and those of a whole tile
+          // that no row fills), from the first that sees this key on
+          const int left = p.s.n - q * tpt, hi = MANY && left >= tpt ? a.cols : min(tpt, left) * a.G, lo = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
+          if (hi <= 8) {
             uint32_t v[8];
             tmem_ld8(at, v);
             tmem_wait_ld(v);
-            weigh(v, lb, 0, c0, cols);
+            sum += weigh(v, lb, lo, hi);
           } else {
-            // the next 32 columns come while these are weighed
-            uint32_t v[2][32];
-            tmem_ld32(at, v[0]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (32 * e >= cols) break;
-              wait_ld32(v[e & 1]);
-              if (32 * (e + 1) < cols) tmem_ld32(at + 32 * (e + 1), v[(e + 1) & 1]);
-              weigh(v[e & 1], lb, 32 * e, c0, cols);
+            // A loop of little code: unrolled four times, with the next columns'
+            // loads ahead, it is bound by its instruction fetches.
+#pragma unroll 1
+            for (int e = 0; e < hi; e += 32) {
+              uint32_t v[32];
+              tmem_ld32(at + e, v);
+              wait_ld32(v);
+              sum += weigh(v, lb + e, lo - e, hi - e);
             }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(P::B_S_EMPTY + 2 * g) + 8 * buf);
           ++st;
-          sum += s0 + s1;
         }
         if (!ok) break;
         if (i < p.s.len) {
@@ -555,7 +576,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           else to[k * PAIR] = __fmaf_rn(a.decay, was, sum);
         }
       }
-      if (p.qa == p.qb && again) l = lse_of(nx, nx.qa);  // no token here
+      if (p.qa == p.qb && again) lse_of(nx, nx.qa);  // no token here
       p = nx;
       more = again;
     }
@@ -580,7 +601,7 @@ __global__ void __launch_bounds__(NTHREADS) attn_weights_join_kernel(const Weigh
   w.begin(a, at, 1);
   const int64_t start = at.at - w.u;
   if (w.u == 0 || start < at.total * c / blocks) return;
-  const int64_t end = start + (w.s.before(w.p + 1, a.shift) - w.s.before(w.p, a.shift));
+  const int64_t end = start + w.s.cost(w.p, a.shift);
   const int i = w.p * PAIR + threadIdx.x;
   if (threadIdx.x >= PAIR || i >= w.s.len) return;
   float sum = a.part[(c * 2 + 1) * PAIR + threadIdx.x];
@@ -649,31 +670,32 @@ __global__ void __launch_bounds__(256) attn_weights_any_kernel(const WeightArgs 
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-template <class DT, int D>
+template <class DT, int D, bool MANY>
 int launch_tiles(const WeightArgs &a, cudaStream_t st) {
-  auto *k = attn_weights_kernel<DT, D>;
+  auto *k = attn_weights_kernel<DT, D, MANY>;
   static OncePerDevice sized;
   if (!allow_smem(sized, k, Plan<D>::MOST + 1024)) return WQ_ERR_LAUNCH;
   CUtensorMap mq, mk;
   auto pitch = [](int64_t extent, int64_t stride) { return extent == 1 && stride == 0 ? 8 : stride; };
   const int64_t qd[3] = {a.dk, a.Hq, a.T};
   const int64_t qs[2] = {pitch(a.Hq, a.q_head), pitch(a.T, a.q_token)};
-  const int qb[3] = {64, a.G, 1 << a.shift};
+  const int qb[3] = {64, a.G, a.tpt};
   const int box[4] = {64, a.box, 1, 1};
   const int64_t kd[4] = {a.dk, a.page_size, a.heads, a.num_pages};
   const int64_t ks[3] = {pitch(a.page_size, a.k_token), pitch(a.heads, a.k_head), pitch(a.num_pages, a.k_page)};
   if (!make_tma_nd_b16_sw128(&mq, a.q, 3, qd, qs, qb) || !make_tma_nd_b16_sw128(&mk, a.k, 4, kd, ks, box))
     return WQ_ERR_UNSUPPORTED;
-  k<<<unsigned(a.blocks), NTHREADS, Plan<D>::smem(a.cols, a.split), st>>>(mq, mk, a);
+  k<<<unsigned(a.blocks), NTHREADS, Plan<D>::smem(a.cols, MANY), st>>>(mq, mk, a);
   int rc = launched(1);
-  if (rc == WQ_OK && a.part && a.blocks > 1)
+  if (rc == WQ_OK && MANY && a.blocks > 1)
     rc = attn::launch_chained(attn_weights_join_kernel, unsigned(a.blocks - 1), NTHREADS, 0, true, st, a);
   return rc;
 }
 
 template <class DT>
 int launch_t(const WeightArgs &a, cudaStream_t st) {
-  if (a.tiles) return a.dk > 64 ? launch_tiles<DT, 128>(a, st) : launch_tiles<DT, 64>(a, st);
+  if (a.tiles && a.split) return a.dk > 64 ? launch_tiles<DT, 128, true>(a, st) : launch_tiles<DT, 64, true>(a, st);
+  if (a.tiles) return a.dk > 64 ? launch_tiles<DT, 128, false>(a, st) : launch_tiles<DT, 64, false>(a, st);
   const int64_t blocks = int64_t(a.B) * a.heads * ((a.max_len + 31) / 32);
   if (blocks >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
   attn_weights_any_kernel<DT><<<unsigned(blocks), 256, 0, st>>>(a);
@@ -682,12 +704,13 @@ int launch_t(const WeightArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Query tiles of a power of two of tokens: as many as fill 128 rows, no more
-// than a sequence may have (a decode step's tile is 16 columns wide, not 128).
+// Query tiles of as many tokens as fill 128 rows, no more than a sequence may
+// have (a decode step's tile is 16 columns wide, not 128).
 void plan_weights(WeightArgs &a) {
+  a.tpt = std::max(1, std::min(BR / a.G, a.max_q));
   a.shift = 0;
-  while ((2 << a.shift) * a.G <= BR && (1 << a.shift) < a.max_q) ++a.shift;
-  a.cols = (((1 << a.shift) * a.G) + 15) / 16 * 16;
+  while ((2 << a.shift) <= a.tpt) ++a.shift;
+  a.cols = (a.tpt * a.G + 15) / 16 * 16;
   a.box = gcd(a.page_size, BK);
   a.step_pages = PAIR / a.page_size;
   a.step_place = PAIR % a.page_size;
@@ -697,9 +720,9 @@ void plan_weights(WeightArgs &a) {
   // than zero; waits that end after 1 s, which 2^25 keys do not reach
   a.tiles = a.T > 0 && a.page_size % 8 == 0 && a.num_pages > 0 && pitches && a.max_len <= (1 << 25);
   const int64_t most = int64_t(a.B) * a.heads * ((a.max_len + PAIR - 1) / PAIR) *
-                       std::max(1, (a.max_q + (1 << a.shift) - 1) >> a.shift);
+                       std::max(1, (a.max_q + a.tpt - 1) / a.tpt);
   a.blocks = int(std::max<int64_t>(1, std::min<int64_t>(MAX_BLOCKS, most)));
-  a.split = a.tiles && a.max_q > (1 << a.shift);
+  a.split = a.tiles && a.max_q > a.tpt;
 }
 
 size_t weights_ws_bytes(const WeightArgs &a) {

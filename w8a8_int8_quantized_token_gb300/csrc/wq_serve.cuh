@@ -237,7 +237,8 @@ struct WeightArgs {
   int64_t w_seq, w_head;
   int32_t *status;
   // plan
-  int shift;    // log2 of the tokens of a query tile
+  int tpt;      // tokens of a query tile
+  int shift;    // log2 of the tokens that its cost goes by, at most tpt
   int cols;     // its rows, in whole 16s
   int box;      // cache rows of one TMA box
   int step_pages, step_place;  // a pair of key tiles on: pages, and places beyond them
