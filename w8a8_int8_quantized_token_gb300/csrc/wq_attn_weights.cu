@@ -488,32 +488,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     auto look = [&](const Piece &q, int k0) {
       return q.whole && k0 + col < q.s.old ? *weight_at(a, q.b, q.h, k0 + col) : 0.0f;
     };
-    // The sum over the NC columns of a score tile in v, of which those in [lo,
-    // hi) count; lb: their rows' log-sum-exps
-    auto weigh = [&](auto &v, const float *lb, int lo, int hi) {
-      constexpr int NC = sizeof(v) / 4;
-      Pair s = pair(0.0f, 0.0f), t = s;
+    // Adds the weights of the columns of a score tile in v; lb: their rows'
+    // log-sum-exps.  All of them, or those in [lo, hi).
+    Pair s0, s1;
+    auto weigh = [&](auto &v, const float *lb) {
+      const Pair cc = pair(c, c);
       float x, y;
-      if (__all_sync(0xffffffffu, lo <= 0 && hi >= NC)) {
-        const Pair cc = pair(c, c);
 #pragma unroll
-        for (int e = 0; e < NC; e += 4) {
-          const float4 n = *reinterpret_cast<const float4 *>(lb + e);
-          split(fma_p(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, pair(n.x, n.y)), x, y);
-          s = add_p(s, pair(ex2(x), ex2(y)));
-          split(fma_p(pair(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), cc, pair(n.z, n.w)), x, y);
-          t = add_p(t, pair(ex2(x), ex2(y)));
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < NC; e += 2) {
-          x = ex2(__fmaf_rn(__uint_as_float(v[e]), c, lb[e]));
-          y = ex2(__fmaf_rn(__uint_as_float(v[e + 1]), c, lb[e + 1]));
-          s = add_p(s, pair(e >= lo && e < hi ? x : 0.0f, e + 1 >= lo && e + 1 < hi ? y : 0.0f));
-        }
+      for (int e = 0; e < int(sizeof(v) / 4); e += 4) {
+        const float4 n = *reinterpret_cast<const float4 *>(lb + e);
+        split(fma_p(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), cc, pair(n.x, n.y)), x, y);
+        s0 = add_p(s0, pair(ex2(x), ex2(y)));
+        split(fma_p(pair(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), cc, pair(n.z, n.w)), x, y);
+        s1 = add_p(s1, pair(ex2(x), ex2(y)));
       }
-      split(add_p(s, t), x, y);
-      return x + y;
+    };
+    auto weigh_some = [&](auto &v, const float *lb, int lo, int hi) {
+#pragma unroll
+      for (int e = 0; e < int(sizeof(v) / 4); e += 2) {
+        const float x = ex2(__fmaf_rn(__uint_as_float(v[e]), c, lb[e]));
+        const float y = ex2(__fmaf_rn(__uint_as_float(v[e + 1]), c, lb[e + 1]));
+        s0 = add_p(s0, pair(e >= lo && e < hi ? x : 0.0f, e + 1 >= lo && e + 1 < hi ? y : 0.0f));
+      }
     };
     Piece p, nx;
     bool more = walk.next(a, p);
@@ -548,23 +544,38 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tc_fence_after();
           // columns of the tile that count: its tokens' (and those of a whole tile
           // that no row fills), from the first that sees this key on
-          const int left = p.s.n - q * tpt, hi = MANY && left >= tpt ? a.cols : min(tpt, left) * a.G, lo = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
+          const int left = p.s.n - q * tpt, hi = MANY && left >= tpt ? a.cols : min(tpt, left) * a.G;
+          const int lo = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
+          const bool seen = __all_sync(0xffffffffu, lo == 0);  // by all tokens, all keys of the warp
+          s0 = s1 = pair(0.0f, 0.0f);
+          // Loops of little code: unrolled, with the next columns' loads ahead,
+          // they take longer (prompt of 4096: 174 -> 208 us).
           if (hi <= 8) {
             uint32_t v[8];
             tmem_ld8(at, v);
             tmem_wait_ld(v);
-            sum += weigh(v, lb, lo, hi);
-          } else {
-            // A loop of little code: unrolled four times, with the next columns'
-            // loads ahead, it is bound by its instruction fetches.
+            if (seen && hi == 8) weigh(v, lb);
+            else weigh_some(v, lb, lo, hi);
+          } else if (seen && hi % 32 == 0) {
 #pragma unroll 1
             for (int e = 0; e < hi; e += 32) {
               uint32_t v[32];
               tmem_ld32(at + e, v);
               wait_ld32(v);
-              sum += weigh(v, lb + e, lo - e, hi - e);
+              weigh(v, lb + e);
+            }
+          } else {
+#pragma unroll 1
+            for (int e = 0; e < hi; e += 32) {
+              uint32_t v[32];
+              tmem_ld32(at + e, v);
+              wait_ld32(v);
+              weigh_some(v, lb + e, lo - e, hi - e);
             }
           }
+          float x, y;
+          split(add_p(s0, s1), x, y);
+          sum += x + y;
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(P::B_S_EMPTY + 2 * g) + 8 * buf);
