@@ -11,6 +11,8 @@
 // takes the same place of several heads, whose loads are in flight together and
 // which share the table row's and the weight's part.  Bound by HBM: every
 // element is read once and written once; table rows come from L2.
+#include <algorithm>
+
 #include "wq_serve.cuh"
 
 namespace wq {
@@ -27,7 +29,8 @@ __device__ __forceinline__ Raw *dst_of(const RopeArgs &a, const RopeSeg &s, int6
     if (tell) set_status(a.status, WQ_ERR_INDEX);
     return nullptr;
   }
-  const int64_t page = slot / a.page_size;
+  // a division of 64 bits takes as long as everything else here
+  const int64_t page = slot >> 32 ? slot / a.page_size : int64_t(uint32_t(slot) / uint32_t(a.page_size));
   return d + page * s.d_page + (slot - page * a.page_size) * s.d_token;
 }
 
@@ -48,44 +51,77 @@ __device__ __forceinline__ void turn(float &x, float &y, float c, float s) {
 }
 
 // Lanes of one head: two vectors of W elements each
-__host__ __device__ inline int lanes_of(const RopeSeg &s, int W) {
+inline int lanes_of(const RopeSeg &s, int W) {
   return s.rot / (2 * W) + (s.D - s.rot / (2 * W) * (2 * W) + 2 * W - 1) / (2 * W);
 }
-// Warps that a token takes in a segment: 32 / lanes heads side by side, KH deep
-__host__ __device__ inline int warps_of(const RopeSeg &s, int W, int KH) {
-  const int side = 32 / lanes_of(s, W);
-  return (s.heads + side * KH - 1) / (side * KH);
+
+// How a launch's warps share a token's segments (host values): the heads of a
+// segment side by side in a warp and KH deep
+struct Cut {
+  int per_token;           // warps
+  int tokens;              // of a block of at most 8 warps (1 where a token takes more)
+  int lanes[3], side[3];   // of a head; heads side by side
+  int warps[3], top[3];    // warps of a segment; first step of a head's sum
+};
+
+// A vector's elements as pairs of floats
+template <int W, class V>
+__device__ __forceinline__ void get_pairs(const V &v, Pair (&p)[W / 2]) {
+  float f[W];
+  v.get(f);
+#pragma unroll
+  for (int e = 0; e < W; e += 2) p[e / 2] = pair(f[e], f[e + 1]);
+}
+template <int W, class V>
+__device__ __forceinline__ void set_pairs(V &v, const Pair (&p)[W / 2]) {
+  float f[W];
+#pragma unroll
+  for (int e = 0; e < W; e += 2) split(p[e / 2], f[e], f[e + 1]);
+  v.set(f);
+}
+// (x, y) -> (x c - y s, y c + x s): pairs of neighbours (interleaved layout)
+__device__ __forceinline__ Pair turn_inner(Pair p, float c, float s) {
+  float x, y;
+  split(p, x, y);
+  return fma_p(p, pair(c, c), mul_p(pair(y, x), pair(-s, s)));
 }
 
 template <class DT, int KH>
-__global__ void __launch_bounds__(256) head_norm_vec_kernel(const HeadNormArgs h, int per_token) {
+__global__ void __launch_bounds__(256) head_norm_vec_kernel(const __grid_constant__ HeadNormArgs h,
+                                                            const __grid_constant__ Cut cut) {
   using Raw = typename DT::Raw;
-  constexpr int W = DT::kVec;
+  constexpr int W = DT::kVec, P = W / 2;
   using V = Vec<DT, W>;
   const RopeArgs &a = h.r;
-  const int64_t item = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t t = item / per_token;
-  if (t >= a.T) return;  // whole warps
-  int rest = int(item - t * per_token), i = 0;
-  while (rest >= warps_of(a.seg[i], W, KH)) rest -= warps_of(a.seg[i], W, KH), ++i;
+  const int warp = threadIdx.x >> 5, own_token = warp / cut.per_token;
+  int rest = int(blockIdx.y) * 8 + warp - own_token * cut.per_token, i = 0;
+  const int64_t t = int64_t(blockIdx.x) * cut.tokens + own_token;
+  if (t >= a.T || rest >= cut.per_token) return;  // whole warps
+  while (rest >= cut.warps[i]) rest -= cut.warps[i], ++i;
   const RopeSeg &s = a.seg[i];
-  const int lanes = lanes_of(s, W), side = 32 / lanes, lane = threadIdx.x & 31;
+  const int lanes = cut.lanes[i], side = cut.side[i], lane = threadIdx.x & 31;
   const int own = lane / lanes, piece = lane - own * lanes;
   const int head0 = (rest * KH) * side + own;  // heads head0 + k * side
   const bool live = own < side;
-  const bool half = piece < s.rot / (2 * W) && a.layout == WQ_ROPE_HALF;
+  const bool half = a.layout == WQ_ROPE_HALF && piece * 2 * W < s.rot;
   const int o0 = half ? piece * W : piece * 2 * W, o1 = half ? o0 + s.rot / 2 : o0 + W;
   const bool two = o1 < s.D;
-  const Raw *x = static_cast<const Raw *>(s.src) + t * s.s_token;
+  const Raw *x = static_cast<const Raw *>(s.src) + t * s.s_token + head0 * s.s_head;
   V p[KH], q[KH];
 #pragma unroll
   for (int k = 0; k < KH; ++k) {
-    const int head = head0 + k * side;
     p[k].w = q[k].w = make_uint4(0, 0, 0, 0);
-    if (live && head < s.heads) {
-      p[k] = V::load(x + head * s.s_head + o0);
-      if (two) q[k] = V::load(x + head * s.s_head + o1);
+    if (live && head0 + k * side < s.heads) {
+      p[k] = V::load(x + k * side * s.s_head + o0);
+      if (two) q[k] = V::load(x + k * side * s.s_head + o1);
     }
+  }
+  V w0, w1;
+  w0.w = w1.w = make_uint4(0, 0, 0, 0);
+  const Raw *weight = static_cast<const Raw *>(h.weight[i]);
+  if (weight && live) {
+    w0 = V::load(weight + o0);
+    if (two) w1 = V::load(weight + o1);
   }
   const bool tell = rest == 0 && lane == 0;
   Raw *d = dst_of<Raw>(a, s, t, tell);
@@ -101,73 +137,84 @@ __global__ void __launch_bounds__(256) head_norm_vec_kernel(const HeadNormArgs h
     }
   }
   if (!write) return;  // the same for the whole warp
+  d += head0 * s.d_head;
+  if (!h.norm[i]) {  // values
+#pragma unroll
+    for (int k = 0; k < KH; ++k)
+      if (live && head0 + k * side < s.heads) {
+        p[k].store(d + k * side * s.d_head + o0);
+        if (two) q[k].store(d + k * side * s.d_head + o1);
+      }
+    return;
+  }
   // pairs of the first and of the second vector that turn
   const bool inter = a.layout == WQ_ROPE_INTERLEAVED;
-  const bool first = live && (half || (inter && o0 < s.rot));
-  const bool second = live && inter && o1 < s.rot;
-  float c[W], n[W];  // cos and sin of the pairs
+  const bool first = live && (half || (inter && o0 < s.rot)), second = live && inter && o1 < s.rot;
+  float4 cs[P];  // cos and sin of two of the lane's pairs of elements each
   if (first) {
     const float2 *r = row + (half ? o0 : o0 / 2);
 #pragma unroll
-    for (int e = 0; e < W; e += 2) {
-      if (e < W / 2 || half || second) {
-        const float4 w = *reinterpret_cast<const float4 *>(r + e);
-        c[e] = w.x;
-        n[e] = w.y;
-        c[e + 1] = w.z;
-        n[e + 1] = w.w;
-      }
-    }
+    for (int e = 0; e < P; ++e)
+      if (e < P / 2 || half || second) cs[e] = *reinterpret_cast<const float4 *>(r + 2 * e);
   }
-  float wp[W], wq_[W];
-#pragma unroll
-  for (int e = 0; e < W; ++e) wp[e] = wq_[e] = 1.0f;
-  if (h.weight[i] && live) {
-    const Raw *w = static_cast<const Raw *>(h.weight[i]);
-    V::load(w + o0).get(wp);
-    if (two) V::load(w + o1).get(wq_);
-  }
-  int top = 1;  // the first step of the heads' sums
-  while (2 * top < lanes) top *= 2;
 #pragma unroll
   for (int k = 0; k < KH; ++k) {
     const int head = head0 + k * side;
     if (__all_sync(0xffffffffu, head >= s.heads)) break;
-    if (h.norm[i]) {
-      float f[W], g[W];
-      p[k].get(f);
-      q[k].get(g);
-      float sum = 0.0f;
+    Pair f[P], g[P], sq = pair(0.0f, 0.0f);
+    get_pairs<W>(p[k], f);
+    get_pairs<W>(q[k], g);
 #pragma unroll
-      for (int e = 0; e < W; ++e) sum = __fmaf_rn(f[e], f[e], sum);
+    for (int e = 0; e < P; ++e) sq = fma_p(f[e], f[e], sq);
 #pragma unroll
-      for (int e = 0; e < W; ++e) sum = __fmaf_rn(g[e], g[e], sum);
-      sum = head_sum(sum, lanes, piece, top);
-      const float r = rsqrtf(__fmaf_rn(sum, h.inv_d[i], h.eps));
+    for (int e = 0; e < P; ++e) sq = fma_p(g[e], g[e], sq);
+    float sum, more;
+    split(sq, sum, more);
+    sum = head_sum(__fadd_rn(sum, more), lanes, piece, cut.top[i]);
+    const float r = rsqrtf(__fmaf_rn(sum, h.inv_d[i], h.eps));
+    const Pair rr = pair(r, r);
 #pragma unroll
-      for (int e = 0; e < W; ++e) {
-        f[e] = __fmul_rn(__fmul_rn(f[e], r), wp[e]);
-        g[e] = __fmul_rn(__fmul_rn(g[e], r), wq_[e]);
-      }
-      if (first) {
-        if (half) {
+    for (int e = 0; e < P; ++e) f[e] = mul_p(f[e], rr), g[e] = mul_p(g[e], rr);
+    if (weight) {
+      Pair u[P];
+      get_pairs<W>(w0, u);
 #pragma unroll
-          for (int e = 0; e < W; ++e) turn(f[e], g[e], c[e], n[e]);
-        } else {
+      for (int e = 0; e < P; ++e) f[e] = mul_p(f[e], u[e]);
+      get_pairs<W>(w1, u);
 #pragma unroll
-          for (int e = 0; e < W / 2; ++e) turn(f[2 * e], f[2 * e + 1], c[e], n[e]);
-          if (second) {
+      for (int e = 0; e < P; ++e) g[e] = mul_p(g[e], u[e]);
+    }
+    if (first) {
+      if (half) {
 #pragma unroll
-            for (int e = 0; e < W / 2; ++e) turn(g[2 * e], g[2 * e + 1], c[W / 2 + e], n[W / 2 + e]);
+        for (int e = 0; e < P; ++e) {
+          const Pair c = pair(cs[e].x, cs[e].z), n = pair(cs[e].y, cs[e].w), m = pair(-cs[e].y, -cs[e].w);
+          const Pair u = fma_p(f[e], c, mul_p(g[e], m));
+          g[e] = fma_p(g[e], c, mul_p(f[e], n));
+          f[e] = u;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < P; e += 2) {
+          f[e] = turn_inner(f[e], cs[e / 2].x, cs[e / 2].y);
+          f[e + 1] = turn_inner(f[e + 1], cs[e / 2].z, cs[e / 2].w);
+        }
+        if (second) {
+#pragma unroll
+          for (int e = 0; e < P; e += 2) {
+            g[e] = turn_inner(g[e], cs[(P + e) / 2].x, cs[(P + e) / 2].y);
+            g[e + 1] = turn_inner(g[e + 1], cs[(P + e) / 2].z, cs[(P + e) / 2].w);
           }
         }
       }
-      p[k].set(f);
-      q[k].set(g);
     }
     if (live && head < s.heads) {
-      p[k].store(d + head * s.d_head + o0);
-      if (two) q[k].store(d + head * s.d_head + o1);
+      set_pairs<W>(p[k], f);
+      p[k].store(d + k * side * s.d_head + o0);
+      if (two) {
+        set_pairs<W>(q[k], g);
+        q[k].store(d + k * side * s.d_head + o1);
+      }
     }
   }
 }
@@ -226,11 +273,21 @@ __global__ void __launch_bounds__(256) head_norm_any_kernel(const HeadNormArgs h
 
 template <class DT, int KH>
 int launch_vec(const HeadNormArgs &h, cudaStream_t st) {
-  int per_token = 0;
-  for (int i = 0; i < h.r.nseg; ++i) per_token += warps_of(h.r.seg[i], DT::kVec, KH);
-  const int64_t blocks = (h.r.T * per_token + 7) / 8;
-  if (blocks >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
-  head_norm_vec_kernel<DT, KH><<<unsigned(blocks), 256, 0, st>>>(h, per_token);
+  Cut c{};
+  for (int i = 0; i < h.r.nseg; ++i) {
+    const RopeSeg &s = h.r.seg[i];
+    c.lanes[i] = lanes_of(s, DT::kVec);
+    c.side[i] = 32 / c.lanes[i];
+    c.warps[i] = (s.heads + c.side[i] * KH - 1) / (c.side[i] * KH);
+    for (c.top[i] = 1; 2 * c.top[i] < c.lanes[i];) c.top[i] *= 2;
+    c.per_token += c.warps[i];
+  }
+  c.tokens = std::max(1, 8 / c.per_token);
+  const dim3 grid(unsigned((h.r.T + c.tokens - 1) / c.tokens), unsigned((c.per_token + 7) / 8));
+  if (grid.y > 65535) return WQ_ERR_UNSUPPORTED;
+  const int warps = c.tokens * std::min(c.per_token, 8);
+  if (c.per_token > 8) c.tokens = 1;
+  head_norm_vec_kernel<DT, KH><<<grid, unsigned(warps * 32), 0, st>>>(h, c);
   return launched(1);
 }
 

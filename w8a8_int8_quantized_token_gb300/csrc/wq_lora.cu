@@ -16,9 +16,8 @@
 // only y is rounded.  fp16 operands are taken relative to a power of two near a
 // row's largest, which keeps them in range.
 //
-// Up to 256 tokens every cluster finds its tile itself: that of token t exists
-// if t is the first of its adapter's tokens or comes a multiple of a tile after
-// it.  With more tokens a first kernel sorts them by adapter.
+// Up to 256 tokens every cluster finds its tile itself; with more, a first
+// kernel sorts them by adapter.
 #include <algorithm>
 
 #include "wq_attn.cuh"
@@ -57,6 +56,7 @@ struct Plan {
   static constexpr int OFF_TOK = OFF_UP + BM * 4;      // [BM] int
   static constexpr int OFF_MISC = OFF_TOK + BM * 4;
   static constexpr int SMEM = OFF_MISC + 64;
+  static_assert(OFF_B >= NT * 4, "scratch of find_tile");
   static_assert(SMEM <= 232448, "shared memory plan");
 };
 
@@ -83,9 +83,10 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-// The tokens of this cluster's tile into tok; their adapter, or -1
+// The tokens of this cluster's tile into tok; their adapter, or -1.  Without a
+// list every thread looks at one token: `scratch` holds the adapters of all.
 template <int BM>
-__device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, int *misc, int &count) {
+__device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, int *scratch, int *misc, int &count) {
   if (a.order) {
     wait_last_kernel();
     if (tile >= *a.ntiles) return -1;
@@ -95,29 +96,36 @@ __device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, 
     count = d.z;
     return d.x;
   }
-  // token `tile` and those after it with its adapter, if a tile begins there
-  const int id = a.ids[tile], i = threadIdx.x;
-  if (id < 0 || id >= a.n) {
-    if (id >= a.n && i == 0) set_status(a.status, WQ_ERR_INDEX);
-    return -1;
+  const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  int id = i < a.T ? a.ids[i] : -1;
+  if (id >= a.n) {
+    if (tile == 0) set_status(a.status, WQ_ERR_INDEX);
+    id = -1;
   }
-  const bool same = i < a.T && a.ids[i] == id;
-  const uint32_t m = __ballot_sync(0xffffffffu, same);
-  if ((i & 31) == 0) misc[i >> 5] = int(m);
+  scratch[i] = id;
+  const uint32_t below = (1u << lane) - 1u;
+  int before = __popc(__match_any_sync(0xffffffffu, id) & below);  // tokens of this adapter before
   __syncthreads();
-  int before = 0, mine = __popc(m & ((1u << (i & 31)) - 1u)), all = 0;
-#pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    const uint32_t v = uint32_t(misc[w]);
-    if (w < i >> 5) mine += __popc(v);
-    before += w < tile >> 5 ? __popc(v) : w == tile >> 5 ? __popc(v & ((1u << (tile & 31)) - 1u)) : 0;
-    all += __popc(v);
+  for (int j = 0; j < warp * 8; ++j) {
+    const int4 v = reinterpret_cast<const int4 *>(scratch)[j];
+    before += int(v.x == id) + int(v.y == id) + int(v.z == id) + int(v.w == id);
   }
-  if (before % BM) return -1;
-  if (same && mine >= before && mine < before + BM) tok[mine - before] = i;
+  // tiles begin at every BM-th of an adapter's tokens, and count in the order of those
+  const bool first = id >= 0 && before % BM == 0;
+  const uint32_t m = __ballot_sync(0xffffffffu, first);
+  if (lane == 0) misc[warp] = __popc(m);
+  if (i == 0) misc[NT / 32] = -1;
   __syncthreads();
-  count = min(BM, all - before);
-  return id;
+  int rank = __popc(m & below);
+  for (int w = 0; w < warp; ++w) rank += misc[w];
+  if (first && rank == tile) misc[NT / 32] = id, misc[NT / 32 + 1] = before;
+  __syncthreads();
+  const int own = misc[NT / 32], from = misc[NT / 32 + 1];
+  if (own < 0) return -1;
+  const bool mine = id == own && before >= from && before < from + BM;
+  if (mine) tok[before - from] = i;
+  count = __syncthreads_count(mine);
+  return own;
 }
 
 template <class DT, int BM, int RP>
@@ -129,50 +137,86 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = int(cluster_size()), rank = int(tc::cluster_ctarank());
   int count = 0;
-  const int id = find_tile<BM>(a, int(blockIdx.x) / C, tok, reinterpret_cast<int *>(sm + P::OFF_MISC), count);
+  const int id = find_tile<BM>(a, int(blockIdx.x) / C, tok, reinterpret_cast<int *>(sm),
+                               reinterpret_cast<int *>(sm + P::OFF_MISC), count);
   if (id < 0) return;  // the whole cluster
 
-  // ---- the block's rows of B, ahead of all else
-  const uint16_t *B = a.B + int64_t(id) * a.N * a.r;
+  // A thread's copies keep their places in a stage, and step along in memory.
+  // ---- the block's rows of B, for the second product
   const int chunks = (a.N + P::NC - 1) / P::NC;  // of columns of y, dealt out in stretches
   const int c0 = chunks * rank / C, c1 = chunks * (rank + 1) / C;
-  auto load_b = [&](int c) {
-    if (c < c1) {
-      const uint32_t to = base + P::OFF_B + uint32_t((c - c0) % P::N2 * P::BB);
-      for (int i = threadIdx.x; i < P::NC * (RP / 8); i += NT) {
-        // A thread of the second product gets eight neighbouring columns of y:
-        // column 8t + 2p + e of a group of 32 is column 2t + e of its p-th tile
-        const int row = i / (RP / 8), piece = i % (RP / 8), n = c * P::NC + row;
-        const int g = row & 31, at = (row & ~31) + ((g >> 1) & 3) * 8 + (g >> 3) * 2 + (g & 1);
-        const bool on = n < a.N && piece * 8 < a.r;
-        cp16(to + uint32_t(at * P::BP + piece * 16), B + (on ? int64_t(n) * a.r + piece * 8 : 0), on);
+  constexpr int BP8 = RP / 8, NB = (P::NC * BP8 + NT - 1) / NT;  // pieces of a row; copies of a thread
+  static_assert((P::NC * BP8 % NT == 0 || NB == 1) && NT % BP8 == 0, "whole copies, or one of some threads");
+  const int b_row = threadIdx.x / BP8, b_piece = threadIdx.x % BP8;
+  const uint16_t *b_src = a.B + (int64_t(id) * a.N + c0 * P::NC + b_row) * a.r + b_piece * 8;
+  const bool b_on = b_piece * 8 < a.r;
+  uint32_t b_to[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    // A thread of the second product gets eight neighbouring columns of y:
+    // column 8t + 2p + e of a group of 32 is column 2t + e of its p-th tile
+    const int row = b_row + j * (NT / BP8), g = row & 31;
+    const int at = (row & ~31) + ((g >> 1) & 3) * 8 + (g >> 3) * 2 + (g & 1);
+    b_to[j] = base + P::OFF_B + uint32_t(at * P::BP + b_piece * 16);
+  }
+  uint32_t b_stage = 0;
+  int b_next = c0;
+  auto load_b = [&]() {
+    if (b_next < c1) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (P::NC * BP8 < NT && b_row >= P::NC) break;
+        const bool on = b_on && b_next * P::NC + b_row + j * (NT / BP8) < a.N;
+        cp16(b_to[j] + b_stage, on ? b_src + int64_t(j) * (NT / BP8) * a.r : a.B, on);
       }
+      b_src += int64_t(P::NC) * a.r;
+      b_stage = b_stage == (P::N2 - 1) * P::BB ? 0 : b_stage + P::BB;
+      ++b_next;
     }
     commit();
   };
 
   // ---- first product: this block's slice of the long axis
-  const uint16_t *A = a.A + int64_t(id) * a.r * a.H;
   const int steps = (a.H + P::KS - 1) / P::KS, s0 = steps * rank / C, s1 = steps * (rank + 1) / C;
-  constexpr int PIECES = P::KS / 8;
-  auto load_x = [&](int s) {
-    if (s < s1) {
-      const uint32_t to = base + P::OFF_1 + uint32_t((s - s0) % P::N1 * (P::XB + P::AB));
-      for (int i = threadIdx.x; i < (BM + RP) * PIECES; i += NT) {
-        const int row = i / PIECES, piece = i % PIECES, k = s * P::KS + piece * 8;
-        const bool isx = row < BM;
-        const int rr = isx ? row : row - BM;
-        const bool on = k < a.H && (isx ? rr < count : rr < a.r);
-        const uint16_t *src = isx ? a.x + int64_t(on ? tok[rr] : 0) * a.ldx : A + int64_t(on ? rr : 0) * a.H;
-        cp16(to + uint32_t(row * (P::KS * 2) + ((piece ^ (row & 7)) << 4)), src + (on ? k : 0), on);
+  constexpr int PIECES = P::KS / 8, NX = BM * PIECES / NT, NA = (RP * PIECES + NT - 1) / NT, ROWS = NT / PIECES;
+  static_assert(BM * PIECES % NT == 0 && (RP * PIECES % NT == 0 || NA == 1), "whole copies, or one of some threads");
+  const int x_row = threadIdx.x / PIECES, x_piece = threadIdx.x % PIECES;
+  const uint32_t x_to = base + P::OFF_1 + uint32_t(x_row * (P::KS * 2) + ((x_piece ^ (x_row & 7)) << 4));
+  const uint16_t *x_src[NX], *a_src = a.A + (int64_t(id) * a.r + x_row) * a.H + s0 * P::KS + x_piece * 8;
+  int x_ahead = 0;  // elements that x_src and a_src are to step on
+  bool x_on[NX];
+#pragma unroll
+  for (int j = 0; j < NX; ++j) {
+    const int row = x_row + j * ROWS;
+    x_on[j] = row < count;
+    x_src[j] = a.x + int64_t(x_on[j] ? tok[row] : 0) * a.ldx + s0 * P::KS + x_piece * 8;
+  }
+  uint32_t x_stage = 0;
+  int x_next = s0;
+  auto load_x = [&]() {
+    if (x_next < s1) {
+      const bool in = x_next * P::KS + x_piece * 8 < a.H;
+#pragma unroll
+      for (int j = 0; j < NX; ++j) {
+        const bool on = in && x_on[j];
+        cp16(x_to + x_stage + j * ROWS * (P::KS * 2), on ? x_src[j] + x_ahead : a.x, on);
       }
+#pragma unroll
+      for (int j = 0; j < NA; ++j) {
+        if (RP * PIECES < NT && x_row >= RP) break;
+        const bool on = in && x_row + j * ROWS < a.r;
+        cp16(x_to + x_stage + P::XB + j * ROWS * (P::KS * 2), on ? a_src + int64_t(j) * ROWS * a.H + x_ahead : a.A, on);
+      }
+      x_ahead += P::KS;
+      x_stage = x_stage == (P::N1 - 1) * (P::XB + P::AB) ? 0 : x_stage + P::XB + P::AB;
+      ++x_next;
     }
     commit();
   };
 #pragma unroll
-  for (int i = 0; i < P::N1 - 1; ++i) load_x(s0 + i);
+  for (int i = 0; i < P::N1 - 1; ++i) load_x();
 #pragma unroll
-  for (int i = 0; i < P::N2 - 1; ++i) load_b(c0 + i);
+  for (int i = 0; i < P::N2 - 1; ++i) load_b();
 
   const int wm = warp % P::WM, wk = warp / P::WM;
   float acc[RP / 8][4];
@@ -180,14 +224,15 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   for (int i = 0; i < RP / 8; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] = 0.0f;
+  uint32_t xs = base + P::OFF_1;
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     // groups of copies in order: x of the first stages, all of B's, then x of one stage a step
     if (s - s0 < P::N1 - 1) wait_group<P::N1 - 2 + P::N2 - 1>();
     else wait_group<P::N1 - 2>();
     __syncthreads();
-    load_x(s + P::N1 - 1);
-    const uint32_t xs = base + P::OFF_1 + uint32_t((s - s0) % P::N1 * (P::XB + P::AB)), as = xs + P::XB;
+    load_x();
+    const uint32_t as = xs + P::XB;
 #pragma unroll
     for (int kk = 0; kk < P::KS / 16 / P::WK; ++kk) {
       const int step = kk * P::WK + wk;
@@ -205,6 +250,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
         mma<DT>(acc[2 * p + 1], fa, fb[2], fb[3]);
       }
     }
+    xs = xs == base + P::OFF_1 + (P::N1 - 1) * (P::XB + P::AB) ? base + P::OFF_1 : xs + P::XB + P::AB;
   }
   // ---- its sum over the warps, then over the cluster's blocks
   wait_group<0>();
@@ -293,14 +339,15 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     }
   };
   load_y(c0);
+  uint32_t bs = base + P::OFF_B + uint32_t(wk * 32 * P::BP);
+  const uint32_t b_end = bs + P::N2 * P::BB;
 #pragma unroll 1
   for (int c = c0; c < c1; ++c) {
     wait_group<P::N2 - 2>();
     __syncthreads();
-    load_b(c + P::N2 - 1);
+    load_b();
     const V o0 = v0, o1 = v1;
     load_y(c + 1);
-    const uint32_t bs = base + P::OFF_B + uint32_t((c - c0) % P::N2 * P::BB + wk * 32 * P::BP);
     float d[4][4];
 #pragma unroll
     for (int p = 0; p < 4; ++p)
@@ -345,6 +392,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
         w.store(y1 + col);
       }
     }
+    if ((bs += P::BB) == b_end) bs -= P::N2 * P::BB;
   }
   wait_group<0>();
   cluster_wait();  // this block's part has been read by all
@@ -359,11 +407,21 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = threadIdx.x; i < a.n; i += kGroupThreads) cnt[i] = 0;
   __syncthreads();
-  auto id_of = [&](int t) {
-    const int id = t < a.T ? a.ids[t] : -1;
-    if (id >= a.n) set_status(a.status, WQ_ERR_INDEX);
-    return id >= a.n || id < 0 ? -1 : id;
+  constexpr int E = 8;  // tokens a thread looks at together
+  auto load = [&](int t0, int(&id)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int t = t0 + e * kGroupThreads + int(threadIdx.x);
+      id[e] = t < a.T ? a.ids[t] : -1;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (id[e] >= a.n) set_status(a.status, WQ_ERR_INDEX);
+      id[e] = id[e] >= a.n || id[e] < 0 ? -1 : id[e];
+    }
   };
+  int id[E];
+  load(0, id);
   // one atomic for the lanes that agree
   auto take = [&](int id) {
     const uint32_t m = __match_any_sync(0xffffffffu, id);
@@ -372,7 +430,11 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
     if (lane == lead && id >= 0) at = atomicAdd(&cnt[id], __popc(m));
     return __shfl_sync(0xffffffffu, at, lead) + __popc(m & ((1u << lane) - 1u));
   };
-  for (int t0 = 0; t0 < a.T; t0 += kGroupThreads) take(id_of(t0 + int(threadIdx.x)));
+  for (int t0 = 0; t0 < a.T; t0 += E * kGroupThreads) {
+    if (t0) load(t0, id);
+#pragma unroll
+    for (int e = 0; e < E; ++e) take(id[e]);
+  }
   __syncthreads();
   // first place and first tile of each adapter: a thread has a stretch of them
   const int per = (a.n + kGroupThreads - 1) / kGroupThreads, n0 = min(int(threadIdx.x) * per, a.n), n1 = min(n0 + per, a.n);
@@ -398,9 +460,13 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   }
   if (threadIdx.x == 0) *a.ntiles = all;
   __syncthreads();
-  for (int t0 = 0; t0 < a.T; t0 += kGroupThreads) {
-    const int t = t0 + int(threadIdx.x), id = id_of(t), to = take(id);
-    if (id >= 0) a.order[to] = t;
+  for (int t0 = 0; t0 < a.T; t0 += E * kGroupThreads) {
+    if (a.T > E * kGroupThreads) load(t0, id);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int to = take(id[e]);
+      if (id[e] >= 0) a.order[to] = t0 + e * kGroupThreads + int(threadIdx.x);
+    }
   }
 }
 
@@ -435,12 +501,9 @@ int launch_rank(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
   return launch_one<DT, BM, 128>(a, tiles, C, st);
 }
 
-// Tokens of a tile, by their number
-inline int tile_of(int64_t T) { return T > 1024 ? 64 : 16; }
-// Tiles at most
-inline int64_t tiles_of(int64_t T, int64_t n) {
-  return T <= kInline ? T : std::min(T, n) + T / tile_of(T);
-}
+// Tokens of a tile, by their number; tiles at most
+inline int tile_of(int64_t T) { return T <= kInline ? 16 : 64; }
+inline int64_t tiles_of(int64_t T, int64_t n) { return std::min(T, n + T / tile_of(T)); }
 
 }  // namespace
 
@@ -450,7 +513,7 @@ size_t lora_ws_bytes(int64_t T, int64_t n) {
 }
 
 int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
-  const int BM = a.T <= kInline ? 16 : tile_of(a.T);
+  const int BM = tile_of(a.T);
   const int64_t tiles = tiles_of(a.T, a.n);
   if (a.T > kInline) {
     char *p = static_cast<char *>(ws);
@@ -461,7 +524,9 @@ int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
     const int rc = launched(1);
     if (rc != WQ_OK) return rc;
   }
-  const int C = BM == 16 ? 8 : 4;
+  // Blocks of a tile: as many as let all tiles run at the same time, two blocks an SM
+  int C = 8;
+  while (C > 1 && tiles * C > 2 * 152) C /= 2;
   if (dtype == WQ_DT_BF16) return BM == 16 ? launch_rank<Bf16, 16>(a, tiles, C, st) : launch_rank<Bf16, 64>(a, tiles, C, st);
   return BM == 16 ? launch_rank<F16, 16>(a, tiles, C, st) : launch_rank<F16, 64>(a, tiles, C, st);
 }
