@@ -63,28 +63,6 @@ struct Cut {
   int warps[3], top[3];    // warps of a segment; first step of a head's sum
 };
 
-// A vector's elements as pairs of floats
-template <int W, class V>
-__device__ __forceinline__ void get_pairs(const V &v, Pair (&p)[W / 2]) {
-  float f[W];
-  v.get(f);
-#pragma unroll
-  for (int e = 0; e < W; e += 2) p[e / 2] = pair(f[e], f[e + 1]);
-}
-template <int W, class V>
-__device__ __forceinline__ void set_pairs(V &v, const Pair (&p)[W / 2]) {
-  float f[W];
-#pragma unroll
-  for (int e = 0; e < W; e += 2) split(p[e / 2], f[e], f[e + 1]);
-  v.set(f);
-}
-// (x, y) -> (x c - y s, y c + x s): pairs of neighbours (interleaved layout)
-__device__ __forceinline__ Pair turn_inner(Pair p, float c, float s) {
-  float x, y;
-  split(p, x, y);
-  return fma_p(p, pair(c, c), mul_p(pair(y, x), pair(-s, s)));
-}
-
 // A lane's place in a token: its segment, its heads (head0 + k * side) and the
 // vectors at o0 and o1 of each
 template <int W>
@@ -120,100 +98,87 @@ struct Place {
   }
 };
 
-// The table row's part of a lane: cos and sin of two pairs of elements in each
-template <int W>
-__device__ __forceinline__ void load_turns(const Place<W> &l, const float2 *row, float4 (&cs)[W / 2]) {
-#pragma unroll
-  for (int e = 0; e < W / 4; ++e) {
-    if (l.half || l.first) cs[e] = *reinterpret_cast<const float4 *>(row + (l.half ? l.o0 : l.o0 / 2) + 2 * e);
-    if (l.half || l.second)
-      cs[W / 4 + e] = *reinterpret_cast<const float4 *>(row + (l.half ? l.o0 + W / 2 : l.o1 / 2) + 2 * e);
-  }
-}
-
-// Norm and rotation of one head's two vectors, in place
+// Norm and rotation of one head's two vectors, in place.  row: cos and sin of
+// the token's pairs.  The weight and the rotation are taken before the norm's
+// factor, which all of them wait for the sum of squares for.
 template <class DT, int W = DT::kVec>
 __device__ __forceinline__ void norm_turn(Vec<DT, W> &p, Vec<DT, W> &q, const Vec<DT, W> &w0, const Vec<DT, W> &w1,
-                                          bool weighted, const float4 (&cs)[W / 2], const Place<W> &l, float inv_d,
-                                          float eps) {
-  constexpr int P = W / 2;
-  Pair f[P], g[P], sq = pair(0.0f, 0.0f);
-  get_pairs<W>(p, f);
-  get_pairs<W>(q, g);
+                                          bool weighted, const float2 *row, const Place<W> &l, float inv_d, float eps) {
+  float f[W], g[W], sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  p.get(f);
+  q.get(g);
 #pragma unroll
-  for (int e = 0; e < P; ++e) sq = fma_p(f[e], f[e], sq);
-#pragma unroll
-  for (int e = 0; e < P; ++e) sq = fma_p(g[e], g[e], sq);
-  float sum, more;
-  split(sq, sum, more);
-  sum = head_sum(__fadd_rn(sum, more), l.lanes, l.piece, l.top);
-  const float r = rsqrtf(__fmaf_rn(sum, inv_d, eps));
-  const Pair rr = pair(r, r);
-#pragma unroll
-  for (int e = 0; e < P; ++e) f[e] = mul_p(f[e], rr), g[e] = mul_p(g[e], rr);
+  for (int e = 0; e < W; ++e) {
+    sum[e & 1] = __fmaf_rn(f[e], f[e], sum[e & 1]);
+    sum[2 + (e & 1)] = __fmaf_rn(g[e], g[e], sum[2 + (e & 1)]);
+  }
+  const float all = head_sum(__fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])), l.lanes, l.piece, l.top);
   if (weighted) {
-    Pair u[P];
-    get_pairs<W>(w0, u);
+    float u[W];
+    w0.get(u);
 #pragma unroll
-    for (int e = 0; e < P; ++e) f[e] = mul_p(f[e], u[e]);
-    get_pairs<W>(w1, u);
+    for (int e = 0; e < W; ++e) f[e] = __fmul_rn(f[e], u[e]);
+    w1.get(u);
 #pragma unroll
-    for (int e = 0; e < P; ++e) g[e] = mul_p(g[e], u[e]);
+    for (int e = 0; e < W; ++e) g[e] = __fmul_rn(g[e], u[e]);
   }
   if (l.half) {
+    const float4 *cs = reinterpret_cast<const float4 *>(row + l.o0);
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      const Pair c = pair(cs[e].x, cs[e].z), n = pair(cs[e].y, cs[e].w), m = pair(-cs[e].y, -cs[e].w);
-      const Pair u = fma_p(f[e], c, mul_p(g[e], m));
-      g[e] = fma_p(g[e], c, mul_p(f[e], n));
-      f[e] = u;
+    for (int e = 0; e < W; e += 2) {
+      const float4 t = cs[e / 2];
+      turn(f[e], g[e], t.x, t.y);
+      turn(f[e + 1], g[e + 1], t.z, t.w);
     }
   }
   if (l.first) {
+    const float4 *cs = reinterpret_cast<const float4 *>(row + l.o0 / 2);
 #pragma unroll
-    for (int e = 0; e < P; e += 2) {
-      f[e] = turn_inner(f[e], cs[e / 2].x, cs[e / 2].y);
-      f[e + 1] = turn_inner(f[e + 1], cs[e / 2].z, cs[e / 2].w);
+    for (int e = 0; e < W; e += 4) {
+      const float4 t = cs[e / 4];
+      turn(f[e], f[e + 1], t.x, t.y);
+      turn(f[e + 2], f[e + 3], t.z, t.w);
     }
   }
   if (l.second) {
+    const float4 *cs = reinterpret_cast<const float4 *>(row + l.o1 / 2);
 #pragma unroll
-    for (int e = 0; e < P; e += 2) {
-      g[e] = turn_inner(g[e], cs[(P + e) / 2].x, cs[(P + e) / 2].y);
-      g[e + 1] = turn_inner(g[e + 1], cs[(P + e) / 2].z, cs[(P + e) / 2].w);
+    for (int e = 0; e < W; e += 4) {
+      const float4 t = cs[e / 4];
+      turn(g[e], g[e + 1], t.x, t.y);
+      turn(g[e + 2], g[e + 3], t.z, t.w);
     }
   }
-  set_pairs<W>(p, f);
-  set_pairs<W>(q, g);
+  const float r = rsqrtf(__fmaf_rn(all, inv_d, eps));
+#pragma unroll
+  for (int e = 0; e < W; ++e) f[e] = __fmul_rn(f[e], r), g[e] = __fmul_rn(g[e], r);
+  p.set(f);
+  q.set(g);
 }
 
-// Where a token of a segment goes and its table row; false: it is skipped.
-// With at the token's position and slot (0 where there is none).
-template <class Raw>
-__device__ __forceinline__ bool route(const RopeArgs &a, const RopeSeg &s, int64_t t, int64_t slot, int at, bool tell,
-                                      Raw *&d, const float2 *&row) {
-  d = static_cast<Raw *>(s.dst);
-  row = nullptr;
-  if (s.paged) {
-    if (slot < 0) return false;
-    if (slot >= a.num_slots) {
-      if (tell) set_status(a.status, WQ_ERR_INDEX);
-      return false;
-    }
-    // a division of 64 bits takes as long as all the rest of a lane's work
-    const int64_t page = slot >> 32 ? slot / a.page_size : int64_t(uint32_t(slot) / uint32_t(a.page_size));
-    d += page * s.d_page + (slot - page * a.page_size) * s.d_token;
-  } else {
-    d += t * s.d_token;
+// Offset of a token of a segment from its destination's start, and its table
+// row, -1 where there is none; an offset of -1: it is skipped.
+__device__ __forceinline__ void route(const RopeArgs &a, const RopeSeg &s, int64_t t, bool tell, int64_t &off, int &row) {
+  const int64_t slot = s.paged ? a.slots[t] : 0;
+  const bool turned = s.rot || (s.paged && a.rot);
+  row = turned ? a.positions[t] : -1;
+  off = -1;
+  if (slot < 0) return;
+  if (slot >= a.num_slots && s.paged) {
+    if (tell) set_status(a.status, WQ_ERR_INDEX);
+    return;
   }
-  if (s.rot || (s.paged && a.rot)) {
-    if (at < 0 || at >= a.max_pos) {
-      if (tell) set_status(a.status, WQ_ERR_INDEX);
-      return false;
-    }
-    row = reinterpret_cast<const float2 *>(a.table) + int64_t(at) * (a.rot / 2);
+  if (turned && unsigned(row) >= unsigned(a.max_pos)) {
+    if (tell) set_status(a.status, WQ_ERR_INDEX);
+    return;
   }
-  return true;
+  if (!s.paged) {
+    off = t * s.d_token;
+    return;
+  }
+  // a division of 64 bits takes as long as all the rest of a lane's work
+  const int64_t page = slot >> 32 ? slot / a.page_size : int64_t(uint32_t(slot) / uint32_t(a.page_size));
+  off = page * s.d_page + (slot - page * a.page_size) * s.d_token;
 }
 
 // Few tokens: a warp takes one
@@ -241,42 +206,38 @@ __global__ void __launch_bounds__(256) head_norm_vec_kernel(const __grid_constan
     w0 = V::load(weight + l.o0);
     if (l.two) w1 = V::load(weight + l.o1);
   }
-  Raw *d;
-  const float2 *row;
-  if (!route<Raw>(a, s, t, s.paged ? a.slots[t] : 0, a.rot ? a.positions[t] : 0, (threadIdx.x & 31) == 0, d, row))
-    return;  // the same for the whole warp
-  if (h.norm[l.i]) {
-    float4 cs[W / 2];
-    load_turns<W>(l, row, cs);
-    norm_turn<DT>(p, q, w0, w1, weight != nullptr, cs, l, h.inv_d[l.i], h.eps);
-  }
-  d += l.head0 * s.d_head;
+  int64_t off;
+  int row;
+  route(a, s, t, (threadIdx.x & 31) == 0, off, row);
+  if (off < 0) return;  // the same for the whole warp
+  if (h.norm[l.i])
+    norm_turn<DT>(p, q, w0, w1, weight != nullptr,
+                  reinterpret_cast<const float2 *>(a.table) + int64_t(max(row, 0)) * (a.rot / 2), l, h.inv_d[l.i], h.eps);
+  Raw *d = static_cast<Raw *>(s.dst) + off + l.head0 * s.d_head;
   if (on) p.store(d + l.o0);
   if (on && l.two) q.store(d + l.o1);
 }
 
 // Many tokens: a warp keeps its place and walks over the tokens.  Its lanes
-// copy their own vectors of the tokens to come into shared memory (no thread
-// reads another's, so a thread waits for its own copies alone); position and
-// slot are read two tokens ahead and the table row one, which takes their
-// latencies, one after the other, out of a token's way.
-constexpr int STAGES = 4;
+// copy their own vectors of the tokens to come, and the tokens' table rows
+// together, into shared memory.  Where 32 tokens go and which rows they take is
+// found by a lane each, so that neither the chain of loads (slot or position,
+// page or row) nor the divisions stand in a token's way.
+constexpr int STAGES = 3;
 template <class DT, int KH>
-__global__ void __launch_bounds__(256, 2) head_norm_stream_kernel(const __grid_constant__ HeadNormArgs h,
-                                                               const __grid_constant__ Cut cut) {
+__global__ void __launch_bounds__(256, 3) head_norm_stream_kernel(const __grid_constant__ HeadNormArgs h,
+                                                                  const __grid_constant__ Cut cut) {
   using Raw = typename DT::Raw;
   constexpr int W = DT::kVec;
   using V = Vec<DT, W>;
-  extern __shared__ uint4 ring[];  // [STAGES][2 KH][threads]
+  extern __shared__ uint4 ring[];  // [STAGES][2 KH][threads], then [warps][STAGES] table rows
   const RopeArgs &a = h.r;
-  const int warp = threadIdx.x >> 5, own_token = warp / cut.per_token;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, own_token = warp / cut.per_token;
   const int rest = int(blockIdx.y) * 8 + warp - own_token * cut.per_token;
   const int64_t t0 = int64_t(blockIdx.x) * cut.tokens + own_token, by = int64_t(gridDim.x) * cut.tokens;
   if (t0 >= a.T || rest >= cut.per_token) return;  // whole warps
   const Place<W> l(h, cut, rest, KH);
   const RopeSeg &s = a.seg[l.i];
-  const Raw *x = static_cast<const Raw *>(s.src) + t0 * s.s_token + l.head0 * s.s_head;
-  const Raw *none = static_cast<const Raw *>(s.src);  // of copies of nothing
   const Raw *weight = static_cast<const Raw *>(h.weight[l.i]);
   V w0, w1;
   w0.w = w1.w = make_uint4(0, 0, 0, 0);
@@ -287,68 +248,69 @@ __global__ void __launch_bounds__(256, 2) head_norm_stream_kernel(const __grid_c
   bool on[KH];
 #pragma unroll
   for (int k = 0; k < KH; ++k) on[k] = l.live && l.head0 + k * l.side < s.heads;
-  const uint32_t mine = uint32_t(__cvta_generic_to_shared(ring + threadIdx.x)), stage = 2 * KH * blockDim.x * 16;
-  int64_t t_in = t0;
-  uint32_t in = 0;
-  auto copy = [&]() {
-    if (t_in < a.T) {
-#pragma unroll
-      for (int k = 0; k < KH; ++k) {
-        const uint32_t to = mine + in + 2 * k * blockDim.x * 16;
-        const Raw *from = x + k * l.side * s.s_head;
-        cp16(to, on[k] ? from + l.o0 : none, on[k]);
-        cp16(to + blockDim.x * 16, on[k] && l.two ? from + l.o1 : none, on[k] && l.two);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    x += t_in + by < a.T ? by * s.s_token : 0;
-    t_in += by;
-    in = in == (STAGES - 1) * stage ? 0 : in + stage;
-  };
-#pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) copy();
-  auto slot_of = [&](int64_t t) { return s.paged && t < a.T ? a.slots[t] : 0; };
-  auto at_of = [&](int64_t t) { return a.rot && t < a.T ? a.positions[t] : 0; };
-  const bool tell = (threadIdx.x & 31) == 0;
-  int64_t slot = slot_of(t0 + by);
-  int at = at_of(t0 + by);
-  Raw *d;
-  const float2 *row;
-  float4 cs[W / 2], cs_next[W / 2];
-  bool write = route<Raw>(a, s, t0, slot_of(t0), at_of(t0), tell, d, row);
-  if (write && h.norm[l.i]) load_turns<W>(l, row, cs);
-  uint32_t out = 0;
+  const int threads = int(blockDim.x), pieces = h.norm[l.i] ? s.rot / 4 : 0;  // of a table row
+  uint4 *rows = ring + STAGES * 2 * KH * threads + warp * STAGES * (a.rot / 4);
+  const Raw *src = static_cast<const Raw *>(s.src);
+  auto to_smem = [](const uint4 *p) { return uint32_t(__cvta_generic_to_shared(p)); };
 #pragma unroll 1
-  for (int64_t t = t0; t < a.T; t += by) {
-    copy();
-    const int64_t slot_next = slot_of(t + 2 * by);
-    const int at_next = at_of(t + 2 * by);
-    Raw *d_next = nullptr;
-    bool write_next = false;
-    if (t + by < a.T) {
-      write_next = route<Raw>(a, s, t + by, slot, at, tell, d_next, row);
-      if (write_next && h.norm[l.i]) load_turns<W>(l, row, cs_next);
-    }
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-    if (write) {  // the same for the whole warp
-      Raw *to = d + l.head0 * s.d_head;
+  for (int64_t first = t0; first < a.T; first += 32 * by) {
+    // lane j: the j-th token from here on
+    const int64_t ahead = (a.T - first + by - 1) / by;
+    const int n = int(ahead < 32 ? ahead : 32);
+    int64_t off = -1;
+    int row = -1;
+    if (lane < n) route(a, s, first + lane * by, true, off, row);
+    int in = 0;
+    auto copy = [&](int k) {
+      if (k < n) {
+        const int r = __shfl_sync(0xffffffffu, row, k);
+        const Raw *x = src + (first + k * by) * s.s_token + l.head0 * s.s_head;
+        uint4 *to = ring + in * 2 * KH * threads + threadIdx.x;
 #pragma unroll
-      for (int k = 0; k < KH; ++k) {
-        if (__all_sync(0xffffffffu, !on[k])) break;
-        const uint4 *from = ring + threadIdx.x + out / 16 + 2 * k * blockDim.x;
-        V p{from[0]}, q{from[blockDim.x]};
-        if (h.norm[l.i]) norm_turn<DT>(p, q, w0, w1, weight != nullptr, cs, l, h.inv_d[l.i], h.eps);
-        if (on[k]) p.store(to + k * l.side * s.d_head + l.o0);
-        if (on[k] && l.two) q.store(to + k * l.side * s.d_head + l.o1);
+        for (int e = 0; e < KH; ++e) {
+          if (on[e]) {
+            cp16(to_smem(to + 2 * e * threads), x + e * l.side * s.s_head + l.o0, true);
+            if (l.two) cp16(to_smem(to + (2 * e + 1) * threads), x + e * l.side * s.s_head + l.o1, true);
+          }
+        }
+        if (unsigned(r) < unsigned(a.max_pos)) {
+          const float4 *from = reinterpret_cast<const float4 *>(a.table) + int64_t(r) * (a.rot / 4);
+          for (int e = lane; e < pieces; e += 32) cp16(to_smem(rows + in * (a.rot / 4) + e), from + e, true);
+        }
       }
-    }
-    out = out == (STAGES - 1) * stage ? 0 : out + stage;
-    write = write_next;
-    d = d_next;
-    slot = slot_next;
-    at = at_next;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      in = in == STAGES - 1 ? 0 : in + 1;
+    };
+    __syncwarp();
 #pragma unroll
-    for (int e = 0; e < W / 2; ++e) cs[e] = cs_next[e];
+    for (int k = 0; k < STAGES - 1; ++k) copy(k);
+    int out = 0;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+      __syncwarp();  // the row that the next copies replace has been read
+      copy(k + STAGES - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      __syncwarp();
+      const int64_t at = __shfl_sync(0xffffffffu, off, k);
+      if (at >= 0) {
+        Raw *to = static_cast<Raw *>(s.dst) + at + l.head0 * s.d_head;
+        const uint4 *from = ring + out * 2 * KH * threads + threadIdx.x;
+        const float2 *turns = reinterpret_cast<const float2 *>(rows + out * (a.rot / 4));
+#pragma unroll
+        for (int e = 0; e < KH; ++e) {
+          if (__all_sync(0xffffffffu, !on[e])) break;
+          V p, q;
+          p.w = q.w = make_uint4(0, 0, 0, 0);
+          if (on[e]) p.w = from[2 * e * threads];
+          if (on[e] && l.two) q.w = from[(2 * e + 1) * threads];
+          if (h.norm[l.i]) norm_turn<DT>(p, q, w0, w1, weight != nullptr, turns, l, h.inv_d[l.i], h.eps);
+          if (on[e]) p.store(to + e * l.side * s.d_head + l.o0);
+          if (on[e] && l.two) q.store(to + e * l.side * s.d_head + l.o1);
+        }
+      }
+      out = out == STAGES - 1 ? 0 : out + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 
@@ -423,10 +385,10 @@ int launch_vec(const HeadNormArgs &h, cudaStream_t st) {
   const int64_t blocks = (h.r.T + c.tokens - 1) / c.tokens;
   if constexpr (STREAM) {
     auto *k = head_norm_stream_kernel<DT, KH>;
-    const int smem = STAGES * 2 * KH * threads * 16;
+    const int smem = STAGES * (2 * KH * threads * 16 + threads / 32 * h.r.rot * 4);
     static OncePerDevice sized;
-    if (!allow_smem(sized, k, STAGES * 2 * KH * 256 * 16)) return WQ_ERR_LAUNCH;
-    const int64_t most = std::max<int64_t>(1, 2 * 152 / y);  // two blocks an SM
+    if (!allow_smem(sized, k, STAGES * (2 * KH * 256 * 16 + 8 * 512 * 4))) return WQ_ERR_LAUNCH;
+    const int64_t most = std::max<int64_t>(1, 3 * 152 / y);  // three blocks an SM
     k<<<dim3(unsigned(std::min(blocks, most)), y), threads, smem, st>>>(h, c);
   } else {
     head_norm_vec_kernel<DT><<<dim3(unsigned(blocks), y), threads, 0, st>>>(h, c);
@@ -443,7 +405,7 @@ int launch_t(const HeadNormArgs &h, bool vec, cudaStream_t st) {
     lanes += h.r.T * h.r.seg[i].heads * lanes_of(h.r.seg[i], W);
   }
   // walks over tokens once each warp has several
-  if (vec) return lanes > 2 * 2 * 152 * 256 * 3 ? launch_vec<DT, true>(h, st) : launch_vec<DT, false>(h, st);
+  if (vec) return lanes > 2 * 3 * 152 * 256 * 3 ? launch_vec<DT, true>(h, st) : launch_vec<DT, false>(h, st);
   int per_token = 0;
   for (int i = 0; i < h.r.nseg; ++i) per_token += h.r.seg[i].heads;
   const int64_t blocks = (h.r.T * per_token + 7) / 8;
