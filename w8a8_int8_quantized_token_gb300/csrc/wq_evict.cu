@@ -3,28 +3,31 @@
 // Of a sequence's n > budget keys, head by head, the first and the most recent
 // ones stay, and the heaviest of those between.  Two kernels:
 //
-// evict_select_kernel, a block per (sequence, head): the weights' bits are
-// mapped to unsigned keys of the same order, and the key of the last one that
-// stays is found digit by digit from the top (11, 11 and 10 bits: a histogram
-// in shared memory and a scan over its bins for each).  Then every warp counts
-// the larger and the equal keys of its own stretch, a scan over the warps gives
-// each its place, and the places that stay are written in order; of equal keys
-// the first stay.  Counts do not depend on the order of the atomics that take
-// them.
+// evict_select_kernel, a cluster of blocks per (sequence, head), each with a
+// stretch of the keys: the weights' bits are mapped to unsigned keys of the
+// same order, and the key of the last one that stays is found digit by digit
+// from the top.  A digit is a histogram in shared memory, whose bins are added
+// over the cluster, and a scan over them.  As soon as few keys share the digits
+// found so far, which is mostly after the first one, they are gathered and
+// ranked against one another.  Then every warp counts the larger and the equal
+// keys of its own part, the counts before it give each its place, and the
+// places that stay are written in order; of equal keys the first stay.  Neither
+// counts nor ranks depend on the order of the atomics that take them.  Bound by
+// latency: about ten steps with a barrier each (the cluster's between some).
 //
 // evict_move_kernel packs the rows that stay, in their order.  A row goes to a
 // place at or before its own, so in place no row may be written before all
 // rows at or before its place are read.  A block therefore owns some columns of
 // all rows of a (sequence, head) and walks them in order: it reads a stretch of
-// rows, waits for all its threads, and writes it, with the next stretch's reads
-// in flight; later stretches lie behind everything that it writes.  Columns of
-// a row, keys, values and weights are independent and go to different blocks.
-// Into other pages any block may take any rows.  Bound by HBM: rows that move
-// are read once and written once.
+// rows, waits for all its threads, and writes it; later stretches lie behind
+// everything that it writes.  Columns of a row, keys, values and weights are
+// independent and go to different blocks.  Into other pages any block may take
+// any rows.  Bound by HBM: rows that move are read once and written once.
 #include <algorithm>
 
 #include "wq_attn.cuh"
 #include "wq_serve.cuh"
+#include "wq_tc.cuh"
 
 namespace wq {
 namespace {
@@ -33,8 +36,10 @@ using attn::launch_chained;
 using attn::start_next_kernel;
 using attn::wait_last_kernel;
 
-constexpr int NT = 1024, NW = NT / 32;  // threads, warps of the selection
+constexpr int NT = 512, NW = NT / 32;  // threads, warps of the selection
 constexpr int BINS = 2048;
+constexpr int FEW = 512;               // keys that are ranked against one another
+constexpr int MOST_BLOCKS = 8;         // of a cluster
 
 // Unsigned key in the order of the weights: -0 as 0, NaN below everything
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -68,80 +73,174 @@ __device__ __forceinline__ int block_scan(int v, int *part, int &total) {
   return v + (warp ? before : 0);
 }
 
-// STAGED: the weights between the first and the recent keys fit shared memory
+template <class T>
+__device__ __forceinline__ const T *of_block(const T *p, int rank) {
+  T *r;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+  return r;
+}
+
+struct Shared {
+  int hist[BINS];
+  uint2 few[FEW];        // key and place of the block's keys with the digits found
+  uint2 all[FEW];        // of the cluster's
+  int counts[2];         // the block's larger keys, equal keys
+  int part[NW], part2[NW];
+  int taken, digit, need;
+};
+
+// STAGED: a block's stretch of the weights between the first and the recent
+// keys fits shared memory
 template <bool STAGED>
-__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int C) {
   extern __shared__ float staged[];
-  __shared__ int hist[BINS];
-  __shared__ int part[NW], found[2];
-  const int b = int(blockIdx.x) / a.heads, h = int(blockIdx.x) - b * a.heads;
+  __shared__ Shared sm;
+  const int bh = int(blockIdx.x) / C, rank = int(blockIdx.x) - bh * C;
+  const int b = bh / a.heads, h = bh - b * a.heads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   start_next_kernel();
   const int n = length_of(a, b), fresh = min(n, a.budget);
-  if (h == 0 && threadIdx.x == 0) {
+  if (h == 0 && rank == 0 && threadIdx.x == 0) {
     a.new_len[b] = fresh;
     if (n != a.key_len[b]) set_status(a.status, WQ_ERR_INDEX);
   }
+  if (blockIdx.x == 0) {
+    // the sequences with rows to move, for the other kernel
+    int count = 0;
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
+      const int q = b0 + int(threadIdx.x), len = q < a.B ? length_of(a, q) : 0;
+      const bool moves = a.in_place ? len > a.budget : len > 0;
+      int total;
+      const int upto = block_scan(int(moves), sm.part, total);
+      if (moves) a.moving[count + upto] = q;
+      count += total;
+    }
+    if (threadIdx.x == 0) a.moving[0] = count;
+  }
   const float *w = a.w + b * a.w_seq + h * a.w_head;
+  const float *w_row = w;
+  float *w_out = a.w_out == a.w ? nullptr : a.w_out + b * a.o_seq + h * a.o_head;
   int32_t *kept = a.kept + (int64_t(b) * a.heads + h) * a.budget;
-  int2 *map = a.map + (int64_t(b) * a.heads + h) * a.budget;
   // key i goes to place j
-  const bool moves = !a.in_place || n > a.budget;
   auto emit = [&](int j, int i) {
     kept[j] = i;
-    if (moves) {
-      const int at = i / a.page_size, page = a.page_table[b * a.ld_table + at];
-      const bool good = unsigned(page) < unsigned(a.num_pages);
-      if (!good) set_status(a.status, WQ_ERR_INDEX);
-      map[j] = make_int2(good ? page : -1, i - at * a.page_size);
-    }
+    if (w_out) w_out[j] = w_row[i];
   };
-  for (int j = fresh + threadIdx.x; j < a.budget; j += NT) kept[j] = -1;
+  // the cluster's threads share what needs no order
+  const int all0 = rank * NT + int(threadIdx.x), all = C * NT;
+  for (int j = fresh + all0; j < a.budget; j += all) kept[j] = -1;
   if (n <= a.budget) {
-    for (int j = threadIdx.x; j < n; j += NT) emit(j, j);
-    return;
+    for (int j = all0; j < n; j += all) emit(j, j);
+    return;  // the whole cluster
   }
-  const int lo = a.first, hi = n - a.recent, mid = hi - lo;
-  for (int j = threadIdx.x; j < lo; j += NT) emit(j, j);
-  for (int j = threadIdx.x; j < a.recent; j += NT) emit(a.budget - a.recent + j, hi + j);
-  int need = a.budget - a.first - a.recent;  // of the mid keys, fewer than all
+  const int first = a.first, mid = n - a.recent - first;
+  for (int j = all0; j < first; j += all) emit(j, j);
+  for (int j = all0; j < a.recent; j += all) emit(a.budget - a.recent + j, n - a.recent + j);
+  int need = a.budget - first - a.recent;  // of the mid keys, fewer than all
   if (need == 0) return;
-  auto at = [&](int i) { return key_of(STAGED ? staged[i] : w[lo + i]); };
+  // this block's stretch
+  const int per = (mid + C - 1) / C, lo = min(rank * per, mid), size = min(per, mid - lo);
+  w += first + lo;
+  auto at = [&](int i) { return key_of(STAGED ? staged[i] : w[i]); };
+  auto together = [&]() {  // all blocks of the cluster, or this one
+    if (C > 1) tc::cluster_sync();
+    else __syncthreads();
+  };
   uint32_t prefix = 0;
+  int left = mid;  // keys that begin with prefix
+  int bits_left = 32;
 #pragma unroll 1
-  for (int digit = 0; digit < 3; ++digit) {
-    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
-    for (int i = threadIdx.x; i < BINS; i += NT) hist[i] = 0;
+  for (int digit = 0; digit < 3 && left > FEW; ++digit) {
+    const int bits = digit == 2 ? 10 : 11, shift = bits_left - bits;
+    for (int i = threadIdx.x; i < BINS; i += NT) sm.hist[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < mid; i += NT) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < size; i += NT) {
       uint32_t k;
       if (STAGED && digit == 0) {
-        const float f = w[lo + i];
+        const float f = w[i];
         staged[i] = f;
         k = key_of(f);
       } else {
         k = at(i);
       }
-      if (digit == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+      if (digit == 0 || (k >> bits_left) == prefix) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1)], 1);
     }
-    __syncthreads();
-    // bins from the top: thread t has the t-th pair
-    const int top = BINS - 1 - 2 * int(threadIdx.x), h1 = hist[top], h0 = hist[top - 1];
+    together();
+    // bins from the top, over the cluster: thread t has the t-th four
+    const int top = BINS - 4 - 4 * int(threadIdx.x);
+    int4 c = make_int4(0, 0, 0, 0);
+    for (int r = 0; r < C; ++r) {
+      const int4 v = *reinterpret_cast<const int4 *>(of_block(&sm.hist[top], r));
+      c.x += v.x;
+      c.y += v.y;
+      c.z += v.z;
+      c.w += v.w;
+    }
+    const int own = c.x + c.y + c.z + c.w;
     int total;
-    const int upto = block_scan(h0 + h1, part, total);
-    const int above = upto - h0 - h1;
+    const int upto = block_scan(own, sm.part, total);
+    int above = upto - own;
     if (above < need && need <= upto) {  // one thread
-      const bool upper = need <= above + h1;
-      found[0] = upper ? top : top - 1;
-      found[1] = need - (upper ? above : above + h1);
+      int d = top + 3, in = c.w;
+      if (above + in < need) above += in, --d, in = c.z;
+      if (above + in < need) above += in, --d, in = c.y;
+      if (above + in < need) above += in, --d, in = c.x;
+      sm.digit = d;
+      sm.need = need - above;
+      sm.taken = in;
+    }
+    together();  // the others have read this block's bins
+    prefix = digit == 0 ? uint32_t(sm.digit) : (prefix << bits) | uint32_t(sm.digit);
+    need = sm.need;  // of the keys that begin with prefix
+    left = sm.taken;
+    bits_left = shift;
+    __syncthreads();
+  }
+  if (bits_left > 0) {
+    // few are left: rank them
+    if (threadIdx.x == 0) sm.taken = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < size; i += NT) {
+      uint32_t k;
+      if (STAGED && bits_left == 32) {
+        const float f = w[i];
+        staged[i] = f;
+        k = key_of(f);
+      } else {
+        k = at(i);
+      }
+      if (bits_left == 32 || (k >> bits_left) == prefix) sm.few[atomicAdd(&sm.taken, 1)] = make_uint2(k, uint32_t(lo + i));
+    }
+    together();
+    int from = 0;
+    for (int r = 0; r < C; ++r) {
+      const int c = *of_block(&sm.taken, r);
+      for (int i = threadIdx.x; i < c; i += NT) sm.all[from + i] = of_block(sm.few, r)[i];
+      from += c;
     }
     __syncthreads();
-    prefix = digit == 0 ? uint32_t(found[0]) : (prefix << bits) | uint32_t(found[0]);
-    need = found[1];  // of the keys that begin with prefix
+    // the one that need - 1 others come before (larger, or equal and earlier)
+    for (int i = threadIdx.x; i < left; i += NT) {
+      const uint2 x = sm.all[i];
+      int before = 0, larger = 0;
+      for (int j = 0; j < left; ++j) {
+        const uint2 y = sm.all[j];
+        larger += y.x > x.x;
+        before += y.x > x.x || (y.x == x.x && y.y < x.y);
+      }
+      if (before == need - 1) {
+        sm.digit = int(x.x);
+        sm.need = need - larger;
+      }
+    }
+    together();  // the others have read this block's few
+    prefix = uint32_t(sm.digit);
+    need = sm.need;  // of the keys equal to prefix
   }
   // keys above `prefix` stay, and the first `need` of those equal to it
-  const int stretch = ((mid + NW - 1) / NW + 31) / 32 * 32;
-  const int s0 = min(warp * stretch, mid), s1 = min(s0 + stretch, mid);
+  const int stretch = ((size + NW - 1) / NW + 31) / 32 * 32;
+  const int s0 = min(warp * stretch, size), s1 = min(s0 + stretch, size);
   int more = 0, same = 0;
   for (int i = s0 + lane; i < s1; i += 32) {
     const uint32_t k = at(i);
@@ -152,11 +251,24 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     more += __shfl_xor_sync(0xffffffffu, more, o);
     same += __shfl_xor_sync(0xffffffffu, same, o);
   }
+  if (lane == 0) sm.part[warp] = more, sm.part2[warp] = same;
   __syncthreads();
-  if (lane == 0) hist[warp] = more, hist[NW + warp] = same;
-  __syncthreads();
-  int j = lo, equal = 0;
-  for (int v = 0; v < warp; ++v) j += hist[v], equal += hist[NW + v];
+  if (warp == 0) {
+    int m = lane < NW ? sm.part[lane] : 0, e = lane < NW ? sm.part2[lane] : 0;
+    for (int o = 16; o > 0; o >>= 1) {
+      m += __shfl_xor_sync(0xffffffffu, m, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    if (lane == 0) sm.counts[0] = m, sm.counts[1] = e;
+  }
+  together();
+  int j = first, equal = 0;
+  for (int r = 0; r < rank; ++r) {
+    const int *c = of_block(sm.counts, r);
+    j += c[0];
+    equal += c[1];
+  }
+  for (int v = 0; v < warp; ++v) j += sm.part[v], equal += sm.part2[v];
   j += min(equal, need);
   for (int i0 = s0; i0 < s1; i0 += 32) {
     const int i = i0 + lane;
@@ -164,106 +276,111 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a) {
     const uint32_t eq = __ballot_sync(0xffffffffu, i < s1 && k == prefix), below = (1u << lane) - 1u;
     const bool stays = i < s1 && (k > prefix || (k == prefix && equal + __popc(eq & below) < need));
     const uint32_t st = __ballot_sync(0xffffffffu, stays);
-    if (stays) emit(j + __popc(st & below), lo + i);
+    if (stays) emit(j + __popc(st & below), first + lo + i);
     j += __popc(st);
     equal += __popc(eq);
   }
+  if (C > 1) tc::cluster_sync();  // the others have read this block's counts
 }
 
-// One tensor's columns that a block moves
+constexpr int MT = 256, MU = 8;  // threads of a moving block, rows of a thread a stretch
+
+// Columns c0 .. c0 + cols of one tensor's rows of a (sequence, head)
 template <class V>
-__device__ __forceinline__ void move_rows(const EvictArgs &a, const V *src, V *dst, int64_t s_page, int64_t s_row,
-                                          int64_t d_page, int64_t d_row, int c0, int cols, int b, int h, int rows,
-                                          int rb) {
-  constexpr int U = 4;
-  const int side = 256 / cols, row = int(threadIdx.x) / cols, col = c0 + int(threadIdx.x) - row * cols;
+__device__ __forceinline__ void move_rows(const EvictArgs &a, V *cache, int64_t pitch_page, int64_t pitch_row, int c0,
+                                          int cols, int b, int h, int rows, int rb) {
+  const int side = MT / cols, row = int(threadIdx.x) / cols, col = c0 + int(threadIdx.x) - row * cols;
   const bool live = row < side;
-  const int R = side * U;
-  const int2 *map = a.map + (int64_t(b) * a.heads + h) * a.budget;
   const int32_t *kept = a.kept + (int64_t(b) * a.heads + h) * a.budget;
-  const int32_t *out = a.out_table + b * a.ld_out;
-  V v[U], x[U];
-  bool on[U], nx[U];
-  auto load = [&](int j0, V(&to)[U], bool(&is)[U]) {
+  const int32_t *in = a.page_table + b * a.ld_table, *out = a.out_table + b * a.ld_out;
+  const int R = side * MU;
+  cache += col;
+  for (int j0 = rb * R; j0 < rows; j0 += R * a.row_blocks) {
+    V v[MU];
+    int from[MU], page[MU];  // key and its page; then, where it goes to
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < MU; ++u) {
       const int j = j0 + u * side + row;
-      is[u] = false;
-      if (!live || j >= rows) continue;
-      const int2 m = map[j];
-      is[u] = m.x >= 0 && !(a.in_place && kept[j] == j);
-      if (is[u]) to[u] = src[m.x * s_page + m.y * s_row + col];
+      from[u] = live && j < rows ? kept[j] : -1;
+      if (a.in_place && from[u] == j) from[u] = -1;
     }
-  };
-  const int step = R * a.row_blocks;
-  load(rb * R, v, on);
-  for (int j0 = rb * R; j0 < rows; j0 += step) {
-    load(j0 + step, x, nx);
+#pragma unroll
+    for (int u = 0; u < MU; ++u) {
+      if (from[u] < 0) continue;
+      const int p = from[u] / a.page_size;
+      from[u] -= p * a.page_size;  // the place in its page
+      page[u] = in[p];
+      if (unsigned(page[u]) >= unsigned(a.num_pages)) {
+        set_status(a.status, WQ_ERR_INDEX);
+        from[u] = -1;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < MU; ++u)
+      if (from[u] >= 0) v[u] = cache[page[u] * pitch_page + from[u] * pitch_row];
+#pragma unroll
+    for (int u = 0; u < MU; ++u) {
+      if (from[u] < 0) continue;
+      const int j = j0 + u * side + row, p = j / a.page_size;
+      page[u] = out[p];
+      from[u] = j - p * a.page_size;
+      if (unsigned(page[u]) >= unsigned(a.num_pages)) {
+        set_status(a.status, WQ_ERR_INDEX);
+        from[u] = -1;
+      }
+    }
     if (a.in_place) __syncthreads();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (on[u]) {
-        const int j = j0 + u * side + row, at = j / a.page_size, page = out[at];
-        if (unsigned(page) < unsigned(a.num_pages)) dst[page * d_page + (j - at * a.page_size) * d_row + col] = v[u];
-        else set_status(a.status, WQ_ERR_INDEX);
-      }
-      on[u] = nx[u];
-      v[u] = x[u];
+    for (int u = 0; u < MU; ++u)
+      if (from[u] >= 0) cache[page[u] * pitch_page + from[u] * pitch_row] = v[u];
+  }
+}
+
+// Weights in place, in one walk
+__device__ __forceinline__ void move_weights(const EvictArgs &a, int b, int h, int rows) {
+  float *w = a.w_out + b * a.w_seq + h * a.w_head;
+  const int32_t *kept = a.kept + (int64_t(b) * a.heads + h) * a.budget;
+  for (int j0 = 0; j0 < rows; j0 += MT * MU) {
+    float v[MU];
+#pragma unroll
+    for (int u = 0; u < MU; ++u) {
+      const int j = j0 + u * MT + int(threadIdx.x);
+      if (j < rows) v[u] = w[kept[j]];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < MU; ++u) {
+      const int j = j0 + u * MT + int(threadIdx.x);
+      if (j < rows) w[j] = v[u];
     }
   }
 }
 
+// Blocks that walk over the items of the sequences with rows to move
 template <class V>
-__global__ void __launch_bounds__(256) evict_move_kernel(const EvictArgs a) {
+__global__ void __launch_bounds__(MT, 3) evict_move_kernel(const EvictArgs a) {
   constexpr int E = sizeof(V) / 2;  // elements of a vector
-  const int bh = int(blockIdx.x / unsigned(a.row_blocks)), rb = int(blockIdx.x % unsigned(a.row_blocks));
-  const int b = bh / a.heads, h = bh - b * a.heads;
-  const int n = length_of(a, b), rows = min(n, a.budget);
   wait_last_kernel();  // in every block: what follows may rely on the selection too
-  if (a.in_place && n <= a.budget && a.w_out == a.w) return;
-  int part = int(blockIdx.y);
-  if (part == 0) {  // weights
-    const int blocks = a.w_out == a.w ? 1 : a.row_blocks;  // one walk in place
-    if (rb >= blocks) return;
-    const float *w = a.w + b * a.w_seq + h * a.w_head;
-    float *to = a.w_out + b * a.o_seq + h * a.o_head;
-    const int32_t *kept = a.kept + (int64_t(b) * a.heads + h) * a.budget;
-    constexpr int U = 4;
-    float v[U], x[U];
-    const int step = 256 * U * blocks;
-    auto load = [&](int j0, float(&t)[U]) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * 256 + int(threadIdx.x);
-        if (j < rows) t[u] = w[kept[j]];
-      }
-    };
-    load(rb * 256 * U, v);
-    for (int j0 = rb * 256 * U; j0 < rows; j0 += step) {
-      load(j0 + step, x);
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * 256 + int(threadIdx.x);
-        if (j < rows) to[j] = v[u];
-        v[u] = x[u];
-      }
+  const int per_head = (a.k_parts + a.v_parts) * a.row_blocks + int(a.w_out == a.w);
+  const int64_t items = int64_t(a.moving[0]) * a.heads * per_head;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t bh = it / per_head;
+    int part = int(it - bh * per_head);
+    const int b = a.moving[1 + bh / a.heads], h = int(bh % a.heads), rows = min(length_of(a, b), a.budget);
+    if (part == (a.k_parts + a.v_parts) * a.row_blocks) {
+      move_weights(a, b, h, rows);
+      continue;
     }
-    return;
-  }
-  if (a.in_place && n <= a.budget) return;
-  --part;
-  if (part < a.k_parts) {
-    const int per = (a.dk / E + a.k_parts - 1) / a.k_parts, c0 = part * per, cols = min(per, a.dk / E - c0);
-    if (cols > 0)
-      move_rows<V>(a, reinterpret_cast<const V *>(a.k + h * a.k_head), reinterpret_cast<V *>(a.k + h * a.k_head),
-                   a.k_page / E, a.k_token / E, a.k_page / E, a.k_token / E, c0, cols, b, h, rows, rb);
-  } else {
-    part -= a.k_parts;
-    const int per = (a.dv / E + a.v_parts - 1) / a.v_parts, c0 = part * per, cols = min(per, a.dv / E - c0);
-    if (cols > 0)
-      move_rows<V>(a, reinterpret_cast<const V *>(a.v + h * a.v_head), reinterpret_cast<V *>(a.v + h * a.v_head),
-                   a.v_page / E, a.v_token / E, a.v_page / E, a.v_token / E, c0, cols, b, h, rows, rb);
+    const int rb = part % a.row_blocks;
+    part /= a.row_blocks;
+    const bool keys = part < a.k_parts;
+    if (!keys) part -= a.k_parts;
+    const int all = (keys ? a.dk : a.dv) / E, parts = keys ? a.k_parts : a.v_parts;
+    const int per = (all + parts - 1) / parts, c0 = part * per, cols = min(per, all - c0);
+    if (cols <= 0) continue;
+    uint16_t *cache = keys ? a.k + h * a.k_head : a.v + h * a.v_head;
+    move_rows<V>(a, reinterpret_cast<V *>(cache), (keys ? a.k_page : a.v_page) / E, (keys ? a.k_token : a.v_token) / E,
+                 c0, cols, b, h, rows, rb);
   }
 }
 
@@ -271,46 +388,52 @@ template <class V>
 int launch_move(EvictArgs a, cudaStream_t st) {
   constexpr int E = sizeof(V) / 2;
   const int64_t bh = int64_t(a.B) * a.heads;
-  // Columns in place: four blocks for keys and four for values at least, since
-  // most sequences of a batch may have nothing to move; 32 bytes or more each.
+  // In place: columns of 32 bytes a block.  Into other pages: whole rows, those
+  // of a (sequence, head) over several blocks.
   auto parts = [&](int cols) {
-    const int64_t least = (cols + 255) / 256, most = std::max<int64_t>(least, cols * int64_t(sizeof(V)) / 32);
-    return int(a.in_place ? std::min(std::max<int64_t>({least, 4, 2432 / bh}), most) : least);
+    const int least = (cols + MT - 1) / MT;
+    return a.in_place ? std::max(least, cols * int(sizeof(V)) / 32) : least;
   };
   a.k_parts = parts(a.dk / E);
   a.v_parts = parts(a.dv / E);
-  // Into other pages: rows of a (sequence, head) over several blocks
-  const int64_t side = std::max(1, 256 / std::max(std::min(a.dk, a.dv) / E, 1)) * 4;
-  a.row_blocks = int(a.in_place ? 1 : std::min((a.budget + side - 1) / side, std::max<int64_t>(1, 4864 / (2 * bh))));
-  if (bh * a.row_blocks >= (int64_t(1) << 31) || a.k_parts + a.v_parts >= 65535) return WQ_ERR_UNSUPPORTED;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(bh * a.row_blocks), unsigned(1 + a.k_parts + a.v_parts));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_move_kernel<V>, a) != cudaSuccess) return WQ_ERR_LAUNCH;
-  return launched(1);
+  const int R = std::max(1, MT / std::max(std::min(a.dk, a.dv) / E, 1)) * MU;
+  a.row_blocks = a.in_place ? 1 : (a.budget + R - 1) / R;
+  if (int64_t(a.k_parts + a.v_parts) * a.row_blocks >= (int64_t(1) << 30)) return WQ_ERR_UNSUPPORTED;
+  const int64_t items = bh * (int64_t(a.k_parts + a.v_parts) * a.row_blocks + 1);
+  return launch_chained(evict_move_kernel<V>, unsigned(std::min<int64_t>(items, 3 * 152)), MT, 0, true, st, a);
 }
 
-constexpr int kStaged = 48 * 1024;  // weights that shared memory holds
+template <bool STAGED>
+int launch_select(const EvictArgs &a, int C, int smem, cudaStream_t st) {
+  auto *k = evict_select_kernel<STAGED>;
+  static OncePerDevice sized;
+  if (!allow_smem(sized, k, STAGED ? 200 * 1024 : 1024)) return WQ_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.heads * C));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(C);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, k, a, C) != cudaSuccess) return WQ_ERR_LAUNCH;
+  return launched(1);
+}
 
 }  // namespace
 
 int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st) {
+  // Blocks of a (sequence, head): enough for about 4096 keys each, while there
+  // are SMs for them
   const int64_t bh = int64_t(a.B) * a.heads;
-  if (bh >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
-  if (a.max_len <= kStaged) {
-    static OncePerDevice sized;
-    if (!allow_smem(sized, evict_select_kernel<true>, kStaged * 4)) return WQ_ERR_LAUNCH;
-    evict_select_kernel<true><<<unsigned(bh), NT, size_t(a.max_len) * 4, st>>>(a);
-  } else {
-    evict_select_kernel<false><<<unsigned(bh), NT, 0, st>>>(a);
-  }
-  const int rc = launched(1);
+  int C = 1;
+  while (C < MOST_BLOCKS && a.max_len > 4096 * C && 2 * C * bh <= 152) C *= 2;
+  if (bh * C >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
+  const int64_t stretch = (int64_t(a.max_len) + C - 1) / C * 4;
+  const int rc = stretch <= 200 * 1024 ? launch_select<true>(a, C, int(stretch), st) : launch_select<false>(a, C, 0, st);
   if (rc != WQ_OK) return rc;
   return vec ? launch_move<uint4>(a, st) : launch_move<uint16_t>(a, st);
 }

@@ -266,8 +266,8 @@ struct EvictArgs {
   int64_t o_seq, o_head;
   int32_t *new_len, *kept;
   int32_t *status;
-  int2 *map;  // [B][heads][budget]: page and place of the keys that stay
-  // of the moving kernel: blocks of columns of keys and of values, of rows
+  int32_t *moving;  // sequences with rows to move: their number, then each
+  // of the moving kernel: parts of the columns of keys and of values, of the rows
   int k_parts, v_parts, row_blocks;
 };
 int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st);
