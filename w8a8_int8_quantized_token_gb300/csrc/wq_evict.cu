@@ -81,12 +81,12 @@ __device__ __forceinline__ const T *of_block(const T *p, int rank) {
 }
 
 struct Shared {
-  int hist[BINS];
+  int hist[2][BINS];     // of digits in turn: a block may be a digit ahead of one that reads its bins
   uint2 few[FEW];        // key and place of the block's keys with the digits found
   uint2 all[FEW];        // of the cluster's
   int counts[2];         // the block's larger keys, equal keys
   int part[NW], part2[NW];
-  int taken, digit, need;
+  int taken, left, digit, need;
 };
 
 // STAGED: a block's stretch of the weights between the first and the recent
@@ -146,36 +146,55 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
     if (C > 1) tc::cluster_sync();
     else __syncthreads();
   };
+  for (int i = threadIdx.x; i < 2 * BINS; i += NT) sm.hist[0][i] = 0;
+  if (threadIdx.x == 0) sm.taken = 0;
+  __syncthreads();
   uint32_t prefix = 0;
   int left = mid;  // keys that begin with prefix
   int bits_left = 32;
 #pragma unroll 1
   for (int digit = 0; digit < 3 && left > FEW; ++digit) {
     const int bits = digit == 2 ? 10 : 11, shift = bits_left - bits;
-    for (int i = threadIdx.x; i < BINS; i += NT) sm.hist[i] = 0;
-    __syncthreads();
-#pragma unroll 4
-    for (int i = threadIdx.x; i < size; i += NT) {
-      uint32_t k;
-      if (STAGED && digit == 0) {
-        const float f = w[i];
-        staged[i] = f;
-        k = key_of(f);
-      } else {
-        k = at(i);
+    int *hist = sm.hist[digit & 1];
+    if (digit == 2) {  // the first digit's bins: all have read them before the second's were together
+      for (int i = threadIdx.x; i < BINS; i += NT) hist[i] = 0;
+      __syncthreads();
+    }
+    if (digit == 0) {
+      constexpr int U = 8;
+      for (int i0 = threadIdx.x; i0 < size; i0 += U * NT) {
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i0 + u * NT < size) f[u] = w[i0 + u * NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (i0 + u * NT >= size) break;
+          if (STAGED) staged[i0 + u * NT] = f[u];
+          atomicAdd(&hist[key_of(f[u]) >> shift], 1);
+        }
       }
-      if (digit == 0 || (k >> bits_left) == prefix) atomicAdd(&sm.hist[(k >> shift) & ((1u << bits) - 1)], 1);
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < size; i += NT) {
+        const uint32_t k = at(i);
+        if ((k >> bits_left) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+      }
     }
     together();
     // bins from the top, over the cluster: thread t has the t-th four
     const int top = BINS - 4 - 4 * int(threadIdx.x);
-    int4 c = make_int4(0, 0, 0, 0);
-    for (int r = 0; r < C; ++r) {
-      const int4 v = *reinterpret_cast<const int4 *>(of_block(&sm.hist[top], r));
-      c.x += v.x;
-      c.y += v.y;
-      c.z += v.z;
-      c.w += v.w;
+    int4 c = make_int4(0, 0, 0, 0), v[MOST_BLOCKS];
+#pragma unroll
+    for (int r = 0; r < MOST_BLOCKS; ++r)
+      if (r < C) v[r] = *reinterpret_cast<const int4 *>(of_block(&hist[top], r));
+#pragma unroll
+    for (int r = 0; r < MOST_BLOCKS; ++r) {
+      if (r >= C) break;
+      c.x += v[r].x;
+      c.y += v[r].y;
+      c.z += v[r].z;
+      c.w += v[r].w;
     }
     const int own = c.x + c.y + c.z + c.w;
     int total;
@@ -188,19 +207,17 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
       if (above + in < need) above += in, --d, in = c.x;
       sm.digit = d;
       sm.need = need - above;
-      sm.taken = in;
+      sm.left = in;
     }
-    together();  // the others have read this block's bins
+    __syncthreads();
     prefix = digit == 0 ? uint32_t(sm.digit) : (prefix << bits) | uint32_t(sm.digit);
     need = sm.need;  // of the keys that begin with prefix
-    left = sm.taken;
+    left = sm.left;
     bits_left = shift;
     __syncthreads();
   }
   if (bits_left > 0) {
     // few are left: rank them
-    if (threadIdx.x == 0) sm.taken = 0;
-    __syncthreads();
     for (int i = threadIdx.x; i < size; i += NT) {
       uint32_t k;
       if (STAGED && bits_left == 32) {
@@ -234,7 +251,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
         sm.need = need - larger;
       }
     }
-    together();  // the others have read this block's few
+    __syncthreads();
     prefix = uint32_t(sm.digit);
     need = sm.need;  // of the keys equal to prefix
   }
@@ -268,6 +285,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
     j += c[0];
     equal += c[1];
   }
+  if (C > 1) tc::cluster_arrive();  // the last look at another block
   for (int v = 0; v < warp; ++v) j += sm.part[v], equal += sm.part2[v];
   j += min(equal, need);
   for (int i0 = s0; i0 < s1; i0 += 32) {
@@ -276,11 +294,15 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
     const uint32_t eq = __ballot_sync(0xffffffffu, i < s1 && k == prefix), below = (1u << lane) - 1u;
     const bool stays = i < s1 && (k > prefix || (k == prefix && equal + __popc(eq & below) < need));
     const uint32_t st = __ballot_sync(0xffffffffu, stays);
-    if (stays) emit(j + __popc(st & below), first + lo + i);
+    if (stays) {
+      const int to = j + __popc(st & below);
+      kept[to] = first + lo + i;
+      if (w_out) w_out[to] = STAGED ? staged[i] : w[i];
+    }
     j += __popc(st);
     equal += __popc(eq);
   }
-  if (C > 1) tc::cluster_sync();  // the others have read this block's counts
+  if (C > 1) tc::cluster_wait();  // none looks at this block any more
 }
 
 constexpr int MT = 256, MU = 8;  // threads of a moving block, rows of a thread a stretch

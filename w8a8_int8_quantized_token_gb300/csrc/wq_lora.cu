@@ -78,10 +78,6 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The tokens of this cluster's tile into tok; their adapter, or -1.  Without a
 // list every thread looks at one token: `scratch` holds the adapters of all.
@@ -289,7 +285,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     }
     reinterpret_cast<float4 *>(h)[i] = v;
   }
-  cluster_arrive();  // the others' parts are read
+  tc::cluster_arrive();  // the others' parts are read
   __syncthreads();
   // ---- as operands of the second product, a warp a row at a time
   float *up = reinterpret_cast<float *>(sm + P::OFF_UP);
@@ -395,7 +391,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     if ((bs += P::BB) == b_end) bs -= P::N2 * P::BB;
   }
   wait_group<0>();
-  cluster_wait();  // this block's part has been read by all
+  tc::cluster_wait();  // this block's part has been read by all
 }
 
 // Tokens by adapter, and the tiles: one block.  The order of an adapter's

@@ -255,6 +255,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+// its halves: this block's accesses before, and the others' known to be over
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // arrive (once) on the barrier at this offset in every CTA of `mask` when all
 // prior MMAs of this thread complete
 __device__ __forceinline__ void mma_commit_mc(uint32_t bar, uint16_t mask) {
