@@ -33,30 +33,37 @@ using attn::wait_last_kernel;
 constexpr int NT = 256;
 constexpr int kInline = 256;   // tokens that a cluster looks through itself
 constexpr int kGroupThreads = 1024;
+constexpr int kMostBlocks = 8;  // of a cluster
 
-// BM: tokens of a tile; RP: rank in whole 16s
+// BM: tokens of a tile; RP: rank in whole 16s.  The second product's stages hold
+// rows of B, and for large tiles the columns of y that they go to; they take the
+// first one's place there, while small tiles, whose time is latency, have the
+// first rows of B on their way from the start.
 template <int BM, int RP>
 struct Plan {
+  static constexpr bool LARGE = BM == 64;
   static constexpr int WM = BM / 16, WK = 8 / WM;  // warps along tokens, and along the first product's axis
-  static constexpr int KS = BM == 16 ? 128 : 64;   // elements of x a stage
+  static constexpr int KS = LARGE ? 64 : 128;      // elements of x a stage
   static constexpr int XB = BM * KS * 2, AB = RP * KS * 2;
-  static constexpr int N1 = RP < 128 ? 4 : BM == 16 ? 2 : 3;     // stages of the first product
+  static constexpr int N1 = LARGE ? (RP < 128 ? 5 : 4) : RP < 128 ? 4 : 2;  // stages of the first product
   static constexpr int NC = WK * 32;               // columns of y a stage of the second
   static constexpr int BP = ((RP / 8) | 1) * 16;   // bytes of a row of B in shared memory
-  static constexpr int BB = NC * BP;
-  static constexpr int N2 = RP < 64 ? 4 : RP == 64 ? 3 : BM == 16 ? 2 : 3;      // its stages
+  static constexpr int BB = NC * BP, YB = LARGE ? BM * NC * 2 : 0;
+  static constexpr int N2 = LARGE ? 5 : RP < 64 ? 4 : RP == 64 ? 3 : 2;  // its stages
   static constexpr int HP = BP;                    // bytes of a row of the intermediate
+  static constexpr int RED = WK * BM * RP * 4;     // the warps' sums
   static constexpr int OFF_1 = 0;                  // first product's stages, then the warps' sums and the operands
-  static constexpr int RED = WK * BM * RP * 4;
-  static constexpr int OFF_H = OFF_1 + RED;            // [2][BM] rows: high and low operands
-  static constexpr int S1 = N1 * (XB + AB) > RED + 2 * BM * HP ? N1 * (XB + AB) : RED + 2 * BM * HP;
-  static constexpr int OFF_B = OFF_1 + S1;
-  static constexpr int OFF_P = OFF_B + N2 * BB;        // [BM][RP] float: this block's part
-  static constexpr int OFF_UP = OFF_P + BM * RP * 4;   // [BM] float: the rows' factors
-  static constexpr int OFF_TOK = OFF_UP + BM * 4;      // [BM] int
+  static constexpr int OFF_H = OFF_1 + RED;        // [2][BM] rows: high and low operands
+  static constexpr int S0 = N1 * (XB + AB) > RED + 2 * BM * HP ? N1 * (XB + AB) : RED + 2 * BM * HP;
+  static constexpr int S1 = LARGE && N2 * (BB + YB) > S0 ? N2 * (BB + YB) : S0;
+  static constexpr int OFF_B = LARGE ? 0 : OFF_1 + S1;         // second product's stages: rows of B,
+  static constexpr int OFF_Y = OFF_B + N2 * BB;                // columns of y
+  static constexpr int OFF_P = LARGE ? S1 : OFF_B + N2 * BB;   // [BM][RP] float: this block's part
+  static constexpr int OFF_UP = OFF_P + BM * RP * 4;           // [BM] float: the rows' factors
+  static constexpr int OFF_TOK = OFF_UP + BM * 4;              // [BM] int
   static constexpr int OFF_MISC = OFF_TOK + BM * 4;
   static constexpr int SMEM = OFF_MISC + 64;
-  static_assert(OFF_B >= NT * 4, "scratch of find_tile");
+  static_assert(S1 >= NT * 4, "scratch of find_tile");
   static_assert(SMEM <= 232448, "shared memory plan");
 };
 
@@ -155,10 +162,32 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     const int at = (row & ~31) + ((g >> 1) & 3) * 8 + (g >> 3) * 2 + (g & 1);
     b_to[j] = base + P::OFF_B + uint32_t(at * P::BP + b_piece * 16);
   }
-  uint32_t b_stage = 0;
+  // large tiles: the columns of y, a row's 16-byte pieces where four lanes of
+  // two rows each find theirs in different banks
+  constexpr int NY = P::YB / 16 / NT;
+  const int y_row = threadIdx.x / 8, y_piece = threadIdx.x % 8;
+  uint16_t *y_src[NY > 0 ? NY : 1];
+  if constexpr (P::LARGE) {
+#pragma unroll
+    for (int j = 0; j < NY; ++j) {
+      const int row = y_row + j * (NT / 8);
+      y_src[j] = row < count ? a.y + int64_t(tok[row]) * a.ldy + y_piece * 8 : nullptr;
+    }
+  }
+  const uint32_t y_to = base + P::OFF_Y + uint32_t(y_row * 128 + ((y_piece ^ ((y_row & 1) << 2)) << 4));
+  uint32_t b_stage = 0, y_stage = 0;
   int b_next = c0;
   auto load_b = [&]() {
     if (b_next < c1) {
+      if constexpr (P::LARGE) {
+        const bool in = b_next * P::NC + y_piece * 8 < a.N;
+#pragma unroll
+        for (int j = 0; j < NY; ++j) {
+          const bool on = in && y_src[j];
+          cp16(y_to + y_stage + j * (NT / 8) * 128, on ? y_src[j] + b_next * P::NC : a.y, on);
+        }
+        y_stage = y_stage == (P::N2 - 1) * P::YB ? 0 : y_stage + P::YB;
+      }
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         if (P::NC * BP8 < NT && b_row >= P::NC) break;
@@ -211,8 +240,10 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < P::N1 - 1; ++i) load_x();
+  if constexpr (!P::LARGE) {
 #pragma unroll
-  for (int i = 0; i < P::N2 - 1; ++i) load_b();
+    for (int i = 0; i < P::N2 - 1; ++i) load_b();
+  }
 
   const int wm = warp % P::WM, wk = warp / P::WM;
   float acc[RP / 8][4];
@@ -223,8 +254,8 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   uint32_t xs = base + P::OFF_1;
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
-    // groups of copies in order: x of the first stages, all of B's, then x of one stage a step
-    if (s - s0 < P::N1 - 1) wait_group<P::N1 - 2 + P::N2 - 1>();
+    // groups of copies in order: x of the first stages, small tiles' first of B, then x of one stage a step
+    if (!P::LARGE && s - s0 < P::N1 - 1) wait_group<P::N1 - 2 + P::N2 - 1>();
     else wait_group<P::N1 - 2>();
     __syncthreads();
     load_x();
@@ -275,13 +306,17 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   tc::cluster_sync();
   float *h = red;  // [BM][RP], the whole sum
   for (int i = threadIdx.x; i < BM * RP / 4; i += NT) {
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = 0; c < C; ++c) {
-      const float4 u = ld_cluster4(tc::mapa(base + P::OFF_P, uint32_t(c)) + uint32_t(i * 16));
-      v.x += u.x;
-      v.y += u.y;
-      v.z += u.z;
-      v.w += u.w;
+    float4 u[kMostBlocks], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < kMostBlocks; ++c)
+      if (c < C) u[c] = ld_cluster4(tc::mapa(base + P::OFF_P, uint32_t(c)) + uint32_t(i * 16));
+#pragma unroll
+    for (int c = 0; c < kMostBlocks; ++c) {
+      if (c >= C) break;
+      v.x += u[c].x;
+      v.y += u[c].y;
+      v.z += u[c].z;
+      v.w += u[c].w;
     }
     reinterpret_cast<float4 *>(h)[i] = v;
   }
@@ -334,7 +369,14 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
       if (r1 < count) v1 = V::load(y1 + col);
     }
   };
-  load_y(c0);
+  if constexpr (P::LARGE) {
+    __syncthreads();  // the operands are in registers: their place is the stages' now
+#pragma unroll
+    for (int i = 0; i < P::N2 - 1; ++i) load_b();
+  } else {
+    load_y(c0);
+  }
+  uint32_t ys = P::OFF_Y;
   uint32_t bs = base + P::OFF_B + uint32_t(wk * 32 * P::BP);
   const uint32_t b_end = bs + P::N2 * P::BB;
 #pragma unroll 1
@@ -342,8 +384,15 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     wait_group<P::N2 - 2>();
     __syncthreads();
     load_b();
-    const V o0 = v0, o1 = v1;
-    load_y(c + 1);
+    V o0 = v0, o1 = v1;
+    if constexpr (P::LARGE) {
+      const int at = ((wk * 4 + (lane & 3)) ^ ((r0 & 1) << 2)) << 4;  // r1 = r0 + 8
+      o0 = V{*reinterpret_cast<const uint4 *>(sm + ys + r0 * 128 + at)};
+      o1 = V{*reinterpret_cast<const uint4 *>(sm + ys + r1 * 128 + at)};
+      if ((ys += P::YB) == P::OFF_Y + P::N2 * P::YB) ys = P::OFF_Y;
+    } else {
+      load_y(c + 1);
+    }
     float d[4][4];
 #pragma unroll
     for (int p = 0; p < 4; ++p)
