@@ -36,34 +36,34 @@ constexpr int kGroupThreads = 1024;
 constexpr int kMostBlocks = 8;  // of a cluster
 
 // BM: tokens of a tile; RP: rank in whole 16s.  The second product's stages hold
-// rows of B, and for large tiles the columns of y that they go to; they take the
-// first one's place there, while small tiles, whose time is latency, have the
-// first rows of B on their way from the start.
+// rows of B and the columns of y that they go to.  They take the first one's
+// place, except with small tiles, whose time is latency: those have their first
+// ones on the way from the start.
 template <int BM, int RP>
 struct Plan {
-  static constexpr bool LARGE = BM == 64;
   static constexpr int WM = BM / 16, WK = 8 / WM;  // warps along tokens, and along the first product's axis
-  static constexpr int KS = LARGE ? 64 : 128;      // elements of x a stage
+  static constexpr bool EARLY = BM == 16 && RP < 128;
+  static constexpr int KS = BM == 16 ? 128 : 64;   // elements of x a stage
   static constexpr int XB = BM * KS * 2, AB = RP * KS * 2;
-  static constexpr int N1 = LARGE ? (RP < 128 ? 5 : 4) : RP < 128 ? 4 : 2;  // stages of the first product
+  static constexpr int N1 = BM == 64 && RP < 128 ? 5 : RP < 128 || BM == 64 ? 4 : 2;  // stages of the first product
   static constexpr int NC = WK * 32;               // columns of y a stage of the second
   static constexpr int BP = ((RP / 8) | 1) * 16;   // bytes of a row of B in shared memory
-  static constexpr int BB = NC * BP, YB = LARGE ? BM * NC * 2 : 0;
-  static constexpr int N2 = LARGE ? 5 : RP < 64 ? 4 : RP == 64 ? 3 : 2;  // its stages
+  static constexpr int BB = NC * BP, YB = BM * NC * 2;
+  static constexpr int N2 = BM == 64 ? 5 : RP < 128 ? 3 : 2;  // its stages
   static constexpr int HP = BP;                    // bytes of a row of the intermediate
   static constexpr int RED = WK * BM * RP * 4;     // the warps' sums
   static constexpr int OFF_1 = 0;                  // first product's stages, then the warps' sums and the operands
   static constexpr int OFF_H = OFF_1 + RED;        // [2][BM] rows: high and low operands
   static constexpr int S0 = N1 * (XB + AB) > RED + 2 * BM * HP ? N1 * (XB + AB) : RED + 2 * BM * HP;
-  static constexpr int S1 = LARGE && N2 * (BB + YB) > S0 ? N2 * (BB + YB) : S0;
-  static constexpr int OFF_B = LARGE ? 0 : OFF_1 + S1;         // second product's stages: rows of B,
-  static constexpr int OFF_Y = OFF_B + N2 * BB;                // columns of y
-  static constexpr int OFF_P = LARGE ? S1 : OFF_B + N2 * BB;   // [BM][RP] float: this block's part
-  static constexpr int OFF_UP = OFF_P + BM * RP * 4;           // [BM] float: the rows' factors
-  static constexpr int OFF_TOK = OFF_UP + BM * 4;              // [BM] int
+  static constexpr int S2 = N2 * (BB + YB);
+  static constexpr int OFF_B = EARLY ? S0 : 0;     // second product's stages: rows of B, columns of y
+  static constexpr int OFF_Y = OFF_B + N2 * BB;
+  static constexpr int OFF_P = EARLY ? S0 + S2 : S0 > S2 ? S0 : S2;  // [BM][RP] float: this block's part
+  static constexpr int OFF_UP = OFF_P + BM * RP * 4;                 // [BM] float: the rows' factors
+  static constexpr int OFF_TOK = OFF_UP + BM * 4;                    // [BM] int
   static constexpr int OFF_MISC = OFF_TOK + BM * 4;
   static constexpr int SMEM = OFF_MISC + 64;
-  static_assert(S1 >= NT * 4, "scratch of find_tile");
+  static_assert(S0 >= NT * 4, "scratch of find_tile");
   static_assert(SMEM <= 232448, "shared memory plan");
 };
 
@@ -106,6 +106,12 @@ __device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, 
     id = -1;
   }
   scratch[i] = id;
+  if (a.T == 1) {
+    if (i == 0) tok[0] = 0, misc[0] = id;
+    __syncthreads();
+    count = 1;
+    return misc[0];
+  }
   const uint32_t below = (1u << lane) - 1u;
   int before = __popc(__match_any_sync(0xffffffffu, id) & below);  // tokens of this adapter before
   __syncthreads();
@@ -162,32 +168,28 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     const int at = (row & ~31) + ((g >> 1) & 3) * 8 + (g >> 3) * 2 + (g & 1);
     b_to[j] = base + P::OFF_B + uint32_t(at * P::BP + b_piece * 16);
   }
-  // large tiles: the columns of y, a row's 16-byte pieces where four lanes of
-  // two rows each find theirs in different banks
-  constexpr int NY = P::YB / 16 / NT;
-  const int y_row = threadIdx.x / 8, y_piece = threadIdx.x % 8;
-  uint16_t *y_src[NY > 0 ? NY : 1];
-  if constexpr (P::LARGE) {
+  // the columns of y: four lanes of two rows each find their pieces in different banks
+  constexpr int YP = P::NC / 8, YROWS = NT / YP, NY = P::YB / 16 / NT;  // pieces of a row; rows of a copy; copies
+  const int y_row = threadIdx.x / YP, y_piece = threadIdx.x % YP;
+  uint16_t *y_src[NY];
 #pragma unroll
-    for (int j = 0; j < NY; ++j) {
-      const int row = y_row + j * (NT / 8);
-      y_src[j] = row < count ? a.y + int64_t(tok[row]) * a.ldy + y_piece * 8 : nullptr;
-    }
+  for (int j = 0; j < NY; ++j) {
+    const int row = y_row + j * YROWS;
+    y_src[j] = row < count ? a.y + int64_t(tok[row]) * a.ldy + y_piece * 8 : nullptr;
   }
-  const uint32_t y_to = base + P::OFF_Y + uint32_t(y_row * 128 + ((y_piece ^ ((y_row & 1) << 2)) << 4));
+  static_assert(YROWS % 2 == 0, "a thread's rows lie alike");
+  const uint32_t y_to = base + P::OFF_Y + uint32_t(y_row * (P::NC * 2) + ((y_piece ^ ((y_row & 1) << 2)) << 4));
   uint32_t b_stage = 0, y_stage = 0;
   int b_next = c0;
   auto load_b = [&]() {
     if (b_next < c1) {
-      if constexpr (P::LARGE) {
-        const bool in = b_next * P::NC + y_piece * 8 < a.N;
+      const bool in = b_next * P::NC + y_piece * 8 < a.N;
 #pragma unroll
-        for (int j = 0; j < NY; ++j) {
-          const bool on = in && y_src[j];
-          cp16(y_to + y_stage + j * (NT / 8) * 128, on ? y_src[j] + b_next * P::NC : a.y, on);
-        }
-        y_stage = y_stage == (P::N2 - 1) * P::YB ? 0 : y_stage + P::YB;
+      for (int j = 0; j < NY; ++j) {
+        const bool on = in && y_src[j];
+        cp16(y_to + y_stage + j * YROWS * (P::NC * 2), on ? y_src[j] + b_next * P::NC : a.y, on);
       }
+      y_stage = y_stage == (P::N2 - 1) * P::YB ? 0 : y_stage + P::YB;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         if (P::NC * BP8 < NT && b_row >= P::NC) break;
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   };
 #pragma unroll
   for (int i = 0; i < P::N1 - 1; ++i) load_x();
-  if constexpr (!P::LARGE) {
+  if constexpr (P::EARLY) {
 #pragma unroll
     for (int i = 0; i < P::N2 - 1; ++i) load_b();
   }
@@ -254,8 +256,8 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   uint32_t xs = base + P::OFF_1;
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
-    // groups of copies in order: x of the first stages, small tiles' first of B, then x of one stage a step
-    if (!P::LARGE && s - s0 < P::N1 - 1) wait_group<P::N1 - 2 + P::N2 - 1>();
+    // groups of copies in order: x of the first stages, the second product's first, then x of one stage a step
+    if (P::EARLY && s - s0 < P::N1 - 1) wait_group<P::N1 - 2 + P::N2 - 1>();
     else wait_group<P::N1 - 2>();
     __syncthreads();
     load_x();
@@ -361,20 +363,10 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   uint16_t *y0 = a.y + int64_t(r0 < count ? tok[r0] : 0) * a.ldy, *y1 = a.y + int64_t(r1 < count ? tok[r1] : 0) * a.ldy;
   auto col_of = [&](int c) { return c * P::NC + wk * 32 + (lane & 3) * 8; };
   using V = Vec<DT, 8>;
-  V v0{}, v1{};
-  auto load_y = [&](int c) {
-    const int col = col_of(c);
-    if (c < c1 && col < a.N) {
-      if (r0 < count) v0 = V::load(y0 + col);
-      if (r1 < count) v1 = V::load(y1 + col);
-    }
-  };
-  if constexpr (P::LARGE) {
+  if constexpr (!P::EARLY) {
     __syncthreads();  // the operands are in registers: their place is the stages' now
 #pragma unroll
     for (int i = 0; i < P::N2 - 1; ++i) load_b();
-  } else {
-    load_y(c0);
   }
   uint32_t ys = P::OFF_Y;
   uint32_t bs = base + P::OFF_B + uint32_t(wk * 32 * P::BP);
@@ -384,15 +376,10 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     wait_group<P::N2 - 2>();
     __syncthreads();
     load_b();
-    V o0 = v0, o1 = v1;
-    if constexpr (P::LARGE) {
-      const int at = ((wk * 4 + (lane & 3)) ^ ((r0 & 1) << 2)) << 4;  // r1 = r0 + 8
-      o0 = V{*reinterpret_cast<const uint4 *>(sm + ys + r0 * 128 + at)};
-      o1 = V{*reinterpret_cast<const uint4 *>(sm + ys + r1 * 128 + at)};
-      if ((ys += P::YB) == P::OFF_Y + P::N2 * P::YB) ys = P::OFF_Y;
-    } else {
-      load_y(c + 1);
-    }
+    const int piece = ((wk * 4 + (lane & 3)) ^ ((r0 & 1) << 2)) << 4;  // r1 = r0 + 8
+    const V o0{*reinterpret_cast<const uint4 *>(sm + ys + r0 * (P::NC * 2) + piece)};
+    const V o1{*reinterpret_cast<const uint4 *>(sm + ys + r1 * (P::NC * 2) + piece)};
+    if ((ys += P::YB) == P::OFF_Y + P::N2 * P::YB) ys = P::OFF_Y;
     float d[4][4];
 #pragma unroll
     for (int p = 0; p < 4; ++p)
@@ -569,9 +556,10 @@ int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
     const int rc = launched(1);
     if (rc != WQ_OK) return rc;
   }
-  // Blocks of a tile: as many as let all tiles run at the same time, two blocks an SM
-  int C = 8;
-  while (C > 1 && tiles * C > 2 * 152) C /= 2;
+  // Blocks of a tile: as many as let about all tiles run at the same time, two
+  // blocks an SM (some tiles may not be there)
+  int C = kMostBlocks;
+  while (C > 1 && tiles * C > 2 * 152 * 9 / 8) C /= 2;
   if (dtype == WQ_DT_BF16) return BM == 16 ? launch_rank<Bf16, 16>(a, tiles, C, st) : launch_rank<Bf16, 64>(a, tiles, C, st);
   return BM == 16 ? launch_rank<F16, 16>(a, tiles, C, st) : launch_rank<F16, 64>(a, tiles, C, st);
 }
