@@ -534,7 +534,7 @@ int launch_rank(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
 }
 
 // Tokens of a tile, by their number; tiles at most
-inline int tile_of(int64_t T) { return T <= kInline ? 16 : 64; }
+inline int tile_of(int64_t T) { return T <= kInline ? 16 : 128; }
 inline int64_t tiles_of(int64_t T, int64_t n) { return std::min(T, n + T / tile_of(T)); }
 
 }  // namespace
@@ -554,7 +554,7 @@ int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
     a.order = reinterpret_cast<int *>(p + 16 + tiles * 16);
     lora_group_kernel<<<1, kGroupThreads, size_t(a.n) * 4, st>>>(a, BM);
     const int rc = launched(1);
-    if (rc != WQ_OK) return rc;
+    return rc == WQ_OK ? launch_lora_tiles(a, dtype, tiles, st) : rc;
   }
   // Blocks of a tile: as many as let about all tiles run at the same time, two
   // blocks an SM (some tiles may not be there)

@@ -288,6 +288,7 @@ struct LoraArgs {
   int4 *tiles;
 };
 size_t lora_ws_bytes(int64_t T, int64_t n);
+int launch_lora_tiles(const LoraArgs &a, int dtype, int64_t tiles, cudaStream_t st);
 int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st);
 
 }  // namespace wq
