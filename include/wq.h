@@ -730,12 +730,12 @@ WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
  * of one adapter may stand anywhere.  Adapters of smaller rank are padded with
  * zeros.  Products and sums are float32; x A^T enters the second product with
  * twice the bits of dtype's significand, and y is rounded once.  A row's result
- * depends on its token and T alone, not on the tokens beside it.  y must not
+ * depends on its token, T and n alone, not on the tokens beside it.  y must not
  * overlap the other arguments.
  * Requirements: bf16 or fp16; H, N, r and pitches multiples of 8, r at most 128,
  * n at most 8192, 16-byte aligned tensors.  Workspace:
- * wq_lora_add_workspace_size(T, n) (0 bytes up to 256 tokens). */
-WQ_API size_t wq_lora_add_workspace_size(int64_t T, int n);
+ * wq_lora_add_workspace_size(T, n, r) (0 bytes up to 256 tokens). */
+WQ_API size_t wq_lora_add_workspace_size(int64_t T, int n, int r);
 WQ_API int wq_lora_add(const void *x, int64_t ldx, int64_t T, int64_t H, const void *A,
                        const void *B, const float *scales, int n, int r, const int32_t *adapters,
                        int64_t N, int dtype, void *y, int64_t ldy, void *ws, size_t ws_bytes,

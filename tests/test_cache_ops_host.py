@@ -99,8 +99,9 @@ def test_lora_refusals(lib):
     for kw in (dict(H=60), dict(N=44), dict(r=12), dict(r=136), dict(ldx=68), dict(ldy=52), dict(n=8193), dict(x=FAKE + 2),
                dict(A=FAKE + 8), dict(B=FAKE + 8), dict(y=FAKE + 4), dict(s=FAKE + 2), dict(T=1 << 24)):
         assert call(**kw) == UNSUPPORTED, kw
-    need = lib.wq_lora_add_workspace_size(400, 3)
-    assert need >= 400 * 4 and lib.wq_lora_add_workspace_size(256, 3) == 0 and lib.wq_lora_add_workspace_size(0, 3) == 0
+    need = lib.wq_lora_add_workspace_size(400, 3, 16)
+    assert need >= 400 * 4 + 400 * 16 * 4 and lib.wq_lora_add_workspace_size(256, 3, 16) == 0
+    assert lib.wq_lora_add_workspace_size(0, 3, 16) == 0
     assert call(nb=need - 1) == WORKSPACE and call(ws=None) == WORKSPACE
     for kw in (dict(T=0), dict(H=0), dict(N=0), dict(n=0)):
         assert call(**kw) == 0, kw

@@ -103,7 +103,7 @@ _SIGS = {
     "wq_attention_weights_paged": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _F, _P, _F, _P, _L, _L, _P, _S, _P, _P]),
     "wq_evict_paged_workspace_size": (_S, [_I]),
     "wq_evict_paged": (_I, [_P, _L, _L, _P, _I, _P, _L, _P, _L, _L, _L, _L, _P, _L, _P, _L, _L, _P, _P, _P, _S, _P, _P]),
-    "wq_lora_add_workspace_size": (_S, [_L, _I]),
+    "wq_lora_add_workspace_size": (_S, [_L, _I, _I]),
     "wq_lora_add": (_I, [_P, _L, _L, _L, _P, _P, _P, _I, _I, _P, _L, _I, _P, _L, _P, _S, _P, _P]),
     "wq_moe_forward_masked": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _S, _P, _P]),
 }
@@ -1150,7 +1150,7 @@ def evict_paged(weights, k_cache, v_cache, page_table, key_len, max_len, budget,
 # ---------------------------------------------------------------- adapters beside a projection
 def lora_add_workspace(y, x, A):
     """A workspace for lora_add calls of these sizes."""
-    n = lib().wq_lora_add_workspace_size(x.shape[0], A.shape[0])
+    n = lib().wq_lora_add_workspace_size(x.shape[0], A.shape[0], A.shape[1])
     return torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
 
 
@@ -1174,7 +1174,7 @@ def lora_add(y, x, A, B, adapters, scales=None, ws=None, status=None):
     ids = _dense_as(adapters, (T,), torch.int32, "adapters", dev)
     if scales is not None:
         _dense_as(scales, (n,), torch.float32, "scales", dev)
-    ws, size = _workspace(ws, lambda: lib().wq_lora_add_workspace_size(T, n), dev)
+    ws, size = _workspace(ws, lambda: lib().wq_lora_add_workspace_size(T, n, r), dev)
     _check(lib().wq_lora_add(x.data_ptr(), ldx, T, H, A.data_ptr(), B.data_ptr(), _at(scales), n, r, ids, N, code,
                              y.data_ptr(), ldy, ws.data_ptr(), size, _status(status, dev),
                              _TC._cuda_getCurrentRawStream(dev)), "wq_lora_add")

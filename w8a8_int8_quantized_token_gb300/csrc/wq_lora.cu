@@ -486,7 +486,10 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   }
   for (int i = n0; i < n1; ++i) {
     const int c = cnt[i];
-    for (int k = 0; k < c; k += BM) a.tiles[tile++] = make_int4(i, at + k, min(BM, c - k), 0);
+    for (int k = 0; k < c; k += BM) {
+      a.tickets[tile] = 0;
+      a.tiles[tile++] = make_int4(i, at + k, min(BM, c - k), 0);
+    }
     cnt[i] = at;
     at += c;
   }
@@ -537,21 +540,40 @@ int launch_rank(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
 inline int tile_of(int64_t T) { return T <= kInline ? 16 : 128; }
 inline int64_t tiles_of(int64_t T, int64_t n) { return std::min(T, n + T / tile_of(T)); }
 
+// The workspace of many tokens, from `at` on (0: its size)
+size_t lora_lay_out(LoraArgs &a, char *at) {
+  const int64_t tiles = tiles_of(a.T, a.n), T = a.T, RP = lora_rank(a.r);
+  size_t n = 0;
+  auto take = [&](auto *&p, int64_t count) {
+    p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(at + n);
+    n += (size_t(count) * sizeof(*p) + 15) / 16 * 16;
+  };
+  take(a.ntiles, 1);
+  take(a.tiles, tiles);
+  take(a.tickets, tiles);
+  take(a.order, T);
+  take(a.factors, T);
+  take(a.operands, T * RP);
+  take(a.parts, lora_slices(tiles) * T * RP);
+  return n;
+}
+
 }  // namespace
 
-size_t lora_ws_bytes(int64_t T, int64_t n) {
+size_t lora_ws_bytes(int64_t T, int64_t n, int r) {
   if (T <= kInline) return 0;
-  return 16 + size_t(tiles_of(T, n)) * 16 + size_t(T) * 4;
+  LoraArgs a{};
+  a.T = int(T);
+  a.n = int(n);
+  a.r = r;
+  return lora_lay_out(a, nullptr);
 }
 
 int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
   const int BM = tile_of(a.T);
   const int64_t tiles = tiles_of(a.T, a.n);
   if (a.T > kInline) {
-    char *p = static_cast<char *>(ws);
-    a.ntiles = reinterpret_cast<int *>(p);
-    a.tiles = reinterpret_cast<int4 *>(p + 16);
-    a.order = reinterpret_cast<int *>(p + 16 + tiles * 16);
+    lora_lay_out(a, static_cast<char *>(ws));
     lora_group_kernel<<<1, kGroupThreads, size_t(a.n) * 4, st>>>(a, BM);
     const int rc = launched(1);
     return rc == WQ_OK ? launch_lora_tiles(a, dtype, tiles, st) : rc;

@@ -1,28 +1,26 @@
-// Low-rank adapters for many tokens (tcgen05, sm_103a): a cluster of blocks
-// takes 128 tokens of one adapter.
+// Low-rank adapters for many tokens (tcgen05, sm_103a), 128 of one adapter a
+// tile, in two kernels:
 //
-//   H = x A^T (128 x r),  y += s H B^T (128 x N)
+//   lora_down_kernel  H = x A^T (128 x r), the long axis cut into slices, whose
+//                     parts go to the workspace in float32; the last block of a
+//                     tile adds them, in the order of the slices
+//   lora_up_kernel    y += s H B^T (128 x N), a stretch of columns a block, 64 at a
+//                     time
 //
-// Each block multiplies its slice of x and A into tensor memory, the blocks'
-// parts of H are added through distributed shared memory in the order of the
-// blocks, and each block multiplies the sum with its slice of B's rows and adds
-// the result to its columns of y, 64 at a time.
-//   warps 0-3  H's sum, y: a thread owns a token
-//   warps 4-7  copies into one ring of stages: x and A, then B and y; they run
-//              ahead into the second product while H is being added
-//   warp 8     MMA issue; owns the tensor memory
-// H enters the second product from tensor memory as two 16-bit operands, its
-// rounding and what that leaves, as in the kernel for few tokens; a token's
-// thread holds the whole row, so fp16's factor costs nothing but the maximum.
+// One kernel for both, whose blocks shared a tile in a cluster and added the
+// parts through distributed shared memory, took 89 us at 8192 tokens of width
+// 7168 and rank 64: the sum held each block up for 10 us.
 //
-// Tokens of an adapter lie anywhere, so rows of x and y are copied by 16-byte
-// pieces (eight lanes a row), which land in the products' swizzled layout.
-// Bound by HBM: two blocks share an SM, so that one's sum over the cluster
-// passes in the other's copies.
+// Blocks have warps that copy, one that issues the products, and warps that own
+// a token a thread.  Tokens of an adapter lie anywhere, so rows of x and y are
+// copied by 16-byte pieces (eight lanes a row), which land in the products'
+// swizzled layout.  H enters the second product from tensor memory as two 16-bit
+// operands, its rounding and what that leaves, as in the kernel for few tokens.
+// Bound by HBM: x once, y twice; the adapters come from L2.
 //
 // Every wait on a memory barrier is bounded (1 s); on expiry the kernel records
 // WQ_ERR_TIMEOUT, waits (bounded) for its own copies and MMAs, frees tensor
-// memory and exits; the cluster's barriers are served whatever the waits said.
+// memory and exits.
 #include <algorithm>
 #include <type_traits>
 
@@ -36,31 +34,8 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128, KS = 64, NC = 64;  // tokens; elements of x, columns of y a stage
-constexpr int THREADS = 288, WARP_COPY = 4, WARP_MMA = 8;
-constexpr int MOST_BLOCKS = 8;             // of a cluster
-
-template <int RP>
-struct Plan {
-  static constexpr int XB = BM * 128, AB = RP * 128;                  // a first product's stage
-  static constexpr int BB = (RP + 63) / 64 * NC * 128, YB = BM * 128; // a second one's
-  static constexpr int STAGE = XB + AB > BB + YB ? XB + AB : BB + YB;
-  static constexpr int NS = RP == 16 ? 4 : 3;
-  static constexpr int OFF_P = NS * STAGE;          // [BM][RP] float: parts of H, then its operands
-  static constexpr int OFF_UP = OFF_P + BM * RP * 4;  // [BM] float: the rows' factors
-  static constexpr int OFF_TOK = OFF_UP + BM * 4;
-  static constexpr int OFF_BAR = OFF_TOK + BM * 4;
-  static constexpr int B_FULL = 0, B_EMPTY = NS, B_D1 = 2 * NS, B_H = B_D1 + 1, B_D2_FULL = B_H + 1,
-                       B_D2_EMPTY = B_D2_FULL + 2, B_DONE = B_D2_EMPTY + 2,
-                       B_X = B_DONE + 1,  // [3] the exchange's steps, over the cluster
-                       NBAR = B_X + 3;
-  static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8, OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int SMEM = OFF_ABORT + 4 + 1024;
-  static_assert(STAGE % 1024 == 0 && SMEM <= 232448, "shared memory plan");
-  // tensor memory: the first product's result, whose place H takes as two
-  // operands of RP / 2 columns each; two buffers of the second one's
-  static constexpr uint32_t T_H = 0, T_D2 = RP, COLS = 256;
-  static_assert(T_D2 + 2 * NC <= COLS, "tensor memory plan");
-};
+constexpr int kSlices = 8;                 // of the first product's long axis, at most
+constexpr int RING = 110 * 1024;           // bytes of a block's stages, at most: two blocks share an SM
 
 template <class DT>
 constexpr uint32_t kTypes = std::is_same<DT, Bf16>::value ? (1u << 7) | (1u << 10) : 0u;
@@ -68,369 +43,416 @@ constexpr uint32_t kTypes = std::is_same<DT, Bf16>::value ? (1u << 7) | (1u << 1
 // piece p of 16 bytes of row r in a tile of 128-byte rows
 __device__ __forceinline__ uint32_t place(int r, int p) { return uint32_t(r * 128 + ((p ^ (r & 7)) << 4)); }
 
+// Barriers of a ring of stages, and what follows them in shared memory
+template <int NS, int MORE>
+struct Bars {
+  static constexpr int FULL = 0, EMPTY = NS, REST = 2 * NS, N = REST + MORE;
+};
+
+// A thread's arrival on a barrier once its copies so far are in
+__device__ __forceinline__ void arrive_copied(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// ------------------------------------------------------------------ H's parts
+template <int RP>
+struct Down {
+  static constexpr int THREADS = 160, WARP_MMA = 4;  // warps 0-3 copy, then write the result
+  static constexpr int XB = BM * 128, STAGE = XB + RP * 128;
+  static constexpr int NS = RING / STAGE < 6 ? RING / STAGE : 6;
+  using B = Bars<NS, 1>;
+  static constexpr int DONE = B::REST;
+  static constexpr int OFF_TOK = NS * STAGE, OFF_BAR = OFF_TOK + BM * 4, OFF_TMEM = OFF_BAR + B::N * 8,
+                       OFF_ABORT = OFF_TMEM + 4, SMEM = OFF_ABORT + 4 + 1024;
+  static constexpr uint32_t COLS = RP < 32 ? 32 : RP;
+};
+
 template <class DT, int RP>
-__global__ void __launch_bounds__(THREADS, RP <= 64 ? 2 : 1) lora_tc_kernel(const LoraArgs a) {
-  using P = Plan<RP>;
+__global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const LoraArgs a) {
+  using P = Down<RP>;
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t *sm = smem_raw + (base - raw);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::OFF_ABORT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + P::OFF_TMEM);
   int *tok = reinterpret_cast<int *>(sm + P::OFF_TOK);
   auto bar = [&](int i) { return base + P::OFF_BAR + 8u * uint32_t(i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t csize;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
-  const int C = int(csize), rank = int(cluster_ctarank()), tile = int(blockIdx.x) / C;
+  const int tile = int(blockIdx.x) / a.slices, slice = int(blockIdx.x) - tile * a.slices;
 
-  attn::wait_last_kernel();  // the list of tiles
-  if (tile >= *a.ntiles) return;  // the whole cluster
+  attn::start_next_kernel();
+  attn::wait_last_kernel();  // the list of tiles; in every block
+  if (tile >= *a.ntiles) return;
   const int4 d = a.tiles[tile];
   const int id = d.x, count = d.z;
-  for (int i = threadIdx.x; i < count; i += THREADS) tok[i] = a.order[d.y + i];
+  for (int i = threadIdx.x; i < count; i += P::THREADS) tok[i] = a.order[d.y + i];
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < P::NBAR; ++i)
-      mbar_init(bar(i), i < P::B_EMPTY ? 128                      // copying threads
-                        : i < P::B_D1  ? 5                        // the products, and the tokens' warps
-                        : i >= P::B_X  ? 4 * C                      // tokens' warps of the cluster
-                        : i == P::B_H || (i >= P::B_D2_EMPTY && i < P::B_DONE) ? 4 : 1);
+    for (int i = 0; i < P::B::N; ++i) mbar_init(bar(i), i < P::B::EMPTY ? 128 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == WARP_MMA) tmem_alloc(smem_u32(tmem_slot), P::COLS);
+  if (warp == P::WARP_MMA) tmem_alloc(smem_u32(tmem_slot), P::COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // this block's slices: elements of x, columns of y
-  const int steps = (a.H + KS - 1) / KS, s0 = steps * rank / C, n1 = steps * (rank + 1) / C - s0;
-  const int chunks = (a.N + NC - 1) / NC, c0 = chunks * rank / C, n2 = chunks * (rank + 1) / C - c0;
+  const int steps = (a.H + KS - 1) / KS, s0 = steps * slice / a.slices, n = steps * (slice + 1) / a.slices - s0;
   bool ok = true;  // this role's waits all ended in time
-  cluster_arrive();  // this block's barriers can be used
 
-  if (warp >= WARP_COPY && warp < WARP_MMA) {
-    // -------------------------------------------------------------- copies
-    const int t = threadIdx.x - WARP_COPY * 32, row = t / 8, piece = t % 8;  // rows row + 16 j
+  if (warp < P::WARP_MMA) {
+    const int row = threadIdx.x / 8, piece = threadIdx.x % 8;  // rows row + 16 j
     const uint32_t to = base + place(row, piece);
-    // rows of x and of y (0 elements on from a token's)
-    const uint16_t *xs[BM / 16], *ys[BM / 16];
+    const uint16_t *xs[BM / 16];
 #pragma unroll
     for (int j = 0; j < BM / 16; ++j) {
-      const int r = row + 16 * j, k = r < count ? tok[r] : -1;
-      xs[j] = k < 0 ? nullptr : a.x + int64_t(k) * a.ldx + s0 * KS + piece * 8;
-      ys[j] = k < 0 ? nullptr : a.y + int64_t(k) * a.ldy + c0 * NC + piece * 8;
+      const int r = row + 16 * j;
+      xs[j] = r < count ? a.x + int64_t(tok[r]) * a.ldx + s0 * KS + piece * 8 : nullptr;
     }
     const uint16_t *A = a.A + (int64_t(id) * a.r + row) * a.H + s0 * KS + piece * 8;
-    const uint16_t *B = a.B + (int64_t(id) * a.N + c0 * NC + row) * a.r + piece * 8;
     uint32_t slot = 0, par = 1;
 #pragma unroll 1
-    for (int g = 0; g < n1 + n2; ++g) {
-      if (!(ok = wait_warp(bar(P::B_EMPTY) + 8 * slot, par, abort_flag))) break;
+    for (int g = 0; g < n; ++g) {
+      if (!(ok = wait_warp(bar(P::B::EMPTY) + 8 * slot, par, abort_flag))) break;
       const uint32_t at = to + slot * P::STAGE;
-      if (g < n1) {
-        const bool in = (s0 + g) * KS + piece * 8 < a.H;
+      const bool in = (s0 + g) * KS + piece * 8 < a.H;
 #pragma unroll
-        for (int j = 0; j < BM / 16; ++j) {
-          const bool on = in && xs[j];
-          cp16(at + j * 16 * 128, on ? xs[j] + g * KS : a.x, on);
-        }
-#pragma unroll
-        for (int j = 0; j < RP / 16; ++j) {
-          const bool on = in && row + 16 * j < a.r;
-          cp16(at + P::XB + j * 16 * 128, on ? A + int64_t(16 * j) * a.H + g * KS : a.A, on);
-        }
-      } else {
-        const int c = g - n1;  // from c0 on
-        const bool in = (c0 + c) * NC + piece * 8 < a.N;
-#pragma unroll
-        for (int j = 0; j < NC / 16; ++j) {
-          const bool on = (c0 + c) * NC + row + 16 * j < a.N;
-#pragma unroll
-          for (int p = 0; p < (RP + 63) / 64; ++p) {
-            const bool has = on && p * 64 + piece * 8 < a.r;
-            if (RP >= 64 || piece * 8 < RP)
-              cp16(at + p * NC * 128 + j * 16 * 128,
-                   has ? B + (int64_t(c) * NC + 16 * j) * a.r + p * 64 : a.B, has);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < BM / 16; ++j) {
-          const bool on = in && ys[j];
-          cp16(at + P::BB + j * 16 * 128, on ? ys[j] + c * NC : a.y, on);
-        }
+      for (int j = 0; j < BM / 16; ++j) {
+        const bool on = in && xs[j];
+        cp16(at + j * 16 * 128, on ? xs[j] + g * KS : a.x, on);
       }
-      // arrives once this thread's copies so far are in
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(P::B_FULL) + 8 * slot) : "memory");
+#pragma unroll
+      for (int j = 0; j < RP / 16; ++j) {
+        const bool on = in && row + 16 * j < a.r;
+        cp16(at + P::XB + j * 16 * 128, on ? A + int64_t(16 * j) * a.H + g * KS : a.A, on);
+      }
+      arrive_copied(bar(P::B::FULL) + 8 * slot);
       if (++slot == P::NS) slot = 0, par ^= 1;
     }
     if (!ok) *abort_flag = 1;
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncwarp();
-    cluster_wait();
-  } else if (warp == WARP_MMA) {
-    // -------------------------------------------------------------- products
+    // ---- the result: a thread owns a token
+    if (ok) ok = wait_warp(bar(P::DONE), 0, abort_flag);
+    tc_fence_after();
+    const int r = threadIdx.x;
+    float *h = a.parts + (int64_t(slice) * a.T + d.y + r) * RP;
+#pragma unroll
+    for (int i = 0; i < RP; i += 16) {
+      uint32_t v[16];
+      tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + i, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[e]));
+      if (r < count) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          *reinterpret_cast<uint4 *>(h + i + e) = n > 0 ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0, 0, 0, 0);
+      }
+    }
+    tc_fence_before();
+    // ---- the tile's last block adds the parts, in the order of the slices
+    __threadfence();
+    named_sync(1, 128);
+    if (threadIdx.x == 0) tok[0] = atomicAdd(&a.tickets[tile], 1);
+    named_sync(1, 128);
+    if (tok[0] == a.slices - 1) {
+      __threadfence();
+      constexpr int Q = RP / 4;  // 16-byte pieces of a row, in neighbouring lanes
+      const float scale = a.scales ? a.scales[id] : 1.0f;
+#pragma unroll 2
+      for (int u = r; u < BM * Q; u += 128) {
+        const int row = d.y + min(u / Q, count - 1), q = u % Q;
+        const float4 *from = reinterpret_cast<const float4 *>(a.parts + int64_t(row) * RP) + q;
+        float4 w[kSlices], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int c = 0; c < kSlices; ++c)
+          if (c < a.slices) w[c] = __ldcg(from + int64_t(c) * a.T * Q);
+#pragma unroll
+        for (int c = 0; c < kSlices; ++c) {
+          if (c >= a.slices) break;
+          v.x += w[c].x;
+          v.y += w[c].y;
+          v.z += w[c].z;
+          v.w += w[c].w;
+        }
+        float up = scale;
+        if constexpr (std::is_same<DT, F16>::value) {
+          float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+          for (int o = Q / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // 2^-e with the row's largest in [2^e, 2^(e+1)), e within float's normal range
+          const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
+          const float down = __uint_as_float(uint32_t(127 - e) << 23);
+          up *= __uint_as_float(uint32_t(127 + e) << 23);
+          v.x *= down;
+          v.y *= down;
+          v.z *= down;
+          v.w *= down;
+        }
+        if (u / Q < count) {
+          auto low = [](float x, float y) { return fabsf(y) == INFINITY ? 0.0f : x - y; };
+          float x0, x1, x2, x3;
+          const uint2 hi = make_uint2(DT::pack2(v.x, v.y), DT::pack2(v.z, v.w));
+          DT::unpack2(hi.x, x0, x1);
+          DT::unpack2(hi.y, x2, x3);
+          uint2 *to = reinterpret_cast<uint2 *>(a.operands + int64_t(row) * RP);
+          to[q] = hi;
+          to[Q + q] = make_uint2(DT::pack2(low(v.x, x0), low(v.y, x1)), DT::pack2(low(v.z, x2), low(v.w, x3)));
+          if (q == 0) a.factors[row] = up;
+        }
+      }
+    }
+  } else {
     if (elect_one()) {
-      auto wait = [&](uint32_t b, uint32_t parity) {
-        if (ok) ok = wait_one(b, parity, abort_flag);
-      };
-      const uint32_t id1 = idesc_f16(BM, RP) | kTypes<DT>, id2 = idesc_f16(BM, NC) | kTypes<DT>;
-      const int ks = (a.r + 15) / 16;  // steps of the second product
+      const uint32_t idesc = idesc_f16(BM, RP) | kTypes<DT>;
       uint32_t slot = 0, par = 0;
 #pragma unroll 1
-      for (int g = 0; g < n1 && ok; ++g) {
-        wait(bar(P::B_FULL) + 8 * slot, par);
+      for (int g = 0; g < n && ok; ++g) {
+        ok = wait_one(bar(P::B::FULL) + 8 * slot, par, abort_flag);
         fence_async_smem();  // the copies are ordinary writes, which the products are to read
         tc_fence_after();
         if (ok) {
           const uint64_t dx = sdesc(base + slot * P::STAGE), da = sdesc(base + slot * P::STAGE + P::XB);
 #pragma unroll
-          for (int i = 0; i < KS / 16; ++i) mma_f16(tmem, dx + 2 * i, da + 2 * i, id1, g | i ? 1u : 0u);
-          for (int i = 0; i < 4; ++i) mbar_arrive(bar(P::B_EMPTY) + 8 * slot);  // for the tokens' warps
-          mma_commit(bar(P::B_EMPTY) + 8 * slot);
-        }
-        if (++slot == P::NS) slot = 0, par ^= 1;
-      }
-      if (ok) mma_commit(bar(P::B_D1));
-      if (n2 > 0) wait(bar(P::B_H), 0);
-#pragma unroll 1
-      for (int c = 0; c < n2 && ok; ++c) {
-        const uint32_t buf = c & 1;
-        wait(bar(P::B_FULL) + 8 * slot, par);
-        fence_async_smem();
-        wait(bar(P::B_D2_EMPTY) + 8 * buf, ((c >> 1) & 1) ^ 1);
-        tc_fence_after();
-        if (ok) {
-          const uint64_t db = sdesc(base + slot * P::STAGE);
-          const uint32_t to = tmem + P::T_D2 + buf * NC;
-          for (int i = 0; i < ks; ++i) {
-            const uint64_t b = db + ((i / 4) * (NC * 128) + (i % 4) * 32 >> 4);
-            mma_f16_ts(to, tmem + P::T_H + 8 * i, b, id2, i ? 1u : 0u);
-            mma_f16_ts(to, tmem + P::T_H + RP / 2 + 8 * i, b, id2, 1u);
-          }
-          mma_commit(bar(P::B_EMPTY) + 8 * slot);
-          mma_commit(bar(P::B_D2_FULL) + 8 * buf);
+          for (int i = 0; i < KS / 16; ++i) mma_f16(tmem, dx + 2 * i, da + 2 * i, idesc, g | i ? 1u : 0u);
+          mma_commit(bar(P::B::EMPTY) + 8 * slot);
         }
         if (++slot == P::NS) slot = 0, par ^= 1;
       }
       if (!ok) *abort_flag = 1;
-      mma_commit(bar(P::B_DONE));
-      mbar_wait_bounded(bar(P::B_DONE), 0);
+      mma_commit(bar(P::DONE));
+      mbar_wait_bounded(bar(P::DONE), 0);
     }
     __syncwarp();
-    cluster_wait();
+  }
+  if (!ok) set_status(a.status, WQ_ERR_TIMEOUT);
+  __syncthreads();
+  if (warp == P::WARP_MMA) tmem_dealloc(tmem, P::COLS);
+}
+
+// ------------------------------------------------------------------ y
+template <int RP>
+struct Up {
+  // warps 0-7 own tokens (two threads a token, 32 columns each), 8-11 copy
+  static constexpr int THREADS = 416, WARP_COPY = 8, WARP_MMA = 12;
+  static constexpr int BB = (RP + 63) / 64 * NC * 128, YB = BM * 128, STAGE = BB + YB;
+  static constexpr int NS = RING / STAGE;
+  using B = Bars<NS, 6>;
+  static constexpr int H = B::REST, D_FULL = H + 1, D_EMPTY = D_FULL + 2, DONE = D_EMPTY + 2;
+  static constexpr int OFF_TOK = NS * STAGE, OFF_BAR = OFF_TOK + BM * 4,
+                       OFF_TMEM = OFF_BAR + B::N * 8, OFF_ABORT = OFF_TMEM + 4, SMEM = OFF_ABORT + 4 + 1024;
+  // tensor memory: H as two operands of RP / 2 columns each, two buffers of 64 columns of the result
+  static constexpr uint32_t T_D = RP, COLS = 256;
+  static_assert(T_D + 2 * NC <= COLS, "tensor memory plan");
+};
+
+template <class DT, int RP>
+__global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraArgs a) {
+  using P = Up<RP>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t *sm = smem_raw + (base - raw);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + P::OFF_ABORT);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + P::OFF_TMEM);
+  int *tok = reinterpret_cast<int *>(sm + P::OFF_TOK);
+  auto bar = [&](int i) { return base + P::OFF_BAR + 8u * uint32_t(i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = int(blockIdx.x) / a.stretches, stretch = int(blockIdx.x) - tile * a.stretches;
+
+  attn::wait_last_kernel();  // H's parts; in every block
+  if (tile >= *a.ntiles) return;
+  const int4 d = a.tiles[tile];
+  const int id = d.x, count = d.z;
+  for (int i = threadIdx.x; i < count; i += P::THREADS) tok[i] = a.order[d.y + i];
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < P::B::N; ++i)
+      mbar_init(bar(i), i < P::B::EMPTY  ? 128  // copying threads
+                        : i < P::B::REST ? 9    // the products, and the tokens' warps
+                        : i == P::H || (i >= P::D_EMPTY && i < P::DONE) ? 8 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == P::WARP_MMA) tmem_alloc(smem_u32(tmem_slot), P::COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int chunks = (a.N + NC - 1) / NC, c0 = chunks * stretch / a.stretches, n = chunks * (stretch + 1) / a.stretches - c0;
+  bool ok = true;  // this role's waits all ended in time
+
+  if (warp >= P::WARP_COPY && warp < P::WARP_MMA) {
+    const int t = threadIdx.x - P::WARP_COPY * 32, row = t / 8, piece = t % 8;  // rows row + 16 j
+    const uint32_t to = base + place(row, piece);
+    const uint16_t *ys[BM / 16];
+#pragma unroll
+    for (int j = 0; j < BM / 16; ++j) {
+      const int r = row + 16 * j;
+      ys[j] = r < count ? a.y + int64_t(tok[r]) * a.ldy + c0 * NC + piece * 8 : nullptr;
+    }
+    const uint16_t *B = a.B + (int64_t(id) * a.N + c0 * NC + row) * a.r + piece * 8;
+    uint32_t slot = 0, par = 1;
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+      if (!(ok = wait_warp(bar(P::B::EMPTY) + 8 * slot, par, abort_flag))) break;
+      const uint32_t at = to + slot * P::STAGE;
+      const bool in = (c0 + c) * NC + piece * 8 < a.N;
+#pragma unroll
+      for (int j = 0; j < BM / 16; ++j) {
+        const bool on = in && ys[j];
+        cp16(at + P::BB + j * 16 * 128, on ? ys[j] + c * NC : a.y, on);
+      }
+#pragma unroll
+      for (int j = 0; j < NC / 16; ++j) {
+        const bool on = (c0 + c) * NC + row + 16 * j < a.N;
+#pragma unroll
+        for (int p = 0; p < (RP + 63) / 64; ++p) {
+          const bool has = on && p * 64 + piece * 8 < a.r;
+          if (RP >= 64 || piece * 8 < RP)
+            cp16(at + p * NC * 128 + j * 16 * 128, has ? B + (int64_t(c) * NC + 16 * j) * a.r + p * 64 : a.B, has);
+        }
+      }
+      arrive_copied(bar(P::B::FULL) + 8 * slot);
+      if (++slot == P::NS) slot = 0, par ^= 1;
+    }
+    if (!ok) *abort_flag = 1;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == P::WARP_MMA) {
+    if (elect_one()) {
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        if (ok) ok = wait_one(b, parity, abort_flag);
+      };
+      const uint32_t idesc = idesc_f16(BM, NC) | kTypes<DT>;
+      const int ks = (a.r + 15) / 16;
+      uint32_t slot = 0, par = 0;
+      wait(bar(P::H), 0);
+#pragma unroll 1
+      for (int c = 0; c < n && ok; ++c) {
+        const uint32_t buf = c & 1;
+        wait(bar(P::B::FULL) + 8 * slot, par);
+        fence_async_smem();  // the copies are ordinary writes, which the products are to read
+        wait(bar(P::D_EMPTY) + 8 * buf, ((c >> 1) & 1) ^ 1);
+        tc_fence_after();
+        if (ok) {
+          const uint64_t db = sdesc(base + slot * P::STAGE);
+          const uint32_t to = tmem + P::T_D + buf * NC;
+          for (int i = 0; i < ks; ++i) {
+            const uint64_t b = db + (((i / 4) * (NC * 128) + (i % 4) * 32) >> 4);
+            mma_f16_ts(to, tmem + 8 * i, b, idesc, i ? 1u : 0u);
+            mma_f16_ts(to, tmem + RP / 2 + 8 * i, b, idesc, 1u);
+          }
+          mma_commit(bar(P::B::EMPTY) + 8 * slot);
+          mma_commit(bar(P::D_FULL) + 8 * buf);
+        }
+        if (++slot == P::NS) slot = 0, par ^= 1;
+      }
+      if (!ok) *abort_flag = 1;
+      mma_commit(bar(P::DONE));
+      mbar_wait_bounded(bar(P::DONE), 0);
+    }
+    __syncwarp();
   } else {
-    // -------------------------------------------------------------- tokens
-    const int r = threadIdx.x;  // the token of this thread
-    const uint32_t mine = tmem + (uint32_t(warp * 32) << 16);
-    // H's sum: each block adds up the parts of 128 / C rows, which the blocks
-    // have put into its memory, and gives every block the operands they make.
-    // (Were every block to fetch all parts, the sum alone took 27 us for 8.)
-    constexpr int Q = RP / 4;  // 16-byte pieces of a row, parts or operands
-    const int share = BM / C;  // rows
-    auto at = [](int row, int q) { return P::OFF_P + uint32_t(row * (RP * 4) + ((q ^ (row & (Q < 8 ? Q - 1 : 7))) << 4)); };
-    // a step's end: all that the cluster's warps have written before it is there
-    auto step = [&](int i) {
-      __syncwarp();
-      if (lane == 0)
-        for (int c = 0; c < C; ++c) mbar_arrive_cluster(mapa(bar(P::B_X + i), uint32_t(c)));
-      if (ok) ok = mbar_wait_cluster(bar(P::B_X + i), 0, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-    };
-    if (n1 > 0) {
-      ok = wait_warp(bar(P::B_D1), 0, abort_flag);
-      tc_fence_after();
-    }
-    cluster_wait();  // the others' barriers can be used
-    {
-      const uint32_t owner = uint32_t(r / share);
-      const int row = rank * share + r % share;  // of the owner's place: block by block
+    const int r = threadIdx.x & 127, half = warp >> 2;  // token, columns 32 half ..
+    const uint32_t mine = tmem + (uint32_t((warp & 3) * 32) << 16);
+    // ---- H's operands of this token, high ones by one thread, low ones by the other
+    const int64_t at_row = int64_t(d.y) + min(r, count - 1);
+    const uint4 *from = reinterpret_cast<const uint4 *>(a.operands + at_row * RP + half * (RP / 2));
+    uint4 w[RP / 8];
 #pragma unroll
-      for (int i = 0; i < RP; i += 16) {
-        uint32_t v[16];
-        tmem_ld16(mine + i, v);
-        tmem_wait_ld();
+    for (int i = 0; i < RP / 8; ++i) w[i] = from[i];
+    const float up = a.factors[at_row];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[e]));
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = n1 > 0 ? v[e] : 0u;
-#pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          st_cluster_v4(mapa(base + at(row, (i + e) / 4), owner), v[e], v[e + 1], v[e + 2], v[e + 3]);
-      }
-    }
-    step(0);
-    const float scale = a.scales ? a.scales[id] : 1.0f;
-    // units of a row's piece: at most (128 / C) Q of them, all threads in step
-    uint32_t hi[Q][2], lo[Q][2];
-    float up_row[Q];
-    const int units = (share * Q + BM - 1) / BM;  // of a thread, a row's pieces in neighbouring lanes
-#pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      if (i >= units) break;
-      const int u = min(i * BM + r, share * Q - Q + r % Q), row = u / Q, q = u % Q;
-      float4 v = *reinterpret_cast<const float4 *>(sm + at(row, q));
-      for (int c = 1; c < C; ++c) {
-        const float4 w = *reinterpret_cast<const float4 *>(sm + at(c * share + row, q));
-        v.x += w.x;
-        v.y += w.y;
-        v.z += w.z;
-        v.w += w.w;
-      }
-      float f = 1.0f;  // the row's factor
-      if constexpr (std::is_same<DT, F16>::value) {
-        float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-#pragma unroll
-        for (int o = Q / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // 2^-e with the row's largest in [2^e, 2^(e+1)), e within float's normal range
-        const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
-        const float down = __uint_as_float(uint32_t(127 - e) << 23);
-        f = __uint_as_float(uint32_t(127 + e) << 23);
-        v.x *= down;
-        v.y *= down;
-        v.z *= down;
-        v.w *= down;
-      }
-      up_row[i] = scale * f;
-      auto low = [](float x, float h) { return fabsf(h) == INFINITY ? 0.0f : x - h; };
-      float x, y;
-      hi[i][0] = DT::pack2(v.x, v.y);
-      DT::unpack2(hi[i][0], x, y);
-      lo[i][0] = DT::pack2(low(v.x, x), low(v.y, y));
-      hi[i][1] = DT::pack2(v.z, v.w);
-      DT::unpack2(hi[i][1], x, y);
-      lo[i][1] = DT::pack2(low(v.z, x), low(v.w, y));
-    }
-    step(1);  // the parts are read: their place is the operands' now
-#pragma unroll
-    for (int i = 0; i < Q; ++i) {
-      if (i >= units) break;
-      const int u = i * BM + r, row = rank * share + u / Q, q = u % Q;
-      if (u >= share * Q) break;
-      for (int c = 0; c < C; ++c) {
-        const uint32_t to_hi = base + at(row, q / 2) + (q & 1) * 8, to_lo = base + at(row, Q / 2 + q / 2) + (q & 1) * 8;
-        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(mapa(to_hi, uint32_t(c))), "r"(hi[i][0]), "r"(hi[i][1]) : "memory");
-        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(mapa(to_lo, uint32_t(c))), "r"(lo[i][0]), "r"(lo[i][1]) : "memory");
-        if (q == 0)
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa(base + P::OFF_UP + row * 4, uint32_t(c))), "f"(up_row[i]) : "memory");
-      }
-    }
-    step(2);
-    const float up = *reinterpret_cast<const float *>(sm + P::OFF_UP + r * 4);
-#pragma unroll
-    for (int i = 0; i < Q; i += 4) {
-      uint32_t w[16];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(sm + at(r, i + e));
-        w[4 * e] = x.x;
-        w[4 * e + 1] = x.y;
-        w[4 * e + 2] = x.z;
-        w[4 * e + 3] = x.w;
-      }
-      tmem_st16(mine + P::T_H + 4 * i, w);
+    for (int i = 0; i < RP / 8; i += 2) {
+      const uint32_t x[8] = {w[i].x, w[i].y, w[i].z, w[i].w, w[i + 1].x, w[i + 1].y, w[i + 1].z, w[i + 1].w};
+      tmem_st8(mine + half * (RP / 2) + 4 * i, x);
     }
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(P::B_H));
-    // where a lane's pieces of the warp's rows go: eight lanes a row, rows 4 i + lane / 8
-    uint16_t *rows[8];
+    if (lane == 0) mbar_arrive(bar(P::H));
+    // where a lane's pieces of the warp's rows go: four lanes a row, rows 8 i + lane / 4
+    uint16_t *rows[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int q = warp * 32 + 4 * i + lane / 8;
-      rows[i] = q < count ? a.y + int64_t(tok[q]) * a.ldy + c0 * NC + (lane & 7) * 8 : nullptr;
+    for (int i = 0; i < 4; ++i) {
+      const int q = (warp & 3) * 32 + 8 * i + lane / 4;
+      rows[i] = q < count ? a.y + int64_t(tok[q]) * a.ldy + c0 * NC + half * 32 + (lane & 3) * 8 : nullptr;
     }
     using V = Vec<DT, 8>;
+    uint32_t slot = 0, par = 0;
 #pragma unroll 1
-    for (int c = 0; c < n2 && ok; ++c) {
-      const int g = n1 + c;
-      const uint32_t slot = uint32_t(g) % P::NS, buf = c & 1;
-      ok = wait_warp(bar(P::B_FULL) + 8 * slot, (uint32_t(g) / P::NS) & 1, abort_flag) &&
-           wait_warp(bar(P::B_D2_FULL) + 8 * buf, (c >> 1) & 1, abort_flag);
+    for (int c = 0; c < n && ok; ++c) {
+      const uint32_t buf = c & 1;
+      ok = wait_warp(bar(P::B::FULL) + 8 * slot, par, abort_flag) &&
+           wait_warp(bar(P::D_FULL) + 8 * buf, (c >> 1) & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
       uint8_t *ty = sm + slot * P::STAGE + P::BB;
+      uint32_t v[32];
+      tmem_ld32(mine + P::T_D + buf * NC + 32 * half, v);
+      V y[4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t v[32];
-        tmem_ld32(mine + P::T_D2 + buf * NC + 32 * half, v);
-        wait_ld32(v);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          V y{*reinterpret_cast<const uint4 *>(ty + place(r, 4 * half + p))};
-          float f[8];
-          y.get(f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = __fmaf_rn(__uint_as_float(v[8 * p + e]), up, f[e]);
-          y.set(f);
-          *reinterpret_cast<uint4 *>(ty + place(r, 4 * half + p)) = y.w;
-        }
-      }
+      for (int p = 0; p < 4; ++p) y[p].w = *reinterpret_cast<const uint4 *>(ty + place(r, 4 * half + p));
+      wait_ld32(v);
       tc_fence_before();
-      __syncwarp();  // the warp's rows are written
-      if (lane == 0) mbar_arrive(bar(P::B_D2_EMPTY) + 8 * buf);
-      const bool in = (c0 + c) * NC + (lane & 7) * 8 < a.N;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(ty + place(warp * 32 + 4 * i + lane / 8, lane & 7));
+      for (int p = 0; p < 4; ++p) {
+        float f[8];
+        y[p].get(f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fmaf_rn(__uint_as_float(v[8 * p + e]), up, f[e]);
+        y[p].set(f);
+        *reinterpret_cast<uint4 *>(ty + place(r, 4 * half + p)) = y[p].w;
+      }
+      __syncwarp();  // the warp's rows are written
+      if (lane == 0) mbar_arrive(bar(P::D_EMPTY) + 8 * buf);
+      const bool in = (c0 + c) * NC + half * 32 + (lane & 3) * 8 < a.N;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(ty + place((warp & 3) * 32 + 8 * i + lane / 4, 4 * half + (lane & 3)));
         if (in && rows[i]) *reinterpret_cast<uint4 *>(rows[i] + c * NC) = w;
       }
       __syncwarp();  // and read
-      if (lane == 0) mbar_arrive(bar(P::B_EMPTY) + 8 * slot);
+      if (lane == 0) mbar_arrive(bar(P::B::EMPTY) + 8 * slot);
+      if (++slot == P::NS) slot = 0, par ^= 1;
     }
     if (!ok) *abort_flag = 1;
   }
-  if (!ok) {
-    *abort_flag = 1;
-    set_status(a.status, WQ_ERR_TIMEOUT);
-  }
+  if (!ok) set_status(a.status, WQ_ERR_TIMEOUT);
   __syncthreads();
-  if (warp == WARP_MMA) tmem_dealloc(tmem, P::COLS);
-  cluster_sync();  // no block ends while another may write to it
+  if (warp == P::WARP_MMA) tmem_dealloc(tmem, P::COLS);
 }
 
 template <class DT, int RP>
-int launch_one(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
-  using P = Plan<RP>;
-  auto *k = lora_tc_kernel<DT, RP>;
-  static OncePerDevice sized;
-  if (!allow_smem(sized, k, P::SMEM)) return WQ_ERR_LAUNCH;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(tiles * C));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = size_t(P::SMEM);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(C);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) return WQ_ERR_LAUNCH;
-  return launched(1);
+int launch_one(const LoraArgs &a, int64_t tiles, cudaStream_t st) {
+  auto *down = lora_down_kernel<DT, RP>;
+  auto *up = lora_up_kernel<DT, RP>;
+  static OncePerDevice sized, sized_up;
+  if (!allow_smem(sized, down, Down<RP>::SMEM) || !allow_smem(sized_up, up, Up<RP>::SMEM)) return WQ_ERR_LAUNCH;
+  const int rc = attn::launch_chained(down, unsigned(tiles * a.slices), Down<RP>::THREADS, Down<RP>::SMEM, true, st, a);
+  return rc != WQ_OK ? rc
+                     : attn::launch_chained(up, unsigned(tiles * a.stretches), Up<RP>::THREADS, Up<RP>::SMEM, true, st, a);
 }
 
 template <class DT>
-int launch_rank(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
-  if (a.r <= 16) return launch_one<DT, 16>(a, tiles, C, st);
-  if (a.r <= 32) return launch_one<DT, 32>(a, tiles, C, st);
-  if (a.r <= 64) return launch_one<DT, 64>(a, tiles, C, st);
-  return launch_one<DT, 128>(a, tiles, C, st);
+int launch_rank(const LoraArgs &a, int64_t tiles, cudaStream_t st) {
+  if (a.r <= 16) return launch_one<DT, 16>(a, tiles, st);
+  if (a.r <= 32) return launch_one<DT, 32>(a, tiles, st);
+  if (a.r <= 64) return launch_one<DT, 64>(a, tiles, st);
+  return launch_one<DT, 128>(a, tiles, st);
 }
 
 }  // namespace
 
-// tiles: at most so many tiles of 128 tokens in a.tiles
-int launch_lora_tiles(const LoraArgs &a, int dtype, int64_t tiles, cudaStream_t st) {
-  // Blocks of a tile: as many as let about all tiles run at the same time
-  // (some may not be there)
-  const int slots = (a.r <= 64 ? 2 : 1) * 152;
-  int C = MOST_BLOCKS;
-  while (C > 1 && tiles * C > slots * 9 / 8) C /= 2;
-  return dtype == WQ_DT_BF16 ? launch_rank<Bf16>(a, tiles, C, st) : launch_rank<F16>(a, tiles, C, st);
+// Slices and stretches of a tile: as many as let about all tiles run at the same
+// time, two blocks an SM
+int lora_slices(int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(kSlices, 2 * 152 / tiles))); }
+
+// The rank in shared memory and in the workspace
+int lora_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
+
+int launch_lora_tiles(LoraArgs a, int dtype, int64_t tiles, cudaStream_t st) {
+  a.slices = lora_slices(tiles);
+  a.stretches = int(std::max<int64_t>(1, std::min<int64_t>((a.N + NC - 1) / NC, 2 * 152 / tiles)));
+  if (tiles * std::max(a.slices, a.stretches) >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
+  return dtype == WQ_DT_BF16 ? launch_rank<Bf16>(a, tiles, st) : launch_rank<F16>(a, tiles, st);
 }
 
 }  // namespace wq

@@ -286,9 +286,19 @@ struct LoraArgs {
   // tokens), nullptr where each cluster looks for its own
   int *order, *ntiles;
   int4 *tiles;
+  // Many tokens: slices of the first product's long axis, and stretches of y's
+  // columns; the slices' parts of its result [slices][T][lora_rank(r)], how many
+  // of a tile's are there, and the operands that they make, in the order of the tokens
+  int slices, stretches;
+  int *tickets;        // [tiles]
+  float *parts;
+  uint32_t *operands;  // [T][lora_rank(r)]: high ones, then low ones, in pairs
+  float *factors;      // [T]
 };
-size_t lora_ws_bytes(int64_t T, int64_t n);
-int launch_lora_tiles(const LoraArgs &a, int dtype, int64_t tiles, cudaStream_t st);
+int lora_slices(int64_t tiles);
+int lora_rank(int r);
+size_t lora_ws_bytes(int64_t T, int64_t n, int r);
+int launch_lora_tiles(LoraArgs a, int dtype, int64_t tiles, cudaStream_t st);
 int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st);
 
 }  // namespace wq

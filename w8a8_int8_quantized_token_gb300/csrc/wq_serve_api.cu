@@ -517,7 +517,9 @@ int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq
   return launch_evict(a, vec, stream);
 }
 
-size_t wq_lora_add_workspace_size(int64_t T, int n) { return T < 1 || n < 1 ? 0 : lora_ws_bytes(T, n); }
+size_t wq_lora_add_workspace_size(int64_t T, int n, int r) {
+  return T < 1 || n < 1 || r < 1 || r > 128 ? 0 : lora_ws_bytes(T, n, r);
+}
 
 int wq_lora_add(const void *x, int64_t ldx, int64_t T, int64_t H, const void *A, const void *B,
                 const float *scales, int n, int r, const int32_t *adapters, int64_t N, int dtype,
@@ -530,7 +532,7 @@ int wq_lora_add(const void *x, int64_t ldx, int64_t T, int64_t H, const void *A,
   if (H % 8 || N % 8 || r % 8 || r > 128 || ldx % 8 || ldy % 8 || n > 8192 || T >= (1 << 24) ||
       H > (1 << 20) || N > (1 << 20) || !al(x, 16) || !al(A, 16) || !al(B, 16) || !al(y, 16) || !al(scales, 4))
     return WQ_ERR_UNSUPPORTED;
-  const size_t need = lora_ws_bytes(T, n);
+  const size_t need = lora_ws_bytes(T, n, r);
   if (need > 0 && (!ws || !al(ws, 16) || ws_bytes < need)) return WQ_ERR_WORKSPACE;
   const int rc = device_ok();
   if (rc != WQ_OK) return rc;
