@@ -2,22 +2,24 @@
 //
 //   y[t] += s_a (x[t] A_a^T) B_a^T   for token t with adapter a.
 //
-// Tokens are taken in tiles of one adapter.  A cluster of blocks shares a tile:
-// each block multiplies its slice of x and A (the first product's long axis),
-// the parts are added through distributed shared memory in the order of the
-// blocks, and each block multiplies the sum with its slice of B's rows (the
-// second product's long axis) and adds the result to its columns of y.  So one
-// launch reads x and the adapter once a tile, and reads and writes y once; the
-// intermediate never leaves the cluster.  Bound by HBM: a rank of 16 needs 16
-// operations a byte, one of 64 about 60.
+// Here: the kernel for up to 256 tokens, and the sorting of more by adapter (their
+// products are in wq_lora_tc.cu).
+//
+// Tokens are taken in tiles of up to 16 of one adapter, and a cluster of blocks
+// shares a tile: each block multiplies its slice of x and A (the first product's
+// long axis), the parts are added through distributed shared memory in the order
+// of the blocks, and each block multiplies the sum with its slice of B's rows
+// (the second product's long axis) and adds the result to its columns of y.  So
+// one launch reads x and the adapter once a tile, and reads and writes y once;
+// the intermediate never leaves the cluster.  Every cluster finds its tile among
+// the tokens itself.  Bound by latency: the chain from the adapters' numbers to
+// the tokens' rows, the cluster's barrier, and two memory latencies (one token of
+// width 7168, rank 16: 6.2 us, of which a launch takes 2.5).
 //
 // x A^T is summed in float32 and enters the second product as two 16-bit
 // operands, its rounding and what that leaves (16 bits of it together), so that
 // only y is rounded.  fp16 operands are taken relative to a power of two near a
 // row's largest, which keeps them in range.
-//
-// Up to 256 tokens every cluster finds its tile itself; with more, a first
-// kernel sorts them by adapter.
 #include <algorithm>
 
 #include "wq_attn.cuh"
@@ -35,21 +37,22 @@ constexpr int kInline = 256;   // tokens that a cluster looks through itself
 constexpr int kGroupThreads = 1024;
 constexpr int kMostBlocks = 8;  // of a cluster
 
-// BM: tokens of a tile; RP: rank in whole 16s.  The second product's stages hold
-// rows of B and the columns of y that they go to.  They take the first one's
-// place, except with small tiles, whose time is latency: those have their first
-// ones on the way from the start.
-template <int BM, int RP>
+constexpr int BM = 16;  // tokens of a tile: a row tile of the warp products
+constexpr int WK = 8;   // warps, along the long axes
+constexpr int KS = 128;  // elements of x a stage of the first product
+constexpr int NC = WK * 32;  // columns of y a stage of the second
+
+// RP: rank in whole 16s.  The second product's stages hold rows of B and the
+// columns of y that they go to, and the first ones are on their way from the
+// start; with ranks over 64 they take the first product's place.
+template <int RP>
 struct Plan {
-  static constexpr int WM = BM / 16, WK = 8 / WM;  // warps along tokens, and along the first product's axis
-  static constexpr bool EARLY = BM == 16 && RP < 128;
-  static constexpr int KS = BM == 16 ? 128 : 64;   // elements of x a stage
+  static constexpr bool EARLY = RP < 128;
   static constexpr int XB = BM * KS * 2, AB = RP * KS * 2;
-  static constexpr int N1 = BM == 64 && RP < 128 ? 5 : RP < 128 || BM == 64 ? 4 : 2;  // stages of the first product
-  static constexpr int NC = WK * 32;               // columns of y a stage of the second
+  static constexpr int N1 = RP < 128 ? 4 : 2;      // stages of the first product
   static constexpr int BP = ((RP / 8) | 1) * 16;   // bytes of a row of B in shared memory
   static constexpr int BB = NC * BP, YB = BM * NC * 2;
-  static constexpr int N2 = BM == 64 ? 5 : RP < 128 ? 3 : 2;  // its stages
+  static constexpr int N2 = RP < 128 ? 3 : 2;      // stages of the second
   static constexpr int HP = BP;                    // bytes of a row of the intermediate
   static constexpr int RED = WK * BM * RP * 4;     // the warps' sums
   static constexpr int OFF_1 = 0;                  // first product's stages, then the warps' sums and the operands
@@ -86,19 +89,9 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
-// The tokens of this cluster's tile into tok; their adapter, or -1.  Without a
-// list every thread looks at one token: `scratch` holds the adapters of all.
-template <int BM>
+// The tokens of this cluster's tile into tok; their adapter, or -1.  Every thread
+// looks at one token: `scratch` holds the adapters of all.
 __device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, int *scratch, int *misc, int &count) {
-  if (a.order) {
-    wait_last_kernel();
-    if (tile >= *a.ntiles) return -1;
-    const int4 d = a.tiles[tile];
-    for (int i = threadIdx.x; i < d.z; i += NT) tok[i] = a.order[d.y + i];
-    __syncthreads();
-    count = d.z;
-    return d.x;
-  }
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
   int id = i < a.T ? a.ids[i] : -1;
   if (id >= a.n) {
@@ -137,27 +130,27 @@ __device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, 
   return own;
 }
 
-template <class DT, int BM, int RP>
+template <class DT, int RP>
 __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
-  using P = Plan<BM, RP>;
+  using P = Plan<RP>;
   extern __shared__ __align__(128) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
   int *tok = reinterpret_cast<int *>(sm + P::OFF_TOK);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = int(cluster_size()), rank = int(tc::cluster_ctarank());
   int count = 0;
-  const int id = find_tile<BM>(a, int(blockIdx.x) / C, tok, reinterpret_cast<int *>(sm),
+  const int id = find_tile(a, int(blockIdx.x) / C, tok, reinterpret_cast<int *>(sm),
                                reinterpret_cast<int *>(sm + P::OFF_MISC), count);
   if (id < 0) return;  // the whole cluster
 
   // A thread's copies keep their places in a stage, and step along in memory.
   // ---- the block's rows of B, for the second product
-  const int chunks = (a.N + P::NC - 1) / P::NC;  // of columns of y, dealt out in stretches
+  const int chunks = (a.N + NC - 1) / NC;  // of columns of y, dealt out in stretches
   const int c0 = chunks * rank / C, c1 = chunks * (rank + 1) / C;
-  constexpr int BP8 = RP / 8, NB = (P::NC * BP8 + NT - 1) / NT;  // pieces of a row; copies of a thread
-  static_assert((P::NC * BP8 % NT == 0 || NB == 1) && NT % BP8 == 0, "whole copies, or one of some threads");
+  constexpr int BP8 = RP / 8, NB = (NC * BP8 + NT - 1) / NT;  // pieces of a row; copies of a thread
+  static_assert((NC * BP8 % NT == 0 || NB == 1) && NT % BP8 == 0, "whole copies, or one of some threads");
   const int b_row = threadIdx.x / BP8, b_piece = threadIdx.x % BP8;
-  const uint16_t *b_src = a.B + (int64_t(id) * a.N + c0 * P::NC + b_row) * a.r + b_piece * 8;
+  const uint16_t *b_src = a.B + (int64_t(id) * a.N + c0 * NC + b_row) * a.r + b_piece * 8;
   const bool b_on = b_piece * 8 < a.r;
   uint32_t b_to[NB];
 #pragma unroll
@@ -169,7 +162,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     b_to[j] = base + P::OFF_B + uint32_t(at * P::BP + b_piece * 16);
   }
   // the columns of y: four lanes of two rows each find their pieces in different banks
-  constexpr int YP = P::NC / 8, YROWS = NT / YP, NY = P::YB / 16 / NT;  // pieces of a row; rows of a copy; copies
+  constexpr int YP = NC / 8, YROWS = NT / YP, NY = P::YB / 16 / NT;  // pieces of a row; rows of a copy; copies
   const int y_row = threadIdx.x / YP, y_piece = threadIdx.x % YP;
   uint16_t *y_src[NY];
 #pragma unroll
@@ -178,25 +171,25 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     y_src[j] = row < count ? a.y + int64_t(tok[row]) * a.ldy + y_piece * 8 : nullptr;
   }
   static_assert(YROWS % 2 == 0, "a thread's rows lie alike");
-  const uint32_t y_to = base + P::OFF_Y + uint32_t(y_row * (P::NC * 2) + ((y_piece ^ ((y_row & 1) << 2)) << 4));
+  const uint32_t y_to = base + P::OFF_Y + uint32_t(y_row * (NC * 2) + ((y_piece ^ ((y_row & 1) << 2)) << 4));
   uint32_t b_stage = 0, y_stage = 0;
   int b_next = c0;
   auto load_b = [&]() {
     if (b_next < c1) {
-      const bool in = b_next * P::NC + y_piece * 8 < a.N;
+      const bool in = b_next * NC + y_piece * 8 < a.N;
 #pragma unroll
       for (int j = 0; j < NY; ++j) {
         const bool on = in && y_src[j];
-        cp16(y_to + y_stage + j * YROWS * (P::NC * 2), on ? y_src[j] + b_next * P::NC : a.y, on);
+        cp16(y_to + y_stage + j * YROWS * (NC * 2), on ? y_src[j] + b_next * NC : a.y, on);
       }
       y_stage = y_stage == (P::N2 - 1) * P::YB ? 0 : y_stage + P::YB;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        if (P::NC * BP8 < NT && b_row >= P::NC) break;
-        const bool on = b_on && b_next * P::NC + b_row + j * (NT / BP8) < a.N;
+        if (NC * BP8 < NT && b_row >= NC) break;
+        const bool on = b_on && b_next * NC + b_row + j * (NT / BP8) < a.N;
         cp16(b_to[j] + b_stage, on ? b_src + int64_t(j) * (NT / BP8) * a.r : a.B, on);
       }
-      b_src += int64_t(P::NC) * a.r;
+      b_src += int64_t(NC) * a.r;
       b_stage = b_stage == (P::N2 - 1) * P::BB ? 0 : b_stage + P::BB;
       ++b_next;
     }
@@ -204,37 +197,37 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   };
 
   // ---- first product: this block's slice of the long axis
-  const int steps = (a.H + P::KS - 1) / P::KS, s0 = steps * rank / C, s1 = steps * (rank + 1) / C;
-  constexpr int PIECES = P::KS / 8, NX = BM * PIECES / NT, NA = (RP * PIECES + NT - 1) / NT, ROWS = NT / PIECES;
+  const int steps = (a.H + KS - 1) / KS, s0 = steps * rank / C, s1 = steps * (rank + 1) / C;
+  constexpr int PIECES = KS / 8, NX = BM * PIECES / NT, NA = (RP * PIECES + NT - 1) / NT, ROWS = NT / PIECES;
   static_assert(BM * PIECES % NT == 0 && (RP * PIECES % NT == 0 || NA == 1), "whole copies, or one of some threads");
   const int x_row = threadIdx.x / PIECES, x_piece = threadIdx.x % PIECES;
-  const uint32_t x_to = base + P::OFF_1 + uint32_t(x_row * (P::KS * 2) + ((x_piece ^ (x_row & 7)) << 4));
-  const uint16_t *x_src[NX], *a_src = a.A + (int64_t(id) * a.r + x_row) * a.H + s0 * P::KS + x_piece * 8;
+  const uint32_t x_to = base + P::OFF_1 + uint32_t(x_row * (KS * 2) + ((x_piece ^ (x_row & 7)) << 4));
+  const uint16_t *x_src[NX], *a_src = a.A + (int64_t(id) * a.r + x_row) * a.H + s0 * KS + x_piece * 8;
   int x_ahead = 0;  // elements that x_src and a_src are to step on
   bool x_on[NX];
 #pragma unroll
   for (int j = 0; j < NX; ++j) {
     const int row = x_row + j * ROWS;
     x_on[j] = row < count;
-    x_src[j] = a.x + int64_t(x_on[j] ? tok[row] : 0) * a.ldx + s0 * P::KS + x_piece * 8;
+    x_src[j] = a.x + int64_t(x_on[j] ? tok[row] : 0) * a.ldx + s0 * KS + x_piece * 8;
   }
   uint32_t x_stage = 0;
   int x_next = s0;
   auto load_x = [&]() {
     if (x_next < s1) {
-      const bool in = x_next * P::KS + x_piece * 8 < a.H;
+      const bool in = x_next * KS + x_piece * 8 < a.H;
 #pragma unroll
       for (int j = 0; j < NX; ++j) {
         const bool on = in && x_on[j];
-        cp16(x_to + x_stage + j * ROWS * (P::KS * 2), on ? x_src[j] + x_ahead : a.x, on);
+        cp16(x_to + x_stage + j * ROWS * (KS * 2), on ? x_src[j] + x_ahead : a.x, on);
       }
 #pragma unroll
       for (int j = 0; j < NA; ++j) {
         if (RP * PIECES < NT && x_row >= RP) break;
         const bool on = in && x_row + j * ROWS < a.r;
-        cp16(x_to + x_stage + P::XB + j * ROWS * (P::KS * 2), on ? a_src + int64_t(j) * ROWS * a.H + x_ahead : a.A, on);
+        cp16(x_to + x_stage + P::XB + j * ROWS * (KS * 2), on ? a_src + int64_t(j) * ROWS * a.H + x_ahead : a.A, on);
       }
-      x_ahead += P::KS;
+      x_ahead += KS;
       x_stage = x_stage == (P::N1 - 1) * (P::XB + P::AB) ? 0 : x_stage + P::XB + P::AB;
       ++x_next;
     }
@@ -247,7 +240,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     for (int i = 0; i < P::N2 - 1; ++i) load_b();
   }
 
-  const int wm = warp % P::WM, wk = warp / P::WM;
+  const int wk = warp;
   float acc[RP / 8][4];
 #pragma unroll
   for (int i = 0; i < RP / 8; ++i)
@@ -263,18 +256,18 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     load_x();
     const uint32_t as = xs + P::XB;
 #pragma unroll
-    for (int kk = 0; kk < P::KS / 16 / P::WK; ++kk) {
-      const int step = kk * P::WK + wk;
+    for (int kk = 0; kk < KS / 16 / WK; ++kk) {
+      const int step = kk * WK + wk;
       uint32_t fa[4];
       {
-        const int row = wm * 16 + (lane & 15), piece = 2 * step + (lane >> 4);
-        ldsm4(fa, xs + uint32_t(row * (P::KS * 2) + ((piece ^ (row & 7)) << 4)));
+        const int row = (lane & 15), piece = 2 * step + (lane >> 4);
+        ldsm4(fa, xs + uint32_t(row * (KS * 2) + ((piece ^ (row & 7)) << 4)));
       }
 #pragma unroll
       for (int p = 0; p < RP / 16; ++p) {
         uint32_t fb[4];
         const int row = p * 16 + (lane & 7) + ((lane >> 4) << 3), piece = 2 * step + ((lane >> 3) & 1);
-        ldsm4(fb, as + uint32_t(row * (P::KS * 2) + ((piece ^ (row & 7)) << 4)));
+        ldsm4(fb, as + uint32_t(row * (KS * 2) + ((piece ^ (row & 7)) << 4)));
         mma<DT>(acc[2 * p], fa, fb[0], fb[1]);
         mma<DT>(acc[2 * p + 1], fa, fb[2], fb[3]);
       }
@@ -287,7 +280,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   float *red = reinterpret_cast<float *>(sm + P::OFF_1), *part = reinterpret_cast<float *>(sm + P::OFF_P);
 #pragma unroll
   for (int i = 0; i < RP / 8; ++i) {
-    const int row = wm * 16 + (lane >> 2), col = i * 8 + (lane & 3) * 2;
+    const int row = (lane >> 2), col = i * 8 + (lane & 3) * 2;
     float *to = red + (wk * BM + row) * RP + col;
     *reinterpret_cast<float2 *>(to) = make_float2(acc[i][0], acc[i][1]);
     *reinterpret_cast<float2 *>(to + 8 * RP) = make_float2(acc[i][2], acc[i][3]);
@@ -296,7 +289,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   for (int i = threadIdx.x; i < BM * RP / 4; i += NT) {
     float4 v = reinterpret_cast<float4 *>(red)[i];
 #pragma unroll
-    for (int w = 1; w < P::WK; ++w) {
+    for (int w = 1; w < WK; ++w) {
       const float4 u = reinterpret_cast<float4 *>(red)[w * (BM * RP / 4) + i];
       v.x += u.x;
       v.y += u.y;
@@ -357,11 +350,11 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
   for (int part2 = 0; part2 < 2; ++part2)
 #pragma unroll
     for (int k = 0; k < RP / 16; ++k)
-      ldsm4(fh[part2][k], base + P::OFF_H + uint32_t((part2 * BM + wm * 16 + (lane & 15)) * P::HP + (2 * k + (lane >> 4)) * 16));
-  const int r0 = wm * 16 + (lane >> 2), r1 = r0 + 8;
+      ldsm4(fh[part2][k], base + P::OFF_H + uint32_t((part2 * BM + (lane & 15)) * P::HP + (2 * k + (lane >> 4)) * 16));
+  const int r0 = (lane >> 2), r1 = r0 + 8;
   const float up0 = up[r0], up1 = up[r1];
   uint16_t *y0 = a.y + int64_t(r0 < count ? tok[r0] : 0) * a.ldy, *y1 = a.y + int64_t(r1 < count ? tok[r1] : 0) * a.ldy;
-  auto col_of = [&](int c) { return c * P::NC + wk * 32 + (lane & 3) * 8; };
+  auto col_of = [&](int c) { return c * NC + wk * 32 + (lane & 3) * 8; };
   using V = Vec<DT, 8>;
   if constexpr (!P::EARLY) {
     __syncthreads();  // the operands are in registers: their place is the stages' now
@@ -377,8 +370,8 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     __syncthreads();
     load_b();
     const int piece = ((wk * 4 + (lane & 3)) ^ ((r0 & 1) << 2)) << 4;  // r1 = r0 + 8
-    const V o0{*reinterpret_cast<const uint4 *>(sm + ys + r0 * (P::NC * 2) + piece)};
-    const V o1{*reinterpret_cast<const uint4 *>(sm + ys + r1 * (P::NC * 2) + piece)};
+    const V o0{*reinterpret_cast<const uint4 *>(sm + ys + r0 * (NC * 2) + piece)};
+    const V o1{*reinterpret_cast<const uint4 *>(sm + ys + r1 * (NC * 2) + piece)};
     if ((ys += P::YB) == P::OFF_Y + P::N2 * P::YB) ys = P::OFF_Y;
     float d[4][4];
 #pragma unroll
@@ -432,7 +425,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
 
 // Tokens by adapter, and the tiles: one block.  The order of an adapter's
 // tokens is left to chance; no result depends on a token's place in a tile.
-__global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArgs a, int BM) {
+__global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArgs a) {
   extern __shared__ int cnt[];  // [n] tokens, then first places
   __shared__ int part[2][32];
   start_next_kernel();
@@ -462,16 +455,17 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
     if (lane == lead && id >= 0) at = atomicAdd(&cnt[id], __popc(m));
     return __shfl_sync(0xffffffffu, at, lead) + __popc(m & ((1u << lane) - 1u));
   };
+  int place[E];  // among the adapter's tokens; kept where one look takes all
   for (int t0 = 0; t0 < a.T; t0 += E * kGroupThreads) {
     if (t0) load(t0, id);
 #pragma unroll
-    for (int e = 0; e < E; ++e) take(id[e]);
+    for (int e = 0; e < E; ++e) place[e] = take(id[e]);
   }
   __syncthreads();
   // first place and first tile of each adapter: a thread has a stretch of them
   const int per = (a.n + kGroupThreads - 1) / kGroupThreads, n0 = min(int(threadIdx.x) * per, a.n), n1 = min(n0 + per, a.n);
   int tokens = 0, tiles = 0;
-  for (int i = n0; i < n1; ++i) tokens += cnt[i], tiles += (cnt[i] + BM - 1) / BM;
+  for (int i = n0; i < n1; ++i) tokens += cnt[i], tiles += (cnt[i] + kLoraTile - 1) / kLoraTile;
   int st = tokens, sl = tiles;
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, st, o), v = __shfl_up_sync(0xffffffffu, sl, o);
@@ -486,17 +480,23 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   }
   for (int i = n0; i < n1; ++i) {
     const int c = cnt[i];
-    for (int k = 0; k < c; k += BM) {
+    for (int k = 0; k < c; k += kLoraTile) {
       a.tickets[tile] = 0;
-      a.tiles[tile++] = make_int4(i, at + k, min(BM, c - k), 0);
+      a.tiles[tile++] = make_int4(i, at + k, min(kLoraTile, c - k), 0);
     }
     cnt[i] = at;
     at += c;
   }
   if (threadIdx.x == 0) *a.ntiles = all;
   __syncthreads();
+  if (a.T <= E * kGroupThreads) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (id[e] >= 0) a.order[cnt[id[e]] + place[e]] = e * kGroupThreads + int(threadIdx.x);
+    return;
+  }
   for (int t0 = 0; t0 < a.T; t0 += E * kGroupThreads) {
-    if (a.T > E * kGroupThreads) load(t0, id);
+    load(t0, id);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int to = take(id[e]);
@@ -505,10 +505,10 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   }
 }
 
-template <class DT, int BM, int RP>
+template <class DT, int RP>
 int launch_one(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
-  using P = Plan<BM, RP>;
-  auto *k = lora_kernel<DT, BM, RP>;
+  using P = Plan<RP>;
+  auto *k = lora_kernel<DT, RP>;
   static OncePerDevice sized;
   if (!allow_smem(sized, k, P::SMEM)) return WQ_ERR_LAUNCH;
   cudaLaunchConfig_t cfg{};
@@ -516,29 +516,26 @@ int launch_one(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = size_t(P::SMEM);
   cfg.stream = st;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(C);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.order ? 2 : 1;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = unsigned(C);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) return WQ_ERR_LAUNCH;
   return launched(1);
 }
 
-template <class DT, int BM>
+template <class DT>
 int launch_rank(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
-  if (a.r <= 16) return launch_one<DT, BM, 16>(a, tiles, C, st);
-  if (a.r <= 32) return launch_one<DT, BM, 32>(a, tiles, C, st);
-  if (a.r <= 64) return launch_one<DT, BM, 64>(a, tiles, C, st);
-  return launch_one<DT, BM, 128>(a, tiles, C, st);
+  if (a.r <= 16) return launch_one<DT, 16>(a, tiles, C, st);
+  if (a.r <= 32) return launch_one<DT, 32>(a, tiles, C, st);
+  if (a.r <= 64) return launch_one<DT, 64>(a, tiles, C, st);
+  return launch_one<DT, 128>(a, tiles, C, st);
 }
 
-// Tokens of a tile, by their number; tiles at most
-inline int tile_of(int64_t T) { return T <= kInline ? 16 : 128; }
-inline int64_t tiles_of(int64_t T, int64_t n) { return std::min(T, n + T / tile_of(T)); }
+// Tiles at most, of 16 tokens here and of 128 in the kernels for many tokens
+inline int64_t tiles_of(int64_t T, int64_t n) { return std::min(T, n + T / (T <= kInline ? BM : kLoraTile)); }
 
 // The workspace of many tokens, from `at` on (0: its size)
 size_t lora_lay_out(LoraArgs &a, char *at) {
@@ -570,11 +567,10 @@ size_t lora_ws_bytes(int64_t T, int64_t n, int r) {
 }
 
 int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
-  const int BM = tile_of(a.T);
   const int64_t tiles = tiles_of(a.T, a.n);
   if (a.T > kInline) {
     lora_lay_out(a, static_cast<char *>(ws));
-    lora_group_kernel<<<1, kGroupThreads, size_t(a.n) * 4, st>>>(a, BM);
+    lora_group_kernel<<<1, kGroupThreads, size_t(a.n) * 4, st>>>(a);
     const int rc = launched(1);
     return rc == WQ_OK ? launch_lora_tiles(a, dtype, tiles, st) : rc;
   }
@@ -582,8 +578,7 @@ int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
   // blocks an SM (some tiles may not be there)
   int C = kMostBlocks;
   while (C > 1 && tiles * C > 2 * 152 * 9 / 8) C /= 2;
-  if (dtype == WQ_DT_BF16) return BM == 16 ? launch_rank<Bf16, 16>(a, tiles, C, st) : launch_rank<Bf16, 64>(a, tiles, C, st);
-  return BM == 16 ? launch_rank<F16, 16>(a, tiles, C, st) : launch_rank<F16, 64>(a, tiles, C, st);
+  return dtype == WQ_DT_BF16 ? launch_rank<Bf16>(a, tiles, C, st) : launch_rank<F16>(a, tiles, C, st);
 }
 
 }  // namespace wq

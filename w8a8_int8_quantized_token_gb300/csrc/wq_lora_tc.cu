@@ -33,7 +33,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int BM = 128, KS = 64, NC = 64;  // tokens; elements of x, columns of y a stage
+constexpr int BM = kLoraTile, KS = 64, NC = 64;  // tokens; elements of x, columns of y a stage
 constexpr int kSlices = 8;                 // of the first product's long axis, at most
 constexpr int RING = 110 * 1024;           // bytes of a block's stages, at most: two blocks share an SM
 
@@ -80,17 +80,17 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = int(blockIdx.x) / a.slices, slice = int(blockIdx.x) - tile * a.slices;
 
-  attn::start_next_kernel();
-  attn::wait_last_kernel();  // the list of tiles; in every block
-  if (tile >= *a.ntiles) return;
-  const int4 d = a.tiles[tile];
-  const int id = d.x, count = d.z;
-  for (int i = threadIdx.x; i < count; i += P::THREADS) tok[i] = a.order[d.y + i];
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < P::B::N; ++i) mbar_init(bar(i), i < P::B::EMPTY ? 128 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  attn::wait_last_kernel();  // the list of tiles; in every block
+  attn::start_next_kernel();  // which may then rely on the list too
+  if (tile >= *a.ntiles) return;
+  const int4 d = a.tiles[tile];
+  const int id = d.x, count = d.z;
+  for (int i = threadIdx.x; i < count; i += P::THREADS) tok[i] = a.order[d.y + i];
   if (warp == P::WARP_MMA) tmem_alloc(smem_u32(tmem_slot), P::COLS);
   tc_fence_before();
   __syncthreads();
@@ -158,46 +158,55 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
       __threadfence();
       constexpr int Q = RP / 4;  // 16-byte pieces of a row, in neighbouring lanes
       const float scale = a.scales ? a.scales[id] : 1.0f;
-#pragma unroll 2
-      for (int u = r; u < BM * Q; u += 128) {
-        const int row = d.y + min(u / Q, count - 1), q = u % Q;
-        const float4 *from = reinterpret_cast<const float4 *>(a.parts + int64_t(row) * RP) + q;
-        float4 w[kSlices], v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      constexpr int U = 4;  // units whose loads are in flight together
+#pragma unroll 1
+      for (int u0 = r; u0 < BM * Q; u0 += U * 128) {
+        float4 w[U][kSlices];
 #pragma unroll
-        for (int c = 0; c < kSlices; ++c)
-          if (c < a.slices) w[c] = __ldcg(from + int64_t(c) * a.T * Q);
+        for (int k = 0; k < U; ++k) {
+          const int u = u0 + k * 128, row = d.y + min(u / Q, count - 1);
+          const float4 *from = reinterpret_cast<const float4 *>(a.parts + int64_t(row) * RP) + u % Q;
 #pragma unroll
-        for (int c = 0; c < kSlices; ++c) {
-          if (c >= a.slices) break;
-          v.x += w[c].x;
-          v.y += w[c].y;
-          v.z += w[c].z;
-          v.w += w[c].w;
+          for (int c = 0; c < kSlices; ++c)
+            if (c < a.slices) w[k][c] = __ldcg(from + int64_t(c) * a.T * Q);
         }
-        float up = scale;
-        if constexpr (std::is_same<DT, F16>::value) {
-          float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-          for (int o = Q / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // 2^-e with the row's largest in [2^e, 2^(e+1)), e within float's normal range
-          const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
-          const float down = __uint_as_float(uint32_t(127 - e) << 23);
-          up *= __uint_as_float(uint32_t(127 + e) << 23);
-          v.x *= down;
-          v.y *= down;
-          v.z *= down;
-          v.w *= down;
-        }
-        if (u / Q < count) {
-          auto low = [](float x, float y) { return fabsf(y) == INFINITY ? 0.0f : x - y; };
-          float x0, x1, x2, x3;
-          const uint2 hi = make_uint2(DT::pack2(v.x, v.y), DT::pack2(v.z, v.w));
-          DT::unpack2(hi.x, x0, x1);
-          DT::unpack2(hi.y, x2, x3);
-          uint2 *to = reinterpret_cast<uint2 *>(a.operands + int64_t(row) * RP);
-          to[q] = hi;
-          to[Q + q] = make_uint2(DT::pack2(low(v.x, x0), low(v.y, x1)), DT::pack2(low(v.z, x2), low(v.w, x3)));
-          if (q == 0) a.factors[row] = up;
+        for (int k = 0; k < U; ++k) {
+          const int u = u0 + k * 128, q = u % Q;
+          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int c = 0; c < kSlices; ++c) {
+            if (c >= a.slices) break;
+            v.x += w[k][c].x;
+            v.y += w[k][c].y;
+            v.z += w[k][c].z;
+            v.w += w[k][c].w;
+          }
+          float up = scale;
+          if constexpr (std::is_same<DT, F16>::value) {
+            float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+#pragma unroll
+            for (int o = Q / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^-e with the row's largest in [2^e, 2^(e+1)), e within float's normal range
+            const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
+            const float down = __uint_as_float(uint32_t(127 - e) << 23);
+            up *= __uint_as_float(uint32_t(127 + e) << 23);
+            v.x *= down;
+            v.y *= down;
+            v.z *= down;
+            v.w *= down;
+          }
+          if (u / Q < count) {
+            auto low = [](float x, float y) { return fabsf(y) == INFINITY ? 0.0f : x - y; };
+            float x0, x1, x2, x3;
+            const uint2 hi = make_uint2(DT::pack2(v.x, v.y), DT::pack2(v.z, v.w));
+            DT::unpack2(hi.x, x0, x1);
+            DT::unpack2(hi.y, x2, x3);
+            uint2 *to = reinterpret_cast<uint2 *>(a.operands + int64_t(d.y + u / Q) * RP);
+            to[q] = hi;
+            to[Q + q] = make_uint2(DT::pack2(low(v.x, x0), low(v.y, x1)), DT::pack2(low(v.z, x2), low(v.w, x3)));
+            if (q == 0) a.factors[d.y + u / Q] = up;
+          }
         }
       }
     }
@@ -258,8 +267,12 @@ __global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = int(blockIdx.x) / a.stretches, stretch = int(blockIdx.x) - tile * a.stretches;
 
-  attn::wait_last_kernel();  // H's parts; in every block
-  if (tile >= *a.ntiles) return;
+  // The list of tiles is there: the kernel before let this one start when it had
+  // waited for it.  Only H is not, so y and B are on their way before it is.
+  if (tile >= *a.ntiles) {
+    attn::wait_last_kernel();  // in every block: what follows this kernel may rely on the one before
+    return;
+  }
   const int4 d = a.tiles[tile];
   const int id = d.x, count = d.z;
   for (int i = threadIdx.x; i < count; i += P::THREADS) tok[i] = a.order[d.y + i];
@@ -353,6 +366,7 @@ __global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraA
     const int r = threadIdx.x & 127, half = warp >> 2;  // token, columns 32 half ..
     const uint32_t mine = tmem + (uint32_t((warp & 3) * 32) << 16);
     // ---- H's operands of this token, high ones by one thread, low ones by the other
+    attn::wait_last_kernel();
     const int64_t at_row = int64_t(d.y) + min(r, count - 1);
     const uint4 *from = reinterpret_cast<const uint4 *>(a.operands + at_row * RP + half * (RP / 2));
     uint4 w[RP / 8];

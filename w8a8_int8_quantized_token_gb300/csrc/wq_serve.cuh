@@ -272,6 +272,7 @@ struct EvictArgs {
 };
 int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st);
 
+constexpr int kLoraTile = 128;  // tokens of a tile where there are many
 struct LoraArgs {
   const uint16_t *x;
   int64_t ldx;
