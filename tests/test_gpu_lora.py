@@ -43,7 +43,8 @@ CASES = [  # T, H, N, r, n, dtype
     (17, 512, 256, 16, 1, BF), (33, 264, 520, 24, 2, FP), (128, 1000, 1032, 16, 40, BF), (256, 256, 128, 64, 5, BF),
     (256, 136, 328, 32, 256, FP), (257, 512, 256, 8, 3, BF), (300, 128, 264, 128, 7, FP), (1024, 72, 80, 16, 300, BF),
     (1025, 256, 136, 64, 2, BF), (1500, 264, 200, 24, 9, FP), (2000, 128, 128, 128, 8192, BF), (3100, 192, 88, 40, 1, BF),
-    (1100, 64, 64, 16, 1, FP),
+    (1100, 64, 64, 16, 1, FP), (1537, 200, 136, 16, 3, BF), (1536, 136, 72, 24, 40, FP), (577, 128, 200, 64, 5, FP),
+    (289, 72, 136, 128, 2, BF), (4000, 64, 64, 32, 4000, BF),
 ]
 
 
@@ -52,7 +53,7 @@ def test_lora_add(T, H, N, r, n, dtype):
     check(problem(T, H, N, r, n, dtype))
 
 
-@pytest.mark.parametrize("T", [40, 700, 1300])
+@pytest.mark.parametrize("T", [40, 700, 1300, 2500])
 def test_runs_of_tokens_no_scales_and_strides(T):
     H, N, r, n = 128, 136, 16, 4
     ids = torch.tensor([-1, 2, 0, 3, 2]).repeat_interleave(-(-T // 5))[:T].to(torch.int32).cuda()
@@ -67,7 +68,7 @@ def test_runs_of_tokens_no_scales_and_strides(T):
     assert torch.equal(a["y"], b["y"]) and (wide_y[:, :8] == 7).all() and (wide_y[:, 8 + N:] == 7).all()
 
 
-@pytest.mark.parametrize("T", [30, 600, 1300])
+@pytest.mark.parametrize("T", [30, 600, 2300])
 def test_tokens_without_an_adapter_stay_as_they_are(T):
     a = problem(T, 64, 64, 8, 3, BF, none=0.5)
     off = a["adapters"] < 0
@@ -81,7 +82,7 @@ def test_tokens_without_an_adapter_stay_as_they_are(T):
     assert torch.equal(a["y"].view(torch.int16), before.view(torch.int16))
 
 
-@pytest.mark.parametrize("T", [30, 600, 1300])
+@pytest.mark.parametrize("T", [30, 600, 2300])
 def test_bad_adapters_are_reported_and_skipped(T):
     a = problem(T, 64, 64, 8, 3, BF, none=0.0)
     a["adapters"][5], a["adapters"][T - 1] = 3, 10 ** 9
@@ -105,7 +106,7 @@ def test_a_row_does_not_depend_on_its_neighbours_or_the_run():
     b["y"], b["adapters"][:100] = y0.clone(), -1
     wq.lora_add(**b)
     assert torch.equal(b["y"][100:], a["y"][100:]) and torch.equal(b["y"][:100], y0[:100])
-    c = problem(3000, 128, 128, 16, 5, BF)
+    c = problem(3000, 128, 128, 64, 5, BF)
     y0 = c["y"].clone()
     wq.lora_add(**c)
     for _ in range(3):
@@ -115,7 +116,7 @@ def test_a_row_does_not_depend_on_its_neighbours_or_the_run():
 
 
 @pytest.mark.parametrize("size", [1e4, 1e-4])
-@pytest.mark.parametrize("T", [5, 1100])
+@pytest.mark.parametrize("T", [5, 1100, 2100])
 def test_fp16_sums_past_its_range(size, T):
     """x A^T far past fp16's largest, and below its smallest, with B to match."""
     a = problem(T, 512, 64, 8, 2, FP)
@@ -125,7 +126,7 @@ def test_fp16_sums_past_its_range(size, T):
     check(a)
 
 
-@pytest.mark.parametrize("T", [9, 1100])
+@pytest.mark.parametrize("T", [9, 1100, 2100])
 def test_nonfinite_values_stay_in_their_rows(T):
     a = problem(T, 64, 64, 8, 1, BF, torch.zeros(T, dtype=torch.int32).cuda())
     y0, x0 = a["y"].clone(), a["x"].clone()
@@ -139,7 +140,7 @@ def test_nonfinite_values_stay_in_their_rows(T):
     assert torch.equal(a["y"][rest], clean["y"][rest])
 
 
-@pytest.mark.parametrize("T", [20, 500, 1200])
+@pytest.mark.parametrize("T", [20, 500, 2200])
 def test_replayed_in_a_graph_with_other_adapters(T):
     a = problem(T, 128, 128, 16, 6, BF)
     y0, ws = a["y"].clone(), wq.lora_add_workspace(a["y"], a["x"], a["A"])

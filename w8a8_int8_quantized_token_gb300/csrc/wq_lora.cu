@@ -2,8 +2,8 @@
 //
 //   y[t] += s_a (x[t] A_a^T) B_a^T   for token t with adapter a.
 //
-// Here: the kernel for up to 256 tokens, and the sorting of more by adapter (their
-// products are in wq_lora_tc.cu).
+// Here: the kernel for up to 1024 tokens, and the sorting of more than 256 by
+// adapter (the products of many are in wq_lora_tc.cu).
 //
 // Tokens are taken in tiles of up to 16 of one adapter, and a cluster of blocks
 // shares a tile: each block multiplies its slice of x and A (the first product's
@@ -12,7 +12,7 @@
 // (the second product's long axis) and adds the result to its columns of y.  So
 // one launch reads x and the adapter once a tile, and reads and writes y once;
 // the intermediate never leaves the cluster.  Every cluster finds its tile among
-// the tokens itself.  Bound by latency: the chain from the adapters' numbers to
+// up to 256 tokens itself, and in the sorted list of more.  Bound by latency: the chain from the adapters' numbers to
 // the tokens' rows, the cluster's barrier, and two memory latencies (one token of
 // width 7168, rank 16: 6.2 us, of which a launch takes 2.5).
 //
@@ -89,10 +89,19 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
-// The tokens of this cluster's tile into tok; their adapter, or -1.  Every thread
-// looks at one token: `scratch` holds the adapters of all.
+// The tokens of this cluster's tile into tok; their adapter, or -1.  Without a
+// list every thread looks at one token: `scratch` holds the adapters of all.
 __device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, int *scratch, int *misc, int &count) {
   const int i = threadIdx.x, lane = i & 31, warp = i >> 5;
+  if (a.order) {
+    attn::wait_last_kernel();
+    if (tile >= *a.ntiles) return -1;
+    const int4 d = a.tiles[tile];
+    if (i < d.z) tok[i] = a.order[d.y + i];
+    __syncthreads();
+    count = d.z;
+    return d.x;
+  }
   int id = i < a.T ? a.ids[i] : -1;
   if (id >= a.n) {
     if (tile == 0) set_status(a.status, WQ_ERR_INDEX);
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
 
 // Tokens by adapter, and the tiles: one block.  The order of an adapter's
 // tokens is left to chance; no result depends on a token's place in a tile.
-__global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArgs a) {
+__global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArgs a, int size) {
   extern __shared__ int cnt[];  // [n] tokens, then first places
   __shared__ int part[2][32];
   start_next_kernel();
@@ -465,7 +474,7 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   // first place and first tile of each adapter: a thread has a stretch of them
   const int per = (a.n + kGroupThreads - 1) / kGroupThreads, n0 = min(int(threadIdx.x) * per, a.n), n1 = min(n0 + per, a.n);
   int tokens = 0, tiles = 0;
-  for (int i = n0; i < n1; ++i) tokens += cnt[i], tiles += (cnt[i] + kLoraTile - 1) / kLoraTile;
+  for (int i = n0; i < n1; ++i) tokens += cnt[i], tiles += (cnt[i] + size - 1) / size;
   int st = tokens, sl = tiles;
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, st, o), v = __shfl_up_sync(0xffffffffu, sl, o);
@@ -480,9 +489,9 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   }
   for (int i = n0; i < n1; ++i) {
     const int c = cnt[i];
-    for (int k = 0; k < c; k += kLoraTile) {
-      a.tickets[tile] = 0;
-      a.tiles[tile++] = make_int4(i, at + k, min(kLoraTile, c - k), 0);
+    for (int k = 0; k < c; k += size) {
+      if (a.tickets) a.tickets[tile] = 0;
+      a.tiles[tile++] = make_int4(i, at + k, min(size, c - k), 0);
     }
     cnt[i] = at;
     at += c;
@@ -516,12 +525,14 @@ int launch_one(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = size_t(P::SMEM);
   cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = unsigned(C);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(C);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.order ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, k, a) != cudaSuccess) return WQ_ERR_LAUNCH;
   return launched(1);
 }
@@ -534,12 +545,25 @@ int launch_rank(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
   return launch_one<DT, 128>(a, tiles, C, st);
 }
 
-// Tiles at most, of 16 tokens here and of 128 in the kernels for many tokens
-inline int64_t tiles_of(int64_t T, int64_t n) { return std::min(T, n + T / (T <= kInline ? BM : kLoraTile)); }
+// Whether this kernel takes the tokens.  Its tiles read the adapter once for 16
+// tokens, but need no second launch.  Width 7168, 8 adapters, here and with 128
+// tokens a tile: 1024 tokens of rank 16 18 and 25 us, 2048 of rank 16 29 and 31,
+// 3000 of rank 16 49 and 40, 1536 of rank 32 42 and 33, 768 of rank 64 33 and 33,
+// 2048 of rank 64 57 and 43, 384 of rank 128 37 and 37.
+inline bool few(int64_t T, int r) { return T * std::max(r, 24) <= 36864; }
+// Tokens of a tile, here and in the kernels for many; tiles at most
+inline int tile_of(int64_t T, int r) { return few(T, r) ? BM : kLoraTile; }
+inline int64_t tiles_of(int64_t T, int64_t n, int r) { return std::min(T, n + T / tile_of(T, r)); }
+// Tiles to expect, by which the blocks of a tile are chosen: a batch of single
+// tokens mixes adapters, prompts are runs of tokens.  (By the most, a few prompts
+// among 512 adapters took 141 us, and 52 so.)
+inline int64_t tiles_like(int64_t T, int64_t n, int r) {
+  return T <= kInline ? tiles_of(T, n, r) : T / tile_of(T, r) + std::min(n, T / 256 + 1);
+}
 
-// The workspace of many tokens, from `at` on (0: its size)
+// The workspace, from `at` on (nullptr: its size alone)
 size_t lora_lay_out(LoraArgs &a, char *at) {
-  const int64_t tiles = tiles_of(a.T, a.n), T = a.T, RP = lora_rank(a.r);
+  const int64_t tiles = tiles_of(a.T, a.n, a.r), T = a.T, RP = lora_rank(a.r);
   size_t n = 0;
   auto take = [&](auto *&p, int64_t count) {
     p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(at + n);
@@ -547,11 +571,13 @@ size_t lora_lay_out(LoraArgs &a, char *at) {
   };
   take(a.ntiles, 1);
   take(a.tiles, tiles);
-  take(a.tickets, tiles);
   take(a.order, T);
-  take(a.factors, T);
-  take(a.operands, T * RP);
-  take(a.parts, lora_slices(tiles) * T * RP);
+  if (!few(T, a.r)) {
+    take(a.tickets, tiles);
+    take(a.factors, T);
+    take(a.operands, T * RP);
+    take(a.parts, lora_slices(tiles_like(T, a.n, a.r)) * T * RP);
+  }
   return n;
 }
 
@@ -567,17 +593,18 @@ size_t lora_ws_bytes(int64_t T, int64_t n, int r) {
 }
 
 int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st) {
-  const int64_t tiles = tiles_of(a.T, a.n);
+  const int64_t tiles = tiles_of(a.T, a.n, a.r);
   if (a.T > kInline) {
     lora_lay_out(a, static_cast<char *>(ws));
-    lora_group_kernel<<<1, kGroupThreads, size_t(a.n) * 4, st>>>(a);
+    lora_group_kernel<<<1, kGroupThreads, size_t(a.n) * 4, st>>>(a, tile_of(a.T, a.r));
     const int rc = launched(1);
-    return rc == WQ_OK ? launch_lora_tiles(a, dtype, tiles, st) : rc;
+    if (rc != WQ_OK) return rc;
+    if (!few(a.T, a.r)) return launch_lora_tiles(a, dtype, tiles, tiles_like(a.T, a.n, a.r), st);
   }
   // Blocks of a tile: as many as let about all tiles run at the same time, two
-  // blocks an SM (some tiles may not be there)
+  // blocks an SM
   int C = kMostBlocks;
-  while (C > 1 && tiles * C > 2 * 152 * 9 / 8) C /= 2;
+  while (C > 1 && tiles_like(a.T, a.n, a.r) * C > 2 * 152 * 9 / 8) C /= 2;
   return dtype == WQ_DT_BF16 ? launch_rank<Bf16>(a, tiles, C, st) : launch_rank<F16>(a, tiles, C, st);
 }
 

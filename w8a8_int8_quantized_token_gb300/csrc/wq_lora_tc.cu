@@ -455,16 +455,16 @@ int launch_rank(const LoraArgs &a, int64_t tiles, cudaStream_t st) {
 
 }  // namespace
 
-// Slices and stretches of a tile: as many as let about all tiles run at the same
-// time, two blocks an SM
-int lora_slices(int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(kSlices, 2 * 152 / tiles))); }
+// Slices and stretches of a tile: as many as let about all tiles, of which there
+// are likely `like`, run at the same time, two blocks an SM
+int lora_slices(int64_t like) { return int(std::max<int64_t>(1, std::min<int64_t>(kSlices, 2 * 152 / like))); }
 
 // The rank in shared memory and in the workspace
 int lora_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }
 
-int launch_lora_tiles(LoraArgs a, int dtype, int64_t tiles, cudaStream_t st) {
-  a.slices = lora_slices(tiles);
-  a.stretches = int(std::max<int64_t>(1, std::min<int64_t>((a.N + NC - 1) / NC, 2 * 152 / tiles)));
+int launch_lora_tiles(LoraArgs a, int dtype, int64_t tiles, int64_t like, cudaStream_t st) {
+  a.slices = lora_slices(like);
+  a.stretches = int(std::max<int64_t>(1, std::min<int64_t>((a.N + NC - 1) / NC, 2 * 152 / like)));
   if (tiles * std::max(a.slices, a.stretches) >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
   return dtype == WQ_DT_BF16 ? launch_rank<Bf16>(a, tiles, st) : launch_rank<F16>(a, tiles, st);
 }

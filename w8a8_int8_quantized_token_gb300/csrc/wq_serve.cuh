@@ -296,10 +296,10 @@ struct LoraArgs {
   uint32_t *operands;  // [T][lora_rank(r)]: high ones, then low ones, in pairs
   float *factors;      // [T]
 };
-int lora_slices(int64_t tiles);
+int lora_slices(int64_t like);
 int lora_rank(int r);
 size_t lora_ws_bytes(int64_t T, int64_t n, int r);
-int launch_lora_tiles(LoraArgs a, int dtype, int64_t tiles, cudaStream_t st);
+int launch_lora_tiles(LoraArgs a, int dtype, int64_t tiles, int64_t like, cudaStream_t st);
 int launch_lora(LoraArgs a, int dtype, void *ws, cudaStream_t st);
 
 }  // namespace wq
