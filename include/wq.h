@@ -708,8 +708,9 @@ WQ_API int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_
  * rows are not moved.  key_len and new_len must not overlap.
  * Requirements: budget >= 1, first + recent <= budget, bf16 or fp16, dk and dv
  * at most 16384.  16-byte accesses serve keys, values and pitches in multiples
- * of 8 elements.  Workspace: wq_evict_paged_workspace_size(B), a word a sequence. */
-WQ_API size_t wq_evict_paged_workspace_size(int B);
+ * of 8 elements.  Workspace: wq_evict_paged_workspace_size(), 16 bytes
+ * a key that may stay. */
+WQ_API size_t wq_evict_paged_workspace_size(int B, int heads, int64_t budget);
 WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
                           const wq_paged_cache *cache, int B, const int32_t *page_table,
                           int64_t ld_table, const int32_t *key_len, int64_t max_len,

@@ -83,8 +83,8 @@ def test_evict_refusals(lib):
     for kw in (dict(cache=cache(dk=16386)), dict(cache=cache(k=FAKE + 1)), dict(w=FAKE + 2), dict(wo=FAKE * 3 + 2),
                dict(B=1 << 24, ws_=640, wh=640 * (1 << 24), os=100, oh=100 << 24, nl=FAKE << 10)):
         assert call(**kw) == UNSUPPORTED, kw
-    need = lib.wq_evict_paged_workspace_size(2)
-    assert need >= 2 * 4 and lib.wq_evict_paged_workspace_size(0) == 0
+    need = lib.wq_evict_paged_workspace_size(2, 2, 100)
+    assert need >= 2 * 2 * 100 * 8 and lib.wq_evict_paged_workspace_size(0, 2, 100) == 0
     assert call(n=need - 1) == WORKSPACE and call(ws=None) == WORKSPACE and call(ws=FAKE + 8) == WORKSPACE
     assert call(B=0, kl=None) == 0
 

@@ -101,7 +101,7 @@ _SIGS = {
     "wq_attention_shared_prefix": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _P, _L, _F, _P, _L, _L, _P, _P, _S, _P, _P]),
     "wq_attention_weights_paged_workspace_size": (_S, [_L, _I, _I, _I, _P, _L]),
     "wq_attention_weights_paged": (_I, [_P, _L, _L, _L, _I, _P, _I, _I, _P, _P, _L, _P, _L, _F, _P, _F, _P, _L, _L, _P, _S, _P, _P]),
-    "wq_evict_paged_workspace_size": (_S, [_I]),
+    "wq_evict_paged_workspace_size": (_S, [_I, _I, _L]),
     "wq_evict_paged": (_I, [_P, _L, _L, _P, _I, _P, _L, _P, _L, _L, _L, _L, _P, _L, _P, _L, _L, _P, _P, _P, _S, _P, _P]),
     "wq_lora_add_workspace_size": (_S, [_L, _I, _I]),
     "wq_lora_add": (_I, [_P, _L, _L, _L, _P, _P, _P, _I, _I, _P, _L, _I, _P, _L, _P, _S, _P, _P]),
@@ -1103,7 +1103,7 @@ def attention_weights_paged(q, k_cache, page_table, key_len, max_len, lse, weigh
 
 def evict_paged_workspace(weights, max_len, budget):
     """A workspace for evict_paged calls of these sizes."""
-    n = lib().wq_evict_paged_workspace_size(weights.shape[0])
+    n = lib().wq_evict_paged_workspace_size(weights.shape[0], weights.shape[1], budget)
     return torch.empty(max(n, 1), dtype=torch.uint8, device=weights.device)
 
 
@@ -1138,7 +1138,7 @@ def evict_paged(weights, k_cache, v_cache, page_table, key_len, max_len, budget,
     if kept is None:
         kept = torch.empty(B, heads, budget, dtype=torch.int32, device=key_len.device)
     _dense_as(kept, (B, heads, budget), torch.int32, "kept", dev)
-    ws, size = _workspace(ws, lambda: lib().wq_evict_paged_workspace_size(B), dev)
+    ws, size = _workspace(ws, lambda: lib().wq_evict_paged_workspace_size(B, heads, budget), dev)
     out = tables[2:] or (None, 0)
     _check(lib().wq_evict_paged(
         weights.data_ptr(), sw[0], sw[1], c, B, tables[0], tables[1], key_len.data_ptr(), max_len, budget, recent, first,

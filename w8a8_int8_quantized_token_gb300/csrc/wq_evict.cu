@@ -121,10 +121,26 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
   const float *w_row = w;
   float *w_out = a.w_out == a.w ? nullptr : a.w_out + b * a.o_seq + h * a.o_head;
   int32_t *kept = a.kept + (int64_t(b) * a.heads + h) * a.budget;
+  // What the other kernel needs to move key i to place j: pages and places,
+  // found here once and not by every thread that has a piece of the row
+  int4 *ways = a.ways + (int64_t(b) * a.heads + h) * a.budget;
+  const int32_t *in = a.page_table + b * a.ld_table, *out = a.out_table + b * a.ld_out;
+  auto find_way = [&](int j, int i) {
+    if (a.in_place && i == j) {
+      ways[j] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    const int p = i / a.page_size, q = j / a.page_size, from = in[p], to = out[q];
+    const bool good = unsigned(from) < unsigned(a.num_pages) && unsigned(to) < unsigned(a.num_pages);
+    if (!good) set_status(a.status, WQ_ERR_INDEX);
+    ways[j] = make_int4(good ? from : -1, i - p * a.page_size, to, j - q * a.page_size);
+  };
   // key i goes to place j
+  const bool moves = !a.in_place || n > a.budget;
   auto emit = [&](int j, int i) {
     kept[j] = i;
     if (w_out) w_out[j] = w_row[i];
+    if (moves) find_way(j, i);
   };
   // the cluster's threads share what needs no order
   const int all0 = rank * NT + int(threadIdx.x), all = C * NT;
@@ -285,7 +301,6 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
     j += c[0];
     equal += c[1];
   }
-  if (C > 1) tc::cluster_arrive();  // the last look at another block
   for (int v = 0; v < warp; ++v) j += sm.part[v], equal += sm.part2[v];
   j += min(equal, need);
   for (int i0 = s0; i0 < s1; i0 += 32) {
@@ -302,7 +317,9 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
     j += __popc(st);
     equal += __popc(eq);
   }
-  if (C > 1) tc::cluster_wait();  // none looks at this block any more
+  together();  // none looks at another block any more, and all have written their places
+#pragma unroll 4
+  for (int q = first + all0; q < a.budget - a.recent; q += all) find_way(q, __ldcg(kept + q));
 }
 
 constexpr int MT = 256, MU = 8;  // threads of a moving block, rows of a thread a stretch
@@ -311,50 +328,27 @@ constexpr int MT = 256, MU = 8;  // threads of a moving block, rows of a thread 
 template <class V>
 __device__ __forceinline__ void move_rows(const EvictArgs &a, V *cache, int64_t pitch_page, int64_t pitch_row, int c0,
                                           int cols, int b, int h, int rows, int rb) {
-  const int side = MT / cols, row = int(threadIdx.x) / cols, col = c0 + int(threadIdx.x) - row * cols;
+  const int side = MT / cols, row = int(threadIdx.x) / cols;
   const bool live = row < side;
-  const int32_t *kept = a.kept + (int64_t(b) * a.heads + h) * a.budget;
-  const int32_t *in = a.page_table + b * a.ld_table, *out = a.out_table + b * a.ld_out;
+  const int4 *ways = a.ways + (int64_t(b) * a.heads + h) * a.budget;
   const int R = side * MU;
-  cache += col;
+  cache += c0 + int(threadIdx.x) - row * cols;
   for (int j0 = rb * R; j0 < rows; j0 += R * a.row_blocks) {
+    int4 way[MU];
     V v[MU];
-    int from[MU], page[MU];  // key and its page; then, where it goes to
 #pragma unroll
     for (int u = 0; u < MU; ++u) {
       const int j = j0 + u * side + row;
-      from[u] = live && j < rows ? kept[j] : -1;
-      if (a.in_place && from[u] == j) from[u] = -1;
-    }
-#pragma unroll
-    for (int u = 0; u < MU; ++u) {
-      if (from[u] < 0) continue;
-      const int p = from[u] / a.page_size;
-      from[u] -= p * a.page_size;  // the place in its page
-      page[u] = in[p];
-      if (unsigned(page[u]) >= unsigned(a.num_pages)) {
-        set_status(a.status, WQ_ERR_INDEX);
-        from[u] = -1;
-      }
+      way[u].x = -1;
+      if (live && j < rows) way[u] = ways[j];
     }
 #pragma unroll
     for (int u = 0; u < MU; ++u)
-      if (from[u] >= 0) v[u] = cache[page[u] * pitch_page + from[u] * pitch_row];
-#pragma unroll
-    for (int u = 0; u < MU; ++u) {
-      if (from[u] < 0) continue;
-      const int j = j0 + u * side + row, p = j / a.page_size;
-      page[u] = out[p];
-      from[u] = j - p * a.page_size;
-      if (unsigned(page[u]) >= unsigned(a.num_pages)) {
-        set_status(a.status, WQ_ERR_INDEX);
-        from[u] = -1;
-      }
-    }
+      if (way[u].x >= 0) v[u] = cache[way[u].x * pitch_page + way[u].y * pitch_row];
     if (a.in_place) __syncthreads();
 #pragma unroll
     for (int u = 0; u < MU; ++u)
-      if (from[u] >= 0) cache[page[u] * pitch_page + from[u] * pitch_row] = v[u];
+      if (way[u].x >= 0) cache[way[u].z * pitch_page + way[u].w * pitch_row] = v[u];
   }
 }
 

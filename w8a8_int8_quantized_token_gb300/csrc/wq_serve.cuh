@@ -266,6 +266,7 @@ struct EvictArgs {
   int64_t o_seq, o_head;
   int32_t *new_len, *kept;
   int32_t *status;
+  int4 *ways;       // [B][heads][budget]: page and place that a row that stays comes from, and goes to
   int32_t *moving;  // sequences with rows to move: their number, then each
   // of the moving kernel: parts of the columns of keys and of values, of the rows
   int k_parts, v_parts, row_blocks;

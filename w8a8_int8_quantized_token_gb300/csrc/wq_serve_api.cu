@@ -449,7 +449,10 @@ int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_head, i
   return launch_weights(a, cache->dtype, stream);
 }
 
-size_t wq_evict_paged_workspace_size(int B) { return B < 1 ? 0 : (size_t(B) + 1) * sizeof(int32_t); }
+size_t wq_evict_paged_workspace_size(int B, int heads, int64_t budget) {
+  if (B < 1 || heads < 1 || budget < 1) return 0;
+  return size_t(B) * size_t(heads) * size_t(budget) * sizeof(int4) + (size_t(B) + 1) * sizeof(int32_t);
+}
 
 int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq_paged_cache *cache,
                    int B, const int32_t *page_table, int64_t ld_table, const int32_t *key_len,
@@ -474,7 +477,7 @@ int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq
       cache->dk > (1 << 14) || cache->dv > (1 << 14) || !al(cache->k, 2) || !al(cache->v, 2) || !al(weights, 4) ||
       !al(weights_out, 4))
     return WQ_ERR_UNSUPPORTED;
-  if (!ws || !al(ws, 16) || ws_bytes < wq_evict_paged_workspace_size(B)) return WQ_ERR_WORKSPACE;
+  if (!ws || !al(ws, 16) || ws_bytes < wq_evict_paged_workspace_size(B, cache->heads, budget)) return WQ_ERR_WORKSPACE;
   const int rc = device_ok();
   if (rc != WQ_OK) return rc;
   EvictArgs a{};
@@ -511,7 +514,8 @@ int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq
   a.new_len = new_len;
   a.kept = kept;
   a.status = status;
-  a.moving = static_cast<int32_t *>(ws);
+  a.ways = static_cast<int4 *>(ws);
+  a.moving = reinterpret_cast<int32_t *>(a.ways + int64_t(B) * a.heads * a.budget);
   bool vec = al(cache->k, 16) && al(cache->v, 16) && cache->dk % 8 == 0 && cache->dv % 8 == 0;
   for (int64_t p : {a.k_page, a.k_head, a.k_token, a.v_page, a.v_head, a.v_token}) vec = vec && p % 8 == 0;
   return launch_evict(a, vec, stream);
