@@ -136,7 +136,7 @@ struct Place {
 template <class F>
 __device__ __forceinline__ Place locate(const WeightArgs &a, int64_t *scan, int64_t *out, bool tell,
                                         F &&f) {
-  const int per = (a.B + NTHREADS - 1) / NTHREADS, b0 = threadIdx.x * per;
+  const int threads = int(blockDim.x), per = (a.B + threads - 1) / threads, b0 = threadIdx.x * per;
   auto cost = [&](int b, bool say) {
     const int c0 = first_of(a, b), c1 = first_of(a, b + 1), l = a.key_len[b];
     const Seq s = seq_of(a, c0, c1, l);
@@ -155,8 +155,7 @@ __device__ __forceinline__ Place locate(const WeightArgs &a, int64_t *scan, int6
   if (lane == 31) scan[warp] = sum;
   __syncthreads();
   int64_t total = 0, base = 0;
-#pragma unroll
-  for (int w = 0; w < NTHREADS / 32; ++w) {
+  for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) base += scan[w];
     total += scan[w];
   }
@@ -602,8 +601,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
 // Adds the parts of the pair that block c of the first kernel began and left
 // to the blocks after it, in their order.
-__global__ void __launch_bounds__(NTHREADS) attn_weights_join_kernel(const WeightArgs a) {
-  __shared__ int64_t scan[NTHREADS / 32], out[2];
+// (A thread a key, so that its blocks find room beside those of the first kernel.)
+__global__ void __launch_bounds__(PAIR) attn_weights_join_kernel(const WeightArgs a) {
+  __shared__ int64_t scan[PAIR / 32], out[2];
   const int64_t blocks = gridDim.x + 1, c = blockIdx.x;
   const Place at = locate(a, scan, out, false, [&](int64_t total) { return total * (c + 1) / blocks; });
   wait_last_kernel();  // in every block: what follows the join may then rely on both
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(NTHREADS) attn_weights_join_kernel(const Weigh
   if (w.u == 0 || start < at.total * c / blocks) return;
   const int64_t end = start + w.s.cost(w.p, a.shift);
   const int i = w.p * PAIR + threadIdx.x;
-  if (threadIdx.x >= PAIR || i >= w.s.len) return;
+  if (i >= w.s.len) return;
   float sum = a.part[(c * 2 + 1) * PAIR + threadIdx.x];
   int64_t lo = at.at;  // where block k begins
   for (int64_t k = c + 1; k < blocks && lo < end; ++k) {
@@ -699,7 +699,7 @@ int launch_tiles(const WeightArgs &a, cudaStream_t st) {
   k<<<unsigned(a.blocks), NTHREADS, Plan<D>::smem(a.cols, MANY), st>>>(mq, mk, a);
   int rc = launched(1);
   if (rc == WQ_OK && MANY && a.blocks > 1)
-    rc = attn::launch_chained(attn_weights_join_kernel, unsigned(a.blocks - 1), NTHREADS, 0, true, st, a);
+    rc = attn::launch_chained(attn_weights_join_kernel, unsigned(a.blocks - 1), PAIR, 0, true, st, a);
   return rc;
 }
 
