@@ -668,8 +668,8 @@ WQ_API int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_
  * step, after the attention.
  * max_q, max_len: host bounds, values above them are cut with status =
  * WQ_ERR_INDEX, as in the attention.  A page id outside [0, num_pages) sets the
- * same status; its keys count as zeros.  The cache's values (v) are not read.  Scores, weights and sums are float32 and do not depend on
- * the run.
+ * same status; its keys count as zeros.  The cache's values (v) are not read.
+ * Scores, weights and sums are float32 and do not depend on the run.
  * Requirements: those of wq_attention_shared_prefix on q and the keys; rows of
  * weights that share no place; decay >= 0.
  * Workspace: wq_attention_weights_paged_workspace_size() with the same
@@ -705,7 +705,9 @@ WQ_API int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_
  * with.
  * max_len: host bound on the lengths; longer ones are cut with status =
  * WQ_ERR_INDEX.  A page id outside [0, num_pages) sets the same status and its
- * rows are not moved.  key_len and new_len must not overlap.
+ * rows are not moved.  key_len and new_len must not overlap.  Keys and values may
+ * share elements if their pitches are the same (values that are a part of the
+ * keys).
  * Requirements: budget >= 1, first + recent <= budget, bf16 or fp16, dk and dv
  * at most 16384.  16-byte accesses serve keys, values and pitches in multiples
  * of 8 elements.  Workspace: wq_evict_paged_workspace_size(), 16 bytes
@@ -727,12 +729,12 @@ WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
  * A [n][r][H], B [n][N][r], x [T][H] (pitch ldx), y [T][N] (pitch ldy), all of
  * `dtype`, scales float [n] (NULL: ones), adapters int32 [T].  A token with a
  * negative adapter has none: its row of y is neither read nor written.  An
- * adapter at or past n counts as none and sets status = WQ_ERR_INDEX.  Tokens
- * of one adapter may stand anywhere.  Adapters of smaller rank are padded with
- * zeros.  Products and sums are float32; x A^T enters the second product with
- * twice the bits of dtype's significand, and y is rounded once.  A row's result
- * depends on its token, T and n alone, not on the tokens beside it.  y must not
- * overlap the other arguments.
+ * adapter at or past n counts as none and sets status = WQ_ERR_INDEX (with n = 0
+ * nothing is read).  Tokens of one adapter may stand anywhere.  Adapters of
+ * smaller rank are padded with zeros.  Products and sums are float32; x A^T enters
+ * the second product with twice the bits of dtype's significand, and y is rounded
+ * once.  A row's result depends on its token, T and n alone, not on the tokens
+ * beside it.  y must not overlap the other arguments.
  * Requirements: bf16 or fp16; H, N, r and pitches multiples of 8, r at most 128,
  * n at most 8192, 16-byte aligned tensors.  Workspace:
  * wq_lora_add_workspace_size(T, n, r) (0 bytes up to 256 tokens). */

@@ -206,3 +206,12 @@ def test_attention_over_the_keys_that_stayed():
             # bf16 weights and output: 2^-8 of the values that are weighed, and as much of the result
             tol = 2 ** -8 * (torch.softmax(x, -1) @ v.abs() + want.abs()) + 1e-4
             assert ((got[b * T:(b + 1) * T, h * G:(h + 1) * G].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("at,dv", [(0, 96), (0, 64), (32, 64), (5, 40)])
+def test_values_that_are_part_of_the_keys(apart, at, dv):
+    """Elements that keys and values share move once, in place too."""
+    a = problem([1500, 70, 9], 1 if at else 2, 96, dv, 16, BF, 64, apart, seed=at + dv)
+    a["v_cache"] = a["k_cache"][..., at:at + dv]
+    check(a, 8, 2)

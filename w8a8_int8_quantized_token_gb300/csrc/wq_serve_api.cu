@@ -1,5 +1,6 @@
 // C ABI of the serving operators around the MoE layer: host-side argument
 // checks.  Contracts are in include/wq.h.
+#include <algorithm>
 #include <cmath>
 
 #include "wq_serve.cuh"
@@ -497,6 +498,15 @@ int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq
   a.heads = cache->heads;
   a.dk = cache->dk;
   a.dv = cache->dv;
+  auto alike = [](int64_t extent, int64_t k, int64_t v) { return extent <= 1 || k == v; };
+  if (a.k && a.k < a.v + a.dv && a.v < a.k + a.dk && alike(a.num_pages, a.k_page, a.v_page) &&
+      alike(a.heads, a.k_head, a.v_head) && alike(a.page_size, a.k_token, a.v_token)) {
+    // elements that both have move once
+    uint16_t *end = std::max(a.k + a.dk, a.v + a.dv);
+    a.k = std::min(a.k, a.v);
+    a.dk = int(end - a.k);
+    a.dv = 0;
+  }
   a.B = B;
   a.page_table = page_table;
   a.ld_table = ld_table;
