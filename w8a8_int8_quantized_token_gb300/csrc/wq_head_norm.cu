@@ -9,7 +9,8 @@
 // rotation.  The lanes of a head are neighbours in a warp and add their sums by
 // shuffles; with many tokens a lane takes the same place of two heads, which
 // share the table row's and the weight's part.  Bound by HBM: every element is
-// read once and written once; table rows come from L2.
+// read once and written once; table rows come from L2.  8191 tokens of 40 query
+// heads, 8 keys and 8 values of 128 bf16 take 45 us, 5.2 TB/s, at 0.70 of issue.
 #include <algorithm>
 
 #include "wq_warp_mma.cuh"
@@ -222,7 +223,8 @@ __global__ void __launch_bounds__(256) head_norm_vec_kernel(const __grid_constan
 // copy their own vectors of the tokens to come, and the tokens' table rows
 // together, into shared memory.  Where 32 tokens go and which rows they take is
 // found by a lane each, so that neither the chain of loads (slot or position,
-// page or row) nor the divisions stand in a token's way.
+// page or row) nor the divisions stand in a token's way.  (8191 tokens: a warp a
+// token 83 us, walking with slot, position and row one token ahead 59, so 45.)
 constexpr int STAGES = 3;
 template <class DT, int KH>
 __global__ void __launch_bounds__(256, 3) head_norm_stream_kernel(const __grid_constant__ HeadNormArgs h,
@@ -404,7 +406,7 @@ int launch_t(const HeadNormArgs &h, bool vec, cudaStream_t st) {
     vec = vec && lanes_of(h.r.seg[i], W) <= 32;
     lanes += h.r.T * h.r.seg[i].heads * lanes_of(h.r.seg[i], W);
   }
-  // walks over tokens once each warp has several
+  // walks over tokens once each of three blocks an SM has several
   if (vec) return lanes > 2 * 3 * 152 * 256 * 3 ? launch_vec<DT, true>(h, st) : launch_vec<DT, false>(h, st);
   int per_token = 0;
   for (int i = 0; i < h.r.nseg; ++i) per_token += h.r.seg[i].heads;

@@ -16,7 +16,10 @@
 // copied by 16-byte pieces (eight lanes a row), which land in the products'
 // swizzled layout.  H enters the second product from tensor memory as two 16-bit
 // operands, its rounding and what that leaves, as in the kernel for few tokens.
-// Bound by HBM: x once, y twice; the adapters come from L2.
+// Bound by HBM: x once, y twice; the adapters come from L2.  8192 tokens of width
+// 7168 and rank 64 take 86 us (4.1 TB/s), the list of tiles among them (8); with
+// cold caches and 4096 tokens 28 us (2.0 TB/s of x: the parts' sum and the start
+// are as long as the steps) and 31 (3.8 TB/s of y).
 //
 // Every wait on a memory barrier is bounded (1 s); on expiry the kernel records
 // WQ_ERR_TIMEOUT, waits (bounded) for its own copies and MMAs, frees tensor
@@ -436,6 +439,11 @@ __global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraA
 
 template <class DT, int RP>
 int launch_one(const LoraArgs &a, int64_t tiles, cudaStream_t st) {
+  // lora_up_kernel's blocks may be there before lora_down_kernel's have their
+  // tensor memory, and wait for those: no SM holds two of the first and one of
+  // the second, so that there is always some left.
+  static_assert(2 * Up<RP>::SMEM + Down<RP>::SMEM > 228 * 1024 && Up<RP>::COLS + Down<RP>::COLS <= 512,
+                "tensor memory of blocks that share an SM");
   auto *down = lora_down_kernel<DT, RP>;
   auto *up = lora_up_kernel<DT, RP>;
   static OncePerDevice sized, sized_up;
