@@ -103,3 +103,49 @@ def test_without_eviction_the_weights_are_the_tokens(q):
     assert ((total / (3 * q * s.Hq // s.Hkv)) - 1).abs().max() < 1e-4
     assert torch.equal(s.kept[0, 0, :int(s.len[0])].cpu(), torch.arange(int(s.len[0]), dtype=torch.int32))
     assert int(s.status) == 0
+
+
+def test_calls_on_streams_of_their_own_are_the_calls_alone():
+    """Adapters of many tokens twice, few tokens, weights and eviction side by
+    side, each call with its own workspace."""
+    g = torch.Generator().manual_seed(3)
+    rand = lambda *s, scale=1.0: (torch.randn(*s, generator=g) * scale).to(BF).cuda()
+    status = wq.new_status()
+    x, A, Bm = rand(2300, 512), rand(4, 64, 512, scale=512 ** -0.5), rand(4, 1024, 64, scale=0.125)
+    ids = torch.randint(-1, 4, (2300,), generator=g).to(torch.int32).cuda()
+    pt = torch.randperm(4 * 32, generator=g).to(torch.int32).reshape(4, 32).cuda()
+    q, kc, vc = rand(4 * 100, 8, 128), rand(4 * 32, 2, 64, 128), rand(4 * 32, 2, 64, 128)
+    n, w0 = torch.tensor([2048, 1500, 100, 777], dtype=torch.int32).cuda(), torch.rand(4, 2, 2048, generator=g).cuda()
+    lse = torch.full((400, 8), 4.0).cuda()
+
+    def adapters(T):
+        y0 = rand(T, 1024)
+        def call():
+            return [wq.lora_add(y0.clone(), x[:T], A, Bm, ids[:T], status=status)]
+        return call
+
+    def weights():
+        return [wq.attention_weights_paged(q, kc, pt, n, 2048, lse, w0.clone(), status=status)]
+
+    def evict():
+        k, v, w = kc.clone(), vc.clone(), w0.clone()
+        return [*wq.evict_paged(w, k, v, pt, n, 2048, 700, recent=30, first=2, status=status), k, v, w[..., :700].clone()]
+
+    calls = [adapters(2300), weights, adapters(2000), evict, adapters(100)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[] for _ in calls]
+    for _ in range(5):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(c())
+    torch.cuda.synchronize()
+    for name, w, runs in zip("abcde", want, got):
+        for run in runs:
+            for a, b in zip(run, w):
+                if a.dim() == 3 and a.shape[-1] == 700 and a.dtype == torch.float32:
+                    rows = torch.arange(700, device="cuda") < n.clamp(max=700)[:, None, None]
+                    a, b = a.where(rows, 0), b.where(rows, 0)
+                assert torch.equal(a, b), name
+    assert int(status) == 0
