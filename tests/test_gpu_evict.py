@@ -215,3 +215,16 @@ def test_values_that_are_part_of_the_keys(apart, at, dv):
     a = problem([1500, 70, 9], 1 if at else 2, 96, dv, 16, BF, 64, apart, seed=at + dv)
     a["v_cache"] = a["k_cache"][..., at:at + dv]
     check(a, 8, 2)
+
+
+@pytest.mark.parametrize("n", [131, 515, 2050, 6000, 40000])
+@pytest.mark.parametrize("kind", ["equal", "three", "last bits", "middle bits"])
+def test_weights_that_share_their_digits(n, kind):
+    """Keys that the first digits do not tell apart, more and fewer than a block
+    gathers or ranks, and equal ones."""
+    i = torch.arange(n + 3)
+    mixed = (i * 7919) % 4099
+    w = {"equal": torch.full((n + 3,), 0.5), "three": (mixed % 3).float(),
+         "last bits": 1 + mixed * 2.0 ** -23, "middle bits": 1 + (mixed % 300) * 2.0 ** -16}[kind]
+    a = problem([n, n // 2], 1, 32, 32, 64, BF, max(n // 3, 8), True, weights=lambda x: w.float().expand_as(x).contiguous())
+    check(a, 3, 1)

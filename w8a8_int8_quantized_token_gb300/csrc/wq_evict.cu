@@ -8,13 +8,15 @@
 // same order, and the key of the last one that stays is found digit by digit
 // from the top.  A digit is a histogram in shared memory, whose bins are added
 // over the cluster, and a scan over them.  As soon as few keys share the digits
-// found so far, which is mostly after the first one, they are gathered and
-// ranked against one another.  Then every warp counts the larger and the equal
+// found so far, which is mostly after the first one, every block gathers them and
+// goes on by itself, without the cluster's barriers, and ranks the last ones
+// against one another.  Then every warp counts the larger and the equal
 // keys of its own part, the counts before it give each its place, and the
 // places that stay are written in order; of equal keys the first stay.  Neither
 // counts nor ranks depend on the order of the atomics that take them.  Bound by
 // latency: about ten steps with a barrier each (the cluster's between some).
-// 8 heads of 32768 keys take 21 us with cold caches, a block for 4096 of them.
+// Both kernels take 22 us for 8 heads of 32768 keys, a block for 4096 of them
+// (25 with the last 512 keys ranked and a second digit over the cluster before).
 //
 // evict_move_kernel packs the rows that stay, in their order.  A row goes to a
 // place at or before its own, so in place no row may be written before all
@@ -42,7 +44,8 @@ using attn::wait_last_kernel;
 
 constexpr int NT = 512, NW = NT / 32;  // threads, warps of the selection
 constexpr int BINS = 2048;
-constexpr int FEW = 512;               // keys that are ranked against one another
+constexpr int FEW = 2048;              // keys that a block gathers
+constexpr int LAST = 128;              // keys that are ranked against one another
 constexpr int MOST_BLOCKS = 8;         // of a cluster
 
 // Unsigned key in the order of the weights: -0 as 0, NaN below everything
@@ -86,30 +89,25 @@ __device__ __forceinline__ const T *of_block(const T *p, int rank) {
 
 struct Shared {
   int hist[2][BINS];     // of digits in turn: a block may be a digit ahead of one that reads its bins
-  uint2 few[FEW];        // key and place of the block's keys with the digits found
-  uint2 all[FEW];        // of the cluster's
-  int counts[2];         // the block's larger keys, equal keys
+  uint32_t few[FEW];     // the block's keys with the digits found
+  uint32_t all[FEW];     // the cluster's
+  int2 counts;           // the block's larger keys, equal keys
   int part[NW], part2[NW];
-  int taken, left, digit, need;
+  int taken, last, left, digit, need;
 };
+constexpr int STAGE_BYTES = 192 * 1024;  // of weights in shared memory, at most
+static_assert(STAGE_BYTES + sizeof(Shared) <= 232448, "shared memory plan");
 
 // STAGED: a block's stretch of the weights between the first and the recent
 // keys fits shared memory
 template <bool STAGED>
-__global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int C) {
+__global__ void __launch_bounds__(NT, 2) evict_select_kernel(const EvictArgs a, int C) {
   extern __shared__ float staged[];
   __shared__ Shared sm;
-  const int bh = int(blockIdx.x) / C, rank = int(blockIdx.x) - bh * C;
-  const int b = bh / a.heads, h = bh - b * a.heads;
+  const int cluster = int(blockIdx.x) / C, rank = int(blockIdx.x) - cluster * C;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  start_next_kernel();
-  const int n = length_of(a, b), fresh = min(n, a.budget);
-  if (h == 0 && rank == 0 && threadIdx.x == 0) {
-    a.new_len[b] = fresh;
-    if (n != a.key_len[b]) set_status(a.status, WQ_ERR_INDEX);
-  }
-  if (blockIdx.x == 0) {
-    // the sequences with rows to move, for the other kernel
+  if (cluster == 0) {  // the sequences with rows to move, for the other kernel
+    if (rank > 0) return;
     int count = 0;
     for (int b0 = 0; b0 < a.B; b0 += NT) {
       const int q = b0 + int(threadIdx.x), len = q < a.B ? length_of(a, q) : 0;
@@ -120,6 +118,13 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
       count += total;
     }
     if (threadIdx.x == 0) a.moving[0] = count;
+    return;
+  }
+  const int b = (cluster - 1) / a.heads, h = cluster - 1 - b * a.heads;
+  const int n = length_of(a, b), fresh = min(n, a.budget);
+  if (h == 0 && rank == 0 && threadIdx.x == 0) {
+    a.new_len[b] = fresh;
+    if (n != a.key_len[b]) set_status(a.status, WQ_ERR_INDEX);
   }
   const float *w = a.w + b * a.w_seq + h * a.w_head;
   const float *w_row = w;
@@ -166,56 +171,13 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
     if (C > 1) tc::cluster_sync();
     else __syncthreads();
   };
-  for (int i = threadIdx.x; i < 2 * BINS; i += NT) sm.hist[0][i] = 0;
-  if (threadIdx.x == 0) sm.taken = 0;
-  __syncthreads();
   uint32_t prefix = 0;
   int left = mid;  // keys that begin with prefix
   int bits_left = 32;
-#pragma unroll 1
-  for (int digit = 0; digit < 3 && left > FEW; ++digit) {
-    const int bits = digit == 2 ? 10 : 11, shift = bits_left - bits;
-    int *hist = sm.hist[digit & 1];
-    if (digit == 2) {  // the first digit's bins: all have read them before the second's were together
-      for (int i = threadIdx.x; i < BINS; i += NT) hist[i] = 0;
-      __syncthreads();
-    }
-    if (digit == 0) {
-      constexpr int U = 8;
-      for (int i0 = threadIdx.x; i0 < size; i0 += U * NT) {
-        float f[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (i0 + u * NT < size) f[u] = w[i0 + u * NT];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (i0 + u * NT >= size) break;
-          if (STAGED) staged[i0 + u * NT] = f[u];
-          atomicAdd(&hist[key_of(f[u]) >> shift], 1);
-        }
-      }
-    } else {
-#pragma unroll 4
-      for (int i = threadIdx.x; i < size; i += NT) {
-        const uint32_t k = at(i);
-        if ((k >> bits_left) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
-      }
-    }
-    together();
-    // bins from the top, over the cluster: thread t has the t-th four
-    const int top = BINS - 4 - 4 * int(threadIdx.x);
-    int4 c = make_int4(0, 0, 0, 0), v[MOST_BLOCKS];
-#pragma unroll
-    for (int r = 0; r < MOST_BLOCKS; ++r)
-      if (r < C) v[r] = *reinterpret_cast<const int4 *>(of_block(&hist[top], r));
-#pragma unroll
-    for (int r = 0; r < MOST_BLOCKS; ++r) {
-      if (r >= C) break;
-      c.x += v[r].x;
-      c.y += v[r].y;
-      c.z += v[r].z;
-      c.w += v[r].w;
-    }
+  auto begins = [&](uint32_t k) { return bits_left == 32 || (k >> bits_left) == prefix; };
+  // One digit more, of `bits` bits: c has this thread's four bins, from the top
+  const int top = BINS - 4 - 4 * int(threadIdx.x);
+  auto pick = [&](const int4 &c, int bits) {
     const int own = c.x + c.y + c.z + c.w;
     int total;
     const int upto = block_scan(own, sm.part, total);
@@ -230,51 +192,147 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
       sm.left = in;
     }
     __syncthreads();
-    prefix = digit == 0 ? uint32_t(sm.digit) : (prefix << bits) | uint32_t(sm.digit);
+    prefix = (prefix << bits) | uint32_t(sm.digit);
     need = sm.need;  // of the keys that begin with prefix
     left = sm.left;
-    bits_left = shift;
+    bits_left -= bits;
     __syncthreads();
-  }
-  if (bits_left > 0) {
-    // few are left: rank them
-    for (int i = threadIdx.x; i < size; i += NT) {
-      uint32_t k;
-      if (STAGED && bits_left == 32) {
-        const float f = w[i];
-        staged[i] = f;
-        k = key_of(f);
-      } else {
-        k = at(i);
+  };
+  const int few = C > 1 ? FEW : FEW / 4;  // a digit costs a block alone no more than gathering does
+  const bool digits = left > few;
+  {
+    constexpr int U = 8;
+    float f[U];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * NT < size) f[u] = w[i0 + u * NT];
+    };
+    if (STAGED || digits) load(threadIdx.x);
+    for (int i = threadIdx.x; i < 2 * BINS; i += NT) sm.hist[0][i] = 0;
+    if (threadIdx.x == 0) sm.taken = sm.last = 0;
+    __syncthreads();
+    if (STAGED || digits) {
+      for (int i0 = threadIdx.x; i0 < size; i0 += U * NT) {
+        if (i0 != int(threadIdx.x)) load(i0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (i0 + u * NT >= size) break;
+          if (STAGED) staged[i0 + u * NT] = f[u];
+          if (digits) atomicAdd(&sm.hist[0][key_of(f[u]) >> 21], 1);
+        }
       }
-      if (bits_left == 32 || (k >> bits_left) == prefix) sm.few[atomicAdd(&sm.taken, 1)] = make_uint2(k, uint32_t(lo + i));
+    }
+  }
+#pragma unroll 1
+  for (int digit = 0; digit < 3 && left > few; ++digit) {
+    const int bits = digit == 2 ? 10 : 11, shift = bits_left - bits;
+    int *hist = sm.hist[digit & 1];
+    if (digit == 2) {  // the first digit's bins: all have read them before the second's were together
+      for (int i = threadIdx.x; i < BINS; i += NT) hist[i] = 0;
+      __syncthreads();
+    }
+    if (digit > 0) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < size; i += NT) {
+        const uint32_t k = at(i);
+        if (begins(k)) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+      }
     }
     together();
-    int from = 0;
-    for (int r = 0; r < C; ++r) {
-      const int c = *of_block(&sm.taken, r);
-      for (int i = threadIdx.x; i < c; i += NT) sm.all[from + i] = of_block(sm.few, r)[i];
-      from += c;
-    }
-    __syncthreads();
-    // the one that need - 1 others come before (larger, or equal and earlier)
-    for (int i = threadIdx.x; i < left; i += NT) {
-      const uint2 x = sm.all[i];
-      int before = 0, larger = 0;
-      for (int j = 0; j < left; ++j) {
-        const uint2 y = sm.all[j];
-        larger += y.x > x.x;
-        before += y.x > x.x || (y.x == x.x && y.y < x.y);
-      }
-      if (before == need - 1) {
-        sm.digit = int(x.x);
-        sm.need = need - larger;
+    int4 c = *reinterpret_cast<const int4 *>(&hist[top]);
+    if (C > 1) {
+      int4 v[MOST_BLOCKS];
+#pragma unroll
+      for (int r = 1; r < MOST_BLOCKS; ++r)
+        if (r < C) v[r] = *reinterpret_cast<const int4 *>(of_block(&hist[top], (rank + r) & (C - 1)));
+#pragma unroll
+      for (int r = 1; r < MOST_BLOCKS; ++r) {
+        if (r >= C) break;
+        c.x += v[r].x;
+        c.y += v[r].y;
+        c.z += v[r].z;
+        c.w += v[r].w;
       }
     }
-    __syncthreads();
-    prefix = uint32_t(sm.digit);
-    need = sm.need;  // of the keys equal to prefix
+    pick(c, bits);
   }
+  if (bits_left > 0) {
+    // few are left: every block takes them all (a thread's own keys are staged by itself)
+    for (int i0 = warp * 32; i0 < size; i0 += NT) {
+      const int i = i0 + lane;
+      const uint32_t k = i < size ? at(i) : 0u;
+      const bool take = i < size && begins(k);
+      const uint32_t m = __ballot_sync(0xffffffffu, take);
+      int from = 0;
+      if (lane == 0 && m) from = atomicAdd(&sm.taken, __popc(m));
+      from = __shfl_sync(0xffffffffu, from, 0);
+      if (take) sm.few[from + __popc(m & ((1u << lane) - 1u))] = k;
+    }
+    together();
+    if (left > LAST) {  // none reads another block's bins any more
+      for (int i = threadIdx.x; i < BINS; i += NT) sm.hist[0][i] = 0;
+    }
+    const uint32_t *keys = C > 1 ? sm.all : sm.few;
+    const int all_left = left;
+    if (C > 1) {
+      int c[MOST_BLOCKS];
+#pragma unroll
+      for (int r = 0; r < MOST_BLOCKS; ++r) c[r] = r < C ? *of_block(&sm.taken, r) : 0;
+      for (int i = threadIdx.x; i < left; i += NT) {
+        int r = 0, j = i;
+#pragma unroll
+        for (int q = 0; q < MOST_BLOCKS - 1; ++q)
+          if (r == q && j >= c[q]) j -= c[q], ++r;
+        sm.all[i] = *of_block(&sm.few[j], r);
+      }
+    }
+    if (C > 1 || left > LAST) __syncthreads();
+#pragma unroll 1
+    while (left > LAST && bits_left > 0) {
+      const int bits = min(bits_left, 11), shift = bits_left - bits;
+      for (int i = threadIdx.x; i < all_left; i += NT) {
+        const uint32_t k = keys[i];
+        if (begins(k)) atomicAdd(&sm.hist[0][(k >> shift) & ((1u << bits) - 1)], 1);
+      }
+      __syncthreads();
+      int4 *own = reinterpret_cast<int4 *>(&sm.hist[0][top]);
+      const int4 c = *own;
+      *own = make_int4(0, 0, 0, 0);
+      pick(c, bits);
+    }
+    if (bits_left > 0) {
+      if (left < all_left) {
+        uint32_t *last = reinterpret_cast<uint32_t *>(sm.hist[1]);
+        for (int i = threadIdx.x; i < all_left; i += NT) {
+          const uint32_t k = keys[i];
+          if (begins(k)) last[atomicAdd(&sm.last, 1)] = k;
+        }
+        keys = last;
+        __syncthreads();
+      }
+      // the key that is the need-th from the top
+      if (int(threadIdx.x) < left) {
+        const uint32_t x = keys[threadIdx.x];
+        int larger = 0, same = 0;
+        for (int j = 0; j < left; ++j) {
+          const uint32_t y = keys[j];
+          larger += y > x;
+          same += y == x;
+        }
+        if (larger < need && need <= larger + same) {  // equal ones write the same
+          sm.digit = int(x);
+          sm.need = need - larger;
+        }
+      }
+      __syncthreads();
+      prefix = uint32_t(sm.digit);
+      need = sm.need;  // of the keys equal to prefix
+    }
+  }
+  // The moving kernel's blocks come in from here on.  Earlier, they take the
+  // place of blocks with work still to do (64 sequences 26.0 us, so 24.5).
+  start_next_kernel();
   // keys above `prefix` stay, and the first `need` of those equal to it
   const int stretch = ((size + NW - 1) / NW + 31) / 32 * 32;
   const int s0 = min(warp * stretch, size), s1 = min(s0 + stretch, size);
@@ -296,14 +354,16 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(const EvictArgs a, int
       m += __shfl_xor_sync(0xffffffffu, m, o);
       e += __shfl_xor_sync(0xffffffffu, e, o);
     }
-    if (lane == 0) sm.counts[0] = m, sm.counts[1] = e;
+    if (lane == 0) sm.counts = make_int2(m, e);
   }
   together();
   int j = first, equal = 0;
-  for (int r = 0; r < rank; ++r) {
-    const int *c = of_block(sm.counts, r);
-    j += c[0];
-    equal += c[1];
+  if (rank > 0) {
+    int2 c[MOST_BLOCKS];
+#pragma unroll
+    for (int r = 0; r < MOST_BLOCKS; ++r) c[r] = r < rank ? *of_block(&sm.counts, r) : make_int2(0, 0);
+#pragma unroll
+    for (int r = 0; r < MOST_BLOCKS; ++r) j += c[r].x, equal += c[r].y;
   }
   for (int v = 0; v < warp; ++v) j += sm.part[v], equal += sm.part2[v];
   j += min(equal, need);
@@ -427,9 +487,9 @@ template <bool STAGED>
 int launch_select(const EvictArgs &a, int C, int smem, cudaStream_t st) {
   auto *k = evict_select_kernel<STAGED>;
   static OncePerDevice sized;
-  if (!allow_smem(sized, k, STAGED ? 200 * 1024 : 1024)) return WQ_ERR_LAUNCH;
+  if (!allow_smem(sized, k, STAGED ? STAGE_BYTES : 1024)) return WQ_ERR_LAUNCH;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.heads * C));
+  cfg.gridDim = dim3(unsigned((int64_t(a.B) * a.heads + 1) * C));
   cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
@@ -451,9 +511,9 @@ int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st) {
   const int64_t bh = int64_t(a.B) * a.heads;
   int C = 1;
   while (C < MOST_BLOCKS && a.max_len > 4096 * C && 2 * C * bh <= 152) C *= 2;
-  if (bh * C >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
+  if ((bh + 1) * C >= (int64_t(1) << 31)) return WQ_ERR_UNSUPPORTED;
   const int64_t stretch = (int64_t(a.max_len) + C - 1) / C * 4;
-  const int rc = stretch <= 200 * 1024 ? launch_select<true>(a, C, int(stretch), st) : launch_select<false>(a, C, 0, st);
+  const int rc = stretch <= STAGE_BYTES ? launch_select<true>(a, C, int(stretch), st) : launch_select<false>(a, C, 0, st);
   if (rc != WQ_OK) return rc;
   return vec ? launch_move<uint4>(a, st) : launch_move<uint16_t>(a, st);
 }
