@@ -440,8 +440,6 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   __shared__ int part[2][32];
   start_next_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < a.n; i += kGroupThreads) cnt[i] = 0;
-  __syncthreads();
   constexpr int E = 8;  // tokens a thread looks at together
   auto load = [&](int t0, int(&id)[E]) {
 #pragma unroll
@@ -457,6 +455,8 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   };
   int id[E];
   load(0, id);
+  for (int i = threadIdx.x; i < a.n; i += kGroupThreads) cnt[i] = 0;
+  __syncthreads();
   // one atomic for the lanes that agree
   auto take = [&](int id) {
     const uint32_t m = __match_any_sync(0xffffffffu, id);
@@ -469,7 +469,10 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   for (int t0 = 0; t0 < a.T; t0 += E * kGroupThreads) {
     if (t0) load(t0, id);
 #pragma unroll
-    for (int e = 0; e < E; ++e) place[e] = take(id[e]);
+    for (int e = 0; e < E; ++e) {
+      if (t0 + e * kGroupThreads >= a.T) break;
+      place[e] = take(id[e]);
+    }
   }
   __syncthreads();
   // first place and first tile of each adapter: a thread has a stretch of them
@@ -483,11 +486,14 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
   }
   if (lane == 31) part[0][warp] = st, part[1][warp] = sl;
   __syncthreads();
-  int at = st - tokens, tile = sl - tiles, all = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w < warp) at += part[0][w], tile += part[1][w];
-    all += part[1][w];
+  int pt = part[0][lane], pl = part[1][lane];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, pt, o), v = __shfl_up_sync(0xffffffffu, pl, o);
+    if (lane >= o) pt += u, pl += v;
   }
+  const int before = max(warp - 1, 0), all = __shfl_sync(0xffffffffu, pl, 31);
+  const int bt = __shfl_sync(0xffffffffu, pt, before), bl = __shfl_sync(0xffffffffu, pl, before);
+  int at = st - tokens + (warp ? bt : 0), tile = sl - tiles + (warp ? bl : 0);
   for (int i = n0; i < n1; ++i) {
     const int c = cnt[i];
     for (int k = 0; k < c; k += size) {
