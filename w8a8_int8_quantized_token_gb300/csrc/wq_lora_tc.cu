@@ -17,7 +17,7 @@
 // swizzled layout.  H enters the second product from tensor memory as two 16-bit
 // operands, its rounding and what that leaves, as in the kernel for few tokens.
 // Bound by HBM: x once, y twice; the adapters come from L2.  8192 tokens of width
-// 7168 and rank 64 take 86 us (4.1 TB/s), the list of tiles among them (8); with
+// 7168 and rank 64 take 85 us (4.1 TB/s), the list of tiles among them (7); with
 // cold caches and 4096 tokens 28 us (2.0 TB/s of x: the parts' sum and the start
 // are as long as the steps) and 31 (3.8 TB/s of y).
 //
