@@ -732,9 +732,10 @@ WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
  * adapter at or past n counts as none and sets status = WQ_ERR_INDEX (with n = 0
  * nothing is read).  Tokens of one adapter may stand anywhere.  Adapters of
  * smaller rank are padded with zeros.  Products and sums are float32; x A^T enters
- * the second product with twice the bits of dtype's significand, and y is rounded
- * once.  A row's result depends on its token, T and n alone, not on the tokens
- * beside it.  y must not overlap the other arguments.
+ * the second product with all its 24 bits (fp16: with 22, counted from the largest
+ * of the row's), and y is rounded once.  A row's result depends on its token, T
+ * and n alone, not on the tokens beside it.  y must not overlap the other
+ * arguments.
  * Requirements: bf16 or fp16; H, N, r and pitches multiples of 8, r at most 128,
  * n at most 8192, 16-byte aligned tensors.  Workspace:
  * wq_lora_add_workspace_size(T, n, r) (0 bytes up to 256 tokens). */

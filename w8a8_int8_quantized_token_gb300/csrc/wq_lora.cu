@@ -17,10 +17,10 @@
 // two memory latencies (width 7168, rank 16: one token 6.2 us, of which a launch
 // takes 2.5; 128 tokens over 32 adapters 10.5).
 //
-// x A^T is summed in float32 and enters the second product as two 16-bit
-// operands, its rounding and what that leaves (16 bits of it together), so that
-// only y is rounded.  fp16 operands are taken relative to a power of two near a
-// row's largest, which keeps them in range.
+// x A^T is summed in float32 and enters the second product as 16-bit operands,
+// its rounding and what that leaves: three of them in bf16, which hold all 24
+// bits, two in fp16, taken relative to a power of two near a row's largest, which
+// keeps them in range.  So only y is rounded.
 #include <algorithm>
 
 #include "wq_attn.cuh"
@@ -46,8 +46,9 @@ constexpr int NC = WK * 32;  // columns of y a stage of the second
 // RP: rank in whole 16s.  The second product's stages hold rows of B and the
 // columns of y that they go to, and the first ones are on their way from the
 // start; with ranks over 64 they take the first product's place.
-template <int RP>
+template <class DT, int RP>
 struct Plan {
+  static constexpr int OPS = kLoraOperands<DT>;
   static constexpr bool EARLY = RP < 128;
   static constexpr int XB = BM * KS * 2, AB = RP * KS * 2;
   static constexpr int N1 = RP < 128 ? 4 : 2;      // stages of the first product
@@ -57,8 +58,8 @@ struct Plan {
   static constexpr int HP = BP;                    // bytes of a row of the intermediate
   static constexpr int RED = WK * BM * RP * 4;     // the warps' sums
   static constexpr int OFF_1 = 0;                  // first product's stages, then the warps' sums and the operands
-  static constexpr int OFF_H = OFF_1 + RED;        // [2][BM] rows: high and low operands
-  static constexpr int S0 = N1 * (XB + AB) > RED + 2 * BM * HP ? N1 * (XB + AB) : RED + 2 * BM * HP;
+  static constexpr int OFF_H = OFF_1 + RED;        // [OPS][BM] rows: the operands, high ones first
+  static constexpr int S0 = N1 * (XB + AB) > RED + OPS * BM * HP ? N1 * (XB + AB) : RED + OPS * BM * HP;
   static constexpr int S2 = N2 * (BB + YB);
   static constexpr int OFF_B = EARLY ? S0 : 0;     // second product's stages: rows of B, columns of y
   static constexpr int OFF_Y = OFF_B + N2 * BB;
@@ -142,7 +143,7 @@ __device__ __forceinline__ int find_tile(const LoraArgs &a, int tile, int *tok, 
 
 template <class DT, int RP>
 __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
-  using P = Plan<RP>;
+  using P = Plan<DT, RP>;
   extern __shared__ __align__(128) uint8_t sm[];
   const uint32_t base = tc::smem_u32(sm);
   int *tok = reinterpret_cast<int *>(sm + P::OFF_TOK);
@@ -344,23 +345,25 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
       up[row] = scale;
     }
     for (int c = lane; c < RP; c += 32) {
-      const float v = __fmul_rn(h[row * RP + c], down);
-      const uint16_t hi = DT::from_f(v);
-      const float f = DT::to_f(hi);
+      float v = __fmul_rn(h[row * RP + c], down);
       uint8_t *to = sm + P::OFF_H + row * P::HP + c * 2;
-      *reinterpret_cast<uint16_t *>(to) = hi;
-      *reinterpret_cast<uint16_t *>(to + BM * P::HP) = fabsf(f) == INFINITY ? uint16_t(0) : DT::from_f(v - f);
+#pragma unroll
+      for (int q = 0; q < P::OPS; ++q) {
+        const uint16_t w = DT::from_f(v);
+        *reinterpret_cast<uint16_t *>(to + q * BM * P::HP) = w;
+        v = lora_rest(v, DT::to_f(w));
+      }
     }
   }
   __syncthreads();
 
   // ---- second product, and the sum with y
-  uint32_t fh[2][RP / 16][4];
+  uint32_t fh[P::OPS][RP / 16][4];
 #pragma unroll
-  for (int part2 = 0; part2 < 2; ++part2)
+  for (int q = 0; q < P::OPS; ++q)
 #pragma unroll
     for (int k = 0; k < RP / 16; ++k)
-      ldsm4(fh[part2][k], base + P::OFF_H + uint32_t((part2 * BM + (lane & 15)) * P::HP + (2 * k + (lane >> 4)) * 16));
+      ldsm4(fh[q][k], base + P::OFF_H + uint32_t((q * BM + (lane & 15)) * P::HP + (2 * k + (lane >> 4)) * 16));
   const int r0 = (lane >> 2), r1 = r0 + 8;
   const float up0 = up[r0], up1 = up[r1];
   uint16_t *y0 = a.y + int64_t(r0 < count ? tok[r0] : 0) * a.ldy, *y1 = a.y + int64_t(r1 < count ? tok[r1] : 0) * a.ldy;
@@ -395,7 +398,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
         uint32_t fb[4];
         ldsm4(fb, bs + uint32_t((p * 16 + (lane & 7) + ((lane >> 4) << 3)) * P::BP + (2 * k + ((lane >> 3) & 1)) * 16));
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < P::OPS; ++q) {
           mma<DT>(d[2 * p], fh[q][k], fb[0], fb[1]);
           mma<DT>(d[2 * p + 1], fh[q][k], fb[2], fb[3]);
         }
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const LoraArg
 
 template <class DT, int RP>
 int launch_one(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
-  using P = Plan<RP>;
+  using P = Plan<DT, RP>;
   auto *k = lora_kernel<DT, RP>;
   static OncePerDevice sized;
   if (!allow_smem(sized, k, P::SMEM)) return WQ_ERR_LAUNCH;
@@ -582,7 +585,7 @@ size_t lora_lay_out(LoraArgs &a, char *at) {
   if (!few(T, a.r)) {
     take(a.tickets, tiles);
     take(a.factors, T);
-    take(a.operands, T * RP);
+    take(a.operands, T * RP / 2 * kLoraMostOperands);
     take(a.parts, lora_slices(tiles_like(T, a.n, a.r)) * T * RP);
   }
   return n;

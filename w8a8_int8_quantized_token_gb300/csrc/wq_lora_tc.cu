@@ -14,10 +14,12 @@
 // Blocks have warps that copy, one that issues the products, and warps that own
 // a token a thread.  Tokens of an adapter lie anywhere, so rows of x and y are
 // copied by 16-byte pieces (eight lanes a row), which land in the products'
-// swizzled layout.  H enters the second product from tensor memory as two 16-bit
+// swizzled layout.  H enters the second product from tensor memory as 16-bit
 // operands, its rounding and what that leaves, as in the kernel for few tokens.
 // Bound by HBM: x once, y twice; the adapters come from L2.  8192 tokens of width
-// 7168 and rank 64 take 85 us (4.1 TB/s), the list of tiles among them (7); with
+// 7168 and rank 64 take 90 us (3.9 TB/s), the list of tiles among them (7); with
+// two bf16 operands in place of three 85, and a result further off (0.0021 of the
+// elements of y round otherwise than from a float32 H, so a few in 10,000).  With
 // cold caches and 4096 tokens 28 us (2.0 TB/s of x: the parts' sum and the start
 // are as long as the steps) and 31 (3.8 TB/s of y).
 //
@@ -67,7 +69,11 @@ struct Down {
   static constexpr int DONE = B::REST;
   static constexpr int OFF_TOK = NS * STAGE, OFF_BAR = OFF_TOK + BM * 4, OFF_TMEM = OFF_BAR + B::N * 8,
                        OFF_ABORT = OFF_TMEM + 4, SMEM = OFF_ABORT + 4 + 1024;
-  static constexpr uint32_t COLS = RP < 32 ? 32 : RP;
+  // A product's sum loses what lies below the last bit of what it is added to,
+  // always towards zero; stages take turns among several sums, which makes those
+  // chains a quarter (rank 128: half) as long.
+  static constexpr int SUMS = RP < 128 ? 4 : 2;
+  static constexpr uint32_t COLS = SUMS * RP;
 };
 
 template <class DT, int RP>
@@ -140,15 +146,24 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
     float *h = a.parts + (int64_t(slice) * a.T + d.y + r) * RP;
 #pragma unroll
     for (int i = 0; i < RP; i += 16) {
-      uint32_t v[16];
-      tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + i, v);
-      tmem_wait_ld();
+      uint32_t v[P::SUMS][16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) asm volatile("" : "+r"(v[e]));
+      for (int s = 0; s < P::SUMS; ++s) tmem_ld16(tmem + (uint32_t(warp * 32) << 16) + s * RP + i, v[s]);
+      tmem_wait_ld();
+      float f[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < P::SUMS; ++s) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          asm volatile("" : "+r"(v[s][e]));
+          if (s < n) f[e] += __uint_as_float(v[s][e]);  // no stage added to the others
+        }
+      }
       if (r < count) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<uint4 *>(h + i + e) = n > 0 ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(h + i + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
       }
     }
     tc_fence_before();
@@ -200,14 +215,17 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
             v.w *= down;
           }
           if (u / Q < count) {
-            auto low = [](float x, float y) { return fabsf(y) == INFINITY ? 0.0f : x - y; };
-            float x0, x1, x2, x3;
-            const uint2 hi = make_uint2(DT::pack2(v.x, v.y), DT::pack2(v.z, v.w));
-            DT::unpack2(hi.x, x0, x1);
-            DT::unpack2(hi.y, x2, x3);
-            uint2 *to = reinterpret_cast<uint2 *>(a.operands + int64_t(d.y + u / Q) * RP);
-            to[q] = hi;
-            to[Q + q] = make_uint2(DT::pack2(low(v.x, x0), low(v.y, x1)), DT::pack2(low(v.z, x2), low(v.w, x3)));
+            constexpr int OPS = kLoraOperands<DT>;
+            uint2 *to = reinterpret_cast<uint2 *>(a.operands + int64_t(d.y + u / Q) * (OPS * RP / 2));
+#pragma unroll
+            for (int o = 0; o < OPS; ++o) {
+              const uint2 w = make_uint2(DT::pack2(v.x, v.y), DT::pack2(v.z, v.w));
+              to[o * Q + q] = w;
+              float x0, x1, x2, x3;
+              DT::unpack2(w.x, x0, x1);
+              DT::unpack2(w.y, x2, x3);
+              v = make_float4(lora_rest(v.x, x0), lora_rest(v.y, x1), lora_rest(v.z, x2), lora_rest(v.w, x3));
+            }
             if (q == 0) a.factors[d.y + u / Q] = up;
           }
         }
@@ -225,7 +243,8 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
         if (ok) {
           const uint64_t dx = sdesc(base + slot * P::STAGE), da = sdesc(base + slot * P::STAGE + P::XB);
 #pragma unroll
-          for (int i = 0; i < KS / 16; ++i) mma_f16(tmem, dx + 2 * i, da + 2 * i, idesc, g | i ? 1u : 0u);
+          for (int i = 0; i < KS / 16; ++i)
+            mma_f16(tmem + g % P::SUMS * RP, dx + 2 * i, da + 2 * i, idesc, g >= P::SUMS || i ? 1u : 0u);
           mma_commit(bar(P::B::EMPTY) + 8 * slot);
         }
         if (++slot == P::NS) slot = 0, par ^= 1;
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
 }
 
 // ------------------------------------------------------------------ y
-template <int RP>
+template <class DT, int RP>
 struct Up {
   // warps 0-7 own tokens (two threads a token, 32 columns each), 8-11 copy
   static constexpr int THREADS = 416, WARP_COPY = 8, WARP_MMA = 12;
@@ -252,14 +271,16 @@ struct Up {
   static constexpr int H = B::REST, D_FULL = H + 1, D_EMPTY = D_FULL + 2, DONE = D_EMPTY + 2;
   static constexpr int OFF_TOK = NS * STAGE, OFF_BAR = OFF_TOK + BM * 4,
                        OFF_TMEM = OFF_BAR + B::N * 8, OFF_ABORT = OFF_TMEM + 4, SMEM = OFF_ABORT + 4 + 1024;
-  // tensor memory: H as two operands of RP / 2 columns each, two buffers of 64 columns of the result
-  static constexpr uint32_t T_D = RP, COLS = 256;
-  static_assert(T_D + 2 * NC <= COLS, "tensor memory plan");
+  // tensor memory: H's operands, RP / 2 columns each, and buffers of 64 columns of
+  // the result, one where three operands of rank 128 leave no more room
+  static constexpr int OPS = kLoraOperands<DT>;
+  static constexpr uint32_t T_D = (OPS * RP / 2 + 31) / 32 * 32, COLS = 256, ND = T_D + 2 * NC <= COLS ? 2 : 1;
+  static_assert(T_D + ND * NC <= COLS, "tensor memory plan");
 };
 
 template <class DT, int RP>
-__global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraArgs a) {
-  using P = Up<RP>;
+__global__ void __launch_bounds__(Up<DT, RP>::THREADS, 2) lora_up_kernel(const LoraArgs a) {
+  using P = Up<DT, RP>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t *sm = smem_raw + (base - raw);
@@ -342,18 +363,18 @@ __global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraA
       wait(bar(P::H), 0);
 #pragma unroll 1
       for (int c = 0; c < n && ok; ++c) {
-        const uint32_t buf = c & 1;
+        const uint32_t buf = c % P::ND;
         wait(bar(P::B::FULL) + 8 * slot, par);
         fence_async_smem();  // the copies are ordinary writes, which the products are to read
-        wait(bar(P::D_EMPTY) + 8 * buf, ((c >> 1) & 1) ^ 1);
+        wait(bar(P::D_EMPTY) + 8 * buf, ((c / P::ND) & 1) ^ 1);
         tc_fence_after();
         if (ok) {
           const uint64_t db = sdesc(base + slot * P::STAGE);
           const uint32_t to = tmem + P::T_D + buf * NC;
           for (int i = 0; i < ks; ++i) {
             const uint64_t b = db + (((i / 4) * (NC * 128) + (i % 4) * 32) >> 4);
-            mma_f16_ts(to, tmem + 8 * i, b, idesc, i ? 1u : 0u);
-            mma_f16_ts(to, tmem + RP / 2 + 8 * i, b, idesc, 1u);
+#pragma unroll
+            for (int o = 0; o < P::OPS; ++o) mma_f16_ts(to, tmem + o * (RP / 2) + 8 * i, b, idesc, i | o ? 1u : 0u);
           }
           mma_commit(bar(P::B::EMPTY) + 8 * slot);
           mma_commit(bar(P::D_FULL) + 8 * buf);
@@ -368,18 +389,27 @@ __global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraA
   } else {
     const int r = threadIdx.x & 127, half = warp >> 2;  // token, columns 32 half ..
     const uint32_t mine = tmem + (uint32_t((warp & 3) * 32) << 16);
-    // ---- H's operands of this token, high ones by one thread, low ones by the other
+    // ---- H's operands of this token, 16 elements a group: even groups by one thread, odd ones by the other
     attn::wait_last_kernel();
     const int64_t at_row = int64_t(d.y) + min(r, count - 1);
-    const uint4 *from = reinterpret_cast<const uint4 *>(a.operands + at_row * RP + half * (RP / 2));
-    uint4 w[RP / 8];
-#pragma unroll
-    for (int i = 0; i < RP / 8; ++i) w[i] = from[i];
+    constexpr int GROUPS = P::OPS * RP / 16, AT_ONCE = 6;  // loads in flight: 48 registers
+    const uint4 *from = reinterpret_cast<const uint4 *>(a.operands + at_row * (P::OPS * RP / 2));
     const float up = a.factors[at_row];
 #pragma unroll
-    for (int i = 0; i < RP / 8; i += 2) {
-      const uint32_t x[8] = {w[i].x, w[i].y, w[i].z, w[i].w, w[i + 1].x, w[i + 1].y, w[i + 1].z, w[i + 1].w};
-      tmem_st8(mine + half * (RP / 2) + 4 * i, x);
+    for (int g0 = 0; g0 < GROUPS; g0 += 2 * AT_ONCE) {
+      uint4 w[AT_ONCE][2];
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int g = g0 + 2 * i + half;
+        if (g < GROUPS) w[i][0] = from[2 * g], w[i][1] = from[2 * g + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int g = g0 + 2 * i + half;
+        if (g >= GROUPS) break;  // the same for the whole warp
+        const uint32_t x[8] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w, w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
+        tmem_st8(mine + 8 * g, x);
+      }
     }
     tmem_wait_st();
     tc_fence_before();
@@ -396,9 +426,9 @@ __global__ void __launch_bounds__(Up<RP>::THREADS, 2) lora_up_kernel(const LoraA
     uint32_t slot = 0, par = 0;
 #pragma unroll 1
     for (int c = 0; c < n && ok; ++c) {
-      const uint32_t buf = c & 1;
+      const uint32_t buf = c % P::ND;
       ok = wait_warp(bar(P::B::FULL) + 8 * slot, par, abort_flag) &&
-           wait_warp(bar(P::D_FULL) + 8 * buf, (c >> 1) & 1, abort_flag);
+           wait_warp(bar(P::D_FULL) + 8 * buf, (c / P::ND) & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
       uint8_t *ty = sm + slot * P::STAGE + P::BB;
@@ -442,15 +472,16 @@ int launch_one(const LoraArgs &a, int64_t tiles, cudaStream_t st) {
   // lora_up_kernel's blocks may be there before lora_down_kernel's have their
   // tensor memory, and wait for those: no SM holds two of the first and one of
   // the second, so that there is always some left.
-  static_assert(2 * Up<RP>::SMEM + Down<RP>::SMEM > 228 * 1024 && Up<RP>::COLS + Down<RP>::COLS <= 512,
+  using U = Up<DT, RP>;
+  static_assert(2 * U::SMEM + Down<RP>::SMEM > 228 * 1024 && U::COLS + Down<RP>::COLS <= 512,
                 "tensor memory of blocks that share an SM");
   auto *down = lora_down_kernel<DT, RP>;
   auto *up = lora_up_kernel<DT, RP>;
   static OncePerDevice sized, sized_up;
-  if (!allow_smem(sized, down, Down<RP>::SMEM) || !allow_smem(sized_up, up, Up<RP>::SMEM)) return WQ_ERR_LAUNCH;
+  if (!allow_smem(sized, down, Down<RP>::SMEM) || !allow_smem(sized_up, up, U::SMEM)) return WQ_ERR_LAUNCH;
   const int rc = attn::launch_chained(down, unsigned(tiles * a.slices), Down<RP>::THREADS, Down<RP>::SMEM, true, st, a);
   return rc != WQ_OK ? rc
-                     : attn::launch_chained(up, unsigned(tiles * a.stretches), Up<RP>::THREADS, Up<RP>::SMEM, true, st, a);
+                     : attn::launch_chained(up, unsigned(tiles * a.stretches), U::THREADS, U::SMEM, true, st, a);
 }
 
 template <class DT>

@@ -4,6 +4,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "wq_common.cuh"
 #include "wq_once.h"
 
@@ -274,6 +276,15 @@ struct EvictArgs {
 int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st);
 
 constexpr int kLoraTile = 128;  // tokens of a tile where there are many
+// 16-bit operands that a float32 element of x A^T is cut into: bf16 has 8 bits,
+// so three hold its 24; fp16's two hold 22, counted from a row's largest
+constexpr int kLoraMostOperands = 3;
+template <class DT>
+constexpr int kLoraOperands = std::is_same<DT, F16>::value ? 2 : kLoraMostOperands;
+// What is left of v after an operand (of infinity: nothing)
+__device__ __forceinline__ float lora_rest(float v, float operand) {
+  return fabsf(operand) == INFINITY ? 0.0f : v - operand;
+}
 struct LoraArgs {
   const uint16_t *x;
   int64_t ldx;
@@ -294,7 +305,7 @@ struct LoraArgs {
   int slices, stretches;
   int *tickets;        // [tiles]
   float *parts;
-  uint32_t *operands;  // [T][lora_rank(r)]: high ones, then low ones, in pairs
+  uint32_t *operands;  // [T][kLoraOperands][lora_rank(r) / 2]: high ones first, in pairs
   float *factors;      // [T]
 };
 int lora_slices(int64_t like);
