@@ -523,11 +523,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     bool more = walk.next(a, p);
     float old = more ? look(p, p.k0) : 0.0f;
     if (more) lse_of(p, p.qa);
-    while (more && ok) {
+    // A warp whose wait ran out goes on to the next barrier of its key tile's
+    // warps, without work, and they leave together: none is left there by one
+    // that saw the scores in time or did not.
+    bool go = true;
+    while (more && go) {
       const bool again = walk.next(a, nx);
       float *to = weight_at(a, p.b, p.h, p.k0 + col);
 #pragma unroll 1
-      for (int k = 0; k < p.pairs && ok; ++k) {
+      for (int k = 0; k < p.pairs && go; ++k) {
         const int k0 = p.k0 + k * PAIR, i = k0 + col;
         const float was = old;
         if (k + 1 < p.pairs) old = look(p, k0 + PAIR);
@@ -543,12 +547,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int e = 0; e < LB; ++e) ls[((ql & 1) * LB + e) * BR + tid] = neg_lse2(l[e]);
             if (q + LB < p.qb) lse_of(p, q + LB);
             else if (again) lse_of(nx, nx.qa);
-            named_sync(1 + g, 128);  // two batches on, all have read what was here
+            // two batches on, all have read what was here
+            if (!(go = named_sync_and(1 + g, 128, ok))) break;
           }
-          if (!tile) continue;
+          if (!tile || !ok) continue;
           const float *lb = ls + ((ql & 1) * LB + batch) * BR;
           const uint32_t buf = st & 1, at = ts + buf * 128;
-          if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g) + 8 * buf, (st >> 1) & 1, abort_flag))) break;
+          if (!(ok = wait_warp(bar(P::B_S_FULL + 2 * g) + 8 * buf, (st >> 1) & 1, abort_flag))) {
+            *abort_flag = 1;
+            continue;
+          }
           tc_fence_after();
           // columns of the tile that count: its tokens' (and those of a whole tile
           // that no row fills), from the first that sees this key on
@@ -589,8 +597,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (lane == 0) mbar_arrive(bar(P::B_S_EMPTY + 2 * g) + 8 * buf);
           ++st;
         }
-        if (!ok) break;
-        if (i < p.s.len) {
+        if (go && ok && i < p.s.len) {
           if (!p.whole) a.part[(int64_t(blockIdx.x) * 2 + p.slot) * PAIR + col] = sum;
           else to[k * PAIR] = __fmaf_rn(a.decay, was, sum);
         }
