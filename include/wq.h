@@ -738,7 +738,8 @@ WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
  * arguments.
  * Requirements: bf16 or fp16; H, N, r and pitches multiples of 8, r at most 128,
  * n at most 8192, 16-byte aligned tensors.  Workspace:
- * wq_lora_add_workspace_size(T, n, r) (0 bytes up to 256 tokens). */
+ * wq_lora_add_workspace_size(T, n, r) (0 bytes up to 256 tokens); it does not
+ * shrink as T, n or r grow, so one made for the largest batch serves all. */
 WQ_API size_t wq_lora_add_workspace_size(int64_t T, int n, int r);
 WQ_API int wq_lora_add(const void *x, int64_t ldx, int64_t T, int64_t H, const void *A,
                        const void *B, const float *scales, int n, int r, const int32_t *adapters,

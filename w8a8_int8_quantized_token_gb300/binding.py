@@ -1149,7 +1149,7 @@ def evict_paged(weights, k_cache, v_cache, page_table, key_len, max_len, budget,
 
 # ---------------------------------------------------------------- adapters beside a projection
 def lora_add_workspace(y, x, A):
-    """A workspace for lora_add calls of these sizes."""
+    """A workspace for lora_add calls of these sizes, or of fewer tokens, adapters or ranks."""
     n = lib().wq_lora_add_workspace_size(x.shape[0], A.shape[0], A.shape[1])
     return torch.empty(max(n, 1), dtype=torch.uint8, device=x.device)
 

@@ -571,7 +571,16 @@ inline int64_t tiles_like(int64_t T, int64_t n, int r) {
   return T <= kInline ? tiles_of(T, n, r) : T / tile_of(T, r) + std::min(n, T / 256 + 1);
 }
 
-// The workspace, from `at` on (nullptr: its size alone)
+// Parts of the first product that any batch of up to T tokens has, each one's
+// tokens times its slices.  A smaller batch may have more slices: s > 1 of them
+// where 2 * 152 / s tiles or fewer are to be expected, which are more than
+// tokens / kLoraTile, so that its parts stay below 2 * 152 * kLoraTile.
+inline int64_t most_parts(int64_t T) {
+  return std::max(T, std::min<int64_t>(T * kLoraSlices, 2 * 152 * kLoraTile));
+}
+
+// The workspace, from `at` on (nullptr: its size alone).  A larger T, n or r
+// takes no less: a workspace made for the largest batch serves all.
 size_t lora_lay_out(LoraArgs &a, char *at) {
   const int64_t tiles = tiles_of(a.T, a.n, a.r), T = a.T, RP = lora_rank(a.r);
   size_t n = 0;
@@ -586,7 +595,7 @@ size_t lora_lay_out(LoraArgs &a, char *at) {
     take(a.tickets, tiles);
     take(a.factors, T);
     take(a.operands, T * RP / 2 * kLoraMostOperands);
-    take(a.parts, lora_slices(tiles_like(T, a.n, a.r)) * T * RP);
+    take(a.parts, most_parts(T) * RP);
   }
   return n;
 }

@@ -39,7 +39,6 @@ namespace {
 using namespace tc;
 
 constexpr int BM = kLoraTile, KS = 64, NC = 64;  // tokens; elements of x, columns of y a stage
-constexpr int kSlices = 8;                 // of the first product's long axis, at most
 constexpr int RING = 110 * 1024;           // bytes of a block's stages, at most: two blocks share an SM
 
 template <class DT>
@@ -179,13 +178,13 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
       constexpr int U = 4;  // units whose loads are in flight together
 #pragma unroll 1
       for (int u0 = r; u0 < BM * Q; u0 += U * 128) {
-        float4 w[U][kSlices];
+        float4 w[U][kLoraSlices];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
           const int u = u0 + k * 128, row = d.y + min(u / Q, count - 1);
           const float4 *from = reinterpret_cast<const float4 *>(a.parts + int64_t(row) * RP) + u % Q;
 #pragma unroll
-          for (int c = 0; c < kSlices; ++c)
+          for (int c = 0; c < kLoraSlices; ++c)
             if (c < a.slices) w[k][c] = __ldcg(from + int64_t(c) * a.T * Q);
         }
 #pragma unroll
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
           const int u = u0 + k * 128, q = u % Q;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-          for (int c = 0; c < kSlices; ++c) {
+          for (int c = 0; c < kLoraSlices; ++c) {
             if (c >= a.slices) break;
             v.x += w[k][c].x;
             v.y += w[k][c].y;
@@ -496,7 +495,7 @@ int launch_rank(const LoraArgs &a, int64_t tiles, cudaStream_t st) {
 
 // Slices and stretches of a tile: as many as let about all tiles, of which there
 // are likely `like`, run at the same time, two blocks an SM
-int lora_slices(int64_t like) { return int(std::max<int64_t>(1, std::min<int64_t>(kSlices, 2 * 152 / like))); }
+int lora_slices(int64_t like) { return int(std::max<int64_t>(1, std::min<int64_t>(kLoraSlices, 2 * 152 / like))); }
 
 // The rank in shared memory and in the workspace
 int lora_rank(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128; }

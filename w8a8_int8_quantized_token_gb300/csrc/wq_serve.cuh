@@ -276,6 +276,7 @@ struct EvictArgs {
 int launch_evict(const EvictArgs &a, bool vec, cudaStream_t st);
 
 constexpr int kLoraTile = 128;  // tokens of a tile where there are many
+constexpr int kLoraSlices = 8;  // of the first product's long axis, at most
 // 16-bit operands that a float32 element of x A^T is cut into: bf16 has 8 bits,
 // so three hold its 24; fp16's two hold 22, counted from a row's largest
 constexpr int kLoraMostOperands = 3;

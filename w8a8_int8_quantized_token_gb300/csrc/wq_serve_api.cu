@@ -532,7 +532,7 @@ int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head, const wq
 }
 
 size_t wq_lora_add_workspace_size(int64_t T, int n, int r) {
-  return T < 1 || n < 1 || r < 1 || r > 128 ? 0 : lora_ws_bytes(T, n, r);
+  return T < 1 || n < 1 || r < 1 || r > 128 || T >= (1 << 24) ? 0 : lora_ws_bytes(T, n, r);
 }
 
 int wq_lora_add(const void *x, int64_t ldx, int64_t T, int64_t H, const void *A, const void *B,
