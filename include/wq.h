@@ -734,7 +734,8 @@ WQ_API int wq_evict_paged(const float *weights, int64_t w_seq, int64_t w_head,
  * smaller rank are padded with zeros.  Products and sums are float32; x A^T enters
  * the second product with all its 24 bits (fp16: with 22, counted from the largest
  * of the row's), and y is rounded once.  A row's result depends on its token, T
- * and n alone, not on the tokens beside it.  y must not overlap the other
+ * and n alone, not on the tokens beside it.  Infinities and NaN of x and A go the
+ * formula's way; an infinite element of B gives NaN.  y must not overlap the other
  * arguments.
  * Requirements: bf16 or fp16; H, N, r and pitches multiples of 8, r at most 128,
  * n at most 8192, 16-byte aligned tensors.  Workspace:

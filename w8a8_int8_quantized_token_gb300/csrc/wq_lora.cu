@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
     float down = 1.0f;
     if (std::is_same<DT, F16>::value) {
       float top = 0.0f;
-      for (int c = lane; c < RP; c += 32) top = fmaxf(top, fabsf(h[row * RP + c]));
+      for (int c = lane; c < a.r; c += 32) top = fmaxf(top, fabsf(h[row * RP + c]));
       top = warp_max(top);
       // 2^-e with the row's largest in [2^e, 2^(e+1)), e within float's normal range
       const int e = min(max(int(__float_as_uint(top) >> 23) - 127, -126), 126);
@@ -345,7 +345,8 @@ __global__ void __launch_bounds__(NT) lora_kernel(const LoraArgs a) {
       up[row] = scale;
     }
     for (int c = lane; c < RP; c += 32) {
-      float v = __fmul_rn(h[row * RP + c], down);
+      // past the rank nothing counts: an infinite x makes NaN of the padding's zeros
+      float v = c < a.r ? __fmul_rn(h[row * RP + c], down) : 0.0f;
       uint8_t *to = sm + P::OFF_H + row * P::HP + c * 2;
 #pragma unroll
       for (int q = 0; q < P::OPS; ++q) {

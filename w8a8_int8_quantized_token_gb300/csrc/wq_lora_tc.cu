@@ -162,7 +162,9 @@ __global__ void __launch_bounds__(Down<RP>::THREADS, 2) lora_down_kernel(const L
       }
       if (r < count) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(h + i + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+        for (int e = 0; e < 16; e += 4)  // past the rank nothing counts: an infinite x makes NaN of the padding's zeros
+          *reinterpret_cast<float4 *>(h + i + e) =
+              i + e < a.r ? make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
     tc_fence_before();
