@@ -664,8 +664,8 @@ WQ_API int wq_attention_shared_prefix(const void *q, int64_t q_token, int64_t q_
  * keys, whose places need not be written before.  weights float, pitches w_seq
  * and w_head, last dimension contiguous; places at or past key_len[b] are
  * neither read nor written.  A sequence without new tokens only decays.  A row
- * with lse = -inf (a token that saw no key) gives no weight.  Call it once a
- * step, after the attention.
+ * with lse = -inf (a token that saw no key) gives no weight.  A key that is not
+ * finite changes its own weight alone.  Call it once a step, after the attention.
  * max_q, max_len: host bounds, values above them are cut with status =
  * WQ_ERR_INDEX, as in the attention.  A page id outside [0, num_pages) sets the
  * same status; its keys count as zeros.  The cache's values (v) are not read.

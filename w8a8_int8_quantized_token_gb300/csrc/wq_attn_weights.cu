@@ -304,15 +304,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == WARP_MMA) tmem_alloc(smem_u32(tmem_slot), 512);
-  if constexpr (MANY) {  // rows of the query tiles that no copy fills: their scores are 0, and count nothing
-    const int rows = a.tpt * a.G, rest = (a.cols - rows) * 8, n = P::query_tiles(a.cols, MANY) * P::CH * rest;
-    for (int i = threadIdx.x; i < n; i += NTHREADS) {
-      const int chunk = i / rest;
-      *reinterpret_cast<uint4 *>(sm + P::OFF_Q + (chunk * a.cols + rows) * 128 + (i - chunk * rest) * 16) =
-          make_uint4(0, 0, 0, 0);
-    }
-    fence_async_smem();
-  }
   tc_fence_before();
   const Place at = locate(a, reinterpret_cast<int64_t *>(sm + P::OFF_SCAN),
                           reinterpret_cast<int64_t *>(sm + P::OFF_START), blockIdx.x == 0,
@@ -558,9 +549,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             continue;
           }
           tc_fence_after();
-          // columns of the tile that count: its tokens' (and those of a whole tile
-          // that no row fills), from the first that sees this key on
-          const int left = p.s.n - q * tpt, hi = MANY && left >= tpt ? a.cols : min(tpt, left) * a.G;
+          // columns of the tile that count: its tokens', from the first that sees
+          // this key on (those that no row fills hold whatever was there)
+          const int hi = min(tpt, p.s.n - q * tpt) * a.G;
           const int lo = min(max(0, i - p.s.old - q * tpt), tpt) * a.G;
           const bool seen = __all_sync(0xffffffffu, lo == 0);  // by all tokens, all keys of the warp
           s0 = s1 = pair(0.0f, 0.0f);
@@ -572,17 +563,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_wait_ld(v);
             if (seen && hi == 8) weigh(v, lb);
             else weigh_some(v, lb, lo, hi);
-          } else if (seen && hi % 32 == 0) {
-#pragma unroll 1
-            for (int e = 0; e < hi; e += 32) {
-              uint32_t v[32];
-              tmem_ld32(at + e, v);
-              wait_ld32(v);
-              weigh(v, lb + e);
-            }
           } else {
+            int e = 0;
+            if (seen) {
 #pragma unroll 1
-            for (int e = 0; e < hi; e += 32) {
+              for (; e + 32 <= hi; e += 32) {
+                uint32_t v[32];
+                tmem_ld32(at + e, v);
+                wait_ld32(v);
+                weigh(v, lb + e);
+              }
+            }
+#pragma unroll 1
+            for (; e < hi; e += 32) {
               uint32_t v[32];
               tmem_ld32(at + e, v);
               wait_ld32(v);
