@@ -704,8 +704,9 @@ WQ_API int wq_attention_weights_paged(const void *q, int64_t q_token, int64_t q_
  * be turned to other positions: they carry the ones that they were appended
  * with.
  * max_len: host bound on the lengths; longer ones are cut with status =
- * WQ_ERR_INDEX.  A page id outside [0, num_pages) sets the same status and its
- * rows are not moved.  key_len and new_len must not overlap.  Keys and values may
+ * WQ_ERR_INDEX.  A page id outside [0, num_pages) for a key that stays, or for its
+ * new place, sets the same status, whether it moves or stands, and the key and its
+ * value are not moved.  key_len and new_len must not overlap.  Keys and values may
  * share elements if their pitches are the same (values that are a part of the
  * keys).
  * Requirements: budget >= 1, first + recent <= budget, bf16 or fp16, dk and dv

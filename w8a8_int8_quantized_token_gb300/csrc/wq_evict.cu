@@ -135,14 +135,11 @@ __global__ void __launch_bounds__(NT, 2) evict_select_kernel(const EvictArgs a, 
   int4 *ways = a.ways + (int64_t(b) * a.heads + h) * a.budget;
   const int32_t *in = a.page_table + b * a.ld_table, *out = a.out_table + b * a.ld_out;
   auto find_way = [&](int j, int i) {
-    if (a.in_place && i == j) {
-      ways[j] = make_int4(-1, 0, 0, 0);
-      return;
-    }
     const int p = i / a.page_size, q = j / a.page_size, from = in[p], to = out[q];
     const bool good = unsigned(from) < unsigned(a.num_pages) && unsigned(to) < unsigned(a.num_pages);
     if (!good) set_status(a.status, WQ_ERR_INDEX);
-    ways[j] = make_int4(good ? from : -1, i - p * a.page_size, to, j - q * a.page_size);
+    const bool stands = a.in_place && i == j;  // its page is looked at all the same
+    ways[j] = make_int4(good && !stands ? from : -1, i - p * a.page_size, to, j - q * a.page_size);
   };
   // key i goes to place j
   const bool moves = !a.in_place || n > a.budget;
@@ -156,6 +153,10 @@ __global__ void __launch_bounds__(NT, 2) evict_select_kernel(const EvictArgs a, 
   for (int j = fresh + all0; j < a.budget; j += all) kept[j] = -1;
   if (n <= a.budget) {
     for (int j = all0; j < n; j += all) emit(j, j);
+    if (!moves && h == 0) {  // nothing looks at its pages
+      for (int p = all0; p < (n + a.page_size - 1) / a.page_size; p += all)
+        if (unsigned(in[p]) >= unsigned(a.num_pages)) set_status(a.status, WQ_ERR_INDEX);
+    }
     return;  // the whole cluster
   }
   const int first = a.first, mid = n - a.recent - first;
