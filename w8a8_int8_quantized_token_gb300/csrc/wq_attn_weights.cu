@@ -19,8 +19,8 @@
 //
 // A unit is a (sequence, key head, pair of key tiles, query tile); those in
 // which no token sees a key are left out.  All units lie on one line, which the
-// blocks cut into equal pieces, so that ragged lengths and the triangle of a
-// prompt cost no idle SMs.  Where the cut falls between the query tiles of a
+// blocks cut into equal pieces (wq_weights_line.h), so that ragged lengths and the
+// triangle of a prompt cost no idle SMs.  Where the cut falls between the query tiles of a
 // pair, the parts of its sums go to the workspace and a second kernel adds them
 // in the order of the line.  One query tile a sequence (decode) is never cut.
 //
@@ -52,7 +52,8 @@ using attn::start_next_kernel;
 using attn::wait_last_kernel;
 
 constexpr int BK = 128, BR = 128;  // keys, query rows of a tile
-constexpr int PAIR = 2 * BK;       // keys of a pair of tiles
+constexpr int PAIR = kWeightsPair; // keys of a pair of tiles
+static_assert(PAIR == 2 * BK, "a pair of key tiles");
 constexpr int NTHREADS = 352;
 constexpr int WARP_TMA = 8, WARP_MMA = 9;  // MMA: two warps
 constexpr int MAX_BLOCKS = 152;    // one block an SM
@@ -94,54 +95,8 @@ struct Plan {
   }
 };
 
-// A sequence: its tokens, keys, and the cost of its pairs of key tiles.  A pair
-// costs 1 where all tokens are one query tile.  Else it costs its query tiles,
-// as many as there would be of 2^shift tokens each, which add up without a
-// loop; the tiles themselves have tpt >= 2^shift tokens, and a part of a pair's
-// cost is that part of them.
-struct Seq {
-  int t0, n, len;
-  int old;       // keys that were there before the tokens' own (negative: tokens with no key)
-  int pairs, tiles, costs;
-  int p1, d1;    // first pair whose keys not all tokens see, and how far it starts past `old`
-
-  // query tiles of 2^shift tokens that see nothing of pair p, at the front of the sequence's
-  __device__ __forceinline__ int unseen(int p, int shift) const { return max(0, (p * PAIR - old) >> shift); }
-  __device__ __forceinline__ int cost(int p, int shift) const { return tiles <= 1 ? 1 : costs - unseen(p, shift); }
-  // cost of the pairs before p, of one key head
-  __device__ __forceinline__ int64_t before(int p, int shift) const {
-    if (tiles <= 1) return p;
-    const int64_t m = max(0, p - p1);
-    return int64_t(p) * costs - (m * (d1 >> shift) + int64_t(PAIR >> shift) * (m * (m - 1) / 2));
-  }
-};
-
-__device__ __forceinline__ Seq seq_of(const WeightArgs &a, int c0, int c1, int l) {
-  Seq s;
-  s.t0 = min(max(c0, 0), a.T);
-  s.n = min(max(c1 - s.t0, 0), min(a.max_q, a.T - s.t0));
-  s.len = min(max(l, 0), a.max_len);
-  s.old = s.len - s.n;
-  s.pairs = (s.len + PAIR - 1) / PAIR;
-  s.tiles = (s.n + a.tpt - 1) / a.tpt;
-  s.costs = (s.n + (1 << a.shift) - 1) >> a.shift;
-  s.p1 = s.old <= 0 ? 0 : (s.old + PAIR - 1) / PAIR;
-  s.d1 = s.p1 * PAIR - s.old;
-  return s;
-}
-__device__ __forceinline__ bool in_range(const WeightArgs &a, const Seq &s, int c0, int c1, int l) {
-  return s.t0 == c0 && s.t0 + s.n == c1 && s.len == l;
-}
-__device__ __forceinline__ int first_of(const WeightArgs &a, int b) {
-  return a.cu_q ? a.cu_q[b] : b * a.max_q;
-}
-
-// Sequence and offset in it of place at = f(length of the line), found by the
-// whole block; and that length.
-struct Place {
-  int b;
-  int64_t off, total, at;
-};
+// Place at = f(length of the line), found by the whole block.  The sequences out
+// of range are told of.
 template <class F>
 __device__ __forceinline__ Place locate(const WeightArgs &a, int64_t *scan, int64_t *out, bool tell,
                                         F &&f) {
@@ -181,87 +136,6 @@ __device__ __forceinline__ Place locate(const WeightArgs &a, int64_t *scan, int6
   Place p{int(out[0]), out[1], total, at};
   return p;
 }
-
-// Query tiles [qa, qb) of a sequence against a pair of key tiles; with one
-// query tile in all, against `pairs` pairs one after the other
-struct Piece {
-  int b, h, k0, pairs, qa, qb;
-  Seq s;
-  bool whole;  // all query tiles of the pair
-  int slot;    // else: where its sums go
-};
-
-// The pieces of a block, one after the other
-struct Walk {
-  int b, h, p;
-  int64_t u, left;  // units of the pair that are done; units of the block to come
-  int n0, n1, nl;   // the next sequence, read ahead
-  Seq s;
-
-  __device__ __forceinline__ void ahead(const WeightArgs &a) {
-    const bool some = b + 1 < a.B;
-    n0 = some ? first_of(a, b + 1) : 0;
-    n1 = some ? first_of(a, b + 2) : 0;
-    nl = some ? a.key_len[b + 1] : 0;
-  }
-  __device__ __forceinline__ void begin(const WeightArgs &a, const Place &at, int64_t units) {
-    b = at.b;
-    left = units;
-    u = 0;
-    h = p = 0;
-    if (units <= 0) return;
-    s = seq_of(a, first_of(a, b), first_of(a, b + 1), a.key_len[b]);
-    ahead(a);
-    const int64_t head = s.before(s.pairs, a.shift);
-    h = int(at.off / head);
-    const int64_t rest = at.off - h * head;
-    int lo = 0, hi = s.pairs - 1;  // the last pair that starts at or before `rest`
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (s.before(mid, a.shift) <= rest) lo = mid;
-      else hi = mid - 1;
-    }
-    p = lo;
-    u = rest - s.before(p, a.shift);
-  }
-  __device__ __forceinline__ bool next(const WeightArgs &a, Piece &o) {
-    if (left <= 0) return false;
-    while (p >= s.pairs) {  // the next head, or sequence with keys
-      p = 0;
-      if (s.pairs > 0 && ++h < a.heads) break;
-      h = 0;
-      ++b;
-      s = seq_of(a, n0, n1, nl);
-      ahead(a);
-    }
-    o.b = b;
-    o.h = h;
-    o.k0 = p * PAIR;
-    o.s = s;
-    if (s.tiles <= 1) {  // a unit a pair
-      const int take = int(min(int64_t(s.pairs - p), left));
-      o.pairs = take;
-      o.qa = 0;
-      o.qb = s.tiles;
-      o.whole = true;
-      o.slot = 0;
-      left -= take;
-      p += take;
-      return true;
-    }
-    const int first = max(0, (p * PAIR - s.old) / a.tpt), cost = s.cost(p, a.shift);
-    const int64_t tiles = s.tiles - first, take = min(int64_t(cost) - u, left);
-    o.pairs = 1;
-    o.qa = first + int(u * tiles / cost);
-    o.qb = first + int((u + take) * tiles / cost);
-    o.whole = take == cost;
-    o.slot = u == 0 ? 1 : 0;
-    left -= take;
-    u += take;
-    if (u == cost) u = 0, ++p;
-    return true;
-  }
-};
 
 template <class DT>
 constexpr uint32_t kTypes = std::is_same<DT, Bf16>::value ? (1u << 7) | (1u << 10) : 0u;
@@ -307,11 +181,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_before();
   const Place at = locate(a, reinterpret_cast<int64_t *>(sm + P::OFF_SCAN),
                           reinterpret_cast<int64_t *>(sm + P::OFF_START), blockIdx.x == 0,
-                          [](int64_t total) { return total * blockIdx.x / gridDim.x; });
+                          [](int64_t total) { return first_unit(total, blockIdx.x, gridDim.x); });
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk walk;
-  walk.begin(a, at, at.total * (blockIdx.x + 1) / gridDim.x - at.at);
+  walk.begin(a, at, first_unit(at.total, blockIdx.x + 1, gridDim.x) - at.at);
   const int tpt = a.tpt;
   const uint32_t nk = uint32_t(P::key_tiles(a.cols, MANY)), nq = uint32_t(P::query_tiles(a.cols, MANY));
   const uint32_t qbytes = uint32_t(P::query_bytes(a.cols)), off_k = P::OFF_Q + nq * qbytes;
@@ -613,23 +487,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 __global__ void __launch_bounds__(PAIR) attn_weights_join_kernel(const WeightArgs a) {
   __shared__ int64_t scan[PAIR / 32], out[2];
   const int64_t blocks = gridDim.x + 1, c = blockIdx.x;
-  const Place at = locate(a, scan, out, false, [&](int64_t total) { return total * (c + 1) / blocks; });
+  const Place at = locate(a, scan, out, false, [&](int64_t total) { return first_unit(total, c + 1, blocks); });
   wait_last_kernel();  // in every block: what follows the join may then rely on both
-  if (at.at >= at.total) return;
   Walk w;
-  w.begin(a, at, 1);
-  const int64_t start = at.at - w.u;
-  if (w.u == 0 || start < at.total * c / blocks) return;
-  const int64_t end = start + w.s.cost(w.p, a.shift);
+  int64_t end;
+  if (!left_to_others(a, at, c, blocks, w, end)) return;
   const int i = w.p * PAIR + threadIdx.x;
   if (i >= w.s.len) return;
   float sum = a.part[(c * 2 + 1) * PAIR + threadIdx.x];
-  int64_t lo = at.at;  // where block k begins
-  for (int64_t k = c + 1; k < blocks && lo < end; ++k) {
-    const int64_t hi = at.total * (k + 1) / blocks;
-    if (lo < hi) sum += a.part[k * 2 * PAIR + threadIdx.x];  // not of a block without units
-    lo = hi;
-  }
+  parts_after(at.total, c, blocks, end, [&](int64_t k) { sum += a.part[k * 2 * PAIR + threadIdx.x]; });
   float *to = weight_at(a, w.b, w.h, i);
   *to = __fmaf_rn(a.decay, i < w.s.old ? *to : 0.0f, sum);
 }

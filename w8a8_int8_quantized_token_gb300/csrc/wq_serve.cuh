@@ -8,6 +8,7 @@
 
 #include "wq_common.cuh"
 #include "wq_once.h"
+#include "wq_weights_line.h"
 
 namespace wq {
 
@@ -221,27 +222,22 @@ int launch_attention_tiles(const AttnArgs &a, int dtype, cudaStream_t st);
 size_t attention_ws_bytes(const AttnArgs &a);
 int launch_attention(const AttnArgs &a, int dtype, cudaStream_t st);
 
-struct WeightArgs {
+struct WeightArgs : WeightsLine {
   const uint16_t *q;
   int64_t q_token, q_head;
-  int T, B, max_q, Hq, heads, G;
-  const int32_t *cu_q;
+  int Hq, G;
   const uint16_t *k;
   int64_t k_page, k_head, k_token, num_pages;
   int page_size, dk;
   const int32_t *page_table;
   int64_t ld_table;
-  const int32_t *key_len;
-  int max_len;
   float scale_log2, decay;
   const float *lse;  // [T][Hq]
   float *w;
   int64_t w_seq, w_head;
   int32_t *status;
-  // plan
-  int tpt;      // tokens of a query tile
-  int shift;    // log2 of the tokens that its cost goes by, at most tpt
-  int cols;     // its rows, in whole 16s
+  // plan, beside the line's
+  int cols;     // rows of a query tile, in whole 16s
   int box;      // cache rows of one TMA box
   int step_pages, step_place;  // a pair of key tiles on: pages, and places beyond them
   int blocks;   // that share the line of units
