@@ -25,18 +25,18 @@
 // in the order of the line.  One query tile a sequence (decode) is never cut.
 //
 // Few rows: bound by HBM, every key read once; 64 sequences of up to 8192 keys (8
-// heads of 128, one token each) take 102 us, 6.2 TB/s.  What let it get there:
+// heads of 128, one token each) take 103 us, 6.1 TB/s.  What let it get there:
 // instructions a pair, since every role walks the pairs with one warp a
 // scheduler, which takes about six cycles for each (135 us with the sequence, the
 // pages and the log-sum-exps looked up pair by pair).
 // Many rows: a step of 128 rows against a pair takes 1.3 us (a prompt of 4096
-// tokens, 64 heads, 168 us).  Its products alone take 122 us, where their operands
+// tokens, 64 heads, 171 us).  Its products alone take 122 us, where their operands
 // from shared memory let them, and the chain of waits, loads from tensor memory
 // and sums without any exponential 158.  Shorter code helped (191 us with the loops
-// over a tile's columns unrolled); fewer ex2 (a part of them as polynomials, 179 us),
-// 16 warps that weigh (179) and loads ahead (185) did not.
+// over a tile's columns unrolled, 168 so); fewer ex2 (a part of them as polynomials,
+// 179 us), 16 warps that weigh (179) and loads ahead (185) did not.
 //
-// Every wait is bounded (1 s); on expiry the kernel records WQ_ERR_TIMEOUT,
+// Every wait on a memory barrier is bounded (1 s); on expiry the kernel records WQ_ERR_TIMEOUT,
 // waits (bounded) for its own copies and MMAs, frees tensor memory and exits.
 #include <algorithm>
 #include <type_traits>
@@ -501,7 +501,9 @@ __global__ void __launch_bounds__(PAIR) attn_weights_join_kernel(const WeightArg
 }
 
 // Any page size and pitch: a block takes 32 keys of one head, a lane a key; the
-// warps share the rows, and add their sums in the order of the warps.
+// warps share the rows, and add their sums in the order of the warps.  Bound by two
+// shared-memory reads a product: 16 sequences of 4096 keys, 8 key heads of 8 and 128
+// elements, 160 us with pages of one key, where the kernel above takes 35 with 16.
 template <class DT>
 __global__ void __launch_bounds__(256) attn_weights_any_kernel(const WeightArgs a) {
   constexpr int KT = 32, NW = 8;

@@ -28,7 +28,10 @@
 // any rows.  Bound by HBM: rows that move are read once and written once; 8 heads
 // of 4096 rows (17 MB read, 17 written) take 11 us with cold caches.  In place a
 // block has 32 bytes of a row, which lets it read 1024 rows before it waits, and
-// few sequences leave SMs idle: 2 of 8 heads of 1900 rows (16 MB read) take 15 us.
+// blocks may be left with a second walk while the others are done: 4 sequences of 8
+// heads are 512 walks for 456 blocks (2 of 8 heads of 1900 rows, 16 MB read, take 15
+// us).  All of 64 sequences that give 148 of 2048 keys back take 256 us with their
+// selection (up to 996 MB, 3.9 TB/s).
 #include <algorithm>
 
 #include "wq_attn.cuh"

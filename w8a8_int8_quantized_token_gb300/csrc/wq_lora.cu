@@ -557,17 +557,24 @@ int launch_rank(const LoraArgs &a, int64_t tiles, int C, cudaStream_t st) {
 }
 
 // Whether this kernel takes the tokens.  Its tiles read the adapter once for 16
-// tokens, but need no second launch.  Width 7168, 8 adapters, here and with 128
-// tokens a tile: 1024 tokens of rank 16 18 and 25 us, 2048 of rank 16 29 and 31,
-// 3000 of rank 16 49 and 40, 1536 of rank 32 42 and 33, 768 of rank 64 33 and 33,
-// 2048 of rank 64 57 and 43, 384 of rank 128 37 and 37.
+// tokens, but need no second launch.  Width 7168, 8 adapters in runs of tokens,
+// bf16, us here and with 128 tokens a tile:
+//   rank 16    1024 tokens 16 23, 1536 tokens 24 26 | 2048 tokens 24 30, 3000 tokens 44 36
+//   rank 32    1024 tokens 25 27 | 1536 tokens 39 29
+//   rank 64    512 tokens 35 31 | 768 tokens 34 34, 1024 tokens 34 35, 2048 tokens 57 43
+//   rank 128   288 tokens 38 43 | 384 tokens 38 46, 768 tokens 53 49
+// The rule's border is at the bars: it gives away up to a fifth beside it, where
+// either kernel's last round of blocks is nearly empty.
 inline bool few(int64_t T, int r) { return T * std::max(r, 24) <= 36864; }
 // Tokens of a tile, here and in the kernels for many; tiles at most
 inline int tile_of(int64_t T, int r) { return few(T, r) ? BM : kLoraTile; }
 inline int64_t tiles_of(int64_t T, int64_t n, int r) { return std::min(T, n + T / tile_of(T, r)); }
 // Tiles to expect, by which the blocks of a tile are chosen: a batch of single
 // tokens mixes adapters, prompts are runs of tokens.  (By the most, a few prompts
-// among 512 adapters, 8192 tokens, took 143 us, and 90 so.)
+// among 512 adapters, 8192 tokens, took 143 us, and 90 so.)  Which adapters a batch
+// uses is not known here.  Width 7168, rank 16, us by the most tiles and by runs: 256
+// mixed tokens of 64 adapters 13 and 19, of 256 35 and 50, but 256 tokens that use 3
+// of 512 26 and 20; past 256 tokens, 512 mixed ones of 32 15 and 18, of 256 40 and 57.
 inline int64_t tiles_like(int64_t T, int64_t n, int r) {
   return T <= kInline ? tiles_of(T, n, r) : T / tile_of(T, r) + std::min(n, T / 256 + 1);
 }

@@ -17,11 +17,11 @@
 // swizzled layout.  H enters the second product from tensor memory as 16-bit
 // operands, its rounding and what that leaves, as in the kernel for few tokens.
 // Bound by HBM: x once, y twice; the adapters come from L2.  8192 tokens of width
-// 7168 and rank 64 take 90 us (3.9 TB/s), the list of tiles among them (7); with
-// two bf16 operands in place of three 85, and a result further off (0.0021 of the
-// elements of y round otherwise than from a float32 H, so a few in 10,000).  With
-// cold caches and 4096 tokens 28 us (2.0 TB/s of x: the parts' sum and the start
-// are as long as the steps) and 31 (3.8 TB/s of y).
+// 7168 and rank 64 take 90 us (3.9 TB/s), the list of tiles among them (7); two
+// bf16 operands in place of three took 85, and 0.2% of y's elements then rounded
+// otherwise than from a float32 H.  With cold caches and 4096 tokens 29 us (2.0
+// TB/s of x: the parts' sum and the start are as long as the steps) and 34 (3.5 TB/s
+// of y).
 //
 // Every wait on a memory barrier is bounded (1 s); on expiry the kernel records
 // WQ_ERR_TIMEOUT, waits (bounded) for its own copies and MMAs, frees tensor
